@@ -320,6 +320,73 @@ ws_status ws_nf4_matmul_noalloc(const ws_nf4* W, const uint16_t* act, int64_t M,
                                 int32_t transpose_w, void* out, int32_t out_dtype,
                                 ws_stream_t stream);
 
+/* ---- adapters of many requests beside one frozen NF4 linear ------------------------------ */
+/* The linear of ws_lora_linear_fwd / _bwd for a batch whose rows belong to
+ * different adapters of one frozen base: served requests, or adapters trained
+ * side by side.  row_adapter[m] names row m's adapter; any value outside
+ * [0, n_adapters) means none (the row gets the base alone).  With a = its
+ * adapter:
+ *   U[m]  = (mask . x)[m] A_a^T                 (zeros without an adapter)
+ *   y[m]  = x[m] W'^T + scale_a U[m] B_a^T      one rounding to bf16
+ *   G[m]  = dY[m] B_a
+ *   dX[m] = dY[m] W' + mask[m] . scale_a G[m] A_a
+ *   dB_a  = scale_a sum_{m of a} dY[m]^T U[m];  dA_a = scale_a sum_{m of a} G[m]^T (mask . x)[m]
+ * Adapters lie at a stride, so a pool of adapters' parameter arrays (one
+ * ws_stack_param_offset layout after another) serves as it is. */
+typedef struct {
+  const void* A;       /* adapter a: [r, K] at A + a*stride_a elements (device) */
+  const void* B;       /* adapter a: [N, r] at B + a*stride_b elements (device) */
+  const float* scale;  /* [n_adapters] alpha/r, with dropout alpha/r/(1-p) (device, 4-byte aligned) */
+  int64_t stride_a;    /* >= r*K, a multiple of 8 elements                      */
+  int64_t stride_b;    /* >= N*r, a multiple of 8 elements                      */
+  int32_t n_adapters;  /* 1 .. WS_MULTI_MAX_ADAPTERS                            */
+  int32_t r;           /* 16                                                    */
+  int32_t dtype;       /* WS_DTYPE_F32, or WS_DTYPE_BF16 (forward only)         */
+} ws_lora_set;
+enum { WS_MULTI_MAX_ADAPTERS = 4096 };
+
+/* The dropout keep bits [M, K/32] of one linear (the bits ws_lora_linear_fwd
+ * saves for the same key), for the calls below, which take them as input. */
+ws_status ws_dropout_mask(ws_dropout_key key, int64_t M, int64_t K, uint32_t* mask,
+                          ws_stream_t stream);
+
+/* The rows of a batch sorted by adapter, made on the device from row_adapter
+ * [M] (int32, device) once per batch: every linear of every layer that the
+ * batch passes through shares it, forward and backward.  data: device, 16-byte
+ * aligned, ws_lora_multi_plan_size bytes.  ws_lora_multi_plan_init only
+ * enqueues; a captured call rereads row_adapter at every replay, and calls
+ * that use the plan after it see the new rows. */
+typedef struct {
+  void* data;
+  int64_t M;
+  int32_t n_adapters;
+} ws_lora_plan;
+ws_status ws_lora_multi_plan_size(int64_t M, int32_t n_adapters, size_t* bytes);
+ws_status ws_lora_multi_plan_init(const ws_lora_plan* plan, const int32_t* row_adapter,
+                                  ws_stream_t stream);
+
+/* Workspace (device bytes) of ws_lora_linear_fwd_multi / _bwd_multi. */
+ws_status ws_lora_multi_workspace_size(int64_t M, int64_t N, int64_t K, int32_t n_adapters,
+                                       size_t* bytes);
+/* Forward.  x [M,K] bf16, mask [M,K/32] uint32 or NULL (no dropout), y [M,N]
+ * bf16 out, U_saved [M,r] fp32 out; M is the plan's.  The base term sums in
+ * fp32 and the adapter term is added before the one rounding.  No atomics; a
+ * given shape and row order always gives the same bits. */
+ws_status ws_lora_linear_fwd_multi(const ws_nf4* W, const uint16_t* x, const ws_lora_set* set,
+                                   const ws_lora_plan* plan, const uint32_t* mask, uint16_t* y,
+                                   float* U_saved, void* workspace, size_t ws_bytes,
+                                   ws_stream_t stream);
+/* Backward, given the forward's U_saved and mask; adapters fp32.  dX [M,K] bf16
+ * or fp32 (dX_dtype); adapter a's gradients dA [r,K] at dA + a*stride_a and dB
+ * [N,r] at dB + a*stride_b (the strides of the set), fp32.  accumulate: WS_ACC_DX
+ * adds into an fp32 dX, WS_ACC_GRADS adds into dA and dB; without it the
+ * gradients of adapters that have no row are set to zero. */
+ws_status ws_lora_linear_bwd_multi(const ws_nf4* W, const uint16_t* x, const ws_lora_set* set,
+                                   const ws_lora_plan* plan, const uint32_t* mask,
+                                   const float* U_saved, const uint16_t* dY, void* dX,
+                                   int32_t dX_dtype, int32_t accumulate, float* dA, float* dB,
+                                   void* workspace, size_t ws_bytes, ws_stream_t stream);
+
 /* ---- attention core ---------------------------------------------------------- */
 /* The attention of the trained model, which streaming leaves unchanged (the
  * research page "Poros", the paragraph saying the learning problem itself is
@@ -355,6 +422,85 @@ ws_status ws_attention_bwd(const uint16_t* q, const uint16_t* k, const uint16_t*
                            int32_t n_seq, int32_t seq_len, int32_t n_heads, int32_t n_kv_heads,
                            int32_t head_dim, uint16_t* dq, uint16_t* dk, uint16_t* dv,
                            void* workspace, size_t workspace_bytes, ws_stream_t stream);
+
+/* ---- AdamW over many tensors ------------------------------------------------------- */
+/* One optimizer step of many tensors at once (the adapters of several runs, or
+ * any others), beside the Adam of ws_stack_train_step, which knows one flat
+ * array.  Decoupled weight decay (Loshchilov & Hutter, 2019); for an element of
+ * group h at step t (1, 2, ...), with gradient factor c:
+ *   m = beta1 m + (1 - beta1) c g;   v = beta2 v + (1 - beta2) (c g)^2
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32; a bf16 p is rounded once, when it is stored.
+ * Moments in 32 bits: m and v fp32 [n].  In 8 bits: blocks of 256 consecutive
+ * elements of a tensor (the last may be short) with an fp32 scale each:
+ *   m: e4m3 code [n] times m_scale [ceil(n/256)] = max|m| / 448;
+ *   v: code c [n] of sqrt(v): (1 + (c & 15)/16) 2^((c >> 4) - 15), 0 for c = 0,
+ *      times v_scale [ceil(n/256)] = max sqrt(v) / 1.9375; never 0 for v > 0.
+ * Both to nearest (ties to even); the step uses the moments before this
+ * rounding.  Zero codes and scales are zero moments.  A gradient that is not
+ * finite makes its element's moments (in 8 bits: its whole block's) NaN,
+ * unless clipping skips the step. */
+typedef struct {
+  void* p;        /* parameters [n] (device)                               */
+  const void* g;  /* gradients [n] (device; two tensors may share one)      */
+  void* m;        /* first moment: fp32 [n], or e4m3 codes [n]              */
+  void* v;        /* second moment: fp32 [n], or 8-bit codes of its root [n] */
+  float* m_scale; /* 8-bit states: [ceil(n/256)], 4-byte aligned; else NULL  */
+  float* v_scale;
+  int64_t n;      /* elements, >= 1                                          */
+  int32_t group;  /* parameter group, < n_groups                             */
+  int32_t reserved;
+} ws_adamw_tensor;
+/* Types shared by every tensor of a plan: WS_DTYPE_* of p and g, 8 or 32. */
+typedef struct {
+  int32_t p_dtype, g_dtype, state_bits;
+} ws_adamw_types;
+/* A parameter group, in device memory (16-byte aligned array of n_groups): the
+ * caller may rewrite it between steps, also between replays of a captured
+ * step.  step counts the steps taken (0 before the first) and is advanced by
+ * ws_adamw_step. */
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  double max_norm; /* WS_ADAMW_CLIP: the largest gradient norm, <= 0 for none */
+  double step;
+  double reserved;
+} ws_adamw_group;
+/* A plan: which chunk of which tensor each CTA works on.  ws_adamw_plan_init
+ * (host only, no CUDA call) checks the tensors and fills `image` (host memory,
+ * plan_bytes) and *plan; the caller copies the image to the device and sets
+ * plan->image to that copy (16-byte aligned).  The plan keeps the tensors'
+ * addresses; it serves every step while they stand.  WS_ERR_INVALID if
+ * anything the step writes overlaps another range of the plan (the same
+ * parameter listed twice). */
+typedef struct {
+  const void* image; /* device */
+  ws_adamw_types types;
+  int32_t n_tensors, n_groups, n_chunks;
+} ws_adamw_plan;
+ws_status ws_adamw_plan_size(const ws_adamw_tensor* tensors, int32_t n_tensors, int32_t n_groups,
+                             ws_adamw_types types, size_t* plan_bytes, size_t* workspace_bytes);
+ws_status ws_adamw_plan_init(const ws_adamw_tensor* tensors, int32_t n_tensors, int32_t n_groups,
+                             ws_adamw_types types, void* image, size_t image_bytes,
+                             ws_adamw_plan* plan);
+/* One step of every tensor of the plan.  norms (device [n_groups], may be NULL)
+ * receives each group's gradient norm, before clipping.  WS_ADAMW_CLIP: c =
+ * min(1, max_norm / (norm + 1e-6)), and a group whose norm is not finite takes
+ * no step (its tensors and counter stay as they are); else c = 1.  Norms sum
+ * squares in fp32 within 16 elements of a thread and a chunk of 4096, and in
+ * double across chunks, in a fixed order. */
+enum { WS_ADAMW_CLIP = 1 };
+ws_status ws_adamw_step(const ws_adamw_plan* plan, ws_adamw_group* groups, int32_t flags,
+                        float* norms, void* workspace, size_t ws_bytes, ws_stream_t stream);
+
+/* 8-bit states to and from values, a tensor at a time (to begin from 32-bit
+ * moments, to inspect or to save): WS_ADAMW_M the first moment, WS_ADAMW_V_ROOT
+ * the ROOT of the second (values >= 0; encoding takes sqrt(v), decoding gives
+ * it).  codes [n], scale [ceil(n/256)]; decoded values fp32 or, rounded, bf16. */
+enum { WS_ADAMW_M = 0, WS_ADAMW_V_ROOT = 1 };
+ws_status ws_adamw_encode8(const float* values, int64_t n, int32_t moment, uint8_t* codes,
+                           float* scale, ws_stream_t stream);
+ws_status ws_adamw_decode8(const uint8_t* codes, const float* scale, int64_t n, int32_t moment,
+                           void* out, int32_t out_dtype, ws_stream_t stream);
 
 /* ---- the synthetic stack ----------------------------------------------------- */
 /* The transformer layers the method trains ("Poros", learning-problem

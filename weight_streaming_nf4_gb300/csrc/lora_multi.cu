@@ -1,0 +1,654 @@
+// lora_multi.cu -- low-rank adapters of many requests beside one frozen NF4
+// linear: rows sorted by adapter, the skinny products U = (mask . x) A_a^T and
+// G = dY B_a, the weight gradients of every adapter, and the C entry points of
+// the forward and backward.  Every reduction runs in a fixed order.
+#include <math.h>
+#include <string.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace ws {
+
+namespace {
+
+constexpr int kR = 16;            // adapter rank
+constexpr int kTileRows = 64;     // rows of one skinny-product tile
+constexpr int kPlanThreads = 1024;
+
+size_t al16(size_t x) { return (x + 15) & ~size_t(15); }
+size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
+bool al16p(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// ------------------------------------------------------------------------ the batch's plan
+// Sections of the plan buffer (int32 words): header {tiles}, the adapter of
+// each row (-1: none), the rows sorted by adapter (stable; rows without one
+// last), each adapter's first position in that order (n + 1 entries: the last
+// is where the rows without an adapter begin), and tiles {adapter, first
+// position, rows, 0} of at most kTileRows rows of one adapter.
+struct PlanLayout {
+  int64_t row, perm, off, tile, words;
+  int64_t max_tiles;
+};
+PlanLayout plan_layout(int64_t M, int64_t n) {
+  PlanLayout L{};
+  auto up4 = [](int64_t x) { return (x + 3) & ~int64_t(3); };
+  const int64_t groups = n + 1 < M ? n + 1 : M;  // non-empty groups, rows without an adapter among them
+  L.max_tiles = M / kTileRows + groups;
+  L.row = 4;
+  L.perm = L.row + up4(M);
+  L.off = L.perm + up4(M);
+  L.tile = L.off + up4(n + 1);
+  L.words = L.tile + 4 * L.max_tiles;
+  return L;
+}
+
+// One CTA.  Rows are counted with shared-memory atomics (integer counts: any
+// order gives the same), the counts scanned, and the rows placed warp by warp
+// so that equal adapters keep the row order.
+__global__ void __launch_bounds__(kPlanThreads)
+    k_multi_plan(const int32_t* __restrict__ row_adapter, int M, int n, int32_t* __restrict__ plan,
+                 int64_t o_row, int64_t o_perm, int64_t o_off, int64_t o_tile) {
+  pdl_wait();
+  pdl_launch_dependents();
+  // position counters of the adapters and, at [n], of the rows without one
+  __shared__ int pos[WS_MULTI_MAX_ADAPTERS + 1];
+  __shared__ int wsum[2][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i <= n; i += kPlanThreads) pos[i] = 0;
+  __syncthreads();
+  for (int i = tid; i < M; i += kPlanThreads) {
+    const int a = row_adapter[i];
+    const bool has = a >= 0 && a < n;
+    plan[o_row + i] = has ? a : -1;
+    atomicAdd(&pos[has ? a : n], 1);
+  }
+  __syncthreads();
+  // exclusive scan of rows and tiles over the n + 1 groups, kPer per thread
+  constexpr int kPer = (WS_MULTI_MAX_ADAPTERS + 1 + kPlanThreads - 1) / kPlanThreads;
+  int c[kPer], rows = 0, tiles = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int i = tid * kPer + k;
+    c[k] = i <= n ? pos[i] : 0;
+    rows += c[k];
+    tiles += (c[k] + kTileRows - 1) / kTileRows;
+  }
+  int ir = rows, it = tiles;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int r = __shfl_up_sync(0xffffffffu, ir, o), t = __shfl_up_sync(0xffffffffu, it, o);
+    if (lane >= o) ir += r, it += t;
+  }
+  if (lane == 31) wsum[0][warp] = ir, wsum[1][warp] = it;
+  __syncthreads();
+  int br = 0, bt = 0, all = 0;
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w < warp) br += wsum[0][w], bt += wsum[1][w];
+    all += wsum[1][w];
+  }
+  if (tid == 0) plan[0] = all;
+  int r0 = br + ir - rows, t0 = bt + it - tiles;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int i = tid * kPer + k;
+    if (i <= n) {
+      plan[o_off + i] = r0;
+      pos[i] = r0;
+      for (int q = 0; q < c[k]; q += kTileRows, ++t0)
+        *reinterpret_cast<int4*>(plan + o_tile + 4 * (int64_t)t0) =
+            make_int4(i < n ? i : -1, r0 + q, min(kTileRows, c[k] - q), 0);
+      r0 += c[k];
+    }
+  }
+  __syncthreads();
+  for (int b = 0; b < M; b += kPlanThreads) {
+    const int i = b + tid;
+    int a = -1;
+    if (i < M) {
+      a = row_adapter[i];
+      if (a < 0 || a >= n) a = n;
+    }
+    const uint32_t same = __match_any_sync(0xffffffffu, a);
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    const int nw = min(kPlanThreads / 32, (M - b + 31) / 32);
+    for (int w = 0; w < nw; ++w) {
+      if (w == warp) {
+        const int at = a >= 0 ? pos[a] + rank : 0;
+        __syncwarp();
+        if (a >= 0 && rank == 0) pos[a] += __popc(same);
+        if (a >= 0) plan[o_perm + at] = i;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// ------------------------------------------------------------------------ mma.sync pieces
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), bf16.  Lane (g = lane / 4, t =
+// lane % 4) holds A rows g, g + 8 at k = 2t, 2t+1 (a[0], a[1]) and 2t+8, 2t+9
+// (a[2], a[3]); B column g at the same k (b[0], b[1]); D rows g (d[0], d[1])
+// and g + 8 at columns 2t, 2t+1.  The kernels below permute the contraction
+// index (alike in A and B), so that a lane's elements are contiguous in memory.
+WS_DEVINL void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Two fp32 values as bf16 high parts and bf16 low parts (the remainders):
+// together 16 significant bits or more.
+WS_DEVINL void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(x, y);
+  lo = pack_bf16x2(x - bf16_lo(hi), y - bf16_hi(hi));
+}
+// Zeroes the halves of a bf16 pair whose keep bit (bits 0, 1 of b) is clear.
+WS_DEVINL uint32_t keep2(uint32_t v, uint32_t b) {
+  return v & (((b & 1u) ? 0x0000ffffu : 0u) | ((b & 2u) ? 0xffff0000u : 0u));
+}
+
+// ------------------------------------------------------------------------ skinny products
+// out[row][0..16) = sum_c X~[row][c] F_a[.][c] for the rows of one tile (one
+// adapter): U = (mask . x) A_a^T with F = A [16, C], or G = dY B_a with F = B
+// [C, 16] (F_CJ).  X is bf16 and exact; an fp32 F enters as two bf16 parts.
+//
+// Bound by reading X and the adapters once.  A cluster of CTAs shares a tile's
+// contraction: its warps take the 64-deep steps in turn (a single-row tile of
+// a decode batch then reads its adapter with 64 warps), the warps' sums are
+// added in warp order, the CTAs' in rank order through distributed shared
+// memory.  A lane reads 16 consecutive elements of a row (whole 128-byte
+// lines per four lanes).
+constexpr int kSkWarps = 8;
+template <bool F_CJ, bool F16, bool MASKED>
+__global__ void __launch_bounds__(kSkWarps * 32)
+    k_multi_skinny(const uint16_t* __restrict__ X, const void* __restrict__ Fv, int64_t strideF,
+                   int C, const uint32_t* __restrict__ mask, const int32_t* __restrict__ plan,
+                   int64_t o_perm, int64_t o_tile, float* __restrict__ out) {
+  __shared__ float part[kSkWarps][kTileRows * kR];
+  __shared__ float sum[kTileRows * kR];
+  const int lane = (int)lane_id(), warp = (int)warp_id(), g = lane >> 2, t = lane & 3;
+  const int CS = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
+  pdl_wait();
+  pdl_launch_dependents();
+  if ((int)blockIdx.y >= plan[0]) return;  // the whole cluster alike
+  const int4 tile = *reinterpret_cast<const int4*>(plan + o_tile + 4 * (int64_t)blockIdx.y);
+  const int32_t* rows = plan + o_perm + tile.y;
+  const int cnt = tile.z, nsub = (cnt + 15) / 16;
+  if (tile.x < 0) {  // rows without an adapter
+    if (rank == 0)
+      for (int i = threadIdx.x; i < cnt * kR; i += kSkWarps * 32) out[(int64_t)rows[i / kR] * kR + i % kR] = 0.0f;
+    return;
+  }
+  float acc[4][2][4] = {};
+  int64_t ro[4][2];  // row offsets (or -1) of this lane's rows of each 16-row part
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = s * 16 + h * 8 + g;
+      ro[s][h] = r < cnt ? (int64_t)rows[r] * C : -1;
+    }
+  for (int st = rank * kSkWarps + warp; st < C / 64; st += kSkWarps * CS) {
+    const int c0 = st * 64 + 16 * t;
+    uint32_t bh[2][4][2], bl[2][4][2];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      const int j = nt * 8 + g;
+      if constexpr (F16) {
+        const uint4* f = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(Fv) +
+                                                        tile.x * strideF + (int64_t)j * C + c0);
+        const uint4 p = f[0], q = f[1];
+        bh[nt][0][0] = p.x, bh[nt][0][1] = p.y, bh[nt][1][0] = p.z, bh[nt][1][1] = p.w;
+        bh[nt][2][0] = q.x, bh[nt][2][1] = q.y, bh[nt][3][0] = q.z, bh[nt][3][1] = q.w;
+      } else {
+        float v[16];
+        const float* F = static_cast<const float*>(Fv) + tile.x * strideF;
+        if constexpr (F_CJ) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = F[(int64_t)(c0 + e) * kR + j];
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 w = reinterpret_cast<const float4*>(F + (int64_t)j * C + c0)[q];
+            v[4 * q] = w.x, v[4 * q + 1] = w.y, v[4 * q + 2] = w.z, v[4 * q + 3] = w.w;
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          split2(v[4 * s], v[4 * s + 1], bh[nt][s][0], bl[nt][s][0]);
+          split2(v[4 * s + 2], v[4 * s + 3], bh[nt][s][1], bl[nt][s][1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (u >= nsub) break;
+      uint32_t x[2][8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (ro[u][h] >= 0) {
+          const uint4* s = reinterpret_cast<const uint4*>(X + ro[u][h] + c0);
+          const uint4 p = s[0], q = s[1];
+          x[h][0] = p.x, x[h][1] = p.y, x[h][2] = p.z, x[h][3] = p.w;
+          x[h][4] = q.x, x[h][5] = q.y, x[h][6] = q.z, x[h][7] = q.w;
+          if constexpr (MASKED) {
+            const uint32_t b = mask[(ro[u][h] + c0) >> 5] >> (c0 & 31);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[h][e] = keep2(x[h][e], b >> (2 * e));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[h][e] = 0u;
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          mma16816(acc[u][nt], x[0][2 * s], x[1][2 * s], x[0][2 * s + 1], x[1][2 * s + 1],
+                   bh[nt][s][0], bh[nt][s][1]);
+          if constexpr (!F16)
+            mma16816(acc[u][nt], x[0][2 * s], x[1][2 * s], x[0][2 * s + 1], x[1][2 * s + 1],
+                     bl[nt][s][0], bl[nt][s][1]);
+        }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if (u >= nsub) break;
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float2*>(&part[warp][(u * 16 + h * 8 + g) * kR + nt * 8 + 2 * t]) =
+            make_float2(acc[u][nt][2 * h], acc[u][nt][2 * h + 1]);
+  }
+  __syncthreads();
+  const int elems = cnt * kR;
+  for (int i = threadIdx.x; i < elems; i += kSkWarps * 32) {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kSkWarps; ++w) s += part[w][i];
+    if (CS == 1) out[(int64_t)rows[i / kR] * kR + i % kR] = s;
+    else sum[i] = s;
+  }
+  if (CS == 1) return;
+  cluster_sync();
+  for (int i = rank * kSkWarps * 32 + threadIdx.x; i < elems; i += CS * kSkWarps * 32) {
+    float s = 0.0f;
+    for (int c = 0; c < CS; ++c) {
+      float v;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                   : "=f"(v)
+                   : "r"(mapa_shared(smem_u32(&sum[i]), (uint32_t)c))
+                   : "memory");
+      s += v;
+    }
+    out[(int64_t)rows[i / kR] * kR + i % kR] = s;
+  }
+  cluster_sync();  // the sums stay until every CTA of the cluster has read them
+}
+
+// ------------------------------------------------------------------------ weight gradients
+// One launch for both gradients of every adapter:
+//   dB_a [N, 16] = s_a sum_{m of a} dY[m]^T U[m],  dA_a [16, K] = s_a sum_{m of a} G[m]^T (mask . x)[m]
+// CTA = 64 columns of dY or x for one adapter: D (16 x 64) += P^T Q over the
+// adapter's rows, 16 at a time, warps taking turns; the warps' sums are added
+// in warp order.  Q is bf16 and exact, the fp32 P enters as two bf16 parts.
+// A lane reads 8 consecutive columns of four rows (16 bytes each, 128 bytes of
+// a row per eight lanes) and pairs rows with byte permutes: column 8g + i of
+// the tile is column g of the i-th 8-wide product, so nothing is transposed
+// through shared memory.  Bound by reading dY and x once.
+constexpr int kWgWarps = 8;
+struct WgArgs {
+  const float* P[2];      // U, G  [M, 16]
+  const uint16_t* Q[2];   // dY [M, C0], x [M, C1]
+  float* out[2];          // dB, dA
+  int C[2];
+  int64_t stride[2];
+  const uint32_t* mask;   // of Q[1], or NULL
+  const float* scale;
+  const int32_t* plan;
+  int64_t o_perm, o_off;
+  int accumulate;
+};
+WS_DEVINL uint32_t lo_pair(uint32_t a, uint32_t b) { return (a & 0xffffu) | (b << 16); }
+WS_DEVINL uint32_t hi_pair(uint32_t a, uint32_t b) { return (a >> 16) | (b & 0xffff0000u); }
+
+__global__ void __launch_bounds__(kWgWarps * 32) k_multi_wgrad(const WgArgs w) {
+  __shared__ float red[kWgWarps][kR][64];
+  const int lane = (int)lane_id(), warp = (int)warp_id(), g = lane >> 2, t = lane & 3;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int nb = w.C[0] / 64;
+  const int which = (int)blockIdx.x >= nb ? 1 : 0;
+  const int col0 = ((int)blockIdx.x - (which ? nb : 0)) * 64;
+  const int a = blockIdx.y;
+  const int C = which ? w.C[1] : w.C[0];
+  const float* P = which ? w.P[1] : w.P[0];
+  const uint16_t* Q = which ? w.Q[1] : w.Q[0];
+  const uint32_t* mask = which ? w.mask : nullptr;
+  const int r_beg = w.plan[w.o_off + a], r_end = w.plan[w.o_off + a + 1];
+  const int cnt = r_end - r_beg;
+  if (cnt == 0 && w.accumulate) return;
+  const int32_t* rows = w.plan + w.o_perm + r_beg;
+  float d[8][4] = {};
+  for (int s0 = warp * 16; s0 < cnt; s0 += kWgWarps * 16) {
+    uint32_t q[4][4];    // rows 2t, 2t+1, 2t+8, 2t+9 of the step; 8 columns
+    float p[4][2];       // P of those rows at j = g, g + 8
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = s0 + 2 * t + (i & 1) + (i >> 1) * 8;
+      if (r < cnt) {
+        const int64_t row = rows[r];
+        const uint4 v = *reinterpret_cast<const uint4*>(Q + row * C + col0 + 8 * g);
+        q[i][0] = v.x, q[i][1] = v.y, q[i][2] = v.z, q[i][3] = v.w;
+        if (mask) {
+          const int64_t e = row * C + col0 + 8 * g;
+          const uint32_t b = mask[e >> 5] >> (e & 31);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) q[i][k] = keep2(q[i][k], b >> (2 * k));
+        }
+        p[i][0] = P[row * kR + g];
+        p[i][1] = P[row * kR + g + 8];
+      } else {
+        q[i][0] = q[i][1] = q[i][2] = q[i][3] = 0u;
+        p[i][0] = p[i][1] = 0.0f;
+      }
+    }
+    uint32_t ah[4], al[4];
+    split2(p[0][0], p[1][0], ah[0], al[0]);
+    split2(p[0][1], p[1][1], ah[1], al[1]);
+    split2(p[2][0], p[3][0], ah[2], al[2]);
+    split2(p[2][1], p[3][1], ah[3], al[3]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = i / 2;
+      const uint32_t b0 = (i & 1) ? hi_pair(q[0][k], q[1][k]) : lo_pair(q[0][k], q[1][k]);
+      const uint32_t b1 = (i & 1) ? hi_pair(q[2][k], q[3][k]) : lo_pair(q[2][k], q[3][k]);
+      mma16816(d[i], ah[0], ah[1], ah[2], ah[3], b0, b1);
+      mma16816(d[i], al[0], al[1], al[2], al[3], b0, b1);
+    }
+  }
+  const int nw = min(kWgWarps, (cnt + 15) / 16);  // warps that had rows
+  if (warp < nw) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; i += 4)
+          *reinterpret_cast<float4*>(&red[warp][g + 8 * h][(2 * t + c) * 8 + i]) =
+              make_float4(d[i][2 * h + c], d[i + 1][2 * h + c], d[i + 2][2 * h + c], d[i + 3][2 * h + c]);
+  }
+  __syncthreads();
+  const float s = w.scale[a];
+  float* out = (which ? w.out[1] : w.out[0]) + a * (which ? w.stride[1] : w.stride[0]);
+#pragma unroll
+  for (int k = 0; k < kR * 64 / (kWgWarps * 32); ++k) {
+    const int i = k * kWgWarps * 32 + threadIdx.x;
+    const int j = which ? i / 64 : i % kR, c = which ? i % 64 : i / kR;
+    float v = 0.0f;
+    for (int x = 0; x < nw; ++x) v += red[x][j][c];
+    v = __fmul_rn(v, s);  // rounded by itself: accumulating adds the finished contribution once
+    float* o = out + (which ? (int64_t)j * C + col0 + c : (int64_t)(col0 + c) * kR + j);
+    *o = w.accumulate ? *o + v : v;
+  }
+}
+
+// ------------------------------------------------------------------------ adapter term of y and dX
+// out = base + the adapter term, one rounding.  FWD: + s_a sum_j U[m][j]
+// B_a[n][j]; else + mask . s_a sum_j G[m][j] A_a[j][k].  Four columns per thread.
+template <bool FWD, bool F16, bool O16>
+__global__ void __launch_bounds__(256)
+    k_multi_add(const float* base, const float* __restrict__ P, const void* __restrict__ Fv,
+                int64_t strideF, const float* __restrict__ scale, const uint32_t* __restrict__ mask,
+                const int32_t* __restrict__ row_adapter, int C, void* out) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t m = blockIdx.x;
+  const int c = ((int)blockIdx.y * 256 + (int)threadIdx.x) * 4;
+  if (c >= C) return;
+  const int a = row_adapter[m];
+  float4 v = *reinterpret_cast<const float4*>(base + m * C + c);
+  if (a >= 0) {
+    float d[4] = {};
+    for (int j = 0; j < kR; ++j) {
+      const float u = P[m * kR + j];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t o = a * strideF + (FWD ? (int64_t)(c + e) * kR + j : (int64_t)j * C + c + e);
+        const float f = F16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(Fv)[o]) : static_cast<const float*>(Fv)[o];
+        d[e] = fmaf(u, f, d[e]);
+      }
+    }
+    const float s = scale[a];
+    uint32_t b = 15u;
+    if (!FWD && mask) b = mask[(m * C + c) >> 5] >> (c & 31);
+    v.x += (b & 1u) ? s * d[0] : 0.0f;
+    v.y += (b & 2u) ? s * d[1] : 0.0f;
+    v.z += (b & 4u) ? s * d[2] : 0.0f;
+    v.w += (b & 8u) ? s * d[3] : 0.0f;
+  }
+  if (O16)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + m * C + c) =
+        make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  else
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + m * C + c) = v;
+}
+
+// ------------------------------------------------------------------------ host side
+struct WsLayout {
+  size_t G, base, partial, total;
+};
+WsLayout ws_layout(int64_t M, int64_t N, int64_t K) {
+  WsLayout L{};
+  const GemmPlan f = plan_gemm(false, M, N, K), b = plan_gemm(true, M, K, N);
+  const size_t pf = gemm_partial_bytes(f, M, N), pb = gemm_partial_bytes(b, M, K);
+  L.G = 0;
+  L.base = al256((size_t)M * kR * 4);
+  L.partial = L.base + al256((size_t)M * (size_t)(N > K ? N : K) * 4);
+  L.total = L.partial + al256(pf > pb ? pf : pb);
+  return L;
+}
+
+template <typename K, typename... Args>
+cudaError_t launch_cluster(K k, dim3 grid, int threads, int cluster, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
+// CTAs that share a tile's contraction: as many as have a step for every warp.
+int skinny_cluster(int64_t C) {
+  int cs = 8;
+  while (cs > 1 && cs * kSkWarps > C / 64) cs /= 2;
+  return cs;
+}
+
+cudaError_t run_skinny(bool f_cj, const uint16_t* X, const void* F, bool f16, int64_t strideF, int64_t C,
+                       const uint32_t* mask, const ws_lora_plan& plan, float* out, cudaStream_t st) {
+  const PlanLayout L = plan_layout(plan.M, plan.n_adapters);
+  const int cs = skinny_cluster(C);
+  auto k = f_cj ? k_multi_skinny<true, false, false>
+                : (f16 ? (mask ? k_multi_skinny<false, true, true> : k_multi_skinny<false, true, false>)
+                       : (mask ? k_multi_skinny<false, false, true> : k_multi_skinny<false, false, false>));
+  return launch_cluster(k, dim3((unsigned)cs, (unsigned)L.max_tiles), kSkWarps * 32, cs, st, X, F, strideF,
+                        (int)C, mask, (const int32_t*)plan.data, L.perm, L.tile, out);
+}
+
+ws_status check_plan(const ws_lora_plan* p) {
+  if (!p || !p->data) return WS_ERR_INVALID;
+  if (p->M < 1 || p->M > (1 << 20) || p->n_adapters < 1 || p->n_adapters > WS_MULTI_MAX_ADAPTERS) return WS_ERR_SHAPE;
+  if (!al16p(p->data)) return WS_ERR_ALIGN;
+  return WS_OK;
+}
+
+// What forward and backward check alike.
+ws_status check_multi(const ws_nf4* W, const ws_lora_set* set, const ws_lora_plan* plan,
+                      const uint32_t* mask) {
+  const ws_status s = check_plan(plan);
+  if (s != WS_OK) return s;
+  if (!W || !W->codes || !W->absmax || !set || !set->A || !set->B || !set->scale) return WS_ERR_INVALID;
+  if (set->dtype != WS_DTYPE_F32 && set->dtype != WS_DTYPE_BF16) return WS_ERR_INVALID;
+  if (W->N < 64 || W->K < 64 || W->N % 64 || W->K % 64 || W->N > (1 << 30) || W->K > (1 << 30)) return WS_ERR_SHAPE;
+  if (set->r != kR || set->n_adapters != plan->n_adapters) return WS_ERR_SHAPE;
+  if (set->stride_a < kR * W->K || set->stride_b < kR * W->N || set->stride_a % 8 || set->stride_b % 8) return WS_ERR_SHAPE;
+  if ((double)plan->M * (double)(W->N > W->K ? W->N : W->K) >= 17179869184.0) return WS_ERR_SHAPE;  // 2^34
+  if (!al16p(W->codes) || !al16p(W->absmax) || !al16p(set->A) || !al16p(set->B) || !al16p(mask)) return WS_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(set->scale) & 3u) return WS_ERR_ALIGN;
+  return WS_OK;
+}
+
+NF4View view(const ws_nf4* W) {
+  NF4View v;
+  v.codes = W->codes;
+  v.absmax = W->absmax;
+  v.N = W->N;
+  v.K = W->K;
+  return v;
+}
+
+#define WS_RUN(x)                                \
+  do {                                           \
+    if ((x) != cudaSuccess) return WS_ERR_CUDA;  \
+  } while (0)
+
+}  // namespace
+
+}  // namespace ws
+
+using namespace ws;
+
+extern "C" {
+
+ws_status ws_dropout_mask(ws_dropout_key key, int64_t M, int64_t K, uint32_t* mask, ws_stream_t stream) {
+  if (!mask) return WS_ERR_INVALID;
+  if (M < 1 || K < 64 || K % 64 || (double)M * (double)K >= 17179869184.0) return WS_ERR_SHAPE;
+  if (!(key.p >= 0.0 && key.p < 1.0) || key.linear > 255u || key.microbatch > 0xFFFFFFu) return WS_ERR_INVALID;
+  if (!al16p(mask)) return WS_ERR_ALIGN;
+  WS_RUN(run_mask_gen(M, K, make_drop_key(key), mask, (cudaStream_t)stream));
+  return WS_OK;
+}
+
+ws_status ws_lora_multi_plan_size(int64_t M, int32_t n_adapters, size_t* bytes) {
+  if (!bytes) return WS_ERR_INVALID;
+  if (M < 1 || M > (1 << 20) || n_adapters < 1 || n_adapters > WS_MULTI_MAX_ADAPTERS) return WS_ERR_SHAPE;
+  *bytes = (size_t)plan_layout(M, n_adapters).words * 4;
+  return WS_OK;
+}
+
+ws_status ws_lora_multi_plan_init(const ws_lora_plan* plan, const int32_t* row_adapter,
+                                  ws_stream_t stream) {
+  const ws_status s = check_plan(plan);
+  if (s != WS_OK) return s;
+  if (!row_adapter) return WS_ERR_INVALID;
+  if (reinterpret_cast<uintptr_t>(row_adapter) & 3u) return WS_ERR_ALIGN;
+  const PlanLayout L = plan_layout(plan->M, plan->n_adapters);
+  note_launch();
+  WS_RUN(launch_pdl(k_multi_plan, dim3(1), dim3(kPlanThreads), 0, (cudaStream_t)stream, row_adapter,
+                    (int)plan->M, (int)plan->n_adapters, (int32_t*)plan->data, L.row, L.perm, L.off, L.tile));
+  return WS_OK;
+}
+
+ws_status ws_lora_multi_workspace_size(int64_t M, int64_t N, int64_t K, int32_t n_adapters,
+                                       size_t* bytes) {
+  if (!bytes) return WS_ERR_INVALID;
+  if (M < 1 || M > (1 << 20) || N < 64 || K < 64 || N % 64 || K % 64 || n_adapters < 1 ||
+      n_adapters > WS_MULTI_MAX_ADAPTERS)
+    return WS_ERR_SHAPE;
+  *bytes = ws_layout(M, N, K).total;
+  return WS_OK;
+}
+
+ws_status ws_lora_linear_fwd_multi(const ws_nf4* W, const uint16_t* x, const ws_lora_set* set,
+                                   const ws_lora_plan* plan, const uint32_t* mask, uint16_t* y,
+                                   float* U_saved, void* workspace, size_t ws_bytes,
+                                   ws_stream_t stream) {
+  const ws_status s = check_multi(W, set, plan, mask);
+  if (s != WS_OK) return s;
+  if (!x || !y || !U_saved || !workspace) return WS_ERR_INVALID;
+  if (!al16p(x) || !al16p(y) || !al16p(U_saved) || !al16p(workspace)) return WS_ERR_ALIGN;
+  const int64_t M = plan->M, N = W->N, K = W->K;
+  const WsLayout L = ws_layout(M, N, K);
+  if (ws_bytes < L.total) return WS_ERR_OOM;
+  cudaStream_t st = (cudaStream_t)stream;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const bool f16 = set->dtype == WS_DTYPE_BF16;
+  WS_RUN(run_skinny(false, x, set->A, f16, set->stride_a, K, mask, *plan, U_saved, st));
+  float* base = reinterpret_cast<float*>(ws + L.base);
+  WS_RUN(run_nf4_gemm(plan_gemm(false, M, N, K), view(W), x, M, nullptr, nullptr, 0.0f, nullptr, base, 1, 0,
+                      reinterpret_cast<float*>(ws + L.partial), st));
+  const int32_t* pl = static_cast<const int32_t*>(plan->data);
+  const PlanLayout P = plan_layout(M, plan->n_adapters);
+  note_launch();
+  WS_RUN(launch_pdl(f16 ? k_multi_add<true, true, true> : k_multi_add<true, false, true>,
+                    dim3((unsigned)M, (unsigned)((N + 1023) / 1024)), dim3(256), 0, st, (const float*)base,
+                    (const float*)U_saved, set->B, set->stride_b, set->scale, (const uint32_t*)nullptr,
+                    pl + P.row, (int)N, (void*)y));
+  return WS_OK;
+}
+
+ws_status ws_lora_linear_bwd_multi(const ws_nf4* W, const uint16_t* x, const ws_lora_set* set,
+                                   const ws_lora_plan* plan, const uint32_t* mask,
+                                   const float* U_saved, const uint16_t* dY, void* dX,
+                                   int32_t dX_dtype, int32_t accumulate, float* dA, float* dB,
+                                   void* workspace, size_t ws_bytes, ws_stream_t stream) {
+  const ws_status s = check_multi(W, set, plan, mask);
+  if (s != WS_OK) return s;
+  if (!x || !U_saved || !dY || !dX || !dA || !dB || !workspace) return WS_ERR_INVALID;
+  if (dX_dtype != WS_DTYPE_BF16 && dX_dtype != WS_DTYPE_F32) return WS_ERR_INVALID;
+  if (accumulate & ~(WS_ACC_DX | WS_ACC_GRADS)) return WS_ERR_INVALID;
+  if ((accumulate & WS_ACC_DX) && dX_dtype != WS_DTYPE_F32) return WS_ERR_INVALID;
+  if (set->dtype != WS_DTYPE_F32) return WS_ERR_UNSUPPORTED;
+  if (!al16p(x) || !al16p(U_saved) || !al16p(dY) || !al16p(dX) || !al16p(dA) || !al16p(dB) || !al16p(workspace))
+    return WS_ERR_ALIGN;
+  const int64_t M = plan->M, N = W->N, K = W->K;
+  const WsLayout L = ws_layout(M, N, K);
+  if (ws_bytes < L.total) return WS_ERR_OOM;
+  cudaStream_t st = (cudaStream_t)stream;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const int32_t* pl = static_cast<const int32_t*>(plan->data);
+  const PlanLayout P = plan_layout(M, plan->n_adapters);
+  float* G = reinterpret_cast<float*>(ws + L.G);
+  WS_RUN(run_skinny(true, dY, set->B, false, set->stride_b, N, nullptr, *plan, G, st));
+  WgArgs w{};
+  w.P[0] = U_saved, w.P[1] = G;
+  w.Q[0] = dY, w.Q[1] = x;
+  w.out[0] = dB, w.out[1] = dA;
+  w.C[0] = (int)N, w.C[1] = (int)K;
+  w.stride[0] = set->stride_b, w.stride[1] = set->stride_a;
+  w.mask = mask;
+  w.scale = set->scale;
+  w.plan = pl;
+  w.o_perm = P.perm, w.o_off = P.off;
+  w.accumulate = (accumulate & WS_ACC_GRADS) ? 1 : 0;
+  note_launch();
+  WS_RUN(launch_pdl(k_multi_wgrad, dim3((unsigned)((N + K) / 64), (unsigned)set->n_adapters), dim3(kWgWarps * 32),
+                    0, st, w));
+  const bool o32 = dX_dtype == WS_DTYPE_F32;
+  float* base = o32 ? static_cast<float*>(dX) : reinterpret_cast<float*>(ws + L.base);
+  WS_RUN(run_nf4_gemm(plan_gemm(true, M, K, N), view(W), dY, M, nullptr, nullptr, 0.0f, nullptr, base, 1,
+                      (accumulate & WS_ACC_DX) ? 1 : 0, reinterpret_cast<float*>(ws + L.partial), st));
+  note_launch();
+  WS_RUN(launch_pdl(o32 ? k_multi_add<false, false, false> : k_multi_add<false, false, true>,
+                    dim3((unsigned)M, (unsigned)((K + 1023) / 1024)), dim3(256), 0, st, (const float*)base,
+                    (const float*)G, set->A, set->stride_a, set->scale, mask, pl + P.row, (int)K, dX));
+  return WS_OK;
+}
+
+}  // extern "C"

@@ -63,6 +63,29 @@ BASE_NF4, BASE_BF16 = 0, 1
 ATTN_REPEAT_V, ATTN_CAUSAL = 0, 1
 
 
+class LoraSetC(C.Structure):
+    _fields_ = [("A", P), ("B", P), ("scale", P), ("stride_a", i64), ("stride_b", i64),
+                ("n_adapters", i32), ("r", i32), ("dtype", i32)]
+
+
+class LoraPlanC(C.Structure):
+    _fields_ = [("data", P), ("M", i64), ("n_adapters", i32)]
+
+
+class AdamwTensorC(C.Structure):
+    _fields_ = [("p", P), ("g", P), ("m", P), ("v", P), ("m_scale", P), ("v_scale", P),
+                ("n", i64), ("group", i32), ("reserved", i32)]
+
+
+class AdamwTypesC(C.Structure):
+    _fields_ = [("p_dtype", i32), ("g_dtype", i32), ("state_bits", i32)]
+
+
+class AdamwPlanC(C.Structure):
+    _fields_ = [("image", P), ("types", AdamwTypesC), ("n_tensors", i32), ("n_groups", i32),
+                ("n_chunks", i32)]
+
+
 class StackCfgC(C.Structure):
     _fields_ = [("M", i64), ("H", i64), ("KV", i64), ("I", i64), ("head_dim", i64),
                 ("n_layers", i32), ("r", i32), ("alpha", C.c_float), ("p", C.c_double),
@@ -110,6 +133,19 @@ _sig("ws_lora_group_workspace_size", [i32, P, i64, i64, C.POINTER(C.c_size_t)])
 _sig("ws_lora_linear_fwd_group", [i32, P, P, P, P, LoraShape, P, P, P, P, P, C.c_size_t, P])
 _sig("ws_lora_linear_bwd_group", [i32, P, P, P, P, LoraShape, P, P, P, P, P, i32, i32, P, P, P,
                                   C.c_size_t, P])
+_sig("ws_dropout_mask", [DropoutKey, i64, i64, P, P])
+_sig("ws_lora_multi_plan_size", [i64, i32, C.POINTER(C.c_size_t)])
+_sig("ws_lora_multi_plan_init", [C.POINTER(LoraPlanC), P, P])
+_sig("ws_lora_multi_workspace_size", [i64, i64, i64, i32, C.POINTER(C.c_size_t)])
+_sig("ws_lora_linear_fwd_multi", [C.POINTER(Nf4), P, C.POINTER(LoraSetC), C.POINTER(LoraPlanC), P, P,
+                                  P, P, C.c_size_t, P])
+_sig("ws_lora_linear_bwd_multi", [C.POINTER(Nf4), P, C.POINTER(LoraSetC), C.POINTER(LoraPlanC), P, P,
+                                  P, P, i32, i32, P, P, P, C.c_size_t, P])
+_sig("ws_adamw_plan_size", [P, i32, i32, AdamwTypesC, C.POINTER(C.c_size_t), C.POINTER(C.c_size_t)])
+_sig("ws_adamw_plan_init", [P, i32, i32, AdamwTypesC, P, C.c_size_t, C.POINTER(AdamwPlanC)])
+_sig("ws_adamw_step", [C.POINTER(AdamwPlanC), P, i32, P, P, C.c_size_t, P])
+_sig("ws_adamw_encode8", [P, i64, i32, P, P, P])
+_sig("ws_adamw_decode8", [P, P, i64, i32, P, i32, P])
 _sig("ws_attention_fwd", [P, P, P, i32, i32, i32, i32, i32, P, P, P, P])
 _sig("ws_attention_workspace_size", [i64, i32, i32, C.POINTER(C.c_size_t)])
 _sig("ws_attention_bwd", [P, P, P, P, P, P, i32, i32, i32, i32, i32, P, P, P, P, C.c_size_t, P])
@@ -143,7 +179,11 @@ EXPORTED = ("ws_status_string", "ws_device_error", "ws_selfcheck_bounded_wait", 
             "ws_lora_linear_fwd", "ws_lora_linear_bwd", "ws_lora_linear_fwd_bf16",
             "ws_lora_linear_bwd_bf16", "ws_nf4_matmul_workspace_size",
             "ws_nf4_matmul", "ws_nf4_matmul_noalloc", "ws_lora_group_workspace_size",
-            "ws_lora_linear_fwd_group", "ws_lora_linear_bwd_group", "ws_attention_fwd",
+            "ws_lora_linear_fwd_group", "ws_lora_linear_bwd_group", "ws_dropout_mask",
+            "ws_lora_multi_plan_size", "ws_lora_multi_plan_init", "ws_lora_multi_workspace_size",
+            "ws_lora_linear_fwd_multi", "ws_lora_linear_bwd_multi", "ws_adamw_plan_size",
+            "ws_adamw_plan_init", "ws_adamw_step", "ws_adamw_encode8", "ws_adamw_decode8",
+            "ws_attention_fwd",
             "ws_attention_workspace_size", "ws_attention_bwd", "ws_stack_sizes",
             "ws_stack_weight_offset", "ws_stack_param_offset", "ws_stack_saved_offset",
             "ws_stack_workspace_offset", "ws_stack_loader_staging_bytes", "ws_stack_put_weight",
@@ -401,6 +441,291 @@ def nf4_matmul_noalloc(W: NF4Weight, act, transpose_w=False, out=None, out_f32=F
     _check("ws_nf4_matmul_noalloc",
            _lib.ws_nf4_matmul_noalloc(C.byref(w), _ptr(act), M, 1 if transpose_w else 0,
                                       _ptr(out), dt, _stream(stream)))
+    return out
+
+
+# ------------------------------------------------------------------------------ many adapters
+def _need(ok, msg):
+    if not ok:
+        raise ValueError(msg)
+
+
+def _here(*ts):
+    """Every tensor (or None) is contiguous and on the current CUDA device."""
+    d = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for t in ts:
+        if t is not None:
+            _need(t.is_cuda and t.get_device() == d,
+                  f"tensor on {t.device}; the call runs on the current device, cuda:{d}")
+            _need(t.is_contiguous(), "tensors must be contiguous")
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory of `stream` (the caching allocator then reuses it in that stream's order)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def dropout_mask(key: DropoutKey, M: int, K: int, mask=None, device="cuda", stream=None):
+    """ws_dropout_mask: the keep bits int32 [M, K/32] of a dropout key."""
+    if mask is None:
+        mask = _empty((M, K // 32), torch.int32, device, stream)
+    _here(mask)
+    _need(mask.dtype == torch.int32 and tuple(mask.shape) == (M, K // 32), "mask: int32 [M, K/32]")
+    _check("ws_dropout_mask", _lib.ws_dropout_mask(key, M, K, _ptr(mask), _stream(stream)))
+    return mask
+
+
+class LoraSet:
+    """The adapters of one linear (ws_lora_set): A [n, 16, K], B [n, N, 16], both fp32 or both
+    bf16 (serving only), scale fp32 [n] (alpha/r; with dropout alpha/r/(1-p)).  The first
+    dimension may have any stride that is a multiple of 8 (a slice of a pool of adapters)."""
+
+    def __init__(self, A, B, scale):
+        _need(A.dim() == 3 and B.dim() == 3 and A.shape[0] == B.shape[0], "A [n, r, K], B [n, N, r]")
+        n, r, K = A.shape
+        N = B.shape[1]
+        _need(B.shape[2] == r, "A and B have different ranks")
+        _need(A.dtype == B.dtype and A.dtype in (torch.float32, torch.bfloat16), "A and B: both fp32 or both bf16")
+        _need(scale.dtype == torch.float32 and tuple(scale.shape) == (n,), "scale: fp32 [n]")
+        _need(n > 0 and A[0].is_contiguous() and B[0].is_contiguous(), "each adapter's A and B must be contiguous")
+        _here(A[0], B[0], scale)
+        self.A, self.B, self.scale = A, B, scale
+        self.n, self.r, self.K, self.N = n, r, K, N
+        sa, sb = (A.stride(0), B.stride(0)) if n > 1 else (r * K, r * N)
+        self.c = LoraSetC(A.data_ptr(), B.data_ptr(), scale.data_ptr(), sa, sb, n, r,
+                          WS_DTYPE_F32 if A.dtype == torch.float32 else WS_DTYPE_BF16)
+
+    def empty_grads(self):
+        """(dA, dB) with the strides of A and B."""
+        return (torch.empty_strided(self.A.shape, self.A.stride(), dtype=torch.float32, device=self.A.device),
+                torch.empty_strided(self.B.shape, self.B.stride(), dtype=torch.float32, device=self.B.device))
+
+
+class LoraPlan:
+    """A batch's rows sorted by adapter (ws_lora_plan), shared by all linears the batch passes."""
+
+    def __init__(self, data, M, n_adapters):
+        self.data, self.M, self.n = data, M, n_adapters
+        self.c = LoraPlanC(data.data_ptr(), M, n_adapters)
+
+
+def lora_multi_plan(row_adapter, n_adapters: int, plan: LoraPlan = None, stream=None) -> LoraPlan:
+    """ws_lora_multi_plan_init from row_adapter int32 [M]; `plan` (of the same M and n) is refilled."""
+    _here(row_adapter)
+    _need(row_adapter.dtype == torch.int32 and row_adapter.dim() == 1, "row_adapter: int32 [M]")
+    M = row_adapter.shape[0]
+    if plan is None:
+        n = C.c_size_t(0)
+        _check("ws_lora_multi_plan_size", _lib.ws_lora_multi_plan_size(M, n_adapters, C.byref(n)))
+        plan = LoraPlan(_empty((int(n.value) // 4,), torch.int32, row_adapter.device, stream), M, n_adapters)
+    _need(plan.M == M and plan.n == n_adapters, "the plan was made for another M or number of adapters")
+    _check("ws_lora_multi_plan_init",
+           _lib.ws_lora_multi_plan_init(C.byref(plan.c), _ptr(row_adapter), _stream(stream)))
+    return plan
+
+
+def lora_multi_workspace_size(M: int, N: int, K: int, n_adapters: int) -> int:
+    n = C.c_size_t(0)
+    _check("ws_lora_multi_workspace_size",
+           _lib.ws_lora_multi_workspace_size(M, N, K, n_adapters, C.byref(n)))
+    return int(n.value)
+
+
+def _multi_checks(W, x, aset, plan, mask):
+    _need(isinstance(W, NF4Weight), "the base must be an NF4Weight")
+    _need(aset.N == W.N and aset.K == W.K, "the adapters' shapes are not the weight's")
+    _need(plan.n == aset.n, "the plan was made for another number of adapters")
+    _need(x.dtype == torch.bfloat16 and tuple(x.shape) == (plan.M, W.K), "x: bf16 [M, K] with the plan's M")
+    if mask is not None:
+        _need(mask.dtype == torch.int32 and tuple(mask.shape) == (plan.M, W.K // 32), "mask: int32 [M, K/32]")
+
+
+def lora_linear_fwd_multi(W: NF4Weight, x, aset: LoraSet, plan: LoraPlan, mask=None, y=None, U=None,
+                          workspace=None, stream=None):
+    """ws_lora_linear_fwd_multi: row m of x [M, K] through the frozen W and its own adapter.
+    Returns (y bf16 [M, N], U fp32 [M, 16])."""
+    _multi_checks(W, x, aset, plan, mask)
+    M = plan.M
+    if y is None:
+        y = _empty((M, W.N), torch.bfloat16, x.device, stream)
+    if U is None:
+        U = _empty((M, aset.r), torch.float32, x.device, stream)
+    if workspace is None:
+        workspace = _empty((lora_multi_workspace_size(M, W.N, W.K, aset.n),), torch.uint8, x.device, stream)
+    _need(y.dtype == torch.bfloat16 and tuple(y.shape) == (M, W.N), "y: bf16 [M, N]")
+    _need(U.dtype == torch.float32 and tuple(U.shape) == (M, aset.r), "U: fp32 [M, 16]")
+    _here(x, mask, y, U, workspace, W.codes, W.absmax)
+    w = W.c()
+    _check("ws_lora_linear_fwd_multi",
+           _lib.ws_lora_linear_fwd_multi(C.byref(w), _ptr(x), C.byref(aset.c), C.byref(plan.c), _ptr(mask),
+                                         _ptr(y), _ptr(U), _ptr(workspace), workspace.nbytes,
+                                         _stream(stream)))
+    return y, U
+
+
+def lora_linear_bwd_multi(W: NF4Weight, x, aset: LoraSet, plan: LoraPlan, U, dY, mask=None, dX=None,
+                          dX_f32=False, accumulate=False, dA=None, dB=None, workspace=None,
+                          stream=None, grad_accumulate=False):
+    """ws_lora_linear_bwd_multi: (dX, dA, dB) for the upstream gradient dY bf16 [M, N], given the
+    forward's U and mask.  dA and dB have the strides of the set's A and B.  accumulate: add into the
+    given fp32 dX; grad_accumulate: add into the given dA and dB."""
+    _multi_checks(W, x, aset, plan, mask)
+    M = plan.M
+    _need(not accumulate or dX is not None, "accumulate needs a dX to add into")
+    _need(not grad_accumulate or (dA is not None and dB is not None), "grad_accumulate needs dA and dB")
+    _need(dY.dtype == torch.bfloat16 and tuple(dY.shape) == (M, W.N), "dY: bf16 [M, N]")
+    _need(U.dtype == torch.float32 and tuple(U.shape) == (M, aset.r), "U: fp32 [M, 16]")
+    if dX is None:
+        dX = _empty((M, W.K), torch.float32 if dX_f32 else torch.bfloat16, x.device, stream)
+    _need(tuple(dX.shape) == (M, W.K) and dX.dtype in (torch.float32, torch.bfloat16), "dX: fp32 or bf16 [M, K]")
+    if dA is None or dB is None:
+        gA, gB = aset.empty_grads()
+        dA, dB = gA if dA is None else dA, gB if dB is None else dB
+    for g, p, name in ((dA, aset.A, "dA"), (dB, aset.B, "dB")):
+        _need(g.dtype == torch.float32 and g.shape == p.shape and g[0].is_contiguous()
+              and (aset.n == 1 or g.stride(0) == p.stride(0)), f"{name}: fp32 with the shape and strides of the set's")
+    if workspace is None:
+        workspace = _empty((lora_multi_workspace_size(M, W.N, W.K, aset.n),), torch.uint8, x.device, stream)
+    _here(x, mask, U, dY, dX, dA[0], dB[0], workspace, W.codes, W.absmax)
+    w = W.c()
+    dt = WS_DTYPE_F32 if dX.dtype == torch.float32 else WS_DTYPE_BF16
+    _check("ws_lora_linear_bwd_multi",
+           _lib.ws_lora_linear_bwd_multi(C.byref(w), _ptr(x), C.byref(aset.c), C.byref(plan.c), _ptr(mask),
+                                         _ptr(U), _ptr(dY), _ptr(dX), dt,
+                                         (WS_ACC_DX if accumulate else 0)
+                                         | (WS_ACC_GRADS if grad_accumulate else 0),
+                                         _ptr(dA), _ptr(dB), _ptr(workspace), workspace.nbytes,
+                                         _stream(stream)))
+    return dX, dA, dB
+
+
+# ------------------------------------------------------------------------------ AdamW
+WS_ADAMW_CLIP = 1
+ADAMW_BLOCK = 256  # elements of one 8-bit state block
+
+
+def adamw_groups(groups, device="cuda"):
+    """ws_adamw_group array (float64 [n_groups, 8], device) from dicts with lr and, optionally, beta1,
+    beta2, eps, weight_decay, max_norm (0: none), step (steps taken).  Columns in that order."""
+    d = dict(beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, max_norm=0.0, step=0)
+    names = ("lr", "beta1", "beta2", "eps", "weight_decay", "max_norm", "step")
+    rows = []
+    for g in groups:
+        _need(set(g) <= set(names) and "lr" in g, f"a group has lr and any of {names[1:]}")
+        rows.append([float({**d, **g}[k]) for k in names] + [0.0])
+    return torch.tensor(rows, dtype=torch.float64, device=device)
+
+
+class AdamWPlan:
+    """Device plan of an AdamW step over many tensors (ws_adamw_plan) with its workspace.  Keeps the
+    tensors; a step reads and writes them where they are."""
+
+    def __init__(self, params, grads, exp_avg, exp_avg_sq, groups=None, exp_avg_scales=None,
+                 exp_avg_sq_scales=None, n_groups=None):
+        n = len(params)
+        groups = [0] * n if groups is None else [int(g) for g in groups]
+        lists = [params, grads, exp_avg, exp_avg_sq, groups]
+        eight = exp_avg_scales is not None or exp_avg_sq_scales is not None
+        if eight:
+            _need(exp_avg_scales is not None and exp_avg_sq_scales is not None, "8-bit states need both scale lists")
+            lists += [exp_avg_scales, exp_avg_sq_scales]
+        _need(n > 0 and all(len(x) == n for x in lists), "lists of one length, at least one tensor")
+        f = {torch.float32: WS_DTYPE_F32, torch.bfloat16: WS_DTYPE_BF16}
+        pd, gd = params[0].dtype, grads[0].dtype
+        _need(pd in f and gd in f, "parameters and gradients: fp32 or bf16")
+        arr = (AdamwTensorC * n)()
+        for i in range(n):
+            p, g, m, v = params[i], grads[i], exp_avg[i], exp_avg_sq[i]
+            _here(p, g, m, v)
+            _need(p.dtype == pd and g.dtype == gd, "one type of parameters and one of gradients a plan")
+            _need(p.numel() == g.numel() == m.numel() == v.numel(), "p, g and the states have one size")
+            ms = vs = None
+            if eight:
+                ms, vs = exp_avg_scales[i], exp_avg_sq_scales[i]
+                _here(ms, vs)
+                _need(m.element_size() == 1 and v.element_size() == 1, "8-bit states are one byte an element")
+                nb = -(-p.numel() // ADAMW_BLOCK)
+                _need(ms.dtype == vs.dtype == torch.float32 and ms.numel() == vs.numel() == nb,
+                      "scales: fp32 [ceil(n/256)]")
+            else:
+                _need(m.dtype == v.dtype == torch.float32, "32-bit states are fp32")
+            arr[i] = AdamwTensorC(p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(),
+                                  ms.data_ptr() if eight else None, vs.data_ptr() if eight else None,
+                                  p.numel(), groups[i], 0)
+        ng = max(groups) + 1 if n_groups is None else n_groups
+        ty = AdamwTypesC(f[pd], f[gd], 8 if eight else 32)
+        pb, wb = C.c_size_t(0), C.c_size_t(0)
+        _check("ws_adamw_plan_size",
+               _lib.ws_adamw_plan_size(arr, n, ng, ty, C.byref(pb), C.byref(wb)))
+        image = torch.empty(int(pb.value), dtype=torch.uint8)
+        self.c = AdamwPlanC()
+        _check("ws_adamw_plan_init",
+               _lib.ws_adamw_plan_init(arr, n, ng, ty, _ptr(image), image.numel(), C.byref(self.c)))
+        self.image = image.to(params[0].device)
+        self.c.image = self.image.data_ptr()
+        self.workspace = torch.empty(int(wb.value), dtype=torch.uint8, device=params[0].device)
+        self.n_groups = ng
+        self.tensors = (params, grads, exp_avg, exp_avg_sq, exp_avg_scales, exp_avg_sq_scales)
+
+
+def adamw_plan(params, grads, exp_avg, exp_avg_sq, groups=None, exp_avg_scales=None,
+               exp_avg_sq_scales=None, n_groups=None) -> AdamWPlan:
+    """Plan of an AdamW step over lists of tensors; groups: each tensor's group.  States: fp32, or 8-bit
+    codes (one byte an element) with fp32 scales [ceil(n/256)]; zeros to begin with."""
+    return AdamWPlan(params, grads, exp_avg, exp_avg_sq, groups, exp_avg_scales, exp_avg_sq_scales, n_groups)
+
+
+def adamw_step(plan: AdamWPlan, groups, norms=None, clip=False, workspace=None, stream=None):
+    """ws_adamw_step: one step of every tensor of the plan.  groups: adamw_groups' tensor (its step column
+    advances); norms (fp32 [n_groups]): receives the gradient norms; clip: by each group's max_norm.
+    The plan's own workspace serves one call at a time; steps of one plan that may overlap (two streams)
+    would race on its tensors anyway."""
+    ws = plan.workspace if workspace is None else workspace
+    _need(groups.dtype == torch.float64 and tuple(groups.shape) == (plan.n_groups, 8), "groups: float64 [n_groups, 8]")
+    _need(norms is None or (norms.dtype == torch.float32 and norms.numel() == plan.n_groups), "norms: fp32 [n_groups]")
+    _here(groups, norms, ws, plan.image)
+    _check("ws_adamw_step",
+           _lib.ws_adamw_step(C.byref(plan.c), _ptr(groups), WS_ADAMW_CLIP if clip else 0, _ptr(norms),
+                              _ptr(ws), ws.nbytes, _stream(stream)))
+
+
+def _adamw_codes(codes, scales):
+    _need(codes.element_size() == 1 and scales.dtype == torch.float32
+          and scales.numel() == -(-codes.numel() // ADAMW_BLOCK), "codes: one byte an element; scales: fp32 [ceil(n/256)]")
+
+
+def adamw_encode8(values, root: bool, codes=None, scales=None, stream=None):
+    """ws_adamw_encode8: fp32 first moments, or (root) square roots of second moments, as 8-bit codes
+    (e4m3 / uint8) and fp32 block scales."""
+    _need(values.dtype == torch.float32 and values.numel() > 0, "values: fp32")
+    n = values.numel()
+    if codes is None:
+        codes = _empty(values.shape, torch.uint8 if root else torch.float8_e4m3fn, values.device, stream)
+    if scales is None:
+        scales = _empty((-(-n // ADAMW_BLOCK),), torch.float32, values.device, stream)
+    _here(values, codes, scales)
+    _adamw_codes(codes, scales)
+    _need(codes.numel() == n, "codes: one a value")
+    _check("ws_adamw_encode8", _lib.ws_adamw_encode8(_ptr(values), n, 1 if root else 0, _ptr(codes),
+                                                     _ptr(scales), _stream(stream)))
+    return codes, scales
+
+
+def adamw_decode8(codes, scales, root: bool, out=None, dtype=torch.float32, stream=None):
+    """ws_adamw_decode8: the values (fp32 or bf16) that 8-bit codes stand for; root: of sqrt(v)."""
+    if out is None:
+        out = _empty(codes.shape, dtype, codes.device, stream)
+    _need(out.dtype in (torch.float32, torch.bfloat16) and out.numel() == codes.numel() > 0,
+          "out: fp32 or bf16, one value a code")
+    _here(codes, scales, out)
+    _adamw_codes(codes, scales)
+    _check("ws_adamw_decode8",
+           _lib.ws_adamw_decode8(_ptr(codes), _ptr(scales), codes.numel(), 1 if root else 0, _ptr(out),
+                                 WS_DTYPE_F32 if out.dtype == torch.float32 else WS_DTYPE_BF16,
+                                 _stream(stream)))
     return out
 
 
