@@ -324,7 +324,11 @@ def _own(s):
                                                dX=s["dX"], dA=s["dA"], dB=s["dB"], workspace=s["ws"])
         return dict(dX=dx, dA=da, dB=db)
     ops.adamw_step(s["plan"], s["groups"], clip=c["clip"], norms=s["norms"] if c["clip"] else None)
-    return dict({"norms": s["norms"]} if c["clip"] else {}, p=s["p"], **_states(s))
+    out = dict({"norms": s["norms"]} if c["clip"] else {}, p=s["p"])
+    if c["bits"] == 32:
+        return dict(out, m=s["m"], v=s["v"])
+    return dict(out, m=ops.adamw_decode8(s["m"], s["ms"], False, dtype=torch.bfloat16), m_scale=s["ms"],
+                r=ops.adamw_decode8(s["v"], s["vs"], True, dtype=torch.bfloat16), r_scale=s["vs"])
 
 
 def run(state):
