@@ -289,6 +289,45 @@ def test_masks_are_those_of_the_single_adapter_linear(ops):
         assert float((p - q).norm()) <= 1e-4 * float(p.norm())
 
 
+@pytest.mark.parametrize("M", [3, 60, 200, 400])
+@pytest.mark.parametrize("n", [3, 40])
+def test_a_diverged_adapter_stays_alone(ops, M, n):
+    """NaN and infinities in one adapter (and in a dropped element of x) reach no row of another."""
+    N, K = 128, 192
+    c = Case(ops, M, N, K, n, "distinct", mask=True, seed=M)
+    good = Case(ops, M, N, K, n, "distinct", mask=True, seed=M)
+    c.B[1, 5, 3], c.B[1, 70, :] = float("nan"), float("inf")
+    c.A[1, 2, 9] = float("-inf")
+    r = c.rows.to(dev()).long()
+    bad = r == 1
+    y0, U0 = ops.lora_linear_fwd_multi(good.W, good.x, good.set, good.plan, mask=good.mask)
+    y1, U1 = ops.lora_linear_fwd_multi(c.W, c.x, c.set, c.plan, mask=c.mask)
+    assert torch.equal(y0[~bad], y1[~bad]) and torch.equal(U0[~bad], U1[~bad])
+    assert not torch.isfinite(y1[bad][:, 5]).any() and not torch.isfinite(y1[bad][:, 70]).any()
+    U = good.forward()["U"].float()
+    g0 = ops.lora_linear_bwd_multi(good.W, good.x, good.set, good.plan, U, good.dY, mask=good.mask, dX_f32=True)
+    g1 = ops.lora_linear_bwd_multi(c.W, c.x, c.set, c.plan, U, c.dY, mask=c.mask, dX_f32=True)
+    others = torch.arange(n, device=dev()) != 1
+    assert torch.equal(g0[0][~bad], g1[0][~bad])
+    assert torch.equal(g0[1][others], g1[1][others]) and torch.equal(g0[2], g1[2])
+    assert torch.isnan(g1[1][1]).any() == bad.any()
+    # only B's diverged rows: A and U are finite, so only these columns of y are not
+    c2 = Case(ops, M, N, K, n, "distinct", mask=True, seed=M)
+    c2.B[1, 5, 3] = float("nan")
+    y2, _ = ops.lora_linear_fwd_multi(c2.W, c2.x, c2.set, c2.plan, mask=c2.mask)
+    keep = torch.ones(N, dtype=torch.bool, device=dev())
+    keep[5] = False
+    assert torch.equal(y2[:, keep], y0[:, keep]) and torch.isnan(y2[bad][:, 5]).all() and torch.equal(y2[~bad], y0[~bad])
+    # a dropped element of x: the adapter does not see it, the frozen base does
+    c3 = Case(ops, M, N, K, n, "distinct", mask=True, seed=M)
+    c3.mask[0, 1] &= ~4
+    U3a = ops.lora_linear_fwd_multi(c3.W, c3.x, c3.set, c3.plan, mask=c3.mask)[1]
+    c3.x[0, 34] = float("nan")
+    y3, U3 = ops.lora_linear_fwd_multi(c3.W, c3.x, c3.set, c3.plan, mask=c3.mask)
+    assert torch.equal(U3, U3a) and torch.isfinite(y3[1:]).all()
+    assert ops.device_error() == 0
+
+
 @pytest.mark.parametrize("M", [5, 40, 150, 600])
 def test_another_stream_and_a_captured_call(ops, M):
     """plan, forward and backward on a side stream, captured once and replayed with other rows and inputs."""

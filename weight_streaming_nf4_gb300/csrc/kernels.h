@@ -58,6 +58,38 @@ struct GemmArgs {
   const float* gabsmax[kMaxGroups];
   const float* glora_F[kMaxGroups];
   void* gout[kMaxGroups];
+  // Rows with different adapters (kernels instantiated for it; see
+  // lora_multi.cu): row m adds s_a * ml_P[m] . F_a with a = ml_row[m] (none
+  // below 0), F_a at ml_F + a * ml_stride elements ([N, 16] or [16, K]).
+  // *ml_slots = L >= 0: tile row mt has at most L adapters, listed at
+  // ml_tile_ad[mt * kMultiSlots ..] (-1: none); each tile then runs L LoRA
+  // steps, step l with the rows of its l-th adapter (the lora map's rows l*M +
+  // m hold row m's split factor, or zeros).  L < 0: too many adapters; the
+  // epilogue adds the term.
+  const float* ml_P;       // U or G [M, 16]
+  const void* ml_F;
+  const float* ml_scale;   // [adapters]
+  const int32_t* ml_row;   // [M]
+  const int32_t* ml_slots;
+  const int32_t* ml_tile_ad;
+  uint32_t* ml_bad;        // set when an F value is left to the epilogue (see lora_tile_ml)
+  int64_t ml_stride;
+  int ml_f16;              // ml_F is bf16
+};
+
+// The adapter term of run_nf4_gemm_multi (see GemmArgs::ml_*).
+constexpr int kMultiSlots = 16;  // adapters of one tile row that get a tensor-core step each
+struct MultiLora {
+  const float* P;
+  const uint16_t* ext;  // [kMultiSlots][M][64] bf16 split factor by slot
+  const void* F;
+  const float* scale;
+  const int32_t* row;
+  const int32_t* slots;
+  const int32_t* tile_ad;
+  uint32_t* bad;
+  int64_t stride;
+  int f16;
 };
 
 // Tile configuration: a pure function of the shape and the SM count, so a
@@ -97,6 +129,14 @@ cudaError_t run_nf4_gemm(const GemmPlan& p, const NF4View& W, const uint16_t* ac
                          const uint16_t* lora_act, const float* lora_F, float lora_scale,
                          const uint32_t* mask, void* out, int out_f32, int out_accum,
                          float* partial, cudaStream_t st);
+
+// The same product with rows of different adapters: out = act . W'^T (or act .
+// W') + the adapter term (under `mask` in the backward), one rounding.
+// Rows of one tile row of that product (a function of M and the device).
+int64_t gemm_tile_rows(int64_t M);
+cudaError_t run_nf4_gemm_multi(const GemmPlan& p, const NF4View& W, const uint16_t* act, int64_t M,
+                               const MultiLora& ml, const uint32_t* mask, void* out, int out_f32,
+                               int out_accum, float* partial, cudaStream_t st);
 
 // Forward of ng linears sharing the activation act [M, K] in one launch:
 // out[g] = act . W[g]'^T + s * lora_act[g] . F[g]^T, lora_act [ng][M][64]

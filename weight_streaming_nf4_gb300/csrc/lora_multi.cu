@@ -21,13 +21,16 @@ size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 bool al16p(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // ------------------------------------------------------------------------ the batch's plan
-// Sections of the plan buffer (int32 words): header {tiles}, the adapter of
-// each row (-1: none), the rows sorted by adapter (stable; rows without one
+// Sections of the plan buffer (int32 words): header {tiles, slots}, the adapter
+// of each row (-1: none), the rows sorted by adapter (stable; rows without one
 // last), each adapter's first position in that order (n + 1 entries: the last
-// is where the rows without an adapter begin), and tiles {adapter, first
-// position, rows, 0} of at most kTileRows rows of one adapter.
+// is where the rows without an adapter begin), tiles {adapter, first position,
+// rows, 0} of at most kTileRows rows of one adapter; and for the tensor-core
+// steps of the GEMM each row's slot and, for each of its tile rows, the
+// adapters of its slots (in order of their first row; -1: none).  slots: the
+// most adapters of any tile row, or -1 if one has more than kMultiSlots.
 struct PlanLayout {
-  int64_t row, perm, off, tile, words;
+  int64_t row, perm, off, tile, slot, tile_ad, words;
   int64_t max_tiles;
 };
 PlanLayout plan_layout(int64_t M, int64_t n) {
@@ -39,7 +42,9 @@ PlanLayout plan_layout(int64_t M, int64_t n) {
   L.perm = L.row + up4(M);
   L.off = L.perm + up4(M);
   L.tile = L.off + up4(n + 1);
-  L.words = L.tile + 4 * L.max_tiles;
+  L.slot = L.tile + 4 * L.max_tiles;
+  L.tile_ad = L.slot + up4(M);
+  L.words = L.tile_ad + kMultiSlots * ((M + 127) / 128);  // tile rows are 128 rows or more
   return L;
 }
 
@@ -48,14 +53,17 @@ PlanLayout plan_layout(int64_t M, int64_t n) {
 // so that equal adapters keep the row order.
 __global__ void __launch_bounds__(kPlanThreads)
     k_multi_plan(const int32_t* __restrict__ row_adapter, int M, int n, int32_t* __restrict__ plan,
-                 int64_t o_row, int64_t o_perm, int64_t o_off, int64_t o_tile) {
+                 int64_t o_row, int64_t o_perm, int64_t o_off, int64_t o_tile, int64_t o_slot,
+                 int64_t o_tile_ad, int tile_rows) {
   pdl_wait();
   pdl_launch_dependents();
   // position counters of the adapters and, at [n], of the rows without one
   __shared__ int pos[WS_MULTI_MAX_ADAPTERS + 1];
   __shared__ int wsum[2][32];
+  __shared__ int most_slots, too_many;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i <= n; i += kPlanThreads) pos[i] = 0;
+  if (tid == 0) most_slots = too_many = 0;
   __syncthreads();
   for (int i = tid; i < M; i += kPlanThreads) {
     const int a = row_adapter[i];
@@ -122,6 +130,42 @@ __global__ void __launch_bounds__(kPlanThreads)
       __syncthreads();
     }
   }
+  // slots: one warp per tile row collects its adapters, 32 rows at a time
+  for (int mt = warp; mt * (int64_t)tile_rows < M; mt += kPlanThreads / 32) {
+    int32_t* list = plan + o_tile_ad + (int64_t)mt * kMultiSlots;
+    int mine = -1, used = 0;  // lane l holds slot l's adapter
+    const int end = min(M, (mt + 1) * tile_rows);
+    for (int b = mt * tile_rows; b < end && used <= kMultiSlots; b += 32) {
+      const int i = b + lane;
+      int a = i < end ? row_adapter[i] : -1;
+      if (a < 0 || a >= n) a = -1;
+      int slot = -1;
+      for (;;) {
+        // lanes whose adapter has no slot yet
+        for (int l = 0; l < used; ++l) {
+          const int has = __shfl_sync(0xffffffffu, mine, l);
+          if (a >= 0 && has == a) slot = l;
+        }
+        const uint32_t open = __ballot_sync(0xffffffffu, a >= 0 && slot < 0);
+        if (!open) break;
+        const int next = __shfl_sync(0xffffffffu, a, __ffs((int)open) - 1);
+        if (used == kMultiSlots) {
+          ++used;
+          break;
+        }
+        if (lane == used) mine = next;
+        ++used;
+      }
+      if (i < end) plan[o_slot + i] = slot;
+    }
+    if (lane < kMultiSlots) list[lane] = mine;
+    if (lane == 0) {
+      if (used > kMultiSlots) atomicOr(&too_many, 1);
+      else atomicMax(&most_slots, used);
+    }
+  }
+  __syncthreads();
+  if (tid == 0) plan[1] = too_many ? -1 : most_slots;
 }
 
 // ------------------------------------------------------------------------ mma.sync pieces
@@ -165,20 +209,41 @@ template <bool F_CJ, bool F16, bool MASKED>
 __global__ void __launch_bounds__(kSkWarps * 32)
     k_multi_skinny(const uint16_t* __restrict__ X, const void* __restrict__ Fv, int64_t strideF,
                    int C, const uint32_t* __restrict__ mask, const int32_t* __restrict__ plan,
-                   int64_t o_perm, int64_t o_tile, float* __restrict__ out) {
+                   int64_t o_perm, int64_t o_tile, int64_t o_slot, float* __restrict__ out,
+                   uint32_t* __restrict__ ext, int64_t M, uint32_t* __restrict__ bad) {
   __shared__ float part[kSkWarps][kTileRows * kR];
   __shared__ float sum[kTileRows * kR];
   const int lane = (int)lane_id(), warp = (int)warp_id(), g = lane >> 2, t = lane & 3;
   const int CS = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
   pdl_wait();
   pdl_launch_dependents();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *bad = 0u;  // for the GEMM that follows
   if ((int)blockIdx.y >= plan[0]) return;  // the whole cluster alike
   const int4 tile = *reinterpret_cast<const int4*>(plan + o_tile + 4 * (int64_t)blockIdx.y);
   const int32_t* rows = plan + o_perm + tile.y;
   const int cnt = tile.z, nsub = (cnt + 15) / 16;
+  const int slots = plan[1];
+  // a pair of results (r, j), (r, j + 1), i = r * 16 + j: fp32, and split into
+  // bf16 parts [hi | lo | hi | 0] in the row's slot, zeros in the others
+  auto put = [&](int i, float v0, float v1) {
+    const int64_t row = rows[i / kR];
+    const int j = i % kR;
+    *reinterpret_cast<float2*>(out + row * kR + j) = make_float2(v0, v1);
+    if (slots <= 0) return;
+    const int own = plan[o_slot + row];
+    uint32_t hi, lo;
+    split2(v0, v1, hi, lo);
+    for (int l = 0; l < slots; ++l) {
+      uint32_t* e = ext + ((int64_t)l * M + row) * 32 + j / 2;
+      e[0] = l == own ? hi : 0u;
+      e[8] = l == own ? lo : 0u;
+      e[16] = l == own ? hi : 0u;
+      e[24] = 0u;
+    }
+  };
   if (tile.x < 0) {  // rows without an adapter
     if (rank == 0)
-      for (int i = threadIdx.x; i < cnt * kR; i += kSkWarps * 32) out[(int64_t)rows[i / kR] * kR + i % kR] = 0.0f;
+      for (int i = 2 * threadIdx.x; i < cnt * kR; i += 2 * kSkWarps * 32) put(i, 0.0f, 0.0f);
     return;
   }
   float acc[4][2][4] = {};
@@ -267,26 +332,31 @@ __global__ void __launch_bounds__(kSkWarps * 32)
   }
   __syncthreads();
   const int elems = cnt * kR;
-  for (int i = threadIdx.x; i < elems; i += kSkWarps * 32) {
-    float s = 0.0f;
+  for (int i = 2 * threadIdx.x; i < elems; i += 2 * kSkWarps * 32) {
+    float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int w = 0; w < kSkWarps; ++w) s += part[w][i];
-    if (CS == 1) out[(int64_t)rows[i / kR] * kR + i % kR] = s;
-    else sum[i] = s;
+    for (int w = 0; w < kSkWarps; ++w) {
+      const float2 p = *reinterpret_cast<const float2*>(&part[w][i]);
+      s.x += p.x;
+      s.y += p.y;
+    }
+    if (CS == 1) put(i, s.x, s.y);
+    else *reinterpret_cast<float2*>(&sum[i]) = s;
   }
   if (CS == 1) return;
   cluster_sync();
-  for (int i = rank * kSkWarps * 32 + threadIdx.x; i < elems; i += CS * kSkWarps * 32) {
-    float s = 0.0f;
+  for (int i = 2 * (rank * kSkWarps * 32 + threadIdx.x); i < elems; i += 2 * CS * kSkWarps * 32) {
+    float2 s = make_float2(0.0f, 0.0f);
     for (int c = 0; c < CS; ++c) {
-      float v;
-      asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                   : "=f"(v)
+      float x, y;
+      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                   : "=f"(x), "=f"(y)
                    : "r"(mapa_shared(smem_u32(&sum[i]), (uint32_t)c))
                    : "memory");
-      s += v;
+      s.x += x;
+      s.y += y;
     }
-    out[(int64_t)rows[i / kR] * kR + i % kR] = s;
+    put(i, s.x, s.y);
   }
   cluster_sync();  // the sums stay until every CTA of the cluster has read them
 }
@@ -398,58 +468,18 @@ __global__ void __launch_bounds__(kWgWarps * 32) k_multi_wgrad(const WgArgs w) {
   }
 }
 
-// ------------------------------------------------------------------------ adapter term of y and dX
-// out = base + the adapter term, one rounding.  FWD: + s_a sum_j U[m][j]
-// B_a[n][j]; else + mask . s_a sum_j G[m][j] A_a[j][k].  Four columns per thread.
-template <bool FWD, bool F16, bool O16>
-__global__ void __launch_bounds__(256)
-    k_multi_add(const float* base, const float* __restrict__ P, const void* __restrict__ Fv,
-                int64_t strideF, const float* __restrict__ scale, const uint32_t* __restrict__ mask,
-                const int32_t* __restrict__ row_adapter, int C, void* out) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int64_t m = blockIdx.x;
-  const int c = ((int)blockIdx.y * 256 + (int)threadIdx.x) * 4;
-  if (c >= C) return;
-  const int a = row_adapter[m];
-  float4 v = *reinterpret_cast<const float4*>(base + m * C + c);
-  if (a >= 0) {
-    float d[4] = {};
-    for (int j = 0; j < kR; ++j) {
-      const float u = P[m * kR + j];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t o = a * strideF + (FWD ? (int64_t)(c + e) * kR + j : (int64_t)j * C + c + e);
-        const float f = F16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(Fv)[o]) : static_cast<const float*>(Fv)[o];
-        d[e] = fmaf(u, f, d[e]);
-      }
-    }
-    const float s = scale[a];
-    uint32_t b = 15u;
-    if (!FWD && mask) b = mask[(m * C + c) >> 5] >> (c & 31);
-    v.x += (b & 1u) ? s * d[0] : 0.0f;
-    v.y += (b & 2u) ? s * d[1] : 0.0f;
-    v.z += (b & 4u) ? s * d[2] : 0.0f;
-    v.w += (b & 8u) ? s * d[3] : 0.0f;
-  }
-  if (O16)
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + m * C + c) =
-        make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-  else
-    *reinterpret_cast<float4*>(static_cast<float*>(out) + m * C + c) = v;
-}
-
 // ------------------------------------------------------------------------ host side
 struct WsLayout {
-  size_t G, base, partial, total;
+  size_t G, ext, bad, partial, total;
 };
 WsLayout ws_layout(int64_t M, int64_t N, int64_t K) {
   WsLayout L{};
   const GemmPlan f = plan_gemm(false, M, N, K), b = plan_gemm(true, M, K, N);
   const size_t pf = gemm_partial_bytes(f, M, N), pb = gemm_partial_bytes(b, M, K);
   L.G = 0;
-  L.base = al256((size_t)M * kR * 4);
-  L.partial = L.base + al256((size_t)M * (size_t)(N > K ? N : K) * 4);
+  L.ext = al256((size_t)M * kR * 4);
+  L.bad = L.ext + (size_t)M * kMultiSlots * 128;
+  L.partial = L.bad + 256;
   L.total = L.partial + al256(pf > pb ? pf : pb);
   return L;
 }
@@ -481,14 +511,35 @@ int skinny_cluster(int64_t C) {
 }
 
 cudaError_t run_skinny(bool f_cj, const uint16_t* X, const void* F, bool f16, int64_t strideF, int64_t C,
-                       const uint32_t* mask, const ws_lora_plan& plan, float* out, cudaStream_t st) {
+                       const uint32_t* mask, const ws_lora_plan& plan, float* out, uint8_t* ws,
+                       const WsLayout& W, cudaStream_t st) {
   const PlanLayout L = plan_layout(plan.M, plan.n_adapters);
   const int cs = skinny_cluster(C);
   auto k = f_cj ? k_multi_skinny<true, false, false>
                 : (f16 ? (mask ? k_multi_skinny<false, true, true> : k_multi_skinny<false, true, false>)
                        : (mask ? k_multi_skinny<false, false, true> : k_multi_skinny<false, false, false>));
   return launch_cluster(k, dim3((unsigned)cs, (unsigned)L.max_tiles), kSkWarps * 32, cs, st, X, F, strideF,
-                        (int)C, mask, (const int32_t*)plan.data, L.perm, L.tile, out);
+                        (int)C, mask, (const int32_t*)plan.data, L.perm, L.tile, L.slot, out,
+                        reinterpret_cast<uint32_t*>(ws + W.ext), plan.M, reinterpret_cast<uint32_t*>(ws + W.bad));
+}
+
+// The GEMM's view of the adapter term with P = U or G and F = B or A.
+MultiLora multi_of(const ws_lora_plan& plan, uint8_t* ws, const WsLayout& W, const float* P, const void* F, bool f16,
+                   int64_t stride, const float* scale) {
+  const PlanLayout L = plan_layout(plan.M, plan.n_adapters);
+  const int32_t* pl = static_cast<const int32_t*>(plan.data);
+  MultiLora m{};
+  m.P = P;
+  m.ext = reinterpret_cast<const uint16_t*>(ws + W.ext);
+  m.F = F;
+  m.scale = scale;
+  m.row = pl + L.row;
+  m.slots = pl + 1;
+  m.tile_ad = pl + L.tile_ad;
+  m.bad = reinterpret_cast<uint32_t*>(ws + W.bad);
+  m.stride = stride;
+  m.f16 = f16 ? 1 : 0;
+  return m;
 }
 
 ws_status check_plan(const ws_lora_plan* p) {
@@ -561,7 +612,8 @@ ws_status ws_lora_multi_plan_init(const ws_lora_plan* plan, const int32_t* row_a
   const PlanLayout L = plan_layout(plan->M, plan->n_adapters);
   note_launch();
   WS_RUN(launch_pdl(k_multi_plan, dim3(1), dim3(kPlanThreads), 0, (cudaStream_t)stream, row_adapter,
-                    (int)plan->M, (int)plan->n_adapters, (int32_t*)plan->data, L.row, L.perm, L.off, L.tile));
+                    (int)plan->M, (int)plan->n_adapters, (int32_t*)plan->data, L.row, L.perm, L.off, L.tile,
+                    L.slot, L.tile_ad, (int)gemm_tile_rows(plan->M)));
   return WS_OK;
 }
 
@@ -589,17 +641,10 @@ ws_status ws_lora_linear_fwd_multi(const ws_nf4* W, const uint16_t* x, const ws_
   cudaStream_t st = (cudaStream_t)stream;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const bool f16 = set->dtype == WS_DTYPE_BF16;
-  WS_RUN(run_skinny(false, x, set->A, f16, set->stride_a, K, mask, *plan, U_saved, st));
-  float* base = reinterpret_cast<float*>(ws + L.base);
-  WS_RUN(run_nf4_gemm(plan_gemm(false, M, N, K), view(W), x, M, nullptr, nullptr, 0.0f, nullptr, base, 1, 0,
-                      reinterpret_cast<float*>(ws + L.partial), st));
-  const int32_t* pl = static_cast<const int32_t*>(plan->data);
-  const PlanLayout P = plan_layout(M, plan->n_adapters);
-  note_launch();
-  WS_RUN(launch_pdl(f16 ? k_multi_add<true, true, true> : k_multi_add<true, false, true>,
-                    dim3((unsigned)M, (unsigned)((N + 1023) / 1024)), dim3(256), 0, st, (const float*)base,
-                    (const float*)U_saved, set->B, set->stride_b, set->scale, (const uint32_t*)nullptr,
-                    pl + P.row, (int)N, (void*)y));
+  WS_RUN(run_skinny(false, x, set->A, f16, set->stride_a, K, mask, *plan, U_saved, ws, L, st));
+  const MultiLora ml = multi_of(*plan, ws, L, U_saved, set->B, f16, set->stride_b, set->scale);
+  WS_RUN(run_nf4_gemm_multi(plan_gemm(false, M, N, K), view(W), x, M, ml, nullptr, y, 0, 0,
+                            reinterpret_cast<float*>(ws + L.partial), st));
   return WS_OK;
 }
 
@@ -625,7 +670,7 @@ ws_status ws_lora_linear_bwd_multi(const ws_nf4* W, const uint16_t* x, const ws_
   const int32_t* pl = static_cast<const int32_t*>(plan->data);
   const PlanLayout P = plan_layout(M, plan->n_adapters);
   float* G = reinterpret_cast<float*>(ws + L.G);
-  WS_RUN(run_skinny(true, dY, set->B, false, set->stride_b, N, nullptr, *plan, G, st));
+  WS_RUN(run_skinny(true, dY, set->B, false, set->stride_b, N, nullptr, *plan, G, ws, L, st));
   WgArgs w{};
   w.P[0] = U_saved, w.P[1] = G;
   w.Q[0] = dY, w.Q[1] = x;
@@ -640,14 +685,9 @@ ws_status ws_lora_linear_bwd_multi(const ws_nf4* W, const uint16_t* x, const ws_
   note_launch();
   WS_RUN(launch_pdl(k_multi_wgrad, dim3((unsigned)((N + K) / 64), (unsigned)set->n_adapters), dim3(kWgWarps * 32),
                     0, st, w));
-  const bool o32 = dX_dtype == WS_DTYPE_F32;
-  float* base = o32 ? static_cast<float*>(dX) : reinterpret_cast<float*>(ws + L.base);
-  WS_RUN(run_nf4_gemm(plan_gemm(true, M, K, N), view(W), dY, M, nullptr, nullptr, 0.0f, nullptr, base, 1,
-                      (accumulate & WS_ACC_DX) ? 1 : 0, reinterpret_cast<float*>(ws + L.partial), st));
-  note_launch();
-  WS_RUN(launch_pdl(o32 ? k_multi_add<false, false, false> : k_multi_add<false, false, true>,
-                    dim3((unsigned)M, (unsigned)((K + 1023) / 1024)), dim3(256), 0, st, (const float*)base,
-                    (const float*)G, set->A, set->stride_a, set->scale, mask, pl + P.row, (int)K, dX));
+  const MultiLora ml = multi_of(*plan, ws, L, G, set->A, false, set->stride_a, set->scale);
+  WS_RUN(run_nf4_gemm_multi(plan_gemm(true, M, K, N), view(W), dY, M, ml, mask, dX, dX_dtype == WS_DTYPE_F32 ? 1 : 0,
+                            (accumulate & WS_ACC_DX) ? 1 : 0, reinterpret_cast<float*>(ws + L.partial), st));
   return WS_OK;
 }
 

@@ -614,7 +614,136 @@ struct WMaps {
   CUtensorMap m[kMaxGroups];
 };
 
-template <bool BWD, int UM, int BN, int PAIR, bool WB>
+// The adapter term of 16 columns from n of one row: v += u . F, with u = s_a
+// P[m] (ML kernels).  Forward: F rows n .. n+15 of B_a [N, 16]; backward:
+// columns of A_a [16, ld], under the keep bits.  Lanes are rows, so lanes of
+// one adapter read the same addresses.
+template <bool BWD>
+WS_DEVINL void ml_add(const GemmArgs& a, int ad, int64_t n, int64_t ld, const float (&u)[16], uint32_t keep,
+                      float (&v)[16]) {
+  if constexpr (BWD) {
+    const float* F = static_cast<const float*>(a.ml_F) + ad * a.ml_stride + n;
+    float d[16] = {};
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 f = __ldg(reinterpret_cast<const float4*>(F + j * ld) + q);
+        d[4 * q] = fmaf(u[j], f.x, d[4 * q]);
+        d[4 * q + 1] = fmaf(u[j], f.y, d[4 * q + 1]);
+        d[4 * q + 2] = fmaf(u[j], f.z, d[4 * q + 2]);
+        d[4 * q + 3] = fmaf(u[j], f.w, d[4 * q + 3]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] += ((keep >> e) & 1u) ? d[e] : 0.0f;
+  } else if (a.ml_f16) {
+    const uint4* F = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.ml_F) + ad * a.ml_stride + n * 16);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint4 f = __ldg(F + 2 * e + q);
+        v[e] = fmaf(u[8 * q], bf16_lo(f.x), v[e]);
+        v[e] = fmaf(u[8 * q + 1], bf16_hi(f.x), v[e]);
+        v[e] = fmaf(u[8 * q + 2], bf16_lo(f.y), v[e]);
+        v[e] = fmaf(u[8 * q + 3], bf16_hi(f.y), v[e]);
+        v[e] = fmaf(u[8 * q + 4], bf16_lo(f.z), v[e]);
+        v[e] = fmaf(u[8 * q + 5], bf16_hi(f.z), v[e]);
+        v[e] = fmaf(u[8 * q + 6], bf16_lo(f.w), v[e]);
+        v[e] = fmaf(u[8 * q + 7], bf16_hi(f.w), v[e]);
+      }
+    }
+  } else {
+    const float4* F = reinterpret_cast<const float4*>(static_cast<const float*>(a.ml_F) + ad * a.ml_stride + n * 16);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 f = __ldg(F + 4 * e + q);
+        v[e] = fmaf(u[4 * q], f.x, v[e]);
+        v[e] = fmaf(u[4 * q + 1], f.y, v[e]);
+        v[e] = fmaf(u[4 * q + 2], f.z, v[e]);
+        v[e] = fmaf(u[4 * q + 3], f.w, v[e]);
+      }
+    }
+  }
+}
+
+// An F value times its scale that the tensor cores must not see: a zero factor
+// of another adapter's row would turn it into NaN there.
+WS_DEVINL bool ml_is_bad(float v) { return !(fabsf(v) <= 3e38f); }
+// The part of the adapter term that such values make, for the row's own
+// adapter (rare: an adapter that has diverged).
+template <bool BWD>
+__device__ __noinline__ float ml_bad_term(const GemmArgs& a, int ad, int64_t n, int64_t ld, int64_t m) {
+  const float s = a.ml_scale[ad];
+  float d = 0.0f;
+  for (int j = 0; j < 16; ++j) {
+    const int64_t o = ad * a.ml_stride + (BWD ? (int64_t)j * ld + n : n * 16 + j);
+    const float f = a.ml_f16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(a.ml_F)[o]) : static_cast<const float*>(a.ml_F)[o];
+    if (ml_is_bad(s * f)) d += a.ml_P[m * 16 + j] * (s * f);
+  }
+  return d;
+}
+// lora_tile for one adapter of many (ad < 0: a tile of zeros), leaving out bad values.
+template <bool BWD, int BN, int PAIR>
+WS_DEVINL void lora_tile_ml(const GemmArgs& a, int ad, int64_t rows_total, int64_t ld, int n0, uint8_t* Bt, int rank,
+                            int t) {
+  constexpr int ROWS = PAIR ? BN / 2 : BN;
+  constexpr int TPR = kDqThreads / ROWS;  // threads per row
+  const int j = t / TPR, part = t % TPR;  // buffer row
+  const int64_t n = (int64_t)n0 + (PAIR ? rank * ROWS : 0) + j;
+  const bool in = ad >= 0 && n < rows_total;
+  const float s = in ? a.ml_scale[ad] : 0.0f;
+  const int64_t base = in ? ad * a.ml_stride + (BWD ? n : n * 16) : 0;
+  bool bad = false;
+  uint32_t hi[8], lo[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float f0 = 0.0f, f1 = 0.0f;
+    if (in) {
+      if constexpr (BWD) {
+        f0 = static_cast<const float*>(a.ml_F)[base + (int64_t)(2 * i) * ld];
+        f1 = static_cast<const float*>(a.ml_F)[base + (int64_t)(2 * i + 1) * ld];
+      } else if (a.ml_f16) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.ml_F) + base + 2 * i);
+        f0 = bf16_lo(w);
+        f1 = bf16_hi(w);
+      } else {
+        const float2 w = *reinterpret_cast<const float2*>(static_cast<const float*>(a.ml_F) + base + 2 * i);
+        f0 = w.x;
+        f1 = w.y;
+      }
+    }
+    f0 *= s;
+    f1 *= s;
+    bad = bad || ml_is_bad(f0) || ml_is_bad(f1);
+    f0 = ml_is_bad(f0) ? 0.0f : f0;
+    f1 = ml_is_bad(f1) ? 0.0f : f1;
+    hi[i] = pack_bf16x2(f0, f1);
+    lo[i] = pack_bf16x2(f0 - bf16_lo(hi[i]), f1 - bf16_hi(hi[i]));
+  }
+  if (bad) {
+    // before the tile is handed over: the epilogue that follows its MMAs sees it
+    atomicOr(a.ml_bad, 1u);
+    __threadfence();
+  }
+#pragma unroll
+  for (int q = 0; q < 8 / TPR; ++q) {
+    const int cc = part * (8 / TPR) + q;
+    uint4 val;
+    if (cc == 0 || cc == 2) val = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    else if (cc == 1 || cc == 3) val = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+    else if (cc == 4) val = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    else if (cc == 5) val = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+    else val = make_uint4(0u, 0u, 0u, 0u);
+    sts128(Bt + j * 128 + ((cc ^ (j & 7)) << 4), val.x, val.y, val.z, val.w);
+  }
+}
+
+// ML: rows of different adapters (GemmArgs::ml_*), no has_lora step.
+template <bool BWD, int UM, int BN, int PAIR, bool WB, bool ML>
 __global__ void __launch_bounds__(kThreads, 1)
     k_nf4_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmL,
                const GemmArgs args, const __grid_constant__ WMaps wm) {
@@ -649,14 +778,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = (int)lane_id();
   const int rank = PAIR ? (int)(cluster_ctarank() & 1u) : 0;
   // ---- static stream-K schedule over units (CTAs, or pairs of CTAs)
-  const int S = args.nk_total + (args.has_lora ? 1 : 0);  // steps per tile
-  // the LoRA step: last in the forward, first in the backward (where it is
-  // masked before the main steps accumulate on top); kc = contraction step
-  const bool lora_first = BWD && args.has_lora;
+  // the LoRA step (ML: steps, as many as the batch needs): last in the
+  // forward, first in the backward (where it is masked before the main steps
+  // accumulate on top); kc = contraction step
+  if constexpr (ML) pdl_wait();  // the number of steps is an earlier kernel's result
+  const int ml_slots = ML ? *args.ml_slots : 0;
+  const int nl = ML ? max(ml_slots, 0) : (args.has_lora ? 1 : 0);
+  const int S = args.nk_total + nl;  // steps per tile
+  const bool lora_first = BWD && nl > 0;
   auto is_lora_step = [&](int i) {
+    if constexpr (ML) return BWD ? i < nl : i >= args.nk_total;
     return args.has_lora && (lora_first ? i == 0 : i == args.nk_total);
   };
-  auto kstep = [&](int i) { return lora_first ? i - 1 : i; };
+  auto kstep = [&](int i) { return lora_first ? i - nl : i; };
+  // slot of a LoRA step (ML)
+  auto lora_slot = [&](int i) { return BWD ? i : i - args.nk_total; };
+  // the epilogue masks the LoRA term before the main steps add on top
+  const bool lora_masks = lora_first && (!ML || args.mask != nullptr);
   const int64_t T = (int64_t)args.mtiles * args.ntiles;
   // ranges are cut over SV = S + epad iterations per tile; the last epad
   // carry no work (a range boundary inside them moves to the next tile)
@@ -734,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------ TMA producer (activations)
       if (lane == 0) {
         tma_prefetch_desc(&tmA);
-        if (args.has_lora) tma_prefetch_desc(&tmL);
+        if (ML || args.has_lora) tma_prefetch_desc(&tmL);
         int64_t issued = 0;
         int s = 0;
         uint32_t ph = 0;
@@ -748,7 +886,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const CUtensorMap* map = is_lora_step(ps.i) ? &tmL : &tmA;
           const int32_t x = is_lora_step(ps.i) ? 0 : kstep(ps.i) * 64;
           // a grouped forward's LoRA activation rows of group g start at g * M
-          const int32_t y = m0 + ((!BWD && is_lora_step(ps.i)) ? (int32_t)(tile_grp(args, (int64_t)ps.nt * BN).g * args.M) : 0);
+          const int32_t y = (ML && is_lora_step(ps.i)) ? m0 + lora_slot(ps.i) * (int32_t)args.M
+                            : m0 + ((!BWD && is_lora_step(ps.i)) ? (int32_t)(tile_grp(args, (int64_t)ps.nt * BN).g * args.M) : 0);
           if constexpr (PM) {
             // both CTAs' tiles complete on the even CTA's barrier
             if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::A_BYTES);
@@ -861,7 +1000,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if constexpr (PAIR == 1) tc_commit_multicast(&bempty[b], (uint16_t)0x3);
               else tc_commit(&bempty[b]);
             }
-            if (BWD && is_lora) {
+            // (ML: after the segment's last LoRA step)
+            if (BWD && is_lora && lora_masks && (!ML || i == nl - 1 || p2 + 1 == seg_end)) {
               // the epilogue masks s G A in TMEM before the main steps add on top
               if constexpr (PM) tc_commit_pair_multicast(lora_done, (uint16_t)0x3);
               else tc_commit(lora_done);
@@ -990,8 +1130,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           const TileGrp tg = tile_grp(args, (int64_t)ps.nt * BN);
-          lora_tile<BWD, BN, PAIR>(tg.lora_F, tg.width, tg.width, (int)((int64_t)ps.nt * BN - tg.c0),
-                                   args.lora_scale, Bt, rank, t_idx);
+          if constexpr (ML)
+            lora_tile_ml<BWD, BN, PAIR>(args, args.ml_tile_ad[ps.mt * kMultiSlots + lora_slot(ps.i)], tg.width,
+                                        tg.width, ps.nt * BN, Bt, rank, t_idx);
+          else
+            lora_tile<BWD, BN, PAIR>(tg.lora_F, tg.width, tg.width, (int)((int64_t)ps.nt * BN - tg.c0),
+                                     args.lora_scale, Bt, rank, t_idx);
         }
         return tma_step;
       };
@@ -1145,7 +1289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t kb = seg_end - t * S;
         const int a = (int)(seg % NACC);
         const uint32_t aph = (uint32_t)(seg / NACC) & 1u;
-        if (lora_first && i0 == 0) {
+        if (lora_masks && (ML ? i0 < nl : i0 == 0)) {
           // the tile's first step was s G A: zero its dropped elements in
           // TMEM, then let the main steps accumulate on top
           const bool lok = !*abort_flag && mbar_wait_backoff(lora_done, lora_ph, DERR_TIMEOUT_ACC);
@@ -1266,6 +1410,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row = u * 128 + r;
           const int64_t m = m0 + row;
           const bool row_ok = ok && m < args.M;
+          int ml_ad = -1;
+          float ml_u[16];
+          bool ml_bad = false;
+          if constexpr (ML) {
+            ml_bad = ml_slots > 0 && *(volatile const uint32_t*)args.ml_bad != 0u;
+            if (!writer && row_ok) ml_ad = args.ml_row[m];
+            if (ml_ad >= 0 && ml_slots < 0) {
+              const float s = args.ml_scale[ml_ad];
+              const float4* up = reinterpret_cast<const float4*>(args.ml_P + m * 16);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float4 q = up[e];
+                ml_u[4 * e] = s * q.x;
+                ml_u[4 * e + 1] = s * q.y;
+                ml_u[4 * e + 2] = s * q.z;
+                ml_u[4 * e + 3] = s * q.w;
+              }
+            }
+          }
 #pragma unroll 1
           for (int c = 0; c < kv; ++c) {
             const int cc = half * (BN / 2) + c * 16;
@@ -1304,6 +1467,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!row_ok) continue;
             const int64_t o_off = m * og.width + (n - og.c0);
+            if constexpr (ML) {
+              if (ml_ad >= 0 && (ml_slots < 0 || ml_bad)) {
+                const uint32_t keep = BWD && args.mask ? args.mask[o_off >> 5] >> (o_off & 31) : 0xffffu;
+                if (ml_slots < 0) {
+                  ml_add<BWD>(args, ml_ad, n, og.width, ml_u, keep, v);
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 16; ++e)
+                    if ((keep >> e) & 1u) v[e] += ml_bad_term<BWD>(args, ml_ad, n + e, og.width, m);
+                }
+              }
+            }
             if (v8_out) {
               // one 32-byte store per 8 fp32 or 16 bf16 values: whole
               // sectors (16-byte stores of the rows of a warp write half
@@ -2071,9 +2246,9 @@ constexpr int64_t kBn256MinSteps = WS_GEMM_BN256_MIN_STEPS;
 // iterations per CTA so tiny problems are not shredded into partials.
 constexpr int64_t kMinSteps = 8;
 
-template <bool BWD, int UM, int BN, int PAIR, bool WB = false>
+template <bool BWD, int UM, int BN, int PAIR, bool WB = false, bool ML = false>
 cudaError_t set_smem_attr() {
-  static cudaError_t e = cudaFuncSetAttribute(k_nf4_gemm<BWD, UM, BN, PAIR, WB>,
+  static cudaError_t e = cudaFuncSetAttribute(k_nf4_gemm<BWD, UM, BN, PAIR, WB, ML>,
                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
                                               (int)Cfg<BWD, UM, BN, PAIR, WB>::SMEM_BYTES);
   return e;
@@ -2110,12 +2285,12 @@ int pair_mode() {
 }
 
 // Pairs of CTAs that can be resident at once (one CTA per SM).
-template <bool BWD, int BN, int PAIR, bool WB = false>
+template <bool BWD, int BN, int PAIR, bool WB = false, bool ML = false>
 int64_t pair_capacity_of() {
   static int64_t cap = -1;
   if (cap < 0) {
     cap = 0;
-    if (set_smem_attr<BWD, 2, BN, PAIR, WB>() == cudaSuccess) {
+    if (set_smem_attr<BWD, 2, BN, PAIR, WB, ML>() == cudaSuccess) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(2 * (unsigned)(device_sm_count() / 2));
       cfg.blockDim = dim3(kThreads);
@@ -2128,7 +2303,7 @@ int64_t pair_capacity_of() {
       cfg.attrs = attr;
       cfg.numAttrs = 1;
       int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, k_nf4_gemm<BWD, 2, BN, PAIR, WB>, &cfg) == cudaSuccess)
+      if (cudaOccupancyMaxActiveClusters(&n, k_nf4_gemm<BWD, 2, BN, PAIR, WB, ML>, &cfg) == cudaSuccess)
         cap = n;
       else
         cudaGetLastError();
@@ -2139,16 +2314,17 @@ int64_t pair_capacity_of() {
   return cap;
 }
 
-template <bool BWD, int UM, int BN, int PAIR, bool WB = false>
+template <bool BWD, int UM, int BN, int PAIR, bool WB = false, bool ML = false>
 cudaError_t launch_cfg(const GemmPlan& p, const GemmArgs& a, const CUtensorMap& tA,
                        const CUtensorMap& tL, const WMaps& wm, cudaStream_t st) {
   using C = Cfg<BWD, UM, BN, PAIR, WB>;
-  cudaError_t e = set_smem_attr<BWD, UM, BN, PAIR, WB>();
+  cudaError_t e = set_smem_attr<BWD, UM, BN, PAIR, WB, ML>();
   if (e != cudaSuccess) return e;
-  const int64_t G = grid_ctas(p, a.has_lora != 0);
+  const int64_t G = grid_ctas(p, ML || a.has_lora != 0);
   // the plan sizes pair grids by the NF4 kernel's residency; the bf16
-  // variant (no code ring) must fit the same grid at once
-  if (WB && PAIR != 0 && G / 2 > pair_capacity_of<BWD, BN, PAIR, WB>())
+  // variant (no code ring) and the one for many adapters must fit the same
+  // grid at once
+  if ((WB || ML) && PAIR != 0 && G / 2 > pair_capacity_of<BWD, BN, PAIR, WB, ML>())
     return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)G);
@@ -2189,7 +2365,7 @@ cudaError_t launch_cfg(const GemmPlan& p, const GemmArgs& a, const CUtensorMap& 
   cfg.attrs = attr;
   cfg.numAttrs = na;
   note_launch();
-  return cudaLaunchKernelEx(&cfg, k_nf4_gemm<BWD, UM, BN, PAIR, WB>, tA, tL, a, wm);
+  return cudaLaunchKernelEx(&cfg, k_nf4_gemm<BWD, UM, BN, PAIR, WB, ML>, tA, tL, a, wm);
 }
 
 }  // namespace
@@ -2358,6 +2534,27 @@ cudaError_t dispatch_gemm_wb(const GemmPlan& p, const GemmArgs& a, const CUtenso
   return launch_cfg<true, 1, 128, 0, true>(p, a, tA, tL, wm, st);
 }
 
+// The same for rows of different adapters: pairs always share the tile
+// through the pair MMA.
+cudaError_t dispatch_gemm_ml(const GemmPlan& p, const GemmArgs& a, const CUtensorMap& tA,
+                             const CUtensorMap& tL, const WMaps& wm, cudaStream_t st) {
+  if (!p.bwd) {
+    if (p.pair) {
+      if (p.bn == 256) return launch_cfg<false, 2, 256, 2, false, true>(p, a, tA, tL, wm, st);
+      return launch_cfg<false, 2, 128, 2, false, true>(p, a, tA, tL, wm, st);
+    }
+    if (p.um == 2 && p.bn == 256) return launch_cfg<false, 2, 256, 0, false, true>(p, a, tA, tL, wm, st);
+    if (p.um == 2) return launch_cfg<false, 2, 128, 0, false, true>(p, a, tA, tL, wm, st);
+    return launch_cfg<false, 1, 128, 0, false, true>(p, a, tA, tL, wm, st);
+  }
+  if (p.pair) {
+    if (p.bn == 256) return launch_cfg<true, 2, 256, 2, false, true>(p, a, tA, tL, wm, st);
+    return launch_cfg<true, 2, 128, 2, false, true>(p, a, tA, tL, wm, st);
+  }
+  if (p.um == 2) return launch_cfg<true, 2, 128, 0, false, true>(p, a, tA, tL, wm, st);
+  return launch_cfg<true, 1, 128, 0, false, true>(p, a, tA, tL, wm, st);
+}
+
 // Tensor maps of bf16 weights for a plan: rows of W [N, K] in boxes of
 // 64 x (this CTA's share of the tile's rows) for the forward, 64 x 64 for the
 // backward (which reads BW / 64 column groups per contraction step).
@@ -2421,6 +2618,59 @@ cudaError_t run_nf4_gemm(const GemmPlan& p, const NF4View& W, const uint16_t* ac
     return dispatch_gemm_wb(p, a, tA, tL, wm, st);
   }
   return dispatch_gemm(p, a, tA, tL, wm, st);
+}
+
+int64_t gemm_tile_rows(int64_t M) {
+  const GemmPlan p = plan_gemm(false, M, 64, 64);
+  return 128 * p.um * (p.pair ? 2 : 1);
+}
+
+cudaError_t run_nf4_gemm_multi(const GemmPlan& p, const NF4View& W, const uint16_t* act, int64_t M,
+                               const MultiLora& ml, const uint32_t* mask, void* out, int out_f32,
+                               int out_accum, float* partial, cudaStream_t st) {
+  if (!encode_fn()) return cudaErrorNotSupported;
+  const int64_t Nout = p.bwd ? W.K : W.N, Kc = p.bwd ? W.N : W.K;
+  // the batch's plan lists adapters by tile row
+  if (128 * p.um * (p.pair ? 2 : 1) != gemm_tile_rows(M)) return cudaErrorInvalidConfiguration;
+  CUtensorMap tA, tL;
+  if (!make_map(&tA, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act, (uint64_t)Kc, (uint64_t)M,
+                (uint64_t)Kc * 2, 64, (uint32_t)(128 * p.um), CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&tL, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ml.ext, 64, (uint64_t)(kMultiSlots * M), 128, 64,
+                (uint32_t)(128 * p.um), CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  GemmArgs a{};
+  a.M = M;
+  a.Nout = Nout;
+  a.nk_total = p.nk;
+  a.mtiles = p.mtiles;
+  a.ntiles = p.ntiles;
+  a.mask = mask;
+  a.out = out;
+  a.out_f32 = out_f32;
+  a.out_accum = out_accum;
+  a.partial = partial;
+  a.codes = W.codes;
+  a.absmax = W.absmax;
+  a.wN = W.N;
+  a.wK = W.K;
+  a.epad = p.epad;
+  a.ml_P = ml.P;
+  a.ml_F = ml.F;
+  a.ml_scale = ml.scale;
+  a.ml_row = ml.row;
+  a.ml_slots = ml.slots;
+  a.ml_tile_ad = ml.tile_ad;
+  a.ml_bad = ml.bad;
+  a.ml_stride = ml.stride;
+  a.ml_f16 = ml.f16;
+  if (grid_units(p, true) > 1) {
+    if (partial == nullptr) return cudaErrorInvalidValue;
+    const cudaError_t e = ring_slots((uint32_t)grid_ctas(p, true), &a.flags);
+    if (e != cudaSuccess) return e;
+  }
+  WMaps wm;
+  memset(&wm, 0, sizeof(wm));
+  return dispatch_gemm_ml(p, a, tA, tL, wm, st);
 }
 
 cudaError_t run_nf4_gemm_group(const GemmPlan& p, int ng, const NF4View* W, const uint16_t* act,
