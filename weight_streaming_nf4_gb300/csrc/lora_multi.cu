@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "nf4_decode.cuh"
 
 namespace ws {
 
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(kSkWarps * 32)
   const int CS = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
   pdl_wait();
   pdl_launch_dependents();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *bad = 0u;  // for the GEMM that follows
+  if (ext && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *bad = 0u;  // for the GEMM that follows
   if ((int)blockIdx.y >= plan[0]) return;  // the whole cluster alike
   const int4 tile = *reinterpret_cast<const int4*>(plan + o_tile + 4 * (int64_t)blockIdx.y);
   const int32_t* rows = plan + o_perm + tile.y;
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(kSkWarps * 32)
     const int64_t row = rows[i / kR];
     const int j = i % kR;
     *reinterpret_cast<float2*>(out + row * kR + j) = make_float2(v0, v1);
-    if (slots <= 0) return;
+    if (slots <= 0 || !ext) return;
     const int own = plan[o_slot + row];
     uint32_t hi, lo;
     split2(v0, v1, hi, lo);
@@ -468,6 +469,194 @@ __global__ void __launch_bounds__(kWgWarps * 32) k_multi_wgrad(const WgArgs w) {
   }
 }
 
+// ------------------------------------------------------------------------ few rows
+// y = x W'^T + the adapter term for at most 8 NT rows at a time (decode): bound
+// by reading the codes, and with few rows by decoding them.  The tensor-core
+// tile of the dequant GEMM needs 128 rows and a pipeline of a dozen steps; here
+// a warp decodes 16 RG weight rows in registers, as the 16-row operand of
+// mma.sync, and the rows of x are its 8-wide operand, so no decoded weight
+// passes through shared memory.  A lane holds 16 code bytes (32 weights, one
+// block scale) of two weight rows per 128-deep step; x is staged in shared
+// memory in that order of k.  CTA = 128 RG weight rows; a cluster of CTAs
+// shares their contraction, and adds its partial sums in rank order through
+// distributed shared memory.
+//
+// Starts beside the kernel that makes U (programmatic launch): the weights and
+// x are read before the wait for it (that kernel has waited for everything
+// earlier), U and the adapters after.
+constexpr int kFewWarps = 8;
+constexpr int kFewStages = 4;   // 128-deep steps of x in flight
+struct FewArgs {
+  const uint8_t* codes;
+  const float* absmax;
+  const uint16_t* x;
+  int M, N, K;
+  const float* P;        // U [M, 16]
+  const void* F;         // B of adapter a at a * stride, [N, 16]
+  int64_t stride;
+  const float* scale;
+  const int32_t* row;    // adapter of each row
+  uint16_t* y;
+};
+template <int NT, int RG>
+struct FewCfg {
+  static constexpr int ROWS = kFewWarps * 16 * RG;
+  static constexpr int MR = NT * 8;
+  static constexpr int STAGE = MR * 256;           // bytes of 128 k of MR rows
+  static constexpr int PITCH = ROWS + 4;           // floats; [MR][PITCH] partial sums
+  static constexpr int SMEM = kFewStages * STAGE > MR * PITCH * 4 ? kFewStages * STAGE : MR * PITCH * 4;
+  static constexpr int PF = RG == 1 ? 4 : 2;       // steps of codes in registers
+};
+
+template <int NT, int RG, bool F16>
+__global__ void __launch_bounds__(kFewWarps * 32) k_multi_few(const FewArgs a) {
+  using C = FewCfg<NT, RG>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int lane = (int)lane_id(), warp = (int)warp_id(), g = lane >> 2, t = lane & 3;
+  const int CS = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
+  const int m0 = (int)blockIdx.z * C::MR, mrows = min(C::MR, a.M - m0);
+  const int n0 = (int)blockIdx.y * C::ROWS, nw = n0 + warp * 16 * RG;  // this warp's first weight row
+  const int segs = (a.K + 127) / 128;
+  const int s_beg = (int)((int64_t)rank * segs / CS), s_end = (int)((int64_t)(rank + 1) * segs / CS);
+
+  // x of one 128-deep step: 16-byte chunk c (k = 8c ..) of row m at chunk place
+  // (c % 4) * 4 + c / 4, odd rows with the 64-byte halves swapped, so that the
+  // eight lanes of a quarter warp read eight different bank groups
+  auto stage_x = [&](int s) {
+    if (s < s_end) {
+      uint8_t* dst = smem + (s % kFewStages) * C::STAGE;
+      for (int i = threadIdx.x; i < C::MR * 16; i += kFewWarps * 32) {
+        const int m = i / 16, c = i % 16, k = s * 128 + c * 8;
+        const bool in = m < mrows && k < a.K;
+        const uint32_t at = (uint32_t)(m * 256 + ((((c & 3) * 4 + (c >> 2)) * 16) ^ ((m & 1) * 64)));
+        cp_async16(smem_u32(dst + at), a.x + (in ? (int64_t)(m0 + m) * a.K + k : 0), in ? 16u : 0u);
+      }
+    }
+    cp_async_commit();
+  };
+  struct Codes {
+    uint4 w[RG][2];
+    float s[RG][2];
+  };
+  auto load_codes = [&](Codes& f, int s) {
+    const int k = s * 128 + t * 32;
+#pragma unroll
+    for (int r = 0; r < RG; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int n = nw + r * 16 + h * 8 + g;
+        const bool in = s < s_end && n < a.N && k < a.K;
+        f.w[r][h] = in ? __ldg(reinterpret_cast<const uint4*>(a.codes + (int64_t)n * (a.K / 2) + k / 2)) : make_uint4(0, 0, 0, 0);
+        f.s[r][h] = in ? __ldg(a.absmax + (int64_t)(k / 64) * a.N + n) : 0.0f;
+      }
+  };
+#pragma unroll
+  for (int i = 0; i < kFewStages - 1; ++i) stage_x(s_beg + i);
+  Codes f[C::PF];
+#pragma unroll
+  for (int i = 0; i < C::PF; ++i) load_codes(f[i], s_beg + i);
+  float acc[RG][NT][4] = {};
+  for (int sb = s_beg; sb < s_end; sb += C::PF) {
+#pragma unroll
+    for (int i = 0; i < C::PF; ++i) {
+      const int s = sb + i;
+      if (s >= s_end) break;  // CTA-uniform
+      cp_async_wait<kFewStages - 2>();
+      __syncthreads();  // step s of x has landed; everyone is done with step s - 1
+      stage_x(s + kFewStages - 1);
+      Nf4Table tb[RG][2];
+#pragma unroll
+      for (int r = 0; r < RG; ++r)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) tb[r][h] = make_table(f[i].s[r][h]);
+      const uint8_t* xs = smem + (s % kFewStages) * C::STAGE + g * 256 + t * 16;
+      const uint32_t flip = (uint32_t)(g & 1) * 64;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint4 d[RG][2];
+#pragma unroll
+        for (int r = 0; r < RG; ++r)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 q = f[i].w[r][h];
+            d[r][h] = dq8(w == 0 ? q.x : w == 1 ? q.y : w == 2 ? q.z : q.w, tb[r][h]);
+          }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint4 b = *reinterpret_cast<const uint4*>(xs + nt * 2048 + ((w * 64) ^ flip));
+#pragma unroll
+          for (int r = 0; r < RG; ++r) {
+            mma16816(acc[r][nt], d[r][0].x, d[r][1].x, d[r][0].y, d[r][1].y, b.x, b.y);
+            mma16816(acc[r][nt], d[r][0].z, d[r][1].z, d[r][0].w, d[r][1].w, b.z, b.w);
+          }
+        }
+      }
+      load_codes(f[i], s + C::PF);
+    }
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+  // partial sums [m][n]
+  float* red = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int r = 0; r < RG; ++r)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        red[(nt * 8 + 2 * t + (e & 1)) * C::PITCH + (warp * RG + r) * 16 + (e >> 1) * 8 + g] = acc[r][nt][e];
+  // U, and y's earlier readers, are an earlier kernel's business until here
+  pdl_wait();
+  pdl_launch_dependents();
+  if (CS > 1) cluster_sync();
+  else __syncthreads();
+  // this CTA finishes ROWS / CS of the columns, two per thread
+  const int per = C::ROWS / CS, half = per / 2;
+  for (int i = threadIdx.x; i < half * mrows; i += kFewWarps * 32) {
+    const int m = i / half, nl = rank * per + 2 * (i % half), n = n0 + nl;
+    if (n >= a.N) continue;
+    float v0 = 0.0f, v1 = 0.0f;
+    for (int c = 0; c < CS; ++c) {
+      float p0, p1;
+      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                   : "=f"(p0), "=f"(p1)
+                   : "r"(mapa_shared(smem_u32(&red[m * C::PITCH + nl]), (uint32_t)c))
+                   : "memory");
+      v0 += p0;
+      v1 += p1;
+    }
+    const int ad = a.row[m0 + m];
+    if (ad >= 0) {
+      const float s = a.scale[ad];
+      const float4* u = reinterpret_cast<const float4*>(a.P + (int64_t)(m0 + m) * kR);
+      float d0 = 0.0f, d1 = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 uu = u[q];
+        float b0[4], b1[4];
+        const int64_t o = ad * a.stride + (int64_t)n * kR + 4 * q;
+        if constexpr (F16) {
+          const uint2 x0 = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.F) + o));
+          const uint2 x1 = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.F) + o + kR));
+          b0[0] = bf16_lo(x0.x), b0[1] = bf16_hi(x0.x), b0[2] = bf16_lo(x0.y), b0[3] = bf16_hi(x0.y);
+          b1[0] = bf16_lo(x1.x), b1[1] = bf16_hi(x1.x), b1[2] = bf16_lo(x1.y), b1[3] = bf16_hi(x1.y);
+        } else {
+          const float4 x0 = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.F) + o));
+          const float4 x1 = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.F) + o + kR));
+          b0[0] = x0.x, b0[1] = x0.y, b0[2] = x0.z, b0[3] = x0.w;
+          b1[0] = x1.x, b1[1] = x1.y, b1[2] = x1.z, b1[3] = x1.w;
+        }
+        d0 = fmaf(uu.x, b0[0], d0), d0 = fmaf(uu.y, b0[1], d0), d0 = fmaf(uu.z, b0[2], d0), d0 = fmaf(uu.w, b0[3], d0);
+        d1 = fmaf(uu.x, b1[0], d1), d1 = fmaf(uu.y, b1[1], d1), d1 = fmaf(uu.z, b1[2], d1), d1 = fmaf(uu.w, b1[3], d1);
+      }
+      v0 = fmaf(s, d0, v0);
+      v1 = fmaf(s, d1, v1);
+    }
+    *reinterpret_cast<uint32_t*>(a.y + (int64_t)(m0 + m) * a.N + n) = pack_bf16x2(v0, v1);
+  }
+  if (CS > 1) cluster_sync();  // the sums stay until every CTA of the cluster has read them
+}
+
 // ------------------------------------------------------------------------ host side
 struct WsLayout {
   size_t G, ext, bad, partial, total;
@@ -485,10 +674,11 @@ WsLayout ws_layout(int64_t M, int64_t N, int64_t K) {
 }
 
 template <typename K, typename... Args>
-cudaError_t launch_cluster(K k, dim3 grid, int threads, int cluster, cudaStream_t st, Args... args) {
+cudaError_t launch_cluster(K k, dim3 grid, int threads, int cluster, size_t smem, cudaStream_t st, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -512,15 +702,16 @@ int skinny_cluster(int64_t C) {
 
 cudaError_t run_skinny(bool f_cj, const uint16_t* X, const void* F, bool f16, int64_t strideF, int64_t C,
                        const uint32_t* mask, const ws_lora_plan& plan, float* out, uint8_t* ws,
-                       const WsLayout& W, cudaStream_t st) {
+                       const WsLayout& W, bool slots, cudaStream_t st) {
   const PlanLayout L = plan_layout(plan.M, plan.n_adapters);
   const int cs = skinny_cluster(C);
   auto k = f_cj ? k_multi_skinny<true, false, false>
                 : (f16 ? (mask ? k_multi_skinny<false, true, true> : k_multi_skinny<false, true, false>)
                        : (mask ? k_multi_skinny<false, false, true> : k_multi_skinny<false, false, false>));
-  return launch_cluster(k, dim3((unsigned)cs, (unsigned)L.max_tiles), kSkWarps * 32, cs, st, X, F, strideF,
+  return launch_cluster(k, dim3((unsigned)cs, (unsigned)L.max_tiles), kSkWarps * 32, cs, 0, st, X, F, strideF,
                         (int)C, mask, (const int32_t*)plan.data, L.perm, L.tile, L.slot, out,
-                        reinterpret_cast<uint32_t*>(ws + W.ext), plan.M, reinterpret_cast<uint32_t*>(ws + W.bad));
+                        slots ? reinterpret_cast<uint32_t*>(ws + W.ext) : nullptr, plan.M,
+                        reinterpret_cast<uint32_t*>(ws + W.bad));
 }
 
 // The GEMM's view of the adapter term with P = U or G and F = B or A.
@@ -540,6 +731,44 @@ MultiLora multi_of(const ws_lora_plan& plan, uint8_t* ws, const WsLayout& W, con
   m.stride = stride;
   m.f16 = f16 ? 1 : 0;
   return m;
+}
+
+#ifndef WS_FEW_ROWS
+#define WS_FEW_ROWS 64
+#endif
+constexpr int kFewRows = WS_FEW_ROWS;  // rows up to which k_multi_few runs the forward
+template <int NT, int RG, bool F16>
+cudaError_t launch_few(const FewArgs& a, cudaStream_t st) {
+  using C = FewCfg<NT, RG>;
+  auto k = k_multi_few<NT, RG, F16>;
+  static const int resident = [&] {  // CTAs of the whole GPU at once
+    int per = 0;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, k, kFewWarps * 32, C::SMEM) != cudaSuccess)
+      return 0;
+    return per * device_sm_count();
+  }();
+  if (resident <= 0) return cudaErrorInvalidConfiguration;
+  const int blocks = (a.N + C::ROWS - 1) / C::ROWS, chunks = (a.M + C::MR - 1) / C::MR, segs = (a.K + 127) / 128;
+  // CTAs sharing a contraction: the fewest steps in a row, a wave of CTAs
+  // counting its longest CTA and about three steps to start and join
+  int cs = 1, best = 0x7fffffff;
+  for (int c = 1; c <= 8; c *= 2) {
+    const int waves = (blocks * chunks * c + resident - 1) / resident;
+    const int cost = waves * ((segs + c - 1) / c + 3);
+    if (cost < best) best = cost, cs = c;
+  }
+  return launch_cluster(k, dim3((unsigned)cs, (unsigned)blocks, (unsigned)chunks), kFewWarps * 32, cs, C::SMEM, st, a);
+}
+template <bool F16>
+cudaError_t run_few_t(const FewArgs& a, cudaStream_t st) {
+  if (a.M <= 8) return launch_few<1, 1, F16>(a, st);
+  if (a.M <= 16) return launch_few<2, 1, F16>(a, st);
+  if (a.M <= 32) return launch_few<4, 2, F16>(a, st);
+  return launch_few<8, 2, F16>(a, st);
+}
+cudaError_t run_few(const FewArgs& a, bool f16, cudaStream_t st) {
+  return f16 ? run_few_t<true>(a, st) : run_few_t<false>(a, st);
 }
 
 ws_status check_plan(const ws_lora_plan* p) {
@@ -641,7 +870,18 @@ ws_status ws_lora_linear_fwd_multi(const ws_nf4* W, const uint16_t* x, const ws_
   cudaStream_t st = (cudaStream_t)stream;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const bool f16 = set->dtype == WS_DTYPE_BF16;
-  WS_RUN(run_skinny(false, x, set->A, f16, set->stride_a, K, mask, *plan, U_saved, ws, L, st));
+  const bool few = M <= kFewRows;
+  WS_RUN(run_skinny(false, x, set->A, f16, set->stride_a, K, mask, *plan, U_saved, ws, L, !few, st));
+  if (few) {
+    FewArgs a{};
+    a.codes = W->codes, a.absmax = W->absmax, a.x = x;
+    a.M = (int)M, a.N = (int)N, a.K = (int)K;
+    a.P = U_saved, a.F = set->B, a.stride = set->stride_b, a.scale = set->scale;
+    a.row = static_cast<const int32_t*>(plan->data) + plan_layout(M, plan->n_adapters).row;
+    a.y = y;
+    WS_RUN(run_few(a, f16, st));
+    return WS_OK;
+  }
   const MultiLora ml = multi_of(*plan, ws, L, U_saved, set->B, f16, set->stride_b, set->scale);
   WS_RUN(run_nf4_gemm_multi(plan_gemm(false, M, N, K), view(W), x, M, ml, nullptr, y, 0, 0,
                             reinterpret_cast<float*>(ws + L.partial), st));
@@ -670,7 +910,7 @@ ws_status ws_lora_linear_bwd_multi(const ws_nf4* W, const uint16_t* x, const ws_
   const int32_t* pl = static_cast<const int32_t*>(plan->data);
   const PlanLayout P = plan_layout(M, plan->n_adapters);
   float* G = reinterpret_cast<float*>(ws + L.G);
-  WS_RUN(run_skinny(true, dY, set->B, false, set->stride_b, N, nullptr, *plan, G, ws, L, st));
+  WS_RUN(run_skinny(true, dY, set->B, false, set->stride_b, N, nullptr, *plan, G, ws, L, true, st));
   WgArgs w{};
   w.P[0] = U_saved, w.P[1] = G;
   w.Q[0] = dY, w.Q[1] = x;
