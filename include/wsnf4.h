@@ -485,9 +485,9 @@ ws_status ws_adamw_plan_init(const ws_adamw_tensor* tensors, int32_t n_tensors, 
 /* One step of every tensor of the plan.  norms (device [n_groups], may be NULL)
  * receives each group's gradient norm, before clipping.  WS_ADAMW_CLIP: c =
  * min(1, max_norm / (norm + 1e-6)), and a group whose norm is not finite takes
- * no step (its tensors and counter stay as they are); else c = 1.  Norms sum
- * squares in fp32 within 16 elements of a thread and a chunk of 4096, and in
- * double across chunks, in a fixed order. */
+ * no step (its tensors and counter stay as they are); else c = 1.  Squares are
+ * taken and summed in fp32, in a fixed order: a norm beyond 1.8e19 counts as not
+ * finite, and gradients below 1e-19 count for nothing. */
 enum { WS_ADAMW_CLIP = 1 };
 ws_status ws_adamw_step(const ws_adamw_plan* plan, ws_adamw_group* groups, int32_t flags,
                         float* norms, void* workspace, size_t ws_bytes, ws_stream_t stream);

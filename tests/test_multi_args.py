@@ -129,21 +129,20 @@ def _init(ops, arr, n_groups=1, types=(1, 1, 32), n=None):
 def test_adamw_plan_lists_every_chunk_once_by_group(ops):
     sizes = [1, 4096, 4097, 3, 20000, 8192, 5]
     groups = [2, 0, 2, 0, 3, 2, 0]   # group 1 has no tensor
-    st, image, plan = _init(ops, _tensors(ops, sizes, groups), 4)
+    arr = _tensors(ops, sizes, groups)
+    st, image, plan = _init(ops, arr, 4)
     assert st == OK
-    n = len(sizes)
-    first = image[n * 64:n * 64 + 20].view(np.int32)
-    off = n * 64 + -(-20 // 16) * 16
-    chunk = image[off:off + 4 * plan.n_chunks].view(np.int32)
     per = [-(-s // 4096) for s in sizes]
-    assert plan.n_chunks == sum(per) and first[0] == 0 and first[-1] == sum(per)
-    want = [i for g in range(4) for i in range(n) if groups[i] == g for _ in range(per[i])]
-    assert chunk.tolist() == want
+    assert plan.n_chunks == sum(per)
+    c = image[:plan.n_chunks * 64]
+    first = image[plan.n_chunks * 64:plan.n_chunks * 64 + 20].view(np.int32)
+    assert first[0] == 0 and first[-1] == sum(per)
+    ptr, num = c.view(np.uint64).reshape(-1, 8), c.view(np.int32).reshape(-1, 16)
+    want = [(arr[i].p + 4 * e, arr[i].g + 4 * e, arr[i].m + 4 * e, arr[i].v + 4 * e, min(4096, sizes[i] - e), g)
+            for g in range(4) for i in range(len(sizes)) if groups[i] == g for e in range(0, sizes[i], 4096)]
+    assert [(*map(int, p[:4]), int(q[12]), int(q[13])) for p, q in zip(ptr, num)] == want
     for g in range(4):
         assert first[g + 1] - first[g] == sum(p for p, h in zip(per, groups) if h == g)
-    entry = image[:n * 64].view(np.int32).reshape(n, 16)
-    for i in range(n):
-        assert entry[i, 14] == groups[i] and chunk[entry[i, 15]] == i and (entry[i, 15] == 0 or chunk[entry[i, 15] - 1] != i)
 
 
 def test_adamw_plan_refusals(ops):

@@ -3,15 +3,15 @@
 // gradient norm of each parameter group and clipping by it.
 //
 // All tensors of a plan run in one launch: the plan cuts every tensor into
-// chunks of kChunk elements and lists the chunks by group, so CTA c reads
-// which tensor it works on from the chunk table.  Every operand is read once
+// chunks of kChunk elements and lists the chunks by group; CTA c works on
+// chunk c.  Every operand is read once
 // and written once; each element needs the group's coefficients only, so the
 // step is bound by memory (28 bytes per fp32 parameter with 32-bit states,
 // 16 with 8-bit ones).
 //
-// Sums of squares run in a fixed order (inside a thread, a fixed butterfly in
-// the warp, warps and then chunks in index order, the chunks' sums in double),
-// so a norm does not depend on the launch.
+// Sums of squares run in a fixed order in fp32 (16 elements of a thread, a
+// butterfly, 8 warps; then the chunks the same way), so repeated steps give the
+// same bits.
 #include <math.h>
 #include <string.h>
 
@@ -30,19 +30,20 @@ constexpr int kChunk = 4096;   // elements per CTA: 16 per thread, all loads in 
 constexpr int kThreads = 256;
 constexpr int kBlock8 = 256;   // elements per 8-bit state block: one warp, 8 per lane
 
-// Device image of one tensor of a plan (64 bytes).
-struct TensorDev {
+// One chunk of the plan's device image (64 bytes): the addresses of its first
+// elements, so that a CTA's data is one load away.
+struct Chunk {
   void* p;
   const void* g;
   void* m;
   void* v;
   float* ms;
   float* vs;
-  int64_t n;
+  int32_t n;  // elements, 1 .. kChunk
   int32_t group;
-  int32_t first_chunk;  // index of the tensor's first chunk in the table
+  int32_t pad[2];
 };
-static_assert(sizeof(TensorDev) == 64, "tensor entry");
+static_assert(sizeof(Chunk) == 64, "chunk entry");
 
 // Coefficients of a group's step, written by k_adamw_begin.
 struct Coef {
@@ -59,16 +60,16 @@ static_assert(sizeof(Coef) == 48, "coefficients");
 
 size_t al16(size_t x) { return (x + 15) & ~size_t(15); }
 
-// Sections of the plan image and of the workspace.
+// Sections of the plan image: the chunks listed by group, and the first chunk
+// of each group (n_groups + 1 entries).
 struct Layout {
-  size_t tensors, group_first, chunk, bytes;  // plan: entries, first chunk of each group, chunk -> tensor
+  size_t chunk, group_first, bytes;
 };
-Layout plan_layout(int32_t n_tensors, int32_t n_groups, int64_t n_chunks) {
+Layout plan_layout(int32_t n_groups, int64_t n_chunks) {
   Layout L{};
-  L.tensors = 0;
-  L.group_first = al16((size_t)n_tensors * sizeof(TensorDev));
-  L.chunk = L.group_first + al16((size_t)(n_groups + 1) * 4);
-  L.bytes = L.chunk + al16((size_t)n_chunks * 4);
+  L.chunk = 0;
+  L.group_first = (size_t)n_chunks * sizeof(Chunk);
+  L.bytes = L.group_first + al16((size_t)(n_groups + 1) * 4);
   return L;
 }
 size_t coef_bytes(int32_t n_groups) { return al16((size_t)n_groups * sizeof(Coef)); }
@@ -95,22 +96,21 @@ WS_DEVINL void e4m3x2_to_f32(uint32_t v, float& lo, float& hi) {
 // bit more than e4m3 has, for the sign a root does not need.
 constexpr uint32_t kRootBias = (127u - 15u) << 4;
 WS_DEVINL uint32_t root_code(float q) {
-  const uint32_t b = __float_as_uint(q);
-  const uint32_t r = (b + 0x3FFFFu + ((b >> 19) & 1u)) >> 19;
-  const int c = max(1, min(255, (int)r - (int)kRootBias));
-  return q > 0.0f ? (uint32_t)c : 0u;
+  const uint32_t b = __float_as_uint(q);  // q >= 0
+  const int r = (int)(b + ((b >> 19) & 1u) + (0x3FFFFu - (kRootBias << 19))) >> 19;
+  return (uint32_t)max(r, (int)min(b, 1u));
 }
 WS_DEVINL float root_value(uint32_t c) {
-  return c ? __uint_as_float((c + kRootBias) << 19) : 0.0f;
+  return c ? __uint_as_float(c * (1u << 19) + (kRootBias << 19)) : 0.0f;
 }
 constexpr float kMTop = 448.0f, kVTop = 1.9375f;
 
 // ---- elements ------------------------------------------------------------------------
 // N (4 or 8) consecutive elements from i0 of an fp32 or bf16 array of n; past
-// the end they read as 0 and are not written.  Full vectors use 16-byte (bf16
-// x 4: 8-byte) accesses.
+// the end they read as 0 and are not written.  Full vectors use 32-byte
+// (fp32 x 8, where aligned), 16-byte or (bf16 x 4) 8-byte accesses.
 template <bool BF16, int N>
-WS_DEVINL void load_n(const void* base, int64_t i0, int64_t n, float (&x)[N]) {
+WS_DEVINL void load_n(const void* base, int i0, int n, float (&x)[N]) {
   if (i0 + N <= n) {
     if constexpr (BF16) {
       const uint32_t* s = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(base) + i0);
@@ -126,6 +126,16 @@ WS_DEVINL void load_n(const void* base, int64_t i0, int64_t n, float (&x)[N]) {
       for (int k = 0; k < N / 2; ++k) x[2 * k] = bf16_lo(w[k]), x[2 * k + 1] = bf16_hi(w[k]);
     } else {
       const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i0);
+      if constexpr (N == 8) {
+        // one 32-byte access: two of 16 bytes would each touch half of every sector
+        if ((reinterpret_cast<uintptr_t>(s) & 31u) == 0u) {
+          uint32_t w[8];
+          ld_global_v8(s, w);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(w[k]);
+          return;
+        }
+      }
 #pragma unroll
       for (int k = 0; k < N / 4; ++k) {
         const float4 q = s[k];
@@ -143,7 +153,7 @@ WS_DEVINL void load_n(const void* base, int64_t i0, int64_t n, float (&x)[N]) {
   }
 }
 template <bool BF16, int N>
-WS_DEVINL void store_n(void* base, int64_t i0, int64_t n, const float (&x)[N]) {
+WS_DEVINL void store_n(void* base, int i0, int n, const float (&x)[N]) {
   if (i0 + N <= n) {
     if constexpr (BF16) {
       uint32_t w[N / 2];
@@ -154,6 +164,13 @@ WS_DEVINL void store_n(void* base, int64_t i0, int64_t n, const float (&x)[N]) {
       else *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
     } else {
       float4* d = reinterpret_cast<float4*>(static_cast<float*>(base) + i0);
+      if constexpr (N == 8) {
+        if ((reinterpret_cast<uintptr_t>(d) & 31u) == 0u) {
+          st_global_v8(d, __float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]),
+                       __float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+          return;
+        }
+      }
 #pragma unroll
       for (int k = 0; k < N / 4; ++k) d[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
     }
@@ -167,142 +184,199 @@ WS_DEVINL void store_n(void* base, int64_t i0, int64_t n, const float (&x)[N]) {
     }
 }
 
+WS_DEVINL float sqrt_approx(float x) {
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+WS_DEVINL float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // m, v and p of one element.  Products and sums are rounded one by one (no
 // contraction), as the formula is written: a value that lies on the border
 // between two 8-bit codes then falls the way it does for anybody who
 // evaluates the formula in fp32.
-WS_DEVINL void adamw1(float& p, float g, float& m, float& v, const Coef& c) {
+// Returns the root of the new v.
+WS_DEVINL float adamw1(float& p, float g, float& m, float& v, const Coef& c) {
   g = __fmul_rn(g, c.clip);
   m = __fadd_rn(__fmul_rn(m, c.beta1), __fmul_rn(g, c.one_m_beta1));
   v = __fadd_rn(__fmul_rn(v, c.beta2), __fmul_rn(__fmul_rn(g, g), c.one_m_beta2));
-  const float den = fmaf(sqrtf(v), c.rbc2, c.eps);
-  p = p * c.decay - c.step_size * (m / den);
+  // root and reciprocal of the step to 2^-22 or better: it is a small change of p
+  const float root = sqrt_approx(v);
+  p = fmaf(-c.step_size, m * rcp_approx(fmaf(root, c.rbc2, c.eps)), p * c.decay);
+  return root;
 }
 
 // ---- kernels ---------------------------------------------------------------------------
+// Only the plan's tables are declared __restrict__: what an earlier kernel
+// writes may not be, or the compiler may load it ahead of the wait for that
+// kernel.
 template <bool G16>
 __global__ void __launch_bounds__(kThreads)
-    k_adamw_sumsq(const TensorDev* __restrict__ tensors, const int32_t* __restrict__ chunk,
-                  double* __restrict__ partial) {
+    k_adamw_sumsq(const Chunk* __restrict__ chunks, float* partial) {
   pdl_wait();
   pdl_launch_dependents();
   __shared__ float red[kThreads / 32];
-  const TensorDev t = tensors[chunk[blockIdx.x]];
-  const int64_t base = (int64_t)((int)blockIdx.x - t.first_chunk) * kChunk;
-  float g[4][4];
+  const Chunk t = chunks[blockIdx.x];
+  float g[2][8];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) load_n<G16, 4>(t.g, base + (u * kThreads + threadIdx.x) * 4, t.n, g[u]);
+  for (int u = 0; u < 2; ++u) load_n<G16, 8>(t.g, (u * kThreads + (int)threadIdx.x) * 8, t.n, g[u]);
   float s = 0.0f;
 #pragma unroll
-  for (int u = 0; u < 4; ++u)
+  for (int u = 0; u < 2; ++u)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) s = fmaf(g[u][k], g[u][k], s);
+    for (int k = 0; k < 8; ++k) s = fmaf(g[u][k], g[u][k], s);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (lane_id() == 0) red[warp_id()] = s;
   __syncthreads();
   if (threadIdx.x == 0) {
-    double d = 0.0;
-    for (int w = 0; w < kThreads / 32; ++w) d += (double)red[w];
-    partial[blockIdx.x] = d;
+    s = 0.0f;
+    for (int w = 0; w < kThreads / 32; ++w) s += red[w];
+    partial[blockIdx.x] = s;
   }
 }
 
-// One CTA per group: the norm from the chunks' sums (double, chunk order per
-// thread, threads in index order), the step counter and the coefficients.
-__global__ void __launch_bounds__(kThreads)
-    k_adamw_begin(ws_adamw_group* __restrict__ groups, const int32_t* __restrict__ group_first,
-                  const double* __restrict__ partial, float* __restrict__ norms, int clip,
-                  Coef* __restrict__ coef) {
+// b^t for an integer t, by squaring.
+WS_DEVINL double pow_int(double b, double t) {
+  uint32_t n = (uint32_t)fmin(t, 4e9);
+  double r = 1.0;
+  for (; n; n >>= 1, b *= b)
+    if (n & 1u) r *= b;
+  return r;
+}
+
+// One CTA per group: the norm from the chunks' sums, the step counter and the
+// coefficients.  A thread adds its chunks (every kBeginThreads-th) in order, a
+// butterfly and then the warps in index order follow.  Double precision is
+// slow here (a warp's product takes as long as dozens in fp32: with every
+// thread computing the powers the kernel took 25 us), so only one thread each
+// makes them and the sums stay in fp32.
+constexpr int kBeginThreads = 1024;
+__global__ void __launch_bounds__(kBeginThreads)
+    k_adamw_begin(ws_adamw_group* groups, const int32_t* __restrict__ group_first,
+                  const float* partial, float* norms, int clip,
+                  Coef* coef) {
+  __shared__ float red[kBeginThreads / 32];
+  __shared__ float bc[2];  // 1 - beta^t
+  const int h = blockIdx.x;
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ double red[kThreads / 32];
-  const int h = blockIdx.x;
-  double norm = 0.0;
   if (partial) {
-    double s = 0.0;
-    for (int i = group_first[h] + threadIdx.x; i < group_first[h + 1]; i += kThreads) s += partial[i];
+    float s = 0.0f;
+    const int end = group_first[h + 1];
+    int i = group_first[h] + threadIdx.x;
+    for (; i + 3 * kBeginThreads < end; i += 4 * kBeginThreads) {
+      const float a = partial[i], b = partial[i + kBeginThreads], c = partial[i + 2 * kBeginThreads],
+                  d = partial[i + 3 * kBeginThreads];
+      s += a;
+      s += b;
+      s += c;
+      s += d;
+    }
+    for (; i < end; i += kBeginThreads) s += partial[i];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane_id() == 0) red[warp_id()] = s;
-    __syncthreads();
-    if (threadIdx.x == 0)
-      for (int w = 0; w < kThreads / 32; ++w) norm += red[w];
-    norm = sqrt(norm);
   }
+  if (threadIdx.x == 32 || threadIdx.x == 64) {
+    const double b = threadIdx.x == 32 ? groups[h].beta1 : groups[h].beta2;
+    bc[threadIdx.x / 32 - 1] = (float)(1.0 - pow_int(b, groups[h].step + 1.0));
+  }
+  __syncthreads();
   if (threadIdx.x != 0) return;
-  ws_adamw_group g = groups[h];
+  const ws_adamw_group g = groups[h];
   Coef c{};
   c.clip = 1.0f;
   if (partial) {
-    if (norms) norms[h] = (float)norm;
+    float s = 0.0f;
+    for (int w = 0; w < kBeginThreads / 32; ++w) s += red[w];
+    const float norm = sqrtf(s);
+    if (norms) norms[h] = norm;
     if (clip) {
       // a norm that is not finite would write NaN over every parameter of
       // the group: the group takes no step and its counter stands
-      if (!isfinite(norm)) c.skip = 1;
-      else if (g.max_norm > 0.0) c.clip = (float)fmin(1.0, g.max_norm / (norm + 1e-6));
+      if (!(norm <= 3.402823466e38f)) c.skip = 1;
+      else if (g.max_norm > 0.0) c.clip = fminf(1.0f, (float)g.max_norm / (norm + 1e-6f));
     }
   }
-  if (!c.skip) {
-    g.step += 1.0;
-    groups[h].step = g.step;
-  }
+  if (!c.skip) groups[h].step = g.step + 1.0;
   c.beta1 = (float)g.beta1;
   c.one_m_beta1 = (float)(1.0 - g.beta1);
   c.beta2 = (float)g.beta2;
   c.one_m_beta2 = (float)(1.0 - g.beta2);
   c.decay = (float)(1.0 - g.lr * g.weight_decay);
-  c.step_size = (float)(g.lr / (1.0 - pow(g.beta1, g.step)));
-  c.rbc2 = (float)(1.0 / sqrt(1.0 - pow(g.beta2, g.step)));
+  c.step_size = (float)g.lr / bc[0];
+  c.rbc2 = 1.0f / sqrtf(bc[1]);
   c.eps = (float)g.eps;
   coef[h] = c;
 }
 
+// Chunks run last to first: the norm's pass read the gradients first to last,
+// and the last of them are still in L2 (134M parameters with clipping: 653 ->
+// 617 us for the step, 6.1 TB/s of what it cannot do without).  Parameters, gradients and moments are read
+// before the wait for the coefficients: the kernel that makes those has itself
+// waited for everything before it.
 template <bool P16, bool G16>
 __global__ void __launch_bounds__(kThreads)
-    k_adamw32(const TensorDev* __restrict__ tensors, const int32_t* __restrict__ chunk,
-              const Coef* __restrict__ coef) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const TensorDev t = tensors[chunk[blockIdx.x]];
-  const Coef c = coef[t.group];
-  if (c.skip) return;
-  const int64_t base = (int64_t)((int)blockIdx.x - t.first_chunk) * kChunk;
+    k_adamw32(const Chunk* __restrict__ chunks, const Coef* coef) {
+  const Chunk t = chunks[gridDim.x - 1 - blockIdx.x];
+  float p[4][4], g[4][4], m[4][4], v[4][4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    const int64_t i = base + (u * kThreads + threadIdx.x) * 4;
-    float p[4], g[4], m[4], v[4];
-    load_n<P16, 4>(t.p, i, t.n, p);
-    load_n<G16, 4>(t.g, i, t.n, g);
-    load_n<false, 4>(t.m, i, t.n, m);
-    load_n<false, 4>(t.v, i, t.n, v);
+    const int i = (u * kThreads + (int)threadIdx.x) * 4;
+    load_n<G16, 4>(t.g, i, t.n, g[u]);
+    load_n<P16, 4>(t.p, i, t.n, p[u]);
+    load_n<false, 4>(t.m, i, t.n, m[u]);
+    load_n<false, 4>(t.v, i, t.n, v[u]);
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  const Coef c = coef[t.group];
+  if (c.skip) return;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) adamw1(p[k], g[k], m[k], v[k], c);
-    store_n<P16, 4>(t.p, i, t.n, p);
-    store_n<false, 4>(t.m, i, t.n, m);
-    store_n<false, 4>(t.v, i, t.n, v);
+  for (int u = 0; u < 4; ++u) {
+    const int i = (u * kThreads + (int)threadIdx.x) * 4;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) adamw1(p[u][k], g[u][k], m[u][k], v[u][k], c);
+    store_n<P16, 4>(t.p, i, t.n, p[u]);
+    store_n<false, 4>(t.m, i, t.n, m[u]);
+    store_n<false, 4>(t.v, i, t.n, v[u]);
   }
 }
 
-// Larger of two values; NaN wins and stays, so that a block's scale says it.
-WS_DEVINL float max_nan(float a, float b) { return (b > a || b != b) ? b : a; }
-// Largest of a warp's non-negative values, NaN above all (as bit patterns
-// they order like integers).
-WS_DEVINL float warp_max_nonneg(float x) {
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x) & 0x7fffffffu));
+// Largest of a warp's non-negative values, as bit patterns (which order like
+// the values, NaN above all: a block's scale then says it).
+WS_DEVINL float warp_max_bits(uint32_t x) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, x));
 }
 
-// Codes of 8 values with their block's scale (ROOT: of roots, >= 0).
+// Codes of 8 values with their block's scale (ROOT: of roots, >= 0).  The
+// quotients are the correctly rounded ones (a code border is where x / scale
+// says it is) from the block's one reciprocal and a residual each (Markstein,
+// IBM J. Res. Dev. 34, 1990), with tiny scales moved away from subnormal
+// reciprocals.
 template <bool ROOT>
 WS_DEVINL void encode8(const float (&x)[8], float scale, uint32_t (&o)[2]) {
+  const float up = scale < 0x1p-64f ? 0x1p64f : 1.0f;
+  const float d = scale * up, inv = 1.0f / d;
+  float q[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float y = x[k] * up, q0 = y * inv;
+    q[k] = scale > 0.0f ? fmaf(fmaf(-q0, d, y), inv, q0) : 0.0f;
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t a = 0u;
 #pragma unroll
     for (int k = 0; k < 4; k += 2) {
-      const int e = 4 * h + k;
-      const float q0 = scale > 0.0f ? x[e] / scale : 0.0f, q1 = scale > 0.0f ? x[e + 1] / scale : 0.0f;
-      a |= (ROOT ? root_code(q0) | (root_code(q1) << 8) : e4m3x2(q0, q1)) << (8 * k);
+      const float q0 = q[4 * h + k], q1 = q[4 * h + k + 1];
+      a += (ROOT ? root_code(q0) + root_code(q1) * 256u : e4m3x2(q0, q1)) << (8 * k);
     }
     o[h] = a;
   }
@@ -311,12 +385,11 @@ template <bool ROOT>
 WS_DEVINL void decode8(const uint32_t (&w)[2], float scale, float (&x)[8]) {
 #pragma unroll
   for (int k = 0; k < 8; k += 2) {
-    const uint32_t c = w[k >> 2] >> (8 * (k & 3));
     if constexpr (ROOT) {
-      x[k] = root_value(c & 255u);
-      x[k + 1] = root_value((c >> 8) & 255u);
+      x[k] = root_value(__byte_perm(w[k >> 2], 0u, 0x4440u + (k & 3)));
+      x[k + 1] = root_value(__byte_perm(w[k >> 2], 0u, 0x4441u + (k & 3)));
     } else {
-      e4m3x2_to_f32(c & 0xffffu, x[k], x[k + 1]);
+      e4m3x2_to_f32((w[k >> 2] >> (8 * (k & 3))) & 0xffffu, x[k], x[k + 1]);
     }
     x[k] *= scale;
     x[k + 1] *= scale;
@@ -345,53 +418,61 @@ WS_DEVINL void store_codes(uint8_t* q, int left, const uint32_t (&w)[2]) {
 }
 
 // One warp per block of 256, 8 elements per lane.  The step uses the moments
-// before they are rounded to 8 bits; the scales stay fp32.
+// before they are rounded to 8 bits; the scales stay fp32.  134M fp32
+// parameters: 320 us, 6.7 TB/s; it was 410 us with a division for every code
+// and a table lookup ahead of every chunk's addresses.
 template <bool P16, bool G16>
-__global__ void __launch_bounds__(kThreads)
-    k_adamw8(const TensorDev* __restrict__ tensors, const int32_t* __restrict__ chunk,
-             const Coef* __restrict__ coef) {
+__global__ void __launch_bounds__(kThreads, 3)
+    k_adamw8(const Chunk* __restrict__ chunks, const Coef* coef) {
+  const int lane = (int)lane_id(), warp = (int)warp_id();
+  constexpr int kPer = kChunk / (kBlock8 * (kThreads / 32));  // blocks of a warp
+  const Chunk t = chunks[gridDim.x - 1 - blockIdx.x];
+  float pa[kPer][8], ga[kPer][8], sc[kPer][2];
+  uint32_t ma[kPer][2], va[kPer][2];
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int blk = u * (kThreads / 32) + warp, i = blk * kBlock8 + lane * 8;
+    const int left = min(8, t.n - i);  // elements of this lane (may be <= 0)
+    load_n<G16, 8>(t.g, i, t.n, ga[u]);
+    load_n<P16, 8>(t.p, i, t.n, pa[u]);
+    load_codes(static_cast<uint8_t*>(t.m) + i, left, ma[u]);
+    load_codes(static_cast<uint8_t*>(t.v) + i, left, va[u]);
+    const bool in = blk * kBlock8 < t.n;
+    sc[u][0] = in ? t.ms[blk] : 0.0f;
+    sc[u][1] = in ? t.vs[blk] : 0.0f;
+  }
   pdl_wait();
   pdl_launch_dependents();
-  const TensorDev t = tensors[chunk[blockIdx.x]];
   const Coef c = coef[t.group];
   if (c.skip) return;
-  const int64_t base = (int64_t)((int)blockIdx.x - t.first_chunk) * kChunk;
-  const int lane = (int)lane_id();
 #pragma unroll
-  for (int u = 0; u < kChunk / (kBlock8 * (kThreads / 32)); ++u) {
-    const int64_t b0 = base + (int64_t)(u * (kThreads / 32) + (int)warp_id()) * kBlock8;
-    if (b0 >= t.n) return;  // warp-uniform
-    const int64_t i = b0 + lane * 8;
-    const int left = (int)min((int64_t)8, t.n - i);  // elements of this lane (may be <= 0)
-    float p[8], g[8], m[8], v[8];
-    load_n<P16, 8>(t.p, i, t.n, p);
-    load_n<G16, 8>(t.g, i, t.n, g);
-    uint8_t* mq = static_cast<uint8_t*>(t.m) + i;
-    uint8_t* vq = static_cast<uint8_t*>(t.v) + i;
-    uint32_t mw[2], vw[2];
-    load_codes(mq, left, mw);
-    load_codes(vq, left, vw);
-    decode8<false>(mw, t.ms[b0 / kBlock8], m);
-    decode8<true>(vw, t.vs[b0 / kBlock8], v);
-    float mx = 0.0f, vx = 0.0f;
+  for (int u = 0; u < kPer; ++u) {
+    const int blk = u * (kThreads / 32) + warp, i = blk * kBlock8 + lane * 8;
+    if (blk * kBlock8 >= t.n) return;  // warp-uniform
+    const int left = min(8, t.n - i);
+    float(&p)[8] = pa[u];
+    float(&g)[8] = ga[u];
+    float m[8], v[8];
+    decode8<false>(ma[u], sc[u][0], m);
+    decode8<true>(va[u], sc[u][1], v);
+    uint32_t mx = 0u, vx = 0u;  // as bit patterns: NaN is above all
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       v[k] = v[k] * v[k];
-      adamw1(p[k], g[k], m[k], v[k], c);
-      v[k] = sqrtf(v[k]);  // what is kept is the root
-      mx = max_nan(mx, fabsf(m[k]));
-      vx = max_nan(vx, v[k]);
+      v[k] = adamw1(p[k], g[k], m[k], v[k], c);  // what is kept is the root
+      mx = max(mx, __float_as_uint(m[k]) & 0x7fffffffu);
+      vx = max(vx, __float_as_uint(v[k]) & 0x7fffffffu);
     }
-    const float sm = warp_max_nonneg(mx) / kMTop, sv = warp_max_nonneg(vx) / kVTop;
+    const float sm = warp_max_bits(mx) / kMTop, sv = warp_max_bits(vx) / kVTop;
     uint32_t mo[2], vo[2];
     encode8<false>(m, sm, mo);
     encode8<true>(v, sv, vo);
     store_n<P16, 8>(t.p, i, t.n, p);
-    store_codes(mq, left, mo);
-    store_codes(vq, left, vo);
+    store_codes(static_cast<uint8_t*>(t.m) + i, left, mo);
+    store_codes(static_cast<uint8_t*>(t.v) + i, left, vo);
     if (lane == 0) {
-      t.ms[b0 / kBlock8] = sm;
-      t.vs[b0 / kBlock8] = sv;
+      t.ms[blk] = sm;
+      t.vs[blk] = sv;
     }
   }
 }
@@ -399,39 +480,37 @@ __global__ void __launch_bounds__(kThreads)
 // Conversion of 8-bit states to and from fp32 (one warp per block of 256).
 template <bool ROOT>
 __global__ void __launch_bounds__(kThreads)
-    k_adamw_encode8(const float* __restrict__ x, int64_t n, uint8_t* __restrict__ codes,
-                    float* __restrict__ scale) {
+    k_adamw_encode8(const float* x, int64_t n, uint8_t* codes, float* scale) {
   pdl_wait();
   pdl_launch_dependents();
   const int64_t b = (int64_t)blockIdx.x * (kThreads / 32) + warp_id();
   if (b * kBlock8 >= n) return;
-  const int64_t i = b * kBlock8 + lane_id() * 8;
-  const int left = (int)min((int64_t)8, n - i);
+  const int i = (int)lane_id() * 8, nb = (int)min((int64_t)kBlock8, n - b * kBlock8);
+  const int left = min(8, nb - i);
   float v[8];
-  load_n<false, 8>(x, i, n, v);
-  float mx = 0.0f;
+  load_n<false, 8>(x + b * kBlock8, i, nb, v);
+  uint32_t mx = 0u;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) mx = max_nan(mx, fabsf(v[k]));
-  const float s = warp_max_nonneg(mx) / (ROOT ? kVTop : kMTop);
+  for (int k = 0; k < 8; ++k) mx = max(mx, __float_as_uint(v[k]) & 0x7fffffffu);
+  const float s = warp_max_bits(mx) / (ROOT ? kVTop : kMTop);
   uint32_t o[2];
   encode8<ROOT>(v, s, o);
-  store_codes(codes + i, left, o);
+  store_codes(codes + b * kBlock8 + i, left, o);
   if (lane_id() == 0) scale[b] = s;
 }
 template <bool ROOT, bool O16>
 __global__ void __launch_bounds__(kThreads)
-    k_adamw_decode8(const uint8_t* __restrict__ codes, const float* __restrict__ scale, int64_t n,
-                    void* __restrict__ out) {
+    k_adamw_decode8(const uint8_t* codes, const float* scale, int64_t n, void* out) {
   pdl_wait();
   pdl_launch_dependents();
   const int64_t b = (int64_t)blockIdx.x * (kThreads / 32) + warp_id();
   if (b * kBlock8 >= n) return;
-  const int64_t i = b * kBlock8 + lane_id() * 8;
+  const int i = (int)lane_id() * 8, nb = (int)min((int64_t)kBlock8, n - b * kBlock8);
   uint32_t w[2];
-  load_codes(codes + i, (int)min((int64_t)8, n - i), w);
+  load_codes(codes + b * kBlock8 + i, min(8, nb - i), w);
   float v[8];
   decode8<ROOT>(w, scale[b], v);
-  store_n<O16, 8>(out, i, n, v);
+  store_n<O16, 8>(static_cast<uint8_t*>(out) + b * kBlock8 * (O16 ? 2 : 4), i, nb, v);
 }
 
 bool al16p(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -477,8 +556,8 @@ ws_status ws_adamw_plan_size(const ws_adamw_tensor* tensors, int32_t n_tensors, 
   int64_t nc = 0;
   const ws_status s = check_tensors(tensors, n_tensors, n_groups, types, &nc);
   if (s != WS_OK) return s;
-  *plan_bytes = plan_layout(n_tensors, n_groups, nc).bytes;
-  *workspace_bytes = coef_bytes(n_groups) + (size_t)nc * sizeof(double);
+  *plan_bytes = plan_layout(n_groups, nc).bytes;
+  *workspace_bytes = coef_bytes(n_groups) + (size_t)nc * sizeof(float);
   return WS_OK;
 }
 
@@ -489,7 +568,7 @@ ws_status ws_adamw_plan_init(const ws_adamw_tensor* tensors, int32_t n_tensors, 
   int64_t nc = 0;
   const ws_status s = check_tensors(tensors, n_tensors, n_groups, types, &nc);
   if (s != WS_OK) return s;
-  const Layout L = plan_layout(n_tensors, n_groups, nc);
+  const Layout L = plan_layout(n_groups, nc);
   if (image_bytes < L.bytes) return WS_ERR_OOM;
   try {
     // every range the step writes, and the gradients, must be apart
@@ -528,19 +607,29 @@ ws_status ws_adamw_plan_init(const ws_adamw_tensor* tensors, int32_t n_tensors, 
   }
   memset(image, 0, L.bytes);
   uint8_t* im = static_cast<uint8_t*>(image);
-  TensorDev* td = reinterpret_cast<TensorDev*>(im + L.tensors);
+  Chunk* ch = reinterpret_cast<Chunk*>(im + L.chunk);
   int32_t* gf = reinterpret_cast<int32_t*>(im + L.group_first);
-  int32_t* ch = reinterpret_cast<int32_t*>(im + L.chunk);
   // chunks listed by group, tensors in the caller's order inside a group
   // (one pass over the tensors per group would be quadratic: count, then place)
   for (int32_t i = 0; i < n_tensors; ++i) gf[tensors[i].group + 1] += (int32_t)chunks_of(tensors[i].n);
   for (int32_t h = 0; h < n_groups; ++h) gf[h + 1] += gf[h];
+  const int64_t pb = types.p_dtype == WS_DTYPE_F32 ? 4 : 2, gb = types.g_dtype == WS_DTYPE_F32 ? 4 : 2;
+  const int64_t sb = types.state_bits / 8;
   for (int32_t i = 0; i < n_tensors; ++i) {
     const ws_adamw_tensor& t = tensors[i];
-    const int32_t first = gf[t.group], c = (int32_t)chunks_of(t.n);
-    td[i] = TensorDev{t.p, t.g, t.m, t.v, t.m_scale, t.v_scale, t.n, t.group, first};
-    for (int32_t k = 0; k < c; ++k) ch[first + k] = i;
-    gf[t.group] = first + c;
+    for (int64_t e = 0; e < t.n; e += kChunk) {
+      Chunk& c = ch[gf[t.group]++];
+      c.p = static_cast<uint8_t*>(t.p) + e * pb;
+      c.g = static_cast<const uint8_t*>(t.g) + e * gb;
+      c.m = static_cast<uint8_t*>(t.m) + e * sb;
+      c.v = static_cast<uint8_t*>(t.v) + e * sb;
+      if (types.state_bits == 8) {
+        c.ms = t.m_scale + e / kBlock8;
+        c.vs = t.v_scale + e / kBlock8;
+      }
+      c.n = (int32_t)std::min<int64_t>(kChunk, t.n - e);
+      c.group = t.group;
+    }
   }
   // gf[h] now holds the end of group h: shift it back to the starts
   for (int32_t h = n_groups; h > 0; --h) gf[h] = gf[h - 1];
@@ -564,14 +653,13 @@ ws_status ws_adamw_step(const ws_adamw_plan* plan, ws_adamw_group* groups, int32
     return WS_ERR_INVALID;
   if (!al16p(plan->image) || !al16p(groups) || !al16p(workspace)) return WS_ERR_ALIGN;
   if (reinterpret_cast<uintptr_t>(norms) & 3u) return WS_ERR_ALIGN;
-  if (ws_bytes < coef_bytes(plan->n_groups) + (size_t)plan->n_chunks * sizeof(double)) return WS_ERR_OOM;
-  const Layout L = plan_layout(plan->n_tensors, plan->n_groups, plan->n_chunks);
+  if (ws_bytes < coef_bytes(plan->n_groups) + (size_t)plan->n_chunks * sizeof(float)) return WS_ERR_OOM;
+  const Layout L = plan_layout(plan->n_groups, plan->n_chunks);
   const uint8_t* im = static_cast<const uint8_t*>(plan->image);
-  const TensorDev* td = reinterpret_cast<const TensorDev*>(im + L.tensors);
   const int32_t* gf = reinterpret_cast<const int32_t*>(im + L.group_first);
-  const int32_t* ch = reinterpret_cast<const int32_t*>(im + L.chunk);
+  const Chunk* ch = reinterpret_cast<const Chunk*>(im + L.chunk);
   Coef* coef = static_cast<Coef*>(workspace);
-  double* partial = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + coef_bytes(plan->n_groups));
+  float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + coef_bytes(plan->n_groups));
   cudaStream_t st = (cudaStream_t)stream;
   const dim3 grid((unsigned)plan->n_chunks), block(kThreads);
   const bool p16 = ty.p_dtype == WS_DTYPE_BF16, g16 = ty.g_dtype == WS_DTYPE_BF16;
@@ -579,22 +667,22 @@ ws_status ws_adamw_step(const ws_adamw_plan* plan, ws_adamw_group* groups, int32
   cudaError_t e = cudaSuccess;
   if (measure) {
     note_launch();
-    e = launch_pdl(g16 ? k_adamw_sumsq<true> : k_adamw_sumsq<false>, grid, block, 0, st, td, ch, partial);
+    e = launch_pdl(g16 ? k_adamw_sumsq<true> : k_adamw_sumsq<false>, grid, block, 0, st, ch, partial);
     if (e != cudaSuccess) return WS_ERR_CUDA;
   }
   note_launch();
-  e = launch_pdl(k_adamw_begin, dim3((unsigned)plan->n_groups), block, 0, st, groups, gf,
-                 (const double*)(measure ? partial : nullptr), norms, (flags & WS_ADAMW_CLIP) ? 1 : 0, coef);
+  e = launch_pdl(k_adamw_begin, dim3((unsigned)plan->n_groups), dim3(kBeginThreads), 0, st, groups, gf,
+                 (const float*)(measure ? partial : nullptr), norms, (flags & WS_ADAMW_CLIP) ? 1 : 0, coef);
   if (e != cudaSuccess) return WS_ERR_CUDA;
   note_launch();
-  void (*k)(const TensorDev*, const int32_t*, const Coef*);
+  void (*k)(const Chunk*, const Coef*);
   if (ty.state_bits == 32)
     k = p16 ? (g16 ? k_adamw32<true, true> : k_adamw32<true, false>)
             : (g16 ? k_adamw32<false, true> : k_adamw32<false, false>);
   else
     k = p16 ? (g16 ? k_adamw8<true, true> : k_adamw8<true, false>)
             : (g16 ? k_adamw8<false, true> : k_adamw8<false, false>);
-  e = launch_pdl(k, grid, block, 0, st, td, ch, (const Coef*)coef);
+  e = launch_pdl(k, grid, block, 0, st, ch, (const Coef*)coef);
   return e == cudaSuccess ? WS_OK : WS_ERR_CUDA;
 }
 

@@ -53,7 +53,7 @@ PlanLayout plan_layout(int64_t M, int64_t n) {
 // order gives the same), the counts scanned, and the rows placed warp by warp
 // so that equal adapters keep the row order.
 __global__ void __launch_bounds__(kPlanThreads)
-    k_multi_plan(const int32_t* __restrict__ row_adapter, int M, int n, int32_t* __restrict__ plan,
+    k_multi_plan(const int32_t* row_adapter, int M, int n, int32_t* plan,
                  int64_t o_row, int64_t o_perm, int64_t o_off, int64_t o_tile, int64_t o_slot,
                  int64_t o_tile_ad, int tile_rows) {
   pdl_wait();
@@ -208,10 +208,10 @@ WS_DEVINL uint32_t keep2(uint32_t v, uint32_t b) {
 constexpr int kSkWarps = 8;
 template <bool F_CJ, bool F16, bool MASKED>
 __global__ void __launch_bounds__(kSkWarps * 32)
-    k_multi_skinny(const uint16_t* __restrict__ X, const void* __restrict__ Fv, int64_t strideF,
-                   int C, const uint32_t* __restrict__ mask, const int32_t* __restrict__ plan,
-                   int64_t o_perm, int64_t o_tile, int64_t o_slot, float* __restrict__ out,
-                   uint32_t* __restrict__ ext, int64_t M, uint32_t* __restrict__ bad) {
+    k_multi_skinny(const uint16_t* X, const void* Fv, int64_t strideF,
+                   int C, const uint32_t* mask, const int32_t* plan,
+                   int64_t o_perm, int64_t o_tile, int64_t o_slot, float* out,
+                   uint32_t* ext, int64_t M, uint32_t* bad) {
   __shared__ float part[kSkWarps][kTileRows * kR];
   __shared__ float sum[kTileRows * kR];
   const int lane = (int)lane_id(), warp = (int)warp_id(), g = lane >> 2, t = lane & 3;
@@ -475,17 +475,17 @@ __global__ void __launch_bounds__(kWgWarps * 32) k_multi_wgrad(const WgArgs w) {
 // tile of the dequant GEMM needs 128 rows and a pipeline of a dozen steps; here
 // a warp decodes 16 RG weight rows in registers, as the 16-row operand of
 // mma.sync, and the rows of x are its 8-wide operand, so no decoded weight
-// passes through shared memory.  A lane holds 16 code bytes (32 weights, one
-// block scale) of two weight rows per 128-deep step; x is staged in shared
-// memory in that order of k.  CTA = 128 RG weight rows; a cluster of CTAs
-// shares their contraction, and adds its partial sums in rank order through
-// distributed shared memory.
+// passes through shared memory.  A lane holds one 64-weight block (one scale,
+// one value table) of two weight rows per 256-deep step, so four lanes read a
+// whole 128-byte line of codes; x is staged in shared memory in that order of
+// k.  CTA = 128 RG weight rows; a cluster of CTAs shares their contraction, and
+// adds its partial sums in rank order through distributed shared memory.
 //
 // Starts beside the kernel that makes U (programmatic launch): the weights and
 // x are read before the wait for it (that kernel has waited for everything
 // earlier), U and the adapters after.
 constexpr int kFewWarps = 8;
-constexpr int kFewStages = 4;   // 128-deep steps of x in flight
+constexpr int kFewStages = 3;   // stages of x in flight
 struct FewArgs {
   const uint8_t* codes;
   const float* absmax;
@@ -502,96 +502,128 @@ template <int NT, int RG>
 struct FewCfg {
   static constexpr int ROWS = kFewWarps * 16 * RG;
   static constexpr int MR = NT * 8;
-  static constexpr int STAGE = MR * 256;           // bytes of 128 k of MR rows
+  static constexpr int SPS = NT <= 2 ? 2 : 1;      // 256-deep steps per stage of x
+  static constexpr int STAGE = MR * 512 * SPS;     // bytes
+  static constexpr int CTAS = NT <= 2 ? 3 : (RG == 1 ? 2 : 1);  // CTAs of an SM that the registers allow
   static constexpr int PITCH = ROWS + 4;           // floats; [MR][PITCH] partial sums
   static constexpr int SMEM = kFewStages * STAGE > MR * PITCH * 4 ? kFewStages * STAGE : MR * PITCH * 4;
-  static constexpr int PF = RG == 1 ? 4 : 2;       // steps of codes in registers
 };
 
 template <int NT, int RG, bool F16>
-__global__ void __launch_bounds__(kFewWarps * 32) k_multi_few(const FewArgs a) {
+__global__ void __launch_bounds__(kFewWarps * 32, FewCfg<NT, RG>::CTAS) k_multi_few(const FewArgs a) {
   using C = FewCfg<NT, RG>;
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = (int)lane_id(), warp = (int)warp_id(), g = lane >> 2, t = lane & 3;
   const int CS = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
   const int m0 = (int)blockIdx.z * C::MR, mrows = min(C::MR, a.M - m0);
-  const int n0 = (int)blockIdx.y * C::ROWS, nw = n0 + warp * 16 * RG;  // this warp's first weight row
-  const int segs = (a.K + 127) / 128;
-  const int s_beg = (int)((int64_t)rank * segs / CS), s_end = (int)((int64_t)(rank + 1) * segs / CS);
+  const int n0 = (int)blockIdx.y * C::ROWS;
+  // this warp's first weight row (a warp past the last row repeats the last
+  // ones: its sums are not used)
+  const int nw = min(n0 + warp * 16 * RG, a.N - 16 * RG);
+  const int steps = (a.K + 255) / 256;
+  const int s_beg = (int)((int64_t)rank * steps / CS), s_end = (int)((int64_t)(rank + 1) * steps / CS);
 
-  // x of one 128-deep step: 16-byte chunk c (k = 8c ..) of row m at chunk place
-  // (c % 4) * 4 + c / 4, odd rows with the 64-byte halves swapped, so that the
-  // eight lanes of a quarter warp read eight different bank groups
-  auto stage_x = [&](int s) {
-    if (s < s_end) {
-      uint8_t* dst = smem + (s % kFewStages) * C::STAGE;
-      for (int i = threadIdx.x; i < C::MR * 16; i += kFewWarps * 32) {
-        const int m = i / 16, c = i % 16, k = s * 128 + c * 8;
-        const bool in = m < mrows && k < a.K;
-        const uint32_t at = (uint32_t)(m * 256 + ((((c & 3) * 4 + (c >> 2)) * 16) ^ ((m & 1) * 64)));
-        cp_async16(smem_u32(dst + at), a.x + (in ? (int64_t)(m0 + m) * a.K + k : 0), in ? 16u : 0u);
+  // x of one stage: 16-byte chunk c (k = 8c ..) of row m of a 256-deep step at
+  // chunk place (c % 8) * 4 + c / 8, odd rows with the 64-byte halves of each
+  // 128 bytes swapped, so that the eight lanes of a quarter warp read eight
+  // different bank groups.  A thread copies chunk xc of rows xm, xm + XM, ...
+  constexpr int XC = 32 * C::SPS, XM = kFewWarps * 32 / XC, XQ = C::MR / XM;
+  static_assert(XQ >= 1 && C::MR % XM == 0, "every thread has a row");
+  const int xc = threadIdx.x % XC, xm = threadIdx.x / XC;
+  const uint16_t* xsrc = a.x + (int64_t)(m0 + xm) * a.K + (int64_t)s_beg * 256 + xc * 8;
+  const uint32_t xdst = smem_u32(smem) + (uint32_t)((xc / 32) * C::MR * 512 + xm * 512 +
+                                                    ((((xc & 7) * 4 + ((xc & 31) >> 3)) * 16) ^ ((xm & 1) * 64)));
+  static_assert(XM % 2 == 0, "a thread's rows have one parity");
+  int xk = s_beg * 256 + xc * 8;  // first element of the chunk
+  const int xk_end = min(a.K, s_end * 256);
+  auto stage_x = [&](int slot) {
+    if (xk - xc * 8 < xk_end) {
+#pragma unroll
+      for (int q = 0; q < XQ; ++q) {
+        const bool in = xm + q * XM < mrows && xk < xk_end;
+        cp_async16(xdst + (uint32_t)(slot * C::STAGE + q * XM * 512), in ? xsrc + (int64_t)q * XM * a.K : a.x, in ? 16u : 0u);
       }
+      xsrc += 256 * C::SPS;
+      xk += 256 * C::SPS;
     }
     cp_async_commit();
   };
-  struct Codes {
-    uint4 w[RG][2];
-    float s[RG][2];
-  };
-  auto load_codes = [&](Codes& f, int s) {
-    const int k = s * 128 + t * 32;
+  // codes and scales of the step to come, reloaded as they are used
+  uint4 cw[RG][2][2];
+  float cs[RG][2];
+  const int64_t kb = a.K / 2;
+  const uint8_t* cp = a.codes + (int64_t)(nw + g) * kb + (int64_t)s_beg * 128 + t * 32;
+  const float* sp = a.absmax + ((int64_t)s_beg * 4 + t) * a.N + nw + g;
+  // the last step may end inside its four blocks: lanes past the end read
+  // codes that exist and a scale of 0
+  int k_lane = s_beg * 256 + t * 64;
+  auto load_w = [&](int q) {
+    const uint8_t* p = k_lane < a.K ? cp : a.codes;
 #pragma unroll
     for (int r = 0; r < RG; ++r)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int n = nw + r * 16 + h * 8 + g;
-        const bool in = s < s_end && n < a.N && k < a.K;
-        f.w[r][h] = in ? __ldg(reinterpret_cast<const uint4*>(a.codes + (int64_t)n * (a.K / 2) + k / 2)) : make_uint4(0, 0, 0, 0);
-        f.s[r][h] = in ? __ldg(a.absmax + (int64_t)(k / 64) * a.N + n) : 0.0f;
-      }
+      for (int h = 0; h < 2; ++h)
+        cw[r][h][q] = __ldg(reinterpret_cast<const uint4*>(p + (int64_t)(r * 16 + h * 8) * kb) + q);
+  };
+  auto load_s = [&]() {
+#pragma unroll
+    for (int r = 0; r < RG; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) cs[r][h] = k_lane < a.K ? __ldg(sp + r * 16 + h * 8) : 0.0f;
   };
 #pragma unroll
-  for (int i = 0; i < kFewStages - 1; ++i) stage_x(s_beg + i);
-  Codes f[C::PF];
-#pragma unroll
-  for (int i = 0; i < C::PF; ++i) load_codes(f[i], s_beg + i);
+  for (int i = 0; i < kFewStages - 1; ++i) stage_x(i);
+  if (s_beg < s_end) {
+    load_s();
+    load_w(0);
+    load_w(1);
+  }
   float acc[RG][NT][4] = {};
-  for (int sb = s_beg; sb < s_end; sb += C::PF) {
-#pragma unroll
-    for (int i = 0; i < C::PF; ++i) {
-      const int s = sb + i;
-      if (s >= s_end) break;  // CTA-uniform
+  int slot = 0, part = 0;  // stage of x and step within it
+  for (int s = s_beg; s < s_end; ++s) {
+    if (part == 0) {
       cp_async_wait<kFewStages - 2>();
-      __syncthreads();  // step s of x has landed; everyone is done with step s - 1
-      stage_x(s + kFewStages - 1);
-      Nf4Table tb[RG][2];
+      __syncthreads();  // this stage of x has landed; everyone is done with the one before
+      stage_x(slot == 0 ? kFewStages - 1 : slot - 1);
+    }
+    Nf4Table tb[RG][2];
+#pragma unroll
+    for (int r = 0; r < RG; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) tb[r][h] = make_table(cs[r][h]);
+    const bool more = s + 1 < s_end;
+    const int k_now = k_lane;
+    cp += 128;
+    sp += (int64_t)4 * a.N;
+    k_lane = k_now + 256;
+    if (more) load_s();
+    const uint8_t* xs = smem + slot * C::STAGE + part * C::MR * 512 + g * 512 + t * 16;
+    const uint32_t flip = (uint32_t)(g & 1) * 64;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      uint4 d[RG][2];
 #pragma unroll
       for (int r = 0; r < RG; ++r)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) tb[r][h] = make_table(f[i].s[r][h]);
-      const uint8_t* xs = smem + (s % kFewStages) * C::STAGE + g * 256 + t * 16;
-      const uint32_t flip = (uint32_t)(g & 1) * 64;
+        for (int h = 0; h < 2; ++h) {
+          const uint4 q = cw[r][h][w / 4];
+          const uint32_t c = (w & 3) == 0 ? q.x : (w & 3) == 1 ? q.y : (w & 3) == 2 ? q.z : q.w;
+          d[r][h] = dq8(c, tb[r][h]);
+        }
+      if ((w & 3) == 3 && more) load_w(w / 4);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint4 d[RG][2];
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint4 b = *reinterpret_cast<const uint4*>(xs + nt * 4096 + ((w * 64) ^ flip));
 #pragma unroll
-        for (int r = 0; r < RG; ++r)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4 q = f[i].w[r][h];
-            d[r][h] = dq8(w == 0 ? q.x : w == 1 ? q.y : w == 2 ? q.z : q.w, tb[r][h]);
-          }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint4 b = *reinterpret_cast<const uint4*>(xs + nt * 2048 + ((w * 64) ^ flip));
-#pragma unroll
-          for (int r = 0; r < RG; ++r) {
-            mma16816(acc[r][nt], d[r][0].x, d[r][1].x, d[r][0].y, d[r][1].y, b.x, b.y);
-            mma16816(acc[r][nt], d[r][0].z, d[r][1].z, d[r][0].w, d[r][1].w, b.z, b.w);
-          }
+        for (int r = 0; r < RG; ++r) {
+          mma16816(acc[r][nt], d[r][0].x, d[r][1].x, d[r][0].y, d[r][1].y, b.x, b.y);
+          mma16816(acc[r][nt], d[r][0].z, d[r][1].z, d[r][0].w, d[r][1].w, b.z, b.w);
         }
       }
-      load_codes(f[i], s + C::PF);
+    }
+    if (++part == C::SPS) {
+      part = 0;
+      if (++slot == kFewStages) slot = 0;
     }
   }
   cp_async_wait<0>();
@@ -749,13 +781,13 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t st) {
     return per * device_sm_count();
   }();
   if (resident <= 0) return cudaErrorInvalidConfiguration;
-  const int blocks = (a.N + C::ROWS - 1) / C::ROWS, chunks = (a.M + C::MR - 1) / C::MR, segs = (a.K + 127) / 128;
+  const int blocks = (a.N + C::ROWS - 1) / C::ROWS, chunks = (a.M + C::MR - 1) / C::MR, steps = (a.K + 255) / 256;
   // CTAs sharing a contraction: the fewest steps in a row, a wave of CTAs
-  // counting its longest CTA and about three steps to start and join
+  // counting its longest CTA and about two steps to start and join
   int cs = 1, best = 0x7fffffff;
   for (int c = 1; c <= 8; c *= 2) {
     const int waves = (blocks * chunks * c + resident - 1) / resident;
-    const int cost = waves * ((segs + c - 1) / c + 3);
+    const int cost = waves * ((steps + c - 1) / c + 2);
     if (cost < best) best = cost, cs = c;
   }
   return launch_cluster(k, dim3((unsigned)cs, (unsigned)blocks, (unsigned)chunks), kFewWarps * 32, cs, C::SMEM, st, a);
@@ -764,7 +796,7 @@ template <bool F16>
 cudaError_t run_few_t(const FewArgs& a, cudaStream_t st) {
   if (a.M <= 8) return launch_few<1, 1, F16>(a, st);
   if (a.M <= 16) return launch_few<2, 1, F16>(a, st);
-  if (a.M <= 32) return launch_few<4, 2, F16>(a, st);
+  if (a.M <= 32) return launch_few<4, 1, F16>(a, st);
   return launch_few<8, 2, F16>(a, st);
 }
 cudaError_t run_few(const FewArgs& a, bool f16, cudaStream_t st) {

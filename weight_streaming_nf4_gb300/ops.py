@@ -450,14 +450,27 @@ def _need(ok, msg):
         raise ValueError(msg)
 
 
+def _device():
+    """The current CUDA device, or -2 while CUDA is not in use (no tensor is there)."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+
+
 def _here(*ts):
     """Every tensor (or None) is contiguous and on the current CUDA device."""
-    d = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    d = _device()
     for t in ts:
-        if t is not None:
-            _need(t.is_cuda and t.get_device() == d,
-                  f"tensor on {t.device}; the call runs on the current device, cuda:{d}")
+        if t is not None and (t.get_device() != d or not t.is_contiguous()):
             _need(t.is_contiguous(), "tensors must be contiguous")
+            raise ValueError(f"tensor on {t.device}; the call runs on the current device (cuda:{d})")
+
+
+def _raw(stream):
+    """cudaStream_t of a stream, or of the current one."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(_device())
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _empty(shape, dtype, device, stream):
@@ -474,7 +487,7 @@ def dropout_mask(key: DropoutKey, M: int, K: int, mask=None, device="cuda", stre
         mask = _empty((M, K // 32), torch.int32, device, stream)
     _here(mask)
     _need(mask.dtype == torch.int32 and tuple(mask.shape) == (M, K // 32), "mask: int32 [M, K/32]")
-    _check("ws_dropout_mask", _lib.ws_dropout_mask(key, M, K, _ptr(mask), _stream(stream)))
+    _check("ws_dropout_mask", _lib.ws_dropout_mask(key, M, K, _addr(mask), _raw(stream)))
     return mask
 
 
@@ -523,7 +536,7 @@ def lora_multi_plan(row_adapter, n_adapters: int, plan: LoraPlan = None, stream=
         plan = LoraPlan(_empty((int(n.value) // 4,), torch.int32, row_adapter.device, stream), M, n_adapters)
     _need(plan.M == M and plan.n == n_adapters, "the plan was made for another M or number of adapters")
     _check("ws_lora_multi_plan_init",
-           _lib.ws_lora_multi_plan_init(C.byref(plan.c), _ptr(row_adapter), _stream(stream)))
+           _lib.ws_lora_multi_plan_init(C.byref(plan.c), _addr(row_adapter), _raw(stream)))
     return plan
 
 
@@ -560,9 +573,9 @@ def lora_linear_fwd_multi(W: NF4Weight, x, aset: LoraSet, plan: LoraPlan, mask=N
     _here(x, mask, y, U, workspace, W.codes, W.absmax)
     w = W.c()
     _check("ws_lora_linear_fwd_multi",
-           _lib.ws_lora_linear_fwd_multi(C.byref(w), _ptr(x), C.byref(aset.c), C.byref(plan.c), _ptr(mask),
-                                         _ptr(y), _ptr(U), _ptr(workspace), workspace.nbytes,
-                                         _stream(stream)))
+           _lib.ws_lora_linear_fwd_multi(C.byref(w), _addr(x), C.byref(aset.c), C.byref(plan.c), _addr(mask),
+                                         _addr(y), _addr(U), _addr(workspace), workspace.nbytes,
+                                         _raw(stream)))
     return y, U
 
 
@@ -593,12 +606,12 @@ def lora_linear_bwd_multi(W: NF4Weight, x, aset: LoraSet, plan: LoraPlan, U, dY,
     w = W.c()
     dt = WS_DTYPE_F32 if dX.dtype == torch.float32 else WS_DTYPE_BF16
     _check("ws_lora_linear_bwd_multi",
-           _lib.ws_lora_linear_bwd_multi(C.byref(w), _ptr(x), C.byref(aset.c), C.byref(plan.c), _ptr(mask),
-                                         _ptr(U), _ptr(dY), _ptr(dX), dt,
+           _lib.ws_lora_linear_bwd_multi(C.byref(w), _addr(x), C.byref(aset.c), C.byref(plan.c), _addr(mask),
+                                         _addr(U), _addr(dY), _addr(dX), dt,
                                          (WS_ACC_DX if accumulate else 0)
                                          | (WS_ACC_GRADS if grad_accumulate else 0),
-                                         _ptr(dA), _ptr(dB), _ptr(workspace), workspace.nbytes,
-                                         _stream(stream)))
+                                         _addr(dA), _addr(dB), _addr(workspace), workspace.nbytes,
+                                         _raw(stream)))
     return dX, dA, dB
 
 
@@ -663,7 +676,7 @@ class AdamWPlan:
         image = torch.empty(int(pb.value), dtype=torch.uint8)
         self.c = AdamwPlanC()
         _check("ws_adamw_plan_init",
-               _lib.ws_adamw_plan_init(arr, n, ng, ty, _ptr(image), image.numel(), C.byref(self.c)))
+               _lib.ws_adamw_plan_init(arr, n, ng, ty, _addr(image), image.numel(), C.byref(self.c)))
         self.image = image.to(params[0].device)
         self.c.image = self.image.data_ptr()
         self.workspace = torch.empty(int(wb.value), dtype=torch.uint8, device=params[0].device)
@@ -688,8 +701,8 @@ def adamw_step(plan: AdamWPlan, groups, norms=None, clip=False, workspace=None, 
     _need(norms is None or (norms.dtype == torch.float32 and norms.numel() == plan.n_groups), "norms: fp32 [n_groups]")
     _here(groups, norms, ws, plan.image)
     _check("ws_adamw_step",
-           _lib.ws_adamw_step(C.byref(plan.c), _ptr(groups), WS_ADAMW_CLIP if clip else 0, _ptr(norms),
-                              _ptr(ws), ws.nbytes, _stream(stream)))
+           _lib.ws_adamw_step(C.byref(plan.c), _addr(groups), WS_ADAMW_CLIP if clip else 0, _addr(norms),
+                              _addr(ws), ws.nbytes, _raw(stream)))
 
 
 def _adamw_codes(codes, scales):
@@ -709,8 +722,8 @@ def adamw_encode8(values, root: bool, codes=None, scales=None, stream=None):
     _here(values, codes, scales)
     _adamw_codes(codes, scales)
     _need(codes.numel() == n, "codes: one a value")
-    _check("ws_adamw_encode8", _lib.ws_adamw_encode8(_ptr(values), n, 1 if root else 0, _ptr(codes),
-                                                     _ptr(scales), _stream(stream)))
+    _check("ws_adamw_encode8", _lib.ws_adamw_encode8(_addr(values), n, 1 if root else 0, _addr(codes),
+                                                     _addr(scales), _raw(stream)))
     return codes, scales
 
 
@@ -723,9 +736,9 @@ def adamw_decode8(codes, scales, root: bool, out=None, dtype=torch.float32, stre
     _here(codes, scales, out)
     _adamw_codes(codes, scales)
     _check("ws_adamw_decode8",
-           _lib.ws_adamw_decode8(_ptr(codes), _ptr(scales), codes.numel(), 1 if root else 0, _ptr(out),
+           _lib.ws_adamw_decode8(_addr(codes), _addr(scales), codes.numel(), 1 if root else 0, _addr(out),
                                  WS_DTYPE_F32 if out.dtype == torch.float32 else WS_DTYPE_BF16,
-                                 _stream(stream)))
+                                 _raw(stream)))
     return out
 
 
