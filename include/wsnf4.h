@@ -433,9 +433,9 @@ ws_status ws_attention_bwd(const uint16_t* q, const uint16_t* k, const uint16_t*
  * in fp32; a bf16 p is rounded once, when it is stored.
  * Moments in 32 bits: m and v fp32 [n].  In 8 bits: blocks of 256 consecutive
  * elements of a tensor (the last may be short) with an fp32 scale each:
- *   m: e4m3 code [n] times m_scale [ceil(n/256)] = max|m| / 448;
+ *   m: e4m3 code [n] times m_scale [ceil(n/256)] = max|m| (1/448);
  *   v: code c [n] of sqrt(v): (1 + (c & 15)/16) 2^((c >> 4) - 15), 0 for c = 0,
- *      times v_scale [ceil(n/256)] = max sqrt(v) / 1.9375; never 0 for v > 0.
+ *      times v_scale [ceil(n/256)] = max sqrt(v) (1/1.9375); never 0 for v > 0.
  * Both to nearest (ties to even); the step uses the moments before this
  * rounding.  Zero codes and scales are zero moments.  A gradient that is not
  * finite makes its element's moments (in 8 bits: its whole block's) NaN,
@@ -486,8 +486,8 @@ ws_status ws_adamw_plan_init(const ws_adamw_tensor* tensors, int32_t n_tensors, 
  * receives each group's gradient norm, before clipping.  WS_ADAMW_CLIP: c =
  * min(1, max_norm / (norm + 1e-6)), and a group whose norm is not finite takes
  * no step (its tensors and counter stay as they are); else c = 1.  Squares are
- * taken and summed in fp32, in a fixed order: a norm beyond 1.8e19 counts as not
- * finite, and gradients below 1e-19 count for nothing. */
+ * summed in two fp32 parts, in a fixed order: a norm beyond 1.8e19 counts as
+ * not finite, and gradients below 1e-19 count for little. */
 enum { WS_ADAMW_CLIP = 1 };
 ws_status ws_adamw_step(const ws_adamw_plan* plan, ws_adamw_group* groups, int32_t flags,
                         float* norms, void* workspace, size_t ws_bytes, ws_stream_t stream);

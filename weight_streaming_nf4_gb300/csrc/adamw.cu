@@ -9,9 +9,9 @@
 // step is bound by memory (28 bytes per fp32 parameter with 32-bit states,
 // 16 with 8-bit ones).
 //
-// Sums of squares run in a fixed order in fp32 (16 elements of a thread, a
-// butterfly, 8 warps; then the chunks the same way), so repeated steps give the
-// same bits.
+// Sums of squares run in a fixed order in two fp32 parts (16 elements of a
+// thread, a butterfly, 8 warps; then the chunks the same way), so repeated steps
+// give the same bits and the clip factor is the rounded one of exact sums.
 #include <math.h>
 #include <string.h>
 
@@ -200,13 +200,15 @@ WS_DEVINL float rcp_approx(float x) {
 // contraction), as the formula is written: a value that lies on the border
 // between two 8-bit codes then falls the way it does for anybody who
 // evaluates the formula in fp32.
-// Returns the root of the new v.
+// Returns the root of the new v, correctly rounded (EXACT: it is kept, as an
+// 8-bit code) or to 2^-22.
+template <bool EXACT>
 WS_DEVINL float adamw1(float& p, float g, float& m, float& v, const Coef& c) {
   g = __fmul_rn(g, c.clip);
   m = __fadd_rn(__fmul_rn(m, c.beta1), __fmul_rn(g, c.one_m_beta1));
   v = __fadd_rn(__fmul_rn(v, c.beta2), __fmul_rn(__fmul_rn(g, g), c.one_m_beta2));
-  // root and reciprocal of the step to 2^-22 or better: it is a small change of p
-  const float root = sqrt_approx(v);
+  // the step to 2^-21 or better: it is a small change of p
+  const float root = EXACT ? __fsqrt_rn(v) : sqrt_approx(v);
   p = fmaf(-c.step_size, m * rcp_approx(fmaf(root, c.rbc2, c.eps)), p * c.decay);
   return root;
 }
@@ -215,29 +217,51 @@ WS_DEVINL float adamw1(float& p, float g, float& m, float& v, const Coef& c) {
 // Only the plan's tables are declared __restrict__: what an earlier kernel
 // writes may not be, or the compiler may load it ahead of the wait for that
 // kernel.
+// A sum in two fp32 parts, h + l: twice the precision at a few operations an
+// element, where double precision would bind the pass (Knuth's two-sum, and a
+// product's error by a fused multiply-add).
+struct Sum2 {
+  float h, l;
+};
+WS_DEVINL void add2(Sum2& s, float x, float e) {
+  const float t = __fadd_rn(s.h, x), z = __fsub_rn(t, s.h);
+  s.l = __fadd_rn(s.l, __fadd_rn(__fadd_rn(__fsub_rn(s.h, __fsub_rn(t, z)), __fsub_rn(x, z)), e));
+  s.h = t;
+}
+WS_DEVINL Sum2 warp_sum2(Sum2 s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float h = __shfl_xor_sync(0xffffffffu, s.h, o), l = __shfl_xor_sync(0xffffffffu, s.l, o);
+    add2(s, h, l);  // (a NaN stays)
+  }
+  return s;
+}
+
 template <bool G16>
 __global__ void __launch_bounds__(kThreads)
-    k_adamw_sumsq(const Chunk* __restrict__ chunks, float* partial) {
+    k_adamw_sumsq(const Chunk* __restrict__ chunks, float2* partial) {
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ float red[kThreads / 32];
+  __shared__ Sum2 red[kThreads / 32];
   const Chunk t = chunks[blockIdx.x];
   float g[2][8];
 #pragma unroll
   for (int u = 0; u < 2; ++u) load_n<G16, 8>(t.g, (u * kThreads + (int)threadIdx.x) * 8, t.n, g[u]);
-  float s = 0.0f;
+  Sum2 s{0.0f, 0.0f};
 #pragma unroll
   for (int u = 0; u < 2; ++u)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s = fmaf(g[u][k], g[u][k], s);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    for (int k = 0; k < 8; ++k) {
+      const float q = __fmul_rn(g[u][k], g[u][k]);
+      add2(s, q, fmaf(g[u][k], g[u][k], -q));
+    }
+  s = warp_sum2(s);
   if (lane_id() == 0) red[warp_id()] = s;
   __syncthreads();
   if (threadIdx.x == 0) {
-    s = 0.0f;
-    for (int w = 0; w < kThreads / 32; ++w) s += red[w];
-    partial[blockIdx.x] = s;
+    s = red[0];
+    for (int w = 1; w < kThreads / 32; ++w) add2(s, red[w].h, red[w].l);
+    partial[blockIdx.x] = make_float2(s.h, s.l);
   }
 }
 
@@ -255,32 +279,31 @@ WS_DEVINL double pow_int(double b, double t) {
 // butterfly and then the warps in index order follow.  Double precision is
 // slow here (a warp's product takes as long as dozens in fp32: with every
 // thread computing the powers the kernel took 25 us), so only one thread each
-// makes them and the sums stay in fp32.
+// makes them and the sums stay in fp32 parts.
 constexpr int kBeginThreads = 1024;
 __global__ void __launch_bounds__(kBeginThreads)
     k_adamw_begin(ws_adamw_group* groups, const int32_t* __restrict__ group_first,
-                  const float* partial, float* norms, int clip,
+                  const float2* partial, float* norms, int clip,
                   Coef* coef) {
-  __shared__ float red[kBeginThreads / 32];
+  __shared__ Sum2 red[kBeginThreads / 32];
   __shared__ float bc[2];  // 1 - beta^t
   const int h = blockIdx.x;
   pdl_wait();
   pdl_launch_dependents();
   if (partial) {
-    float s = 0.0f;
+    Sum2 s{0.0f, 0.0f};
     const int end = group_first[h + 1];
     int i = group_first[h] + threadIdx.x;
     for (; i + 3 * kBeginThreads < end; i += 4 * kBeginThreads) {
-      const float a = partial[i], b = partial[i + kBeginThreads], c = partial[i + 2 * kBeginThreads],
-                  d = partial[i + 3 * kBeginThreads];
-      s += a;
-      s += b;
-      s += c;
-      s += d;
+      const float2 a = partial[i], b = partial[i + kBeginThreads], c = partial[i + 2 * kBeginThreads],
+                   d = partial[i + 3 * kBeginThreads];
+      add2(s, a.x, a.y);
+      add2(s, b.x, b.y);
+      add2(s, c.x, c.y);
+      add2(s, d.x, d.y);
     }
-    for (; i < end; i += kBeginThreads) s += partial[i];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    for (; i < end; i += kBeginThreads) add2(s, partial[i].x, partial[i].y);
+    s = warp_sum2(s);
     if (lane_id() == 0) red[warp_id()] = s;
   }
   if (threadIdx.x == 32 || threadIdx.x == 64) {
@@ -293,15 +316,16 @@ __global__ void __launch_bounds__(kBeginThreads)
   Coef c{};
   c.clip = 1.0f;
   if (partial) {
-    float s = 0.0f;
-    for (int w = 0; w < kBeginThreads / 32; ++w) s += red[w];
-    const float norm = sqrtf(s);
-    if (norms) norms[h] = norm;
+    Sum2 s = red[0];
+    for (int w = 1; w < kBeginThreads / 32; ++w) add2(s, red[w].h, red[w].l);
+    // (a sum that is not finite has no error part)
+    const double norm = isfinite(s.h) ? sqrt((double)s.h + (double)s.l) : (double)s.h;
+    if (norms) norms[h] = (float)norm;
     if (clip) {
       // a norm that is not finite would write NaN over every parameter of
       // the group: the group takes no step and its counter stands
-      if (!(norm <= 3.402823466e38f)) c.skip = 1;
-      else if (g.max_norm > 0.0) c.clip = fminf(1.0f, (float)g.max_norm / (norm + 1e-6f));
+      if (!isfinite(s.h)) c.skip = 1;
+      else if (g.max_norm > 0.0) c.clip = (float)fmin(1.0, g.max_norm / (norm + 1e-6));
     }
   }
   if (!c.skip) groups[h].step = g.step + 1.0;
@@ -342,7 +366,7 @@ __global__ void __launch_bounds__(kThreads)
   for (int u = 0; u < 4; ++u) {
     const int i = (u * kThreads + (int)threadIdx.x) * 4;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) adamw1(p[u][k], g[u][k], m[u][k], v[u][k], c);
+    for (int k = 0; k < 4; ++k) (void)adamw1<false>(p[u][k], g[u][k], m[u][k], v[u][k], c);
     store_n<P16, 4>(t.p, i, t.n, p[u]);
     store_n<false, 4>(t.m, i, t.n, m[u]);
     store_n<false, 4>(t.v, i, t.n, v[u]);
@@ -459,11 +483,11 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       v[k] = v[k] * v[k];
-      v[k] = adamw1(p[k], g[k], m[k], v[k], c);  // what is kept is the root
+      v[k] = adamw1<true>(p[k], g[k], m[k], v[k], c);  // what is kept is the root
       mx = max(mx, __float_as_uint(m[k]) & 0x7fffffffu);
       vx = max(vx, __float_as_uint(v[k]) & 0x7fffffffu);
     }
-    const float sm = warp_max_bits(mx) / kMTop, sv = warp_max_bits(vx) / kVTop;
+    const float sm = warp_max_bits(mx) * (1.0f / kMTop), sv = warp_max_bits(vx) * (1.0f / kVTop);
     uint32_t mo[2], vo[2];
     encode8<false>(m, sm, mo);
     encode8<true>(v, sv, vo);
@@ -492,7 +516,7 @@ __global__ void __launch_bounds__(kThreads)
   uint32_t mx = 0u;
 #pragma unroll
   for (int k = 0; k < 8; ++k) mx = max(mx, __float_as_uint(v[k]) & 0x7fffffffu);
-  const float s = warp_max_bits(mx) / (ROOT ? kVTop : kMTop);
+  const float s = warp_max_bits(mx) * (ROOT ? 1.0f / kVTop : 1.0f / kMTop);
   uint32_t o[2];
   encode8<ROOT>(v, s, o);
   store_codes(codes + b * kBlock8 + i, left, o);
@@ -557,7 +581,7 @@ ws_status ws_adamw_plan_size(const ws_adamw_tensor* tensors, int32_t n_tensors, 
   const ws_status s = check_tensors(tensors, n_tensors, n_groups, types, &nc);
   if (s != WS_OK) return s;
   *plan_bytes = plan_layout(n_groups, nc).bytes;
-  *workspace_bytes = coef_bytes(n_groups) + (size_t)nc * sizeof(float);
+  *workspace_bytes = coef_bytes(n_groups) + (size_t)nc * sizeof(float2);
   return WS_OK;
 }
 
@@ -653,13 +677,13 @@ ws_status ws_adamw_step(const ws_adamw_plan* plan, ws_adamw_group* groups, int32
     return WS_ERR_INVALID;
   if (!al16p(plan->image) || !al16p(groups) || !al16p(workspace)) return WS_ERR_ALIGN;
   if (reinterpret_cast<uintptr_t>(norms) & 3u) return WS_ERR_ALIGN;
-  if (ws_bytes < coef_bytes(plan->n_groups) + (size_t)plan->n_chunks * sizeof(float)) return WS_ERR_OOM;
+  if (ws_bytes < coef_bytes(plan->n_groups) + (size_t)plan->n_chunks * sizeof(float2)) return WS_ERR_OOM;
   const Layout L = plan_layout(plan->n_groups, plan->n_chunks);
   const uint8_t* im = static_cast<const uint8_t*>(plan->image);
   const int32_t* gf = reinterpret_cast<const int32_t*>(im + L.group_first);
   const Chunk* ch = reinterpret_cast<const Chunk*>(im + L.chunk);
   Coef* coef = static_cast<Coef*>(workspace);
-  float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + coef_bytes(plan->n_groups));
+  float2* partial = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + coef_bytes(plan->n_groups));
   cudaStream_t st = (cudaStream_t)stream;
   const dim3 grid((unsigned)plan->n_chunks), block(kThreads);
   const bool p16 = ty.p_dtype == WS_DTYPE_BF16, g16 = ty.g_dtype == WS_DTYPE_BF16;
@@ -672,7 +696,7 @@ ws_status ws_adamw_step(const ws_adamw_plan* plan, ws_adamw_group* groups, int32
   }
   note_launch();
   e = launch_pdl(k_adamw_begin, dim3((unsigned)plan->n_groups), dim3(kBeginThreads), 0, st, groups, gf,
-                 (const float*)(measure ? partial : nullptr), norms, (flags & WS_ADAMW_CLIP) ? 1 : 0, coef);
+                 (const float2*)(measure ? partial : nullptr), norms, (flags & WS_ADAMW_CLIP) ? 1 : 0, coef);
   if (e != cudaSuccess) return WS_ERR_CUDA;
   note_launch();
   void (*k)(const Chunk*, const Coef*);

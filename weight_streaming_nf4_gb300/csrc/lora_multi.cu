@@ -189,6 +189,13 @@ WS_DEVINL void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
   hi = pack_bf16x2(x, y);
   lo = pack_bf16x2(x - bf16_lo(hi), y - bf16_hi(hi));
 }
+// Three parts: 24 bits, all of an fp32 value.
+WS_DEVINL void split3(float x, float y, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  hi = pack_bf16x2(x, y);
+  x -= bf16_lo(hi);
+  y -= bf16_hi(hi);
+  split2(x, y, mid, lo);
+}
 // Zeroes the halves of a bf16 pair whose keep bit (bits 0, 1 of b) is clear.
 WS_DEVINL uint32_t keep2(uint32_t v, uint32_t b) {
   return v & (((b & 1u) ? 0x0000ffffu : 0u) | ((b & 2u) ? 0xffff0000u : 0u));
@@ -197,7 +204,8 @@ WS_DEVINL uint32_t keep2(uint32_t v, uint32_t b) {
 // ------------------------------------------------------------------------ skinny products
 // out[row][0..16) = sum_c X~[row][c] F_a[.][c] for the rows of one tile (one
 // adapter): U = (mask . x) A_a^T with F = A [16, C], or G = dY B_a with F = B
-// [C, 16] (F_CJ).  X is bf16 and exact; an fp32 F enters as two bf16 parts.
+// [C, 16] (F_CJ).  X is bf16 and exact; an fp32 F enters as three bf16 parts,
+// all of its bits (two parts cost U a factor of ten in error).
 //
 // Bound by reading X and the adapters once.  A cluster of CTAs shares a tile's
 // contraction: its warps take the 64-deep steps in turn (a single-row tile of
@@ -258,7 +266,7 @@ __global__ void __launch_bounds__(kSkWarps * 32)
     }
   for (int st = rank * kSkWarps + warp; st < C / 64; st += kSkWarps * CS) {
     const int c0 = st * 64 + 16 * t;
-    uint32_t bh[2][4][2], bl[2][4][2];
+    uint32_t bh[2][4][2], bm[2][4][2], bl[2][4][2];
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
       const int j = nt * 8 + g;
@@ -283,8 +291,8 @@ __global__ void __launch_bounds__(kSkWarps * 32)
         }
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          split2(v[4 * s], v[4 * s + 1], bh[nt][s][0], bl[nt][s][0]);
-          split2(v[4 * s + 2], v[4 * s + 3], bh[nt][s][1], bl[nt][s][1]);
+          split3(v[4 * s], v[4 * s + 1], bh[nt][s][0], bm[nt][s][0], bl[nt][s][0]);
+          split3(v[4 * s + 2], v[4 * s + 3], bh[nt][s][1], bm[nt][s][1], bl[nt][s][1]);
         }
       }
     }
@@ -315,9 +323,12 @@ __global__ void __launch_bounds__(kSkWarps * 32)
         for (int nt = 0; nt < 2; ++nt) {
           mma16816(acc[u][nt], x[0][2 * s], x[1][2 * s], x[0][2 * s + 1], x[1][2 * s + 1],
                    bh[nt][s][0], bh[nt][s][1]);
-          if constexpr (!F16)
+          if constexpr (!F16) {
+            mma16816(acc[u][nt], x[0][2 * s], x[1][2 * s], x[0][2 * s + 1], x[1][2 * s + 1],
+                     bm[nt][s][0], bm[nt][s][1]);
             mma16816(acc[u][nt], x[0][2 * s], x[1][2 * s], x[0][2 * s + 1], x[1][2 * s + 1],
                      bl[nt][s][0], bl[nt][s][1]);
+          }
         }
     }
   }
@@ -367,7 +378,7 @@ __global__ void __launch_bounds__(kSkWarps * 32)
 //   dB_a [N, 16] = s_a sum_{m of a} dY[m]^T U[m],  dA_a [16, K] = s_a sum_{m of a} G[m]^T (mask . x)[m]
 // CTA = 64 columns of dY or x for one adapter: D (16 x 64) += P^T Q over the
 // adapter's rows, 16 at a time, warps taking turns; the warps' sums are added
-// in warp order.  Q is bf16 and exact, the fp32 P enters as two bf16 parts.
+// in warp order.  Q is bf16 and exact, the fp32 P enters as three bf16 parts.
 // A lane reads 8 consecutive columns of four rows (16 bytes each, 128 bytes of
 // a row per eight lanes) and pairs rows with byte permutes: column 8g + i of
 // the tile is column g of the i-th 8-wide product, so nothing is transposed
@@ -429,17 +440,18 @@ __global__ void __launch_bounds__(kWgWarps * 32) k_multi_wgrad(const WgArgs w) {
         p[i][0] = p[i][1] = 0.0f;
       }
     }
-    uint32_t ah[4], al[4];
-    split2(p[0][0], p[1][0], ah[0], al[0]);
-    split2(p[0][1], p[1][1], ah[1], al[1]);
-    split2(p[2][0], p[3][0], ah[2], al[2]);
-    split2(p[2][1], p[3][1], ah[3], al[3]);
+    uint32_t ah[4], am[4], al[4];
+    split3(p[0][0], p[1][0], ah[0], am[0], al[0]);
+    split3(p[0][1], p[1][1], ah[1], am[1], al[1]);
+    split3(p[2][0], p[3][0], ah[2], am[2], al[2]);
+    split3(p[2][1], p[3][1], ah[3], am[3], al[3]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int k = i / 2;
       const uint32_t b0 = (i & 1) ? hi_pair(q[0][k], q[1][k]) : lo_pair(q[0][k], q[1][k]);
       const uint32_t b1 = (i & 1) ? hi_pair(q[2][k], q[3][k]) : lo_pair(q[2][k], q[3][k]);
       mma16816(d[i], ah[0], ah[1], ah[2], ah[3], b0, b1);
+      mma16816(d[i], am[0], am[1], am[2], am[3], b0, b1);
       mma16816(d[i], al[0], al[1], al[2], al[3], b0, b1);
     }
   }
