@@ -214,6 +214,10 @@ WS_DEVINL uint32_t keep2(uint32_t v, uint32_t b) {
 // memory.  A lane reads 16 consecutive elements of a row (whole 128-byte
 // lines per four lanes).
 constexpr int kSkWarps = 8;
+template <int V>
+struct Int {
+  static constexpr int value = V;
+};
 template <bool F_CJ, bool F16, bool MASKED>
 __global__ void __launch_bounds__(kSkWarps * 32)
     k_multi_skinny(const uint16_t* X, const void* Fv, int64_t strideF,
@@ -227,18 +231,18 @@ __global__ void __launch_bounds__(kSkWarps * 32)
   pdl_wait();
   pdl_launch_dependents();
   if (ext && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *bad = 0u;  // for the GEMM that follows
+  const int4 tile = *reinterpret_cast<const int4*>(plan + o_tile + 4 * (int64_t)blockIdx.y);  // (the table has room for it)
   if ((int)blockIdx.y >= plan[0]) return;  // the whole cluster alike
-  const int4 tile = *reinterpret_cast<const int4*>(plan + o_tile + 4 * (int64_t)blockIdx.y);
   const int32_t* rows = plan + o_perm + tile.y;
   const int cnt = tile.z, nsub = (cnt + 15) / 16;
-  const int slots = plan[1];
+  const int slots = ext ? plan[1] : 0;
   // a pair of results (r, j), (r, j + 1), i = r * 16 + j: fp32, and split into
   // bf16 parts [hi | lo | hi | 0] in the row's slot, zeros in the others
   auto put = [&](int i, float v0, float v1) {
     const int64_t row = rows[i / kR];
     const int j = i % kR;
     *reinterpret_cast<float2*>(out + row * kR + j) = make_float2(v0, v1);
-    if (slots <= 0 || !ext) return;
+    if (slots <= 0) return;
     const int own = plan[o_slot + row];
     uint32_t hi, lo;
     split2(v0, v1, hi, lo);
@@ -256,82 +260,117 @@ __global__ void __launch_bounds__(kSkWarps * 32)
     return;
   }
   float acc[4][2][4] = {};
-  int64_t ro[4][2];  // row offsets (or -1) of this lane's rows of each 16-row part
+  // one 64-deep step: the factor's fragments, then the rows 16 at a time.  The
+  // step's products are summed by themselves and added in fp32: the tensor
+  // cores cut off what a long running sum cannot hold.
+  auto run = [&](auto ns) {
+    constexpr int NS = decltype(ns)::value;
+    int64_t ro[NS][2];  // row offsets (or -1) of this lane's rows of each 16-row part
 #pragma unroll
-  for (int s = 0; s < 4; ++s)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = s * 16 + h * 8 + g;
-      ro[s][h] = r < cnt ? (int64_t)rows[r] * C : -1;
-    }
-  for (int st = rank * kSkWarps + warp; st < C / 64; st += kSkWarps * CS) {
-    const int c0 = st * 64 + 16 * t;
-    uint32_t bh[2][4][2], bm[2][4][2], bl[2][4][2];
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      const int j = nt * 8 + g;
-      if constexpr (F16) {
-        const uint4* f = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(Fv) +
-                                                        tile.x * strideF + (int64_t)j * C + c0);
-        const uint4 p = f[0], q = f[1];
-        bh[nt][0][0] = p.x, bh[nt][0][1] = p.y, bh[nt][1][0] = p.z, bh[nt][1][1] = p.w;
-        bh[nt][2][0] = q.x, bh[nt][2][1] = q.y, bh[nt][3][0] = q.z, bh[nt][3][1] = q.w;
-      } else {
-        float v[16];
-        const float* F = static_cast<const float*>(Fv) + tile.x * strideF;
-        if constexpr (F_CJ) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = F[(int64_t)(c0 + e) * kR + j];
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float4 w = reinterpret_cast<const float4*>(F + (int64_t)j * C + c0)[q];
-            v[4 * q] = w.x, v[4 * q + 1] = w.y, v[4 * q + 2] = w.z, v[4 * q + 3] = w.w;
-          }
-        }
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          split3(v[4 * s], v[4 * s + 1], bh[nt][s][0], bm[nt][s][0], bl[nt][s][0]);
-          split3(v[4 * s + 2], v[4 * s + 3], bh[nt][s][1], bm[nt][s][1], bl[nt][s][1]);
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (u >= nsub) break;
-      uint32_t x[2][8];
+    for (int u = 0; u < NS; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (ro[u][h] >= 0) {
-          const uint4* s = reinterpret_cast<const uint4*>(X + ro[u][h] + c0);
-          const uint4 p = s[0], q = s[1];
-          x[h][0] = p.x, x[h][1] = p.y, x[h][2] = p.z, x[h][3] = p.w;
-          x[h][4] = q.x, x[h][5] = q.y, x[h][6] = q.z, x[h][7] = q.w;
-          if constexpr (MASKED) {
-            const uint32_t b = mask[(ro[u][h] + c0) >> 5] >> (c0 & 31);
+        const int r = u * 16 + h * 8 + g;
+        ro[u][h] = r < cnt ? (int64_t)rows[r] * C : -1;
+      }
+    struct Fac {
+      uint4 w[F16 ? 4 : 8];  // this lane's 16 values for j = g and for j = g + 8
+    };
+    auto load_f = [&](Fac& f, int st) {
+      const int c0 = st * 64 + 16 * t;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[h][e] = keep2(x[h][e], b >> (2 * e));
-          }
+      for (int nt = 0; nt < 2; ++nt) {
+        const int j = nt * 8 + g;
+        if constexpr (F16) {
+          const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(Fv) + tile.x * strideF + (int64_t)j * C + c0);
+          f.w[2 * nt] = p[0], f.w[2 * nt + 1] = p[1];
+        } else if constexpr (F_CJ) {
+          const uint32_t* p = static_cast<const uint32_t*>(Fv) + tile.x * strideF + (int64_t)c0 * kR + j;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            f.w[4 * nt + q] = make_uint4(p[(4 * q) * kR], p[(4 * q + 1) * kR], p[(4 * q + 2) * kR], p[(4 * q + 3) * kR]);
         } else {
+          const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(Fv) + tile.x * strideF + (int64_t)j * C + c0);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[h][e] = 0u;
+          for (int q = 0; q < 4; ++q) f.w[4 * nt + q] = p[q];
         }
       }
+    };
+    struct Row {
+      uint4 x[2][2];
+      uint32_t keep[2];
+    };
+    auto load_x = [&](Row& r, int st, int u) {
+      const int c0 = st * 64 + 16 * t;
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+      for (int h = 0; h < 2; ++h) {
+        r.x[h][0] = r.x[h][1] = make_uint4(0u, 0u, 0u, 0u);
+        r.keep[h] = 0xffffu;
+        if (ro[u][h] >= 0) {
+          const uint4* p = reinterpret_cast<const uint4*>(X + ro[u][h] + c0);
+          r.x[h][0] = p[0], r.x[h][1] = p[1];
+          if constexpr (MASKED) r.keep[h] = mask[(ro[u][h] + c0) >> 5] >> (c0 & 31);
+        }
+      }
+    };
+    const int step = kSkWarps * CS;
+    int st = rank * kSkWarps + warp;
+    const int end = C / 64;
+    Fac f;
+    Row r;
+    if (st < end) {
+      load_f(f, st);
+      load_x(r, st, 0);
+    }
+    for (; st < end; st += step) {
+      uint32_t b[F16 ? 1 : 3][2][4][2];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          mma16816(acc[u][nt], x[0][2 * s], x[1][2 * s], x[0][2 * s + 1], x[1][2 * s + 1],
-                   bh[nt][s][0], bh[nt][s][1]);
-          if constexpr (!F16) {
-            mma16816(acc[u][nt], x[0][2 * s], x[1][2 * s], x[0][2 * s + 1], x[1][2 * s + 1],
-                     bm[nt][s][0], bm[nt][s][1]);
-            mma16816(acc[u][nt], x[0][2 * s], x[1][2 * s], x[0][2 * s + 1], x[1][2 * s + 1],
-                     bl[nt][s][0], bl[nt][s][1]);
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          if constexpr (F16) {
+            const uint4 q = f.w[2 * nt + s / 2];
+            b[0][nt][s][0] = (s & 1) ? q.z : q.x;
+            b[0][nt][s][1] = (s & 1) ? q.w : q.y;
+          } else {
+            const uint4 q = f.w[4 * nt + s];
+            split3(__uint_as_float(q.x), __uint_as_float(q.y), b[0][nt][s][0], b[1][nt][s][0], b[2][nt][s][0]);
+            split3(__uint_as_float(q.z), __uint_as_float(q.w), b[0][nt][s][1], b[1][nt][s][1], b[2][nt][s][1]);
           }
         }
+      const bool more = st + step < end;
+      if (more) load_f(f, st + step);
+#pragma unroll
+      for (int u = 0; u < NS; ++u) {
+        uint32_t x[2][8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          x[h][0] = r.x[h][0].x, x[h][1] = r.x[h][0].y, x[h][2] = r.x[h][0].z, x[h][3] = r.x[h][0].w;
+          x[h][4] = r.x[h][1].x, x[h][5] = r.x[h][1].y, x[h][6] = r.x[h][1].z, x[h][7] = r.x[h][1].w;
+          if constexpr (MASKED) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[h][e] = keep2(x[h][e], r.keep[h] >> (2 * e));
+          }
+        }
+        if (u + 1 < NS) load_x(r, st, u + 1);
+        else if (more) load_x(r, st + step, 0);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          float d[4] = {};
+#pragma unroll
+          for (int k = F16 ? 0 : 2; k >= 0; --k)  // small parts first
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              mma16816(d, x[0][2 * s], x[1][2 * s], x[0][2 * s + 1], x[1][2 * s + 1], b[k][nt][s][0], b[k][nt][s][1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[u][nt][e] += d[e];
+        }
+      }
     }
-  }
+  };
+  if (nsub == 1) run(Int<1>{});
+  else if (nsub == 2) run(Int<2>{});
+  else run(Int<4>{});
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     if (u >= nsub) break;
@@ -376,14 +415,15 @@ __global__ void __launch_bounds__(kSkWarps * 32)
 // ------------------------------------------------------------------------ weight gradients
 // One launch for both gradients of every adapter:
 //   dB_a [N, 16] = s_a sum_{m of a} dY[m]^T U[m],  dA_a [16, K] = s_a sum_{m of a} G[m]^T (mask . x)[m]
-// CTA = 64 columns of dY or x for one adapter: D (16 x 64) += P^T Q over the
-// adapter's rows, 16 at a time, warps taking turns; the warps' sums are added
-// in warp order.  Q is bf16 and exact, the fp32 P enters as three bf16 parts.
-// A lane reads 8 consecutive columns of four rows (16 bytes each, 128 bytes of
-// a row per eight lanes) and pairs rows with byte permutes: column 8g + i of
-// the tile is column g of the i-th 8-wide product, so nothing is transposed
-// through shared memory.  Bound by reading dY and x once.
-constexpr int kWgWarps = 8;
+// CTA = 128 columns of dY or x for one adapter: four warps take the adapter's
+// rows in turn, 16 at a time, for each 64 columns, D (16 x 64) += P^T Q, and
+// their sums are added in warp order.  Q is bf16 and exact, the fp32 P enters
+// as three bf16 parts.  A lane reads 8 consecutive columns of four rows (16
+// bytes each, 128 bytes of a row per eight lanes) one step ahead and pairs rows
+// with byte permutes: column 8g + i of the tile is column g of the i-th 8-wide
+// product, so nothing is transposed through shared memory.  Bound by reading
+// dY and x once.
+constexpr int kWgWarps = 8, kWgSplit = 4;
 struct WgArgs {
   const float* P[2];      // U, G  [M, 16]
   const uint16_t* Q[2];   // dY [M, C0], x [M, C1]
@@ -396,67 +436,81 @@ struct WgArgs {
   int64_t o_perm, o_off;
   int accumulate;
 };
-WS_DEVINL uint32_t lo_pair(uint32_t a, uint32_t b) { return (a & 0xffffu) | (b << 16); }
-WS_DEVINL uint32_t hi_pair(uint32_t a, uint32_t b) { return (a >> 16) | (b & 0xffff0000u); }
+WS_DEVINL uint32_t lo_pair(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
+WS_DEVINL uint32_t hi_pair(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
 
-__global__ void __launch_bounds__(kWgWarps * 32) k_multi_wgrad(const WgArgs w) {
+__global__ void __launch_bounds__(kWgWarps * 32, 2) k_multi_wgrad(const WgArgs w) {
   __shared__ float red[kWgWarps][kR][64];
   const int lane = (int)lane_id(), warp = (int)warp_id(), g = lane >> 2, t = lane & 3;
   pdl_wait();
   pdl_launch_dependents();
-  const int nb = w.C[0] / 64;
-  const int which = (int)blockIdx.x >= nb ? 1 : 0;
-  const int col0 = ((int)blockIdx.x - (which ? nb : 0)) * 64;
   const int a = blockIdx.y;
-  const int C = which ? w.C[1] : w.C[0];
-  const float* P = which ? w.P[1] : w.P[0];
-  const uint16_t* Q = which ? w.Q[1] : w.Q[0];
-  const uint32_t* mask = which ? w.mask : nullptr;
-  const int r_beg = w.plan[w.o_off + a], r_end = w.plan[w.o_off + a + 1];
-  const int cnt = r_end - r_beg;
+  const int r_beg = w.plan[w.o_off + a], cnt = w.plan[w.o_off + a + 1] - r_beg;
   if (cnt == 0 && w.accumulate) return;
+  const int nb = (w.C[0] + 127) / 128;
+  const int which = (int)blockIdx.x >= nb ? 1 : 0;
+  const int C = which ? w.C[1] : w.C[0];
+  const int cta0 = ((int)blockIdx.x - (which ? nb : 0)) * 128;
+  const int col0 = cta0 + (warp / kWgSplit) * 64, part = warp % kWgSplit;
+  const bool cols = col0 < C;
+  const float* P = which ? w.P[1] : w.P[0];
+  const uint16_t* Q = (which ? w.Q[1] : w.Q[0]) + col0 + 8 * g;
+  const uint32_t* mask = which ? w.mask : nullptr;
   const int32_t* rows = w.plan + w.o_perm + r_beg;
-  float d[8][4] = {};
-  for (int s0 = warp * 16; s0 < cnt; s0 += kWgWarps * 16) {
-    uint32_t q[4][4];    // rows 2t, 2t+1, 2t+8, 2t+9 of the step; 8 columns
-    float p[4][2];       // P of those rows at j = g, g + 8
+  struct Step {
+    uint4 q[4];      // rows 2t, 2t+1, 2t+8, 2t+9 of the step; 8 columns
+    float p[4][2];   // P of those rows at j = g, g + 8
+    uint32_t keep[4];
+  };
+  auto load = [&](Step& f, int s0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = s0 + 2 * t + (i & 1) + (i >> 1) * 8;
+      f.q[i] = make_uint4(0u, 0u, 0u, 0u);
+      f.p[i][0] = f.p[i][1] = 0.0f;
+      f.keep[i] = 0xffu;
       if (r < cnt) {
         const int64_t row = rows[r];
-        const uint4 v = *reinterpret_cast<const uint4*>(Q + row * C + col0 + 8 * g);
-        q[i][0] = v.x, q[i][1] = v.y, q[i][2] = v.z, q[i][3] = v.w;
-        if (mask) {
-          const int64_t e = row * C + col0 + 8 * g;
-          const uint32_t b = mask[e >> 5] >> (e & 31);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) q[i][k] = keep2(q[i][k], b >> (2 * k));
-        }
-        p[i][0] = P[row * kR + g];
-        p[i][1] = P[row * kR + g + 8];
-      } else {
-        q[i][0] = q[i][1] = q[i][2] = q[i][3] = 0u;
-        p[i][0] = p[i][1] = 0.0f;
+        f.q[i] = *reinterpret_cast<const uint4*>(Q + row * C);
+        if (mask) f.keep[i] = mask[(row * C + col0) / 32 + g / 4] >> (8 * (g & 3));
+        f.p[i][0] = P[row * kR + g];
+        f.p[i][1] = P[row * kR + g + 8];
       }
     }
-    uint32_t ah[4], am[4], al[4];
-    split3(p[0][0], p[1][0], ah[0], am[0], al[0]);
-    split3(p[0][1], p[1][1], ah[1], am[1], al[1]);
-    split3(p[2][0], p[3][0], ah[2], am[2], al[2]);
-    split3(p[2][1], p[3][1], ah[3], am[3], al[3]);
+  };
+  float d[8][4] = {};
+  if (cols) {
+    Step f;
+    int s0 = part * 16;
+    if (s0 < cnt) load(f, s0);
+    for (; s0 < cnt; s0 += kWgSplit * 16) {
+      uint32_t ah[4], am[4], al[4], q[4][4];
+      split3(f.p[0][0], f.p[1][0], ah[0], am[0], al[0]);
+      split3(f.p[0][1], f.p[1][1], ah[1], am[1], al[1]);
+      split3(f.p[2][0], f.p[3][0], ah[2], am[2], al[2]);
+      split3(f.p[2][1], f.p[3][1], ah[3], am[3], al[3]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int k = i / 2;
-      const uint32_t b0 = (i & 1) ? hi_pair(q[0][k], q[1][k]) : lo_pair(q[0][k], q[1][k]);
-      const uint32_t b1 = (i & 1) ? hi_pair(q[2][k], q[3][k]) : lo_pair(q[2][k], q[3][k]);
-      mma16816(d[i], ah[0], ah[1], ah[2], ah[3], b0, b1);
-      mma16816(d[i], am[0], am[1], am[2], am[3], b0, b1);
-      mma16816(d[i], al[0], al[1], al[2], al[3], b0, b1);
+      for (int i = 0; i < 4; ++i) {
+        q[i][0] = f.q[i].x, q[i][1] = f.q[i].y, q[i][2] = f.q[i].z, q[i][3] = f.q[i].w;
+        if (mask) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) q[i][k] = keep2(q[i][k], f.keep[i] >> (2 * k));
+        }
+      }
+      if (s0 + kWgSplit * 16 < cnt) load(f, s0 + kWgSplit * 16);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int k = i / 2;
+        const uint32_t b0 = (i & 1) ? hi_pair(q[0][k], q[1][k]) : lo_pair(q[0][k], q[1][k]);
+        const uint32_t b1 = (i & 1) ? hi_pair(q[2][k], q[3][k]) : lo_pair(q[2][k], q[3][k]);
+        mma16816(d[i], ah[0], ah[1], ah[2], ah[3], b0, b1);
+        mma16816(d[i], am[0], am[1], am[2], am[3], b0, b1);
+        mma16816(d[i], al[0], al[1], al[2], al[3], b0, b1);
+      }
     }
   }
-  const int nw = min(kWgWarps, (cnt + 15) / 16);  // warps that had rows
-  if (warp < nw) {
+  const int nw = min(kWgSplit, (cnt + 15) / 16);  // parts that had rows
+  if (part < nw) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -469,15 +523,27 @@ __global__ void __launch_bounds__(kWgWarps * 32) k_multi_wgrad(const WgArgs w) {
   __syncthreads();
   const float s = w.scale[a];
   float* out = (which ? w.out[1] : w.out[0]) + a * (which ? w.stride[1] : w.stride[0]);
+  // four results a thread at a time: along k for dA [16, K], along j for dB [N, 16]
 #pragma unroll
-  for (int k = 0; k < kR * 64 / (kWgWarps * 32); ++k) {
-    const int i = k * kWgWarps * 32 + threadIdx.x;
-    const int j = which ? i / 64 : i % kR, c = which ? i % 64 : i / kR;
-    float v = 0.0f;
-    for (int x = 0; x < nw; ++x) v += red[x][j][c];
-    v = __fmul_rn(v, s);  // rounded by itself: accumulating adds the finished contribution once
-    float* o = out + (which ? (int64_t)j * C + col0 + c : (int64_t)(col0 + c) * kR + j);
-    *o = w.accumulate ? *o + v : v;
+  for (int k = 0; k < 2 * kR * 64 / (kWgWarps * 32 * 4); ++k) {
+    const int i = (k * kWgWarps * 32 + (int)threadIdx.x) * 4;
+    const int grp = i / (kR * 64), e = i % (kR * 64);
+    const int j = which ? e / 64 : e % kR, c = which ? e % 64 : e / kR;
+    if (cta0 + grp * 64 >= C) continue;
+    float v[4] = {};
+    for (int x = 0; x < nw; ++x)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] += which ? red[grp * kWgSplit + x][j][c + u] : red[grp * kWgSplit + x][j + u][c];
+    float4* o = reinterpret_cast<float4*>(out + (which ? (int64_t)j * C + cta0 + grp * 64 + c
+                                                       : (int64_t)(cta0 + grp * 64 + c) * kR + j));
+    // rounded by themselves: accumulating adds the finished contribution once
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = __fmul_rn(v[u], s);
+    if (w.accumulate) {
+      const float4 old = *o;
+      v[0] = old.x + v[0], v[1] = old.y + v[1], v[2] = old.z + v[2], v[3] = old.w + v[3];
+    }
+    *o = make_float4(v[0], v[1], v[2], v[3]);
   }
 }
 
@@ -737,10 +803,11 @@ cudaError_t launch_cluster(K k, dim3 grid, int threads, int cluster, size_t smem
   return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
-// CTAs that share a tile's contraction: as many as have a step for every warp.
-int skinny_cluster(int64_t C) {
+// CTAs that share a tile's contraction: as many as have a step for every warp
+// and fit the GPU at once (two an SM) with the most tiles a batch can have.
+int skinny_cluster(int64_t C, int64_t tiles) {
   int cs = 8;
-  while (cs > 1 && cs * kSkWarps > C / 64) cs /= 2;
+  while (cs > 1 && (cs * kSkWarps > C / 64 || cs * tiles > 2 * device_sm_count())) cs /= 2;
   return cs;
 }
 
@@ -748,7 +815,7 @@ cudaError_t run_skinny(bool f_cj, const uint16_t* X, const void* F, bool f16, in
                        const uint32_t* mask, const ws_lora_plan& plan, float* out, uint8_t* ws,
                        const WsLayout& W, bool slots, cudaStream_t st) {
   const PlanLayout L = plan_layout(plan.M, plan.n_adapters);
-  const int cs = skinny_cluster(C);
+  const int cs = skinny_cluster(C, L.max_tiles);
   auto k = f_cj ? k_multi_skinny<true, false, false>
                 : (f16 ? (mask ? k_multi_skinny<false, true, true> : k_multi_skinny<false, true, false>)
                        : (mask ? k_multi_skinny<false, false, true> : k_multi_skinny<false, false, false>));
@@ -967,7 +1034,7 @@ ws_status ws_lora_linear_bwd_multi(const ws_nf4* W, const uint16_t* x, const ws_
   w.o_perm = P.perm, w.o_off = P.off;
   w.accumulate = (accumulate & WS_ACC_GRADS) ? 1 : 0;
   note_launch();
-  WS_RUN(launch_pdl(k_multi_wgrad, dim3((unsigned)((N + K) / 64), (unsigned)set->n_adapters), dim3(kWgWarps * 32),
+  WS_RUN(launch_pdl(k_multi_wgrad, dim3((unsigned)((N + 127) / 128 + (K + 127) / 128), (unsigned)set->n_adapters), dim3(kWgWarps * 32),
                     0, st, w));
   const MultiLora ml = multi_of(*plan, ws, L, G, set->A, false, set->stride_a, set->scale);
   WS_RUN(run_nf4_gemm_multi(plan_gemm(true, M, K, N), view(W), dY, M, ml, mask, dX, dX_dtype == WS_DTYPE_F32 ? 1 : 0,

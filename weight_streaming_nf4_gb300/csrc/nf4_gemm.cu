@@ -521,59 +521,44 @@ struct WMaps {
   CUtensorMap m[kMaxGroups];
 };
 
-// The adapter term of 16 columns from n of one row: v += u . F, with u = s_a
-// P[m] (ML kernels).  Forward: F rows n .. n+15 of B_a [N, 16]; backward:
-// columns of A_a [16, ld], under the keep bits.  Lanes are rows, so lanes of
-// one adapter read the same addresses.
+// The adapter term of 16 columns from n of row m, whose adapter is ad: the
+// path of tile rows with more than kMultiSlots adapters.  Forward: rows n ..
+// n+15 of B_a [N, 16]; backward: columns of A_a [16, ld], under the keep bits.
+// Out of line, with the sums in local memory: inside the epilogue its registers
+// made every warp of the kernel spill (backward of 2048 rows of 5120x27648:
+// 768 -> 598 us in all).
 template <bool BWD>
-WS_DEVINL void ml_add(const GemmArgs& a, int ad, int64_t n, int64_t ld, const float (&u)[16], uint32_t keep,
-                      float (&v)[16]) {
-  if constexpr (BWD) {
-    const float* F = static_cast<const float*>(a.ml_F) + ad * a.ml_stride + n;
-    float d[16] = {};
+__device__ __noinline__ void ml_add(const GemmArgs& a, int ad, int64_t m, int64_t n, int64_t ld, uint32_t keep,
+                                    float* v) {
+  const float s = a.ml_scale[ad];
+  const float* u = a.ml_P + m * 16;
+#pragma unroll 1
+  for (int e = 0; e < 16; ++e) {
+    float d = 0.0f;
+    if constexpr (BWD) {
+      const float* F = static_cast<const float*>(a.ml_F) + ad * a.ml_stride + n + e;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
+      for (int j = 0; j < 16; ++j) d = fmaf(u[j], F[j * ld], d);
+    } else if (a.ml_f16) {
+      const uint32_t* F = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.ml_F) + ad * a.ml_stride + (n + e) * 16);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float4 f = __ldg(reinterpret_cast<const float4*>(F + j * ld) + q);
-        d[4 * q] = fmaf(u[j], f.x, d[4 * q]);
-        d[4 * q + 1] = fmaf(u[j], f.y, d[4 * q + 1]);
-        d[4 * q + 2] = fmaf(u[j], f.z, d[4 * q + 2]);
-        d[4 * q + 3] = fmaf(u[j], f.w, d[4 * q + 3]);
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t f = F[j];
+        d = fmaf(u[2 * j], bf16_lo(f), d);
+        d = fmaf(u[2 * j + 1], bf16_hi(f), d);
+      }
+    } else {
+      const float4* F = reinterpret_cast<const float4*>(static_cast<const float*>(a.ml_F) + ad * a.ml_stride + (n + e) * 16);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 f = F[j];
+        d = fmaf(u[4 * j], f.x, d);
+        d = fmaf(u[4 * j + 1], f.y, d);
+        d = fmaf(u[4 * j + 2], f.z, d);
+        d = fmaf(u[4 * j + 3], f.w, d);
       }
     }
-#pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] += ((keep >> e) & 1u) ? d[e] : 0.0f;
-  } else if (a.ml_f16) {
-    const uint4* F = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.ml_F) + ad * a.ml_stride + n * 16);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const uint4 f = __ldg(F + 2 * e + q);
-        v[e] = fmaf(u[8 * q], bf16_lo(f.x), v[e]);
-        v[e] = fmaf(u[8 * q + 1], bf16_hi(f.x), v[e]);
-        v[e] = fmaf(u[8 * q + 2], bf16_lo(f.y), v[e]);
-        v[e] = fmaf(u[8 * q + 3], bf16_hi(f.y), v[e]);
-        v[e] = fmaf(u[8 * q + 4], bf16_lo(f.z), v[e]);
-        v[e] = fmaf(u[8 * q + 5], bf16_hi(f.z), v[e]);
-        v[e] = fmaf(u[8 * q + 6], bf16_lo(f.w), v[e]);
-        v[e] = fmaf(u[8 * q + 7], bf16_hi(f.w), v[e]);
-      }
-    }
-  } else {
-    const float4* F = reinterpret_cast<const float4*>(static_cast<const float*>(a.ml_F) + ad * a.ml_stride + n * 16);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float4 f = __ldg(F + 4 * e + q);
-        v[e] = fmaf(u[4 * q], f.x, v[e]);
-        v[e] = fmaf(u[4 * q + 1], f.y, v[e]);
-        v[e] = fmaf(u[4 * q + 2], f.z, v[e]);
-        v[e] = fmaf(u[4 * q + 3], f.w, v[e]);
-      }
-    }
+    if ((keep >> e) & 1u) v[e] = fmaf(s, d, v[e]);
   }
 }
 
@@ -583,15 +568,17 @@ WS_DEVINL bool ml_is_bad(float v) { return !(fabsf(v) <= 3e38f); }
 // The part of the adapter term that such values make, for the row's own
 // adapter (rare: an adapter that has diverged).
 template <bool BWD>
-__device__ __noinline__ float ml_bad_term(const GemmArgs& a, int ad, int64_t n, int64_t ld, int64_t m) {
+__device__ __noinline__ void ml_add_bad_values(const GemmArgs& a, int ad, int64_t m, int64_t n, int64_t ld,
+                                               uint32_t keep, float* v) {
   const float s = a.ml_scale[ad];
-  float d = 0.0f;
-  for (int j = 0; j < 16; ++j) {
-    const int64_t o = ad * a.ml_stride + (BWD ? (int64_t)j * ld + n : n * 16 + j);
-    const float f = a.ml_f16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(a.ml_F)[o]) : static_cast<const float*>(a.ml_F)[o];
-    if (ml_is_bad(s * f)) d += a.ml_P[m * 16 + j] * (s * f);
+  for (int e = 0; e < 16; ++e) {
+    if (!((keep >> e) & 1u)) continue;
+    for (int j = 0; j < 16; ++j) {
+      const int64_t o = ad * a.ml_stride + (BWD ? (int64_t)j * ld + n + e : (n + e) * 16 + j);
+      const float f = s * (a.ml_f16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(a.ml_F)[o]) : static_cast<const float*>(a.ml_F)[o]);
+      if (ml_is_bad(f)) v[e] += a.ml_P[m * 16 + j] * f;
+    }
   }
-  return d;
 }
 // lora_tile for one adapter of many (ad < 0: a tile of zeros), leaving out bad values.
 template <bool BWD, int BN, int PAIR>
@@ -1317,24 +1304,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row = u * 128 + r;
           const int64_t m = m0 + row;
           const bool row_ok = ok && m < args.M;
-          int ml_ad = -1;
-          float ml_u[16];
-          bool ml_bad = false;
+          // whether the epilogue has a part of the adapter term to add (ML)
+          bool ml_add_all = false, ml_add_bad = false;
           if constexpr (ML) {
-            ml_bad = ml_slots > 0 && *(volatile const uint32_t*)args.ml_bad != 0u;
-            if (!writer && row_ok) ml_ad = args.ml_row[m];
-            if (ml_ad >= 0 && ml_slots < 0) {
-              const float s = args.ml_scale[ml_ad];
-              const float4* up = reinterpret_cast<const float4*>(args.ml_P + m * 16);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float4 q = up[e];
-                ml_u[4 * e] = s * q.x;
-                ml_u[4 * e + 1] = s * q.y;
-                ml_u[4 * e + 2] = s * q.z;
-                ml_u[4 * e + 3] = s * q.w;
-              }
-            }
+            ml_add_all = ml_slots < 0;
+            ml_add_bad = ml_slots > 0 && *(volatile const uint32_t*)args.ml_bad != 0u;
           }
 #pragma unroll 1
           for (int c = 0; c < kv; ++c) {
@@ -1375,14 +1349,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!row_ok) continue;
             const int64_t o_off = m * og.width + (n - og.c0);
             if constexpr (ML) {
-              if (ml_ad >= 0 && (ml_slots < 0 || ml_bad)) {
-                const uint32_t keep = BWD && args.mask ? args.mask[o_off >> 5] >> (o_off & 31) : 0xffffu;
-                if (ml_slots < 0) {
-                  ml_add<BWD>(args, ml_ad, n, og.width, ml_u, keep, v);
-                } else {
+              if (ml_add_all || ml_add_bad) {
+                const int ad = args.ml_row[m];
+                if (ad >= 0) {
+                  const uint32_t keep = BWD && args.mask ? args.mask[o_off >> 5] >> (o_off & 31) : 0xffffu;
+                  float w[16];
 #pragma unroll
-                  for (int e = 0; e < 16; ++e)
-                    if ((keep >> e) & 1u) v[e] += ml_bad_term<BWD>(args, ml_ad, n + e, og.width, m);
+                  for (int e = 0; e < 16; ++e) w[e] = v[e];
+                  if (ml_add_all) ml_add<BWD>(args, ad, m, n, og.width, keep, w);
+                  else ml_add_bad_values<BWD>(args, ad, m, n, og.width, keep, w);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) v[e] = w[e];
                 }
               }
             }
