@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libwsnf4.so")
 SOURCES = ["nf4_gemm.cu", "lora_small.cu", "stack.cu", "api.cu", "attention.cu", "lora_multi.cu",
-           "adamw.cu"]
+           "lora_few.cu", "adamw.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

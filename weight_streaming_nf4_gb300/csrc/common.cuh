@@ -32,9 +32,10 @@ static_assert((DERR_TIMEOUT_FULL | DERR_TIMEOUT_EMPTY | DERR_TIMEOUT_BFULL | DER
                DERR_TIMEOUT_ACC | DERR_TIMEOUT_DRAIN) == WS_DERR_PIPELINE_MASK,
               "device error bits");
 
-#if defined(WS_GEMM_TU) || defined(WS_ATTN_TU)
-// Device error word of a translation unit with spin-waits (the GEMM unit and
-// the attention unit each own one); ws_device_error reads and clears both.
+#if defined(WS_GEMM_TU) || defined(WS_ATTN_TU) || defined(WS_FEW_TU)
+// Device error word of a translation unit with spin-waits (the GEMM unit, the
+// attention unit and the few-row unit each own one); ws_device_error reads and
+// clears them all.
 static __device__ uint32_t g_dev_error = 0;
 #define WS_HAS_WAITS 1
 #endif

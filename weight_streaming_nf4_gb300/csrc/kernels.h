@@ -221,6 +221,27 @@ cudaError_t run_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v
                          int nh, int nkv, int hd, uint16_t* dq, uint16_t* dk, uint16_t* dv,
                          void* ws, cudaStream_t st);
 
+// ---- many adapters, few rows (lora_few.cu) ----------------------------------------------
+// y = x W'^T + s_a U . B_a for M rows, 64 at a time.
+constexpr int kFewUnits = 256;  // CTAs of a launch at most
+struct FewArgs {
+  const uint8_t* codes;
+  const float* absmax;
+  const uint16_t* x;
+  int M, N, K;
+  const float* P;        // U [M, 16]
+  const void* F;         // B of adapter a at a * stride, [N, 16]
+  int64_t stride;
+  const float* scale;
+  const int32_t* row;    // adapter of each row, < 0: none
+  uint16_t* y;
+  float* partial;        // [kFewUnits][64][128] fp32 partial sums of cut tiles
+  uint32_t* flags;       // [kFewUnits], zeroed by the kernel before this one
+  int blocks, chunks, steps;  // set by run_few
+};
+cudaError_t few_read_and_clear_dev_error(uint32_t* flags);
+cudaError_t run_few(const FewArgs& a, bool f16, cudaStream_t st);
+
 // ---- one LoRA linear (linear.cu) --------------------------------------------------------
 size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 cudaError_t linear_fwd(const NF4View& W, const uint16_t* x, const float* A, const float* B,

@@ -223,14 +223,15 @@ __global__ void __launch_bounds__(kSkWarps * 32)
     k_multi_skinny(const uint16_t* X, const void* Fv, int64_t strideF,
                    int C, const uint32_t* mask, const int32_t* plan,
                    int64_t o_perm, int64_t o_tile, int64_t o_slot, float* out,
-                   uint32_t* ext, int64_t M, uint32_t* bad) {
+                   uint32_t* ext, int64_t M, uint32_t* zero, int n_zero) {
   __shared__ float part[kSkWarps][kTileRows * kR];
   __shared__ float sum[kTileRows * kR];
   const int lane = (int)lane_id(), warp = (int)warp_id(), g = lane >> 2, t = lane & 3;
   const int CS = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
   pdl_wait();
   pdl_launch_dependents();
-  if (ext && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *bad = 0u;  // for the GEMM that follows
+  // words the kernel that follows wants zeroed
+  if (blockIdx.x == 0 && blockIdx.y == 0 && (int)threadIdx.x < n_zero) zero[threadIdx.x] = 0u;
   const int4 tile = *reinterpret_cast<const int4*>(plan + o_tile + 4 * (int64_t)blockIdx.y);  // (the table has room for it)
   if ((int)blockIdx.y >= plan[0]) return;  // the whole cluster alike
   const int32_t* rows = plan + o_perm + tile.y;
@@ -462,15 +463,23 @@ __global__ void __launch_bounds__(kWgWarps * 32, 2) k_multi_wgrad(const WgArgs w
     float p[4][2];   // P of those rows at j = g, g + 8
     uint32_t keep[4];
   };
-  auto load = [&](Step& f, int s0) {
+  // rows of a step (-1: none), two steps ahead of their use
+  int idx[4];
+  auto load_idx = [&](int s0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = s0 + 2 * t + (i & 1) + (i >> 1) * 8;
+      idx[i] = r < cnt ? rows[r] : -1;
+    }
+  };
+  auto load = [&](Step& f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
       f.q[i] = make_uint4(0u, 0u, 0u, 0u);
       f.p[i][0] = f.p[i][1] = 0.0f;
       f.keep[i] = 0xffu;
-      if (r < cnt) {
-        const int64_t row = rows[r];
+      if (idx[i] >= 0) {
+        const int64_t row = idx[i];
         f.q[i] = *reinterpret_cast<const uint4*>(Q + row * C);
         if (mask) f.keep[i] = mask[(row * C + col0) / 32 + g / 4] >> (8 * (g & 3));
         f.p[i][0] = P[row * kR + g];
@@ -482,7 +491,9 @@ __global__ void __launch_bounds__(kWgWarps * 32, 2) k_multi_wgrad(const WgArgs w
   if (cols) {
     Step f;
     int s0 = part * 16;
-    if (s0 < cnt) load(f, s0);
+    load_idx(s0);
+    load(f);
+    load_idx(s0 + kWgSplit * 16);
     for (; s0 < cnt; s0 += kWgSplit * 16) {
       uint32_t ah[4], am[4], al[4], q[4][4];
       split3(f.p[0][0], f.p[1][0], ah[0], am[0], al[0]);
@@ -497,7 +508,8 @@ __global__ void __launch_bounds__(kWgWarps * 32, 2) k_multi_wgrad(const WgArgs w
           for (int k = 0; k < 4; ++k) q[i][k] = keep2(q[i][k], f.keep[i] >> (2 * k));
         }
       }
-      if (s0 + kWgSplit * 16 < cnt) load(f, s0 + kWgSplit * 16);
+      load(f);
+      load_idx(s0 + 2 * kWgSplit * 16);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int k = i / 2;
@@ -547,229 +559,14 @@ __global__ void __launch_bounds__(kWgWarps * 32, 2) k_multi_wgrad(const WgArgs w
   }
 }
 
-// ------------------------------------------------------------------------ few rows
-// y = x W'^T + the adapter term for at most 8 NT rows at a time (decode): bound
-// by reading the codes, and with few rows by decoding them.  The tensor-core
-// tile of the dequant GEMM needs 128 rows and a pipeline of a dozen steps; here
-// a warp decodes 16 RG weight rows in registers, as the 16-row operand of
-// mma.sync, and the rows of x are its 8-wide operand, so no decoded weight
-// passes through shared memory.  A lane holds one 64-weight block (one scale,
-// one value table) of two weight rows per 256-deep step, so four lanes read a
-// whole 128-byte line of codes; x is staged in shared memory in that order of
-// k.  CTA = 128 RG weight rows; a cluster of CTAs shares their contraction, and
-// adds its partial sums in rank order through distributed shared memory.
-//
-// Starts beside the kernel that makes U (programmatic launch): the weights and
-// x are read before the wait for it (that kernel has waited for everything
-// earlier), U and the adapters after.
-constexpr int kFewWarps = 8;
-constexpr int kFewStages = 3;   // stages of x in flight
-struct FewArgs {
-  const uint8_t* codes;
-  const float* absmax;
-  const uint16_t* x;
-  int M, N, K;
-  const float* P;        // U [M, 16]
-  const void* F;         // B of adapter a at a * stride, [N, 16]
-  int64_t stride;
-  const float* scale;
-  const int32_t* row;    // adapter of each row
-  uint16_t* y;
-};
-template <int NT, int RG>
-struct FewCfg {
-  static constexpr int ROWS = kFewWarps * 16 * RG;
-  static constexpr int MR = NT * 8;
-  static constexpr int SPS = NT <= 2 ? 2 : 1;      // 256-deep steps per stage of x
-  static constexpr int STAGE = MR * 512 * SPS;     // bytes
-  static constexpr int CTAS = NT <= 2 ? 3 : (RG == 1 ? 2 : 1);  // CTAs of an SM that the registers allow
-  static constexpr int PITCH = ROWS + 4;           // floats; [MR][PITCH] partial sums
-  static constexpr int SMEM = kFewStages * STAGE > MR * PITCH * 4 ? kFewStages * STAGE : MR * PITCH * 4;
-};
-
-template <int NT, int RG, bool F16>
-__global__ void __launch_bounds__(kFewWarps * 32, FewCfg<NT, RG>::CTAS) k_multi_few(const FewArgs a) {
-  using C = FewCfg<NT, RG>;
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int lane = (int)lane_id(), warp = (int)warp_id(), g = lane >> 2, t = lane & 3;
-  const int CS = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
-  const int m0 = (int)blockIdx.z * C::MR, mrows = min(C::MR, a.M - m0);
-  const int n0 = (int)blockIdx.y * C::ROWS;
-  // this warp's first weight row (a warp past the last row repeats the last
-  // ones: its sums are not used)
-  const int nw = min(n0 + warp * 16 * RG, a.N - 16 * RG);
-  const int steps = (a.K + 255) / 256;
-  const int s_beg = (int)((int64_t)rank * steps / CS), s_end = (int)((int64_t)(rank + 1) * steps / CS);
-
-  // x of one stage: 16-byte chunk c (k = 8c ..) of row m of a 256-deep step at
-  // chunk place (c % 8) * 4 + c / 8, odd rows with the 64-byte halves of each
-  // 128 bytes swapped, so that the eight lanes of a quarter warp read eight
-  // different bank groups.  A thread copies chunk xc of rows xm, xm + XM, ...
-  constexpr int XC = 32 * C::SPS, XM = kFewWarps * 32 / XC, XQ = C::MR / XM;
-  static_assert(XQ >= 1 && C::MR % XM == 0, "every thread has a row");
-  const int xc = threadIdx.x % XC, xm = threadIdx.x / XC;
-  const uint16_t* xsrc = a.x + (int64_t)(m0 + xm) * a.K + (int64_t)s_beg * 256 + xc * 8;
-  const uint32_t xdst = smem_u32(smem) + (uint32_t)((xc / 32) * C::MR * 512 + xm * 512 +
-                                                    ((((xc & 7) * 4 + ((xc & 31) >> 3)) * 16) ^ ((xm & 1) * 64)));
-  static_assert(XM % 2 == 0, "a thread's rows have one parity");
-  int xk = s_beg * 256 + xc * 8;  // first element of the chunk
-  const int xk_end = min(a.K, s_end * 256);
-  auto stage_x = [&](int slot) {
-    if (xk - xc * 8 < xk_end) {
-#pragma unroll
-      for (int q = 0; q < XQ; ++q) {
-        const bool in = xm + q * XM < mrows && xk < xk_end;
-        cp_async16(xdst + (uint32_t)(slot * C::STAGE + q * XM * 512), in ? xsrc + (int64_t)q * XM * a.K : a.x, in ? 16u : 0u);
-      }
-      xsrc += 256 * C::SPS;
-      xk += 256 * C::SPS;
-    }
-    cp_async_commit();
-  };
-  // codes and scales of the step to come, reloaded as they are used
-  uint4 cw[RG][2][2];
-  float cs[RG][2];
-  const int64_t kb = a.K / 2;
-  const uint8_t* cp = a.codes + (int64_t)(nw + g) * kb + (int64_t)s_beg * 128 + t * 32;
-  const float* sp = a.absmax + ((int64_t)s_beg * 4 + t) * a.N + nw + g;
-  // the last step may end inside its four blocks: lanes past the end read
-  // codes that exist and a scale of 0
-  int k_lane = s_beg * 256 + t * 64;
-  auto load_w = [&](int q) {
-    const uint8_t* p = k_lane < a.K ? cp : a.codes;
-#pragma unroll
-    for (int r = 0; r < RG; ++r)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        cw[r][h][q] = __ldg(reinterpret_cast<const uint4*>(p + (int64_t)(r * 16 + h * 8) * kb) + q);
-  };
-  auto load_s = [&]() {
-#pragma unroll
-    for (int r = 0; r < RG; ++r)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) cs[r][h] = k_lane < a.K ? __ldg(sp + r * 16 + h * 8) : 0.0f;
-  };
-#pragma unroll
-  for (int i = 0; i < kFewStages - 1; ++i) stage_x(i);
-  if (s_beg < s_end) {
-    load_s();
-    load_w(0);
-    load_w(1);
-  }
-  float acc[RG][NT][4] = {};
-  int slot = 0, part = 0;  // stage of x and step within it
-  for (int s = s_beg; s < s_end; ++s) {
-    if (part == 0) {
-      cp_async_wait<kFewStages - 2>();
-      __syncthreads();  // this stage of x has landed; everyone is done with the one before
-      stage_x(slot == 0 ? kFewStages - 1 : slot - 1);
-    }
-    Nf4Table tb[RG][2];
-#pragma unroll
-    for (int r = 0; r < RG; ++r)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) tb[r][h] = make_table(cs[r][h]);
-    const bool more = s + 1 < s_end;
-    const int k_now = k_lane;
-    cp += 128;
-    sp += (int64_t)4 * a.N;
-    k_lane = k_now + 256;
-    if (more) load_s();
-    const uint8_t* xs = smem + slot * C::STAGE + part * C::MR * 512 + g * 512 + t * 16;
-    const uint32_t flip = (uint32_t)(g & 1) * 64;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      uint4 d[RG][2];
-#pragma unroll
-      for (int r = 0; r < RG; ++r)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 q = cw[r][h][w / 4];
-          const uint32_t c = (w & 3) == 0 ? q.x : (w & 3) == 1 ? q.y : (w & 3) == 2 ? q.z : q.w;
-          d[r][h] = dq8(c, tb[r][h]);
-        }
-      if ((w & 3) == 3 && more) load_w(w / 4);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const uint4 b = *reinterpret_cast<const uint4*>(xs + nt * 4096 + ((w * 64) ^ flip));
-#pragma unroll
-        for (int r = 0; r < RG; ++r) {
-          mma16816(acc[r][nt], d[r][0].x, d[r][1].x, d[r][0].y, d[r][1].y, b.x, b.y);
-          mma16816(acc[r][nt], d[r][0].z, d[r][1].z, d[r][0].w, d[r][1].w, b.z, b.w);
-        }
-      }
-    }
-    if (++part == C::SPS) {
-      part = 0;
-      if (++slot == kFewStages) slot = 0;
-    }
-  }
-  cp_async_wait<0>();
-  __syncthreads();
-  // partial sums [m][n]
-  float* red = reinterpret_cast<float*>(smem);
-#pragma unroll
-  for (int r = 0; r < RG; ++r)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        red[(nt * 8 + 2 * t + (e & 1)) * C::PITCH + (warp * RG + r) * 16 + (e >> 1) * 8 + g] = acc[r][nt][e];
-  // U, and y's earlier readers, are an earlier kernel's business until here
-  pdl_wait();
-  pdl_launch_dependents();
-  if (CS > 1) cluster_sync();
-  else __syncthreads();
-  // this CTA finishes ROWS / CS of the columns, two per thread
-  const int per = C::ROWS / CS, half = per / 2;
-  for (int i = threadIdx.x; i < half * mrows; i += kFewWarps * 32) {
-    const int m = i / half, nl = rank * per + 2 * (i % half), n = n0 + nl;
-    if (n >= a.N) continue;
-    float v0 = 0.0f, v1 = 0.0f;
-    for (int c = 0; c < CS; ++c) {
-      float p0, p1;
-      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
-                   : "=f"(p0), "=f"(p1)
-                   : "r"(mapa_shared(smem_u32(&red[m * C::PITCH + nl]), (uint32_t)c))
-                   : "memory");
-      v0 += p0;
-      v1 += p1;
-    }
-    const int ad = a.row[m0 + m];
-    if (ad >= 0) {
-      const float s = a.scale[ad];
-      const float4* u = reinterpret_cast<const float4*>(a.P + (int64_t)(m0 + m) * kR);
-      float d0 = 0.0f, d1 = 0.0f;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float4 uu = u[q];
-        float b0[4], b1[4];
-        const int64_t o = ad * a.stride + (int64_t)n * kR + 4 * q;
-        if constexpr (F16) {
-          const uint2 x0 = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.F) + o));
-          const uint2 x1 = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.F) + o + kR));
-          b0[0] = bf16_lo(x0.x), b0[1] = bf16_hi(x0.x), b0[2] = bf16_lo(x0.y), b0[3] = bf16_hi(x0.y);
-          b1[0] = bf16_lo(x1.x), b1[1] = bf16_hi(x1.x), b1[2] = bf16_lo(x1.y), b1[3] = bf16_hi(x1.y);
-        } else {
-          const float4 x0 = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.F) + o));
-          const float4 x1 = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.F) + o + kR));
-          b0[0] = x0.x, b0[1] = x0.y, b0[2] = x0.z, b0[3] = x0.w;
-          b1[0] = x1.x, b1[1] = x1.y, b1[2] = x1.z, b1[3] = x1.w;
-        }
-        d0 = fmaf(uu.x, b0[0], d0), d0 = fmaf(uu.y, b0[1], d0), d0 = fmaf(uu.z, b0[2], d0), d0 = fmaf(uu.w, b0[3], d0);
-        d1 = fmaf(uu.x, b1[0], d1), d1 = fmaf(uu.y, b1[1], d1), d1 = fmaf(uu.z, b1[2], d1), d1 = fmaf(uu.w, b1[3], d1);
-      }
-      v0 = fmaf(s, d0, v0);
-      v1 = fmaf(s, d1, v1);
-    }
-    *reinterpret_cast<uint32_t*>(a.y + (int64_t)(m0 + m) * a.N + n) = pack_bf16x2(v0, v1);
-  }
-  if (CS > 1) cluster_sync();  // the sums stay until every CTA of the cluster has read them
-}
-
 // ------------------------------------------------------------------------ host side
+#ifndef WS_FEW_ROWS
+#define WS_FEW_ROWS 64
+#endif
+constexpr int kFewRows = WS_FEW_ROWS;  // rows up to which run_few makes the forward
+
 struct WsLayout {
-  size_t G, ext, bad, partial, total;
+  size_t G, ext, bad, partial, total;  // bad: words of the GEMM (1) or of run_few (kFewUnits)
 };
 WsLayout ws_layout(int64_t M, int64_t N, int64_t K) {
   WsLayout L{};
@@ -778,8 +575,10 @@ WsLayout ws_layout(int64_t M, int64_t N, int64_t K) {
   L.G = 0;
   L.ext = al256((size_t)M * kR * 4);
   L.bad = L.ext + (size_t)M * kMultiSlots * 128;
-  L.partial = L.bad + 256;
-  L.total = L.partial + al256(pf > pb ? pf : pb);
+  L.partial = L.bad + kFewUnits * 4;
+  size_t p = pf > pb ? pf : pb;
+  if (M <= kFewRows && p < kFewUnits * 64 * 128 * 4) p = kFewUnits * 64 * 128 * 4;
+  L.total = L.partial + al256(p);
   return L;
 }
 
@@ -822,8 +621,9 @@ cudaError_t run_skinny(bool f_cj, const uint16_t* X, const void* F, bool f16, in
   return launch_cluster(k, dim3((unsigned)cs, (unsigned)L.max_tiles), kSkWarps * 32, cs, 0, st, X, F, strideF,
                         (int)C, mask, (const int32_t*)plan.data, L.perm, L.tile, L.slot, out,
                         slots ? reinterpret_cast<uint32_t*>(ws + W.ext) : nullptr, plan.M,
-                        reinterpret_cast<uint32_t*>(ws + W.bad));
+                        reinterpret_cast<uint32_t*>(ws + W.bad), slots ? 1 : kFewUnits);
 }
+static_assert(kFewUnits <= kSkWarps * 32, "one thread zeroes each word");
 
 // The GEMM's view of the adapter term with P = U or G and F = B or A.
 MultiLora multi_of(const ws_lora_plan& plan, uint8_t* ws, const WsLayout& W, const float* P, const void* F, bool f16,
@@ -842,44 +642,6 @@ MultiLora multi_of(const ws_lora_plan& plan, uint8_t* ws, const WsLayout& W, con
   m.stride = stride;
   m.f16 = f16 ? 1 : 0;
   return m;
-}
-
-#ifndef WS_FEW_ROWS
-#define WS_FEW_ROWS 64
-#endif
-constexpr int kFewRows = WS_FEW_ROWS;  // rows up to which k_multi_few runs the forward
-template <int NT, int RG, bool F16>
-cudaError_t launch_few(const FewArgs& a, cudaStream_t st) {
-  using C = FewCfg<NT, RG>;
-  auto k = k_multi_few<NT, RG, F16>;
-  static const int resident = [&] {  // CTAs of the whole GPU at once
-    int per = 0;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, k, kFewWarps * 32, C::SMEM) != cudaSuccess)
-      return 0;
-    return per * device_sm_count();
-  }();
-  if (resident <= 0) return cudaErrorInvalidConfiguration;
-  const int blocks = (a.N + C::ROWS - 1) / C::ROWS, chunks = (a.M + C::MR - 1) / C::MR, steps = (a.K + 255) / 256;
-  // CTAs sharing a contraction: the fewest steps in a row, a wave of CTAs
-  // counting its longest CTA and about two steps to start and join
-  int cs = 1, best = 0x7fffffff;
-  for (int c = 1; c <= 8; c *= 2) {
-    const int waves = (blocks * chunks * c + resident - 1) / resident;
-    const int cost = waves * ((steps + c - 1) / c + 2);
-    if (cost < best) best = cost, cs = c;
-  }
-  return launch_cluster(k, dim3((unsigned)cs, (unsigned)blocks, (unsigned)chunks), kFewWarps * 32, cs, C::SMEM, st, a);
-}
-template <bool F16>
-cudaError_t run_few_t(const FewArgs& a, cudaStream_t st) {
-  if (a.M <= 8) return launch_few<1, 1, F16>(a, st);
-  if (a.M <= 16) return launch_few<2, 1, F16>(a, st);
-  if (a.M <= 32) return launch_few<4, 1, F16>(a, st);
-  return launch_few<8, 2, F16>(a, st);
-}
-cudaError_t run_few(const FewArgs& a, bool f16, cudaStream_t st) {
-  return f16 ? run_few_t<true>(a, st) : run_few_t<false>(a, st);
 }
 
 ws_status check_plan(const ws_lora_plan* p) {
@@ -990,6 +752,8 @@ ws_status ws_lora_linear_fwd_multi(const ws_nf4* W, const uint16_t* x, const ws_
     a.P = U_saved, a.F = set->B, a.stride = set->stride_b, a.scale = set->scale;
     a.row = static_cast<const int32_t*>(plan->data) + plan_layout(M, plan->n_adapters).row;
     a.y = y;
+    a.partial = reinterpret_cast<float*>(ws + L.partial);
+    a.flags = reinterpret_cast<uint32_t*>(ws + L.bad);
     WS_RUN(run_few(a, f16, st));
     return WS_OK;
   }

@@ -72,6 +72,10 @@ cudaError_t read_and_clear_dev_error(uint32_t* flags) {
   uint32_t attn = 0;
   e = attn_read_and_clear_dev_error(&attn);
   *flags |= attn;
+  if (e != cudaSuccess) return e;
+  uint32_t few = 0;
+  e = few_read_and_clear_dev_error(&few);
+  *flags |= few;
   return e;
 }
 
