@@ -237,7 +237,7 @@ struct FewArgs {
   uint16_t* y;
   float* partial;        // [kFewUnits][64][128] fp32 partial sums of cut tiles
   uint32_t* flags;       // [kFewUnits], zeroed by the kernel before this one
-  int blocks, chunks, steps;  // set by run_few
+  int blocks, chunks, steps, base, extra;  // set by run_few
 };
 cudaError_t few_read_and_clear_dev_error(uint32_t* flags);
 cudaError_t run_few(const FewArgs& a, bool f16, cudaStream_t st);

@@ -5,7 +5,7 @@
 // pipe of 64 lanes an SM), then by reading them.  The dequant GEMM's tile has
 // the activation rows as the 128-row operand and hands over 64-deep steps; with
 // few rows its time is that handshake.  Here the WEIGHT rows are the 128-row
-// operand and the rows of x the N-wide one (16, 32 or 64), and a step is 256
+// operand and the rows of x the N-wide one (32 or 64), and a step is 256
 // deep: sixteen warps decode 128 x 256 weights, each thread one 64-weight block
 // (one value table for 64 weights), straight into the 128-byte swizzled operand
 // layout, then hand over once; one thread loads x by TMA and issues the
@@ -49,8 +49,9 @@ struct Cfg {
   static constexpr uint32_t OFF_A = 0, OFF_X = 2 * kABytes, OFF_BAR = OFF_X + XS * X_BYTES;
   static constexpr uint32_t SMEM = OFF_BAR + 192 + 1024;  // + alignment slack
   static_assert(SMEM <= 227u * 1024u, "shared memory");
-  static constexpr uint32_t TMEM_COLS = NX < 32 ? 32 : NX;
+  static constexpr uint32_t TMEM_COLS = NX;
   static constexpr int CPW = NX / 4;             // accumulator columns (rows of x) of one epilogue warp
+  static_assert(NX == 32 || NX == 64, "rows of x");
 };
 
 // True in one lane of a converged warp.
@@ -83,11 +84,60 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   volatile uint32_t* got_flag = misc + 2;
   // (the shuffle tells the compiler that a warp's index is one value)
   const int warp = __shfl_sync(0xffffffffu, (int)warp_id(), 0), lane = (int)lane_id();
-  const int T = a.blocks * a.chunks, S = a.steps;
-  const int64_t I = (int64_t)T * S, U = gridDim.x, u = blockIdx.x;
-  const int64_t pb = u * I / U, pe = (u + 1) * I / U;
+  // this CTA's range: base iterations, one more for the first `extra` CTAs
+  const int S = a.steps, u = (int)blockIdx.x;
+  const int pb = u * a.base + min(u, a.extra), n_all = a.base + (u < a.extra ? 1 : 0);
+  const int tile0 = (int)((uint32_t)pb / (uint32_t)S), step0 = pb - tile0 * S;
+
+  // Codes of the thread's weight row r and 64-weight block t (four lanes read
+  // a 128-byte line), two steps in registers and two more on their way to L2;
+  // the first are asked for before anything is set up.
+  const int r = (int)threadIdx.x >> 2, t = (int)threadIdx.x & 3;
+  struct Codes {
+    uint2 w[4];
+    float s;
+  };
+  const int64_t kb = a.K / 2;
+  int lt = tile0, ls = step0, left = warp < kDecWarps ? n_all : 0;  // next step to load
+  const uint8_t* cp = a.codes;
+  const float* sp = a.absmax;
+  auto seek = [&]() {
+    // rows past the last repeat it: their sums are not stored
+    const int n = min(lt % a.blocks * kRows + r, a.N - 1);
+    cp = a.codes + n * kb + (int64_t)ls * 128 + t * 32;
+    sp = a.absmax + ((int64_t)ls * 4 + t) * a.N + n;
+  };
+  auto load = [&](Codes& f) {
+    if (left <= 0) return;
+    // the last step may end inside its four blocks: blocks past the end take
+    // codes that exist and a scale of 0
+    const bool in = ls * 256 + t * 64 < a.K;
+    const uint2* c = reinterpret_cast<const uint2*>(in ? cp : a.codes);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f.w[i] = __ldg(c + ((i + t) & 3));
+    f.s = in ? __ldg(sp) : 0.0f;
+    if (left > 2 && ls + 2 < S && (ls + 2) * 256 + t * 64 < a.K) {
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(cp + 256));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(sp + (int64_t)8 * a.N));
+    }
+    --left;
+    if (++ls == S) {
+      ls = 0;
+      ++lt;
+      seek();
+    } else {
+      cp += 128;
+      sp += (int64_t)4 * a.N;
+    }
+  };
+  Codes f0{}, f1{};
+  if (warp < kDecWarps) {
+    seek();
+    load(f0);
+    load(f1);
+  }
+  if (threadIdx.x == 32) *abort_flag = *(volatile uint32_t*)&g_dev_error;  // an earlier kernel gave up: do nothing
   if (threadIdx.x == 0) {
-    *abort_flag = *(volatile uint32_t*)&g_dev_error;  // an earlier kernel gave up: do nothing
     for (int s = 0; s < 2; ++s) {
       mbar_init(&full[s], kDecWarps);
       mbar_init(&empty[s], 1);
@@ -109,7 +159,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   tc_fence_after();
   const uint32_t tmem = misc[0];
   const bool skip = *abort_flag != 0u;
-  const int n_it = skip ? 0 : (int)(pe - pb);
+  const int n_it = skip ? 0 : n_all;
 
   if (warp == kDecWarps) {
     // ------------------------------------------------------------ the products
@@ -120,7 +170,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     constexpr uint32_t idesc = idesc_bf16_f32(kRows, NX, 0u);
     const uint64_t ad0 = smem_desc_sw128(smem_u32(smem + C::OFF_A), 16, 1024);
     const uint64_t bd0 = smem_desc_sw128(smem_u32(smem + C::OFF_X), 16, 1024);
-    int step = (int)(pb % S), xs = 0;
+    int step = step0, xs = 0;
     uint32_t pieces = 0, xph = 0;
     bool first = true;  // of its piece
     for (int q = 0; q < n_it; ++q) {
@@ -172,7 +222,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     // ------------------------------------------------------------ x
     if (lane == 0) {
       tma_prefetch_desc(&tmX);
-      int tile = (int)(pb / S), step = (int)(pb % S), xs = 0;
+      int tile = tile0, step = step0, xs = 0;
       uint32_t ph = 1;
       for (int q = 0; q < n_it; ++q) {
         if (*abort_flag || !mbar_wait(&xempty[xs], ph, DERR_TIMEOUT_EMPTY)) {
@@ -203,48 +253,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     pdl_launch_dependents();
   } else {
     // ------------------------------------------------------------ decode and epilogue
-    // Thread = weight row r of the tile, 64-weight block t of the step (four
-    // lanes read a 128-byte line of codes).  It takes its eight 8-weight words
-    // from word 2t on, so that the eight lanes of a quarter warp (two rows,
-    // four blocks) store to eight different 16-byte places of the swizzle.
-    const int r = (int)threadIdx.x >> 2, t = (int)threadIdx.x & 3;
+    // A thread takes its eight 8-weight words from word 2t on, so that the
+    // eight lanes of a quarter warp (two rows, four blocks) store to eight
+    // different 16-byte places of the swizzle.
     uint32_t dst[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       dst[i] = smem_u32(smem + C::OFF_A) + (uint32_t)(t * 16384 + r * 128 + ((((i + 2 * t) & 7) ^ (r & 7)) << 4));
-    struct Codes {
-      uint2 w[4];
-      float s;
-    };
-    const int64_t kb = a.K / 2;
-    int lt = (int)(pb / S), ls = (int)(pb % S), left = n_it;  // next step to load
-    const uint8_t* cp = nullptr;
-    const float* sp = nullptr;
-    auto seek = [&]() {
-      // rows past the last repeat it: their sums are not stored
-      const int n = min(lt % a.blocks * kRows + r, a.N - 1);
-      cp = a.codes + n * kb + (int64_t)ls * 128 + t * 32;
-      sp = a.absmax + ((int64_t)ls * 4 + t) * a.N + n;
-    };
-    auto load = [&](Codes& f) {
-      if (left <= 0) return;
-      // the last step may end inside its four blocks: blocks past the end take
-      // codes that exist and a scale of 0
-      const bool in = ls * 256 + t * 64 < a.K;
-      const uint2* c = reinterpret_cast<const uint2*>(in ? cp : a.codes);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f.w[i] = __ldg(c + ((i + t) & 3));
-      f.s = in ? __ldg(sp) : 0.0f;
-      --left;
-      if (++ls == S) {
-        ls = 0;
-        ++lt;
-        seek();
-      } else {
-        cp += 128;
-        sp += (int64_t)4 * a.N;
-      }
-    };
     auto decode = [&](const Codes& f, int s) {
       const Nf4Table tb = make_table(f.s);
 #pragma unroll
@@ -263,7 +278,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     // The piece that ends with iteration q: tile `tile`, whether it holds the
     // tile's first and its last step.
     auto epilogue = [&](int tile, bool head, bool tail) {
-      const bool ok = !*abort_flag && mbar_wait_backoff(acc_done, piece & 1u, DERR_TIMEOUT_ACC);
+      const bool ok = !*abort_flag && mbar_wait(acc_done, piece & 1u, DERR_TIMEOUT_ACC);
       ++piece;
       if (!ok) *abort_flag = 1u;
       tc_fence_after();
@@ -275,15 +290,17 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       const int q4 = warp & 3, c0 = warp / 4 * C::CPW;  // lanes (weight rows) and columns of this warp
       const int nl = q4 * 32 + lane, n = tile % a.blocks * kRows + nl;
       const int m0 = tile / a.blocks * NX + c0;
-      int64_t last = u;  // CTA that holds the tile's last step
+      int last = u;  // CTA that holds the tile's last step
       if (head && !tail) {
-        last = ((int64_t)(tile + 1) * S * U - 1) / I;
-        if (threadIdx.x == 0) {
+        const int i = (tile + 1) * S - 1, cut = a.extra * (a.base + 1);
+        last = i < cut ? i / (a.base + 1) : a.extra + (i - cut) / a.base;
+        if (warp == 0) {  // a lane polls every 32nd flag
           bool got = ok;
-          for (int64_t v = u + 1; v <= last && got; ++v) {
+          for (int v = u + 1 + lane; v <= last && got; v += 32)
             got = wait_flag_bounded(a.flags + v, 1u, kWaitLimitNs, DERR_TIMEOUT_PEER);
-          }
-          *got_flag = got ? 1u : 0u;
+          got = __all_sync(0xffffffffu, got);
+          __threadfence();
+          if (lane == 0) *got_flag = got ? 1u : 0u;
         }
         named_bar_sync(1, kDecThreads);
         if (*got_flag == 0u) last = u;
@@ -302,17 +319,17 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(raw[e]);
         if (!head) {  // a later piece of its tile: hand it over
-          float* p = a.partial + (u * NX + c0 + cc) * kRows + nl;
+          float* p = a.partial + (int64_t)(u * NX + c0 + cc) * kRows + nl;
 #pragma unroll
           for (int e = 0; e < 4; ++e) __stcg(p + e * kRows, v[e]);
           continue;
         }
         // later pieces in step order, four at a time in flight
-        for (int64_t w = u + 1; w <= last; w += 4) {
+        for (int w = u + 1; w <= last; w += 4) {
           float x[4][4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float* p = a.partial + ((w + i) * NX + c0 + cc) * kRows + nl;
+            const float* p = a.partial + (int64_t)((w + i) * NX + c0 + cc) * kRows + nl;
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[i][e] = w + i <= last ? __ldcg(p + e * kRows) : 0.0f;
           }
@@ -321,32 +338,35 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] += x[i][e];
         }
+        int ad[4];
+        float d[4] = {};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ad[e] = m0 + cc + e < a.M && n < a.N ? a.row[m0 + cc + e] : -1;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int m = m0 + cc + e;
-          if (!ok || m >= a.M || n >= a.N) continue;
-          const int ad = a.row[m];
-          if (ad >= 0) {
-            const float4* up = reinterpret_cast<const float4*>(a.P + (int64_t)m * 16);
-            float d = 0.0f;
+          if (ad[e] < 0) continue;
+          const float4* up = reinterpret_cast<const float4*>(a.P + (int64_t)(m0 + cc + e) * 16);
+          const int64_t o = ad[e] * a.stride + (int64_t)n * 16;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float4 uu = up[j];
-              float b[4];
-              const int64_t o = ad * a.stride + (int64_t)n * 16 + 4 * j;
-              if constexpr (F16) {
-                const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.F) + o);
-                b[0] = bf16_lo(x.x), b[1] = bf16_hi(x.x), b[2] = bf16_lo(x.y), b[3] = bf16_hi(x.y);
-              } else {
-                const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.F) + o);
-                b[0] = x.x, b[1] = x.y, b[2] = x.z, b[3] = x.w;
-              }
-              d = fmaf(uu.x, b[0], d), d = fmaf(uu.y, b[1], d), d = fmaf(uu.z, b[2], d), d = fmaf(uu.w, b[3], d);
+          for (int j = 0; j < 4; ++j) {
+            const float4 x = up[j];
+            float b[4];
+            if constexpr (F16) {
+              const uint2 f = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.F) + o)[j];
+              b[0] = bf16_lo(f.x), b[1] = bf16_hi(f.x), b[2] = bf16_lo(f.y), b[3] = bf16_hi(f.y);
+            } else {
+              const float4 f = reinterpret_cast<const float4*>(static_cast<const float*>(a.F) + o)[j];
+              b[0] = f.x, b[1] = f.y, b[2] = f.z, b[3] = f.w;
             }
-            v[e] = fmaf(a.scale[ad], d, v[e]);
+            d[e] = fmaf(x.x, b[0], d[e]), d[e] = fmaf(x.y, b[1], d[e]);
+            d[e] = fmaf(x.z, b[2], d[e]), d[e] = fmaf(x.w, b[3], d[e]);
           }
-          a.y[(int64_t)m * a.N + n] = f32_to_bf16_bits(v[e]);
+          d[e] *= a.scale[ad[e]];
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (ok && m0 + cc + e < a.M && n < a.N)
+            a.y[(int64_t)(m0 + cc + e) * a.N + n] = f32_to_bf16_bits(ad[e] >= 0 ? v[e] + d[e] : v[e]);
       }
       if (!head) {
         // every thread's stores, then the flag
@@ -356,12 +376,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
     };
 
-    int tile = lt, step = ls;
-    bool head = ls == 0;  // of the piece being made
-    Codes f0{}, f1{};
-    seek();
-    load(f0);
-    load(f1);
+    int tile = tile0, step = step0;
+    bool head = step0 == 0;  // of the piece being made
     // After a wait has given up, every warp still runs all its iterations,
     // without waiting: the epilogue's barriers count on all of them.
     auto iter = [&](int q, Codes& f, int s) {
@@ -392,6 +408,255 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   if (warp == kDecWarps) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
+
+// ------------------------------------------------------------------------ up to 16 rows, or a small weight
+// The same product with mma.sync: a warp decodes 16 weight rows in registers,
+// as the 16-row operand, and the rows of x are its 8-wide operand, so no decoded
+// weight passes through shared memory and nothing is handed over.  A lane holds
+// one 64-weight block of two weight rows per 256-deep step, so four lanes read
+// a whole 128-byte line of codes; x is staged in shared memory in that order of
+// k.  CTA = 128 weight rows; a cluster of CTAs shares their contraction and adds
+// its partial sums in rank order through distributed shared memory.  Bound by
+// the integer pipe too, with three CTAs an SM.
+constexpr int kMmaWarps = 8;
+constexpr int kMmaStages = 3;   // stages of x in flight
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), bf16; operand layout as in
+// lora_multi.cu.
+WS_DEVINL void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <int NT>
+struct MmaCfg {
+  static constexpr int ROWS = kMmaWarps * 16;
+  static constexpr int MR = NT * 8;
+  static constexpr int SPS = NT <= 2 ? 2 : 1;      // 256-deep steps per stage of x
+  static constexpr int STAGE = MR * 512 * SPS;     // bytes
+  static constexpr int CTAS = NT <= 2 ? 3 : 2;  // CTAs of an SM that the registers allow
+  static constexpr int PITCH = ROWS + 4;           // floats; [MR][PITCH] partial sums
+  static constexpr int SMEM = kMmaStages * STAGE > MR * PITCH * 4 ? kMmaStages * STAGE : MR * PITCH * 4;
+};
+
+template <int NT, bool F16>
+__global__ void __launch_bounds__(kMmaWarps * 32, MmaCfg<NT>::CTAS) k_few_mma(const FewArgs a) {
+  using C = MmaCfg<NT>;
+  constexpr int RG = 1;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int lane = (int)lane_id(), warp = (int)warp_id(), g = lane >> 2, t = lane & 3;
+  const int CS = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
+  const int m0 = (int)blockIdx.z * C::MR, mrows = min(C::MR, a.M - m0);
+  const int n0 = (int)blockIdx.y * C::ROWS;
+  // this warp's first weight row (a warp past the last row repeats the last
+  // ones: its sums are not used)
+  const int nw = min(n0 + warp * 16 * RG, a.N - 16 * RG);
+  const int steps = (a.K + 255) / 256;
+  const int s_beg = (int)((int64_t)rank * steps / CS), s_end = (int)((int64_t)(rank + 1) * steps / CS);
+
+  // x of one stage: 16-byte chunk c (k = 8c ..) of row m of a 256-deep step at
+  // chunk place (c % 8) * 4 + c / 8, odd rows with the 64-byte halves of each
+  // 128 bytes swapped, so that the eight lanes of a quarter warp read eight
+  // different bank groups.  A thread copies chunk xc of rows xm, xm + XM, ...
+  constexpr int XC = 32 * C::SPS, XM = kMmaWarps * 32 / XC, XQ = C::MR / XM;
+  static_assert(XQ >= 1 && C::MR % XM == 0, "every thread has a row");
+  const int xc = threadIdx.x % XC, xm = threadIdx.x / XC;
+  const uint16_t* xsrc = a.x + (int64_t)(m0 + xm) * a.K + (int64_t)s_beg * 256 + xc * 8;
+  const uint32_t xdst = smem_u32(smem) + (uint32_t)((xc / 32) * C::MR * 512 + xm * 512 +
+                                                    ((((xc & 7) * 4 + ((xc & 31) >> 3)) * 16) ^ ((xm & 1) * 64)));
+  static_assert(XM % 2 == 0, "a thread's rows have one parity");
+  int xk = s_beg * 256 + xc * 8;  // first element of the chunk
+  const int xk_end = min(a.K, s_end * 256);
+  auto stage_x = [&](int slot) {
+    if (xk - xc * 8 < xk_end) {
+#pragma unroll
+      for (int q = 0; q < XQ; ++q) {
+        const bool in = xm + q * XM < mrows && xk < xk_end;
+        cp_async16(xdst + (uint32_t)(slot * C::STAGE + q * XM * 512), in ? xsrc + (int64_t)q * XM * a.K : a.x, in ? 16u : 0u);
+      }
+      xsrc += 256 * C::SPS;
+      xk += 256 * C::SPS;
+    }
+    cp_async_commit();
+  };
+  // codes and scales of the step to come, reloaded as they are used
+  uint4 cw[RG][2][2];
+  float cs[RG][2];
+  const int64_t kb = a.K / 2;
+  const uint8_t* cp = a.codes + (int64_t)(nw + g) * kb + (int64_t)s_beg * 128 + t * 32;
+  const float* sp = a.absmax + ((int64_t)s_beg * 4 + t) * a.N + nw + g;
+  // the last step may end inside its four blocks: lanes past the end read
+  // codes that exist and a scale of 0
+  int k_lane = s_beg * 256 + t * 64;
+  auto load_w = [&](int q) {
+    const uint8_t* p = k_lane < a.K ? cp : a.codes;
+#pragma unroll
+    for (int r = 0; r < RG; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        cw[r][h][q] = __ldg(reinterpret_cast<const uint4*>(p + (int64_t)(r * 16 + h * 8) * kb) + q);
+  };
+  auto load_s = [&]() {
+#pragma unroll
+    for (int r = 0; r < RG; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) cs[r][h] = k_lane < a.K ? __ldg(sp + r * 16 + h * 8) : 0.0f;
+  };
+#pragma unroll
+  for (int i = 0; i < kMmaStages - 1; ++i) stage_x(i);
+  if (s_beg < s_end) {
+    load_s();
+    load_w(0);
+    load_w(1);
+  }
+  float acc[RG][NT][4] = {};
+  int slot = 0, part = 0;  // stage of x and step within it
+  for (int s = s_beg; s < s_end; ++s) {
+    if (part == 0) {
+      cp_async_wait<kMmaStages - 2>();
+      __syncthreads();  // this stage of x has landed; everyone is done with the one before
+      stage_x(slot == 0 ? kMmaStages - 1 : slot - 1);
+    }
+    Nf4Table tb[RG][2];
+#pragma unroll
+    for (int r = 0; r < RG; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) tb[r][h] = make_table(cs[r][h]);
+    const bool more = s + 1 < s_end;
+    const int k_now = k_lane;
+    cp += 128;
+    sp += (int64_t)4 * a.N;
+    k_lane = k_now + 256;
+    if (more) load_s();
+    const uint8_t* xs = smem + slot * C::STAGE + part * C::MR * 512 + g * 512 + t * 16;
+    const uint32_t flip = (uint32_t)(g & 1) * 64;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      uint4 d[RG][2];
+#pragma unroll
+      for (int r = 0; r < RG; ++r)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 q = cw[r][h][w / 4];
+          const uint32_t c = (w & 3) == 0 ? q.x : (w & 3) == 1 ? q.y : (w & 3) == 2 ? q.z : q.w;
+          d[r][h] = dq8(c, tb[r][h]);
+        }
+      if ((w & 3) == 3 && more) load_w(w / 4);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint4 b = *reinterpret_cast<const uint4*>(xs + nt * 4096 + ((w * 64) ^ flip));
+#pragma unroll
+        for (int r = 0; r < RG; ++r) {
+          mma16816(acc[r][nt], d[r][0].x, d[r][1].x, d[r][0].y, d[r][1].y, b.x, b.y);
+          mma16816(acc[r][nt], d[r][0].z, d[r][1].z, d[r][0].w, d[r][1].w, b.z, b.w);
+        }
+      }
+    }
+    if (++part == C::SPS) {
+      part = 0;
+      if (++slot == kMmaStages) slot = 0;
+    }
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+  // partial sums [m][n]
+  float* red = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int r = 0; r < RG; ++r)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        red[(nt * 8 + 2 * t + (e & 1)) * C::PITCH + (warp * RG + r) * 16 + (e >> 1) * 8 + g] = acc[r][nt][e];
+  // U, and y's earlier readers, are an earlier kernel's business until here
+  pdl_wait();
+  pdl_launch_dependents();
+  if (CS > 1) cluster_sync();
+  else __syncthreads();
+  // the cluster's threads share the results out, two columns each at a time
+  for (int i = rank * kMmaWarps * 32 + (int)threadIdx.x; i < C::ROWS / 2 * mrows; i += CS * kMmaWarps * 32) {
+    const int m = i / (C::ROWS / 2), nl = 2 * (i % (C::ROWS / 2)), n = n0 + nl;
+    if (n >= a.N) continue;
+    float v0 = 0.0f, v1 = 0.0f;
+    for (int c = 0; c < CS; ++c) {
+      float p0, p1;
+      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                   : "=f"(p0), "=f"(p1)
+                   : "r"(mapa_shared(smem_u32(&red[m * C::PITCH + nl]), (uint32_t)c))
+                   : "memory");
+      v0 += p0;
+      v1 += p1;
+    }
+    const int ad = a.row[m0 + m];
+    if (ad >= 0) {
+      const float s = a.scale[ad];
+      const float4* u = reinterpret_cast<const float4*>(a.P + (int64_t)(m0 + m) * 16);
+      float d0 = 0.0f, d1 = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 uu = u[q];
+        float b0[4], b1[4];
+        const int64_t o = ad * a.stride + (int64_t)n * 16 + 4 * q;
+        if constexpr (F16) {
+          const uint2 x0 = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.F) + o));
+          const uint2 x1 = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.F) + o + 16));
+          b0[0] = bf16_lo(x0.x), b0[1] = bf16_hi(x0.x), b0[2] = bf16_lo(x0.y), b0[3] = bf16_hi(x0.y);
+          b1[0] = bf16_lo(x1.x), b1[1] = bf16_hi(x1.x), b1[2] = bf16_lo(x1.y), b1[3] = bf16_hi(x1.y);
+        } else {
+          const float4 x0 = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.F) + o));
+          const float4 x1 = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.F) + o + 16));
+          b0[0] = x0.x, b0[1] = x0.y, b0[2] = x0.z, b0[3] = x0.w;
+          b1[0] = x1.x, b1[1] = x1.y, b1[2] = x1.z, b1[3] = x1.w;
+        }
+        d0 = fmaf(uu.x, b0[0], d0), d0 = fmaf(uu.y, b0[1], d0), d0 = fmaf(uu.z, b0[2], d0), d0 = fmaf(uu.w, b0[3], d0);
+        d1 = fmaf(uu.x, b1[0], d1), d1 = fmaf(uu.y, b1[1], d1), d1 = fmaf(uu.z, b1[2], d1), d1 = fmaf(uu.w, b1[3], d1);
+      }
+      v0 = fmaf(s, d0, v0);
+      v1 = fmaf(s, d1, v1);
+    }
+    *reinterpret_cast<uint32_t*>(a.y + (int64_t)(m0 + m) * a.N + n) = pack_bf16x2(v0, v1);
+  }
+  if (CS > 1) cluster_sync();  // the sums stay until every CTA of the cluster has read them
+}
+
+template <int NT, bool F16>
+cudaError_t launch_mma(const FewArgs& a, cudaStream_t st) {
+  using C = MmaCfg<NT>;
+  auto k = k_few_mma<NT, F16>;
+  static const cudaError_t attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  if (attr != cudaSuccess) return attr;
+  const int blocks = (a.N + C::ROWS - 1) / C::ROWS, chunks = (a.M + C::MR - 1) / C::MR, steps = (a.K + 255) / 256;
+  // CTAs sharing a contraction: the shortest time of the busiest SM, in tenths
+  // of a step's decoding.  One or two CTAs leave part of the SM idle (k steps
+  // side by side take 2.2, 2.8 and 3, 4, ... steps' time), and a CTA counts
+  // about a step to start and join.
+  int cs = 1;
+  int64_t best = INT64_MAX;
+  for (int c = 1; c <= 8; ++c) {
+    const int64_t per_sm = ((int64_t)blocks * chunks * c + device_sm_count() - 1) / device_sm_count();
+    const int64_t cost = (per_sm == 1 ? 22 : per_sm == 2 ? 28 : 10 * per_sm) * ((steps + c - 1) / c + 1);
+    if (cost <= best) best = cost, cs = c;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)cs, (unsigned)blocks, (unsigned)chunks);
+  cfg.blockDim = dim3(kMmaWarps * 32);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeClusterDimension;
+  attrs[0].val.clusterDim.x = (unsigned)cs;
+  attrs[0].val.clusterDim.y = 1;
+  attrs[0].val.clusterDim.z = 1;
+  attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, k, a);
+}
+
 template <int NX, bool F16>
 cudaError_t launch(FewArgs a, cudaStream_t st) {
   using C = Cfg<NX>;
@@ -406,16 +671,32 @@ cudaError_t launch(FewArgs a, cudaStream_t st) {
   const int64_t iters = (int64_t)a.blocks * a.chunks * a.steps;
   int64_t grid = device_sm_count() < kFewUnits ? device_sm_count() : kFewUnits;
   if (grid > iters) grid = iters;
+  if (iters >= (1ll << 31)) return cudaErrorInvalidValue;
+  a.base = (int)(iters / grid);
+  a.extra = (int)(iters % grid);
   note_launch();
   return launch_pdl(k_few<NX, F16>, dim3((unsigned)grid), dim3(kFewThreads), C::SMEM, st, tm, a);
 }
 
 }  // namespace
 
+namespace {
+template <bool F16>
+cudaError_t run_few_t(const FewArgs& a, cudaStream_t st) {
+  if (a.M <= 8) return launch_mma<1, F16>(a, st);
+  if (a.M <= 16) return launch_mma<2, F16>(a, st);
+  // With more rows mma.sync's own rate and its reads of x bind: k_few is ahead
+  // once it has several steps for every SM to make good its joins (32 rows,
+  // k_few / k_few_mma: 896x896 13 / 7 us, 5120x5120 25 / 25 us, 5120x27648 57 /
+  // 89 us; 64 rows: 17 / 9, 30 / 37, 63 / 156 us).
+  const int64_t steps = (int64_t)((a.N + 127) / 128) * ((a.K + 255) / 256);
+  if (steps >= (a.M <= 32 ? 6 : 4) * device_sm_count()) return a.M <= 32 ? launch<32, F16>(a, st) : launch<64, F16>(a, st);
+  return a.M <= 32 ? launch_mma<4, F16>(a, st) : launch_mma<8, F16>(a, st);
+}
+}  // namespace
+
 cudaError_t run_few(const FewArgs& a, bool f16, cudaStream_t st) {
-  if (a.M <= 16) return f16 ? launch<16, true>(a, st) : launch<16, false>(a, st);
-  if (a.M <= 32) return f16 ? launch<32, true>(a, st) : launch<32, false>(a, st);
-  return f16 ? launch<64, true>(a, st) : launch<64, false>(a, st);
+  return f16 ? run_few_t<true>(a, st) : run_few_t<false>(a, st);
 }
 
 }  // namespace ws

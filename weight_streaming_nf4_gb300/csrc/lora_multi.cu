@@ -743,9 +743,7 @@ ws_status ws_lora_linear_fwd_multi(const ws_nf4* W, const uint16_t* x, const ws_
   cudaStream_t st = (cudaStream_t)stream;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const bool f16 = set->dtype == WS_DTYPE_BF16;
-  const bool few = M <= kFewRows;
-  WS_RUN(run_skinny(false, x, set->A, f16, set->stride_a, K, mask, *plan, U_saved, ws, L, !few, st));
-  if (few) {
+  if (M <= kFewRows) {
     FewArgs a{};
     a.codes = W->codes, a.absmax = W->absmax, a.x = x;
     a.M = (int)M, a.N = (int)N, a.K = (int)K;
@@ -754,9 +752,11 @@ ws_status ws_lora_linear_fwd_multi(const ws_nf4* W, const uint16_t* x, const ws_
     a.y = y;
     a.partial = reinterpret_cast<float*>(ws + L.partial);
     a.flags = reinterpret_cast<uint32_t*>(ws + L.bad);
+    WS_RUN(run_skinny(false, x, set->A, f16, set->stride_a, K, mask, *plan, U_saved, ws, L, false, st));
     WS_RUN(run_few(a, f16, st));
     return WS_OK;
   }
+  WS_RUN(run_skinny(false, x, set->A, f16, set->stride_a, K, mask, *plan, U_saved, ws, L, true, st));
   const MultiLora ml = multi_of(*plan, ws, L, U_saved, set->B, f16, set->stride_b, set->scale);
   WS_RUN(run_nf4_gemm_multi(plan_gemm(false, M, N, K), view(W), x, M, ml, nullptr, y, 0, 0,
                             reinterpret_cast<float*>(ws + L.partial), st));
