@@ -65,20 +65,21 @@ struct GemmArgs {
   // ml_tile_ad[mt * kMultiSlots ..] (-1: none); each tile then runs L LoRA
   // steps, step l with the rows of its l-th adapter (the lora map's rows l*M +
   // m hold row m's split factor, or zeros).  L < 0: too many adapters; the
-  // epilogue adds the term.
+  // base term alone goes to ml_out32 [M, Nout], in fp32.
   const float* ml_P;       // U or G [M, 16]
   const void* ml_F;
   const float* ml_scale;   // [adapters]
   const int32_t* ml_row;   // [M]
   const int32_t* ml_slots;
   const int32_t* ml_tile_ad;
+  float* ml_out32;
   uint32_t* ml_bad;        // set when an F value is left to the epilogue (see lora_tile_ml)
   int64_t ml_stride;
   int ml_f16;              // ml_F is bf16
 };
 
 // The adapter term of run_nf4_gemm_multi (see GemmArgs::ml_*).
-constexpr int kMultiSlots = 16;  // adapters of one tile row that get a tensor-core step each
+constexpr int kMultiSlots = 8;  // adapters of one tile row that get a tensor-core step each
 struct MultiLora {
   const float* P;
   const uint16_t* ext;  // [kMultiSlots][M][64] bf16 split factor by slot
@@ -88,6 +89,7 @@ struct MultiLora {
   const int32_t* slots;
   const int32_t* tile_ad;
   uint32_t* bad;
+  float* out32;  // the base term where a tile row has more adapters
   int64_t stride;
   int f16;
 };
@@ -103,6 +105,7 @@ struct GemmPlan {
   // epad of which carry no work: a unit whose range ends more tiles (one
   // accumulator drain each) gets fewer contraction steps.
   int epad;
+  int64_t units = 0;  // units of the grid, where not grid_units' own choice
 };
 
 int device_sm_count();

@@ -419,12 +419,17 @@ __global__ void __launch_bounds__(kSkWarps * 32)
 // CTA = 128 columns of dY or x for one adapter: four warps take the adapter's
 // rows in turn, 16 at a time, for each 64 columns, D (16 x 64) += P^T Q, and
 // their sums are added in warp order.  Q is bf16 and exact, the fp32 P enters
-// as three bf16 parts.  A lane reads 8 consecutive columns of four rows (16
-// bytes each, 128 bytes of a row per eight lanes) one step ahead and pairs rows
-// with byte permutes: column 8g + i of the tile is column g of the i-th 8-wide
-// product, so nothing is transposed through shared memory.  Bound by reading
-// dY and x once.
-constexpr int kWgWarps = 8, kWgSplit = 4;
+// as three bf16 parts.  A lane takes 8 consecutive columns of four rows and
+// pairs rows with byte permutes: column 8g + i of the tile is column g of the
+// i-th 8-wide product, so nothing is transposed.  Bound by reading dY and x
+// once; each warp keeps kWgStages steps of rows on their way through a ring of
+// its own in shared memory (with one step ahead in registers the pass over
+// 2048 rows of 5120 + 27648 columns took 70 us).
+constexpr int kWgWarps = 8, kWgSplit = 4, kWgStages = 4;
+constexpr int kWgQ = 16 * 128, kWgP = 16 * 80, kWgM = 16 * 8;  // bytes of a step: Q, P (rows padded), mask
+constexpr int kWgStage = kWgQ + kWgP + kWgM;
+constexpr int kWgSmem = kWgWarps * kWgStages * kWgStage;
+static_assert(kWgSmem >= kWgWarps * kR * 64 * 4, "the sums fit the ring");
 struct WgArgs {
   const float* P[2];      // U, G  [M, 16]
   const uint16_t* Q[2];   // dY [M, C0], x [M, C1]
@@ -441,7 +446,8 @@ WS_DEVINL uint32_t lo_pair(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x
 WS_DEVINL uint32_t hi_pair(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
 
 __global__ void __launch_bounds__(kWgWarps * 32, 2) k_multi_wgrad(const WgArgs w) {
-  __shared__ float red[kWgWarps][kR][64];
+  extern __shared__ __align__(128) uint8_t wg_smem[];
+  float(*red)[kR][64] = reinterpret_cast<float(*)[kR][64]>(wg_smem);
   const int lane = (int)lane_id(), warp = (int)warp_id(), g = lane >> 2, t = lane & 3;
   pdl_wait();
   pdl_launch_dependents();
@@ -455,61 +461,76 @@ __global__ void __launch_bounds__(kWgWarps * 32, 2) k_multi_wgrad(const WgArgs w
   const int col0 = cta0 + (warp / kWgSplit) * 64, part = warp % kWgSplit;
   const bool cols = col0 < C;
   const float* P = which ? w.P[1] : w.P[0];
-  const uint16_t* Q = (which ? w.Q[1] : w.Q[0]) + col0 + 8 * g;
+  const uint16_t* Q = (which ? w.Q[1] : w.Q[0]) + col0;
   const uint32_t* mask = which ? w.mask : nullptr;
   const int32_t* rows = w.plan + w.o_perm + r_beg;
-  struct Step {
-    uint4 q[4];      // rows 2t, 2t+1, 2t+8, 2t+9 of the step; 8 columns
-    float p[4][2];   // P of those rows at j = g, g + 8
-    uint32_t keep[4];
-  };
-  // rows of a step (-1: none), two steps ahead of their use
-  int idx[4];
-  auto load_idx = [&](int s0) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = s0 + 2 * t + (i & 1) + (i >> 1) * 8;
-      idx[i] = r < cnt ? rows[r] : -1;
-    }
-  };
-  auto load = [&](Step& f) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f.q[i] = make_uint4(0u, 0u, 0u, 0u);
-      f.p[i][0] = f.p[i][1] = 0.0f;
-      f.keep[i] = 0xffu;
-      if (idx[i] >= 0) {
-        const int64_t row = idx[i];
-        f.q[i] = *reinterpret_cast<const uint4*>(Q + row * C);
-        if (mask) f.keep[i] = mask[(row * C + col0) / 32 + g / 4] >> (8 * (g & 3));
-        f.p[i][0] = P[row * kR + g];
-        f.p[i][1] = P[row * kR + g + 8];
-      }
-    }
-  };
   float d[8][4] = {};
   if (cols) {
-    Step f;
-    int s0 = part * 16;
-    load_idx(s0);
-    load(f);
-    load_idx(s0 + kWgSplit * 16);
-    for (; s0 < cnt; s0 += kWgSplit * 16) {
-      uint32_t ah[4], am[4], al[4], q[4][4];
-      split3(f.p[0][0], f.p[1][0], ah[0], am[0], al[0]);
-      split3(f.p[0][1], f.p[1][1], ah[1], am[1], al[1]);
-      split3(f.p[2][0], f.p[3][0], ah[2], am[2], al[2]);
-      split3(f.p[2][1], f.p[3][1], ah[3], am[3], al[3]);
+    uint8_t* ring = wg_smem + warp * kWgStages * kWgStage;
+    constexpr int kHop = kWgSplit * 16;
+    // lane l < 16 holds the row of place l of the step that is fetched next
+    int s_idx = part * 16;
+    auto next_idx = [&]() {
+      const int r = s_idx + (lane & 15);
+      s_idx += kHop;
+      return r < cnt ? rows[r] : -1;
+    };
+    int idx = next_idx();
+    int slot_in = 0;
+    // 16-byte chunk c of row r of Q at chunk place c ^ (r & 7); rows past the
+    // end arrive as zeros
+    auto fetch = [&]() {
+      const uint32_t base = smem_u32(ring + slot_in * kWgStage);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        q[i][0] = f.q[i].x, q[i][1] = f.q[i].y, q[i][2] = f.q[i].z, q[i][3] = f.q[i].w;
-        if (mask) {
+        const int r = i * 4 + lane / 8, c = lane % 8;
+        const int64_t row = __shfl_sync(0xffffffffu, idx, r);
+        cp_async16(base + (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)), Q + (row < 0 ? 0 : row * C + c * 8), row < 0 ? 0u : 16u);
+      }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) q[i][k] = keep2(q[i][k], f.keep[i] >> (2 * k));
+      for (int i = 0; i < 2; ++i) {
+        const int r = i * 8 + lane / 4, c = lane % 4;
+        const int64_t row = __shfl_sync(0xffffffffu, idx, r);
+        cp_async16(base + (uint32_t)(kWgQ + r * 80 + c * 16), P + (row < 0 ? 0 : row * kR + c * 4), row < 0 ? 0u : 16u);
+      }
+      if (mask) {
+        const int64_t row = __shfl_sync(0xffffffffu, idx, lane / 2);
+        cp_async4(base + (uint32_t)(kWgQ + kWgP + lane * 4), mask + (row < 0 ? 0 : (row * C + col0) / 32 + (lane & 1)), row < 0 ? 0u : 4u);
+      }
+      cp_async_commit();
+      if (++slot_in == kWgStages) slot_in = 0;
+      idx = next_idx();
+    };
+#pragma unroll
+    for (int i = 0; i < kWgStages - 1; ++i) fetch();
+    int slot = 0;
+    for (int s0 = part * 16; s0 < cnt; s0 += kHop) {
+      cp_async_wait<kWgStages - 2>();
+      __syncwarp();  // the step is there for every lane, and the slot before it is free
+      const uint8_t* st = ring + slot * kWgStage;
+      uint32_t q[4][4];
+      float p[4][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // rows 2t, 2t+1, 2t+8, 2t+9
+        const int r = 2 * t + (i & 1) + (i >> 1) * 8;
+        const uint4 v = *reinterpret_cast<const uint4*>(st + r * 128 + ((g ^ (r & 7)) << 4));
+        q[i][0] = v.x, q[i][1] = v.y, q[i][2] = v.z, q[i][3] = v.w;
+        p[i][0] = *reinterpret_cast<const float*>(st + kWgQ + r * 80 + g * 4);
+        p[i][1] = *reinterpret_cast<const float*>(st + kWgQ + r * 80 + g * 4 + 32);
+        if (mask) {
+          const uint32_t keep = *reinterpret_cast<const uint32_t*>(st + kWgQ + kWgP + r * 8 + (g / 4) * 4) >> (8 * (g & 3));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) q[i][k] = keep2(q[i][k], keep >> (2 * k));
         }
       }
-      load(f);
-      load_idx(s0 + 2 * kWgSplit * 16);
+      __syncwarp();
+      fetch();
+      if (++slot == kWgStages) slot = 0;
+      uint32_t ah[4], am[4], al[4];
+      split3(p[0][0], p[1][0], ah[0], am[0], al[0]);
+      split3(p[0][1], p[1][1], ah[1], am[1], al[1]);
+      split3(p[2][0], p[3][0], ah[2], am[2], al[2]);
+      split3(p[2][1], p[3][1], ah[3], am[3], al[3]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int k = i / 2;
@@ -521,6 +542,8 @@ __global__ void __launch_bounds__(kWgWarps * 32, 2) k_multi_wgrad(const WgArgs w
       }
     }
   }
+  cp_async_wait<0>();
+  __syncthreads();  // the ring becomes the sums
   const int nw = min(kWgSplit, (cnt + 15) / 16);  // parts that had rows
   if (part < nw) {
 #pragma unroll
@@ -559,6 +582,95 @@ __global__ void __launch_bounds__(kWgWarps * 32, 2) k_multi_wgrad(const WgArgs w
   }
 }
 
+// ------------------------------------------------------------------------ the adapter term by itself
+// Where a tile row of the GEMM has more adapters than slots (many requests of
+// few rows): out = base + the adapter term, one rounding.  FWD: + s_a sum_j
+// U[m][j] B_a[n][j]; else + mask . s_a sum_j G[m][j] A_a[j][k].  CTA = the rows
+// of one tile of the plan (one adapter, 64 at most) x 256 columns; a thread
+// keeps the factor of its two columns in registers for all rows, so adapters
+// are read once a tile; bound by the fp32 base it reads and what it writes.  A
+// slot costs the GEMM a 64-deep step of every tile: 512 rows of 5120x5120 take
+// 57 us with 8 adapters in slots, 73 with 16, 324 with the term in the GEMM's
+// epilogue, 62 this way (64 adapters).
+constexpr int kExThreads = 128;
+template <bool FWD, bool F16, bool O16>
+__global__ void __launch_bounds__(kExThreads)
+    k_multi_expand(const float* base, const float* P, const void* Fv, int64_t strideF, const float* scale,
+                   const uint32_t* mask, const int32_t* plan, int64_t o_perm, int64_t o_tile, int C, int accumulate,
+                   void* out) {
+  __shared__ float u[kTileRows][kR];
+  __shared__ int rows[kTileRows];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int4 tile = *reinterpret_cast<const int4*>(plan + o_tile + 4 * (int64_t)blockIdx.y);  // (the table has room for it)
+  if (plan[1] >= 0 || (int)blockIdx.y >= plan[0]) return;
+  const int cnt = tile.z, a = tile.x;
+  const float s = a >= 0 ? scale[a] : 0.0f;
+  for (int i = threadIdx.x; i < cnt * kR; i += kExThreads) {
+    const int row = plan[o_perm + tile.y + i / kR];
+    if (i % kR == 0) rows[i / kR] = row;
+    u[i / kR][i % kR] = a >= 0 ? s * P[(int64_t)row * kR + i % kR] : 0.0f;
+  }
+  __syncthreads();
+  const int c = ((int)blockIdx.x * kExThreads + (int)threadIdx.x) * 2;
+  if (c >= C) return;
+  float f0[kR], f1[kR];  // the factor of columns c and c + 1
+#pragma unroll
+  for (int j = 0; j < kR; ++j) f0[j] = f1[j] = 0.0f;
+  if (a >= 0) {
+    if constexpr (!FWD) {
+      const float* F = static_cast<const float*>(Fv) + a * strideF + c;
+#pragma unroll
+      for (int j = 0; j < kR; ++j) {
+        const float2 v = *reinterpret_cast<const float2*>(F + (int64_t)j * C);
+        f0[j] = v.x, f1[j] = v.y;
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float* f = h ? f1 : f0;
+        const int64_t o = a * strideF + (int64_t)(c + h) * kR;
+#pragma unroll
+        for (int j = 0; j < kR; j += 4) {
+          if constexpr (F16) {
+            const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(Fv) + o + j);
+            f[j] = bf16_lo(v.x), f[j + 1] = bf16_hi(v.x), f[j + 2] = bf16_lo(v.y), f[j + 3] = bf16_hi(v.y);
+          } else {
+            const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(Fv) + o + j);
+            f[j] = v.x, f[j + 1] = v.y, f[j + 2] = v.z, f[j + 3] = v.w;
+          }
+        }
+      }
+    }
+  }
+  for (int r = 0; r < cnt; ++r) {
+    const int64_t at = (int64_t)rows[r] * C + c;
+    float2 v = *reinterpret_cast<const float2*>(base + at);
+    float d0 = 0.0f, d1 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kR; j += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(&u[r][j]);
+      d0 = fmaf(x.x, f0[j], d0), d0 = fmaf(x.y, f0[j + 1], d0), d0 = fmaf(x.z, f0[j + 2], d0), d0 = fmaf(x.w, f0[j + 3], d0);
+      d1 = fmaf(x.x, f1[j], d1), d1 = fmaf(x.y, f1[j + 1], d1), d1 = fmaf(x.z, f1[j + 2], d1), d1 = fmaf(x.w, f1[j + 3], d1);
+    }
+    const uint32_t keep = !FWD && mask ? mask[at >> 5] >> (at & 31) : 3u;
+    if (a >= 0) {
+      if (keep & 1u) v.x += d0;
+      if (keep & 2u) v.y += d1;
+    }
+    if constexpr (O16) {
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + at) = pack_bf16x2(v.x, v.y);
+    } else {
+      float2* o = reinterpret_cast<float2*>(static_cast<float*>(out) + at);
+      if (accumulate) {
+        const float2 old = *o;
+        v.x = old.x + v.x, v.y = old.y + v.y;
+      }
+      *o = v;
+    }
+  }
+}
+
 // ------------------------------------------------------------------------ host side
 #ifndef WS_FEW_ROWS
 #define WS_FEW_ROWS 64
@@ -566,16 +678,19 @@ __global__ void __launch_bounds__(kWgWarps * 32, 2) k_multi_wgrad(const WgArgs w
 constexpr int kFewRows = WS_FEW_ROWS;  // rows up to which run_few makes the forward
 
 struct WsLayout {
-  size_t G, ext, bad, partial, total;  // bad: words of the GEMM (1) or of run_few (kFewUnits)
+  size_t G, ext, bad, base, partial, total;  // bad: words of the GEMM (1) or of run_few (kFewUnits)
 };
-WsLayout ws_layout(int64_t M, int64_t N, int64_t K) {
+// base: the fp32 base term of k_multi_expand, which a set of no more adapters
+// than slots never needs.
+WsLayout ws_layout(int64_t M, int64_t N, int64_t K, int32_t n) {
   WsLayout L{};
   const GemmPlan f = plan_gemm(false, M, N, K), b = plan_gemm(true, M, K, N);
   const size_t pf = gemm_partial_bytes(f, M, N), pb = gemm_partial_bytes(b, M, K);
   L.G = 0;
   L.ext = al256((size_t)M * kR * 4);
   L.bad = L.ext + (size_t)M * kMultiSlots * 128;
-  L.partial = L.bad + kFewUnits * 4;
+  L.base = L.bad + kFewUnits * 4;
+  L.partial = L.base + (n > kMultiSlots ? al256((size_t)M * (size_t)(N > K ? N : K) * 4) : 0);
   size_t p = pf > pb ? pf : pb;
   if (M <= kFewRows && p < kFewUnits * 64 * 128 * 4) p = kFewUnits * 64 * 128 * 4;
   L.total = L.partial + al256(p);
@@ -639,9 +754,20 @@ MultiLora multi_of(const ws_lora_plan& plan, uint8_t* ws, const WsLayout& W, con
   m.slots = pl + 1;
   m.tile_ad = pl + L.tile_ad;
   m.bad = reinterpret_cast<uint32_t*>(ws + W.bad);
+  m.out32 = reinterpret_cast<float*>(ws + W.base);
   m.stride = stride;
   m.f16 = f16 ? 1 : 0;
   return m;
+}
+
+template <typename K>
+cudaError_t run_expand(K k, const MultiLora& ml, const uint32_t* mask, const ws_lora_plan& plan, int64_t C,
+                       int accumulate, void* out, cudaStream_t st) {
+  const PlanLayout L = plan_layout(plan.M, plan.n_adapters);
+  note_launch();
+  return launch_pdl(k, dim3((unsigned)((C + 2 * kExThreads - 1) / (2 * kExThreads)), (unsigned)L.max_tiles),
+                    dim3(kExThreads), 0, st, (const float*)ml.out32, ml.P, ml.F, ml.stride, ml.scale, mask,
+                    (const int32_t*)plan.data, L.perm, L.tile, (int)C, accumulate, out);
 }
 
 ws_status check_plan(const ws_lora_plan* p) {
@@ -725,7 +851,7 @@ ws_status ws_lora_multi_workspace_size(int64_t M, int64_t N, int64_t K, int32_t 
   if (M < 1 || M > (1 << 20) || N < 64 || K < 64 || N % 64 || K % 64 || n_adapters < 1 ||
       n_adapters > WS_MULTI_MAX_ADAPTERS)
     return WS_ERR_SHAPE;
-  *bytes = ws_layout(M, N, K).total;
+  *bytes = ws_layout(M, N, K, n_adapters).total;
   return WS_OK;
 }
 
@@ -738,7 +864,7 @@ ws_status ws_lora_linear_fwd_multi(const ws_nf4* W, const uint16_t* x, const ws_
   if (!x || !y || !U_saved || !workspace) return WS_ERR_INVALID;
   if (!al16p(x) || !al16p(y) || !al16p(U_saved) || !al16p(workspace)) return WS_ERR_ALIGN;
   const int64_t M = plan->M, N = W->N, K = W->K;
-  const WsLayout L = ws_layout(M, N, K);
+  const WsLayout L = ws_layout(M, N, K, set->n_adapters);
   if (ws_bytes < L.total) return WS_ERR_OOM;
   cudaStream_t st = (cudaStream_t)stream;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -760,6 +886,9 @@ ws_status ws_lora_linear_fwd_multi(const ws_nf4* W, const uint16_t* x, const ws_
   const MultiLora ml = multi_of(*plan, ws, L, U_saved, set->B, f16, set->stride_b, set->scale);
   WS_RUN(run_nf4_gemm_multi(plan_gemm(false, M, N, K), view(W), x, M, ml, nullptr, y, 0, 0,
                             reinterpret_cast<float*>(ws + L.partial), st));
+  if (set->n_adapters > kMultiSlots)
+    WS_RUN(run_expand(f16 ? k_multi_expand<true, true, true> : k_multi_expand<true, false, true>, ml, nullptr, *plan,
+                      N, 0, y, st));
   return WS_OK;
 }
 
@@ -778,7 +907,7 @@ ws_status ws_lora_linear_bwd_multi(const ws_nf4* W, const uint16_t* x, const ws_
   if (!al16p(x) || !al16p(U_saved) || !al16p(dY) || !al16p(dX) || !al16p(dA) || !al16p(dB) || !al16p(workspace))
     return WS_ERR_ALIGN;
   const int64_t M = plan->M, N = W->N, K = W->K;
-  const WsLayout L = ws_layout(M, N, K);
+  const WsLayout L = ws_layout(M, N, K, set->n_adapters);
   if (ws_bytes < L.total) return WS_ERR_OOM;
   cudaStream_t st = (cudaStream_t)stream;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -797,12 +926,18 @@ ws_status ws_lora_linear_bwd_multi(const ws_nf4* W, const uint16_t* x, const ws_
   w.plan = pl;
   w.o_perm = P.perm, w.o_off = P.off;
   w.accumulate = (accumulate & WS_ACC_GRADS) ? 1 : 0;
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(k_multi_wgrad, cudaFuncAttributeMaxDynamicSharedMemorySize, kWgSmem);
+  WS_RUN(attr);
   note_launch();
   WS_RUN(launch_pdl(k_multi_wgrad, dim3((unsigned)((N + 127) / 128 + (K + 127) / 128), (unsigned)set->n_adapters), dim3(kWgWarps * 32),
-                    0, st, w));
+                    kWgSmem, st, w));
   const MultiLora ml = multi_of(*plan, ws, L, G, set->A, false, set->stride_a, set->scale);
   WS_RUN(run_nf4_gemm_multi(plan_gemm(true, M, K, N), view(W), dY, M, ml, mask, dX, dX_dtype == WS_DTYPE_F32 ? 1 : 0,
                             (accumulate & WS_ACC_DX) ? 1 : 0, reinterpret_cast<float*>(ws + L.partial), st));
+  if (set->n_adapters > kMultiSlots)
+    WS_RUN(run_expand(dX_dtype == WS_DTYPE_F32 ? k_multi_expand<false, false, false> : k_multi_expand<false, false, true>,
+                      ml, mask, *plan, K, (accumulate & WS_ACC_DX) ? 1 : 0, dX, st));
   return WS_OK;
 }
 

@@ -525,52 +525,13 @@ struct WMaps {
   CUtensorMap m[kMaxGroups];
 };
 
-// The adapter term of 16 columns from n of row m, whose adapter is ad: the
-// path of tile rows with more than kMultiSlots adapters.  Forward: rows n ..
-// n+15 of B_a [N, 16]; backward: columns of A_a [16, ld], under the keep bits.
-// Out of line, with the sums in local memory: inside the epilogue its registers
-// made every warp of the kernel spill (backward of 2048 rows of 5120x27648:
-// 768 -> 598 us in all).
-template <bool BWD>
-__device__ __noinline__ void ml_add(const GemmArgs& a, int ad, int64_t m, int64_t n, int64_t ld, uint32_t keep,
-                                    float* v) {
-  const float s = a.ml_scale[ad];
-  const float* u = a.ml_P + m * 16;
-#pragma unroll 1
-  for (int e = 0; e < 16; ++e) {
-    float d = 0.0f;
-    if constexpr (BWD) {
-      const float* F = static_cast<const float*>(a.ml_F) + ad * a.ml_stride + n + e;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) d = fmaf(u[j], F[j * ld], d);
-    } else if (a.ml_f16) {
-      const uint32_t* F = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.ml_F) + ad * a.ml_stride + (n + e) * 16);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t f = F[j];
-        d = fmaf(u[2 * j], bf16_lo(f), d);
-        d = fmaf(u[2 * j + 1], bf16_hi(f), d);
-      }
-    } else {
-      const float4* F = reinterpret_cast<const float4*>(static_cast<const float*>(a.ml_F) + ad * a.ml_stride + (n + e) * 16);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 f = F[j];
-        d = fmaf(u[4 * j], f.x, d);
-        d = fmaf(u[4 * j + 1], f.y, d);
-        d = fmaf(u[4 * j + 2], f.z, d);
-        d = fmaf(u[4 * j + 3], f.w, d);
-      }
-    }
-    if ((keep >> e) & 1u) v[e] = fmaf(s, d, v[e]);
-  }
-}
-
 // An F value times its scale that the tensor cores must not see: a zero factor
 // of another adapter's row would turn it into NaN there.
 WS_DEVINL bool ml_is_bad(float v) { return !(fabsf(v) <= 3e38f); }
-// The part of the adapter term that such values make, for the row's own
-// adapter (rare: an adapter that has diverged).
+// The part of the adapter term that such values make in 16 columns from n of
+// row m, for the row's own adapter ad (rare: an adapter that has diverged).  Out
+// of line, with the sums in local memory: inside the epilogue its registers
+// make every warp of the kernel spill.
 template <bool BWD>
 __device__ __noinline__ void ml_add_bad_values(const GemmArgs& a, int ad, int64_t m, int64_t n, int64_t ld,
                                                uint32_t keep, float* v) {
@@ -1267,10 +1228,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t dbase = tmem + (uint32_t)(a * C::ACC_COLS);
         // 16-column chunks of this warp's columns that lie inside the output
         // (of this tile's linear, for a grouped forward)
-        const TileGrp og = tile_grp(args, n0);
+        TileGrp og = tile_grp(args, n0);
+        // (ML: the base term alone, in fp32, where the adapter term is added
+        // by a kernel of its own)
+        const bool base_only = ML && ml_slots < 0;
+        if (base_only) og.out = args.ml_out32;
+        const int out_f32 = base_only ? 1 : args.out_f32, out_accum = base_only ? 0 : args.out_accum;
         // 32-byte stores need 32-byte aligned rows of the output
         const bool v8_out = (reinterpret_cast<uintptr_t>(og.out) & 31u) == 0u &&
-                            (og.width & (args.out_f32 ? 7 : 15)) == 0;
+                            (og.width & (out_f32 ? 7 : 15)) == 0;
         constexpr int KCH = (BN / 2) / 16;
         const int64_t cols_left = og.width - (n0 - og.c0 + half * (BN / 2));
         const int kv = cols_left <= 0 ? 0 : (cols_left >= KCH * 16 ? KCH : (int)((cols_left + 15) / 16));
@@ -1308,12 +1274,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row = u * 128 + r;
           const int64_t m = m0 + row;
           const bool row_ok = ok && m < args.M;
-          // whether the epilogue has a part of the adapter term to add (ML)
-          bool ml_add_all = false, ml_add_bad = false;
-          if constexpr (ML) {
-            ml_add_all = ml_slots < 0;
-            ml_add_bad = ml_slots > 0 && *(volatile const uint32_t*)args.ml_bad != 0u;
-          }
+          // whether bad values are left to add (ML)
+          bool ml_add_bad = false;
+          if constexpr (ML) ml_add_bad = ml_slots > 0 && *(volatile const uint32_t*)args.ml_bad != 0u;
 #pragma unroll 1
           for (int c = 0; c < kv; ++c) {
             const int cc = half * (BN / 2) + c * 16;
@@ -1353,15 +1316,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!row_ok) continue;
             const int64_t o_off = m * og.width + (n - og.c0);
             if constexpr (ML) {
-              if (ml_add_all || ml_add_bad) {
+              if (ml_add_bad) {
                 const int ad = args.ml_row[m];
                 if (ad >= 0) {
                   const uint32_t keep = BWD && args.mask ? args.mask[o_off >> 5] >> (o_off & 31) : 0xffffu;
                   float w[16];
 #pragma unroll
                   for (int e = 0; e < 16; ++e) w[e] = v[e];
-                  if (ml_add_all) ml_add<BWD>(args, ad, m, n, og.width, keep, w);
-                  else ml_add_bad_values<BWD>(args, ad, m, n, og.width, keep, w);
+                  ml_add_bad_values<BWD>(args, ad, m, n, og.width, keep, w);
 #pragma unroll
                   for (int e = 0; e < 16; ++e) v[e] = w[e];
                 }
@@ -1371,9 +1333,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               // one 32-byte store per 8 fp32 or 16 bf16 values: whole
               // sectors (16-byte stores of the rows of a warp write half
               // sectors and held every accumulator drain back)
-              if (args.out_f32) {
+              if (out_f32) {
                 float* dst = static_cast<float*>(og.out) + o_off;
-                if (args.out_accum) {
+                if (out_accum) {
                   uint32_t q[16];
                   ld_global_v8(dst, q);
                   ld_global_v8(dst + 8, q + 8);
@@ -1392,12 +1354,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                              pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]),
                              pack_bf16x2(v[12], v[13]), pack_bf16x2(v[14], v[15]));
               }
-            } else if (args.out_f32) {
+            } else if (out_f32) {
               float4* dst = reinterpret_cast<float4*>(static_cast<float*>(og.out) + o_off);
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 float4 o = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-                if (args.out_accum) {
+                if (out_accum) {
                   const float4 q = dst[e];
                   o.x = q.x + o.x;
                   o.y = q.y + o.y;
@@ -2313,6 +2275,7 @@ int64_t pair_capacity(bool bwd, int bn) {
 }
 
 int64_t grid_units(const GemmPlan& p, bool has_lora) {
+  if (p.units > 0) return p.units;
   const int64_t S = (int64_t)p.nk + (has_lora ? 1 : 0);
   const int64_t I = (int64_t)p.mtiles * p.ntiles * S;
   // at least kMinSteps iterations per unit, and at least a third of a short
@@ -2513,9 +2476,17 @@ int64_t gemm_tile_rows(int64_t M) {
   return 128 * p.um * (p.pair ? 2 : 1);
 }
 
-cudaError_t run_nf4_gemm_multi(const GemmPlan& p, const NF4View& W, const uint16_t* act, int64_t M,
+cudaError_t run_nf4_gemm_multi(const GemmPlan& plan, const NF4View& W, const uint16_t* act, int64_t M,
                                const MultiLora& ml, const uint32_t* mask, void* out, int out_f32,
                                int out_accum, float* partial, cudaStream_t st) {
+  GemmPlan p = plan;
+  // short tiles: a unit each where they fit the GPU, instead of several in a
+  // row for eight steps a unit (77 rows of 128x896 backward: 24 -> 14 us)
+  const int64_t tiles = (int64_t)p.mtiles * p.ntiles;
+  if (tiles > grid_units(p, true) && tiles <= (p.pair ? pair_capacity(p.bwd, p.bn) : device_sm_count())) {
+    p.units = tiles;
+    p.epad = 0;
+  }
   if (!encode_fn()) return cudaErrorNotSupported;
   const int64_t Nout = p.bwd ? W.K : W.N, Kc = p.bwd ? W.N : W.K;
   // the batch's plan lists adapters by tile row
@@ -2549,6 +2520,7 @@ cudaError_t run_nf4_gemm_multi(const GemmPlan& p, const NF4View& W, const uint16
   a.ml_slots = ml.slots;
   a.ml_tile_ad = ml.tile_ad;
   a.ml_bad = ml.bad;
+  a.ml_out32 = ml.out32;
   a.ml_stride = ml.stride;
   a.ml_f16 = ml.f16;
   if (grid_units(p, true) > 1) {

@@ -491,6 +491,11 @@ def dropout_mask(key: DropoutKey, M: int, K: int, mask=None, device="cuda", stre
     return mask
 
 
+def _slices_ok(t):
+    """Each t[i] of a 3-D tensor is contiguous, on the current device."""
+    return t.get_device() == _device() and t.stride(2) == 1 and t.stride(1) == t.shape[2]
+
+
 class LoraSet:
     """The adapters of one linear (ws_lora_set): A [n, 16, K], B [n, N, 16], both fp32 or both
     bf16 (serving only), scale fp32 [n] (alpha/r; with dropout alpha/r/(1-p)).  The first
@@ -503,8 +508,8 @@ class LoraSet:
         _need(B.shape[2] == r, "A and B have different ranks")
         _need(A.dtype == B.dtype and A.dtype in (torch.float32, torch.bfloat16), "A and B: both fp32 or both bf16")
         _need(scale.dtype == torch.float32 and tuple(scale.shape) == (n,), "scale: fp32 [n]")
-        _need(n > 0 and A[0].is_contiguous() and B[0].is_contiguous(), "each adapter's A and B must be contiguous")
-        _here(A[0], B[0], scale)
+        _need(n > 0 and _slices_ok(A) and _slices_ok(B), "each adapter's A and B: contiguous, on the current device")
+        _here(scale)
         self.A, self.B, self.scale = A, B, scale
         self.n, self.r, self.K, self.N = n, r, K, N
         sa, sb = (A.stride(0), B.stride(0)) if n > 1 else (r * K, r * N)
@@ -597,12 +602,12 @@ def lora_linear_bwd_multi(W: NF4Weight, x, aset: LoraSet, plan: LoraPlan, U, dY,
     if dA is None or dB is None:
         gA, gB = aset.empty_grads()
         dA, dB = gA if dA is None else dA, gB if dB is None else dB
-    for g, p, name in ((dA, aset.A, "dA"), (dB, aset.B, "dB")):
-        _need(g.dtype == torch.float32 and g.shape == p.shape and g[0].is_contiguous()
-              and (aset.n == 1 or g.stride(0) == p.stride(0)), f"{name}: fp32 with the shape and strides of the set's")
+    for g, p in ((dA, aset.A), (dB, aset.B)):
+        _need(g.dtype == torch.float32 and g.shape == p.shape and _slices_ok(g)
+              and (aset.n == 1 or g.stride(0) == p.stride(0)), "dA, dB: fp32 with the shapes and strides of the set's A, B")
     if workspace is None:
         workspace = _empty((lora_multi_workspace_size(M, W.N, W.K, aset.n),), torch.uint8, x.device, stream)
-    _here(x, mask, U, dY, dX, dA[0], dB[0], workspace, W.codes, W.absmax)
+    _here(x, mask, U, dY, dX, workspace, W.codes, W.absmax)
     w = W.c()
     dt = WS_DTYPE_F32 if dX.dtype == torch.float32 else WS_DTYPE_BF16
     _check("ws_lora_linear_bwd_multi",
