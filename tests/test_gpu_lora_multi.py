@@ -182,6 +182,33 @@ def test_forward(ops, shape, dtype):
     assert ops.device_error() == 0
 
 
+BIG = [
+    # weights large enough for the tensor-core kernel of few rows and for tiles cut between CTAs
+    (17, 9728, 2112, 5, "random", False),
+    (33, 4864, 4864, 33, "distinct", True),
+    (64, 8192, 2880, 6, "wild", False),
+    (48, 5184, 5120, 48, "distinct", False),
+    (1, 5120, 5120, 2, "one", True),
+    (16, 2112, 9728, 3, "random", True),
+    (520, 2560, 896, 9, "runs", True),
+    (520, 2560, 896, 30, "random", True),
+]
+
+
+@pytest.mark.parametrize("shape", BIG, ids=["-".join(map(str, s)) for s in BIG])
+def test_forward_of_large_weights(ops, shape):
+    M, N, K, n, kind, mask = shape
+    c = Case(ops, M, N, K, n, kind, torch.float32, mask, seed=M)
+    ws = torch.full((ops.lora_multi_workspace_size(M, N, K, n),), 255, dtype=torch.uint8, device=dev())
+    y = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device=dev())
+    U = torch.full((M, 16), float("nan"), device=dev())
+    for _ in range(3):   # the same workspace again: what a call leaves in it does not matter
+        y.fill_(float("nan"))
+        ops.lora_linear_fwd_multi(c.W, c.x, c.set, c.plan, mask=c.mask, y=y, U=U, workspace=ws)
+        check_forward(c, y, U)
+    assert ops.device_error() == 0
+
+
 @pytest.mark.parametrize("dx32", [True, False], ids=["dx32", "dx16"])
 @pytest.mark.parametrize("shape", SHAPES, ids=["-".join(map(str, s)) for s in SHAPES])
 def test_backward(ops, shape, dx32):
