@@ -438,8 +438,8 @@ ws_status ws_attention_bwd(const uint16_t* q, const uint16_t* k, const uint16_t*
  *      times v_scale [ceil(n/256)] = max sqrt(v) (1/1.9375); never 0 for v > 0.
  * Both to nearest (ties to even); the step uses the moments before this
  * rounding.  Zero codes and scales are zero moments.  A gradient that is not
- * finite makes its element's moments (in 8 bits: its whole block's) NaN,
- * unless clipping skips the step. */
+ * finite leaves its element's moments (in 8 bits: its whole block's) not
+ * finite, unless clipping skips the step. */
 typedef struct {
   void* p;        /* parameters [n] (device)                               */
   const void* g;  /* gradients [n] (device; two tensors may share one)      */

@@ -268,6 +268,37 @@ def test_accumulation(ops):
     assert ops.device_error() == 0
 
 
+@pytest.mark.parametrize("M", [70, 300])
+def test_accumulation_with_more_adapters_than_slots(ops, M):
+    c = Case(ops, M, 192, 320, 30, "random", mask=True, seed=M)
+    U = c.forward()["U"].float()
+    dX, dA, dB = ops.lora_linear_bwd_multi(c.W, c.x, c.set, c.plan, U, c.dY, mask=c.mask, dX_f32=True)
+    oX, oA, oB = (torch.randn_like(t) for t in (dX, dA, dB))
+    aX, aA, aB = oX.clone(), oA.clone(), oB.clone()
+    ops.lora_linear_bwd_multi(c.W, c.x, c.set, c.plan, U, c.dY, mask=c.mask, dX=aX, dA=aA, dB=aB, accumulate=True,
+                              grad_accumulate=True)
+    # one fp32 add each (adapters without a row: 0 added, or left)
+    assert torch.equal(aX, oX + dX) and torch.equal(aA, oA + dA) and torch.equal(aB, oB + dB)
+
+
+def test_two_streams_at_once(ops):
+    """Calls that overlap, each with its own workspace and plan, do not meet."""
+    cs = [Case(ops, M, 2112, 1088, 12, "random", mask=True, seed=M) for M in (5, 40, 90, 300)]
+    want = [ops.lora_linear_fwd_multi(c.W, c.x, c.set, c.plan, mask=c.mask) for c in cs]
+    grads = [ops.lora_linear_bwd_multi(c.W, c.x, c.set, c.plan, w[1], c.dY, mask=c.mask) for c, w in zip(cs, want)]
+    torch.cuda.synchronize()
+    st = [torch.cuda.Stream() for _ in cs]
+    for _ in range(5):
+        got = []
+        for c, s, w in zip(cs, st, want):
+            f = ops.lora_linear_fwd_multi(c.W, c.x, c.set, c.plan, mask=c.mask, stream=s)
+            got.append((f, ops.lora_linear_bwd_multi(c.W, c.x, c.set, c.plan, f[1], c.dY, mask=c.mask, stream=s)))
+        torch.cuda.synchronize()
+        for (f, b), w, g in zip(got, want, grads):
+            assert all(torch.equal(p, q) for p, q in zip((*f, *b), (*w, *g)))
+    assert ops.device_error() == 0
+
+
 def test_gradients_against_differences(ops):
     """sum(y . dY) as a function of A, B and x, in 64 bits, differenced."""
     c = Case(ops, 37, 128, 128, 3, "random", mask=True, seed=5)

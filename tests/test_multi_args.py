@@ -201,5 +201,8 @@ def test_adamw_groups_refuses_unknown_settings(ops):
         ops.adamw_groups([dict(lr=1e-3, momentum=0.9)], device="cpu")
     with pytest.raises(ValueError):
         ops.adamw_groups([dict(beta1=0.9)], device="cpu")
+    for bad in (dict(beta1=1.0), dict(beta2=-0.1), dict(eps=-1e-8), dict(step=-1), dict(step=0.5)):
+        with pytest.raises(ValueError):
+            ops.adamw_groups([dict(lr=1e-3, **bad)], device="cpu")
     g = ops.adamw_groups([dict(lr=1e-3), dict(lr=2e-3, step=7, max_norm=0.5)], device="cpu")
     assert g.shape == (2, 8) and g[0].tolist() == [1e-3, 0.9, 0.999, 1e-8, 0.01, 0.0, 0.0, 0.0] and g[1, 6] == 7

@@ -98,7 +98,7 @@ constexpr uint32_t kRootBias = (127u - 15u) << 4;
 WS_DEVINL uint32_t root_code(float q) {
   const uint32_t b = __float_as_uint(q);  // q >= 0
   const int r = (int)(b + ((b >> 19) & 1u) + (0x3FFFFu - (kRootBias << 19))) >> 19;
-  return (uint32_t)max(r, (int)min(b, 1u));
+  return (uint32_t)min(max(r, (int)min(b, 1u)), 255);  // (NaN: 255, in a block whose scale is not finite)
 }
 WS_DEVINL float root_value(uint32_t c) {
   return c ? __uint_as_float(c * (1u << 19) + (kRootBias << 19)) : 0.0f;
@@ -626,7 +626,7 @@ ws_status ws_adamw_plan_init(const ws_adamw_tensor* tensors, int32_t n_tensors, 
       end_any = std::max(end_any, q.e);
       if (!q.grad) end_written = std::max(end_written, q.e);
     }
-  } catch (const std::bad_alloc&) {
+  } catch (...) {  // no memory
     return WS_ERR_OOM;
   }
   memset(image, 0, L.bytes);

@@ -633,7 +633,10 @@ def adamw_groups(groups, device="cuda"):
     rows = []
     for g in groups:
         _need(set(g) <= set(names) and "lr" in g, f"a group has lr and any of {names[1:]}")
-        rows.append([float({**d, **g}[k]) for k in names] + [0.0])
+        v = [float({**d, **g}[k]) for k in names]
+        _need(0.0 <= v[1] < 1.0 and 0.0 <= v[2] < 1.0, "beta1 and beta2 lie in [0, 1)")
+        _need(v[3] >= 0.0 and v[6] >= 0.0 and v[6] == int(v[6]), "eps >= 0; step: a whole number, >= 0")
+        rows.append(v + [0.0])
     return torch.tensor(rows, dtype=torch.float64, device=device)
 
 
