@@ -98,7 +98,7 @@ constexpr uint32_t kRootBias = (127u - 15u) << 4;
 WS_DEVINL uint32_t root_code(float q) {
   const uint32_t b = __float_as_uint(q);  // q >= 0
   const int r = (int)(b + ((b >> 19) & 1u) + (0x3FFFFu - (kRootBias << 19))) >> 19;
-  return (uint32_t)min(max(r, (int)min(b, 1u)), 255);  // (NaN: 255, in a block whose scale is not finite)
+  return (uint32_t)max(r, (int)min(b, 1u));  // (NaN: nonsense, in a block whose scale is not finite)
 }
 WS_DEVINL float root_value(uint32_t c) {
   return c ? __uint_as_float(c * (1u << 19) + (kRootBias << 19)) : 0.0f;
@@ -218,15 +218,19 @@ WS_DEVINL float adamw1(float& p, float g, float& m, float& v, const Coef& c) {
 // writes may not be, or the compiler may load it ahead of the wait for that
 // kernel.
 // A sum in two fp32 parts, h + l: twice the precision at a few operations an
-// element, where double precision would bind the pass (Knuth's two-sum, and a
+// addition, where double precision would bind the pass (Knuth's two-sum, and a
 // product's error by a fused multiply-add).
 struct Sum2 {
   float h, l;
 };
-WS_DEVINL void add2(Sum2& s, float x, float e) {
+WS_DEVINL void add2(Sum2& s, float x) {
   const float t = __fadd_rn(s.h, x), z = __fsub_rn(t, s.h);
-  s.l = __fadd_rn(s.l, __fadd_rn(__fadd_rn(__fsub_rn(s.h, __fsub_rn(t, z)), __fsub_rn(x, z)), e));
+  s.l = __fadd_rn(s.l, __fadd_rn(__fsub_rn(s.h, __fsub_rn(t, z)), __fsub_rn(x, z)));
   s.h = t;
+}
+WS_DEVINL void add2(Sum2& s, float x, float e) {
+  add2(s, x);
+  s.l = __fadd_rn(s.l, e);
 }
 WS_DEVINL Sum2 warp_sum2(Sum2 s) {
 #pragma unroll
@@ -237,31 +241,47 @@ WS_DEVINL Sum2 warp_sum2(Sum2 s) {
   return s;
 }
 
+// A CTA takes kSumChunks chunks, all their loads in flight at once.
+constexpr int kSumChunks = 4;
 template <bool G16>
 __global__ void __launch_bounds__(kThreads)
-    k_adamw_sumsq(const Chunk* __restrict__ chunks, float2* partial) {
+    k_adamw_sumsq(const Chunk* __restrict__ chunks, int n_chunks, float2* partial) {
+  __shared__ Sum2 red[kSumChunks][kThreads / 32];
+  const int c0 = (int)blockIdx.x * kSumChunks;
+  const void* gp[kSumChunks];
+  int n[kSumChunks];
+#pragma unroll
+  for (int c = 0; c < kSumChunks; ++c) {
+    const bool in = c0 + c < n_chunks;
+    gp[c] = in ? chunks[c0 + c].g : nullptr;
+    n[c] = in ? chunks[c0 + c].n : 0;
+  }
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ Sum2 red[kThreads / 32];
-  const Chunk t = chunks[blockIdx.x];
-  float g[2][8];
+  float g[kSumChunks][2][8];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) load_n<G16, 8>(t.g, (u * kThreads + (int)threadIdx.x) * 8, t.n, g[u]);
-  Sum2 s{0.0f, 0.0f};
+  for (int c = 0; c < kSumChunks; ++c)
 #pragma unroll
-  for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u) load_n<G16, 8>(gp[c], (u * kThreads + (int)threadIdx.x) * 8, n[c], g[c][u]);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float q = __fmul_rn(g[u][k], g[u][k]);
-      add2(s, q, fmaf(g[u][k], g[u][k], -q));
-    }
-  s = warp_sum2(s);
-  if (lane_id() == 0) red[warp_id()] = s;
+  for (int c = 0; c < kSumChunks; ++c) {
+    Sum2 s{0.0f, 0.0f};
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float x = g[c][u][k], q = __fmul_rn(x, x);
+        if (G16) add2(s, q);  // (the square of a bf16 value is exact)
+        else add2(s, q, fmaf(x, x, -q));
+      }
+    s = warp_sum2(s);
+    if (lane_id() == 0) red[c][warp_id()] = s;
+  }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    s = red[0];
-    for (int w = 1; w < kThreads / 32; ++w) add2(s, red[w].h, red[w].l);
-    partial[blockIdx.x] = make_float2(s.h, s.l);
+  if (threadIdx.x < kSumChunks && c0 + (int)threadIdx.x < n_chunks) {
+    Sum2 s = red[threadIdx.x][0];
+    for (int w = 1; w < kThreads / 32; ++w) add2(s, red[threadIdx.x][w].h, red[threadIdx.x][w].l);
+    partial[c0 + threadIdx.x] = make_float2(s.h, s.l);
   }
 }
 
@@ -387,12 +407,12 @@ WS_DEVINL float warp_max_bits(uint32_t x) {
 template <bool ROOT>
 WS_DEVINL void encode8(const float (&x)[8], float scale, uint32_t (&o)[2]) {
   const float up = scale < 0x1p-64f ? 0x1p64f : 1.0f;
-  const float d = scale * up, inv = 1.0f / d;
+  const float d = scale * up, inv = scale > 0.0f ? 1.0f / d : 0.0f;  // (all zero: codes 0)
   float q[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const float y = x[k] * up, q0 = y * inv;
-    q[k] = scale > 0.0f ? fmaf(fmaf(-q0, d, y), inv, q0) : 0.0f;
+    q[k] = fmaf(fmaf(-q0, d, y), inv, q0);
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -442,11 +462,13 @@ WS_DEVINL void store_codes(uint8_t* q, int left, const uint32_t (&w)[2]) {
 }
 
 // One warp per block of 256, 8 elements per lane.  The step uses the moments
-// before they are rounded to 8 bits; the scales stay fp32.  134M fp32
-// parameters: 320 us, 6.7 TB/s; it was 410 us with a division for every code
-// and a table lookup ahead of every chunk's addresses.
+// before they are rounded to 8 bits; the scales stay fp32.  Four CTAs an SM (a
+// few spilled registers cost less than the fourth CTA's loads give: 39M
+// parameters with bf16 gradients 119 -> 111 us).  134M fp32 parameters: 332 us,
+// 6.5 TB/s; it was 410 us with a division for every code and a table lookup
+// ahead of every chunk's addresses.
 template <bool P16, bool G16>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 4)
     k_adamw8(const Chunk* __restrict__ chunks, const Coef* coef) {
   const int lane = (int)lane_id(), warp = (int)warp_id();
   constexpr int kPer = kChunk / (kBlock8 * (kThreads / 32));  // blocks of a warp
@@ -485,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       v[k] = v[k] * v[k];
       v[k] = adamw1<true>(p[k], g[k], m[k], v[k], c);  // what is kept is the root
       mx = max(mx, __float_as_uint(m[k]) & 0x7fffffffu);
-      vx = max(vx, __float_as_uint(v[k]) & 0x7fffffffu);
+      vx = max(vx, __float_as_uint(v[k]));
     }
     const float sm = warp_max_bits(mx) * (1.0f / kMTop), sv = warp_max_bits(vx) * (1.0f / kVTop);
     uint32_t mo[2], vo[2];
@@ -691,7 +713,9 @@ ws_status ws_adamw_step(const ws_adamw_plan* plan, ws_adamw_group* groups, int32
   cudaError_t e = cudaSuccess;
   if (measure) {
     note_launch();
-    e = launch_pdl(g16 ? k_adamw_sumsq<true> : k_adamw_sumsq<false>, grid, block, 0, st, ch, partial);
+    e = launch_pdl(g16 ? k_adamw_sumsq<true> : k_adamw_sumsq<false>,
+                   dim3((unsigned)((plan->n_chunks + kSumChunks - 1) / kSumChunks)), block, 0, st, ch,
+                   (int)plan->n_chunks, partial);
     if (e != cudaSuccess) return WS_ERR_CUDA;
   }
   note_launch();

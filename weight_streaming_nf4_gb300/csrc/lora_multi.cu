@@ -585,29 +585,30 @@ __global__ void __launch_bounds__(kWgWarps * 32, 2) k_multi_wgrad(const WgArgs w
 // ------------------------------------------------------------------------ the adapter term by itself
 // Where a tile row of the GEMM has more adapters than slots (many requests of
 // few rows): out = base + the adapter term, one rounding.  FWD: + s_a sum_j
-// U[m][j] B_a[n][j]; else + mask . s_a sum_j G[m][j] A_a[j][k].  CTA = the rows
-// of one tile of the plan (one adapter, 64 at most) x 256 columns; a thread
-// keeps the factor of its two columns in registers for all rows, so adapters
-// are read once a tile; bound by the fp32 base it reads and what it writes.  A
+// U[m][j] B_a[n][j]; else + mask . s_a sum_j G[m][j] A_a[j][k].  CTA = 16 rows
+// of one tile of the plan (one adapter) x 256 columns; a thread keeps the factor
+// of its two columns in registers for all rows and has eight rows of the base on
+// their way at a time; bound by the fp32 base it reads and what it writes.  A
 // slot costs the GEMM a 64-deep step of every tile: 512 rows of 5120x5120 take
 // 57 us with 8 adapters in slots, 73 with 16, 324 with the term in the GEMM's
 // epilogue, 62 this way (64 adapters).
-constexpr int kExThreads = 128;
+constexpr int kExThreads = 128, kExRows = 16;
 template <bool FWD, bool F16, bool O16>
 __global__ void __launch_bounds__(kExThreads)
     k_multi_expand(const float* base, const float* P, const void* Fv, int64_t strideF, const float* scale,
                    const uint32_t* mask, const int32_t* plan, int64_t o_perm, int64_t o_tile, int C, int accumulate,
                    void* out) {
-  __shared__ float u[kTileRows][kR];
-  __shared__ int rows[kTileRows];
+  __shared__ float u[kExRows][kR];
+  __shared__ int rows[kExRows];
   pdl_wait();
   pdl_launch_dependents();
   const int4 tile = *reinterpret_cast<const int4*>(plan + o_tile + 4 * (int64_t)blockIdx.y);  // (the table has room for it)
   if (plan[1] >= 0 || (int)blockIdx.y >= plan[0]) return;
-  const int cnt = tile.z, a = tile.x;
+  const int a = tile.x, r0 = (int)blockIdx.z * kExRows, cnt = min(kExRows, tile.z - r0);
+  if (cnt <= 0) return;
   const float s = a >= 0 ? scale[a] : 0.0f;
   for (int i = threadIdx.x; i < cnt * kR; i += kExThreads) {
-    const int row = plan[o_perm + tile.y + i / kR];
+    const int row = plan[o_perm + tile.y + r0 + i / kR];
     if (i % kR == 0) rows[i / kR] = row;
     u[i / kR][i % kR] = a >= 0 ? s * P[(int64_t)row * kR + i % kR] : 0.0f;
   }
@@ -643,30 +644,42 @@ __global__ void __launch_bounds__(kExThreads)
       }
     }
   }
-  for (int r = 0; r < cnt; ++r) {
-    const int64_t at = (int64_t)rows[r] * C + c;
-    float2 v = *reinterpret_cast<const float2*>(base + at);
-    float d0 = 0.0f, d1 = 0.0f;
+  for (int rb = 0; rb < cnt; rb += 8) {
+    float2 base8[8];
+    uint32_t keep[8];
 #pragma unroll
-    for (int j = 0; j < kR; j += 4) {
-      const float4 x = *reinterpret_cast<const float4*>(&u[r][j]);
-      d0 = fmaf(x.x, f0[j], d0), d0 = fmaf(x.y, f0[j + 1], d0), d0 = fmaf(x.z, f0[j + 2], d0), d0 = fmaf(x.w, f0[j + 3], d0);
-      d1 = fmaf(x.x, f1[j], d1), d1 = fmaf(x.y, f1[j + 1], d1), d1 = fmaf(x.z, f1[j + 2], d1), d1 = fmaf(x.w, f1[j + 3], d1);
+    for (int i = 0; i < 8; ++i) {
+      const int64_t at = (int64_t)rows[min(rb + i, cnt - 1)] * C + c;
+      base8[i] = *reinterpret_cast<const float2*>(base + at);
+      keep[i] = !FWD && mask ? mask[at >> 5] >> (at & 31) : 3u;
     }
-    const uint32_t keep = !FWD && mask ? mask[at >> 5] >> (at & 31) : 3u;
-    if (a >= 0) {
-      if (keep & 1u) v.x += d0;
-      if (keep & 2u) v.y += d1;
-    }
-    if constexpr (O16) {
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + at) = pack_bf16x2(v.x, v.y);
-    } else {
-      float2* o = reinterpret_cast<float2*>(static_cast<float*>(out) + at);
-      if (accumulate) {
-        const float2 old = *o;
-        v.x = old.x + v.x, v.y = old.y + v.y;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = rb + i;
+      if (r >= cnt) break;
+      const int64_t at = (int64_t)rows[r] * C + c;
+      float2 v = base8[i];
+      float d0 = 0.0f, d1 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kR; j += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(&u[r][j]);
+        d0 = fmaf(x.x, f0[j], d0), d0 = fmaf(x.y, f0[j + 1], d0), d0 = fmaf(x.z, f0[j + 2], d0), d0 = fmaf(x.w, f0[j + 3], d0);
+        d1 = fmaf(x.x, f1[j], d1), d1 = fmaf(x.y, f1[j + 1], d1), d1 = fmaf(x.z, f1[j + 2], d1), d1 = fmaf(x.w, f1[j + 3], d1);
       }
-      *o = v;
+      if (a >= 0) {
+        if (keep[i] & 1u) v.x += d0;
+        if (keep[i] & 2u) v.y += d1;
+      }
+      if constexpr (O16) {
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + at) = pack_bf16x2(v.x, v.y);
+      } else {
+        float2* o = reinterpret_cast<float2*>(static_cast<float*>(out) + at);
+        if (accumulate) {
+          const float2 old = *o;
+          v.x = old.x + v.x, v.y = old.y + v.y;
+        }
+        *o = v;
+      }
     }
   }
 }
@@ -765,7 +778,8 @@ cudaError_t run_expand(K k, const MultiLora& ml, const uint32_t* mask, const ws_
                        int accumulate, void* out, cudaStream_t st) {
   const PlanLayout L = plan_layout(plan.M, plan.n_adapters);
   note_launch();
-  return launch_pdl(k, dim3((unsigned)((C + 2 * kExThreads - 1) / (2 * kExThreads)), (unsigned)L.max_tiles),
+  return launch_pdl(k, dim3((unsigned)((C + 2 * kExThreads - 1) / (2 * kExThreads)), (unsigned)L.max_tiles,
+                             kTileRows / kExRows),
                     dim3(kExThreads), 0, st, (const float*)ml.out32, ml.P, ml.F, ml.stride, ml.scale, mask,
                     (const int32_t*)plan.data, L.perm, L.tile, (int)C, accumulate, out);
 }
