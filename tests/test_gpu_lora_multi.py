@@ -268,6 +268,45 @@ def test_accumulation(ops):
     assert ops.device_error() == 0
 
 
+BIG_FEW = [
+    # gradients of few rows: weights whose tiles are cut between CTAs, ends inside a step or a tile
+    (1, 5120, 5120, 2, "one", True),
+    (2, 9728, 2112, 2, "distinct", False),
+    (16, 2112, 9728, 3, "random", True),
+    (31, 5184, 4928, 31, "wild", True),
+    (32, 4864, 8192, 5, "distinct", False),
+    (33, 2112, 4864, 5, "random", True),
+]
+
+
+@pytest.mark.parametrize("dx32", [True, False], ids=["dx32", "dx16"])
+@pytest.mark.parametrize("shape", BIG_FEW, ids=["-".join(map(str, s)) for s in BIG_FEW])
+def test_backward_of_large_weights(ops, shape, dx32):
+    M, N, K, n, kind, mask = shape
+    c = Case(ops, M, N, K, n, kind, torch.float32, mask, seed=N)
+    U = c.forward()["U"].float()
+    ws = torch.full((ops.lora_multi_workspace_size(M, N, K, n),), 255, dtype=torch.uint8, device=dev())
+    dX = torch.full((M, K), float("nan"), dtype=torch.float32 if dx32 else torch.bfloat16, device=dev())
+    dA, dB = c.set.empty_grads()
+    for _ in range(3):   # the same workspace again
+        dX.fill_(float("nan"))
+        ops.lora_linear_bwd_multi(c.W, c.x, c.set, c.plan, U, c.dY, mask=c.mask, dX=dX, dA=dA, dB=dB, workspace=ws)
+        check_backward(c, U, dX, dA, dB)
+    assert ops.device_error() == 0
+
+
+@pytest.mark.parametrize("M,n", [(1, 1), (5, 40), (32, 3)])
+def test_accumulation_of_few_rows(ops, M, n):
+    c = Case(ops, M, 320, 192, n, "random", mask=True, seed=M)
+    U = c.forward()["U"].float()
+    dX, dA, dB = ops.lora_linear_bwd_multi(c.W, c.x, c.set, c.plan, U, c.dY, mask=c.mask, dX_f32=True)
+    oX, oA, oB = (torch.randn_like(t) for t in (dX, dA, dB))
+    aX, aA, aB = oX.clone(), oA.clone(), oB.clone()
+    ops.lora_linear_bwd_multi(c.W, c.x, c.set, c.plan, U, c.dY, mask=c.mask, dX=aX, dA=aA, dB=aB, accumulate=True,
+                              grad_accumulate=True)
+    assert torch.equal(aX, oX + dX) and torch.equal(aA, oA + dA) and torch.equal(aB, oB + dB)   # one fp32 add each
+
+
 @pytest.mark.parametrize("M", [70, 300])
 def test_accumulation_with_more_adapters_than_slots(ops, M):
     c = Case(ops, M, 192, 320, 30, "random", mask=True, seed=M)

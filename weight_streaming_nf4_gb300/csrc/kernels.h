@@ -225,25 +225,29 @@ cudaError_t run_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v
                          void* ws, cudaStream_t st);
 
 // ---- many adapters, few rows (lora_few.cu) ----------------------------------------------
-// y = x W'^T + s_a U . B_a for M rows, 64 at a time.
+// run_few: y = x W'^T + s_a U . B_a for 64 rows at most; run_few_bwd:
+// dX = dY W' + mask . s_a G . A_a for 32 at most.
 constexpr int kFewUnits = 256;  // CTAs of a launch at most
 struct FewArgs {
   const uint8_t* codes;
   const float* absmax;
-  const uint16_t* x;
+  const uint16_t* x;     // x [M, K], or dY [M, N]
   int M, N, K;
-  const float* P;        // U [M, 16]
-  const void* F;         // B of adapter a at a * stride, [N, 16]
+  const float* P;        // U, or G [M, 16]
+  const void* F;         // B [N, 16], or A [16, K], of adapter a at a * stride
   int64_t stride;
   const float* scale;
   const int32_t* row;    // adapter of each row, < 0: none
-  uint16_t* y;
+  void* y;               // y [M, N] bf16, or dX [M, K]
+  const uint32_t* mask;  // of dX's adapter term, or NULL
+  int out_f32, accumulate;  // of dX
   float* partial;        // [kFewUnits][64][128] fp32 partial sums of cut tiles
   uint32_t* flags;       // [kFewUnits], zeroed by the kernel before this one
-  int blocks, chunks, steps, base, extra;  // set by run_few
+  int steps, base, extra;  // set by the launch
 };
 cudaError_t few_read_and_clear_dev_error(uint32_t* flags);
 cudaError_t run_few(const FewArgs& a, bool f16, cudaStream_t st);
+cudaError_t run_few_bwd(const FewArgs& a, cudaStream_t st);
 
 // ---- one LoRA linear (linear.cu) --------------------------------------------------------
 size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K);

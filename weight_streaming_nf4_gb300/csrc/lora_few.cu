@@ -1,5 +1,6 @@
-// lora_few.cu -- forward of the many-adapter NF4 linear for few rows (decode):
-// y = x W'^T + the adapter term, up to 64 rows at a time.
+// lora_few.cu -- the many-adapter NF4 linear for few rows: y = x W'^T + the
+// adapter term, up to 64 rows at a time (decode), and the input gradient
+// dX = dY W' + the adapter term, up to 32.
 //
 // Bound by decoding the codes (about three integer instructions a weight, on a
 // pipe of 64 lanes an SM), then by reading them.  The dequant GEMM's tile has
@@ -67,7 +68,11 @@ WS_DEVINL void tmem_ld_x4(uint32_t taddr, uint32_t (&r)[4]) {
                : "memory");
 }
 
-template <int NX, bool F16>
+// BWD: the input gradient.  The tile is 128 columns k of W', the contraction
+// runs over its rows n, x is dY and y is dX; a thread decodes one 64-weight
+// block of one row per step, 64 consecutive columns of the operand, which keeps
+// W's own orientation (MN-major).  F is A [16, K], fp32.
+template <int NX, bool BWD, bool F16>
 __global__ void __launch_bounds__(kFewThreads, 1)
     k_few(const __grid_constant__ CUtensorMap tmX, const FewArgs a) {
   using C = Cfg<NX>;
@@ -89,10 +94,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const int pb = u * a.base + min(u, a.extra), n_all = a.base + (u < a.extra ? 1 : 0);
   const int tile0 = (int)((uint32_t)pb / (uint32_t)S), step0 = pb - tile0 * S;
 
-  // Codes of the thread's weight row r and 64-weight block t (four lanes read
-  // a 128-byte line), two steps in registers and two more on their way to L2;
-  // the first are asked for before anything is set up.
-  const int r = (int)threadIdx.x >> 2, t = (int)threadIdx.x & 3;
+  // Codes of the thread's 64-weight block, two steps in registers and two more
+  // on their way to L2; the first are asked for before anything is set up.
+  // Forward: weight row r of the tile, block t of the step (four lanes read a
+  // 128-byte line).  BWD: weight row r of the step, block t of the tile.
+  const int r = BWD ? (int)threadIdx.x & 255 : (int)threadIdx.x >> 2;
+  const int t = BWD ? (int)threadIdx.x >> 8 : (int)threadIdx.x & 3;
+  const int NO = BWD ? a.K : a.N;  // output columns
   struct Codes {
     uint2 w[4];
     float s;
@@ -102,23 +110,33 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const uint8_t* cp = a.codes;
   const float* sp = a.absmax;
   auto seek = [&]() {
-    // rows past the last repeat it: their sums are not stored
-    const int n = min(lt % a.blocks * kRows + r, a.N - 1);
-    cp = a.codes + n * kb + (int64_t)ls * 128 + t * 32;
-    sp = a.absmax + ((int64_t)ls * 4 + t) * a.N + n;
+    if constexpr (BWD) {
+      // blocks past the last column repeat it: their sums are not stored
+      const int kblk = min(lt * 2 + t, a.K / 64 - 1);
+      const int64_t n = (int64_t)ls * 256 + r;
+      cp = a.codes + n * kb + kblk * 32;
+      sp = a.absmax + (int64_t)kblk * a.N + n;
+    } else {
+      // rows past the last repeat it: their sums are not stored
+      const int n = min(lt * kRows + r, a.N - 1);
+      cp = a.codes + n * kb + (int64_t)ls * 128 + t * 32;
+      sp = a.absmax + ((int64_t)ls * 4 + t) * a.N + n;
+    }
   };
+  const int64_t cp_step = BWD ? 256 * kb : 128, sp_step = BWD ? 256 : (int64_t)4 * a.N;
+  // blocks of step s that exist: the last step may end inside it
+  auto inside = [&](int s) { return BWD ? s * 256 + r < a.N : s * 256 + t * 64 < a.K; };
   auto load = [&](Codes& f) {
     if (left <= 0) return;
-    // the last step may end inside its four blocks: blocks past the end take
-    // codes that exist and a scale of 0
-    const bool in = ls * 256 + t * 64 < a.K;
+    // blocks past the end take codes that exist and a scale of 0
+    const bool in = inside(ls);
     const uint2* c = reinterpret_cast<const uint2*>(in ? cp : a.codes);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f.w[i] = __ldg(c + ((i + t) & 3));
+    for (int i = 0; i < 4; ++i) f.w[i] = __ldg(c + (BWD ? i : ((i + t) & 3)));
     f.s = in ? __ldg(sp) : 0.0f;
-    if (left > 2 && ls + 2 < S && (ls + 2) * 256 + t * 64 < a.K) {
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(cp + 256));
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(sp + (int64_t)8 * a.N));
+    if (left > 2 && ls + 2 < S && inside(ls + 2)) {
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(cp + 2 * cp_step));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(sp + 2 * sp_step));
     }
     --left;
     if (++ls == S) {
@@ -126,8 +144,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       ++lt;
       seek();
     } else {
-      cp += 128;
-      sp += (int64_t)4 * a.N;
+      cp += cp_step;
+      sp += sp_step;
     }
   };
   Codes f0{}, f1{};
@@ -167,8 +185,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     // in uniform registers (issued from a single-lane branch, a step's sixteen
     // products took 2000 cycles to issue, as long as decoding it).
     const bool leader = elect_one();
-    constexpr uint32_t idesc = idesc_bf16_f32(kRows, NX, 0u);
-    const uint64_t ad0 = smem_desc_sw128(smem_u32(smem + C::OFF_A), 16, 1024);
+    // (bit 15: the weights' operand is MN-major)
+    constexpr uint32_t idesc = idesc_bf16_f32(kRows, NX, 0u) | (BWD ? 1u << 15 : 0u);
+    // Forward: four 64-deep sub-tiles of 128 rows.  BWD: 8 rows n of a 64-column
+    // group make 1024 bytes, the two column groups lie 1024 apart and 8-row
+    // groups 2048, so a 16-deep slice is 4096 bytes on.
+    const uint64_t ad0 = BWD ? smem_desc_sw128(smem_u32(smem + C::OFF_A), 1024, 2048)
+                             : smem_desc_sw128(smem_u32(smem + C::OFF_A), 16, 1024);
     const uint64_t bd0 = smem_desc_sw128(smem_u32(smem + C::OFF_X), 16, 1024);
     int step = step0, xs = 0;
     uint32_t pieces = 0, xph = 0;
@@ -191,8 +214,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         for (int t = 0; t < 4; ++t)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc_mma_f16(tmem, ad + (uint64_t)(t * 1024 + 2 * k), bd + (uint64_t)(t * NX * 8 + 2 * k), idesc,
-                       (t > 0 || k > 0 || !first) ? 1u : 0u);
+            tc_mma_f16(tmem, ad + (uint64_t)(BWD ? (t * 4 + k) * 256 : t * 1024 + 2 * k),
+                       bd + (uint64_t)(t * NX * 8 + 2 * k), idesc, (t > 0 || k > 0 || !first) ? 1u : 0u);
         tc_commit(&empty[s]);
         tc_commit(&xempty[xs]);
         if (end) tc_commit(acc_done);
@@ -222,7 +245,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     // ------------------------------------------------------------ x
     if (lane == 0) {
       tma_prefetch_desc(&tmX);
-      int tile = tile0, step = step0, xs = 0;
+      int step = step0, xs = 0;
       uint32_t ph = 1;
       for (int q = 0; q < n_it; ++q) {
         if (*abort_flag || !mbar_wait(&xempty[xs], ph, DERR_TIMEOUT_EMPTY)) {
@@ -232,16 +255,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         mbar_arrive_expect_tx(&xfull[xs], C::X_BYTES);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-          tma_load_2d(smem + C::OFF_X + xs * C::X_BYTES + t * (NX * 128), &tmX, &xfull[xs], step * 256 + t * 64,
-                      tile / a.blocks * NX);
+          tma_load_2d(smem + C::OFF_X + xs * C::X_BYTES + t * (NX * 128), &tmX, &xfull[xs], step * 256 + t * 64, 0);
         if (++xs == C::XS) {
           xs = 0;
           ph ^= 1u;
         }
-        if (++step == S) {
-          step = 0;
-          ++tile;
-        }
+        if (++step == S) step = 0;
       }
       if (*abort_flag) {  // copies in flight land first
         const uint64_t t0 = globaltimer();
@@ -253,13 +272,15 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     pdl_launch_dependents();
   } else {
     // ------------------------------------------------------------ decode and epilogue
-    // A thread takes its eight 8-weight words from word 2t on, so that the
-    // eight lanes of a quarter warp (two rows, four blocks) store to eight
-    // different 16-byte places of the swizzle.
+    // Forward: a thread takes its eight 8-weight words from word 2t on, so that
+    // the eight lanes of a quarter warp (two rows, four blocks) store to eight
+    // different 16-byte places of the swizzle.  BWD: they are eight rows.
     uint32_t dst[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      dst[i] = smem_u32(smem + C::OFF_A) + (uint32_t)(t * 16384 + r * 128 + ((((i + 2 * t) & 7) ^ (r & 7)) << 4));
+      dst[i] = smem_u32(smem + C::OFF_A) +
+               (BWD ? (uint32_t)((r >> 3) * 2048 + t * 1024 + (r & 7) * 128 + ((i ^ (r & 7)) << 4))
+                    : (uint32_t)(t * 16384 + r * 128 + ((((i + 2 * t) & 7) ^ (r & 7)) << 4)));
     auto decode = [&](const Codes& f, int s) {
       const Nf4Table tb = make_table(f.s);
 #pragma unroll
@@ -288,8 +309,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         waited = true;
       }
       const int q4 = warp & 3, c0 = warp / 4 * C::CPW;  // lanes (weight rows) and columns of this warp
-      const int nl = q4 * 32 + lane, n = tile % a.blocks * kRows + nl;
-      const int m0 = tile / a.blocks * NX + c0;
+      const int nl = q4 * 32 + lane, n = tile * kRows + nl;
       int last = u;  // CTA that holds the tile's last step
       if (head && !tail) {
         const int i = (tile + 1) * S - 1, cut = a.extra * (a.base + 1);
@@ -341,17 +361,20 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         int ad[4];
         float d[4] = {};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ad[e] = m0 + cc + e < a.M && n < a.N ? a.row[m0 + cc + e] : -1;
+        for (int e = 0; e < 4; ++e) ad[e] = c0 + cc + e < a.M && n < NO ? a.row[c0 + cc + e] : -1;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if (ad[e] < 0) continue;
-          const float4* up = reinterpret_cast<const float4*>(a.P + (int64_t)(m0 + cc + e) * 16);
-          const int64_t o = ad[e] * a.stride + (int64_t)n * 16;
+          const float4* up = reinterpret_cast<const float4*>(a.P + (int64_t)(c0 + cc + e) * 16);
+          const int64_t o = ad[e] * a.stride + (BWD ? (int64_t)n : (int64_t)n * 16);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float4 x = up[j];
             float b[4];
-            if constexpr (F16) {
+            if constexpr (BWD) {
+              const float* f = static_cast<const float*>(a.F) + o + (int64_t)(4 * j) * a.K;
+              b[0] = f[0], b[1] = f[a.K], b[2] = f[2 * (int64_t)a.K], b[3] = f[3 * (int64_t)a.K];
+            } else if constexpr (F16) {
               const uint2 f = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.F) + o)[j];
               b[0] = bf16_lo(f.x), b[1] = bf16_hi(f.x), b[2] = bf16_lo(f.y), b[3] = bf16_hi(f.y);
             } else {
@@ -362,11 +385,24 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             d[e] = fmaf(x.z, b[2], d[e]), d[e] = fmaf(x.w, b[3], d[e]);
           }
           d[e] *= a.scale[ad[e]];
+          if (BWD && a.mask) {
+            const int64_t at = (int64_t)(c0 + cc + e) * a.K + n;
+            if (!((a.mask[at >> 5] >> (at & 31)) & 1u)) ad[e] = -1;  // dropped here
+          }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (ok && m0 + cc + e < a.M && n < a.N)
-            a.y[(int64_t)(m0 + cc + e) * a.N + n] = f32_to_bf16_bits(ad[e] >= 0 ? v[e] + d[e] : v[e]);
+        for (int e = 0; e < 4; ++e) {
+          if (!ok || c0 + cc + e >= a.M || n >= NO) continue;
+          const int64_t at = (int64_t)(c0 + cc + e) * NO + n;
+          float w = ad[e] >= 0 ? v[e] + d[e] : v[e];
+          if (BWD && a.out_f32) {
+            float* o = static_cast<float*>(a.y) + at;
+            if (a.accumulate) w = *o + w;
+            *o = w;
+          } else {
+            static_cast<uint16_t*>(a.y)[at] = f32_to_bf16_bits(w);
+          }
+        }
       }
       if (!head) {
         // every thread's stores, then the flag
@@ -616,7 +652,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, MmaCfg<NT>::CTAS) k_few_mma(co
       v0 = fmaf(s, d0, v0);
       v1 = fmaf(s, d1, v1);
     }
-    *reinterpret_cast<uint32_t*>(a.y + (int64_t)(m0 + m) * a.N + n) = pack_bf16x2(v0, v1);
+    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.y) + (int64_t)(m0 + m) * a.N + n) = pack_bf16x2(v0, v1);
   }
   if (CS > 1) cluster_sync();  // the sums stay until every CTA of the cluster has read them
 }
@@ -657,25 +693,25 @@ cudaError_t launch_mma(const FewArgs& a, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, k, a);
 }
 
-template <int NX, bool F16>
+template <int NX, bool BWD, bool F16>
 cudaError_t launch(FewArgs a, cudaStream_t st) {
   using C = Cfg<NX>;
   static const cudaError_t attr =
-      cudaFuncSetAttribute(k_few<NX, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+      cudaFuncSetAttribute(k_few<NX, BWD, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
   if (attr != cudaSuccess) return attr;
-  a.blocks = (a.N + kRows - 1) / kRows;
-  a.chunks = (a.M + NX - 1) / NX;
-  a.steps = (a.K + 255) / 256;
+  const int kc = BWD ? a.N : a.K, no = BWD ? a.K : a.N;  // contraction, outputs
+  const int blocks = (no + kRows - 1) / kRows;
+  a.steps = (kc + 255) / 256;
   CUtensorMap tm;
-  if (!tmap_bf16_sw128(&tm, a.x, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.K * 2, 64, NX)) return cudaErrorInvalidValue;
-  const int64_t iters = (int64_t)a.blocks * a.chunks * a.steps;
+  if (!tmap_bf16_sw128(&tm, a.x, (uint64_t)kc, (uint64_t)a.M, (uint64_t)kc * 2, 64, NX)) return cudaErrorInvalidValue;
+  const int64_t iters = (int64_t)blocks * a.steps;
   int64_t grid = device_sm_count() < kFewUnits ? device_sm_count() : kFewUnits;
   if (grid > iters) grid = iters;
   if (iters >= (1ll << 31)) return cudaErrorInvalidValue;
   a.base = (int)(iters / grid);
   a.extra = (int)(iters % grid);
   note_launch();
-  return launch_pdl(k_few<NX, F16>, dim3((unsigned)grid), dim3(kFewThreads), C::SMEM, st, tm, a);
+  return launch_pdl(k_few<NX, BWD, F16>, dim3((unsigned)grid), dim3(kFewThreads), C::SMEM, st, tm, a);
 }
 
 }  // namespace
@@ -690,13 +726,18 @@ cudaError_t run_few_t(const FewArgs& a, cudaStream_t st) {
   // k_few / k_few_mma: 896x896 13 / 7 us, 5120x5120 25 / 25 us, 5120x27648 57 /
   // 89 us; 64 rows: 17 / 9, 30 / 37, 63 / 156 us).
   const int64_t steps = (int64_t)((a.N + 127) / 128) * ((a.K + 255) / 256);
-  if (steps >= (a.M <= 32 ? 6 : 4) * device_sm_count()) return a.M <= 32 ? launch<32, F16>(a, st) : launch<64, F16>(a, st);
+  if (steps >= (a.M <= 32 ? 6 : 4) * device_sm_count())
+    return a.M <= 32 ? launch<32, false, F16>(a, st) : launch<64, false, F16>(a, st);
   return a.M <= 32 ? launch_mma<4, F16>(a, st) : launch_mma<8, F16>(a, st);
 }
 }  // namespace
 
 cudaError_t run_few(const FewArgs& a, bool f16, cudaStream_t st) {
   return f16 ? run_few_t<true>(a, st) : run_few_t<false>(a, st);
+}
+
+cudaError_t run_few_bwd(const FewArgs& a, cudaStream_t st) {
+  return launch<32, true, false>(a, st);
 }
 
 }  // namespace ws

@@ -17,7 +17,6 @@ constexpr int kR = 16;            // adapter rank
 constexpr int kTileRows = 64;     // rows of one skinny-product tile
 constexpr int kPlanThreads = 1024;
 
-size_t al16(size_t x) { return (x + 15) & ~size_t(15); }
 size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 bool al16p(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -689,6 +688,11 @@ __global__ void __launch_bounds__(kExThreads)
 #define WS_FEW_ROWS 64
 #endif
 constexpr int kFewRows = WS_FEW_ROWS;  // rows up to which run_few makes the forward
+// ... and run_few_bwd the input gradient: on the tensor-core GEMM the backward of
+// 32 rows takes 21.5 us at 896 x 896 and 109 us at 27648 x 5120, this way 16.5 and
+// 88; of 64 rows 22.8 and 114, this way 24.0 and 101 (weights from DRAM, in a graph).
+constexpr int kFewRowsBwd = 32;
+static_assert(kFewRowsBwd <= kFewRows, "workspace");
 
 struct WsLayout {
   size_t G, ext, bad, base, partial, total;  // bad: words of the GEMM (1) or of run_few (kFewUnits)
@@ -782,6 +786,19 @@ cudaError_t run_expand(K k, const MultiLora& ml, const uint32_t* mask, const ws_
                              kTileRows / kExRows),
                     dim3(kExThreads), 0, st, (const float*)ml.out32, ml.P, ml.F, ml.stride, ml.scale, mask,
                     (const int32_t*)plan.data, L.perm, L.tile, (int)C, accumulate, out);
+}
+
+FewArgs few_args(const ws_nf4* W, const uint16_t* x, const ws_lora_plan& plan, const float* P, const void* F,
+                 int64_t stride, const float* scale, void* y, uint8_t* ws, const WsLayout& L) {
+  FewArgs a{};
+  a.codes = W->codes, a.absmax = W->absmax, a.x = x;
+  a.M = (int)plan.M, a.N = (int)W->N, a.K = (int)W->K;
+  a.P = P, a.F = F, a.stride = stride, a.scale = scale;
+  a.row = static_cast<const int32_t*>(plan.data) + plan_layout(plan.M, plan.n_adapters).row;
+  a.y = y;
+  a.partial = reinterpret_cast<float*>(ws + L.partial);
+  a.flags = reinterpret_cast<uint32_t*>(ws + L.bad);
+  return a;
 }
 
 ws_status check_plan(const ws_lora_plan* p) {
@@ -884,14 +901,7 @@ ws_status ws_lora_linear_fwd_multi(const ws_nf4* W, const uint16_t* x, const ws_
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const bool f16 = set->dtype == WS_DTYPE_BF16;
   if (M <= kFewRows) {
-    FewArgs a{};
-    a.codes = W->codes, a.absmax = W->absmax, a.x = x;
-    a.M = (int)M, a.N = (int)N, a.K = (int)K;
-    a.P = U_saved, a.F = set->B, a.stride = set->stride_b, a.scale = set->scale;
-    a.row = static_cast<const int32_t*>(plan->data) + plan_layout(M, plan->n_adapters).row;
-    a.y = y;
-    a.partial = reinterpret_cast<float*>(ws + L.partial);
-    a.flags = reinterpret_cast<uint32_t*>(ws + L.bad);
+    const FewArgs a = few_args(W, x, *plan, U_saved, set->B, set->stride_b, set->scale, y, ws, L);
     WS_RUN(run_skinny(false, x, set->A, f16, set->stride_a, K, mask, *plan, U_saved, ws, L, false, st));
     WS_RUN(run_few(a, f16, st));
     return WS_OK;
@@ -928,7 +938,7 @@ ws_status ws_lora_linear_bwd_multi(const ws_nf4* W, const uint16_t* x, const ws_
   const int32_t* pl = static_cast<const int32_t*>(plan->data);
   const PlanLayout P = plan_layout(M, plan->n_adapters);
   float* G = reinterpret_cast<float*>(ws + L.G);
-  WS_RUN(run_skinny(true, dY, set->B, false, set->stride_b, N, nullptr, *plan, G, ws, L, true, st));
+  WS_RUN(run_skinny(true, dY, set->B, false, set->stride_b, N, nullptr, *plan, G, ws, L, M > kFewRowsBwd, st));
   WgArgs w{};
   w.P[0] = U_saved, w.P[1] = G;
   w.Q[0] = dY, w.Q[1] = x;
@@ -946,6 +956,14 @@ ws_status ws_lora_linear_bwd_multi(const ws_nf4* W, const uint16_t* x, const ws_
   note_launch();
   WS_RUN(launch_pdl(k_multi_wgrad, dim3((unsigned)((N + 127) / 128 + (K + 127) / 128), (unsigned)set->n_adapters), dim3(kWgWarps * 32),
                     kWgSmem, st, w));
+  if (M <= kFewRowsBwd) {
+    FewArgs a = few_args(W, dY, *plan, G, set->A, set->stride_a, set->scale, dX, ws, L);
+    a.mask = mask;
+    a.out_f32 = dX_dtype == WS_DTYPE_F32 ? 1 : 0;
+    a.accumulate = (accumulate & WS_ACC_DX) ? 1 : 0;
+    WS_RUN(run_few_bwd(a, st));
+    return WS_OK;
+  }
   const MultiLora ml = multi_of(*plan, ws, L, G, set->A, false, set->stride_a, set->scale);
   WS_RUN(run_nf4_gemm_multi(plan_gemm(true, M, K, N), view(W), dY, M, ml, mask, dX, dX_dtype == WS_DTYPE_F32 ? 1 : 0,
                             (accumulate & WS_ACC_DX) ? 1 : 0, reinterpret_cast<float*>(ws + L.partial), st));
