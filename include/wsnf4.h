@@ -332,7 +332,12 @@ ws_status ws_nf4_matmul_noalloc(const ws_nf4* W, const uint16_t* act, int64_t M,
  *   dX[m] = dY[m] W' + mask[m] . scale_a G[m] A_a
  *   dB_a  = scale_a sum_{m of a} dY[m]^T U[m];  dA_a = scale_a sum_{m of a} G[m]^T (mask . x)[m]
  * Adapters lie at a stride, so a pool of adapters' parameter arrays (one
- * ws_stack_param_offset layout after another) serves as it is. */
+ * ws_stack_param_offset layout after another) serves as it is.
+ * 1 <= M <= 2^20; N and K multiples of 64 up to 2^30; M max(N, K) < 2^34.  All
+ * arrays are device memory, 16-byte aligned where no other alignment is named;
+ * what a call writes, its workspace included, overlaps nothing else it is
+ * given.  Calls that may run at the same time need a workspace each; a plan is
+ * only read and may be shared. */
 typedef struct {
   const void* A;       /* adapter a: [r, K] at A + a*stride_a elements (device) */
   const void* B;       /* adapter a: [N, r] at B + a*stride_b elements (device) */
@@ -365,7 +370,8 @@ ws_status ws_lora_multi_plan_size(int64_t M, int32_t n_adapters, size_t* bytes);
 ws_status ws_lora_multi_plan_init(const ws_lora_plan* plan, const int32_t* row_adapter,
                                   ws_stream_t stream);
 
-/* Workspace (device bytes) of ws_lora_linear_fwd_multi / _bwd_multi. */
+/* Workspace (device bytes) of ws_lora_linear_fwd_multi / _bwd_multi; what it
+ * holds before a call does not matter. */
 ws_status ws_lora_multi_workspace_size(int64_t M, int64_t N, int64_t K, int32_t n_adapters,
                                        size_t* bytes);
 /* Forward.  x [M,K] bf16, mask [M,K/32] uint32 or NULL (no dropout), y [M,N]

@@ -464,6 +464,54 @@ def test_another_stream_and_a_captured_call(ops, M):
     assert ops.device_error() == 0
 
 
+def test_memory_of_the_call_s_stream(ops):
+    """Gradients made by a call on another stream come from that stream's memory, not from what the
+    current one has just given back."""
+    c = Case(ops, 9, 128, 256, 3)
+    U = torch.zeros(9, 16, device=dev())
+    st = torch.cuda.Stream()
+    old = [torch.empty(3, 16, 256, device=dev()), torch.empty(3, 128, 16, device=dev())]
+    ptrs = {t.data_ptr() for t in old}
+    del old
+    torch.cuda.synchronize()
+    _, dA, dB = ops.lora_linear_bwd_multi(c.W, c.x, c.set, c.plan, U, c.dY, stream=st)
+    torch.cuda.synchronize()
+    assert not ptrs & {dA.data_ptr(), dB.data_ptr()}
+
+
+def test_more_outputs_than_a_grid_s_second_axis(ops):
+    """2^23 + 64 output rows: 65537 tiles of the weight; checked at both ends and at the 65535th tile."""
+    M, N, K = 2, 2 ** 23 + 64, 64
+    g = torch.Generator(device=dev()).manual_seed(4)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8, device=dev())
+    absmax = 0.02 * (2 + torch.rand(1, N, generator=g, device=dev()))
+    x = torch.randn(M, K, generator=g, device=dev()).bfloat16()
+    A = torch.randn(1, 16, K, generator=g, device=dev()) / 8
+    B = torch.randn(1, N, 16, generator=g, device=dev()) / 8
+    W, aset = ops.NF4Weight(codes, absmax, N, K), ops.LoraSet(A, B, torch.ones(1, device=dev()))
+    plan = ops.lora_multi_plan(torch.zeros(M, dtype=torch.int32, device=dev()), 1)
+    y, U = ops.lora_linear_fwd_multi(W, x, aset, plan)
+    close(U, x.double() @ A[0].double().t(), acc(K) * (x.double().abs() @ A[0].double().abs().t()), "U")
+    for a in (0, 65535 * 128 - 64, N - 128):
+        q = torch.stack([codes[a:a + 128] >> 4, codes[a:a + 128] & 15], -1).view(128, K).long()
+        w = (torch.tensor(LEVELS, device=dev())[q] * absmax[0, a:a + 128, None]).bfloat16().double()
+        b, S = B[0, a:a + 128].double(), x.double().abs() @ w.abs().t()
+        want = x.double() @ w.t() + U.double() @ b.t()
+        close(y[:, a:a + 128], want, 2.0 ** -8 * want.abs() + acc(K) * S + 2.0 ** -14 * (U.double().abs() @ b.abs().t()), "y")
+    assert ops.device_error() == 0
+
+
+def test_a_plan_of_another_device_is_refused(ops):
+    c = Case(ops, 9, 128, 128, 3)
+    elsewhere = ops.LoraPlan(torch.empty_like(c.plan.data, device="cpu"), 9, 3)
+    with pytest.raises(ValueError, match="device"):
+        ops.lora_linear_fwd_multi(c.W, c.x, c.set, elsewhere)
+    with pytest.raises(ValueError, match="device"):
+        ops.lora_linear_bwd_multi(c.W, c.x, c.set, elsewhere, torch.zeros(9, 16, device=dev()), c.dY)
+    with pytest.raises(ValueError, match="device"):
+        ops.lora_multi_plan(c.rows.to(dev()), 3, plan=elsewhere)
+
+
 def test_refusals(ops):
     c = Case(ops, 9, 128, 128, 3)
     f = lambda **k: ops.lora_linear_fwd_multi(k.pop("W", c.W), k.pop("x", c.x), k.pop("s", c.set), k.pop("p", c.plan), **k)

@@ -13,6 +13,13 @@
 // tensor-core products (tcgen05, fp32 sums in tensor memory) of one step while
 // the next is decoded.
 //
+// Measured (weights from DRAM): 48 rows of 48 adapters at 27648 x 5120 take 70
+// us, integer pipe 55%, tensor pipe 13%, 1.5 TB/s; a step takes 1.3 us of which
+// its instructions would fill 0.8 to 1.0, and a tile's epilogue 8 us with one
+// adapter, 12 with 48 (latency of the factors' loads).  Loading the factors of
+// four rows at once, into registers or by cp.async into the idle stages, made the
+// epilogue no faster and cost the decode loop its registers (1.3 -> 1.5 us a step).
+//
 // Schedule: the (tile, step) iterations of the whole problem are cut into equal
 // contiguous ranges, one per CTA, all resident at once.  A tile cut by range
 // ends is finished by the CTA that holds its first steps (its range's last
@@ -719,8 +726,9 @@ cudaError_t launch(FewArgs a, cudaStream_t st) {
 namespace {
 template <bool F16>
 cudaError_t run_few_t(const FewArgs& a, cudaStream_t st) {
-  if (a.M <= 8) return launch_mma<1, F16>(a, st);
-  if (a.M <= 16) return launch_mma<2, F16>(a, st);
+  const bool fits = a.N <= 65535 * kMmaWarps * 16;  // k_few_mma's grid holds that many tiles
+  if (a.M <= 8 && fits) return launch_mma<1, F16>(a, st);
+  if (a.M <= 16 && fits) return launch_mma<2, F16>(a, st);
   // With more rows mma.sync's own rate and its reads of x bind: k_few is ahead
   // once it has several steps for every SM to make good its joins (32 rows,
   // k_few / k_few_mma: 896x896 13 / 7 us, 5120x5120 25 / 25 us, 5120x27648 57 /

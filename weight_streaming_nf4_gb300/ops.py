@@ -516,8 +516,11 @@ class LoraSet:
         self.c = LoraSetC(A.data_ptr(), B.data_ptr(), scale.data_ptr(), sa, sb, n, r,
                           WS_DTYPE_F32 if A.dtype == torch.float32 else WS_DTYPE_BF16)
 
-    def empty_grads(self):
-        """(dA, dB) with the strides of A and B."""
+    def empty_grads(self, stream=None):
+        """(dA, dB) with the strides of A and B, memory of `stream` (or of the current one)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.empty_grads()
         return (torch.empty_strided(self.A.shape, self.A.stride(), dtype=torch.float32, device=self.A.device),
                 torch.empty_strided(self.B.shape, self.B.stride(), dtype=torch.float32, device=self.B.device))
 
@@ -540,6 +543,7 @@ def lora_multi_plan(row_adapter, n_adapters: int, plan: LoraPlan = None, stream=
         _check("ws_lora_multi_plan_size", _lib.ws_lora_multi_plan_size(M, n_adapters, C.byref(n)))
         plan = LoraPlan(_empty((int(n.value) // 4,), torch.int32, row_adapter.device, stream), M, n_adapters)
     _need(plan.M == M and plan.n == n_adapters, "the plan was made for another M or number of adapters")
+    _need(plan.data.get_device() == row_adapter.get_device(), "the plan lies on row_adapter's device")
     _check("ws_lora_multi_plan_init",
            _lib.ws_lora_multi_plan_init(C.byref(plan.c), _addr(row_adapter), _raw(stream)))
     return plan
@@ -556,6 +560,8 @@ def _multi_checks(W, x, aset, plan, mask):
     _need(isinstance(W, NF4Weight), "the base must be an NF4Weight")
     _need(aset.N == W.N and aset.K == W.K, "the adapters' shapes are not the weight's")
     _need(plan.n == aset.n, "the plan was made for another number of adapters")
+    d = x.get_device()
+    _need(plan.data.get_device() == d and aset.A.get_device() == d, "the plan and the adapters lie on x's device")
     _need(x.dtype == torch.bfloat16 and tuple(x.shape) == (plan.M, W.K), "x: bf16 [M, K] with the plan's M")
     if mask is not None:
         _need(mask.dtype == torch.int32 and tuple(mask.shape) == (plan.M, W.K // 32), "mask: int32 [M, K/32]")
@@ -600,7 +606,7 @@ def lora_linear_bwd_multi(W: NF4Weight, x, aset: LoraSet, plan: LoraPlan, U, dY,
         dX = _empty((M, W.K), torch.float32 if dX_f32 else torch.bfloat16, x.device, stream)
     _need(tuple(dX.shape) == (M, W.K) and dX.dtype in (torch.float32, torch.bfloat16), "dX: fp32 or bf16 [M, K]")
     if dA is None or dB is None:
-        gA, gB = aset.empty_grads()
+        gA, gB = aset.empty_grads(stream)
         dA, dB = gA if dA is None else dA, gB if dB is None else dB
     for g, p in ((dA, aset.A), (dB, aset.B)):
         _need(g.dtype == torch.float32 and g.shape == p.shape and _slices_ok(g)
