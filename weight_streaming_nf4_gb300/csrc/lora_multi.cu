@@ -316,11 +316,16 @@ __global__ void __launch_bounds__(kSkWarps * 32)
     const int step = kSkWarps * CS;
     int st = rank * kSkWarps + warp;
     const int end = C / 64;
-    // Tiles of more than 16 rows ask for the 128-byte lines of two steps ahead, a
-    // lane for its two rows (333 rows of 27648: 23 us instead of 26; 2048 rows of
-    // 5120: 15 instead of 16.4).  Two 16-row parts in registers gave no more.
+    // Ahead of the registers, which hold one step of the factor and 16 rows: the
+    // lines of two steps ahead are asked for, and of tiles of more than 16 rows
+    // those rows', a lane for its two (333 rows of 27648: 21 us; 23 without the
+    // factor's, 26 with neither; two 16-row parts in registers gave no more).
     int64_t po[2] = {-1, -1};
     auto ask = [&](int s) {
+      // the factor's lines: 32 in fp32 (two for each of 16 rows, or all of [64, 16]), 16 in bf16
+      const int64_t at = F_CJ ? (int64_t)s * 64 * kR + lane * 32
+                              : (F16 ? (int64_t)(lane & 15) * C + s * 64 : (int64_t)(lane >> 1) * C + s * 64 + (lane & 1) * 32);
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(Fv) + (tile.x * strideF + at) * (F16 ? 2 : 4)));
 #pragma unroll
       for (int h = 0; h < NS / 2; ++h)
         if (po[h] >= 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(X + po[h] + s * 64));
