@@ -2,23 +2,27 @@
 // adapter term, up to 64 rows at a time (decode), and the input gradient
 // dX = dY W' + the adapter term, up to 32.
 //
-// Bound by decoding the codes (about three integer instructions a weight, on a
+// Bound by decoding the codes (about 3.5 integer instructions a weight, on a
 // pipe of 64 lanes an SM), then by reading them.  The dequant GEMM's tile has
 // the activation rows as the 128-row operand and hands over 64-deep steps; with
 // few rows its time is that handshake.  Here the WEIGHT rows are the 128-row
 // operand and the rows of x the N-wide one (32 or 64), and a step is 256
 // deep: sixteen warps decode 128 x 256 weights, each thread one 64-weight block
-// (one value table for 64 weights), straight into the 128-byte swizzled operand
-// layout, then hand over once; one thread loads x by TMA and issues the
-// tensor-core products (tcgen05, fp32 sums in tensor memory) of one step while
-// the next is decoded.
+// (one value table for 64 weights), then hand over once; one thread loads x by
+// TMA and one issues the tensor-core products (tcgen05, fp32 sums in tensor
+// memory) of one step while the next is decoded.
 //
-// Measured (weights from DRAM): 48 rows of 48 adapters at 27648 x 5120 take 70
-// us, integer pipe 55%, tensor pipe 13%, 1.5 TB/s; a step takes 1.3 us of which
-// its instructions would fill 0.8 to 1.0, and a tile's epilogue 8 us with one
-// adapter, 12 with 48 (latency of the factors' loads).  Loading the factors of
-// four rows at once, into registers or by cp.async into the idle stages, made the
-// epilogue no faster and cost the decode loop its registers (1.3 -> 1.5 us a step).
+// Forward: the weights go from registers into tensor memory, a row a lane, as
+// the products' first operand (through shared memory a step takes as long).  The
+// shared memory that is left holds the factors of the tile's rows (4 KB a row in
+// bf16), brought by bulk copies while the tile's steps run; read from L2 in the
+// epilogue, 48 rows of 48 adapters at 27648 x 5120 took 74 us, this way 64.  The
+// input gradient wants the weights' columns as its rows: they go through shared
+// memory, which keeps their orientation.
+//
+// Measured (weights from DRAM): 48 rows of 48 adapters at 27648 x 5120 take 64
+// us with the kernel before it; a step takes 1.2 us, 0.93 of them the integer
+// pipe's (counted: 224 instructions a thread).
 //
 // Schedule: the (tile, step) iterations of the whole problem are cut into equal
 // contiguous ranges, one per CTA, all resident at once.  A tile cut by range
@@ -50,18 +54,42 @@ constexpr int kFewThreads = kDecThreads + 64;  // and a warp for the products, o
 constexpr int kRows = 128;              // weight rows of a tile
 constexpr uint32_t kABytes = 4 * 16384; // a step's operand: four 64-deep sub-tiles of 128 rows
 
-template <int NX>
+template <int NX, bool BWD, bool F16>
 struct Cfg {
   static constexpr uint32_t X_BYTES = NX * 512;  // a step of x: four sub-tiles of NX rows
   static constexpr int XS = NX == 64 ? 3 : 4;    // steps of x in flight
-  static constexpr uint32_t OFF_A = 0, OFF_X = 2 * kABytes, OFF_BAR = OFF_X + XS * X_BYTES;
+  // The adapters' factors of a tile (forward): slots of one row of x each, 16
+  // values for each of 128 outputs; RP slots for each of the four groups of CPW
+  // rows that share an epilogue warp.
+  static constexpr int RP = F16 ? 8 : 4;
+  static constexpr uint32_t ROW_BYTES = kRows * 16 * (F16 ? 2 : 4);
+  static constexpr uint32_t OFF_A = 0, OFF_F = 0, OFF_X = BWD ? 2 * kABytes : 4 * RP * ROW_BYTES,
+                            OFF_BAR = OFF_X + XS * X_BYTES;
   static constexpr uint32_t SMEM = OFF_BAR + 192 + 1024;  // + alignment slack
   static_assert(SMEM <= 227u * 1024u, "shared memory");
-  static constexpr uint32_t TMEM_COLS = NX;
+  // tensor memory: the sums, and in the forward two steps of weights (a row a
+  // lane, two values a column)
+  static constexpr uint32_t COL_A = 128, TMEM_COLS = BWD ? NX : 512;
   static constexpr int CPW = NX / 4;             // accumulator columns (rows of x) of one epilogue warp
   static_assert(NX == 32 || NX == 64, "rows of x");
 };
 
+// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16 (bf16 in, fp32 sums).
+WS_DEVINL void tc_mma_f16_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+WS_DEVINL float4 lds128f(uint32_t a) {
+  float4 r;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
+               : "r"(a)
+               : "memory");
+  return r;
+}
 // True in one lane of a converged warp.
 WS_DEVINL bool elect_one() {
   uint32_t p;
@@ -82,7 +110,7 @@ WS_DEVINL void tmem_ld_x4(uint32_t taddr, uint32_t (&r)[4]) {
 template <int NX, bool BWD, bool F16>
 __global__ void __launch_bounds__(kFewThreads, 1)
     k_few(const __grid_constant__ CUtensorMap tmX, const FewArgs a) {
-  using C = Cfg<NX>;
+  using C = Cfg<NX, BWD, F16>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [2] a step's weights are there
@@ -91,7 +119,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   uint64_t* xempty = xfull + C::XS;
   uint64_t* acc_done = xempty + C::XS;                              // a piece's sums are complete
   uint64_t* acc_free = acc_done + 1;                                // ... and have been read
-  uint32_t* misc = reinterpret_cast<uint32_t*>(acc_free + 1);
+  uint64_t* fac = acc_free + 1;                                     // factors have landed
+  uint32_t* misc = reinterpret_cast<uint32_t*>(fac + 1);
   volatile uint32_t* abort_flag = misc + 1;
   volatile uint32_t* got_flag = misc + 2;
   // (the shuffle tells the compiler that a warp's index is one value)
@@ -103,13 +132,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
   // Codes of the thread's 64-weight block, two steps in registers and two more
   // on their way to L2; the first are asked for before anything is set up.
-  // Forward: weight row r of the tile, block t of the step (four lanes read a
-  // 128-byte line).  BWD: weight row r of the step, block t of the tile.
-  const int r = BWD ? (int)threadIdx.x & 255 : (int)threadIdx.x >> 2;
-  const int t = BWD ? (int)threadIdx.x >> 8 : (int)threadIdx.x & 3;
+  // Forward: weight row r of the tile (a warp: the 32 lanes of tensor memory
+  // that it may write), block t of the step.  BWD: weight row r of the step,
+  // block t of the tile.
+  const int r = (int)threadIdx.x & (BWD ? 255 : 127);
+  const int t = (int)threadIdx.x >> (BWD ? 8 : 7);
   const int NO = BWD ? a.K : a.N;  // output columns
   struct Codes {
-    uint2 w[4];
+    uint4 w[2];
     float s;
   };
   const int64_t kb = a.K / 2;
@@ -137,9 +167,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     if (left <= 0) return;
     // blocks past the end take codes that exist and a scale of 0
     const bool in = inside(ls);
-    const uint2* c = reinterpret_cast<const uint2*>(in ? cp : a.codes);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f.w[i] = __ldg(c + (BWD ? i : ((i + t) & 3)));
+    const uint4* c = reinterpret_cast<const uint4*>(in ? cp : a.codes);
+    f.w[0] = __ldg(c);
+    f.w[1] = __ldg(c + 1);
     f.s = in ? __ldg(sp) : 0.0f;
     if (left > 2 && ls + 2 < S && inside(ls + 2)) {
       asm volatile("prefetch.global.L2 [%0];" ::"l"(cp + 2 * cp_step));
@@ -173,6 +203,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     }
     mbar_init(acc_done, 1);
     mbar_init(acc_free, kDecWarps);
+    mbar_init(fac, 1);
     fence_barrier_init();
   }
   if (warp == kDecWarps) {
@@ -194,11 +225,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const bool leader = elect_one();
     // (bit 15: the weights' operand is MN-major)
     constexpr uint32_t idesc = idesc_bf16_f32(kRows, NX, 0u) | (BWD ? 1u << 15 : 0u);
-    // Forward: four 64-deep sub-tiles of 128 rows.  BWD: 8 rows n of a 64-column
-    // group make 1024 bytes, the two column groups lie 1024 apart and 8-row
-    // groups 2048, so a 16-deep slice is 4096 bytes on.
-    const uint64_t ad0 = BWD ? smem_desc_sw128(smem_u32(smem + C::OFF_A), 1024, 2048)
-                             : smem_desc_sw128(smem_u32(smem + C::OFF_A), 16, 1024);
+    // BWD: 8 rows n of a 64-column group make 1024 bytes, the two column groups
+    // lie 1024 apart and 8-row groups 2048, so a 16-deep slice is 4096 bytes on.
+    const uint64_t ad0 = smem_desc_sw128(smem_u32(smem + C::OFF_A), 1024, 2048);
     const uint64_t bd0 = smem_desc_sw128(smem_u32(smem + C::OFF_X), 16, 1024);
     int step = step0, xs = 0;
     uint32_t pieces = 0, xph = 0;
@@ -220,9 +249,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma_f16(tmem, ad + (uint64_t)(BWD ? (t * 4 + k) * 256 : t * 1024 + 2 * k),
-                       bd + (uint64_t)(t * NX * 8 + 2 * k), idesc, (t > 0 || k > 0 || !first) ? 1u : 0u);
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t b = bd + (uint64_t)(t * NX * 8 + 2 * k);
+            const uint32_t more = (t > 0 || k > 0 || !first) ? 1u : 0u;
+            if constexpr (BWD) tc_mma_f16(tmem, ad + (uint64_t)((t * 4 + k) * 256), b, idesc, more);
+            else tc_mma_f16_ta(tmem, tmem + C::COL_A + (uint32_t)(s * 128 + (t * 4 + k) * 8), b, idesc, more);
+          }
         tc_commit(&empty[s]);
         tc_commit(&xempty[xs]);
         if (end) tc_commit(acc_done);
@@ -279,25 +311,40 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     pdl_launch_dependents();
   } else {
     // ------------------------------------------------------------ decode and epilogue
-    // Forward: a thread takes its eight 8-weight words from word 2t on, so that
-    // the eight lanes of a quarter warp (two rows, four blocks) store to eight
-    // different 16-byte places of the swizzle.  BWD: they are eight rows.
+    // BWD: the eight lanes of a quarter warp are eight rows, which the swizzle
+    // keeps apart.
     uint32_t dst[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       dst[i] = smem_u32(smem + C::OFF_A) +
-               (BWD ? (uint32_t)((r >> 3) * 2048 + t * 1024 + (r & 7) * 128 + ((i ^ (r & 7)) << 4))
-                    : (uint32_t)(t * 16384 + r * 128 + ((((i + 2 * t) & 7) ^ (r & 7)) << 4)));
+               (uint32_t)((r >> 3) * 2048 + t * 1024 + (r & 7) * 128 + ((i ^ (r & 7)) << 4));
+    const uint32_t ta = tmem + ((uint32_t)(r & ~31) << 16) + C::COL_A + (uint32_t)t * 32;
     auto decode = [&](const Codes& f, int s) {
       const Nf4Table tb = make_table(f.s);
+      const uint32_t w[8] = {f.w[0].x, f.w[0].y, f.w[0].z, f.w[0].w, f.w[1].x, f.w[1].y, f.w[1].z, f.w[1].w};
+      if constexpr (BWD) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint4 v = dq8((i & 1) ? f.w[i / 2].y : f.w[i / 2].x, tb);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst[i] + (uint32_t)s * kABytes), "r"(v.x),
-                     "r"(v.y), "r"(v.z), "r"(v.w)
-                     : "memory");
+        for (int i = 0; i < 8; ++i) {
+          const uint4 v = dq8(w[i], tb);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst[i] + (uint32_t)s * kABytes), "r"(v.x),
+                       "r"(v.y), "r"(v.z), "r"(v.w)
+                       : "memory");
+        }
+        fence_proxy_async_smem();
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 d = dq8(w[4 * h + i], tb);
+            v[4 * i] = d.x, v[4 * i + 1] = d.y, v[4 * i + 2] = d.z, v[4 * i + 3] = d.w;
+          }
+          tmem_st_32x32b_x16(ta + (uint32_t)(s * 128 + h * 16), v);
+        }
+        tmem_st_wait();
+        tc_fence_before();
       }
-      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[s]);
     };
@@ -305,7 +352,33 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     uint32_t piece = 0;
     // The piece that ends with iteration q: tile `tile`, whether it holds the
     // tile's first and its last step.
+    int q = 0;            // iterations made
+    uint32_t fac_ph = 0;
+    // One warp: the factors of the p-th RP rows of every group, for tile `tile`.
+    // The plan and the adapters are older than the kernel before this one.
+    auto ask = [&](int tile, int p) {
+      if constexpr (!BWD) {
+        constexpr int EB = F16 ? 2 : 4;
+        const int n0 = tile * kRows, m = lane / C::RP * C::CPW + p * C::RP + lane % C::RP;
+        const uint32_t bytes = (uint32_t)min(kRows, a.N - n0) * 16 * EB;
+        const int ad = lane < 4 * C::RP && m < a.M ? a.row[m] : -1;
+        const uint32_t some = __ballot_sync(0xffffffffu, ad >= 0);
+        if (lane == 0) mbar_arrive_expect_tx(fac, (uint32_t)__popc(some) * bytes);
+        __syncwarp();
+        if (ad >= 0)
+          bulk_load(smem + C::OFF_F + lane * C::ROW_BYTES,
+                    static_cast<const uint8_t*>(a.F) + (ad * a.stride + (int64_t)n0 * 16) * EB, bytes, fac);
+      }
+    };
     auto epilogue = [&](int tile, bool head, bool tail) {
+      const int q4 = warp & 3, c0 = warp / 4 * C::CPW;  // lanes (weight rows) and columns of this warp
+      const int nl = q4 * 32 + lane, n = tile * kRows + nl;
+      int row_ad = -1;     // of the warp's rows, a lane each
+      float row_sc = 0.0f;
+      if (!BWD && head) {
+        if (lane < C::CPW && c0 + lane < a.M) row_ad = a.row[c0 + lane];
+        row_sc = a.scale[max(row_ad, 0)];
+      }
       const bool ok = !*abort_flag && mbar_wait(acc_done, piece & 1u, DERR_TIMEOUT_ACC);
       ++piece;
       if (!ok) *abort_flag = 1u;
@@ -315,8 +388,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         pdl_launch_dependents();
         waited = true;
       }
-      const int q4 = warp & 3, c0 = warp / 4 * C::CPW;  // lanes (weight rows) and columns of this warp
-      const int nl = q4 * 32 + lane, n = tile * kRows + nl;
+      if (!BWD && head && lane < C::CPW / 2 && c0 + 2 * lane < a.M)  // P's rows, to L1
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(a.P + (int64_t)(c0 + 2 * lane) * 16));
       int last = u;  // CTA that holds the tile's last step
       if (head && !tail) {
         const int i = (tile + 1) * S - 1, cut = a.extra * (a.base + 1);
@@ -332,7 +405,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         named_bar_sync(1, kDecThreads);
         if (*got_flag == 0u) last = u;
       }
-#pragma unroll
+#pragma unroll(BWD ? 2 : 1)
       for (int cc = 0; cc < C::CPW; cc += 4) {
         uint32_t raw[4];
         tmem_ld_x4(tmem + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(c0 + cc), raw);
@@ -365,43 +438,82 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] += x[i][e];
         }
-        int ad[4];
-        float d[4] = {};
+        float d[4];
+        if constexpr (BWD) {
+          int ad[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ad[e] = c0 + cc + e < a.M && n < NO ? a.row[c0 + cc + e] : -1;
+          for (int e = 0; e < 4; ++e) ad[e] = c0 + cc + e < a.M && n < NO ? a.row[c0 + cc + e] : -1;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (ad[e] < 0) continue;
-          const float4* up = reinterpret_cast<const float4*>(a.P + (int64_t)(c0 + cc + e) * 16);
-          const int64_t o = ad[e] * a.stride + (BWD ? (int64_t)n : (int64_t)n * 16);
+          for (int e = 0; e < 4; ++e) {
+            d[e] = -0.0f;  // changes no sum
+            if (ad[e] < 0) continue;
+            const float4* up = reinterpret_cast<const float4*>(a.P + (int64_t)(c0 + cc + e) * 16);
+            const int64_t o = ad[e] * a.stride + n;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4 x = up[j];
-            float b[4];
-            if constexpr (BWD) {
+            for (int j = 0; j < 4; ++j) {
+              const float4 x = up[j];
+              float b[4];
               const float* f = static_cast<const float*>(a.F) + o + (int64_t)(4 * j) * a.K;
               b[0] = f[0], b[1] = f[a.K], b[2] = f[2 * (int64_t)a.K], b[3] = f[3 * (int64_t)a.K];
-            } else if constexpr (F16) {
-              const uint2 f = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.F) + o)[j];
-              b[0] = bf16_lo(f.x), b[1] = bf16_hi(f.x), b[2] = bf16_lo(f.y), b[3] = bf16_hi(f.y);
-            } else {
-              const float4 f = reinterpret_cast<const float4*>(static_cast<const float*>(a.F) + o)[j];
-              b[0] = f.x, b[1] = f.y, b[2] = f.z, b[3] = f.w;
+              d[e] = fmaf(x.x, b[0], d[e]), d[e] = fmaf(x.y, b[1], d[e]);
+              d[e] = fmaf(x.z, b[2], d[e]), d[e] = fmaf(x.w, b[3], d[e]);
             }
-            d[e] = fmaf(x.x, b[0], d[e]), d[e] = fmaf(x.y, b[1], d[e]);
-            d[e] = fmaf(x.z, b[2], d[e]), d[e] = fmaf(x.w, b[3], d[e]);
+            d[e] *= a.scale[ad[e]];
+            if (a.mask) {
+              const int64_t at = (int64_t)(c0 + cc + e) * a.K + n;
+              if (!((a.mask[at >> 5] >> (at & 31)) & 1u)) d[e] = -0.0f;  // dropped here
+            }
           }
-          d[e] *= a.scale[ad[e]];
-          if (BWD && a.mask) {
-            const int64_t at = (int64_t)(c0 + cc + e) * a.K + n;
-            if (!((a.mask[at >> 5] >> (at & 31)) & 1u)) ad[e] = -1;  // dropped here
+        } else {
+          if (cc % C::RP == 0) {
+            if (!*abort_flag && !mbar_wait(fac, fac_ph, DERR_TIMEOUT_FULL)) *abort_flag = 1u;
+            fac_ph ^= 1u;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            d[e] = 0.0f;
+            const uint32_t f = smem_u32(smem + C::OFF_F) +
+                               (uint32_t)(warp / 4 * C::RP + cc % C::RP + e) * C::ROW_BYTES + (uint32_t)nl * (F16 ? 32 : 64);
+            const float4* up = reinterpret_cast<const float4*>(a.P + (int64_t)min(c0 + cc + e, a.M - 1) * 16);
+            // the 16-byte parts in an order that sets eight lanes on eight
+            // places of the banks
+            if constexpr (F16) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int j = i ^ ((lane >> 2) & 1);
+                const float4 w = lds128f(f + (uint32_t)j * 16), x = up[2 * j], z = up[2 * j + 1];
+                d[e] = fmaf(x.x, bf16_lo(__float_as_uint(w.x)), d[e]), d[e] = fmaf(x.y, bf16_hi(__float_as_uint(w.x)), d[e]);
+                d[e] = fmaf(x.z, bf16_lo(__float_as_uint(w.y)), d[e]), d[e] = fmaf(x.w, bf16_hi(__float_as_uint(w.y)), d[e]);
+                d[e] = fmaf(z.x, bf16_lo(__float_as_uint(w.z)), d[e]), d[e] = fmaf(z.y, bf16_hi(__float_as_uint(w.z)), d[e]);
+                d[e] = fmaf(z.z, bf16_lo(__float_as_uint(w.w)), d[e]), d[e] = fmaf(z.w, bf16_hi(__float_as_uint(w.w)), d[e]);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int j = (i + (lane >> 1)) & 3;
+                const float4 w = lds128f(f + (uint32_t)j * 16), x = up[j];
+                d[e] = fmaf(x.x, w.x, d[e]), d[e] = fmaf(x.y, w.y, d[e]);
+                d[e] = fmaf(x.z, w.z, d[e]), d[e] = fmaf(x.w, w.w, d[e]);
+              }
+            }
+            d[e] *= __shfl_sync(0xffffffffu, row_sc, cc + e);
+            // -0 changes no sum
+            if (__shfl_sync(0xffffffffu, row_ad, cc + e) < 0) d[e] = -0.0f;
+          }
+          if (cc % C::RP == C::RP - 4) {
+            // the slots have been read: the next rows' factors, or the next tile's
+            named_bar_sync(1, kDecThreads);
+            if (warp == 0 && !*abort_flag) {
+              if (cc + 4 < C::CPW) ask(tile, cc / C::RP + 1);
+              else if (q < n_it) ask(tile + 1, 0);
+            }
           }
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if (!ok || c0 + cc + e >= a.M || n >= NO) continue;
           const int64_t at = (int64_t)(c0 + cc + e) * NO + n;
-          float w = ad[e] >= 0 ? v[e] + d[e] : v[e];
+          float w = v[e] + d[e];
           if (BWD && a.out_f32) {
             float* o = static_cast<float*>(a.y) + at;
             if (a.accumulate) w = *o + w;
@@ -419,26 +531,38 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
     };
 
-    int tile = tile0, step = step0;
-    bool head = step0 == 0;  // of the piece being made
+    // the first tile whose first step this CTA makes
+    if (warp == 0 && (step0 == 0 ? n_it > 0 : n_it > S - step0)) ask(step0 == 0 ? tile0 : tile0 + 1, 0);
     // After a wait has given up, every warp still runs all its iterations,
     // without waiting: the epilogue's barriers count on all of them.
-    auto iter = [&](int q, Codes& f, int s) {
+    auto iter = [&](Codes& f) {
+      const int s = q & 1;
       if (q >= 2 && !*abort_flag && !mbar_wait(&empty[s], (uint32_t)((q >> 1) - 1) & 1u, DERR_TIMEOUT_BEMPTY))
         *abort_flag = 1u;
+      if constexpr (!BWD) {
+        tc_fence_after();  // of the products that read this stage
+        __syncwarp();
+      }
       decode(f, s);
       load(f);  // two steps ahead
-      const bool tail = ++step == S;
-      if (tail || q + 1 == n_it) {
-        epilogue(tile, head, tail);
-        head = true;
-        step = 0;
-        ++tile;
-      }
+      ++q;
     };
-    for (int q = 0; q < n_it; q += 2) {
-      iter(q, f0, 0);
-      if (q + 1 < n_it) iter(q + 1, f1, 1);
+    for (int tile = tile0, step = step0; q < n_it; ++tile, step = 0) {
+      const int len = min(S - step, n_it - q);
+      for (int i = 1; i < len; i += 2) {
+        iter(f0);
+        iter(f1);
+      }
+      if (len & 1) {
+        iter(f0);
+        const Codes f = f0;
+        f0 = f1, f1 = f;
+      }
+      epilogue(tile, step == 0, step + len == S);
+    }
+    if (!BWD && warp == 0 && *abort_flag) {  // copies in flight land first
+      const uint64_t t0 = globaltimer();
+      while (globaltimer() - t0 < 200000ull) __nanosleep(1000);
     }
     if (!waited) {
       pdl_wait();
@@ -702,7 +826,7 @@ cudaError_t launch_mma(const FewArgs& a, cudaStream_t st) {
 
 template <int NX, bool BWD, bool F16>
 cudaError_t launch(FewArgs a, cudaStream_t st) {
-  using C = Cfg<NX>;
+  using C = Cfg<NX, BWD, F16>;
   static const cudaError_t attr =
       cudaFuncSetAttribute(k_few<NX, BWD, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
   if (attr != cudaSuccess) return attr;
@@ -731,10 +855,10 @@ cudaError_t run_few_t(const FewArgs& a, cudaStream_t st) {
   if (a.M <= 16 && fits) return launch_mma<2, F16>(a, st);
   // With more rows mma.sync's own rate and its reads of x bind: k_few is ahead
   // once it has several steps for every SM to make good its joins (32 rows,
-  // k_few / k_few_mma: 896x896 13 / 7 us, 5120x5120 25 / 25 us, 5120x27648 57 /
-  // 89 us; 64 rows: 17 / 9, 30 / 37, 63 / 156 us).
+  // k_few / k_few_mma: 3584x3584 16 / 13 us, 5120x5120 20 / 24 us, 27648x5120
+  // 52 / 62 us; 64 rows: 22 / 20, 25 / 37, 62 / 103 us).
   const int64_t steps = (int64_t)((a.N + 127) / 128) * ((a.K + 255) / 256);
-  if (steps >= (a.M <= 32 ? 6 : 4) * device_sm_count())
+  if (steps >= 4 * device_sm_count())
     return a.M <= 32 ? launch<32, false, F16>(a, st) : launch<64, false, F16>(a, st);
   return a.M <= 32 ? launch_mma<4, F16>(a, st) : launch_mma<8, F16>(a, st);
 }
