@@ -209,6 +209,42 @@ def test_forward_of_large_weights(ops, shape):
     assert ops.device_error() == 0
 
 
+BIG_ROWS = [
+    # rows without an adapter, one row past the narrow form, a tile of 64 outputs at the end, ends inside a step
+    (20, 5184, 5184, 3, "none", False),
+    (32, 9792, 2880, 32, "distinct", True),
+    (33, 5184, 5120, 7, "wild", False),
+    (64, 19456, 1088, 64, "distinct", False),
+    (50, 4928, 8256, 1, "one", True),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", BIG_ROWS, ids=["-".join(map(str, s)) for s in BIG_ROWS])
+def test_forward_of_large_weights_in_both_types(ops, shape, dtype):
+    M, N, K, n, kind, mask = shape
+    c = Case(ops, M, N, K, n, kind, dtype, mask, seed=M + K, pool=24)
+    ws = torch.full((ops.lora_multi_workspace_size(M, N, K, n),), 255, dtype=torch.uint8, device=dev())
+    y = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device=dev())
+    U = torch.full((M, 16), float("nan"), device=dev())
+    for _ in range(2):
+        y.fill_(float("nan"))
+        ops.lora_linear_fwd_multi(c.W, c.x, c.set, c.plan, mask=c.mask, y=y, U=U, workspace=ws)
+        check_forward(c, y, U)
+    assert ops.device_error() == 0
+
+
+def test_a_diverged_adapter_stays_alone_beside_large_weights(ops):
+    """Infinite and NaN factors of one adapter reach its own rows only."""
+    c = Case(ops, 40, 5184, 5120, 5, "distinct", seed=8)
+    want, _ = ops.lora_linear_fwd_multi(c.W, c.x, c.set, c.plan)
+    c.A[2].fill_(float("inf")), c.B[2].fill_(float("nan"))
+    y, U = ops.lora_linear_fwd_multi(c.W, c.x, c.set, c.plan)
+    own = (c.rows == 2).to(dev())
+    assert own.any() and not torch.isfinite(y[own]).any()
+    assert torch.equal(y[~own], want[~own])
+
+
 @pytest.mark.parametrize("dx32", [True, False], ids=["dx32", "dx16"])
 @pytest.mark.parametrize("shape", SHAPES, ids=["-".join(map(str, s)) for s in SHAPES])
 def test_backward(ops, shape, dx32):
