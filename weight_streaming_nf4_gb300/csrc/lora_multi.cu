@@ -710,8 +710,9 @@ __global__ void __launch_bounds__(kExThreads)
 #endif
 constexpr int kFewRows = WS_FEW_ROWS;  // rows up to which run_few makes the forward
 // ... and run_few_bwd the input gradient: on the tensor-core GEMM the backward of
-// 32 rows takes 21.5 us at 896 x 896 and 109 us at 27648 x 5120, this way 16.5 and
-// 88; of 64 rows 22.8 and 114, this way 24.0 and 101 (weights from DRAM, in a graph).
+// 32 rows takes 21.5 us at 896 x 896 and 109 us at 27648 x 5120, this way 16.0 and
+// 76; of 64 rows 22.8 and 114, this way (as first built) 24.0 and 101 (weights
+// from DRAM, in a graph).
 constexpr int kFewRowsBwd = 32;
 static_assert(kFewRowsBwd <= kFewRows, "workspace");
 
