@@ -312,6 +312,8 @@ BIG_FEW = [
     (31, 5184, 4928, 31, "wild", True),
     (32, 4864, 8192, 5, "distinct", False),
     (33, 2112, 4864, 5, "random", True),
+    (33, 9728, 8256, 40, "wild", True),
+    (64, 8256, 9728, 64, "distinct", False),
 ]
 
 

@@ -225,8 +225,8 @@ cudaError_t run_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v
                          void* ws, cudaStream_t st);
 
 // ---- many adapters, few rows (lora_few.cu) ----------------------------------------------
-// run_few: y = x W'^T + s_a U . B_a for 64 rows at most; run_few_bwd:
-// dX = dY W' + mask . s_a G . A_a for 32 at most.
+// run_few: y = x W'^T + s_a U . B_a and run_few_bwd: dX = dY W' +
+// mask . s_a G . A_a, for 64 rows at most.
 constexpr int kFewUnits = 256;  // CTAs of a launch at most
 struct FewArgs {
   const uint8_t* codes;

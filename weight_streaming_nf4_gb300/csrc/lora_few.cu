@@ -1,6 +1,6 @@
 // lora_few.cu -- the many-adapter NF4 linear for few rows: y = x W'^T + the
 // adapter term, up to 64 rows at a time (decode), and the input gradient
-// dX = dY W' + the adapter term, up to 32.
+// dX = dY W' + the adapter term, up to 64.
 //
 // Bound by decoding the codes (about 3.5 integer instructions a weight, on a
 // pipe of 64 lanes an SM), then by reading them.  The dequant GEMM's tile has
@@ -869,7 +869,7 @@ cudaError_t run_few(const FewArgs& a, bool f16, cudaStream_t st) {
 }
 
 cudaError_t run_few_bwd(const FewArgs& a, cudaStream_t st) {
-  return launch<32, true, false>(a, st);
+  return a.M <= 32 ? launch<32, true, false>(a, st) : launch<64, true, false>(a, st);
 }
 
 }  // namespace ws

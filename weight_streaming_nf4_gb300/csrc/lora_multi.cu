@@ -709,12 +709,15 @@ __global__ void __launch_bounds__(kExThreads)
 #define WS_FEW_ROWS 64
 #endif
 constexpr int kFewRows = WS_FEW_ROWS;  // rows up to which run_few makes the forward
-// ... and run_few_bwd the input gradient: on the tensor-core GEMM the backward of
-// 32 rows takes 21.5 us at 896 x 896 and 109 us at 27648 x 5120, this way 16.0 and
-// 76; of 64 rows 22.8 and 114, this way (as first built) 24.0 and 101 (weights
-// from DRAM, in a graph).
-constexpr int kFewRowsBwd = 32;
-static_assert(kFewRowsBwd <= kFewRows, "workspace");
+// Whether run_few_bwd makes the input gradient, and not the tensor-core GEMM: up
+// to 32 rows always (backward of 32 rows, weights from DRAM, in a graph: 16.0 us
+// against 21.5 at 896 x 896, 76 against 109 at 27648 x 5120), up to 64 with eight
+// steps of 128 x 256 weights for every SM (64 rows: 5120 x 5120, 5.3 steps, 42.6
+// against 42.6; 3584 x 18944, 13.6 steps, 59 against 64; 27648 x 5120, 28 steps, 92
+// against 114; 896 x 896 27.6 against 23.0).
+bool few_makes_dx(int64_t M, int64_t N, int64_t K) {
+  return M <= 32 || (M <= kFewRows && (K + 127) / 128 * ((N + 255) / 256) >= 8 * device_sm_count());
+}
 
 struct WsLayout {
   size_t G, ext, bad, base, partial, total;  // bad: words of the GEMM (1) or of run_few (kFewUnits)
@@ -960,7 +963,7 @@ ws_status ws_lora_linear_bwd_multi(const ws_nf4* W, const uint16_t* x, const ws_
   const int32_t* pl = static_cast<const int32_t*>(plan->data);
   const PlanLayout P = plan_layout(M, plan->n_adapters);
   float* G = reinterpret_cast<float*>(ws + L.G);
-  WS_RUN(run_skinny(true, dY, set->B, false, set->stride_b, N, nullptr, *plan, G, ws, L, M > kFewRowsBwd, st));
+  WS_RUN(run_skinny(true, dY, set->B, false, set->stride_b, N, nullptr, *plan, G, ws, L, !few_makes_dx(M, N, K), st));
   WgArgs w{};
   w.P[0] = U_saved, w.P[1] = G;
   w.Q[0] = dY, w.Q[1] = x;
@@ -978,7 +981,7 @@ ws_status ws_lora_linear_bwd_multi(const ws_nf4* W, const uint16_t* x, const ws_
   note_launch();
   WS_RUN(launch_pdl(k_multi_wgrad, dim3((unsigned)((N + 127) / 128 + (K + 127) / 128), (unsigned)set->n_adapters), dim3(kWgWarps * 32),
                     kWgSmem, st, w));
-  if (M <= kFewRowsBwd) {
+  if (few_makes_dx(M, N, K)) {
     FewArgs a = few_args(W, dY, *plan, G, set->A, set->stride_a, set->scale, dX, ws, L);
     a.mask = mask;
     a.out_f32 = dX_dtype == WS_DTYPE_F32 ? 1 : 0;
