@@ -376,6 +376,24 @@ def test_two_streams_at_once(ops):
     assert ops.device_error() == 0
 
 
+def test_two_streams_beside_large_weights(ops):
+    """The same, where tiles are cut between CTAs that wait for one another's sums."""
+    cs = [Case(ops, M, N, K, 6, "random", seed=M) for M, N, K in ((40, 5184, 5120), (20, 9728, 4928), (64, 8256, 9728))]
+    want = [ops.lora_linear_fwd_multi(c.W, c.x, c.set, c.plan) for c in cs]
+    grads = [ops.lora_linear_bwd_multi(c.W, c.x, c.set, c.plan, w[1], c.dY) for c, w in zip(cs, want)]
+    torch.cuda.synchronize()
+    st = [torch.cuda.Stream() for _ in cs]
+    for _ in range(5):
+        got = []
+        for c, s in zip(cs, st):
+            f = ops.lora_linear_fwd_multi(c.W, c.x, c.set, c.plan, stream=s)
+            got.append((*f, *ops.lora_linear_bwd_multi(c.W, c.x, c.set, c.plan, f[1], c.dY, stream=s)))
+        torch.cuda.synchronize()
+        for g, f, b in zip(got, want, grads):
+            assert all(torch.equal(p, q) for p, q in zip(g, (*f, *b)))
+    assert ops.device_error() == 0
+
+
 def test_gradients_against_differences(ops):
     """sum(y . dY) as a function of A, B and x, in 64 bits, differenced."""
     c = Case(ops, 37, 128, 128, 3, "random", mask=True, seed=5)
