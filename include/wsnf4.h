@@ -441,7 +441,7 @@ ws_status ws_attention_bwd(const uint16_t* q, const uint16_t* k, const uint16_t*
  * elements of a tensor (the last may be short) with an fp32 scale each:
  *   m: e4m3 code [n] times m_scale [ceil(n/256)] = max|m| (1/448);
  *   v: code c [n] of sqrt(v): (1 + (c & 15)/16) 2^((c >> 4) - 15), 0 for c = 0,
- *      times v_scale [ceil(n/256)] = max sqrt(v) (1/1.9375); never 0 for v > 0.
+ *      times v_scale [ceil(n/256)] = max sqrt(v) (1/1.9375); c is never 0 for v > 0.
  * Both to nearest (ties to even); the step uses the moments before this
  * rounding.  Zero codes and scales are zero moments.  A gradient that is not
  * finite leaves its element's moments (in 8 bits: its whole block's) not

@@ -399,15 +399,19 @@ WS_DEVINL float warp_max_bits(uint32_t x) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, x));
 }
 
-// Codes of 8 values with their block's scale (ROOT: of roots, >= 0).  The
-// quotients are the correctly rounded ones (a code border is where x / scale
+// Codes of 8 values with their block's scale (ROOT: of roots, >= 0).  ANY: the
+// scale may be subnormal, a few units of 2^-149 and rounded to one of them, so
+// that quotients reach 2 and their code has to be held to 255 (a step's roots
+// begin at 2^-74.5, far above; the clamp is for values that a caller brings).
+// The quotients are the correctly rounded ones (a code border is where x / scale
 // says it is) from the block's one reciprocal and a residual each (Markstein,
 // IBM J. Res. Dev. 34, 1990), with tiny scales moved away from subnormal
 // reciprocals.
-template <bool ROOT>
+template <bool ROOT, bool ANY>
 WS_DEVINL void encode8(const float (&x)[8], float scale, uint32_t (&o)[2]) {
   const float up = scale < 0x1p-64f ? 0x1p64f : 1.0f;
   const float d = scale * up, inv = scale > 0.0f ? 1.0f / d : 0.0f;  // (all zero: codes 0)
+  auto root = [](float v) { return ANY ? min(root_code(v), 255u) : root_code(v); };
   float q[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
@@ -420,7 +424,7 @@ WS_DEVINL void encode8(const float (&x)[8], float scale, uint32_t (&o)[2]) {
 #pragma unroll
     for (int k = 0; k < 4; k += 2) {
       const float q0 = q[4 * h + k], q1 = q[4 * h + k + 1];
-      a += (ROOT ? root_code(q0) + root_code(q1) * 256u : e4m3x2(q0, q1)) << (8 * k);
+      a += (ROOT ? root(q0) + root(q1) * 256u : e4m3x2(q0, q1)) << (8 * k);
     }
     o[h] = a;
   }
@@ -511,8 +515,8 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
     const float sm = warp_max_bits(mx) * (1.0f / kMTop), sv = warp_max_bits(vx) * (1.0f / kVTop);
     uint32_t mo[2], vo[2];
-    encode8<false>(m, sm, mo);
-    encode8<true>(v, sv, vo);
+    encode8<false, false>(m, sm, mo);
+    encode8<true, false>(v, sv, vo);
     store_n<P16, 8>(t.p, i, t.n, p);
     store_codes(static_cast<uint8_t*>(t.m) + i, left, mo);
     store_codes(static_cast<uint8_t*>(t.v) + i, left, vo);
@@ -540,7 +544,7 @@ __global__ void __launch_bounds__(kThreads)
   for (int k = 0; k < 8; ++k) mx = max(mx, __float_as_uint(v[k]) & 0x7fffffffu);
   const float s = warp_max_bits(mx) * (ROOT ? 1.0f / kVTop : 1.0f / kMTop);
   uint32_t o[2];
-  encode8<ROOT>(v, s, o);
+  encode8<ROOT, true>(v, s, o);
   store_codes(codes + b * kBlock8 + i, left, o);
   if (lane_id() == 0) scale[b] = s;
 }
