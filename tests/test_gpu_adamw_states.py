@@ -1,4 +1,6 @@
-"""The states of ws_adamw_step: 8-bit codes over the whole range of fp32."""
+"""The states of ws_adamw_step: 8-bit codes over the whole range of fp32; the memory a plan keeps."""
+import gc
+
 import numpy as np
 import pytest
 import torch
@@ -50,3 +52,29 @@ def test_codes_of_subnormal_blocks(ops):
     c = codes.float().cpu().numpy().astype(np.float64).reshape(bits.shape)
     near = torch.from_numpy(np.minimum(q, 448.0)).float().to(torch.float8_e4m3fn).double().numpy()
     assert (np.abs(c) == near).all() and (np.signbit(c)[:, 1::4] | (c[:, 1::4] == 0)).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_plan_keeps_its_tensors(ops, bits):
+    """A caller may clear or refill its lists, or give a tensor other storage: the plan's step still finds the memory
+    that the plan was made for."""
+    n = 1000
+    z = lambda dt=F, k=n: [torch.zeros(k, dtype=dt, device=dev()) for _ in range(2)]
+    p, g = z(), z()
+    if bits == 32:
+        m, v, kw = z(), z(), {}
+    else:
+        m, v = z(torch.uint8), z(torch.uint8)
+        kw = dict(exp_avg_scales=z(k=4), exp_avg_sq_scales=z(k=4))
+    lists = [p, g, m, v, *kw.values()]
+    plan = ops.adamw_plan(p, g, m, v, **kw)
+    where = [[t.data_ptr() for t in x] for x in lists]
+    p[1].data = torch.ones(n, device=dev())     # other storage for the same tensor
+    for x in lists:
+        x.clear()
+    gc.collect()
+    assert [[t.data_ptr() for t in x] for x in plan.tensors if x is not None] == where
+    # nobody else is given that memory while the plan lives
+    taken = {q for x in where for q in x}
+    fresh = [torch.empty(k, dtype=dt, device=dev()) for k, dt in ((n, F), (n, torch.uint8), (4, F)) for _ in range(64)]
+    assert not taken & {t.data_ptr() for t in fresh}

@@ -499,7 +499,7 @@ def _slices_ok(t):
 class LoraSet:
     """The adapters of one linear (ws_lora_set): A [n, 16, K], B [n, N, 16], both fp32 or both
     bf16 (serving only), scale fp32 [n] (alpha/r; with dropout alpha/r/(1-p)).  The first
-    dimension may have any stride that is a multiple of 8 (a slice of a pool of adapters)."""
+    dimension may have any stride that is a multiple of 8 (a slice of a pool of adapters)."""""
 
     def __init__(self, A, B, scale):
         _need(A.dim() == 3 and B.dim() == 3 and A.shape[0] == B.shape[0], "A [n, r, K], B [n, N, r]")
@@ -647,8 +647,9 @@ def adamw_groups(groups, device="cuda"):
 
 
 class AdamWPlan:
-    """Device plan of an AdamW step over many tensors (ws_adamw_plan) with its workspace.  Keeps the
-    tensors; a step reads and writes them where they are."""
+    """Device plan of an AdamW step over many tensors (ws_adamw_plan) with its workspace.  A step reads and
+    writes the memory that the tensors have now; the plan keeps that memory, whatever becomes of the
+    caller's lists or of the tensors' .data."""
 
     def __init__(self, params, grads, exp_avg, exp_avg_sq, groups=None, exp_avg_scales=None,
                  exp_avg_sq_scales=None, n_groups=None):
@@ -695,7 +696,8 @@ class AdamWPlan:
         self.c.image = self.image.data_ptr()
         self.workspace = torch.empty(int(wb.value), dtype=torch.uint8, device=params[0].device)
         self.n_groups = ng
-        self.tensors = (params, grads, exp_avg, exp_avg_sq, exp_avg_scales, exp_avg_sq_scales)
+        self.tensors = tuple(None if x is None else tuple(t.detach() for t in x)
+                             for x in (params, grads, exp_avg, exp_avg_sq, exp_avg_scales, exp_avg_sq_scales))
 
 
 def adamw_plan(params, grads, exp_avg, exp_avg_sq, groups=None, exp_avg_scales=None,
