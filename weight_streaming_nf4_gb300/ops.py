@@ -499,7 +499,8 @@ def _slices_ok(t):
 class LoraSet:
     """The adapters of one linear (ws_lora_set): A [n, 16, K], B [n, N, 16], both fp32 or both
     bf16 (serving only), scale fp32 [n] (alpha/r; with dropout alpha/r/(1-p)).  The first
-    dimension may have any stride that is a multiple of 8 (a slice of a pool of adapters)."""""
+    dimension may have any stride that is a multiple of 8 (a slice of a pool of adapters).  Calls
+    read the memory that the tensors have now, and the set keeps it; later values are written into it."""
 
     def __init__(self, A, B, scale):
         _need(A.dim() == 3 and B.dim() == 3 and A.shape[0] == B.shape[0], "A [n, r, K], B [n, N, r]")
@@ -510,7 +511,7 @@ class LoraSet:
         _need(scale.dtype == torch.float32 and tuple(scale.shape) == (n,), "scale: fp32 [n]")
         _need(n > 0 and _slices_ok(A) and _slices_ok(B), "each adapter's A and B: contiguous, on the current device")
         _here(scale)
-        self.A, self.B, self.scale = A, B, scale
+        self.A, self.B, self.scale = A.detach(), B.detach(), scale.detach()
         self.n, self.r, self.K, self.N = n, r, K, N
         sa, sb = (A.stride(0), B.stride(0)) if n > 1 else (r * K, r * N)
         self.c = LoraSetC(A.data_ptr(), B.data_ptr(), scale.data_ptr(), sa, sb, n, r,
