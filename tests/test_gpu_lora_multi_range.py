@@ -1,4 +1,4 @@
-"""The many-adapter linear over its whole range: each form of its kernels, long sums, many rows and adapters, offsets past
+"""The many-adapter linear over its whole range: long sums, many rows and adapters, offsets past
 32 bits, against the formulas in 64 bits (Case, check_forward and check_backward are those of test_gpu_lora_multi)."""
 import pytest
 import torch
@@ -21,3 +21,36 @@ def test_a_set_keeps_its_tensors(ops):  # noqa: F811
     fresh = [torch.full(t.shape, float("nan"), device=dev()) for t in (A, B, s) for _ in range(16)]
     assert not taken & {t.data_ptr() for t in fresh}
     assert torch.equal(ops.lora_linear_fwd_multi(c.W, c.x, aset, c.plan)[0], want)
+
+
+@pytest.mark.parametrize("mask", [False, True])
+@pytest.mark.parametrize("M", [20000, 65536, 262144 + 5])
+def test_gradients_of_an_adapter_with_many_rows(ops, M, mask):  # noqa: F811
+    """dA and dB of one adapter whose terms all have one sign.
+
+    A warp adds up a sixty-fourth of the rows, 16 at a time: n = M / 64 sums.  The 16 rows' own sum is off by at most
+    2^-20 of itself (a few truncations at 2^-23), and each of the n additions rounds to nearest, 2^-24 of the sum so far,
+    in no fixed direction: by Hoeffding's inequality 8 sqrt(n) 2^-24 of the whole holds but for one element in 10^13, and
+    the root mean square over all elements is below sqrt(n) 2^-24.  (Sums that cut off instead of rounding drift by
+    about 0.2 n 2^-23 for each addition.)  dA's G adds its own error, 2^-20: a sum of 128 terms in fp32 from three bf16
+    parts, which hold all 24 bits."""
+    N = K = 128
+    g = torch.Generator(device=dev()).manual_seed(M)
+    pos = lambda *s: torch.rand(*s, generator=g, device=dev()) + 0.25
+    x, dY, U = pos(M, K).bfloat16(), pos(M, N).bfloat16(), pos(M, 16)
+    A, B, scale = pos(1, 16, K), pos(1, N, 16), torch.full((1,), 0.75, device=dev())
+    W = ops.NF4Weight(torch.zeros(N, K // 2, dtype=torch.uint8, device=dev()), torch.ones(K // 64, N, device=dev()), N, K)
+    bits = torch.randint(-2 ** 31, 2 ** 31 - 1, (M, K // 32), generator=g, dtype=torch.int32, device=dev()) if mask else None
+    plan = ops.lora_multi_plan(torch.zeros(M, dtype=torch.int32, device=dev()), 1)
+    _, dA, dB = ops.lora_linear_bwd_multi(W, x, ops.LoraSet(A, B, scale), plan, U, dY, mask=bits)
+    xm = x.double()
+    if mask:
+        xm *= ((bits.long()[:, :, None] >> torch.arange(32, device=dev())) & 1).view(M, K)
+    G = dY.double() @ B[0].double()
+    step, n = 2.0 ** -20, M / 64
+    for what, got, want, own in (("dB", dB[0], 0.75 * (dY.double().t() @ U.double()), step),
+                                 ("dA", dA[0], 0.75 * (G.t() @ xm), 2 * step)):
+        off = (got.double() - want) / want
+        assert float(off.abs().max()) <= 8 * n ** 0.5 * 2.0 ** -24 + own, (what, float(off.abs().max()))
+        assert float(off.square().mean().sqrt()) <= n ** 0.5 * 2.0 ** -24 + own, (what, float(off.square().mean().sqrt()))
+    assert ops.device_error() == 0

@@ -556,9 +556,16 @@ __global__ void __launch_bounds__(kWgWarps * 32, 2) k_multi_wgrad(const WgArgs w
         const int k = i / 2;
         const uint32_t b0 = (i & 1) ? hi_pair(q[0][k], q[1][k]) : lo_pair(q[0][k], q[1][k]);
         const uint32_t b1 = (i & 1) ? hi_pair(q[2][k], q[3][k]) : lo_pair(q[2][k], q[3][k]);
-        mma16816(d[i], ah[0], ah[1], ah[2], ah[3], b0, b1);
-        mma16816(d[i], am[0], am[1], am[2], am[3], b0, b1);
-        mma16816(d[i], al[0], al[1], al[2], al[3], b0, b1);
+        // The step by itself, small parts first, then one fp32 addition that
+        // rounds: the tensor cores cut off what a long running sum cannot hold
+        // (one adapter of 262144 rows of one sign: 4.4e-4 off that way, always
+        // towards zero; at most 1.7e-6 this way, 2 us of 545 more at 2048 rows).
+        float e[4] = {};
+        mma16816(e, al[0], al[1], al[2], al[3], b0, b1);
+        mma16816(e, am[0], am[1], am[2], am[3], b0, b1);
+        mma16816(e, ah[0], ah[1], ah[2], ah[3], b0, b1);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) d[i][z] += e[z];
       }
     }
   }
