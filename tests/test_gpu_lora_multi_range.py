@@ -54,3 +54,21 @@ def test_gradients_of_an_adapter_with_many_rows(ops, M, mask):  # noqa: F811
         assert float(off.abs().max()) <= 8 * n ** 0.5 * 2.0 ** -24 + own, (what, float(off.abs().max()))
         assert float(off.square().mean().sqrt()) <= n ** 0.5 * 2.0 ** -24 + own, (what, float(off.square().mean().sqrt()))
     assert ops.device_error() == 0
+
+
+@pytest.mark.parametrize("M", [1, 40, 100, 300])
+def test_gradients_of_an_adapter_without_rows_are_zero_whatever_its_scale(ops, M):  # noqa: F811
+    c = Case(ops, M, 128, 192, 4, "none", seed=M)
+    c.rows = torch.zeros(M, dtype=torch.int32)
+    c.plan = ops.lora_multi_plan(c.rows.to(dev()), 4)
+    c.scale[1], c.scale[2], c.scale[3] = float("nan"), float("inf"), float("-inf")
+    U = c.forward()["U"].float()
+    _, dA, dB = ops.lora_linear_bwd_multi(c.W, c.x, c.set, c.plan, U, c.dY)
+    assert torch.isfinite(dA[0]).all() and (dA[0] != 0).any()
+    for d in (dA, dB):
+        assert (d[1:] == 0).all() and not torch.signbit(d[1:]).any()
+    # added into what is there: those stay as they are, bit for bit
+    oA, oB = torch.randn_like(dA), torch.randn_like(dB)
+    aA, aB = oA.clone(), oB.clone()
+    ops.lora_linear_bwd_multi(c.W, c.x, c.set, c.plan, U, c.dY, dA=aA, dB=aB, grad_accumulate=True)
+    assert torch.equal(aA[1:], oA[1:]) and torch.equal(aB[1:], oB[1:])

@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(kWgWarps * 32, 2) k_multi_wgrad(const WgArgs w
               make_float4(d[i][2 * h + c], d[i + 1][2 * h + c], d[i + 2][2 * h + c], d[i + 3][2 * h + c]);
   }
   __syncthreads();
-  const float s = w.scale[a];
+  const float s = cnt > 0 ? w.scale[a] : 0.0f;  // (no rows: zeros, whatever the scale)
   float* out = (which ? w.out[1] : w.out[0]) + a * (which ? w.stride[1] : w.stride[0]);
   // four results a thread at a time: along k for dA [16, K], along j for dB [N, 16]
 #pragma unroll
