@@ -72,3 +72,45 @@ def test_gradients_of_an_adapter_without_rows_are_zero_whatever_its_scale(ops, M
     aA, aB = oA.clone(), oB.clone()
     ops.lora_linear_bwd_multi(c.W, c.x, c.set, c.plan, U, c.dY, dA=aA, dB=aB, grad_accumulate=True)
     assert torch.equal(aA[1:], oA[1:]) and torch.equal(aB[1:], oB[1:])
+
+
+def test_graphs_captured_far_apart_share_nothing(ops):  # noqa: F811
+    """Graphs of calls whose tiles are cut between CTAs, captured thousands of calls apart and replayed at once, each with
+    its own workspace: no flag of one is another's, however many calls of any kind were made in between."""
+    M, N, K, n = 300, 2112, 1088, 6
+    cs = [Case(ops, M, N, K, n, "random", mask=True, seed=s) for s in range(5)]
+    want, made = [], []
+    for c in cs:
+        f = ops.lora_linear_fwd_multi(c.W, c.x, c.set, c.plan, mask=c.mask)
+        want.append((*f, *ops.lora_linear_bwd_multi(c.W, c.x, c.set, c.plan, f[1], c.dY, mask=c.mask)))
+    ws = torch.empty(ops.lora_multi_workspace_size(M, N, K, n), dtype=torch.uint8, device=dev())
+    out = dict(y=torch.empty_like(want[0][0]), U=torch.empty_like(want[0][1]), workspace=ws)
+
+    def capture(c, w):
+        st, got = torch.cuda.Stream(), [torch.empty_like(t) for t in w]
+        own = torch.empty_like(ws)
+        st.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            ops.lora_linear_fwd_multi(c.W, c.x, c.set, c.plan, mask=c.mask, y=got[0], U=got[1], workspace=own, stream=st)
+            ops.lora_linear_bwd_multi(c.W, c.x, c.set, c.plan, got[1], c.dY, mask=c.mask, dX=got[2], dA=got[3], dB=got[4],
+                                      workspace=own, stream=st)
+        made.append((g, st, got, own))
+    capture(cs[0], want[0])
+    for c, w in zip(cs[1:], want[1:]):
+        for _ in range(3450):
+            ops.lora_linear_fwd_multi(cs[0].W, cs[0].x, cs[0].set, cs[0].plan, mask=cs[0].mask, **out)
+        capture(c, w)
+    torch.cuda.synchronize()
+    for _ in range(40):
+        for _, _, got, _ in made:
+            for t in got:
+                t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for g, st, _, _ in made:
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for (_, _, got, _), w in zip(made, want):
+            assert all(torch.equal(p, q) for p, q in zip(got, w))
+    assert ops.device_error() == 0

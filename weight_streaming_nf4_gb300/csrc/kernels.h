@@ -88,7 +88,8 @@ struct MultiLora {
   const int32_t* row;
   const int32_t* slots;
   const int32_t* tile_ad;
-  uint32_t* bad;
+  uint32_t* bad;    // zero before the launch
+  uint32_t* flags;  // [kFewUnits - 1] of the CTAs, zero before the launch
   float* out32;  // the base term where a tile row has more adapters
   int64_t stride;
   int f16;

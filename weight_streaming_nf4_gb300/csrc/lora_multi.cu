@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kSkWarps * 32)
     k_multi_skinny(const uint16_t* X, const void* Fv, int64_t strideF,
                    int C, const uint32_t* mask, const int32_t* plan,
                    int64_t o_perm, int64_t o_tile, int64_t o_slot, float* out,
-                   uint32_t* ext, int64_t M, uint32_t* zero, int n_zero) {
+                   uint32_t* ext, int64_t M, uint32_t* zero) {
   __shared__ float part[kSkWarps][kTileRows * kR];
   __shared__ float sum[kTileRows * kR];
   const int lane = (int)lane_id(), warp = (int)warp_id(), g = lane >> 2, t = lane & 3;
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kSkWarps * 32)
   pdl_wait();
   pdl_launch_dependents();
   // words the kernel that follows wants zeroed
-  if (blockIdx.x == 0 && blockIdx.y == 0 && (int)threadIdx.x < n_zero) zero[threadIdx.x] = 0u;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && (int)threadIdx.x < kFewUnits) zero[threadIdx.x] = 0u;
   const int4 tile = *reinterpret_cast<const int4*>(plan + o_tile + 4 * (int64_t)blockIdx.y);  // (the table has room for it)
   if ((int)blockIdx.y >= plan[0]) return;  // the whole cluster alike
   const int32_t* rows = plan + o_perm + tile.y;
@@ -727,8 +727,12 @@ bool few_makes_dx(int64_t M, int64_t N, int64_t K) {
 }
 
 struct WsLayout {
-  size_t G, ext, bad, base, partial, total;  // bad: words of the GEMM (1) or of run_few (kFewUnits)
+  size_t G, ext, words, base, partial, total;
 };
+// words: kFewUnits words that the skinny product zeroes for the kernel after it.
+// run_few: a flag for each CTA; the GEMM: the word of bad values, then the flags
+// (from the caller's workspace, and not the library's ring: a captured graph
+// keeps the words it was given, and the ring comes round to them again).
 // base: the fp32 base term of k_multi_expand, which a set of no more adapters
 // than slots never needs.
 WsLayout ws_layout(int64_t M, int64_t N, int64_t K, int32_t n) {
@@ -737,8 +741,8 @@ WsLayout ws_layout(int64_t M, int64_t N, int64_t K, int32_t n) {
   const size_t pf = gemm_partial_bytes(f, M, N), pb = gemm_partial_bytes(b, M, K);
   L.G = 0;
   L.ext = al256((size_t)M * kR * 4);
-  L.bad = L.ext + (size_t)M * kMultiSlots * 128;
-  L.base = L.bad + kFewUnits * 4;
+  L.words = L.ext + (size_t)M * kMultiSlots * 128;
+  L.base = L.words + kFewUnits * 4;
   L.partial = L.base + (n > kMultiSlots ? al256((size_t)M * (size_t)(N > K ? N : K) * 4) : 0);
   size_t p = pf > pb ? pf : pb;
   if (M <= kFewRows && p < kFewUnits * 64 * 128 * 4) p = kFewUnits * 64 * 128 * 4;
@@ -785,7 +789,7 @@ cudaError_t run_skinny(bool f_cj, const uint16_t* X, const void* F, bool f16, in
   return launch_cluster(k, dim3((unsigned)cs, (unsigned)L.max_tiles), kSkWarps * 32, cs, 0, st, X, F, strideF,
                         (int)C, mask, (const int32_t*)plan.data, L.perm, L.tile, L.slot, out,
                         slots ? reinterpret_cast<uint32_t*>(ws + W.ext) : nullptr, plan.M,
-                        reinterpret_cast<uint32_t*>(ws + W.bad), slots ? 1 : kFewUnits);
+                        reinterpret_cast<uint32_t*>(ws + W.words));
 }
 static_assert(kFewUnits <= kSkWarps * 32, "one thread zeroes each word");
 
@@ -802,7 +806,8 @@ MultiLora multi_of(const ws_lora_plan& plan, uint8_t* ws, const WsLayout& W, con
   m.row = pl + L.row;
   m.slots = pl + 1;
   m.tile_ad = pl + L.tile_ad;
-  m.bad = reinterpret_cast<uint32_t*>(ws + W.bad);
+  m.bad = reinterpret_cast<uint32_t*>(ws + W.words);
+  m.flags = m.bad + 1;
   m.out32 = reinterpret_cast<float*>(ws + W.base);
   m.stride = stride;
   m.f16 = f16 ? 1 : 0;
@@ -829,7 +834,7 @@ FewArgs few_args(const ws_nf4* W, const uint16_t* x, const ws_lora_plan& plan, c
   a.row = static_cast<const int32_t*>(plan.data) + plan_layout(plan.M, plan.n_adapters).row;
   a.y = y;
   a.partial = reinterpret_cast<float*>(ws + L.partial);
-  a.flags = reinterpret_cast<uint32_t*>(ws + L.bad);
+  a.flags = reinterpret_cast<uint32_t*>(ws + L.words);
   return a;
 }
 

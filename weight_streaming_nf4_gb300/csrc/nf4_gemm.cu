@@ -2525,8 +2525,8 @@ cudaError_t run_nf4_gemm_multi(const GemmPlan& plan, const NF4View& W, const uin
   a.ml_f16 = ml.f16;
   if (grid_units(p, true) > 1) {
     if (partial == nullptr) return cudaErrorInvalidValue;
-    const cudaError_t e = ring_slots((uint32_t)grid_ctas(p, true), &a.flags);
-    if (e != cudaSuccess) return e;
+    if (grid_ctas(p, true) > kFewUnits - 1) return cudaErrorInvalidConfiguration;
+    a.flags = ml.flags;
   }
   WMaps wm;
   memset(&wm, 0, sizeof(wm));
