@@ -845,6 +845,12 @@ ws_status check_plan(const ws_lora_plan* p) {
   return WS_OK;
 }
 
+// The shapes that the calls take (and their workspace is sized for).
+bool shape_ok(int64_t M, int64_t N, int64_t K, int32_t n) {
+  return M >= 1 && M <= (1 << 20) && n >= 1 && n <= WS_MULTI_MAX_ADAPTERS && N >= 64 && K >= 64 && N % 64 == 0 &&
+         K % 64 == 0 && N <= (1 << 30) && K <= (1 << 30) && (double)M * (double)(N > K ? N : K) < 17179869184.0;  // 2^34
+}
+
 // What forward and backward check alike.
 ws_status check_multi(const ws_nf4* W, const ws_lora_set* set, const ws_lora_plan* plan,
                       const uint32_t* mask) {
@@ -852,10 +858,9 @@ ws_status check_multi(const ws_nf4* W, const ws_lora_set* set, const ws_lora_pla
   if (s != WS_OK) return s;
   if (!W || !W->codes || !W->absmax || !set || !set->A || !set->B || !set->scale) return WS_ERR_INVALID;
   if (set->dtype != WS_DTYPE_F32 && set->dtype != WS_DTYPE_BF16) return WS_ERR_INVALID;
-  if (W->N < 64 || W->K < 64 || W->N % 64 || W->K % 64 || W->N > (1 << 30) || W->K > (1 << 30)) return WS_ERR_SHAPE;
+  if (!shape_ok(plan->M, W->N, W->K, plan->n_adapters)) return WS_ERR_SHAPE;
   if (set->r != kR || set->n_adapters != plan->n_adapters) return WS_ERR_SHAPE;
   if (set->stride_a < kR * W->K || set->stride_b < kR * W->N || set->stride_a % 8 || set->stride_b % 8) return WS_ERR_SHAPE;
-  if ((double)plan->M * (double)(W->N > W->K ? W->N : W->K) >= 17179869184.0) return WS_ERR_SHAPE;  // 2^34
   if (!al16p(W->codes) || !al16p(W->absmax) || !al16p(set->A) || !al16p(set->B) || !al16p(mask)) return WS_ERR_ALIGN;
   if (reinterpret_cast<uintptr_t>(set->scale) & 3u) return WS_ERR_ALIGN;
   return WS_OK;
@@ -916,9 +921,7 @@ ws_status ws_lora_multi_plan_init(const ws_lora_plan* plan, const int32_t* row_a
 ws_status ws_lora_multi_workspace_size(int64_t M, int64_t N, int64_t K, int32_t n_adapters,
                                        size_t* bytes) {
   if (!bytes) return WS_ERR_INVALID;
-  if (M < 1 || M > (1 << 20) || N < 64 || K < 64 || N % 64 || K % 64 || n_adapters < 1 ||
-      n_adapters > WS_MULTI_MAX_ADAPTERS)
-    return WS_ERR_SHAPE;
+  if (!shape_ok(M, N, K, n_adapters)) return WS_ERR_SHAPE;
   *bytes = ws_layout(M, N, K, n_adapters).total;
   return WS_OK;
 }
