@@ -114,3 +114,175 @@ def test_graphs_captured_far_apart_share_nothing(ops):  # noqa: F811
         for (_, _, got, _), w in zip(made, want):
             assert all(torch.equal(p, q) for p, q in zip(got, w))
     assert ops.device_error() == 0
+
+
+@pytest.mark.parametrize("M,n,kind", [(100, 8, "all"), (100, 9, "all"), (129, 3, "all"), (256, 40, "one tile of 8"),
+                                      (1300, 40, "one tile of 8"), (1300, 40, "one tile of 9"), (700, 5, "none"),
+                                      (513, 4096, "one each")])
+def test_slots_of_a_plan(ops, M, n, kind):  # noqa: F811
+    """The plan's second half: each row's slot and each tile row's adapters in order of their first row; the most slots of
+    any tile row, or -1 where one has more than eight."""
+    tile = 128 if M <= 128 else 256 if M <= 256 else 512
+    rows = torch.full((M,), 7 % n, dtype=torch.int32)
+    if kind == "all":
+        rows = (torch.arange(M, dtype=torch.int32) * 5) % n
+    elif kind.startswith("one tile"):
+        k, a = int(kind[-1]), (M - 1) // tile * tile        # (the last tile row; the others hold adapter 7)
+        rows[a:] = torch.arange(M - a, dtype=torch.int32) % k * 3 + 10
+        rows[a + 1] = -1
+    elif kind == "none":
+        rows[:] = n
+    else:
+        rows[:] = torch.arange(M, dtype=torch.int32) // tile * 17
+    p = ops.lora_multi_plan(rows.to(dev()), n).data.cpu()
+    up = lambda x: -(-x // 4) * 4
+    tiles = M // 64 + min(n + 1, M)
+    o_slot = 4 + 2 * up(M) + up(n + 1) + 4 * tiles
+    o_list = o_slot + up(M)
+    most, many = 0, False
+    for t in range(-(-M // tile)):
+        seen = []
+        for i in range(t * tile, min(M, (t + 1) * tile)):
+            a = int(rows[i])
+            if 0 <= a < n and a not in seen:
+                seen.append(a)
+        if len(seen) > 8:
+            many = True      # the batch takes the other form: slots are not read
+            continue
+        most = max(most, len(seen))
+        assert p[o_list + 8 * t:o_list + 8 * t + 8].tolist() == seen + [-1] * (8 - len(seen))
+        want = [seen.index(int(a)) if int(a) in seen else -1 for a in rows[t * tile:min(M, (t + 1) * tile)]]
+        assert p[o_slot + t * tile:o_slot + t * tile + len(want)].tolist() == want
+    assert int(p[1]) == (-1 if many else most) and many == (kind == "one tile of 9" or (kind, n) == ("all", 9))
+
+
+def rms(x):
+    return float(x.double().square().mean().sqrt())
+
+
+def two_parts(t):
+    """A value as the sum of two bf16 numbers: what two parts would keep of it."""
+    hi = t.bfloat16().float()
+    return hi + (t - hi).bfloat16().float()
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 1024, 4096), (200, 4096, 4096), (700, 1024, 2048)])
+def test_fp32_factors_enter_with_all_their_bits(ops, M, N, K):  # noqa: F811
+    """Root mean square errors of U, dA and dB relative to the values'.
+
+    U: a 64-deep step is 12 tensor-core sums, small parts first, so that the last four (the high part's, 16 products each)
+    cut off up to 2^-23 of the step's sum each, and those before them 2^-8 of that; the steps' sums are random in sign and
+    add up in fp32 (2^-24 each, in at most 8 rounds that see the whole): 2^-21 + 2^-23 of the root mean square.  G is made
+    the same way.  dA, dB: a 16-row step cuts off 2^-23 of itself and the additions round by 2^-24 of sums that grow like
+    the square root of their number: 2^-22 in all, for dA beside G's error.  A factor of two bf16 parts would be off by
+    2^-18 at most in each product, about 2^-19.3 root mean square: more than each bound, which is asserted."""
+    c = Case(ops, M, N, K, 3, "random", mask=True, seed=N)
+    y, U = ops.lora_linear_fwd_multi(c.W, c.x, c.set, c.plan, mask=c.mask)
+    r = c.forward()
+    U64 = r["U"].float()
+    _, dA, dB = ops.lora_linear_bwd_multi(c.W, c.x, c.set, c.plan, U64, c.dY, mask=c.mask)
+    b = c.backward(U64)
+    one, total = 2.0 ** -21 + 2.0 ** -23, 2.0 ** -22
+    assert rms(U - r["U"]) <= one * rms(r["U"]), rms(U - r["U"]) / rms(r["U"])
+    assert rms(dB - b["dB"]) <= total * rms(b["dB"]), rms(dB - b["dB"]) / rms(b["dB"])
+    assert rms(dA - b["dA"]) <= (one + total) * rms(b["dA"]), rms(dA - b["dA"]) / rms(b["dA"])
+    # two parts fail each of them
+    A, B = c.A, c.B
+    c.A, c.B = two_parts(A), two_parts(B)
+    assert rms(c.forward()["U"] - r["U"]) > one * rms(r["U"])
+    assert rms(c.backward(U64)["dA"] - b["dA"]) > (one + total) * rms(b["dA"])
+    c.A, c.B = A, B
+    assert rms(c.backward(two_parts(U64))["dB"] - b["dB"]) > total * rms(b["dB"])
+
+
+def test_the_most_adapters(ops):  # noqa: F811
+    """4096 adapters: a few with rows, the gradients of all others zero; every row another adapter, too."""
+    for M, kind in ((300, "random"), (4096, "distinct"), (50, "random")):
+        c = Case(ops, M, 64, 128, 4096, kind, mask=True, seed=M)
+        y, U = ops.lora_linear_fwd_multi(c.W, c.x, c.set, c.plan, mask=c.mask)
+        a, has = c.own()
+        xm = c.x.double() * c.keep()
+        U64 = torch.einsum("mjk,mk->mj", c.A[a].double(), xm) * has
+        assert ((U - U64).abs() <= 2.0 ** -18 * torch.einsum("mjk,mk->mj", c.A[a].double().abs(), xm.abs()) + 1e-30).all()
+        check_forward(c, y, U)
+        _, dA, dB = ops.lora_linear_bwd_multi(c.W, c.x, c.set, c.plan, U, c.dY, mask=c.mask)
+        have = torch.zeros(4096, dtype=torch.bool, device=dev())
+        have[a[has[:, 0] > 0]] = True
+        assert (dA[~have] == 0).all() and (dB[~have] == 0).all() and (dB[have] != 0).flatten(1).any(1).all()
+        hot = torch.zeros(4096, M, dtype=torch.float64, device=dev())
+        hot[a, torch.arange(M, device=dev())] = has[:, 0]
+        su = c.scale.double()[a][:, None] * U.double()
+        want = torch.stack([hot @ (su[:, j:j + 1] * c.dY.double()) for j in range(16)], -1)
+        S = torch.stack([hot @ (su[:, j:j + 1] * c.dY.double()).abs() for j in range(16)], -1)
+        assert ((dB - want).abs() <= 2.0 ** -18 * S + 1e-30).all()
+    assert ops.device_error() == 0
+
+
+@pytest.mark.parametrize("n", [3, 24])
+def test_offsets_past_32_bits(ops, n):  # noqa: F811
+    """2^20 rows of 4160 outputs: y and dX hold more than 2^32 elements, the mask 2^32 bits; checked on rows from all over
+    and the last ones, with adapters in slots and with more than slots."""
+    M, K = 1 << 20, 64
+    N = 4160
+    g = torch.Generator(device=dev()).manual_seed(n)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=dev())
+    rows = torch.randint(-1, n, (M,), generator=g, device=dev(), dtype=torch.int32)
+    plan = ops.lora_multi_plan(rows, n)
+    at = torch.cat([torch.randint(0, M, (500,), generator=g, device=dev()), torch.arange(M - 40, M, device=dev())])
+    a = rows[at].long().clamp(min=0)
+    has = (rows[at] >= 0).double()[:, None]
+    lev = torch.tensor([-1.0, -0.6962, -0.5251, -0.3949, -0.2844, -0.1848, -0.0911, 0.0,
+                        0.0796, 0.1609, 0.2461, 0.3379, 0.4407, 0.5626, 0.7230, 1.0], device=dev())
+
+    def weight(codes, absmax):
+        q = torch.stack([codes >> 4, codes & 15], -1).view(codes.shape[0], -1).long()
+        return (lev[q].view(codes.shape[0], -1, 64) * absmax.t()[:, :, None]).bfloat16().double().view(codes.shape[0], -1)
+    scale = torch.rand(n, generator=g, device=dev()) + 0.5
+    s = scale.double()[a][:, None] * has
+    # forward: [M, 64] -> [M, 4160]
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, device=dev(), dtype=torch.uint8)
+    absmax = torch.rand(K // 64, N, generator=g, device=dev()) + 0.5
+    x, A, B = rnd(M, K).bfloat16(), rnd(n, 16, K) / 8, rnd(n, N, 16)
+    y, U = ops.lora_linear_fwd_multi(ops.NF4Weight(codes, absmax, N, K), x, ops.LoraSet(A, B, scale), plan)
+    xd, w = x[at].double(), weight(codes, absmax)
+    u = torch.einsum("mjk,mk->mj", A.double()[a], xd) * has
+    want = xd @ w.t() + s * torch.einsum("mnj,mj->mn", B.double()[a], u)
+    S = xd.abs() @ w.abs().t() + s * torch.einsum("mnj,mj->mn", B.double()[a].abs(), torch.einsum("mjk,mk->mj", A.double()[a].abs(), xd.abs()))
+    # a bf16 result, and sums of 64 + 16 products with factors of 16 bits or more
+    assert ((y[at].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -13 * S).all()
+    assert ((U[at].double() - u).abs() <= 2.0 ** -18 * torch.einsum("mjk,mk->mj", A.double()[a].abs(), xd.abs()) + 1e-30).all()
+    del y
+    # backward: dY [M, 64], x and the mask [M, 4160] -> dX [M, 4160]
+    N, K = K, N
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, device=dev(), dtype=torch.uint8)
+    absmax = torch.rand(K // 64, N, generator=g, device=dev()) + 0.5
+    dY, A, B = rnd(M, N).bfloat16(), rnd(n, 16, K), rnd(n, N, 16) / 8
+    x = torch.empty(M, K, dtype=torch.bfloat16, device=dev())
+    for i in range(0, M, 1 << 16):
+        x[i:i + (1 << 16)] = rnd(1 << 16, K)
+    mask = torch.randint(-2 ** 31, 2 ** 31 - 1, (M, K // 32), generator=g, dtype=torch.int32, device=dev())
+    U = rnd(M, 16)
+    dX, dA, dB = ops.lora_linear_bwd_multi(ops.NF4Weight(codes, absmax, N, K), x, ops.LoraSet(A, B, scale), plan, U, dY, mask=mask)
+    dd, w = dY[at].double(), weight(codes, absmax)
+    keep = ((mask[at].long()[:, :, None] >> torch.arange(32, device=dev())) & 1).view(len(at), K).double()
+    G = torch.einsum("mn,mnj->mj", dd, B.double()[a])
+    SG = torch.einsum("mn,mnj->mj", dd.abs(), B.double()[a].abs())
+    want = dd @ w + keep * s * torch.einsum("mj,mjk->mk", G, A.double()[a])
+    S = dd.abs() @ w.abs() + s * torch.einsum("mj,mjk->mk", SG, A.double()[a].abs())
+    assert ((dX[at].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -13 * S).all()
+    # gradients: all rows, in 64 bits, some at a time
+    wA, SA, wB, SB = (torch.zeros(k, dtype=torch.float64, device=dev()) for k in ((n, 16, K), (n, 16, K), (n, N, 16), (n, N, 16)))
+    for i in range(0, M, 1 << 16):
+        r, d = rows[i:i + (1 << 16)], dY[i:i + (1 << 16)].double()
+        xm = x[i:i + (1 << 16)].double() * ((mask[i:i + (1 << 16)].long()[:, :, None] >> torch.arange(32, device=dev())) & 1).view(-1, K)
+        for h in range(n):
+            o = (r == h).nonzero()[:, 0]
+            sc = float(scale[h])
+            Gh = d[o] @ B[h].double()
+            wA[h] += sc * (Gh.t() @ xm[o])
+            SA[h] += sc * (d[o].abs() @ B[h].double().abs()).t() @ xm[o].abs()
+            wB[h] += sc * (d[o].t() @ U[i:i + (1 << 16)][o].double())
+            SB[h] += sc * (d[o].abs().t() @ U[i:i + (1 << 16)][o].double().abs())
+    # (2^20 / n rows of random sign: the sums stay far below S, and with them the roundings)
+    assert ((dA - wA).abs() <= 2.0 ** -18 * SA).all() and ((dB - wB).abs() <= 2.0 ** -18 * SB).all()
+    assert ops.device_error() == 0
