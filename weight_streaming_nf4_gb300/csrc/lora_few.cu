@@ -587,16 +587,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 // the integer pipe too, with three CTAs an SM.
 constexpr int kMmaWarps = 8;
 constexpr int kMmaStages = 3;   // stages of x in flight
-// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), bf16; operand layout as in
-// lora_multi.cu.
-WS_DEVINL void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                        uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 template <int NT>
 struct MmaCfg {
   static constexpr int ROWS = kMmaWarps * 16;
@@ -611,7 +601,6 @@ struct MmaCfg {
 template <int NT, bool F16>
 __global__ void __launch_bounds__(kMmaWarps * 32, MmaCfg<NT>::CTAS) k_few_mma(const FewArgs a) {
   using C = MmaCfg<NT>;
-  constexpr int RG = 1;
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = (int)lane_id(), warp = (int)warp_id(), g = lane >> 2, t = lane & 3;
   const int CS = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
@@ -619,7 +608,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, MmaCfg<NT>::CTAS) k_few_mma(co
   const int n0 = (int)blockIdx.y * C::ROWS;
   // this warp's first weight row (a warp past the last row repeats the last
   // ones: its sums are not used)
-  const int nw = min(n0 + warp * 16 * RG, a.N - 16 * RG);
+  const int nw = min(n0 + warp * 16, a.N - 16);
   const int steps = (a.K + 255) / 256;
   const int s_beg = (int)((int64_t)rank * steps / CS), s_end = (int)((int64_t)(rank + 1) * steps / CS);
 
@@ -649,8 +638,8 @@ __global__ void __launch_bounds__(kMmaWarps * 32, MmaCfg<NT>::CTAS) k_few_mma(co
     cp_async_commit();
   };
   // codes and scales of the step to come, reloaded as they are used
-  uint4 cw[RG][2][2];
-  float cs[RG][2];
+  uint4 cw[2][2];
+  float cs[2];
   const int64_t kb = a.K / 2;
   const uint8_t* cp = a.codes + (int64_t)(nw + g) * kb + (int64_t)s_beg * 128 + t * 32;
   const float* sp = a.absmax + ((int64_t)s_beg * 4 + t) * a.N + nw + g;
@@ -660,16 +649,11 @@ __global__ void __launch_bounds__(kMmaWarps * 32, MmaCfg<NT>::CTAS) k_few_mma(co
   auto load_w = [&](int q) {
     const uint8_t* p = k_lane < a.K ? cp : a.codes;
 #pragma unroll
-    for (int r = 0; r < RG; ++r)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        cw[r][h][q] = __ldg(reinterpret_cast<const uint4*>(p + (int64_t)(r * 16 + h * 8) * kb) + q);
+    for (int h = 0; h < 2; ++h) cw[h][q] = __ldg(reinterpret_cast<const uint4*>(p + (int64_t)(h * 8) * kb) + q);
   };
   auto load_s = [&]() {
 #pragma unroll
-    for (int r = 0; r < RG; ++r)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) cs[r][h] = k_lane < a.K ? __ldg(sp + r * 16 + h * 8) : 0.0f;
+    for (int h = 0; h < 2; ++h) cs[h] = k_lane < a.K ? __ldg(sp + h * 8) : 0.0f;
   };
 #pragma unroll
   for (int i = 0; i < kMmaStages - 1; ++i) stage_x(i);
@@ -678,7 +662,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, MmaCfg<NT>::CTAS) k_few_mma(co
     load_w(0);
     load_w(1);
   }
-  float acc[RG][NT][4] = {};
+  float acc[NT][4] = {};
   int slot = 0, part = 0;  // stage of x and step within it
   for (int s = s_beg; s < s_end; ++s) {
     if (part == 0) {
@@ -686,11 +670,9 @@ __global__ void __launch_bounds__(kMmaWarps * 32, MmaCfg<NT>::CTAS) k_few_mma(co
       __syncthreads();  // this stage of x has landed; everyone is done with the one before
       stage_x(slot == 0 ? kMmaStages - 1 : slot - 1);
     }
-    Nf4Table tb[RG][2];
+    Nf4Table tb[2];
 #pragma unroll
-    for (int r = 0; r < RG; ++r)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) tb[r][h] = make_table(cs[r][h]);
+    for (int h = 0; h < 2; ++h) tb[h] = make_table(cs[h]);
     const bool more = s + 1 < s_end;
     const int k_now = k_lane;
     cp += 128;
@@ -701,24 +683,19 @@ __global__ void __launch_bounds__(kMmaWarps * 32, MmaCfg<NT>::CTAS) k_few_mma(co
     const uint32_t flip = (uint32_t)(g & 1) * 64;
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
-      uint4 d[RG][2];
+      uint4 d[2];
 #pragma unroll
-      for (int r = 0; r < RG; ++r)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 q = cw[r][h][w / 4];
-          const uint32_t c = (w & 3) == 0 ? q.x : (w & 3) == 1 ? q.y : (w & 3) == 2 ? q.z : q.w;
-          d[r][h] = dq8(c, tb[r][h]);
-        }
+      for (int h = 0; h < 2; ++h) {
+        const uint4 q = cw[h][w / 4];
+        const uint32_t c = (w & 3) == 0 ? q.x : (w & 3) == 1 ? q.y : (w & 3) == 2 ? q.z : q.w;
+        d[h] = dq8(c, tb[h]);
+      }
       if ((w & 3) == 3 && more) load_w(w / 4);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const uint4 b = *reinterpret_cast<const uint4*>(xs + nt * 4096 + ((w * 64) ^ flip));
-#pragma unroll
-        for (int r = 0; r < RG; ++r) {
-          mma16816(acc[r][nt], d[r][0].x, d[r][1].x, d[r][0].y, d[r][1].y, b.x, b.y);
-          mma16816(acc[r][nt], d[r][0].z, d[r][1].z, d[r][0].w, d[r][1].w, b.z, b.w);
-        }
+        mma16816(acc[nt], d[0].x, d[1].x, d[0].y, d[1].y, b.x, b.y);
+        mma16816(acc[nt], d[0].z, d[1].z, d[0].w, d[1].w, b.z, b.w);
       }
     }
     if (++part == C::SPS) {
@@ -731,12 +708,10 @@ __global__ void __launch_bounds__(kMmaWarps * 32, MmaCfg<NT>::CTAS) k_few_mma(co
   // partial sums [m][n]
   float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
-  for (int r = 0; r < RG; ++r)
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        red[(nt * 8 + 2 * t + (e & 1)) * C::PITCH + (warp * RG + r) * 16 + (e >> 1) * 8 + g] = acc[r][nt][e];
+    for (int e = 0; e < 4; ++e)
+      red[(nt * 8 + 2 * t + (e & 1)) * C::PITCH + warp * 16 + (e >> 1) * 8 + g] = acc[nt][e];
   // U, and y's earlier readers, are an earlier kernel's business until here
   pdl_wait();
   pdl_launch_dependents();

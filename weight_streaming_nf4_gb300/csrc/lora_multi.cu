@@ -169,19 +169,6 @@ __global__ void __launch_bounds__(kPlanThreads)
 }
 
 // ------------------------------------------------------------------------ mma.sync pieces
-// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), bf16.  Lane (g = lane / 4, t =
-// lane % 4) holds A rows g, g + 8 at k = 2t, 2t+1 (a[0], a[1]) and 2t+8, 2t+9
-// (a[2], a[3]); B column g at the same k (b[0], b[1]); D rows g (d[0], d[1])
-// and g + 8 at columns 2t, 2t+1.  The kernels below permute the contraction
-// index (alike in A and B), so that a lane's elements are contiguous in memory.
-WS_DEVINL void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                        uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 // Two fp32 values as bf16 high parts and bf16 low parts (the remainders):
 // together 16 significant bits or more.
 WS_DEVINL void split2(float x, float y, uint32_t& hi, uint32_t& lo) {

@@ -1,5 +1,6 @@
-// nf4_decode.cuh -- NF4 codes to bf16 values in registers, and the asynchronous
-// global -> shared copies of the kernels that stage codes or activations.
+// nf4_decode.cuh -- NF4 codes to bf16 values in registers, the asynchronous
+// global -> shared copies of the kernels that stage codes or activations, and
+// the warp-wide matrix product of the many-adapter kernels.
 #pragma once
 #include "common.cuh"
 
@@ -98,6 +99,20 @@ WS_DEVINL void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "me
 template <int N>
 WS_DEVINL void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), bf16.  Lane (g = lane / 4, t =
+// lane % 4) holds A rows g, g + 8 at k = 2t, 2t+1 (a0, a1) and 2t+8, 2t+9 (a2,
+// a3); B column g at the same k (b0, b1); D rows g (d[0], d[1]) and g + 8 at
+// columns 2t, 2t+1.  The kernels that use it permute the contraction index
+// (alike in A and B), so that a lane's elements are contiguous in memory.
+WS_DEVINL void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 }  // namespace ws
