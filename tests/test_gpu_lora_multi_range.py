@@ -286,3 +286,34 @@ def test_offsets_past_32_bits(ops, n):  # noqa: F811
     # (2^20 / n rows of random sign: the sums stay far below S, and with them the roundings)
     assert ((dA - wA).abs() <= 2.0 ** -18 * SA).all() and ((dB - wB).abs() <= 2.0 ** -18 * SB).all()
     assert ops.device_error() == 0
+
+
+@pytest.mark.parametrize("mask", [False, True])
+@pytest.mark.parametrize("M", [100, 250, 600])
+def test_the_adapter_term_of_an_fp32_gradient(ops, M, mask):  # noqa: F811
+    """dX of a weight of zeros with one product an element: scale (dY B) A.
+
+    The GEMM takes both factors of the term as two bf16 parts.  The first is off by half a step, at most 2^-8 of the value;
+    what remains lies in binades below 2^-8 of the value's, where half a step is 2^-17 of it.  All four products of the
+    parts are taken, so the term is off by 2^-16 (the roundings of scale A and G and the cut sums of four add less than
+    2^-20).  Without the product of the two second parts it would be off by up to 2^-16 more."""
+    N, K, n = 64, 4096, 3
+    g = torch.Generator(device=dev()).manual_seed(M)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=dev())
+    A, B = torch.zeros(n, 16, K, device=dev()), torch.zeros(n, N, 16, device=dev())
+    A[:, 3], B[:, 7, 3] = rnd(n, K), rnd(n)
+    dY = torch.zeros(M, N, dtype=torch.bfloat16, device=dev())
+    dY[:, 7] = rnd(M)
+    scale = torch.rand(n, generator=g, device=dev()) + 0.5
+    W = ops.NF4Weight(torch.zeros(N, K // 2, dtype=torch.uint8, device=dev()), torch.zeros(K // 64, N, device=dev()), N, K)
+    rows = torch.randint(0, n, (M,), generator=g, device=dev(), dtype=torch.int32)
+    bits = torch.randint(-2 ** 31, 2 ** 31 - 1, (M, K // 32), generator=g, dtype=torch.int32, device=dev()) if mask else None
+    x = rnd(M, K).bfloat16()
+    dX, _, _ = ops.lora_linear_bwd_multi(W, x, ops.LoraSet(A, B, scale), ops.lora_multi_plan(rows, n), rnd(M, 16), dY,
+                                         mask=bits, dX_f32=True)
+    a = rows.long()
+    want = (scale[a].double() * dY[:, 7].double() * B[a, 7, 3].double())[:, None] * A[a, 3].double()
+    if mask:
+        want *= ((bits.long()[:, :, None] >> torch.arange(32, device=dev())) & 1).view(M, K)
+    assert ((dX.double() - want).abs() <= (2.0 ** -16 + 2.0 ** -20) * want.abs()).all(), float(((dX.double() - want).abs() / want.abs().clamp(min=1e-30)).max())
+    assert ops.device_error() == 0

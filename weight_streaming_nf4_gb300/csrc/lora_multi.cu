@@ -224,7 +224,11 @@ __global__ void __launch_bounds__(kSkWarps * 32)
   const int cnt = tile.z, nsub = (cnt + 15) / 16;
   const int slots = ext ? plan[1] : 0;
   // a pair of results (r, j), (r, j + 1), i = r * 16 + j: fp32, and split into
-  // bf16 parts [hi | lo | hi | 0] in the row's slot, zeros in the others
+  // bf16 parts [hi | lo | hi | lo] in the row's slot, zeros in the others: all
+  // four products with [F_hi | F_hi | F_lo | F_lo] in one 64-deep step.  Two
+  // parts hold 2^-17 of a value or better, so the term is off by 2^-16 at most
+  // (root mean square 3.5e-6); six products of three parts would take a second
+  // step for every slot.
   auto put = [&](int i, float v0, float v1) {
     const int64_t row = rows[i / kR];
     const int j = i % kR;
@@ -238,7 +242,7 @@ __global__ void __launch_bounds__(kSkWarps * 32)
       e[0] = l == own ? hi : 0u;
       e[8] = l == own ? lo : 0u;
       e[16] = l == own ? hi : 0u;
-      e[24] = 0u;
+      e[24] = l == own ? lo : 0u;
     }
   };
   if (tile.x < 0) {  // rows without an adapter

@@ -545,7 +545,8 @@ __device__ __noinline__ void ml_add_bad_values(const GemmArgs& a, int ad, int64_
     }
   }
 }
-// lora_tile for one adapter of many (ad < 0: a tile of zeros), leaving out bad values.
+// lora_tile for one adapter of many (ad < 0: a tile of zeros), [hi | hi | lo | lo],
+// leaving out bad values.
 template <bool BWD, int BN, int PAIR>
 WS_DEVINL void lora_tile_ml(const GemmArgs& a, int ad, int64_t rows_total, int64_t ld, int n0, uint8_t* Bt, int rank,
                             int t) {
@@ -594,9 +595,8 @@ WS_DEVINL void lora_tile_ml(const GemmArgs& a, int ad, int64_t rows_total, int64
     uint4 val;
     if (cc == 0 || cc == 2) val = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     else if (cc == 1 || cc == 3) val = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-    else if (cc == 4) val = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    else if (cc == 5) val = make_uint4(lo[4], lo[5], lo[6], lo[7]);
-    else val = make_uint4(0u, 0u, 0u, 0u);
+    else if (cc == 4 || cc == 6) val = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    else val = make_uint4(lo[4], lo[5], lo[6], lo[7]);
     sts128(Bt + j * 128 + ((cc ^ (j & 7)) << 4), val.x, val.y, val.z, val.w);
   }
 }
