@@ -386,7 +386,11 @@ ws_status ws_lora_linear_fwd_multi(const ws_nf4* W, const uint16_t* x, const ws_
  * or fp32 (dX_dtype); adapter a's gradients dA [r,K] at dA + a*stride_a and dB
  * [N,r] at dB + a*stride_b (the strides of the set), fp32.  accumulate: WS_ACC_DX
  * adds into an fp32 dX, WS_ACC_GRADS adds into dA and dB; without it the
- * gradients of adapters that have no row are set to zero. */
+ * gradients of adapters that have no row are set to zero.  An fp32 dX sums its
+ * N products in fp32: 1152 at most in the tensor cores' accumulator, which cuts
+ * off, then by additions that round (root mean square error below 1e-6 of it
+ * where signs are random); the adapter term's factors enter it as two bf16
+ * parts each (2^-16 of the term). */
 ws_status ws_lora_linear_bwd_multi(const ws_nf4* W, const uint16_t* x, const ws_lora_set* set,
                                    const ws_lora_plan* plan, const uint32_t* mask,
                                    const float* U_saved, const uint16_t* dY, void* dX,

@@ -317,3 +317,46 @@ def test_the_adapter_term_of_an_fp32_gradient(ops, M, mask):  # noqa: F811
         want *= ((bits.long()[:, :, None] >> torch.arange(32, device=dev())) & 1).view(M, K)
     assert ((dX.double() - want).abs() <= (2.0 ** -16 + 2.0 ** -20) * want.abs()).all(), float(((dX.double() - want).abs() / want.abs().clamp(min=1e-30)).max())
     assert ops.device_error() == 0
+
+
+SUMS = [
+    # M, N, K, adapters: few rows (pieces of several parts), one CTA, pairs of 128-wide tiles, and of 256-wide ones
+    (5, 16384, 2048, 3), (32, 5120, 5120, 3), (33, 8192, 9728, 3), (64, 27648, 5120, 3), (40, 8192, 256, 3),
+    (100, 8192, 512, 3), (200, 8192, 512, 20), (300, 8192, 512, 3), (512, 5120, 5120, 8),
+    (520, 4160, 9792, 5), (520, 8192, 4864, 20), (1100, 27648, 2112, 3), (300, 1216, 19456, 8),
+]
+
+
+@pytest.mark.parametrize("M,N,K,n", SUMS, ids=["-".join(map(str, s)) for s in SUMS])
+def test_an_fp32_gradient_s_long_sums_round(ops, M, N, K, n):  # noqa: F811
+    """Root mean square error of an fp32 dX relative to its values'.
+
+    The tensor cores cut off, at each of the L = 72 products of 16 after which the sum moves on, less than 2^-23 of the sum
+    so far, half of it on average, in units that are 0.72 (1 / (2 ln 2)) of that: 0.36 2^-23 of a sum that grows like the
+    square root of its length, all in one direction while the sum keeps its sign: 0.36 (2 / 3) L 2^-23 = 2.1e-6 at most.
+    The additions that follow round by 2^-24 of what they hold, in no fixed direction, N / 1152 of them: 2^-24 sqrt(N /
+    1152).  The adapter term, which is a hundredth of dX here, adds 2^-16 of itself at most: 2^-22.  (Sums left to the
+    accumulator as a whole were 4.9e-6 off at N = 5120, and 1.3e-5 at 27648.)"""
+    c = Case(ops, M, N, K, n, "random", mask=True, seed=M + 1)
+    c.A.mul_(0.2)
+    U = torch.zeros(M, 16, device=dev())
+    go = lambda **kw: ops.lora_linear_bwd_multi(c.W, c.x, c.set, c.plan, U, c.dY, mask=c.mask, **kw)
+    dX = go(dX_f32=True)[0]
+    a, has = c.own()
+    G = torch.stack([c.dY[i].double() @ c.B[a[i]].double() for i in range(M)]) * has * c.scale.double()[a][:, None]
+    want = c.dY.double() @ c.weight()
+    for h in range(n):
+        o = (a == h).nonzero()[:, 0]
+        want[o] += c.keep()[o] * (G[o] @ c.A[h].double())
+    tol = 0.36 * (2 / 3) * 72 * 2.0 ** -23 + 2.0 ** -24 * (N / 1152) ** 0.5 + 2.0 ** -22
+    off = float((dX.double() - want).norm() / want.norm())
+    assert off <= tol, (off, tol)
+    assert torch.equal(dX, go(dX_f32=True)[0])
+    old = torch.randn_like(dX)
+    add = old.clone()
+    go(dX=add, accumulate=True)
+    assert torch.equal(add, old + dX)
+    # the same in bf16, whose sums need no such care: one rounding, of a value off by no more than 2e-5 of the largest
+    d16 = go()[0].double()
+    assert ((d16 - want).abs() <= 2.0 ** -8 * want.abs() + 2e-5 * want.abs().max()).all()
+    assert ops.device_error() == 0

@@ -76,6 +76,11 @@ struct GemmArgs {
   uint32_t* ml_bad;        // set when an F value is left to the epilogue (see lora_tile_ml)
   int64_t ml_stride;
   int ml_f16;              // ml_F is bf16
+  // Backward with an fp32 result: steps of a tile after which the accumulator
+  // is added, in fp32, to a running sum (0: never), which for 256-wide tiles is
+  // ml_spill's [CTA][BN/4][BM] float4.
+  int ml_drain;
+  float* ml_spill;
 };
 
 // The adapter term of run_nf4_gemm_multi (see GemmArgs::ml_*).
@@ -138,6 +143,8 @@ cudaError_t run_nf4_gemm(const GemmPlan& p, const NF4View& W, const uint16_t* ac
 // W') + the adapter term (under `mask` in the backward), one rounding.
 // Rows of one tile row of that product (a function of M and the device).
 int64_t gemm_tile_rows(int64_t M);
+// Bytes of its `partial`.
+size_t gemm_multi_bytes(const GemmPlan& p, int64_t M, int64_t Nout);
 cudaError_t run_nf4_gemm_multi(const GemmPlan& p, const NF4View& W, const uint16_t* act, int64_t M,
                                const MultiLora& ml, const uint32_t* mask, void* out, int out_f32,
                                int out_accum, float* partial, cudaStream_t st);

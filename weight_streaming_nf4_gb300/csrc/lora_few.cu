@@ -69,7 +69,11 @@ struct Cfg {
   static_assert(SMEM <= 227u * 1024u, "shared memory");
   // tensor memory: the sums, and in the forward two steps of weights (a row a
   // lane, two values a column)
-  static constexpr uint32_t COL_A = 128, TMEM_COLS = BWD ? NX : 512;
+  static constexpr uint32_t COL_A = 128, TMEM_COLS = BWD ? 4 * NX : 512;
+  // input gradient: the products' sums in two buffers of NX columns, and after
+  // them the running sums that they are added to (kGroup)
+  static constexpr int NACC = BWD ? 2 : 1;
+  static constexpr uint32_t COL_RUN = 2 * NX;
   static constexpr int CPW = NX / 4;             // accumulator columns (rows of x) of one epilogue warp
   static_assert(NX == 32 || NX == 64, "rows of x");
 };
@@ -103,6 +107,24 @@ WS_DEVINL void tmem_ld_x4(uint32_t taddr, uint32_t (&r)[4]) {
                : "memory");
 }
 
+WS_DEVINL void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+WS_DEVINL void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// Steps (256 products each) of an fp32 gradient's sum that are left to the
+// tensor cores, which cut off what their accumulator cannot hold: 28 of them
+// were 6.9e-6 off (root mean square, N = 27648).  Even, as steps run in pairs.
+constexpr int kGroup = 4;
+static_assert(kGroup % 2 == 0, "take() sees each segment's first step");
+
 // BWD: the input gradient.  The tile is 128 columns k of W', the contraction
 // runs over its rows n, x is dY and y is dX; a thread decodes one 64-weight
 // block of one row per step, 64 consecutive columns of the operand, which keeps
@@ -117,9 +139,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   uint64_t* empty = full + 2;                                       // [2] ... and have been used
   uint64_t* xfull = empty + 2;                                      // [XS] the same for x
   uint64_t* xempty = xfull + C::XS;
-  uint64_t* acc_done = xempty + C::XS;                              // a piece's sums are complete
-  uint64_t* acc_free = acc_done + 1;                                // ... and have been read
-  uint64_t* fac = acc_free + 1;                                     // factors have landed
+  uint64_t* acc_done = xempty + C::XS;                              // [NACC] a segment's sums are complete
+  uint64_t* acc_free = acc_done + C::NACC;                          // [NACC] ... and have been read
+  uint64_t* fac = acc_free + C::NACC;                               // factors have landed
   uint32_t* misc = reinterpret_cast<uint32_t*>(fac + 1);
   volatile uint32_t* abort_flag = misc + 1;
   volatile uint32_t* got_flag = misc + 2;
@@ -201,8 +223,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       mbar_init(&xfull[s], 1);
       mbar_init(&xempty[s], 1);
     }
-    mbar_init(acc_done, 1);
-    mbar_init(acc_free, kDecWarps);
+    for (int s = 0; s < C::NACC; ++s) {
+      mbar_init(&acc_done[s], 1);
+      mbar_init(&acc_free[s], kDecWarps);
+    }
     mbar_init(fac, 1);
     fence_barrier_init();
   }
@@ -216,6 +240,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const uint32_t tmem = misc[0];
   const bool skip = *abort_flag != 0u;
   const int n_it = skip ? 0 : n_all;
+  // Steps of a segment: a piece is one, but that of an fp32 gradient kGroup
+  // steps, after which its sums move to the running ones.
+  const int group = BWD && a.out_f32 ? kGroup : 0x7fffffff;
 
   if (warp == kDecWarps) {
     // ------------------------------------------------------------ the products
@@ -229,35 +256,38 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     // lie 1024 apart and 8-row groups 2048, so a 16-deep slice is 4096 bytes on.
     const uint64_t ad0 = smem_desc_sw128(smem_u32(smem + C::OFF_A), 1024, 2048);
     const uint64_t bd0 = smem_desc_sw128(smem_u32(smem + C::OFF_X), 16, 1024);
-    int step = step0, xs = 0;
-    uint32_t pieces = 0, xph = 0;
-    bool first = true;  // of its piece
+    int step = step0, xs = 0, in_seg = 0, b = 0;
+    uint32_t xph = 0, fph = 1, last_ph = 0;  // phases of acc_free[b], and of the last acc_done
+    int last_b = -1;
+    bool first = true;  // of its segment
     for (int q = 0; q < n_it; ++q) {
       const int s = q & 1;
       bool ok = *abort_flag == 0u && mbar_wait(&full[s], (uint32_t)(q >> 1) & 1u, DERR_TIMEOUT_FULL) &&
                 mbar_wait(&xfull[xs], xph, DERR_TIMEOUT_FULL) &&
-                !(first && pieces > 0 && !mbar_wait(acc_free, (pieces - 1) & 1u, DERR_TIMEOUT_ACC));
+                (!first || mbar_wait(&acc_free[b], fph, DERR_TIMEOUT_ACC));
       if (!__all_sync(0xffffffffu, ok)) {
         *abort_flag = 1u;
         break;
       }
       tc_fence_after();
-      const bool end = ++step == S || q + 1 == n_it;
+      const bool tile_end = ++step == S;
+      const bool end = tile_end || q + 1 == n_it || ++in_seg == group;
       if (leader) {
+        const uint32_t acc = tmem + (uint32_t)(b * NX);
         const uint64_t ad = ad0 + (uint64_t)(s * (kABytes >> 4));
         const uint64_t bd = bd0 + (uint64_t)(xs * (C::X_BYTES >> 4));
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint64_t b = bd + (uint64_t)(t * NX * 8 + 2 * k);
+            const uint64_t xd = bd + (uint64_t)(t * NX * 8 + 2 * k);
             const uint32_t more = (t > 0 || k > 0 || !first) ? 1u : 0u;
-            if constexpr (BWD) tc_mma_f16(tmem, ad + (uint64_t)((t * 4 + k) * 256), b, idesc, more);
-            else tc_mma_f16_ta(tmem, tmem + C::COL_A + (uint32_t)(s * 128 + (t * 4 + k) * 8), b, idesc, more);
+            if constexpr (BWD) tc_mma_f16(acc, ad + (uint64_t)((t * 4 + k) * 256), xd, idesc, more);
+            else tc_mma_f16_ta(acc, tmem + C::COL_A + (uint32_t)(s * 128 + (t * 4 + k) * 8), xd, idesc, more);
           }
         tc_commit(&empty[s]);
         tc_commit(&xempty[xs]);
-        if (end) tc_commit(acc_done);
+        if (end) tc_commit(&acc_done[b]);
       }
       __syncwarp();
       if (++xs == C::XS) {
@@ -265,14 +295,20 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         xph ^= 1u;
       }
       first = end;
+      if (tile_end) step = 0;
       if (end) {
-        step = 0;
-        ++pieces;
+        in_seg = 0;
+        last_b = b;
+        last_ph = fph ^ 1u;
+        if (++b == C::NACC) {
+          b = 0;
+          fph ^= 1u;
+        }
       }
     }
     // every product has completed before tensor memory is freed (the last
     // piece's commit covers all before it)
-    if (pieces > 0) mbar_wait(acc_done, (pieces - 1) & 1u, DERR_TIMEOUT_DRAIN);
+    if (last_b >= 0) mbar_wait(&acc_done[last_b], last_ph, DERR_TIMEOUT_DRAIN);
     if (*abort_flag) {
       const uint64_t t0 = globaltimer();
       while (globaltimer() - t0 < 200000ull) __nanosleep(1000);
@@ -349,7 +385,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       if (lane == 0) mbar_arrive(&full[s]);
     };
     bool waited = false;  // for the earlier kernels
-    uint32_t piece = 0;
+    uint32_t seg = 0;     // segments read
     // The piece that ends with iteration q: tile `tile`, whether it holds the
     // tile's first and its last step.
     int q = 0;            // iterations made
@@ -370,7 +406,33 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     static_cast<const uint8_t*>(a.F) + (ad * a.stride + (int64_t)n0 * 16) * EB, bytes, fac);
       }
     };
-    auto epilogue = [&](int tile, bool head, bool tail) {
+    // The next segment's sums, added to the running ones or (had = false) the
+    // first of them.
+    auto drain = [&](bool had) {
+      const int b = (int)(seg % C::NACC);
+      if (!*abort_flag && !mbar_wait(&acc_done[b], (seg / C::NACC) & 1u, DERR_TIMEOUT_ACC)) *abort_flag = 1u;
+      tc_fence_after();
+      __syncwarp();
+      const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(warp / 4 * C::CPW);
+#pragma unroll
+      for (int c = 0; c < C::CPW; c += 8) {
+        uint32_t v[8], run[8] = {};
+        tmem_ld_x8(at + (uint32_t)(b * NX + c), v);
+        if (had) tmem_ld_x8(at + C::COL_RUN + (uint32_t)c, run);
+        tmem_ld_wait();
+        if (had)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(__uint_as_float(run[e]) + __uint_as_float(v[e]));
+        tmem_st_x8(at + C::COL_RUN + (uint32_t)c, v);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_free[b]);
+      ++seg;
+    };
+    // had: the piece has running sums, the last segment's among them
+    auto epilogue = [&](int tile, bool head, bool tail, bool had) {
       const int q4 = warp & 3, c0 = warp / 4 * C::CPW;  // lanes (weight rows) and columns of this warp
       const int nl = q4 * 32 + lane, n = tile * kRows + nl;
       int row_ad = -1;     // of the warp's rows, a lane each
@@ -379,8 +441,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         if (lane < C::CPW && c0 + lane < a.M) row_ad = a.row[c0 + lane];
         row_sc = a.scale[max(row_ad, 0)];
       }
-      const bool ok = !*abort_flag && mbar_wait(acc_done, piece & 1u, DERR_TIMEOUT_ACC);
-      ++piece;
+      const int ab = (int)(seg % C::NACC);
+      const bool ok = !*abort_flag && (had || mbar_wait(&acc_done[ab], (seg / C::NACC) & 1u, DERR_TIMEOUT_ACC));
+      const uint32_t sums = !BWD ? 0u : had ? C::COL_RUN : (uint32_t)(ab * NX);  // column of the sums
+      if (!had) ++seg;
       if (!ok) *abort_flag = 1u;
       tc_fence_after();
       if (!waited) {
@@ -408,12 +472,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll(BWD ? 2 : 1)
       for (int cc = 0; cc < C::CPW; cc += 4) {
         uint32_t raw[4];
-        tmem_ld_x4(tmem + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(c0 + cc), raw);
+        tmem_ld_x4(tmem + ((uint32_t)(q4 * 32) << 16) + sums + (uint32_t)(c0 + cc), raw);
         tmem_ld_wait();
-        if (cc + 4 == C::CPW) {  // the sums are in registers
+        if (cc + 4 == C::CPW && !had) {  // the sums are in registers
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(acc_free);
+          if (lane == 0) mbar_arrive(&acc_free[ab]);
         }
         float v[4];
 #pragma unroll
@@ -549,16 +613,30 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     };
     for (int tile = tile0, step = step0; q < n_it; ++tile, step = 0) {
       const int len = min(S - step, n_it - q);
+      // a segment that is followed by another is taken over once the first
+      // step of that one is decoded: its products have long been made
+      auto take = [&](int i) {
+        if constexpr (BWD) {
+          if (i > 0 && i % kGroup == 0 && group == kGroup) drain(i > kGroup);
+        }
+      };
       for (int i = 1; i < len; i += 2) {
         iter(f0);
+        take(i - 1);
         iter(f1);
       }
       if (len & 1) {
         iter(f0);
+        take(len - 1);
         const Codes f = f0;
         f0 = f1, f1 = f;
       }
-      epilogue(tile, step == 0, step + len == S);
+      bool had = false;
+      if constexpr (BWD) {
+        had = len > group;
+        if (had) drain(true);
+      }
+      epilogue(tile, step == 0, step + len == S, had);
     }
     if (!BWD && warp == 0 && *abort_flag) {  // copies in flight land first
       const uint64_t t0 = globaltimer();

@@ -728,8 +728,7 @@ struct WsLayout {
 // than slots never needs.
 WsLayout ws_layout(int64_t M, int64_t N, int64_t K, int32_t n) {
   WsLayout L{};
-  const GemmPlan f = plan_gemm(false, M, N, K), b = plan_gemm(true, M, K, N);
-  const size_t pf = gemm_partial_bytes(f, M, N), pb = gemm_partial_bytes(b, M, K);
+  const size_t pf = gemm_multi_bytes(plan_gemm(false, M, N, K), M, N), pb = gemm_multi_bytes(plan_gemm(true, M, K, N), M, K);
   L.G = 0;
   L.ext = al256((size_t)M * kR * 4);
   L.words = L.ext + (size_t)M * kMultiSlots * 128;

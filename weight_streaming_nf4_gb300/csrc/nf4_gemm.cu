@@ -601,6 +601,60 @@ WS_DEVINL void lora_tile_ml(const GemmArgs& a, int ad, int64_t rows_total, int64
   }
 }
 
+// Adds a warp's half of a tile (BN / 2 columns of UM atoms, 32 lanes, from
+// taddr) to the running sum `off` columns on, or begins it (had = false).
+template <int UM, int BN>
+WS_DEVINL void drain_acc(uint32_t taddr, uint32_t off, bool had) {
+#pragma unroll 1
+  for (int c = 0; c < UM * (BN / 2); c += 16) {
+    const uint32_t at = taddr + (uint32_t)(c / (BN / 2) * BN + c % (BN / 2));
+    uint32_t v[16];
+    tmem_ld_32x32b_x16(at, v);
+    if (had) {
+      uint32_t run[16];
+      tmem_ld_32x32b_x16(at + off, run);
+      tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(run[e]) + __uint_as_float(v[e]));
+    } else {
+      tmem_ld_wait();
+    }
+    tmem_st_32x32b_x16(at + off, v);
+  }
+  tmem_st_wait();
+}
+
+// The same for a 256-wide tile, whose accumulator fills tensor memory: the
+// running sum lies in global memory, `to` its float4 of this lane's row and the
+// half's first columns, and is added to there.  One thread makes every addition
+// to an address, so their order is its own.  rows: of each atom, from this
+// lane's on, that exist; cols: of the half.
+template <int UM, int BN>
+WS_DEVINL void spill_acc(uint32_t taddr, float4* to, bool had, int64_t rows, int64_t cols) {
+#pragma unroll
+  for (int u = 0; u < UM; ++u)
+#pragma unroll 1
+    for (int c = 0; c < BN / 2 && c < cols; c += 16) {
+      uint32_t v[16];
+      tmem_ld_32x32b_x16(taddr + (uint32_t)(u * BN + c), v);
+      tmem_ld_wait();
+      if (rows > u * 128) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float4* q = to + (int64_t)(c / 4 + e) * (UM * 128) + u * 128;
+          const float4 x = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
+                                       __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
+          if (had)
+            asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(q), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w)
+                         : "memory");
+          else
+            __stcg(q, x);
+        }
+      }
+      __syncwarp();
+    }
+}
+
 // ML: rows of different adapters (GemmArgs::ml_*), no has_lora step.
 template <bool BWD, int UM, int BN, int PAIR, bool WB, bool ML>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -667,6 +721,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   const int64_t pb = real_of(sk_begin(unit, I, U));
   const int64_t pe = real_of(sk_begin(unit + 1, I, U));
+  // ML, backward, fp32 result: a tile's steps run in parts of at most ml_drain,
+  // after each of which its accumulator moves to a running sum: the second
+  // accumulator (drain_acc) or, where one fills tensor memory, global memory
+  // (spill_acc).  (Equal parts: the first holds every LoRA step.)
+  constexpr bool kDrain = ML && BWD;
+  constexpr bool kSpill = kDrain && NACC == 1;
+  const int parts = kDrain && args.ml_drain > 0 ? (S + args.ml_drain - 1) / args.ml_drain : 1;
+  const int D = kDrain && parts > 1 ? (S + parts - 1) / parts : 0;
+  const int nacc = D > 0 ? 1 : NACC;
+  auto drained = [&](int64_t t, int64_t p, int64_t end) -> int64_t {
+    if constexpr (!kDrain) return end;
+    return D > 0 ? min(end, t * S + ((p - t * S) / D + 1) * D) : end;
+  };
   const Pos pos0 = {(int)(pb % S), (int)((pb / S) % args.mtiles), (int)((pb / S) / args.mtiles)};
   constexpr int UROWS = PAIR ? 2 * C::BM : C::BM;  // activation rows per tile
 
@@ -788,9 +855,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t lora_ph = 0;
         for (int64_t p = pb; p < pe && !*abort_flag; ++seg) {
           const int64_t t = p / S;
-          const int64_t seg_end = min(pe, (t + 1) * S);
-          const int a = (int)(seg % NACC);
-          const uint32_t aph = (uint32_t)(seg / NACC) & 1u;
+          const int64_t seg_end = drained(t, p, min(pe, (t + 1) * S));
+          const int a = (int)(seg % nacc);
+          const uint32_t aph = (uint32_t)(seg / nacc) & 1u;
           const bool acc_ok = PM ? mbar_wait_cluster(&accempty[a], aph ^ 1u, DERR_TIMEOUT_ACC)
                                  : mbar_wait(&accempty[a], aph ^ 1u, DERR_TIMEOUT_ACC);
           if (!acc_ok) {
@@ -1139,15 +1206,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         return reinterpret_cast<float4*>(args.partial + cta * C::TILE_FLOATS) +
                (int64_t)(cc / 4) * C::BM + row;
       };
+      // this CTA's running sums of a tile (kSpill), laid out the same way
+      auto spill4 = [&](int row, int cc) -> float4* {
+        return reinterpret_cast<float4*>(args.ml_spill + (int64_t)blockIdx.x * C::TILE_FLOATS) +
+               (int64_t)(cc / 4) * C::BM + row;
+      };
       int64_t seg = 0;
       uint32_t lora_ph = 0;
       for (int64_t p = pb; p < pe; ++seg) {
         const int64_t t = p / S;
+        const int64_t piece_end = min(pe, (t + 1) * S);  // of this unit's steps of the tile
+        const int64_t seg_end = drained(t, p, piece_end);
         const int64_t i0 = p % S;
-        const int64_t seg_end = min(pe, (t + 1) * S);
-        const int64_t kb = seg_end - t * S;
-        const int a = (int)(seg % NACC);
-        const uint32_t aph = (uint32_t)(seg / NACC) & 1u;
+        const int a = (int)(seg % nacc);
+        const uint32_t aph = (uint32_t)(seg / nacc) & 1u;
         if (lora_masks && (ML ? i0 < nl : i0 == 0)) {
           // the tile's first step was s G A: zero its dropped elements in
           // TMEM, then let the main steps accumulate on top
@@ -1203,9 +1275,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const int64_t m0 = (t % args.mtiles) * UROWS + rank * C::BM;
         const int64_t n0 = (t / args.mtiles) * BN;
-        const bool whole = (i0 == 0 && kb == S);
+        const int64_t p0 = kDrain ? max(pb, t * S) : p;  // the piece's first step
+        uint32_t sums = tmem + (uint32_t)(a * C::ACC_COLS);
+        const bool had = p > p0;  // a running sum of the piece's earlier segments
+        if constexpr (kSpill) {
+          if (D > 0) {
+            spill_acc<UM, BN>(tmem + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(half * (BN / 2)),
+                              spill4(r, half * (BN / 2)), had, args.M - m0 - r, args.Nout - n0 - half * (BN / 2));
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (PM && rank == 1) mbar_arrive_remote(mapa_shared(smem_u32(&accempty[a]), 0u));
+              else mbar_arrive(&accempty[a]);
+            }
+            if (seg_end < piece_end) {
+              p = seg_end;
+              continue;
+            }
+          }
+        } else if constexpr (kDrain) {
+          if (had || seg_end < piece_end)
+            drain_acc<UM, BN>(tmem + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(half * (BN / 2)), (uint32_t)C::ACC_COLS, had);
+          if (had) sums = tmem + (uint32_t)C::ACC_COLS;
+          if (seg_end < piece_end) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (PM && rank == 1) mbar_arrive_remote(mapa_shared(smem_u32(&accempty[a]), 0u));
+              else mbar_arrive(&accempty[a]);
+            }
+            p = seg_end;
+            continue;
+          }
+        }
+        const int64_t kb = piece_end - t * S;
+        const bool first = (kDrain ? p0 - t * S : i0) == 0;
+        const bool whole = (first && kb == S);
         // the tile's first steps with the rest held by later units: finish it here
-        const bool finisher = (i0 == 0 && kb < S);
+        const bool finisher = (first && kb < S);
         const bool writer = !whole && !finisher;  // a later piece: hand it over
         (void)kb;
         int64_t u_last = unit;
@@ -1225,7 +1332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           named_bar_sync(2, kEpiWarps * 32);
           if (*fin_got == 0u) u_last = unit;  // timed out: store what is here, flagged as an error
         }
-        const uint32_t dbase = tmem + (uint32_t)(a * C::ACC_COLS);
+        const uint32_t dbase = sums;
         // 16-column chunks of this warp's columns that lie inside the output
         // (of this tile's linear, for a grouped forward)
         TileGrp og = tile_grp(args, n0);
@@ -1281,13 +1388,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < kv; ++c) {
             const int cc = half * (BN / 2) + c * 16;
             const int64_t n = n0 + cc;
-            uint32_t acc[16];
-            const uint32_t taddr = dbase + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(u * BN + cc);
-            tmem_ld_32x32b_x16(taddr, acc);
-            tmem_ld_wait();
             float v[16];
+            if (kSpill && D > 0) {
+              const float4* run = spill4(row, cc);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(acc[e]);
+              for (int e = 0; e < 4; ++e) {
+                const float4 x = row_ok ? __ldcg(run + (int64_t)e * C::BM) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                v[4 * e] = x.x, v[4 * e + 1] = x.y, v[4 * e + 2] = x.z, v[4 * e + 3] = x.w;
+              }
+            } else {
+              uint32_t acc[16];
+              const uint32_t taddr = dbase + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(u * BN + cc);
+              tmem_ld_32x32b_x16(taddr, acc);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(acc[e]);
+            }
             if (writer) {
               if (!row_ok) continue;
               float4* dst = part4(blockIdx.x, row, cc);
@@ -1386,11 +1502,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           named_bar_sync(1, kEpiWarps * 32);
           if (ew == 0 && lane == 0) st_release_gpu(args.flags + blockIdx.x, 1u);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (PM && rank == 1) mbar_arrive_remote(mapa_shared(smem_u32(&accempty[a]), 0u));
-          else mbar_arrive(&accempty[a]);
+        if (!(kSpill && D > 0)) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (PM && rank == 1) mbar_arrive_remote(mapa_shared(smem_u32(&accempty[a]), 0u));
+            else mbar_arrive(&accempty[a]);
+          }
         }
         p = seg_end;
       }
@@ -2471,6 +2589,24 @@ cudaError_t run_nf4_gemm(const GemmPlan& p, const NF4View& W, const uint16_t* ac
   return dispatch_gemm(p, a, tA, tL, wm, st);
 }
 
+// Steps of a tile of an fp32 input gradient that are left to the tensor cores'
+// accumulator, which cuts off what it cannot hold at each of their four products:
+// all 80 of N = 5120 were 4.9e-6 off (root mean square), 300 of N = 18944 1.2e-5;
+// in parts of 18, added up by rounding, both are below 9e-7.  128-wide tiles pay
+// 1 to 8% for it (512 rows of 5120 x 5120: backward 79 -> 85 us); 256-wide ones,
+// whose accumulator waits while each part goes to memory, at the 32 bytes a clock
+// that an SM writes, a quarter (2048 rows of 5120 x 27648: 557 -> 709 us; 915 with
+// 128-wide tiles instead).
+constexpr int kDrainSteps = 18;
+namespace {
+bool drains(const GemmPlan& p, bool out_f32) { return p.bwd && out_f32 && p.nk > kDrainSteps; }
+}  // namespace
+
+size_t gemm_multi_bytes(const GemmPlan& p, int64_t M, int64_t Nout) {
+  const size_t b = gemm_partial_bytes(p, M, Nout);
+  return drains(p, true) && p.um == 2 && p.bn == 256 ? 2 * b : b;
+}
+
 int64_t gemm_tile_rows(int64_t M) {
   const GemmPlan p = plan_gemm(false, M, 64, 64);
   return 128 * p.um * (p.pair ? 2 : 1);
@@ -2523,6 +2659,8 @@ cudaError_t run_nf4_gemm_multi(const GemmPlan& plan, const NF4View& W, const uin
   a.ml_out32 = ml.out32;
   a.ml_stride = ml.stride;
   a.ml_f16 = ml.f16;
+  a.ml_drain = drains(p, out_f32 != 0) ? kDrainSteps : 0;
+  a.ml_spill = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(partial) + gemm_partial_bytes(p, M, Nout));
   if (grid_units(p, true) > 1) {
     if (partial == nullptr) return cudaErrorInvalidValue;
     if (grid_ctas(p, true) > kFewUnits - 1) return cudaErrorInvalidConfiguration;
