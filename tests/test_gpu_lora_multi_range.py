@@ -360,3 +360,34 @@ def test_an_fp32_gradient_s_long_sums_round(ops, M, N, K, n):  # noqa: F811
     d16 = go()[0].double()
     assert ((d16 - want).abs() <= 2.0 ** -8 * want.abs() + 2e-5 * want.abs().max()).all()
     assert ops.device_error() == 0
+
+
+@pytest.mark.parametrize("M,N,K,n", [(1, 5120, 5120, 2), (16, 448, 640, 20), (40, 9728, 2112, 3), (64, 8256, 9728, 9), (90, 448, 640, 9),
+                                     (200, 9728, 8256, 3), (300, 2112, 1088, 12), (520, 4160, 9792, 5), (700, 9792, 4160, 10)])
+def test_a_workspace_of_the_stated_size_is_enough(ops, M, N, K, n):  # noqa: F811
+    """Nothing is written behind it, and nothing of y, U, dX and the gradients goes elsewhere than in them."""
+    c = Case(ops, M, N, K, n, "random", mask=True, seed=M)
+    size, room = ops.lora_multi_workspace_size(M, N, K, n), 1 << 20
+    kept = []
+
+    def guarded(shape, dtype):
+        k = 1
+        for d in shape:
+            k *= d
+        buf = torch.empty(k + room, dtype=dtype, device=dev())
+        buf.view(torch.uint8).fill_(0xA5)
+        kept.append((buf, k))
+        return buf[:k].view(shape)
+    ws = guarded((size,), torch.uint8)
+    y, U = guarded((M, N), torch.bfloat16), guarded((M, 16), torch.float32)
+    dA, dB = guarded((n, 16, K), torch.float32), guarded((n, N, 16), torch.float32)
+    f = ops.lora_linear_fwd_multi(c.W, c.x, c.set, c.plan, mask=c.mask, y=y, U=U, workspace=ws)
+    for dtype in (torch.float32, torch.bfloat16):
+        dX = guarded((M, K), dtype)
+        ops.lora_linear_bwd_multi(c.W, c.x, c.set, c.plan, U, c.dY, mask=c.mask, dX=dX, dA=dA, dB=dB, workspace=ws)
+        want = ops.lora_linear_bwd_multi(c.W, c.x, c.set, c.plan, U, c.dY, mask=c.mask, dX_f32=dtype == torch.float32)
+        assert all(torch.equal(p, q) for p, q in zip((dX, dA, dB), want))
+    assert all(torch.equal(p, q) for p, q in zip(f, ops.lora_linear_fwd_multi(c.W, c.x, c.set, c.plan, mask=c.mask)))
+    for buf, k in kept:
+        assert (buf[k:].view(torch.uint8) == 0xA5).all()
+    assert ops.device_error() == 0
