@@ -362,9 +362,9 @@ __global__ void __launch_bounds__(kBeginThreads)
 
 // Chunks run last to first: the norm's pass read the gradients first to last,
 // and the last of them are still in L2 (134M parameters with clipping: 653 ->
-// 617 us for the step, 6.1 TB/s of what it cannot do without).  Parameters, gradients and moments are read
-// before the wait for the coefficients: the kernel that makes those has itself
-// waited for everything before it.
+// 624 us for the call, 6.0 TB/s of what it cannot do without).  Parameters,
+// gradients and moments are read before the wait for the coefficients: the
+// kernel that makes those has itself waited for everything before it.
 template <bool P16, bool G16>
 __global__ void __launch_bounds__(kThreads)
     k_adamw32(const Chunk* __restrict__ chunks, const Coef* coef) {

@@ -16,11 +16,11 @@
 // the products' first operand (through shared memory a step takes as long).  The
 // shared memory that is left holds the factors of the tile's rows (4 KB a row in
 // bf16), brought by bulk copies while the tile's steps run; read from L2 in the
-// epilogue, 48 rows of 48 adapters at 27648 x 5120 took 74 us, this way 64.  The
+// epilogue, 48 rows of 48 adapters at 27648 x 5120 took 74 us, this way 66.  The
 // input gradient wants the weights' columns as its rows: they go through shared
 // memory, which keeps their orientation.
 //
-// Measured (weights from DRAM): 48 rows of 48 adapters at 27648 x 5120 take 64
+// Measured (weights from DRAM): 48 rows of 48 adapters at 27648 x 5120 take 66
 // us with the kernel before it; a step takes 1.2 us, 0.93 of them the integer
 // pipe's (counted: 224 instructions a thread).
 //

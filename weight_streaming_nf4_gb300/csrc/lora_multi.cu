@@ -434,8 +434,8 @@ __global__ void __launch_bounds__(kSkWarps * 32)
 // i-th 8-wide product, so nothing is transposed.  Bound by reading dY and x
 // once; each warp keeps kWgStages steps of rows on their way through a ring of
 // its own in shared memory (with one step ahead in registers the pass over
-// 2048 rows of 5120 + 27648 columns took 70 us, this way 53: 2.5 TB/s of the
-// 134 MB; ALU 43%, the byte permutes and splits, at two CTAs an SM).
+// 2048 rows of 5120 + 27648 columns took 70 us, this way 55: 2.4 TB/s of the
+// 134 MB; ALU 42%, the byte permutes and splits, at two CTAs an SM).
 constexpr int kWgWarps = 8, kWgSplit = 4, kWgStages = 4;
 constexpr int kWgQ = 16 * 128, kWgP = 16 * 80, kWgM = 16 * 8;  // bytes of a step: Q, P (rows padded), mask
 constexpr int kWgStage = kWgQ + kWgP + kWgM;
