@@ -626,9 +626,10 @@ WS_DEVINL void drain_acc(uint32_t taddr, uint32_t off, bool had) {
 
 // The same for a 256-wide tile, whose accumulator fills tensor memory: the
 // running sum lies in global memory, `to` its float4 of this lane's row and the
-// half's first columns, and is added to there.  One thread makes every addition
-// to an address, so their order is its own.  rows: of each atom, from this
-// lane's on, that exist; cols: of the half.
+// half's first columns, and is added to there, by reductions, which need no
+// round trip.  One thread makes every addition to an address, so their order is
+// its own; each rounds to nearest (parts below 2^-126 may count as zero).  rows:
+// of each atom, from this lane's on, that exist; cols: of the half.
 template <int UM, int BN>
 WS_DEVINL void spill_acc(uint32_t taddr, float4* to, bool had, int64_t rows, int64_t cols) {
 #pragma unroll
