@@ -433,6 +433,58 @@ ws_status ws_attention_bwd(const uint16_t* q, const uint16_t* k, const uint16_t*
                            int32_t head_dim, uint16_t* dq, uint16_t* dk, uint16_t* dv,
                            void* workspace, size_t workspace_bytes, ws_stream_t stream);
 
+/* ---- norm of each head and rotary positions ------------------------------------------- */
+/* The step between the q and k projections and the attention core, in one
+ * pass: RMS norm of each query and key head with a gain (Henry et al., 2020),
+ * then rotary positions (Su et al., 2021).  For a head x of head_dim elements
+ * of a row at position p:
+ *   n = x / sqrt(mean(x^2) + eps) * gain          (n = x where the gain is NULL)
+ *   y_a = factor (n_a cos t_i - n_b sin t_i),  y_b = factor (n_a sin t_i + n_b cos t_i)
+ * for the pairs i < rot/2 of its first rot elements, (a, b) = (i, i + rot/2) or,
+ * interleaved, (2i, 2i + 1); the other elements are n.  t_i = 2 pi p turns[i] /
+ * 2^64: the product is taken modulo 2^64, so the angle is as exact at the
+ * farthest position as at the first.  Sums and rotations are fp32; the result
+ * is rounded to bf16 once. */
+typedef struct {
+  const uint64_t* turns; /* [rot/2] turns a position, in units of 2^-64 (device) */
+  int32_t rot;           /* rotated elements of a head: a multiple of 16, <= head_dim */
+  int32_t interleaved;   /* 0: pairs (i, i + rot/2); 1: pairs (2i, 2i + 1)          */
+  float factor;          /* of cosine and sine (1, or a long-context attention factor) */
+  int32_t reserved;      /* 0 */
+} ws_rope;
+/* turns[i] from angular frequencies (radians a position; host arrays of n). */
+ws_status ws_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns);
+/* Forward.  q [M, n_heads*head_dim], k [M, n_kv_heads*head_dim] bf16 with row
+ * strides in elements (multiples of 8; slices of one wider projection serve),
+ * positions [M] int32 (device), gains fp32 [head_dim] or NULL each; rope NULL: the
+ * norm alone.  An output may be its input itself (same pointer and stride) and
+ * otherwise overlaps nothing.  head_dim 64 or 128; 1 <= M <= 2^30; at most 1024
+ * heads each. */
+ws_status ws_qk_norm_rope_fwd(const ws_rope* rope, const int32_t* positions, int64_t M,
+                              int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float eps,
+                              const float* q_gain, const float* k_gain, const uint16_t* q,
+                              int64_t q_stride, const uint16_t* k, int64_t k_stride, uint16_t* q_out,
+                              int64_t q_out_stride, uint16_t* k_out, int64_t k_out_stride,
+                              ws_stream_t stream);
+/* Workspace of ws_qk_norm_rope_bwd where it makes gradients of the gains. */
+ws_status ws_qk_norm_rope_workspace_size(int64_t M, int32_t n_heads, int32_t n_kv_heads,
+                                         int32_t head_dim, size_t* bytes);
+/* Backward, from the forward's inputs q and k and the upstream gradients dq_out
+ * and dk_out: dq, dk bf16; dq_gain, dk_gain fp32 [head_dim] or NULL each (frozen
+ * gains), with WS_ACC_GRADS added to what they hold.  With d an upstream head
+ * rotated back and u = x / sqrt(mean(x^2) + eps): dx = (d gain - u mean(d gain u)) /
+ * sqrt(mean(x^2) + eps), dgain = sum over rows and heads of d u, in a fixed order.
+ * Where a gain is NULL (no norm) its input is not read and may be NULL.  dq may be
+ * q or dq_out itself, dk likewise.  workspace: needed for gradients of gains only. */
+ws_status ws_qk_norm_rope_bwd(const ws_rope* rope, const int32_t* positions, int64_t M,
+                              int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float eps,
+                              const float* q_gain, const float* k_gain, const uint16_t* q,
+                              int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                              const uint16_t* dq_out, int64_t dq_out_stride, const uint16_t* dk_out,
+                              int64_t dk_out_stride, uint16_t* dq, int64_t dq_stride, uint16_t* dk,
+                              int64_t dk_stride, float* dq_gain, float* dk_gain, int32_t accumulate,
+                              void* workspace, size_t ws_bytes, ws_stream_t stream);
+
 /* ---- AdamW over many tensors ------------------------------------------------------- */
 /* One optimizer step of many tensors at once (the adapters of several runs, or
  * any others), beside the Adam of ws_stack_train_step, which knows one flat

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes as C
 import dataclasses
+import math
 import os
 
 import torch
@@ -86,6 +87,10 @@ class AdamwPlanC(C.Structure):
                 ("n_chunks", i32)]
 
 
+class RopeC(C.Structure):
+    _fields_ = [("turns", P), ("rot", i32), ("interleaved", i32), ("factor", C.c_float), ("reserved", i32)]
+
+
 class StackCfgC(C.Structure):
     _fields_ = [("M", i64), ("H", i64), ("KV", i64), ("I", i64), ("head_dim", i64),
                 ("n_layers", i32), ("r", i32), ("alpha", C.c_float), ("p", C.c_double),
@@ -149,6 +154,11 @@ _sig("ws_adamw_decode8", [P, P, i64, i32, P, i32, P])
 _sig("ws_attention_fwd", [P, P, P, i32, i32, i32, i32, i32, P, P, P, P])
 _sig("ws_attention_workspace_size", [i64, i32, i32, C.POINTER(C.c_size_t)])
 _sig("ws_attention_bwd", [P, P, P, P, P, P, i32, i32, i32, i32, i32, P, P, P, P, C.c_size_t, P])
+_sig("ws_rope_turns", [P, i32, P])
+_sig("ws_qk_norm_rope_fwd", [C.POINTER(RopeC), P, i64, i32, i32, i32, C.c_float, P, P, P, i64, P, i64, P, i64, P, i64, P])
+_sig("ws_qk_norm_rope_workspace_size", [i64, i32, i32, i32, C.POINTER(C.c_size_t)])
+_sig("ws_qk_norm_rope_bwd", [C.POINTER(RopeC), P, i64, i32, i32, i32, C.c_float, P, P, P, i64, P, i64, P, i64, P, i64,
+                             P, i64, P, i64, P, P, i32, P, C.c_size_t, P])
 _sig("ws_stack_sizes", [C.POINTER(StackCfgC), i32, C.POINTER(C.c_size_t), C.POINTER(i64),
                         C.POINTER(C.c_size_t), C.POINTER(C.c_size_t)])
 _sig("ws_stack_weight_offset", [C.POINTER(StackCfgC), i32, i32, C.POINTER(C.c_size_t),
@@ -184,7 +194,8 @@ EXPORTED = ("ws_status_string", "ws_device_error", "ws_selfcheck_bounded_wait", 
             "ws_lora_linear_fwd_multi", "ws_lora_linear_bwd_multi", "ws_adamw_plan_size",
             "ws_adamw_plan_init", "ws_adamw_step", "ws_adamw_encode8", "ws_adamw_decode8",
             "ws_attention_fwd",
-            "ws_attention_workspace_size", "ws_attention_bwd", "ws_stack_sizes",
+            "ws_attention_workspace_size", "ws_attention_bwd", "ws_rope_turns", "ws_qk_norm_rope_fwd",
+            "ws_qk_norm_rope_workspace_size", "ws_qk_norm_rope_bwd", "ws_stack_sizes",
             "ws_stack_weight_offset", "ws_stack_param_offset", "ws_stack_saved_offset",
             "ws_stack_workspace_offset", "ws_stack_loader_staging_bytes", "ws_stack_put_weight",
             "ws_block_forward", "ws_block_backward_recompute",
@@ -803,6 +814,151 @@ def attention_bwd(q, k, v, o32, lse, dO, n_seq: int, head_dim: int, dq=None, dk=
                                  M // n_seq, nh, nkv, head_dim, _ptr(dq), _ptr(dk), _ptr(dv),
                                  _ptr(workspace), workspace.numel(), _stream(stream)))
     return dq, dk, dv
+
+
+# ------------------------------------------------------------------------------ norm and rotary positions
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                     attention_factor: float = None):
+    """Rotary frequencies (radians a position, a list of rot/2) and the factor of cosine and sine.
+    scaling, for contexts `factor` times as long as the `original` positions of training:
+    "none"; "linear": positions divided by the factor (Chen et al., 2023); "ntk": the base raised so
+    that the slowest pair turns a factor slower and the fastest as before; "yarn" (Peng et al., 2023):
+    pairs that turn more than beta_fast times within `original` positions stay, those below beta_slow
+    turns are slowed by the factor, a linear ramp between, and cosine and sine times attention_factor
+    (0.1 ln(factor) + 1 unless given)."""
+    _need(rot >= 16 and rot % 16 == 0, "rot: a multiple of 16")
+    _need(math.isfinite(base) and base > 1.0 and math.isfinite(factor) and factor >= 1.0, "base > 1, factor >= 1")
+    _need(scaling in ("none", "linear", "ntk", "yarn"), "scaling: none, linear, ntk or yarn")
+    if scaling == "ntk":
+        base *= factor ** (rot / (rot - 2))
+    f = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+    out = 1.0
+    if scaling == "linear":
+        f = [x / factor for x in f]
+    if scaling == "yarn":
+        _need(original > 0 and beta_fast > beta_slow > 0, "yarn needs the original positions, beta_fast > beta_slow > 0")
+
+        def at(turns):  # the pair that turns so often within the original positions
+            return rot * math.log(original / (2 * math.pi * turns)) / (2 * math.log(base))
+        lo, hi = max(math.floor(at(beta_fast)), 0), min(math.ceil(at(beta_slow)), rot - 1)
+        ramp = [min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0) for i in range(rot // 2)]
+        f = [x * (1 - r) + x / factor * r for x, r in zip(f, ramp)]
+        out = 0.1 * math.log(factor) + 1.0
+    return f, out if attention_factor is None else attention_factor
+
+
+class Rope:
+    """Rotary positions of a model (ws_rope): the pairs' frequencies, on the device."""
+
+    def __init__(self, inv_freq, interleaved=False, factor=1.0, device="cuda"):
+        n = len(inv_freq)
+        _need(n > 0 and n % 8 == 0, "rotary frequencies: a multiple of 8 of them (rot/2)")
+        _need(math.isfinite(factor), "factor: finite")
+        f, t = (C.c_double * n)(*inv_freq), (u64 * n)()
+        _check("ws_rope_turns", _lib.ws_rope_turns(f, n, t))
+        self.turns = torch.tensor([x - (1 << 64) if x >> 63 else x for x in t], dtype=torch.int64, device=device)
+        self.rot, self.interleaved, self.factor = 2 * n, bool(interleaved), float(factor)
+        self.c = RopeC(self.turns.data_ptr(), self.rot, int(self.interleaved), self.factor, 0)
+
+
+def rope(rot: int, base: float = 10000.0, interleaved=False, scaling="none", inv_freq=None, factor=None,
+         device="cuda", **kw) -> Rope:
+    """Rotary positions of the first `rot` elements of a head: rope_frequencies' (base, scaling, and in
+    kw scale, original, ...), or the caller's own inv_freq (rot/2) with the factor of cosine and sine."""
+    out = 1.0
+    if inv_freq is None:
+        kw["factor"] = kw.pop("scale", 1.0)
+        inv_freq, out = rope_frequencies(rot, base, scaling, **kw)
+    else:
+        _need(not kw and scaling == "none", "inv_freq comes with its scaling done")
+    _need(len(inv_freq) == rot // 2 and rot % 2 == 0, "inv_freq: rot/2 of them")
+    return Rope(inv_freq, interleaved, out if factor is None else factor, device)
+
+
+def _rows_ok(t, M, heads, hd, name):
+    """bf16 rows [M, heads*hd] whose rows are contiguous, at any stride (a multiple of 8)."""
+    _need(t.dtype == torch.bfloat16 and t.dim() == 2 and t.shape[0] == M and t.shape[1] == heads * hd
+          and t.stride(1) == 1 and (M == 1 or t.stride(0) >= heads * hd), f"{name}: bf16 [M, heads*head_dim], rows contiguous")
+    if t.get_device() != _device():
+        raise ValueError(f"{name} on {t.device}; the call runs on the current device (cuda:{_device()})")
+
+
+def _row_stride(t):
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _rope_checks(q, k, head_dim, rope, positions, q_gain, k_gain):
+    _need(q.dim() == 2 and k.dim() == 2 and q.shape[0] == k.shape[0], "q and k: [M, heads*head_dim]")
+    M, nh, nkv = q.shape[0], q.shape[1] // head_dim, k.shape[1] // head_dim
+    _rows_ok(q, M, nh, head_dim, "q")
+    _rows_ok(k, M, nkv, head_dim, "k")
+    _need(rope is None or (positions is not None and positions.dtype == torch.int32 and tuple(positions.shape) == (M,)),
+          "positions: int32 [M]")
+    for g in (q_gain, k_gain):
+        _need(g is None or (g.dtype == torch.float32 and tuple(g.shape) == (head_dim,)), "gains: fp32 [head_dim]")
+    _here(positions if rope is not None else None, q_gain, k_gain, None if rope is None else rope.turns)
+    return M, nh, nkv
+
+
+def qk_norm_rope_fwd(q, k, head_dim: int, rope: Rope = None, positions=None, q_gain=None, k_gain=None,
+                     eps=1e-6, q_out=None, k_out=None, stream=None):
+    """ws_qk_norm_rope_fwd: q [M, n_heads*head_dim] and k [M, n_kv_heads*head_dim] bf16 (rows may lie at a
+    stride), each head normed where its gain (fp32 [head_dim]) is given, then rotated by the positions
+    (int32 [M]) where `rope` is.  Returns (q_out, k_out); they may be q and k themselves."""
+    M, nh, nkv = _rope_checks(q, k, head_dim, rope, positions, q_gain, k_gain)
+    q_out = _empty((M, nh * head_dim), torch.bfloat16, q.device, stream) if q_out is None else q_out
+    k_out = _empty((M, nkv * head_dim), torch.bfloat16, q.device, stream) if k_out is None else k_out
+    _rows_ok(q_out, M, nh, head_dim, "q_out")
+    _rows_ok(k_out, M, nkv, head_dim, "k_out")
+    _check("ws_qk_norm_rope_fwd",
+           _lib.ws_qk_norm_rope_fwd(None if rope is None else C.byref(rope.c), _addr(positions), M, nh, nkv, head_dim,
+                                    eps, _addr(q_gain), _addr(k_gain), _addr(q), _row_stride(q), _addr(k), _row_stride(k),
+                                    _addr(q_out), _row_stride(q_out), _addr(k_out), _row_stride(k_out), _raw(stream)))
+    return q_out, k_out
+
+
+def qk_norm_rope_workspace_size(M: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    n = C.c_size_t(0)
+    _check("ws_qk_norm_rope_workspace_size",
+           _lib.ws_qk_norm_rope_workspace_size(M, n_heads, n_kv_heads, head_dim, C.byref(n)))
+    return int(n.value)
+
+
+def qk_norm_rope_bwd(q, k, dq_out, dk_out, head_dim: int, rope: Rope = None, positions=None, q_gain=None, k_gain=None,
+                     eps=1e-6, dq=None, dk=None, dq_gain=None, dk_gain=None, want_gains=True, grad_accumulate=False,
+                     workspace=None, stream=None):
+    """ws_qk_norm_rope_bwd: (dq, dk, dq_gain, dk_gain) from the forward's inputs and the upstream gradients.
+    want_gains: make gradients of the gains that are given (they come back None otherwise);
+    grad_accumulate: add them into the given dq_gain and dk_gain."""
+    M, nh, nkv = _rope_checks(q, k, head_dim, rope, positions, q_gain, k_gain)
+    dq = _empty((M, nh * head_dim), torch.bfloat16, q.device, stream) if dq is None else dq
+    dk = _empty((M, nkv * head_dim), torch.bfloat16, q.device, stream) if dk is None else dk
+    for t, h, name in ((dq_out, nh, "dq_out"), (dk_out, nkv, "dk_out"), (dq, nh, "dq"), (dk, nkv, "dk")):
+        _rows_ok(t, M, h, head_dim, name)
+    _need(not grad_accumulate or (want_gains and (q_gain is None or dq_gain is not None) and (k_gain is None or dk_gain is not None)),
+          "grad_accumulate needs the gradients to add into")
+    if not want_gains:
+        dq_gain = dk_gain = None
+    else:
+        if q_gain is not None and dq_gain is None:
+            dq_gain = _empty((head_dim,), torch.float32, q.device, stream)
+        if k_gain is not None and dk_gain is None:
+            dk_gain = _empty((head_dim,), torch.float32, q.device, stream)
+    for g, of in ((dq_gain, q_gain), (dk_gain, k_gain)):
+        _need(g is None or (of is not None and g.dtype == torch.float32 and tuple(g.shape) == (head_dim,)),
+              "dq_gain, dk_gain: fp32 [head_dim], for gains that are given")
+    if workspace is None and (dq_gain is not None or dk_gain is not None):
+        workspace = _empty((qk_norm_rope_workspace_size(M, nh, nkv, head_dim),), torch.uint8, q.device, stream)
+    _here(dq_gain, dk_gain, workspace)
+    _check("ws_qk_norm_rope_bwd",
+           _lib.ws_qk_norm_rope_bwd(None if rope is None else C.byref(rope.c), _addr(positions), M, nh, nkv, head_dim,
+                                    eps, _addr(q_gain), _addr(k_gain), _addr(q), _row_stride(q), _addr(k), _row_stride(k),
+                                    _addr(dq_out), _row_stride(dq_out), _addr(dk_out), _row_stride(dk_out),
+                                    _addr(dq), _row_stride(dq), _addr(dk), _row_stride(dk), _addr(dq_gain), _addr(dk_gain),
+                                    WS_ACC_GRADS if grad_accumulate else 0, _addr(workspace),
+                                    0 if workspace is None else workspace.nbytes, _raw(stream)))
+    return dq, dk, dq_gain, dk_gain
 
 
 # ------------------------------------------------------------------------------ stack
