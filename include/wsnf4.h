@@ -485,6 +485,74 @@ ws_status ws_qk_norm_rope_bwd(const ws_rope* rope, const int32_t* positions, int
                               int64_t dk_stride, float* dq_gain, float* dk_gain, int32_t accumulate,
                               void* workspace, size_t ws_bytes, ws_stream_t stream);
 
+/* ---- a paged cache in 8 bits and the attention over it --------------------------------- */
+/* Serving: keys and values of earlier tokens, one cache a layer, in pages of
+ * WS_KV_PAGE tokens that sequences take as they grow.  Codes are e4m3; each page
+ * has one fp32 scale for its keys and one for its values for each kv head:
+ *   k      uint8 [n_pages, n_kv_heads, WS_KV_PAGE, head_dim]
+ *   v      uint8 [n_pages, n_kv_heads, head_dim, WS_KV_PAGE]   (a token a column)
+ *   scale  fp32  [n_pages, n_kv_heads, 2]                      (keys', values')
+ * The value that a code stands for is code * scale.  head_dim 64 or 128; device
+ * memory, 16-byte aligned, the caller's; what is in it before the first append
+ * does not matter. */
+enum { WS_KV_PAGE = 64, WS_KV_MAX_SEQS = 4096 };
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  float* scale;
+  int64_t n_pages;              /* 1 .. 2^31 - 1 */
+  int32_t n_kv_heads, head_dim;
+} ws_kv_cache;
+/* A step's plan, made on the device once a step and shared by all layers (their
+ * caches have the same pages).  n_seq sequences; sequence s has past[s] tokens in
+ * the cache and brings the rows row_start[s] .. row_start[s+1] - 1 of this step's T
+ * rows, tokens past[s], past[s] + 1, ...; none at all is fine.  Token j of it lies
+ * in page page_table[s][j / WS_KV_PAGE], place j % WS_KV_PAGE.  past [n_seq],
+ * row_start [n_seq + 1] and page_table [n_seq, max_pages]: int32, device.
+ * ws_kv_plan_init only enqueues, and a captured call rereads the arrays at every
+ * replay (ws_attention_kv reads page_table too).  Whatever the arrays hold, nothing
+ * outside the given memory is touched: past is taken as at least 0, a sequence's
+ * rows beyond max_new, beyond T or beyond its table are left out (their output
+ * rows stay as they were), and a page below 0 or from n_pages on holds nothing
+ * (append drops its rows, attention passes over them). */
+typedef struct {
+  void* data;                   /* device, ws_kv_plan_size bytes */
+  const int32_t* page_table;
+  int64_t T;                    /* rows of the step: 1 .. 2^20 */
+  int32_t n_seq;                /* 1 .. WS_KV_MAX_SEQS */
+  int32_t max_pages;            /* row length of page_table; n_seq * max_pages <= 2^28 */
+  int32_t max_new;              /* the most rows that a sequence may bring: 1 .. T */
+  int32_t n_heads, n_kv_heads, head_dim;  /* n_heads a multiple of n_kv_heads */
+} ws_kv_plan;
+ws_status ws_kv_plan_size(const ws_kv_plan* plan, size_t* bytes);
+ws_status ws_kv_plan_init(const ws_kv_plan* plan, const int32_t* past, const int32_t* row_start,
+                          ws_stream_t stream);
+/* Appends the step's rows k, v [T, n_kv_heads*head_dim] bf16 (row strides in
+ * elements, multiples of 8) to the cache.  A page's scale is the smallest power of
+ * two 2^e, e >= -126, with max|x| <= 448 2^e over its tokens; a page that goes on
+ * keeps a scale no smaller than it has, and where it grows the older codes are
+ * rounded again (which changes only those that become subnormal).  A value that is
+ * not finite makes its page's scale for that head NaN, and with it what reads the
+ * page, until the page is begun anew.  Rounding is to nearest, ties to even.  A page
+ * that receives rows belongs to one sequence (full pages may be shared); places
+ * behind the appended rows stay as they were. */
+ws_status ws_kv_append(const ws_kv_cache* cache, const ws_kv_plan* plan, const uint16_t* k,
+                       int64_t k_stride, const uint16_t* v, int64_t v_stride, ws_stream_t stream);
+/* Attention of the step's rows q [T, n_heads*head_dim] bf16 over the cache, which
+ * holds the step's own rows already (ws_kv_append): row i of sequence s sees tokens
+ * 0 .. past[s] + i, query head h reads kv head h / (n_heads / n_kv_heads):
+ *   o_i = sum_j softmax_j(scale q_i . k_j) v_j         [T, n_heads*head_dim] bf16
+ *   lse = ln sum_j exp(scale q_i . k_j)                [n_heads, T] fp32, or NULL
+ * with k_j, v_j the values that the codes stand for.  scale > 0 (1/sqrt(head_dim) as
+ * a rule).  A row that sees no page gets zeros and -infinity.  Sums and softmax are
+ * fp32; probabilities enter the second product in fp16, relative to the largest.
+ * No atomics: a given plan always gives the same bits.  Calls that may run at the
+ * same time need a workspace each; a plan is only read. */
+ws_status ws_attention_kv_workspace_size(const ws_kv_plan* plan, size_t* bytes);
+ws_status ws_attention_kv(const ws_kv_cache* cache, const ws_kv_plan* plan, const uint16_t* q,
+                          int64_t q_stride, float scale, uint16_t* o, int64_t o_stride, float* lse,
+                          void* workspace, size_t ws_bytes, ws_stream_t stream);
+
 /* ---- AdamW over many tensors ------------------------------------------------------- */
 /* One optimizer step of many tensors at once (the adapters of several runs, or
  * any others), beside the Adam of ws_stack_train_step, which knows one flat

@@ -257,6 +257,13 @@ cudaError_t few_read_and_clear_dev_error(uint32_t* flags);
 cudaError_t run_few(const FewArgs& a, bool f16, cudaStream_t st);
 cudaError_t run_few_bwd(const FewArgs& a, cudaStream_t st);
 
+// ---- the 8-bit cache (kv_cache.cu, kv_attention.cu; the plan's layout in kv_plan.cuh) ------
+struct KvShape;
+// The arguments of a plan, and of a call that uses a cache with it, checked.
+ws_status kv_shape(const ws_kv_plan* p, KvShape* s);
+ws_status kv_check(const ws_kv_cache* c, const ws_kv_plan* p, KvShape* s);
+cudaError_t kv_read_and_clear_dev_error(uint32_t* flags);
+
 // ---- one LoRA linear (linear.cu) --------------------------------------------------------
 size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 cudaError_t linear_fwd(const NF4View& W, const uint16_t* x, const float* A, const float* B,

@@ -1,0 +1,428 @@
+// kv_cache.cu -- the paged cache of keys and values in 8 bits: the plan of a
+// step (which rows go where, and how attention's work is shared out), and the
+// kernel that appends rows.
+//
+// A page holds 64 tokens of every kv head.  Its keys [64, D] and its values
+// [D, 64] (a token a column: both products of the attention then contract over
+// contiguous bytes) are e4m3 codes with one scale each, the smallest power of
+// two 2^e with max|x| <= 448 2^e.  Codes are floating-point numbers, so a tight
+// scale gains nothing over a power of two, and with powers of two the codes of
+// a page whose scale grows keep their values exactly but for those that become
+// subnormal: appending token by token is as good as all at once.
+#include <math.h>
+
+#include "kv_plan.cuh"
+
+namespace ws {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+struct KvPlanArgs {
+  KvShape s;
+  KvLayout L;
+  uint8_t* data;
+  const int32_t *table, *past, *start;
+  int64_t n_pages;
+};
+
+// Exclusive prefix sum of x over the CTA's threads; total to every thread.
+WS_DEVINL int block_scan(int x, int* total) {
+  __shared__ int part[kPlanThreads / 32 + 1];
+  const int lane = (int)lane_id(), w = (int)warp_id();
+  int v = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  __syncthreads();  // part's last readers are through
+  if (lane == 31) part[w] = v;
+  __syncthreads();
+  if (w == 0) {
+    int p = part[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, p, o);
+      if (lane >= o) p += y;
+    }
+    part[lane] = p;
+  }
+  __syncthreads();
+  *total = part[kPlanThreads / 32 - 1];
+  return (w ? part[w - 1] : 0) + v - x;
+}
+
+// The largest i in [0, n) with at(i) <= x (at(0) <= x; at does not fall).
+template <typename F>
+WS_DEVINL int last_at_most(int n, int x, F at) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (at(mid) <= x)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// One CTA.  Everything read from the caller's arrays is brought into range
+// here, and the other kernels go by the plan alone: tokens beyond the table or
+// beyond max_new, rows beyond T and pages that are none cannot be reached.
+__global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const KvPlanArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = (int)threadIdx.x, n = a.s.n_seq, G = a.s.nh / a.s.nkv;
+  KvHeader* hdr = reinterpret_cast<KvHeader*>(a.data);
+  int4* seq = reinterpret_cast<int4*>(a.data + a.L.seq);
+  int2* pre = reinterpret_cast<int2*>(a.data + a.L.pre);  // pages to append to, tiles
+  int4* append = reinterpret_cast<int4*>(a.data + a.L.append);
+  int4* tile = reinterpret_cast<int4*>(a.data + a.L.tile);
+  int4* split = reinterpret_cast<int4*>(a.data + a.L.split);
+  int* unit = reinterpret_cast<int*>(a.data + a.L.unit);
+  const int room = a.s.max_pages * kPage;
+
+  int n_append = 0, n_tiles = 0;
+  for (int base = 0; base < n; base += kPlanThreads) {
+    const int s = base + tid;
+    int pages = 0, tiles = 0;
+    if (s < n) {
+      const int past = min(max(a.past[s], 0), room);
+      const int row = min(max(a.start[s], 0), (int)a.s.T);
+      const int end = min(max(a.start[s + 1], row), (int)a.s.T);
+      const int c = min(min(end - row, a.s.max_new), room - past);
+      seq[s] = make_int4(past, row, c, 0);
+      if (c > 0) {
+        pages = (past + c + kPage - 1) / kPage - past / kPage;
+        tiles = (c * G + kTileRows - 1) / kTileRows;
+      }
+    }
+    int tp, tt;
+    const int p0 = block_scan(pages, &tp), t0 = block_scan(tiles, &tt);
+    if (s < n) pre[s] = make_int2(n_append + p0, n_tiles + t0);
+    n_append += tp;
+    n_tiles += tt;
+  }
+  // row ranges that overlap could name more than there is room for
+  n_append = min(n_append, (int)a.L.max_append);
+  n_tiles = min(n_tiles, (int)a.L.max_tiles);
+  __syncthreads();
+
+  for (int i = tid; i < n_append; i += kPlanThreads) {
+    const int s = last_at_most(n, i, [&](int j) { return pre[j].x; });
+    const int4 q = seq[s];
+    const int p = q.x / kPage + i - pre[s].x;
+    const int lo = max(q.x, p * kPage), hi = min(q.x + q.z, (p + 1) * kPage);
+    const int page = a.table[(int64_t)s * a.s.max_pages + p];
+    append[i] = make_int4(q.y + lo - q.x, page >= 0 ? page : -1, lo - p * kPage, hi - lo);
+  }
+
+  int W = 0;
+  for (int base = 0; base < n_tiles; base += kPlanThreads) {
+    const int i = base + tid;
+    int pages = 0, s = 0, r0 = 0;
+    if (i < n_tiles) {
+      s = last_at_most(n, i, [&](int j) { return pre[j].y; });
+      const int4 q = seq[s];
+      r0 = (i - pre[s].y) * kTileRows;
+      const int last = min(q.z * G, r0 + kTileRows) - 1;
+      pages = (q.x + last / G) / kPage + 1;
+    }
+    int total;
+    const int at = block_scan(pages, &total);
+    if (i < n_tiles) tile[i] = make_int4(s, r0, W + at, -1);
+    W += total;
+  }
+  if (tid == 0) tile[n_tiles] = make_int4(0, 0, W, -1);
+  __syncthreads();
+
+  const int U = max(1, min((int)a.L.max_units, W));
+  int n_split = 0;
+  for (int base = 0; base < n_tiles; base += kPlanThreads) {
+    const int i = base + tid;
+    int u0 = 0, u1 = 0;
+    if (i < n_tiles) {
+      u0 = unit_of(tile[i].z, W, U);
+      u1 = unit_of(tile[i + 1].z - 1, W, U);
+    }
+    int total;
+    const int j = n_split + block_scan(u1 > u0, &total);
+    if (u1 > u0) {
+      tile[i].w = j;
+      // slot = unit + index among the cut tiles: no two pieces share one
+      split[j] = make_int4(i, u0 + j, u1 - u0 + 1, 0);
+    }
+    n_split += total;
+  }
+  if (n_tiles > 0)
+    for (int u = tid; u < U; u += kPlanThreads)
+      unit[u] = last_at_most(n_tiles, unit_start(u, W, U), [&](int j) { return tile[j].z; });
+  if (tid == 0) {
+    hdr->n_append = n_append;
+    hdr->n_tiles = n_tiles;
+    hdr->pages = W;
+    hdr->units = n_tiles > 0 ? U : 0;
+    hdr->n_split = n_split;
+  }
+}
+
+// ---- append ------------------------------------------------------------------------
+struct AppendArgs {
+  uint8_t *k, *v;
+  float* scale;
+  const uint8_t* plan;
+  size_t off_append;
+  const uint16_t *xk, *xv;
+  int64_t sk, sv, n_pages;
+  int nkv;
+};
+
+// Two codes of the nearest e4m3 values (ties to even); a in the low byte.
+WS_DEVINL uint32_t e4m3x2(float a, float b) {
+  uint16_t h;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(b), "f"(a));
+  return h;
+}
+// The codes of a word again, for a scale 1/ratio times theirs.
+WS_DEVINL uint32_t rescale4(uint32_t w, float ratio) {
+  uint32_t out = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(w >> (16 * i))));
+    float lo, hi;
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(h2));
+    out |= e4m3x2(lo * ratio, hi * ratio) << (16 * i);
+  }
+  return out;
+}
+// The scale for values up to `top` (bf16 bits without the sign): 2^e with the
+// smallest e >= -126 such that top <= 448 2^e; NaN where top is not finite.
+WS_DEVINL float scale_for(uint32_t top) {
+  if (top >= 0x7f80u) return __uint_as_float(0x7fc00000u);
+  // 448 = 1.75 2^8: one exponent more where the mantissa is above 1.75
+  const int e = (int)(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u);
+  return __uint_as_float((uint32_t)(max(e, -126) + 127) << 23);
+}
+WS_DEVINL uint32_t max_abs(const uint4& w, uint32_t m) {
+  m = __vmaxu2(m, w.x & 0x7fff7fffu);
+  m = __vmaxu2(m, w.y & 0x7fff7fffu);
+  m = __vmaxu2(m, w.z & 0x7fff7fffu);
+  return __vmaxu2(m, w.w & 0x7fff7fffu);
+}
+WS_DEVINL float elem(const uint4& w, int i) {  // element i of eight
+  const uint32_t x = i < 2 ? w.x : i < 4 ? w.y : i < 6 ? w.z : w.w;
+  return (i & 1) ? bf16_hi(x) : bf16_lo(x);
+}
+
+// One CTA per (touched page, kv head).  Thread (c, t) has elements 8c .. 8c + 7
+// of the page's tokens 8t .. 8t + 7: rows come in 16-byte pieces, key codes
+// leave in 8-byte pieces of whole rows, value codes are turned round through
+// shared memory.  Bound by memory for prompts (6 bytes an element), by the
+// latency of two dependent loads for single tokens.
+template <int D>
+__global__ void __launch_bounds__(D) k_kv_append(const AppendArgs a) {
+  constexpr int C = D / 8;  // pieces of a row; D = C * 8 threads
+  __shared__ __align__(16) uint8_t vt[D * kPage];
+  __shared__ uint32_t top[2][D / 32];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int item = (int)blockIdx.x / a.nkv, head = (int)blockIdx.x % a.nkv;
+  if (item >= reinterpret_cast<const KvHeader*>(a.plan)->n_append) return;
+  const int4 it = reinterpret_cast<const int4*>(a.plan + a.off_append)[item];
+  if (it.y < 0 || it.y >= a.n_pages) return;
+  const int tid = (int)threadIdx.x, c = tid % C, t = tid / C;
+  const int lo = it.z, hi = it.z + it.w;  // the new tokens' places
+  const int64_t at = (int64_t)it.y * a.nkv + head;
+  uint8_t* pk = a.k + at * (kPage * D);
+  uint8_t* pv = a.v + at * (kPage * D);
+  float2* ps = reinterpret_cast<float2*>(a.scale) + at;
+  const float2 old = lo > 0 ? *ps : make_float2(0.0f, 0.0f);
+
+  uint4 xk[8], xv[8];
+  uint32_t mk = 0, mv = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int p = 8 * t + i;
+    xk[i] = xv[i] = make_uint4(0, 0, 0, 0);
+    if (p >= lo && p < hi) {
+      const int64_t row = it.x + p - lo;
+      xk[i] = *reinterpret_cast<const uint4*>(a.xk + row * a.sk + head * D + c * 8);
+      xv[i] = *reinterpret_cast<const uint4*>(a.xv + row * a.sv + head * D + c * 8);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    mk = max_abs(xk[i], mk);
+    mv = max_abs(xv[i], mv);
+  }
+  mk = __reduce_max_sync(0xffffffffu, max(mk & 0xffffu, mk >> 16));
+  mv = __reduce_max_sync(0xffffffffu, max(mv & 0xffffu, mv >> 16));
+  if (lane_id() == 0) {
+    top[0][warp_id()] = mk;
+    top[1][warp_id()] = mv;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < D / 32; ++w) {
+    mk = max(mk, top[0][w]);
+    mv = max(mv, top[1][w]);
+  }
+  // a page that goes on keeps a scale no smaller than it had, NaN included
+  float ks = scale_for(mk), vs = scale_for(mv);
+  if (lo > 0 && !(old.x <= ks) && !isnan(ks)) ks = old.x;
+  if (lo > 0 && !(old.y <= vs) && !isnan(vs)) vs = old.y;
+  const bool grow_k = lo > 0 && ks > old.x, grow_v = lo > 0 && vs > old.y;
+  const float ik = 1.0f / ks, iv = 1.0f / vs;
+
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int p = 8 * t + i;
+    uint2* dst = reinterpret_cast<uint2*>(pk + p * D + c * 8);
+    if (p >= lo && p < hi) {
+      uint32_t w[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        w[j] = e4m3x2(elem(xk[i], 4 * j) * ik, elem(xk[i], 4 * j + 1) * ik) |
+               e4m3x2(elem(xk[i], 4 * j + 2) * ik, elem(xk[i], 4 * j + 3) * ik) << 16;
+      *dst = make_uint2(w[0], w[1]);
+    } else if (grow_k && p < lo) {
+      const uint2 o = *dst;
+      *dst = make_uint2(rescale4(o.x, old.x * ik), rescale4(o.y, old.x * ik));
+    }
+  }
+  // Values: row d of [D][64] in shared memory, its 8-byte units at unit ^ (d / 8)
+  // % 8, so that a half warp's 16 rows meet in pairs only.
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      w[h] = e4m3x2(elem(xv[4 * h], j) * iv, elem(xv[4 * h + 1], j) * iv) |
+             e4m3x2(elem(xv[4 * h + 2], j) * iv, elem(xv[4 * h + 3], j) * iv) << 16;
+    *reinterpret_cast<uint2*>(vt + (8 * c + j) * kPage + ((t ^ (c & 7)) << 3)) = make_uint2(w[0], w[1]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // D * 4 pieces of 16 tokens
+    const int d = (tid + i * D) / 4, u = (tid + i * D) % 4, f = 16 * u, x = (d / 8) & 7;
+    if (!(f < hi && f + 16 > lo) && !(grow_v && f < lo)) continue;
+    const uint2 n0 = *reinterpret_cast<const uint2*>(vt + d * kPage + (((2 * u) ^ x) << 3));
+    const uint2 n1 = *reinterpret_cast<const uint2*>(vt + d * kPage + (((2 * u + 1) ^ x) << 3));
+    uint32_t w[4] = {n0.x, n0.y, n1.x, n1.y};
+    uint4* dst = reinterpret_cast<uint4*>(pv + d * kPage + f);
+    if (lo > f || hi < f + 16) {  // others' places in it
+      const uint4 o4 = *dst;
+      const uint32_t o[4] = {o4.x, o4.y, o4.z, o4.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int b = f + 4 * j;  // first token of the word
+        const uint32_t older = grow_v && b < lo ? rescale4(o[j], old.y * iv) : o[j];
+        uint32_t keep = 0, mine = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (b + e < lo) keep |= 0xffu << (8 * e);
+          if (b + e >= lo && b + e < hi) mine |= 0xffu << (8 * e);
+        }
+        w[j] = (older & keep) | (w[j] & mine) | (o[j] & ~(keep | mine));
+      }
+    }
+    *dst = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (tid == 0) *ps = make_float2(ks, vs);
+}
+
+bool al16k(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool al4k(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+
+ws_status kv_shape(const ws_kv_plan* p, KvShape* s) {
+  if (!p) return WS_ERR_INVALID;
+  if (p->n_seq < 1 || p->n_seq > WS_KV_MAX_SEQS || p->max_pages < 1 || p->max_pages > 1 << 20 ||
+      (int64_t)p->n_seq * p->max_pages > (int64_t)1 << 28)
+    return WS_ERR_SHAPE;
+  if (p->T < 1 || p->T > (int64_t)1 << 20 || p->max_new < 1 || p->max_new > p->T) return WS_ERR_SHAPE;
+  if (p->n_kv_heads < 1 || p->n_kv_heads > 256 || p->n_heads < 1 || p->n_heads > 1024 ||
+      p->n_heads % p->n_kv_heads)
+    return WS_ERR_SHAPE;
+  if (p->head_dim != 64 && p->head_dim != 128) return WS_ERR_SHAPE;
+  *s = KvShape{p->T, p->n_seq, p->max_pages, p->max_new, p->n_heads, p->n_kv_heads, p->head_dim};
+  return WS_OK;
+}
+ws_status kv_check(const ws_kv_cache* c, const ws_kv_plan* p, KvShape* s) {
+  const ws_status st = kv_shape(p, s);
+  if (st != WS_OK) return st;
+  if (!c || !c->k || !c->v || !c->scale || !p->data || !p->page_table) return WS_ERR_INVALID;
+  if (c->n_pages < 1 || c->n_pages > 0x7fffffff || c->n_kv_heads != s->nkv || c->head_dim != s->hd)
+    return WS_ERR_SHAPE;
+  if (!al16k(c->k) || !al16k(c->v) || !al16k(c->scale) || !al16k(p->data) || !al4k(p->page_table))
+    return WS_ERR_ALIGN;
+  return WS_OK;
+}
+
+}  // namespace ws
+
+using namespace ws;
+
+extern "C" {
+
+ws_status ws_kv_plan_size(const ws_kv_plan* plan, size_t* bytes) {
+  KvShape s;
+  const ws_status st = kv_shape(plan, &s);
+  if (st != WS_OK) return st;
+  if (!bytes) return WS_ERR_INVALID;
+  *bytes = kv_layout(s).bytes;
+  return WS_OK;
+}
+
+ws_status ws_kv_plan_init(const ws_kv_plan* plan, const int32_t* past, const int32_t* row_start,
+                          ws_stream_t stream) {
+  KvPlanArgs a;
+  const ws_status st = kv_shape(plan, &a.s);
+  if (st != WS_OK) return st;
+  if (!plan->data || !plan->page_table || !past || !row_start) return WS_ERR_INVALID;
+  if (!al16k(plan->data) || !al4k(plan->page_table) || !al4k(past) || !al4k(row_start)) return WS_ERR_ALIGN;
+  a.L = kv_layout(a.s);
+  a.data = static_cast<uint8_t*>(plan->data);
+  a.table = plan->page_table;
+  a.past = past;
+  a.start = row_start;
+  note_launch();
+  const cudaError_t e = launch_pdl(k_kv_plan, dim3(1), dim3(kPlanThreads), 0, (cudaStream_t)stream, a);
+  return e == cudaSuccess ? WS_OK : WS_ERR_CUDA;
+}
+
+ws_status ws_kv_append(const ws_kv_cache* cache, const ws_kv_plan* plan, const uint16_t* k,
+                       int64_t k_stride, const uint16_t* v, int64_t v_stride, ws_stream_t stream) {
+  KvShape s;
+  const ws_status st = kv_check(cache, plan, &s);
+  if (st != WS_OK) return st;
+  if (!k || !v) return WS_ERR_INVALID;
+  for (int64_t d : {k_stride, v_stride})
+    if (d < (int64_t)s.nkv * s.hd || d % 8 || d > (int64_t)1 << 31) return WS_ERR_SHAPE;
+  if (!al16k(k) || !al16k(v)) return WS_ERR_ALIGN;
+  const KvLayout L = kv_layout(s);
+  AppendArgs a;
+  a.k = cache->k;
+  a.v = cache->v;
+  a.scale = cache->scale;
+  a.plan = static_cast<const uint8_t*>(plan->data);
+  a.off_append = L.append;
+  a.xk = k;
+  a.xv = v;
+  a.sk = k_stride;
+  a.sv = v_stride;
+  a.n_pages = cache->n_pages;
+  a.nkv = s.nkv;
+  note_launch();
+  const cudaError_t e = launch_pdl(s.hd == 64 ? k_kv_append<64> : k_kv_append<128>,
+                                   dim3((unsigned)(L.max_append * s.nkv)), dim3((unsigned)s.hd), 0,
+                                   (cudaStream_t)stream, a);
+  return e == cudaSuccess ? WS_OK : WS_ERR_CUDA;
+}
+
+}  // extern "C"

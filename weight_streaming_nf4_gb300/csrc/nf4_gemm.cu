@@ -76,6 +76,10 @@ cudaError_t read_and_clear_dev_error(uint32_t* flags) {
   uint32_t few = 0;
   e = few_read_and_clear_dev_error(&few);
   *flags |= few;
+  if (e != cudaSuccess) return e;
+  uint32_t kv = 0;
+  e = kv_read_and_clear_dev_error(&kv);
+  *flags |= kv;
   return e;
 }
 

@@ -91,6 +91,15 @@ class RopeC(C.Structure):
     _fields_ = [("turns", P), ("rot", i32), ("interleaved", i32), ("factor", C.c_float), ("reserved", i32)]
 
 
+class KVCacheC(C.Structure):
+    _fields_ = [("k", P), ("v", P), ("scale", P), ("n_pages", i64), ("n_kv_heads", i32), ("head_dim", i32)]
+
+
+class KVPlanC(C.Structure):
+    _fields_ = [("data", P), ("page_table", P), ("T", i64), ("n_seq", i32), ("max_pages", i32), ("max_new", i32),
+                ("n_heads", i32), ("n_kv_heads", i32), ("head_dim", i32)]
+
+
 class StackCfgC(C.Structure):
     _fields_ = [("M", i64), ("H", i64), ("KV", i64), ("I", i64), ("head_dim", i64),
                 ("n_layers", i32), ("r", i32), ("alpha", C.c_float), ("p", C.c_double),
@@ -159,6 +168,11 @@ _sig("ws_qk_norm_rope_fwd", [C.POINTER(RopeC), P, i64, i32, i32, i32, C.c_float,
 _sig("ws_qk_norm_rope_workspace_size", [i64, i32, i32, i32, C.POINTER(C.c_size_t)])
 _sig("ws_qk_norm_rope_bwd", [C.POINTER(RopeC), P, i64, i32, i32, i32, C.c_float, P, P, P, i64, P, i64, P, i64, P, i64,
                              P, i64, P, i64, P, P, i32, P, C.c_size_t, P])
+_sig("ws_kv_plan_size", [C.POINTER(KVPlanC), C.POINTER(C.c_size_t)])
+_sig("ws_kv_plan_init", [C.POINTER(KVPlanC), P, P, P])
+_sig("ws_kv_append", [C.POINTER(KVCacheC), C.POINTER(KVPlanC), P, i64, P, i64, P])
+_sig("ws_attention_kv_workspace_size", [C.POINTER(KVPlanC), C.POINTER(C.c_size_t)])
+_sig("ws_attention_kv", [C.POINTER(KVCacheC), C.POINTER(KVPlanC), P, i64, C.c_float, P, i64, P, P, C.c_size_t, P])
 _sig("ws_stack_sizes", [C.POINTER(StackCfgC), i32, C.POINTER(C.c_size_t), C.POINTER(i64),
                         C.POINTER(C.c_size_t), C.POINTER(C.c_size_t)])
 _sig("ws_stack_weight_offset", [C.POINTER(StackCfgC), i32, i32, C.POINTER(C.c_size_t),
@@ -195,7 +209,8 @@ EXPORTED = ("ws_status_string", "ws_device_error", "ws_selfcheck_bounded_wait", 
             "ws_adamw_plan_init", "ws_adamw_step", "ws_adamw_encode8", "ws_adamw_decode8",
             "ws_attention_fwd",
             "ws_attention_workspace_size", "ws_attention_bwd", "ws_rope_turns", "ws_qk_norm_rope_fwd",
-            "ws_qk_norm_rope_workspace_size", "ws_qk_norm_rope_bwd", "ws_stack_sizes",
+            "ws_qk_norm_rope_workspace_size", "ws_qk_norm_rope_bwd", "ws_kv_plan_size", "ws_kv_plan_init",
+            "ws_kv_append", "ws_attention_kv_workspace_size", "ws_attention_kv", "ws_stack_sizes",
             "ws_stack_weight_offset", "ws_stack_param_offset", "ws_stack_saved_offset",
             "ws_stack_workspace_offset", "ws_stack_loader_staging_bytes", "ws_stack_put_weight",
             "ws_block_forward", "ws_block_backward_recompute",
@@ -959,6 +974,111 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, head_dim: int, rope: Rope = None, pos
                                     WS_ACC_GRADS if grad_accumulate else 0, _addr(workspace),
                                     0 if workspace is None else workspace.nbytes, _raw(stream)))
     return dq, dk, dq_gain, dk_gain
+
+
+# ------------------------------------------------------------------------------ the paged 8-bit cache
+KV_PAGE = 64  # tokens of a page
+
+
+class KVCache:
+    """One layer's paged cache (ws_kv_cache): k [n_pages, n_kv_heads, 64, head_dim] and v [n_pages, n_kv_heads,
+    head_dim, 64], one byte an element (e4m3), scale fp32 [n_pages, n_kv_heads, 2]."""
+
+    def __init__(self, k, v, scale):
+        _need(k.dim() == 4 and v.dim() == 4 and k.element_size() == 1 and v.element_size() == 1
+              and k.shape[2] == KV_PAGE and tuple(v.shape) == (k.shape[0], k.shape[1], k.shape[3], KV_PAGE),
+              "k [n_pages, n_kv_heads, 64, head_dim], v [n_pages, n_kv_heads, head_dim, 64], one byte an element")
+        _need(scale.dtype == torch.float32 and tuple(scale.shape) == (k.shape[0], k.shape[1], 2),
+              "scale: fp32 [n_pages, n_kv_heads, 2]")
+        _here(k, v, scale)
+        self.k, self.v, self.scale = k.detach(), v.detach(), scale.detach()
+        self.n_pages, self.n_kv_heads, _, self.head_dim = k.shape
+        self.c = KVCacheC(k.data_ptr(), v.data_ptr(), scale.data_ptr(), self.n_pages, self.n_kv_heads, self.head_dim)
+
+
+def kv_cache(n_pages: int, n_kv_heads: int, head_dim: int, device="cuda") -> KVCache:
+    """A cache of n_pages pages of 64 tokens; what is in it before the first append does not matter."""
+    f8 = torch.float8_e4m3fn
+    return KVCache(torch.empty((n_pages, n_kv_heads, KV_PAGE, head_dim), dtype=f8, device=device),
+                   torch.empty((n_pages, n_kv_heads, head_dim, KV_PAGE), dtype=f8, device=device),
+                   torch.empty((n_pages, n_kv_heads, 2), dtype=torch.float32, device=device))
+
+
+class KVPlan:
+    """A step's plan (ws_kv_plan), shared by all layers: which rows go to which pages, and attention's shares."""
+
+    def __init__(self, table, T, max_new, n_heads, n_kv_heads, head_dim, stream):
+        self.table = table
+        self.T, self.max_new, self.n_seq = T, max_new, table.shape[0]
+        self.n_heads, self.n_kv_heads, self.head_dim = n_heads, n_kv_heads, head_dim
+        self.c = KVPlanC(None, table.data_ptr(), T, table.shape[0], table.shape[1], max_new, n_heads, n_kv_heads, head_dim)
+        n = C.c_size_t(0)
+        _check("ws_kv_plan_size", _lib.ws_kv_plan_size(C.byref(self.c), C.byref(n)))
+        self.data = _empty((int(n.value),), torch.uint8, table.device, stream)
+        self.c.data = self.data.data_ptr()
+
+
+def kv_plan(past, row_start, page_table, T: int, max_new: int, n_heads: int, n_kv_heads: int, head_dim: int,
+            plan: KVPlan = None, stream=None) -> KVPlan:
+    """ws_kv_plan_init: sequence s has past[s] tokens in the cache and brings rows row_start[s] ..
+    row_start[s+1] - 1 (at most max_new) of this step's T; page_table [n_seq, max_pages].  All int32 on the
+    device, read again by every replay of a captured call.  `plan` (of the same sizes and table) is refilled."""
+    _here(past, row_start, page_table)
+    _need(page_table.dtype == torch.int32 and page_table.dim() == 2, "page_table: int32 [n_seq, max_pages]")
+    n = page_table.shape[0]
+    _need(past.dtype == torch.int32 and tuple(past.shape) == (n,), "past: int32 [n_seq]")
+    _need(row_start.dtype == torch.int32 and tuple(row_start.shape) == (n + 1,), "row_start: int32 [n_seq + 1]")
+    if plan is None:
+        plan = KVPlan(page_table, T, max_new, n_heads, n_kv_heads, head_dim, stream)
+    _need(plan.table.data_ptr() == page_table.data_ptr() and plan.table.shape == page_table.shape and (plan.T, plan.max_new, plan.n_heads, plan.n_kv_heads,
+          plan.head_dim) == (T, max_new, n_heads, n_kv_heads, head_dim), "the plan was made for other sizes or another table")
+    _check("ws_kv_plan_init", _lib.ws_kv_plan_init(C.byref(plan.c), _addr(past), _addr(row_start), _raw(stream)))
+    return plan
+
+
+def _kv_checks(cache, plan):
+    _need((cache.n_kv_heads, cache.head_dim) == (plan.n_kv_heads, plan.head_dim), "the plan was made for another cache")
+    d = _device()
+    _need(cache.k.get_device() == d and plan.data.get_device() == d, "the cache and the plan lie on the current device")
+
+
+def kv_append(cache: KVCache, plan: KVPlan, k, v, stream=None):
+    """ws_kv_append: the step's rows k and v [T, n_kv_heads*head_dim] bf16 (rows may lie at a stride) into the cache."""
+    _kv_checks(cache, plan)
+    _rows_ok(k, plan.T, plan.n_kv_heads, plan.head_dim, "k")
+    _rows_ok(v, plan.T, plan.n_kv_heads, plan.head_dim, "v")
+    _check("ws_kv_append", _lib.ws_kv_append(C.byref(cache.c), C.byref(plan.c), _addr(k), _row_stride(k), _addr(v),
+                                             _row_stride(v), _raw(stream)))
+
+
+def attention_kv_workspace_size(plan: KVPlan) -> int:
+    n = C.c_size_t(0)
+    _check("ws_attention_kv_workspace_size", _lib.ws_attention_kv_workspace_size(C.byref(plan.c), C.byref(n)))
+    return int(n.value)
+
+
+def attention_kv(q, cache: KVCache, plan: KVPlan, scale: float = None, o=None, lse=None, want_lse=False,
+                 workspace=None, stream=None):
+    """ws_attention_kv: the step's rows q [T, n_heads*head_dim] bf16 over the cache (the step's own keys and values
+    appended before).  scale: 1/sqrt(head_dim) unless given.  Returns (o bf16 [T, n_heads*head_dim], lse fp32
+    [n_heads, T] or None)."""
+    _kv_checks(cache, plan)
+    T, nh, hd = plan.T, plan.n_heads, plan.head_dim
+    _rows_ok(q, T, nh, hd, "q")
+    if o is None:
+        o = _empty((T, nh * hd), torch.bfloat16, q.device, stream)
+    _rows_ok(o, T, nh, hd, "o")
+    if lse is None and want_lse:
+        lse = _empty((nh, T), torch.float32, q.device, stream)
+    _need(lse is None or (lse.dtype == torch.float32 and tuple(lse.shape) == (nh, T)), "lse: fp32 [n_heads, T]")
+    if workspace is None:
+        workspace = _empty((attention_kv_workspace_size(plan),), torch.uint8, q.device, stream)
+    _here(lse, workspace)
+    _check("ws_attention_kv",
+           _lib.ws_attention_kv(C.byref(cache.c), C.byref(plan.c), _addr(q), _row_stride(q),
+                                hd ** -0.5 if scale is None else scale, _addr(o), _row_stride(o), _addr(lse),
+                                _addr(workspace), workspace.nbytes, _raw(stream)))
+    return o, lse
 
 
 # ------------------------------------------------------------------------------ stack
