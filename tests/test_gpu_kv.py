@@ -5,8 +5,11 @@ such roundings is below 2e-3 of the result's).  Before that, probabilities are r
 a score is off by at most
     delta = 2^-17 scale max|q| max_j sum|k_j|,
 which covers queries held with an absolute error of 2^-18 of the row's largest element and as much again for the fp32
-sums; 2^x and the sums after it add less than 2^-19.  So an element is off by 2^-8 of itself and
-(2^-11 + 2 delta + 2^-18) sum_j p_j |v_j|; lse by delta + 2^-18 + 2^-22 |lse|."""
+sums; 2^x and the sums after it add less than 2^-19.  Below 2^-14 fp16 has steps of 2^-24: a probability, relative to the
+row's largest and times its page's scale over the largest scale S, enters as 2^7 times itself, so it is off by as much as
+2^-25 2^-7 = 2^-32 there however small it is, which a code of at most 448 makes 2^-32 448 S for each of the N tokens seen
+(it shows where the large probabilities meet zeros among the values).  So an element is off by 2^-8 of itself,
+(2^-11 + 2 delta + 2^-18) sum_j p_j |v_j| and 2^-32 448 S N; lse by delta + 2^-18 + 2^-22 |lse|."""
 import math
 
 import pytest
@@ -70,7 +73,7 @@ class Model:
                         grown = e4m3(codes[page, :, :p] * (old / s)[:, None, None])
                         codes[page, :, :p] = torch.where((s > old)[:, None, None], grown, codes[page, :, :p])
                     y = x / s[:, None, None]
-                    codes[page, :, p:p + hi - lo] = torch.where(y.isnan(), math.nan, e4m3(y.nan_to_num()))
+                    codes[page, :, p:p + hi - lo] = torch.where(y.isnan(), 0.0, e4m3(y.nan_to_num()))  # under a NaN scale
                     self.s[page, :, c] = s
             row += n
 
@@ -95,6 +98,8 @@ def attention(m, past, new, table, q, G, hd, scale, start=None):
         k = (m.k[at] * m.s[at, :, 0, None, None]).transpose(0, 1).reshape(nkv, -1, hd)[:, :a + n]
         v = (m.v[at] * m.s[at, :, 1, None, None]).transpose(0, 1).reshape(nkv, -1, hd)[:, :a + n]
         k, v = (torch.where(good[None, :, None], t, 0.0) for t in (k, v))
+        kn, vn = k.isnan().any(-1), v.isnan()  # what is not finite reaches the rows that see it, and no others
+        k, v = k.nan_to_num(), v.nan_to_num()
         x = q[r0:r0 + n].double().view(n, nkv, G, hd).permute(1, 2, 0, 3)
         s = torch.einsum("hgnd,hjd->hgnj", x, k) * scale
         seen = (torch.arange(a + n, device=DEV) <= a + torch.arange(n, device=DEV)[:, None]) & good
@@ -103,8 +108,12 @@ def attention(m, past, new, table, q, G, hd, scale, start=None):
         p = torch.exp(s - torch.where(lse.isinf(), 0.0, lse)[..., None])
         o = torch.einsum("hgnj,hjd->hgnd", p, v)
         size = torch.einsum("hgnj,hjd->hgnd", p, v.abs())
+        lost = torch.einsum("nj,hj->hn", seen.double(), kn.double())[:, None] > 0
+        lse = torch.where(lost, math.nan, lse)
+        o = torch.where(lost[..., None] | (torch.einsum("nj,hjd->hnd", seen.double(), vn.double())[:, None] > 0), math.nan, o)
         delta = 2.0 ** -17 * scale * x.abs().amax(-1) * k.abs().sum(-1).amax(-1)[:, None, None]
-        tol = 2.0 ** -8 * o.abs() + (2.0 ** -11 + 2.0 ** -18 + 2 * delta)[..., None] * size
+        top = torch.where((good[::PAGE])[:, None], m.s[at, :, 1], 0.0).nan_to_num().amax(0)[:, None, None, None]
+        tol = 2.0 ** -8 * o.abs() + (2.0 ** -11 + 2.0 ** -18 + 2 * delta)[..., None] * size + 2.0 ** -32 * 448 * top * (a + n)
         out.append([t.permute(2, 0, 1, 3).reshape(n, nkv * G, hd) for t in (o, tol)]
                    + [t.permute(2, 0, 1).reshape(n, nkv * G) for t in (lse, delta + 2.0 ** -18 + 2.0 ** -22 * lse.abs().nan_to_num(posinf=0))] + [r0])
     return out
@@ -315,6 +324,23 @@ def test_scales_that_differ_widely_between_pages(ops):
         check_attention(ops, cache, model, plan, [320], [n], table, rows(5, n, 2 * G, 128, 1.5))
 
 
+def test_scores_that_grow_from_page_to_page(ops):
+    """Every page's largest score is far above the ones before it, in one kv head; far below in the other."""
+    for G, n in ((2, 1), (8, 40)):
+        table = [[0, 1, 2, 3, 4, 5]]
+        cache = empty_cache(ops, 6, 2, 128)
+        model = Model(cache)
+        for i in range(5):
+            k, v = rows(i, 64, 2, 128), rows(i + 20, 64, 2, 128)
+            k.view(64, 2, 128)[:, 0] *= 2.0 ** i
+            k.view(64, 2, 128)[:, 1] *= 2.0 ** (4 - i)
+            plan = ops.kv_plan(ints([64 * i]), ints([0, 64]), ints(table), 64, 64, 2 * G, 2, 128)
+            ops.kv_append(cache, plan, k, v)
+            model.append([64 * i], [64], table, k, v)
+        plan = step(ops, cache, model, [320], [n], table, G=G, seed=9)
+        check_attention(ops, cache, model, plan, [320], [n], table, rows(5, n, 2 * G, 128, 1.5), normwise=False)
+
+
 def test_large_and_tiny_queries_and_peaked_rows(ops):
     for n in (1, 60):
         table = [[3, 1, 0, 2, 4]]
@@ -346,6 +372,28 @@ def test_non_finite_queries_and_pages_reach_their_own_rows_only(ops):
         cache.scale[4, 1, 0] = math.nan  # what append makes of a key that is not finite
         model.s[4, 1, 0] = math.nan
         check_attention(ops, cache, model, plan, past, new, table, q)
+
+
+def test_a_page_that_is_not_finite_stays_out_of_the_rows_before_it(ops):
+    """A new page whose keys, values or both are not finite: rows of the same tile that end before it are untouched."""
+    for n in (2, 40):
+        past, table = [127 if n == 2 else 100], [[0, 1, 2]]
+        for bad_k, bad_v in ((True, False), (False, True), (True, True)):
+            cache = empty_cache(ops, 3, 2, 64)
+            model = Model(cache)
+            step(ops, cache, model, [0], past, table, G=3)
+            k, v = rows(1, n, 2, 64), rows(2, n, 2, 64)
+            if bad_k:
+                k[n - 1, 70] = math.inf
+            if bad_v:
+                v[n - 1, 3] = math.nan
+            plan = ops.kv_plan(ints(past), ints([0, n]), ints(table), n, n, 6, 2, 64)
+            ops.kv_append(cache, plan, k, v)
+            model.append(past, [n], table, k, v)
+            model.check(cache)
+            o, _ = check_attention(ops, cache, model, plan, past, [n], table, rows(6, n, 6, 64), normwise=False)
+            new_page = [past[0] + i >= 128 for i in range(n)]
+            assert o.view(n, 6, 64).isnan().any(2).any(1).tolist() == new_page
 
 
 def test_strided_rows(ops):

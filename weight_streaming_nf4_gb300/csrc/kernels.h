@@ -216,6 +216,10 @@ cudaError_t run_wgrad_tc(const float* P, const uint16_t* Q, const uint32_t* mask
 bool tmap_bf16_sw128(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
                      uint64_t pitch_bytes, uint32_t box_inner, uint32_t box_outer);
 
+// 3-D byte tensor map of `pages` tiles [rows, inner], inner 64 or 128 and the
+// swizzle as wide; the box is one tile (nf4_gemm.cu).
+bool tmap_u8_pages(CUtensorMap* m, const void* base, uint32_t inner, uint32_t rows, uint64_t pages);
+
 // ---- attention core (attention.cu) ----------------------------------------------------
 // Causal attention with grouped kv heads over n_seq sequences of S tokens:
 // q [M, nh*hd], k, v [M, nkv*hd] bf16 (M = n_seq*S, hd 64 or 128).  Forward:
@@ -262,7 +266,12 @@ struct KvShape;
 // The arguments of a plan, and of a call that uses a cache with it, checked.
 ws_status kv_shape(const ws_kv_plan* p, KvShape* s);
 ws_status kv_check(const ws_kv_cache* c, const ws_kv_plan* p, KvShape* s);
+// The chunk kernel (kv_chunk.cu): sequences of more than kTileRows rows.
+struct KvAttnArgs;
+size_t kv_chunk_bytes(const KvShape& s);  // of its partial results
+cudaError_t run_kv_chunk(const KvAttnArgs& a, const KvShape& s, void* partial, cudaStream_t st);
 cudaError_t kv_read_and_clear_dev_error(uint32_t* flags);
+cudaError_t kv_chunk_read_and_clear_dev_error(uint32_t* flags);
 
 // ---- one LoRA linear (linear.cu) --------------------------------------------------------
 size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K);

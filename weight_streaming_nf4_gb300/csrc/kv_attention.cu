@@ -5,7 +5,8 @@
 // n_kv_heads; a sequence's rows for one kv head are its (new token, head of the
 // group) pairs, R = i G + h % G, so a group's heads share what is read.
 //
-// Decoding rows (k_kv_decode).  Bound by memory: each code is read once.  One
+// Decoding rows (k_kv_decode; sequences of more than kTileRows rows go to
+// kv_chunk.cu).  Bound by memory: each code is read once.  One
 // warp has a contiguous share of the pages of all 16-row tiles (equal shares,
 // so ragged batches fill the device), copies a page's keys and values (8 KB
 // each at D = 128) into shared memory while the ones before are used, and joins
@@ -36,45 +37,10 @@ cudaError_t kv_read_and_clear_dev_error(uint32_t* flags) {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kDecodeWarps = 4;
 constexpr int kPMargin = 14;  // P in [0, 1] times 2^14 in fp16, so that pages with small scales keep bits
 
-struct KvAttnArgs {
-  const uint8_t *k, *v;
-  const float* scale;   // [n_pages][nkv][2]
-  const uint8_t* plan;
-  KvLayout L;
-  const int32_t* table;
-  const uint16_t* q;
-  uint16_t* o;
-  float* lse;           // [nh][T] or NULL
-  float* part_o;        // [slot][nkv][kTileRows][D] of cut tiles, divided by their sums
-  float* part_l;        // [slot][nkv][kTileRows] log2 of their sums
-  int64_t n_pages, sq, so, T;
-  int nkv, G, max_pages;
-  float sl2;            // softmax scale times log2(e)
-};
 
-// 2^x with the hardware approximation (relative error about 2^-22).
-WS_DEVINL float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-WS_DEVINL uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// Codes 0, 1 (lo) and 2, 3 (hi) of a word, exact in fp16.
-WS_DEVINL void decode4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
-      " cvt.rn.f16x2.e4m3x2 %1, b;\n}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
 WS_DEVINL void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                        uint32_t b1) {
   asm volatile(
@@ -140,7 +106,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 3) k_kv_decode(const __grid
   const int w = (int)blockIdx.x * kDecodeWarps + warp;
   const int head = w % a.nkv, u = w / a.nkv;
   if (u >= U) return;
-  const int begin = unit_start(u, W, U), end = unit_start(u + 1, W, U);
+  const int begin = (int)unit_start(u, W, U), end = (int)unit_start(u + 1, W, U);
 
   // the steps: pages begin .. end - 1 of the tiles' pages behind one another
   auto fill = [&](Step& s) {
@@ -282,8 +248,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 3) k_kv_decode(const __grid
       // softmax: columns (rows of q) 2t, 2t + 1; tokens 16 (g / 2) + 4 mt + g % 2 (+ 2)
       const int tok0 = cur.p * kPage + 16 * (g >> 1) + (g & 1);
       const bool tail = (cur.p + 1) * kPage > first_lim;
-      float vr = cur.vs == 0.0f ? 0.0f : cur.vs / vref;
-      if (!(cur.vs <= vref)) {  // a larger scale than any before (or NaN)
+      if (cur.vs > vref) {  // a larger scale than any before
         const float c = vref / cur.vs;
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq)
@@ -292,8 +257,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 3) k_kv_decode(const __grid
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[nq][ht][e] *= c;
         vref = cur.vs;
-        vr = cur.vs / vref;
       }
+      float vr = cur.vs == 0.0f ? 0.0f : cur.vs / vref;  // NaN for a page that holds one
       vr *= (float)(1 << kPMargin);
       uint32_t bp[NQ][4][2];
 #pragma unroll
@@ -346,8 +311,14 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 3) k_kv_decode(const __grid
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            bp[nq][mt][h] = transpose8x8(pack_f16x2(s[nq][mt][2 * h] * vr, s[nq][mt][2 * h + 1] * vr));
+          for (int h = 0; h < 2; ++h) {
+            float x0 = s[nq][mt][2 * h] * vr, x1 = s[nq][mt][2 * h + 1] * vr;
+            if (tail) {  // a row that does not see a token gets none of its page's scale, NaN included
+              if (tok0 + 4 * mt + 2 * h >= lim[nq][0]) x0 = 0.0f;
+              if (tok0 + 4 * mt + 2 * h >= lim[nq][1]) x1 = 0.0f;
+            }
+            bp[nq][mt][h] = transpose8x8(pack_f16x2(x0, x1));
+          }
       }
 
       if (!__all_sync(0xffffffffu, mbar_wait(&bars[1], phase, DERR_TIMEOUT_FULL))) {
@@ -497,7 +468,7 @@ KvWork kv_work(const KvShape& s, const KvLayout& L) {
   const size_t rows = (size_t)(2 * L.max_units) * s.nkv * kTileRows;
   KvWork w;
   w.part_l = rows * s.hd * 4;
-  w.bytes = w.part_l + rows * 4;
+  w.bytes = (w.part_l + rows * 4 + 15) / 16 * 16;
   return w;
 }
 
@@ -525,7 +496,7 @@ ws_status ws_attention_kv_workspace_size(const ws_kv_plan* plan, size_t* bytes) 
   const ws_status st = kv_shape(plan, &s);
   if (st != WS_OK) return st;
   if (!bytes) return WS_ERR_INVALID;
-  *bytes = kv_work(s, kv_layout(s)).bytes;
+  *bytes = kv_work(s, kv_layout(s)).bytes + kv_chunk_bytes(s);
   return WS_OK;
 }
 
@@ -544,7 +515,7 @@ ws_status ws_attention_kv(const ws_kv_cache* cache, const ws_kv_plan* plan, cons
   KvAttnArgs a;
   a.L = kv_layout(s);
   const KvWork w = kv_work(s, a.L);
-  if (ws_bytes < w.bytes) return WS_ERR_OOM;
+  if (ws_bytes < w.bytes + kv_chunk_bytes(s)) return WS_ERR_OOM;
   a.k = cache->k;
   a.v = cache->v;
   a.scale = cache->scale;
@@ -564,18 +535,22 @@ ws_status ws_attention_kv(const ws_kv_cache* cache, const ws_kv_plan* plan, cons
   a.max_pages = s.max_pages;
   a.sl2 = scale * kLog2e;
   cudaStream_t st = (cudaStream_t)stream;
-  const bool few = (int64_t)s.max_new * a.G <= 8;  // no tile has more than eight rows
-  cudaError_t e;
-  if (s.hd == 64)
-    e = few ? launch_decode<64, 1>(a, a.L.max_units, st) : launch_decode<64, 2>(a, a.L.max_units, st);
-  else
-    e = few ? launch_decode<128, 1>(a, a.L.max_units, st) : launch_decode<128, 2>(a, a.L.max_units, st);
+  cudaError_t e = cudaSuccess;
+  if (a.L.c_max_tiles > 0) e = run_kv_chunk(a, s, static_cast<uint8_t*>(workspace) + w.bytes, st);
   if (e != cudaSuccess) return WS_ERR_CUDA;
-  // cut tiles: one share's end each at most
-  const dim3 grid((unsigned)std::min<int64_t>(a.L.max_units, a.L.max_tiles), (unsigned)s.nkv,
-                  (unsigned)std::min<int64_t>(kTileRows, (int64_t)s.max_new * a.G));
-  note_launch();
-  e = launch_pdl(s.hd == 64 ? k_kv_join<64> : k_kv_join<128>, grid, dim3(kJoinWarps * 32), 0, st, a);
+  if (a.L.max_tiles > 0) {
+    const bool few = std::min<int64_t>((int64_t)s.max_new * a.G, kTileRows) <= 8;  // rows of a tile
+    if (s.hd == 64)
+      e = few ? launch_decode<64, 1>(a, a.L.max_units, st) : launch_decode<64, 2>(a, a.L.max_units, st);
+    else
+      e = few ? launch_decode<128, 1>(a, a.L.max_units, st) : launch_decode<128, 2>(a, a.L.max_units, st);
+    if (e != cudaSuccess) return WS_ERR_CUDA;
+    // cut tiles: one share's end each at most
+    const dim3 grid((unsigned)std::min<int64_t>(a.L.max_units, a.L.max_tiles), (unsigned)s.nkv,
+                    (unsigned)std::min<int64_t>(kTileRows, (int64_t)s.max_new * a.G));
+    note_launch();
+    e = launch_pdl(s.hd == 64 ? k_kv_join<64> : k_kv_join<128>, grid, dim3(kJoinWarps * 32), 0, st, a);
+  }
   return e == cudaSuccess ? WS_OK : WS_ERR_CUDA;
 }
 

@@ -76,17 +76,20 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const KvPlanArgs a) {
   const int tid = (int)threadIdx.x, n = a.s.n_seq, G = a.s.nh / a.s.nkv;
   KvHeader* hdr = reinterpret_cast<KvHeader*>(a.data);
   int4* seq = reinterpret_cast<int4*>(a.data + a.L.seq);
-  int2* pre = reinterpret_cast<int2*>(a.data + a.L.pre);  // pages to append to, tiles
+  int4* pre = reinterpret_cast<int4*>(a.data + a.L.pre);
   int4* append = reinterpret_cast<int4*>(a.data + a.L.append);
   int4* tile = reinterpret_cast<int4*>(a.data + a.L.tile);
   int4* split = reinterpret_cast<int4*>(a.data + a.L.split);
   int* unit = reinterpret_cast<int*>(a.data + a.L.unit);
+  int4* c_tile = reinterpret_cast<int4*>(a.data + a.L.c_tile);
+  int4* c_split = reinterpret_cast<int4*>(a.data + a.L.c_split);
+  int4* c_unit = reinterpret_cast<int4*>(a.data + a.L.c_unit);
   const int room = a.s.max_pages * kPage;
 
-  int n_append = 0, n_tiles = 0;
+  int n_append = 0, n_tiles = 0, c_tiles = 0;
   for (int base = 0; base < n; base += kPlanThreads) {
     const int s = base + tid;
-    int pages = 0, tiles = 0;
+    int pages = 0, tiles = 0, chunks = 0;
     if (s < n) {
       const int past = min(max(a.past[s], 0), room);
       const int row = min(max(a.start[s], 0), (int)a.s.T);
@@ -95,18 +98,23 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const KvPlanArgs a) {
       seq[s] = make_int4(past, row, c, 0);
       if (c > 0) {
         pages = (past + c + kPage - 1) / kPage - past / kPage;
-        tiles = (c * G + kTileRows - 1) / kTileRows;
+        if (c * G <= kTileRows)
+          tiles = 1;
+        else
+          chunks = (c * G + kChunkRows - 1) / kChunkRows;
       }
     }
-    int tp, tt;
-    const int p0 = block_scan(pages, &tp), t0 = block_scan(tiles, &tt);
-    if (s < n) pre[s] = make_int2(n_append + p0, n_tiles + t0);
+    int tp, tt, tc;
+    const int p0 = block_scan(pages, &tp), t0 = block_scan(tiles, &tt), c0 = block_scan(chunks, &tc);
+    if (s < n) pre[s] = make_int4(n_append + p0, n_tiles + t0, c_tiles + c0, 0);
     n_append += tp;
     n_tiles += tt;
+    c_tiles += tc;
   }
   // row ranges that overlap could name more than there is room for
   n_append = min(n_append, (int)a.L.max_append);
   n_tiles = min(n_tiles, (int)a.L.max_tiles);
+  c_tiles = min(c_tiles, (int)a.L.c_max_tiles);
   __syncthreads();
 
   for (int i = tid; i < n_append; i += kPlanThreads) {
@@ -118,20 +126,18 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const KvPlanArgs a) {
     append[i] = make_int4(q.y + lo - q.x, page >= 0 ? page : -1, lo - p * kPage, hi - lo);
   }
 
+  // ---- decode: one tile a sequence
   int W = 0;
   for (int base = 0; base < n_tiles; base += kPlanThreads) {
     const int i = base + tid;
-    int pages = 0, s = 0, r0 = 0;
+    int pages = 0, s = 0;
     if (i < n_tiles) {
       s = last_at_most(n, i, [&](int j) { return pre[j].y; });
-      const int4 q = seq[s];
-      r0 = (i - pre[s].y) * kTileRows;
-      const int last = min(q.z * G, r0 + kTileRows) - 1;
-      pages = (q.x + last / G) / kPage + 1;
+      pages = (seq[s].x + seq[s].z - 1) / kPage + 1;
     }
     int total;
     const int at = block_scan(pages, &total);
-    if (i < n_tiles) tile[i] = make_int4(s, r0, W + at, -1);
+    if (i < n_tiles) tile[i] = make_int4(s, 0, W + at, -1);
     W += total;
   }
   if (tid == 0) tile[n_tiles] = make_int4(0, 0, W, -1);
@@ -157,13 +163,63 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const KvPlanArgs a) {
   }
   if (n_tiles > 0)
     for (int u = tid; u < U; u += kPlanThreads)
-      unit[u] = last_at_most(n_tiles, unit_start(u, W, U), [&](int j) { return tile[j].z; });
+      unit[u] = last_at_most(n_tiles, (int)unit_start(u, W, U), [&](int j) { return tile[j].z; });
+
+  // ---- chunk: 256-row tiles, shares of all heads' steps
+  int Wc = 0;
+  for (int base = 0; base < c_tiles; base += kPlanThreads) {
+    const int i = base + tid;
+    int steps = 0, s = 0, r0 = 0;
+    if (i < c_tiles) {
+      s = last_at_most(n, i, [&](int j) { return pre[j].z; });
+      r0 = (i - pre[s].z) * kChunkRows;
+      const int last = min(seq[s].z * G, r0 + kChunkRows) - 1;
+      steps = (seq[s].x + last / G) / (2 * kPage) + 1;
+    }
+    int total;
+    const int at = block_scan(steps, &total);
+    if (i < c_tiles) c_tile[i] = make_int4(s, r0, Wc + at, 0);
+    Wc += total;
+  }
+  if (tid == 0) c_tile[c_tiles] = make_int4(0, 0, Wc, 0);
+  __syncthreads();
+  int Uc = 0, n_cut = 0;
+  if (c_tiles > 0) {
+    const int64_t all = (int64_t)Wc * a.s.nkv;
+    Uc = (int)max((int64_t)1, min(a.L.c_max_units, all / kChunkMinSteps));
+    // a unit's start cuts a (head, tile) pair, or lies between two; units that start in one pair come together
+    for (int base = 0; base <= Uc; base += kPlanThreads) {
+      const int u = base + tid;
+      int t = 0, h = a.s.nkv;
+      bool cuts = false, first = false;
+      if (u < Uc) {
+        const int64_t x = unit_start(u, all, Uc);
+        h = (int)(x / Wc);
+        const int y = (int)(x % Wc);
+        t = last_at_most(c_tiles, y, [&](int j) { return c_tile[j].z; });
+        cuts = y != c_tile[t].z;
+        first = cuts && unit_of((int64_t)h * Wc + c_tile[t].z, all, Uc) == u - 1;
+      }
+      int total;
+      const int j = n_cut + block_scan(first, &total);
+      if (u <= Uc) c_unit[u] = make_int4(t, h, cuts ? (first ? j : j - 1) : -1, 0);
+      if (first) {
+        const int64_t end = (int64_t)h * Wc + c_tile[t + 1].z;
+        c_split[j] = make_int4(t, u - 1 + j, unit_of(end - 1, all, Uc) - (u - 1) + 1, h);
+      }
+      n_cut += total;
+    }
+  }
   if (tid == 0) {
     hdr->n_append = n_append;
     hdr->n_tiles = n_tiles;
     hdr->pages = W;
     hdr->units = n_tiles > 0 ? U : 0;
     hdr->n_split = n_split;
+    hdr->c_tiles = c_tiles;
+    hdr->c_steps = Wc;
+    hdr->c_units = Uc;
+    hdr->c_split = n_cut;
   }
 }
 
@@ -178,23 +234,13 @@ struct AppendArgs {
   int nkv;
 };
 
-// Two codes of the nearest e4m3 values (ties to even); a in the low byte.
-WS_DEVINL uint32_t e4m3x2(float a, float b) {
-  uint16_t h;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(b), "f"(a));
-  return h;
-}
 // The codes of a word again, for a scale 1/ratio times theirs.
 WS_DEVINL uint32_t rescale4(uint32_t w, float ratio) {
   uint32_t out = 0;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    uint32_t h2;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(w >> (16 * i))));
     float lo, hi;
-    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}"
-        : "=f"(lo), "=f"(hi)
-        : "r"(h2));
+    e4m3x2_values((w >> (16 * i)) & 0xffffu, lo, hi);
     out |= e4m3x2(lo * ratio, hi * ratio) << (16 * i);
   }
   return out;
@@ -276,6 +322,8 @@ __global__ void __launch_bounds__(D) k_kv_append(const AppendArgs a) {
   if (lo > 0 && !(old.x <= ks) && !isnan(ks)) ks = old.x;
   if (lo > 0 && !(old.y <= vs) && !isnan(vs)) vs = old.y;
   const bool grow_k = lo > 0 && ks > old.x, grow_v = lo > 0 && vs > old.y;
+  // codes under a NaN scale are zero: a code that is NaN would reach rows that do not see it, as 0 * NaN
+  const bool bad_k = isnan(ks), bad_v = isnan(vs);
   const float ik = 1.0f / ks, iv = 1.0f / vs;
 
 #pragma unroll
@@ -288,7 +336,7 @@ __global__ void __launch_bounds__(D) k_kv_append(const AppendArgs a) {
       for (int j = 0; j < 2; ++j)
         w[j] = e4m3x2(elem(xk[i], 4 * j) * ik, elem(xk[i], 4 * j + 1) * ik) |
                e4m3x2(elem(xk[i], 4 * j + 2) * ik, elem(xk[i], 4 * j + 3) * ik) << 16;
-      *dst = make_uint2(w[0], w[1]);
+      *dst = bad_k ? make_uint2(0, 0) : make_uint2(w[0], w[1]);
     } else if (grow_k && p < lo) {
       const uint2 o = *dst;
       *dst = make_uint2(rescale4(o.x, old.x * ik), rescale4(o.y, old.x * ik));
@@ -303,7 +351,8 @@ __global__ void __launch_bounds__(D) k_kv_append(const AppendArgs a) {
     for (int h = 0; h < 2; ++h)
       w[h] = e4m3x2(elem(xv[4 * h], j) * iv, elem(xv[4 * h + 1], j) * iv) |
              e4m3x2(elem(xv[4 * h + 2], j) * iv, elem(xv[4 * h + 3], j) * iv) << 16;
-    *reinterpret_cast<uint2*>(vt + (8 * c + j) * kPage + ((t ^ (c & 7)) << 3)) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(vt + (8 * c + j) * kPage + ((t ^ (c & 7)) << 3)) =
+        bad_v ? make_uint2(0, 0) : make_uint2(w[0], w[1]);
   }
   __syncthreads();
 #pragma unroll
@@ -351,13 +400,15 @@ ws_status kv_shape(const ws_kv_plan* p, KvShape* s) {
     return WS_ERR_SHAPE;
   if (p->head_dim != 64 && p->head_dim != 128) return WS_ERR_SHAPE;
   *s = KvShape{p->T, p->n_seq, p->max_pages, p->max_new, p->n_heads, p->n_kv_heads, p->head_dim};
+  // the chunk kernel's steps of one head are counted in 32 bits
+  if (kv_chunk_tiles(*s) * (s->max_pages / 2 + 1) > 0x7fffffff) return WS_ERR_SHAPE;
   return WS_OK;
 }
 ws_status kv_check(const ws_kv_cache* c, const ws_kv_plan* p, KvShape* s) {
   const ws_status st = kv_shape(p, s);
   if (st != WS_OK) return st;
   if (!c || !c->k || !c->v || !c->scale || !p->data || !p->page_table) return WS_ERR_INVALID;
-  if (c->n_pages < 1 || c->n_pages > 0x7fffffff || c->n_kv_heads != s->nkv || c->head_dim != s->hd)
+  if (c->n_pages < 1 || c->n_pages > 0x7fffffff / s->nkv || c->n_kv_heads != s->nkv || c->head_dim != s->hd)
     return WS_ERR_SHAPE;
   if (!al16k(c->k) || !al16k(c->v) || !al16k(c->scale) || !al16k(p->data) || !al4k(p->page_table))
     return WS_ERR_ALIGN;

@@ -1,0 +1,838 @@
+// kv_chunk.cu -- attention over the paged 8-bit cache for sequences of more
+// than 16 rows (prompts, in chunks behind what the cache holds): the definition
+// is that of kv_attention.cu, the products are tcgen05's.
+//
+// A tile is 256 rows (new token, head of the group) of one kv head, two slots of
+// 128; a step is two pages.  For each step and slot
+//   S = Q K^T    kind::f8f6f4: the key codes as TMA brings them, nothing decoded.
+//                A row of Q enters as a power of two times hi + lo, two e4m3 numbers:
+//                all eight bits of bf16, down to 2^-10 of the row's largest
+//                element, and an absolute error of 2^-17.8 of it below; two
+//                products at twice fp16's rate cost what one fp16 product does
+//   P = 2^(S c - m), fp16, over the same columns of tensor memory
+//   O += P V     kind::f16, A from tensor memory, V decoded to fp16 (exact) by two
+//                warps, once for both slots
+// A row is a thread's, so its maximum and sum need no exchange.  m moves only
+// when a row's maximum has grown by 2^8 or more (P stays below 2^15 in fp16):
+// then the softmax warps wait for the products before and rescale O in tensor
+// memory.  Keys' scales go into c, values' into P relative to the largest so far.
+// A tile of up to 128 rows has both slots on the same rows, on steps of their
+// own (even, odd), joined at the end: without that the products would wait for
+// the softmax at every step.
+//
+// Bound by the tensor pipe (1024 clocks a step and slot at D = 128) and shared
+// memory beside it; the softmax of one slot runs under the products of the other.
+// Shares of equal numbers of steps, over all heads, one CTA an SM: a share
+// that begins or ends inside a tile leaves a partial result, joined by
+// k_kv_chunk_join in the order of the shares.
+//
+// Warps: 0 loads, 1 issues the products, 2 and 3 decode values, 4-7 and 8-11 are the
+// slots' rows (three warps on each quarter of an SM: 168 registers a thread).  Every wait is bounded (see common.cuh).
+#define WS_KV_TU 1
+#include <math.h>
+
+#include "kv_plan.cuh"
+
+namespace ws {
+
+cudaError_t kv_chunk_read_and_clear_dev_error(uint32_t* flags) {
+  cudaError_t e = cudaMemcpyFromSymbol(flags, g_dev_error, sizeof(uint32_t));
+  if (e != cudaSuccess) return e;
+  const uint32_t zero = 0;
+  return cudaMemcpyToSymbol(g_dev_error, &zero, sizeof(uint32_t));
+}
+
+namespace {
+
+constexpr int kChThreads = 384;
+constexpr int kSlotRows = 128;
+constexpr int kStepTokens = 2 * kPage;
+constexpr int kInfo = 64;      // pages of a window of the pages' list
+constexpr int kLag = 8;        // powers of two by which a row's maximum may outgrow m
+constexpr int kChMargin = 7;   // P 2^7: below 2^15 in fp16
+
+struct ChunkArgs {
+  KvAttnArgs a;
+  CUtensorMap tk;  // keys as [n_pages n_kv_heads][64][D] bytes
+  float* part_o;   // [slot][kChunkRows][D], divided by their sums
+  float* part_l;   // [slot][kChunkRows] log2 of their sums
+};
+
+template <int D>
+struct ChSmem {
+  static constexpr int KST = 3;  // steps of keys in flight
+  static constexpr int RST = 2;  // of value codes
+  static constexpr int VST = 2;  // decoded
+  static constexpr uint32_t QP = kSlotRows * D;          // one part of a slot's rows
+  static constexpr uint32_t K = kStepTokens * D;
+  static constexpr uint32_t V = kStepTokens * D * 2;
+  static constexpr uint32_t OFF_K = 4 * QP;
+  static constexpr uint32_t OFF_R = OFF_K + KST * K;
+  static constexpr uint32_t OFF_V = OFF_R + RST * K;
+  static constexpr uint32_t OFF_INFO = OFF_V + VST * V;
+  static constexpr uint32_t OFF_ML = OFF_INFO + 2 * kInfo * 16;
+  static constexpr uint32_t OFF_BAR = OFF_ML + kSlotRows * 16;
+  static constexpr uint32_t BYTES = OFF_BAR + 512 + 1024;
+};
+
+// A page of a step: its place (-1: none) and scales.
+struct PageInfo {
+  int page;
+  float ks, vs;
+  int pad;
+};
+
+// A share's stretch of one (head, tile).
+struct Seg {
+  int head, tile, r0, rows;  // rows of the tile
+  int seq, past, row0, n;
+  int s0, s1;                // its steps of the tile's
+  int slot;                  // of its partial result, -1: the tile is whole
+  bool dual;                 // both slots on the same rows
+};
+
+struct Share {
+  const int4 *tiles, *seqs, *units;
+  int64_t begin, end, at;
+  int W, u, tile, head, nkv, G;
+  WS_DEVINL Share(const ChunkArgs& c, int unit) {
+    const KvHeader* h = reinterpret_cast<const KvHeader*>(c.a.plan);
+    tiles = reinterpret_cast<const int4*>(c.a.plan + c.a.L.c_tile);
+    seqs = reinterpret_cast<const int4*>(c.a.plan + c.a.L.seq);
+    units = reinterpret_cast<const int4*>(c.a.plan + c.a.L.c_unit);
+    u = unit;
+    nkv = c.a.nkv;
+    G = c.a.G;
+    W = h->c_steps;
+    const int U = h->c_units;
+    begin = end = at = 0;
+    if (u >= U) return;
+    begin = unit_start(u, (int64_t)W * nkv, U);
+    end = unit_start(u + 1, (int64_t)W * nkv, U);
+    at = begin;
+    tile = units[u].x;
+    head = units[u].y;
+  }
+  WS_DEVINL bool next(Seg& s) {
+    if (at >= end) return false;
+    if (at != begin && (int64_t)(head + 1) * W == at) {  // the next head begins
+      ++head;
+      tile = 0;
+    } else if (at != begin) {
+      ++tile;
+    }
+    const int4 t = tiles[tile], q = seqs[t.x];
+    const int64_t base = (int64_t)head * W + t.z;
+    const int steps = tiles[tile + 1].z - t.z;
+    s.head = head;
+    s.tile = tile;
+    s.seq = t.x;
+    s.r0 = t.y;
+    s.past = q.x;
+    s.row0 = q.y;
+    s.n = q.z;
+    s.rows = min(kChunkRows, q.z * G - t.y);
+    s.s0 = (int)(at - base);
+    s.s1 = (int)min((int64_t)steps, end - base);
+    s.dual = s.rows <= kSlotRows;
+    // cut by this share's begin, or by its end
+    s.slot = s.s0 > 0 ? u + units[u].z : s.s1 < steps ? u + units[u + 1].z : -1;
+    at = base + s.s1;
+    return true;
+  }
+};
+
+WS_DEVINL void tc_mma_f8(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// A in tensor memory (fp16 pairs), B through a descriptor.
+WS_DEVINL void tc_mma_f16_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+WS_DEVINL void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
+      "%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+WS_DEVINL void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* bar, int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// Operand of D-byte rows, K-major, swizzled over D = 128 or 64 bytes; `base` is
+// that of the 32 bytes of the contraction step.
+template <int D>
+WS_DEVINL uint64_t desc_bytes(uint32_t base) {
+  if (D == 128) return smem_desc_sw128(base, 16, 1024);
+  return (uint64_t)((base >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)(512 >> 4) << 32) | (1ull << 46) |
+         (4ull << 61);
+}
+// Where 16-byte piece c of row r lies in it.
+template <int D>
+WS_DEVINL uint32_t swizzled(int r, int c) {
+  return D == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+WS_DEVINL bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
+
+template <int D>
+__global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constant__ ChunkArgs c) {
+  using L = ChSmem<D>;
+  constexpr int KST = L::KST, RST = L::RST, VST = L::VST;
+  constexpr uint32_t TM_S = 0, TM_O = 2 * kStepTokens, TM_COLS = 512;
+  constexpr uint32_t idS = (1u << 4) | ((kStepTokens >> 3) << 17) | ((kSlotRows >> 4) << 24);  // e4m3, e4m3, fp32
+  constexpr uint32_t idO = (1u << 4) | ((D >> 3) << 17) | ((kSlotRows >> 4) << 24);            // fp16, fp16, fp32
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sq = smem;  // [slot][hi, lo]
+  uint8_t* sk = smem + L::OFF_K;
+  uint8_t* sr = smem + L::OFF_R;
+  uint8_t* sv = smem + L::OFF_V;
+  PageInfo* info = reinterpret_cast<PageInfo*>(smem + L::OFF_INFO);  // [2][kInfo]
+  float4* ml = reinterpret_cast<float4*>(smem + L::OFF_ML);          // slot 1's m, l, vref of each row
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  uint64_t* k_full = bars;
+  uint64_t* k_empty = k_full + KST;
+  uint64_t* r_full = k_empty + KST;
+  uint64_t* r_empty = r_full + RST;
+  uint64_t* v_full = r_empty + RST;
+  uint64_t* v_empty = v_full + VST;
+  uint64_t* q_full = v_empty + VST;      // [slot]
+  uint64_t* s_full = q_full + 2;         // [slot]
+  uint64_t* p_full = s_full + 2;         // [slot][half]
+  uint64_t* o_done = p_full + 4;         // [slot][half]
+  uint64_t* i_full = o_done + 4;         // [window]
+  uint64_t* i_empty = i_full + 2;
+  uint64_t* ml_full = i_empty + 2;
+  uint64_t* o1_free = ml_full + 1;
+  uint64_t* drain = o1_free + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  volatile uint32_t* skip_flag = tmem_slot + 2;
+
+  const int warp = (int)warp_id(), lane = (int)lane_id();
+  if (threadIdx.x == 0) {
+    *abort_flag = 0u;
+    *skip_flag = (*(volatile uint32_t*)&g_dev_error != 0u) ? 1u : 0u;
+    for (int i = 0; i < KST; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < RST; ++i) {
+      mbar_init(&r_full[i], 1);
+      mbar_init(&r_empty[i], 2);
+    }
+    for (int i = 0; i < VST; ++i) {
+      mbar_init(&v_full[i], 2);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 4);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[2 * i], 4);
+      mbar_init(&p_full[2 * i + 1], 4);
+      mbar_init(&o_done[2 * i], 1);
+      mbar_init(&o_done[2 * i + 1], 1);
+      mbar_init(&i_full[i], 1);
+      mbar_init(&i_empty[i], 10);
+    }
+    mbar_init(ml_full, 4);
+    mbar_init(o1_free, 4);
+    mbar_init(drain, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, TM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_launch_dependents();
+  const bool run = *skip_flag == 0u;
+  Share share(c, (int)blockIdx.x);
+  const KvAttnArgs& a = c.a;
+  Seg sg;
+  // Steps are numbered through the share; step n's pages are 2 n and 2 n + 1 of
+  // the share's list of pages, in windows of kInfo.
+  auto info_of = [&](int64_t n, int half) -> const PageInfo& {
+    return info[(2 * n + half) % (2 * kInfo)];
+  };
+  auto give_up = [&]() { *abort_flag = 1u; };
+  // Enter the window that step n begins, if it begins one.
+  auto window = [&](int64_t n) {
+    if (n % (kInfo / 2) != 0) return true;
+    const int64_t w = n / (kInfo / 2);
+    return mbar_wait(&i_full[w & 1], (uint32_t)(w >> 1) & 1u, DERR_TIMEOUT_FULL);
+  };
+  // Leave the window that step n ends.
+  auto leave = [&](int64_t n) {
+    if ((n + 1) % (kInfo / 2) == 0 && lane == 0) mbar_arrive(&i_empty[(n / (kInfo / 2)) & 1]);
+  };
+
+  if (warp == 0) {
+    if (run) {
+      // the whole warp walks: every kInfo pages it looks up the next window
+      const int64_t total = share.end - share.begin;
+      Share ahead = share;  // the walk of the page list
+      Seg as;
+      bool more = ahead.next(as);
+      int as_step = more ? as.s0 : 0;
+      int64_t n = 0;  // steps loaded
+      bool ok = true;
+      while (n < total && ok) {
+        const int64_t w = n / (kInfo / 2);
+        // the window's pages: lane i has pages 2 i, 2 i + 1 = step n + i
+        ok = warp_all(!*abort_flag && mbar_wait(&i_empty[w & 1], ((uint32_t)(w >> 1) & 1u) ^ 1u, DERR_TIMEOUT_EMPTY));
+        if (!ok) break;
+        PageInfo mine[2];
+        int head = 0;
+        for (int i = 0; i < kInfo / 2; ++i) {
+          if (more && as_step == as.s1) {
+            more = ahead.next(as);
+            as_step = as.s0;
+          }
+          if (i == lane) {
+            head = as.head;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int p = 2 * as_step + h;
+              mine[h].page = more && p < a.max_pages ? a.table[(int64_t)as.seq * a.max_pages + p] : -1;
+              // pages that no row of the tile sees are not there
+              const int last = (min(as.n * a.G, as.r0 + kChunkRows) - 1) / a.G;
+              if (!more || p * kPage > as.past + last) mine[h].page = -1;
+            }
+          }
+          if (more) ++as_step;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          mine[h].ks = mine[h].vs = 0.0f;
+          if (mine[h].page >= a.n_pages) mine[h].page = -1;
+          if (mine[h].page >= 0) {
+            mine[h].page = mine[h].page * a.nkv + head;
+            const float2 s = *(reinterpret_cast<const float2*>(a.scale) + mine[h].page);
+            mine[h].ks = s.x;
+            mine[h].vs = s.y;
+          }
+          info[(2 * (n + lane) + h) % (2 * kInfo)] = mine[h];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&i_full[w & 1]);
+        const int64_t stop = min(total, n + kInfo / 2);
+        if (lane == 0) {
+          for (; n < stop; ++n) {
+            const PageInfo p0 = info_of(n, 0), p1 = info_of(n, 1);
+            const uint32_t bytes = ((p0.page >= 0) + (p1.page >= 0)) * kPage * D;
+            const int ks = (int)(n % KST), rs = (int)(n % RST);
+            if (*abort_flag || !mbar_wait(&k_empty[ks], ((uint32_t)(n / KST) & 1u) ^ 1u, DERR_TIMEOUT_EMPTY)) break;
+            mbar_arrive_expect_tx(&k_full[ks], bytes);
+            uint8_t* dk = sk + ks * L::K;
+            if (p0.page >= 0) tma_load_3d(dk, &c.tk, &k_full[ks], 0, 0, p0.page);
+            if (p1.page >= 0) tma_load_3d(dk + kPage * D, &c.tk, &k_full[ks], 0, 0, p1.page);
+            if (*abort_flag || !mbar_wait(&r_empty[rs], ((uint32_t)(n / RST) & 1u) ^ 1u, DERR_TIMEOUT_EMPTY)) {
+              mbar_wait(&k_full[ks], (uint32_t)(n / KST) & 1u, DERR_TIMEOUT_DRAIN);
+              break;
+            }
+            mbar_arrive_expect_tx(&r_full[rs], bytes);
+            uint8_t* dr = sr + rs * L::K;
+            if (p0.page >= 0) bulk_load(dr, a.v + (int64_t)p0.page * (kPage * D), kPage * D, &r_full[rs]);
+            if (p1.page >= 0)
+              bulk_load(dr + kPage * D, a.v + (int64_t)p1.page * (kPage * D), kPage * D, &r_full[rs]);
+          }
+          if (n < stop) {
+            give_up();
+            ok = false;
+          }
+        }
+        n = __shfl_sync(0xffffffffu, n, 0);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      }
+      // nothing may land after the CTA is gone
+      if (lane == 0) {
+        for (int64_t i = n > KST ? n - KST : 0; i < n; ++i)
+          mbar_wait(&k_full[i % KST], (uint32_t)(i / KST) & 1u, DERR_TIMEOUT_DRAIN);
+        for (int64_t i = n > RST ? n - RST : 0; i < n; ++i)
+          mbar_wait(&r_full[i % RST], (uint32_t)(i / RST) & 1u, DERR_TIMEOUT_DRAIN);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && run) {
+      bool ok = true;
+      int64_t n0 = 0;             // steps of the segments before
+      uint32_t qn[2] = {0, 0};    // segments of each slot
+      uint32_t pn[2] = {0, 0};    // P handed over by each slot (steps)
+      auto wait = [&](uint64_t* b, uint32_t parity, uint32_t why) {
+        if (ok && (*abort_flag || !mbar_wait(b, parity, why))) ok = false;
+        return ok;
+      };
+      // S of step j for slot s; the first to use the step waits for its keys, the last frees them
+      auto issue_s = [&](int j, int s, bool first, bool last) {
+        const int64_t n = n0 + j;
+        const int st = (int)(n % KST);
+        if (first && !wait(&k_full[st], (uint32_t)(n / KST) & 1u, DERR_TIMEOUT_FULL)) return;
+        tc_fence_after();
+        const uint32_t q = smem_u32(sq + s * 2 * L::QP), k = smem_u32(sk + st * L::K);
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i)
+            tc_mma_f8(tmem + TM_S + s * kStepTokens, desc_bytes<D>(q + part * L::QP + 32 * i),
+                      desc_bytes<D>(k + 32 * i), idS, (part | i) ? 1u : 0u);
+        tc_commit(&s_full[s]);
+        if (last) tc_commit(&k_empty[st]);
+      };
+      auto issue_pv = [&](int j, int s, bool first, bool last, bool begins) {
+        const int64_t n = n0 + j;
+        const int st = (int)(n % VST);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!wait(&p_full[2 * s + h], pn[s] & 1u, DERR_TIMEOUT_BFULL)) return;
+          if (h == 0 && first && !wait(&v_full[st], (uint32_t)(n / VST) & 1u, DERR_TIMEOUT_FULL)) return;
+          tc_fence_after();
+          const uint32_t v = smem_u32(sv + st * L::V + h * (D * 128));
+#pragma unroll
+          for (int i = 0; i < kPage / 16; ++i)
+            tc_mma_f16_ta(tmem + TM_O + s * D, tmem + TM_S + s * kStepTokens + h * 32 + i * 8,
+                          smem_desc_sw128(v + 32 * i, 16, 1024), idO, (begins && h == 0 && i == 0) ? 0u : 1u);
+          tc_commit(&o_done[2 * s + h]);
+        }
+        ++pn[s];
+        if (last) tc_commit(&v_empty[st]);
+      };
+      while (ok && share.next(sg)) {
+        const int J = sg.s1 - sg.s0;
+        for (int s = 0; s < 2 && ok; ++s) {
+          if (sg.dual && s >= J) continue;
+          if (!wait(&q_full[s], qn[s] & 1u, DERR_TIMEOUT_FULL)) break;
+          ++qn[s];
+        }
+        if (sg.dual) {
+          for (int j = 0; j < min(2, J) && ok; ++j) issue_s(j, j, true, true);
+          for (int j = 0; j < J && ok; ++j) {
+            issue_pv(j, j & 1, true, true, j < 2);
+            if (ok && j + 2 < J) issue_s(j + 2, j & 1, true, true);
+          }
+        } else {
+          for (int s = 0; s < 2 && ok; ++s) issue_s(0, s, s == 0, s == 1);
+          for (int j = 0; j < J && ok; ++j)
+            for (int s = 0; s < 2 && ok; ++s) {
+              issue_pv(j, s, s == 0, s == 1, j == 0);
+              if (ok && j + 1 < J) issue_s(j + 1, s, s == 0, s == 1);
+            }
+        }
+        n0 += J;
+      }
+      if (!ok) give_up();
+      tc_commit(drain);
+      mbar_wait(drain, 0u, DERR_TIMEOUT_DRAIN);
+    }
+  } else if (warp < 4) {
+    // ---- values: codes [D][64 tokens] of each page -> fp16 operand rows of 64 tokens
+    if (run) {
+      const int w = warp - 2;
+      int64_t n = 0;
+      bool ok = true;
+      while (ok && share.next(sg)) {
+        const int kv_end = sg.past + sg.n;
+        for (int j = sg.s0; j < sg.s1 && ok; ++j, ++n) {
+          const int rs = (int)(n % RST), st = (int)(n % VST);
+          ok = warp_all(!*abort_flag && window(n) &&
+                        mbar_wait(&v_empty[st], ((uint32_t)(n / VST) & 1u) ^ 1u, DERR_TIMEOUT_EMPTY) &&
+                        mbar_wait(&r_full[rs], (uint32_t)(n / RST) & 1u, DERR_TIMEOUT_FULL));
+          if (!ok) break;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const bool have = info_of(n, h).page >= 0;
+            const int left = kv_end - (2 * j + h) * kPage;  // tokens of the page that are the sequence's
+            const uint8_t* src = sr + rs * L::K + h * (kPage * D);
+            uint8_t* dst = sv + st * L::V + h * (D * 128);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              const int r = w * (D / 2) + 8 * i + (lane >> 2), u = lane & 3;
+              uint32_t x[4] = {0, 0, 0, 0};
+              if (have) {
+                const uint4 v = *reinterpret_cast<const uint4*>(src + r * kPage + 16 * u);
+                x[0] = v.x;
+                x[1] = v.y;
+                x[2] = v.z;
+                x[3] = v.w;
+                if (left < kPage) {  // places behind the last token hold anything, NaN too
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const int m = left - 16 * u - 4 * e;
+                    x[e] &= m >= 4 ? 0xffffffffu : m <= 0 ? 0u : (1u << (8 * m)) - 1u;
+                  }
+                }
+              }
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) decode4(x[e], y[2 * e], y[2 * e + 1]);
+              sts128(dst + swizzled<128>(r, 2 * u), y[0], y[1], y[2], y[3]);
+              sts128(dst + swizzled<128>(r, 2 * u + 1), y[4], y[5], y[6], y[7]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&r_empty[rs]);
+            mbar_arrive(&v_full[st]);
+          }
+          leave(n);
+        }
+      }
+      if (!ok) give_up();
+    }
+  } else if (run) {
+    // ---- rows: thread <-> row r of slot s
+    const int s = (warp - 4) >> 2, q4 = warp & 3, r = q4 * 32 + lane;
+    const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
+    const uint32_t t_s = trow + TM_S + s * kStepTokens;
+    uint8_t* q_hi = sq + s * 2 * L::QP;
+    int64_t n0 = 0;
+    uint32_t sn = 0;         // steps of this slot
+    uint32_t dn = 0;         // dual segments with both slots in use
+    bool ok = true;
+    auto wait = [&](uint64_t* b, uint32_t parity, uint32_t why) {
+      ok = warp_all(!*abort_flag && mbar_wait(b, parity, why));
+      return ok;
+    };
+    while (ok && share.next(sg)) {
+      const int J = sg.s1 - sg.s0;
+      const int local = sg.dual ? r : s * kSlotRows + r;  // row of the tile
+      const bool valid = local < sg.rows;
+      const int R = sg.r0 + local, tok = valid ? R / a.G : 0;
+      const int h = sg.head * a.G + R - tok * a.G;
+      const int lim = valid ? sg.past + tok + 1 : 0;  // tokens that the row sees
+      const bool active = !sg.dual || s < J;
+      float m = -INFINITY, l = 0.0f, vref = 0.0f, qs = 0.0f;
+      if (active) {
+        // the row of Q in two e4m3 parts
+        const uint16_t* src = a.q + (int64_t)(sg.row0 + tok) * a.sq + h * D;
+        uint32_t top = 0;
+        uint4 x[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          x[i] = valid ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+          top = __vmaxu2(top, __vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu));
+          top = __vmaxu2(top, __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+        }
+        top = max(top & 0xffffu, top >> 16);
+        // the largest at (224, 448]; a row that is not finite gives NaN
+        const int e = (int)(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u);
+        const float qk = __uint_as_float((uint32_t)(127 - max(e, -126)) << 23);
+        qs = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : a.sl2 / qk;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t w[4] = {x[2 * i + j].x, x[2 * i + j].y, x[2 * i + j].z, x[2 * i + j].w};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t ph[2], pl[2];
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const float f0 = bf16_lo(w[2 * k + y]) * qk, f1 = bf16_hi(w[2 * k + y]) * qk;
+                float g0, g1;
+                ph[y] = e4m3x2(f0, f1);
+                e4m3x2_values(ph[y], g0, g1);
+                pl[y] = e4m3x2(f0 - g0, f1 - g1);
+              }
+              hi[2 * j + k] = ph[0] | ph[1] << 16;
+              lo[2 * j + k] = pl[0] | pl[1] << 16;
+            }
+          }
+          sts128(q_hi + swizzled<D>(r, i), hi[0], hi[1], hi[2], hi[3]);
+          sts128(q_hi + L::QP + swizzled<D>(r, i), lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[s]);
+      }
+      int done = 0;  // halves handed over in this segment
+      for (int j = 0; j < J && ok; ++j) {
+        const int64_t n = n0 + j;
+        if (!(ok = warp_all(!*abort_flag && window(n)))) break;
+        if (sg.dual && (j & 1) != s) {
+          leave(n);
+          continue;
+        }
+        if (!wait(&s_full[s], sn & 1u, DERR_TIMEOUT_ACC)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int half = 0; half < 2 && ok; ++half) {
+          const PageInfo pi = info_of(n, half);
+          uint32_t p[32];
+          if (pi.page < 0) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) p[i] = 0u;
+          } else {
+            float v[64];
+            {
+              uint32_t x0[32], x1[32];
+              tmem_ld_32x32b_x32(t_s + half * kPage, x0);
+              tmem_ld_32x32b_x32(t_s + half * kPage + 32, x1);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                v[i] = __uint_as_float(x0[i]);
+                v[32 + i] = __uint_as_float(x1[i]);
+              }
+            }
+            float cf = qs * pi.ks;
+            cf = cf < 1e-37f ? 1e-37f : cf;  // not below fp32's range: -inf * 0 is NaN
+            const int vis = lim - (2 * (sg.s0 + j) + half) * kPage;
+            const bool masked = __any_sync(0xffffffffu, vis < kPage);
+            if (masked) {
+#pragma unroll
+              for (int i = 0; i < 64; ++i)
+                if (i >= vis) v[i] = -INFINITY;
+            }
+            float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 64; i += 4)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) t[k] = fmaxf(t[k], v[i + k]);
+            const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * cf;
+            const bool up = top > m + kLag || pi.vs > vref;
+            if (__any_sync(0xffffffffu, up)) {
+              const float nm = top > m + kLag ? top : m;
+              const float nv = fmaxf(vref, pi.vs);  // a NaN scale is no reference
+              float f = nm == m ? 1.0f : ex2(m - nm);
+              l *= f;
+              f *= vref == nv ? 1.0f : vref / nv;
+              m = nm;
+              vref = nv;
+              if (done > 0) {
+                // O of the halves before
+                if (!wait(&o_done[2 * s + (half ^ 1)], (sn + half - 1) & 1u, DERR_TIMEOUT_ACC)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int cc = 0; cc < D; cc += 32) {
+                  uint32_t o[32];
+                  tmem_ld_32x32b_x32(trow + TM_O + s * D + cc, o);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                  tmem_st_32x32b_x32(trow + TM_O + s * D + cc, o);
+                }
+                tmem_st_wait();
+              }
+            }
+            const float ref = m == -INFINITY ? 0.0f : m;
+            const float vr = (pi.vs == 0.0f ? 0.0f : pi.vs / vref) * (float)(1 << kChMargin);
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+              float y0 = ex2(fmaf(v[i], cf, -ref)), y1 = ex2(fmaf(v[i + 1], cf, -ref));
+              if (masked) {  // a row gets none of the scales of a page that it does not see, NaN included
+                if (i >= vis) y0 = 0.0f;
+                if (i + 1 >= vis) y1 = 0.0f;
+              }
+              sum[i & 2] += y0;
+              sum[(i & 2) + 1] += y1;
+              y0 *= vr;
+              y1 *= vr;
+              if (masked) {
+                if (i >= vis) y0 = 0.0f;
+                if (i + 1 >= vis) y1 = 0.0f;
+              }
+              p[i / 2] = pack_f16x2(y0, y1);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          }
+          tmem_st_32x32b_x32(t_s + half * 32, p);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * s + half]);
+          ++done;
+        }
+        if (!ok) break;
+        ++sn;
+        leave(n);
+      }
+      if (!ok) break;
+      n0 += J;
+      // ---- the segment's end
+      const bool joined = sg.dual && J > 1;
+      if (active && !wait(&o_done[2 * s + 1], (sn - 1) & 1u, DERR_TIMEOUT_ACC)) break;
+      tc_fence_after();
+      float m1 = -INFINITY, l1 = 0.0f, v1 = 0.0f;
+      if (joined) {
+        if (s == 1) {
+          ml[r] = make_float4(m, l, vref, 0.0f);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ml_full);
+          // slot 0 has read O of slot 1 before this slot goes on
+          if (!wait(o1_free, dn & 1u, DERR_TIMEOUT_ACC)) break;
+          ++dn;
+        } else {
+          if (!wait(ml_full, dn & 1u, DERR_TIMEOUT_ACC)) break;
+          tc_fence_after();
+          ++dn;
+          const float4 y = ml[r];
+          m1 = y.x;
+          l1 = y.y;
+          v1 = y.z;
+        }
+      }
+      if (sg.dual && s == 1) continue;
+      const float mm = fmaxf(m, m1), ref = mm == -INFINITY ? 0.0f : mm;
+      const float e0 = m == -INFINITY ? 0.0f : ex2(m - ref), e1 = m1 == -INFINITY ? 0.0f : ex2(m1 - ref);
+      const float sum = l * e0 + l1 * e1;
+      const bool none = sum == 0.0f;
+      const float inv = none ? 0.0f : (1.0f / (1 << kChMargin)) / sum;
+      const float f0 = e0 * vref * inv, f1 = e1 * v1 * inv;
+      const float lse2 = none ? -INFINITY : mm + log2f(sum);
+      uint16_t* dst = a.o + (int64_t)(sg.row0 + tok) * a.so + h * D;
+      const int64_t part = (int64_t)sg.slot * kChunkRows + local;
+      const bool v8 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0u && (a.so & 15) == 0;
+#pragma unroll 1
+      for (int cc = 0; cc < D; cc += 32) {
+        uint32_t o0[32], o1[32];
+        tmem_ld_32x32b_x32(trow + TM_O + cc + s * D, o0);
+        if (joined) tmem_ld_32x32b_x32(trow + TM_O + D + cc, o1);
+        tmem_ld_wait();
+        if (valid) {
+          float y[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            y[i] = none ? 0.0f : __uint_as_float(o0[i]) * f0;
+            if (joined && !none) y[i] += __uint_as_float(o1[i]) * f1;
+          }
+          if (sg.slot >= 0) {
+            float4* d4 = reinterpret_cast<float4*>(c.part_o + part * D + cc);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d4[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          } else {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
+            if (v8) {
+              st_global_v8(dst + cc, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+              st_global_v8(dst + cc + 16, w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4*>(dst + cc + 8 * i) =
+                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            }
+          }
+        }
+        __syncwarp();
+      }
+      if (valid) {
+        if (sg.slot >= 0)
+          c.part_l[part] = lse2;
+        else if (a.lse)
+          a.lse[(int64_t)h * a.T + sg.row0 + tok] = lse2 * kLn2;
+      }
+      tc_fence_before();
+      if (joined) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o1_free);
+      }
+    }
+    if (!ok) give_up();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, TM_COLS);
+}
+
+// Cut (head, tile) pairs: a row's pieces joined in the order of the shares, one
+// warp a row.
+constexpr int kChJoinRows = 8;
+template <int D>
+__global__ void __launch_bounds__(kChJoinRows * 32) k_kv_chunk_join(const __grid_constant__ ChunkArgs c) {
+  constexpr int E = D / 32;
+  pdl_wait();
+  pdl_launch_dependents();
+  const KvAttnArgs& a = c.a;
+  const KvHeader* hdr = reinterpret_cast<const KvHeader*>(a.plan);
+  if ((int)blockIdx.x >= hdr->c_split) return;
+  const int4 sp = reinterpret_cast<const int4*>(a.plan + a.L.c_split)[blockIdx.x];
+  const int4 tl = reinterpret_cast<const int4*>(a.plan + a.L.c_tile)[sp.x];
+  const int4 sq = reinterpret_cast<const int4*>(a.plan + a.L.seq)[tl.x];
+  const int lane = (int)lane_id(), local = (int)blockIdx.y * kChJoinRows + (int)warp_id(), R = tl.y + local;
+  if (R >= sq.z * a.G) return;
+  const int64_t base = (int64_t)sp.y * kChunkRows + local;
+  float m = -INFINITY;
+  for (int i = 0; i < sp.z; ++i) m = fmaxf(m, c.part_l[base + (int64_t)i * kChunkRows]);
+  const float ref = m == -INFINITY ? 0.0f : m;
+  float acc[E], sum = 0.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+#pragma unroll 4
+  for (int i = 0; i < sp.z; ++i) {
+    const int64_t at = base + (int64_t)i * kChunkRows;
+    const float w = ex2(c.part_l[at] - ref);
+    const float* src = c.part_o + at * D + lane * E;
+    sum += w;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] += w * src[e];
+  }
+  const bool none = sum == 0.0f;
+  const int tok = R / a.G, h = sp.w * a.G + R - tok * a.G;
+  uint16_t* dst = a.o + (int64_t)(sq.y + tok) * a.so + h * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(dst + e) =
+        none ? 0u : pack_bf16x2(__fdiv_rn(acc[e], sum), __fdiv_rn(acc[e + 1], sum));
+  if (a.lse && lane == 0) a.lse[(int64_t)h * a.T + sq.y + tok] = none ? -INFINITY : (m + log2f(sum)) * kLn2;
+}
+
+template <int D>
+cudaError_t launch_chunk(const ChunkArgs& c, cudaStream_t st) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(k_kv_chunk<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ChSmem<D>::BYTES);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  const cudaError_t f = launch_pdl(k_kv_chunk<D>, dim3((unsigned)c.a.L.c_max_units), dim3(kChThreads),
+                                   ChSmem<D>::BYTES, st, c);
+  if (f != cudaSuccess) return f;
+  note_launch();
+  return launch_pdl(k_kv_chunk_join<D>, dim3((unsigned)c.a.L.c_max_units, kChunkRows / kChJoinRows),
+                    dim3(kChJoinRows * 32), 0, st, c);
+}
+
+// Partial results lie in slots unit + index of the cut pair: below 2 units.
+size_t chunk_rows() { return (size_t)2 * device_sm_count() * kChunkRows; }
+
+}  // namespace
+
+size_t kv_chunk_bytes(const KvShape& s) {
+  return kv_chunk_tiles(s) > 0 ? chunk_rows() * ((size_t)s.hd + 1) * 4 : 0;
+}
+
+cudaError_t run_kv_chunk(const KvAttnArgs& a, const KvShape& s, void* partial, cudaStream_t st) {
+  ChunkArgs c;
+  c.a = a;
+  if (!tmap_u8_pages(&c.tk, a.k, (uint32_t)s.hd, kPage, (uint64_t)a.n_pages * s.nkv)) return cudaErrorInvalidValue;
+  c.part_o = static_cast<float*>(partial);
+  c.part_l = c.part_o + chunk_rows() * s.hd;
+  return s.hd == 64 ? launch_chunk<64>(c, st) : launch_chunk<128>(c, st);
+}
+
+}  // namespace ws

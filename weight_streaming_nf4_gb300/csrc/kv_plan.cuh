@@ -9,29 +9,42 @@
 namespace ws {
 
 constexpr int kPage = WS_KV_PAGE;
-constexpr int kTileRows = 16;  // rows of a tile of the decode kernel
+constexpr int kTileRows = 16;    // rows of a tile of the decode kernel, which has the sequences of up to so many
 constexpr int kWarpsPerSm = 12;  // of the decode kernel, resident
+constexpr int kChunkRows = 256;  // rows of a tile of the chunk kernel, which has the others
+constexpr int kChunkMinSteps = 4;  // steps (two pages) of a share of the chunk kernel's work, at least
 
 // Rows are a sequence's (new token, query head of one kv head) pairs, token by
-// token.  Everything is per kv head; all kv heads have the same plan.
+// token.  The decode kernel's plan is per kv head, the same for all; the chunk
+// kernel's shares run over all kv heads, one after another.
 struct KvHeader {
   int n_append;  // touched pages
-  int n_tiles;   // 16-row tiles
-  int pages;     // sum of the tiles' pages
+  int n_tiles;   // decode: tiles
+  int pages;     // sum of their pages
   int units;     // equal shares of those pages, one warp each
   int n_split;   // tiles cut by a unit's end
-  int pad[11];
+  int c_tiles;   // chunk: tiles
+  int c_steps;   // sum of their steps
+  int c_units;   // equal shares of n_kv_heads times those steps, one CTA each
+  int c_split;   // (head, tile) pairs cut by a unit's end
+  int pad[7];
 };
-// All int4 arrays.
+// int4 arrays:
 //   seq     {tokens before the call, first row of q, new tokens, 0}
 //   append  {first row, page (-1: none), first place in it, rows}
 //   tile    {sequence, first row, pages of the tiles before it, index among the cut ones or -1},
 //           one more at the end with the pages of all
 //   split   {tile, first slot, pieces, 0}
-// and int  unit   first tile of each unit.
+//   c_tile  {sequence, first row, steps of the tiles before it, 0}, one more at the end
+//   c_split {tile, first slot, pieces, head}
+// and
+//   pre     prefix sums over the sequences {pages to append to, tiles, chunk tiles, 0}
+//   unit    first tile of each unit (int)
+//   c_unit  {first tile, first head, index among the cut pairs of the one that its start cuts or -1, 0},
+//           one more at the end
 struct KvLayout {
-  size_t seq, pre, append, tile, split, unit, bytes;  // byte offsets; pre: prefix sums over sequences
-  int64_t max_append, max_tiles, max_units;
+  size_t seq, pre, append, tile, split, unit, c_tile, c_split, c_unit, bytes;  // byte offsets
+  int64_t max_append, max_tiles, max_units, c_max_tiles, c_max_units;
 };
 
 struct KvShape {
@@ -39,35 +52,96 @@ struct KvShape {
   int n_seq, max_pages, max_new, nh, nkv, hd;
 };
 
+inline int64_t kv_chunk_tiles(const KvShape& s) {
+  const int64_t live = std::min<int64_t>(s.n_seq, s.T), G = s.nh / s.nkv;
+  if ((int64_t)s.max_new * G <= kTileRows) return 0;
+  return s.T * G / kChunkRows + std::min<int64_t>(live, s.T * G / (kTileRows + 1));
+}
+
 inline KvLayout kv_layout(const KvShape& s) {
   KvLayout L = {};
   const int64_t live = std::min<int64_t>(s.n_seq, s.T), G = s.nh / s.nkv;
   // n rows touch (n + 62) / 64 + 1 pages at most
   L.max_append = std::min<int64_t>(std::min<int64_t>(s.T, live * (((int64_t)s.max_new + 62) / kPage + 1)),
                                    s.T / kPage + 2 * live);
-  L.max_tiles = std::min<int64_t>(s.T * G / kTileRows + live, live * (((int64_t)s.max_new * G + kTileRows - 1) / kTileRows));
+  L.max_tiles = G <= kTileRows ? live : 0;
   L.max_units = std::max<int64_t>(1, (int64_t)device_sm_count() * kWarpsPerSm / s.nkv);
+  L.c_max_tiles = kv_chunk_tiles(s);
+  L.c_max_units = device_sm_count();
   size_t o = sizeof(KvHeader);
-  auto take = [&](size_t n) {
+  auto take = [&](int64_t n) {
     const size_t at = o;
-    o += (n + 15) / 16 * 16;
+    o += ((size_t)n + 15) / 16 * 16;
     return at;
   };
-  L.seq = take((size_t)s.n_seq * 16);
-  L.pre = take((size_t)(s.n_seq + 1) * 8);
-  L.append = take((size_t)L.max_append * 16);
-  L.tile = take((size_t)(L.max_tiles + 1) * 16);
-  L.split = take((size_t)L.max_units * 16);
-  L.unit = take((size_t)(L.max_units + 1) * 4);
+  L.seq = take((int64_t)s.n_seq * 16);
+  L.pre = take((int64_t)s.n_seq * 16);
+  L.append = take(L.max_append * 16);
+  L.tile = take((L.max_tiles + 1) * 16);
+  L.split = take(L.max_units * 16);
+  L.unit = take(L.max_units * 4);
+  L.c_tile = take((L.c_max_tiles + 1) * 16);
+  L.c_split = take(L.c_max_units * 16);
+  L.c_unit = take((L.c_max_units + 1) * 16);
   L.bytes = o;
   return L;
 }
 
-// Pages of unit u: [unit_start(u), unit_start(u + 1)) of the W pages of all
-// tiles; unit_of is its inverse.
-__host__ __device__ inline int unit_start(int u, int W, int U) { return (int)((int64_t)u * W / U); }
-__host__ __device__ inline int unit_of(int page, int W, int U) {
-  return (int)((((int64_t)page + 1) * U - 1) / W);
+// Unit u has places [unit_start(u), unit_start(u + 1)) of W; unit_of is its inverse.
+__host__ __device__ inline int64_t unit_start(int u, int64_t W, int U) { return u * W / U; }
+__host__ __device__ inline int unit_of(int64_t place, int64_t W, int U) {
+  return (int)(((place + 1) * U - 1) / W);
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct KvAttnArgs {
+  const uint8_t *k, *v;
+  const float* scale;   // [n_pages][nkv][2]
+  const uint8_t* plan;
+  KvLayout L;
+  const int32_t* table;
+  const uint16_t* q;
+  uint16_t* o;
+  float* lse;           // [nh][T] or NULL
+  float* part_o;        // [slot][nkv][kTileRows][D] of cut tiles, divided by their sums
+  float* part_l;        // [slot][nkv][kTileRows] log2 of their sums
+  int64_t n_pages, sq, so, T;
+  int nkv, G, max_pages;
+  float sl2;            // softmax scale times log2(e)
+};
+
+// 2^x with the hardware approximation (relative error about 2^-22).
+WS_DEVINL float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+WS_DEVINL uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Codes 0, 1 (lo) and 2, 3 (hi) of a word, exact in fp16.
+WS_DEVINL void decode4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+// Two codes of the nearest e4m3 values (ties to even); a in the low byte.
+WS_DEVINL uint32_t e4m3x2(float a, float b) {
+  uint16_t h;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(b), "f"(a));
+  return h;
+}
+// The values of two codes (low byte first).
+WS_DEVINL void e4m3x2_values(uint32_t w, float& lo, float& hi) {
+  asm("{\n .reg .b32 x;\n .reg .b16 l, h;\n cvt.rn.f16x2.e4m3x2 x, %2;\n mov.b32 {l, h}, x;\n"
+      " cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}"
+      : "=f"(lo), "=f"(hi)
+      : "h"((uint16_t)w));
 }
 
 }  // namespace ws

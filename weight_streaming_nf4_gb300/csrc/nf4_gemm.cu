@@ -80,6 +80,10 @@ cudaError_t read_and_clear_dev_error(uint32_t* flags) {
   uint32_t kv = 0;
   e = kv_read_and_clear_dev_error(&kv);
   *flags |= kv;
+  if (e != cudaSuccess) return e;
+  uint32_t chunk = 0;
+  e = kv_chunk_read_and_clear_dev_error(&chunk);
+  *flags |= chunk;
   return e;
 }
 
@@ -2234,6 +2238,18 @@ bool tmap_bf16_sw128(CUtensorMap* m, const void* base, uint64_t inner, uint64_t 
   return encode_fn() && make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, inner, outer,
                                  pitch_bytes, box_inner, box_outer,
                                  CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+bool tmap_u8_pages(CUtensorMap* m, const void* base, uint32_t inner, uint32_t rows, uint64_t pages) {
+  if (!encode_fn()) return false;
+  const cuuint64_t dims[3] = {inner, rows, pages};
+  const cuuint64_t strides[2] = {inner, (cuuint64_t)inner * rows};
+  const cuuint32_t box[3] = {inner, rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  inner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool pdl_enabled() {
