@@ -400,8 +400,9 @@ ws_status kv_shape(const ws_kv_plan* p, KvShape* s) {
     return WS_ERR_SHAPE;
   if (p->head_dim != 64 && p->head_dim != 128) return WS_ERR_SHAPE;
   *s = KvShape{p->T, p->n_seq, p->max_pages, p->max_new, p->n_heads, p->n_kv_heads, p->head_dim};
-  // the chunk kernel's steps of one head are counted in 32 bits
-  if (kv_chunk_tiles(*s) * (s->max_pages / 2 + 1) > 0x7fffffff) return WS_ERR_SHAPE;
+  // the chunk kernel counts the steps of one head, and those of a share of all heads, in 32 bits
+  const int64_t steps = kv_chunk_tiles(*s) * (s->max_pages / 2 + 1);
+  if (steps > 0x7fffffff || steps * s->nkv > (int64_t)1 << 36) return WS_ERR_SHAPE;
   return WS_OK;
 }
 ws_status kv_check(const ws_kv_cache* c, const ws_kv_plan* p, KvShape* s) {

@@ -188,7 +188,63 @@ template <int D>
 WS_DEVINL uint32_t swizzled(int r, int c) {
   return D == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
+// True in one lane of a converged warp.
+WS_DEVINL bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
+  return p != 0u;
+}
 WS_DEVINL bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
+
+// Two fp32 operations an instruction.
+typedef unsigned long long f32x2;
+WS_DEVINL f32x2 pair(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+WS_DEVINL void unpair(f32x2 x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+WS_DEVINL f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+WS_DEVINL f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// A row's 64 scores of a page as 2^(v cf - shift), fp16 pairs; returns their sum.
+WS_DEVINL float weigh_plain(const float (&v)[64], float cf, float shift, uint32_t (&p)[32]) {
+  const f32x2 c2 = pair(cf, cf), r2 = pair(-shift, -shift);
+  f32x2 sum[2] = {0ull, 0ull};  // two zeros each
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    float y0, y1;
+    unpair(fma2(pair(v[2 * i], v[2 * i + 1]), c2, r2), y0, y1);
+    y0 = ex2(y0);
+    y1 = ex2(y1);
+    sum[i & 1] = add2(sum[i & 1], pair(y0, y1));
+    p[i] = pack_f16x2(y0, y1);
+  }
+  float a, b;
+  unpair(add2(sum[0], sum[1]), a, b);
+  return a + b;
+}
+// The same of the first `vis` tokens, y = 2^(v cf - ref): their sum, and y vr as fp16 pairs.  A row gets none
+// of the scales of a page that it does not see, NaN included.
+WS_DEVINL float weigh(const float (&v)[64], float cf, float ref, float vr, int vis, uint32_t (&p)[32]) {
+  float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float y0 = 2 * i < vis ? ex2(fmaf(v[2 * i], cf, -ref)) : 0.0f;
+    const float y1 = 2 * i + 1 < vis ? ex2(fmaf(v[2 * i + 1], cf, -ref)) : 0.0f;
+    sum[0] += y0;
+    sum[1] += y1;
+    p[i] = pack_f16x2(2 * i < vis ? y0 * vr : 0.0f, 2 * i + 1 < vis ? y1 * vr : 0.0f);
+  }
+  return sum[0] + sum[1];
+}
 
 template <int D>
 __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constant__ ChunkArgs c) {
@@ -225,7 +281,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
   volatile uint32_t* abort_flag = tmem_slot + 1;
   volatile uint32_t* skip_flag = tmem_slot + 2;
 
-  const int warp = (int)warp_id(), lane = (int)lane_id();
+  const int warp = __shfl_sync(0xffffffffu, (int)warp_id(), 0), lane = (int)lane_id();
   if (threadIdx.x == 0) {
     *abort_flag = 0u;
     *skip_flag = (*(volatile uint32_t*)&g_dev_error != 0u) ? 1u : 0u;
@@ -272,33 +328,33 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
   Seg sg;
   // Steps are numbered through the share; step n's pages are 2 n and 2 n + 1 of
   // the share's list of pages, in windows of kInfo.
-  auto info_of = [&](int64_t n, int half) -> const PageInfo& {
-    return info[(2 * n + half) % (2 * kInfo)];
+  auto info_of = [&](int n, int half) -> const PageInfo& {
+    return info[(2 * n + half) & (2 * kInfo - 1)];
   };
   auto give_up = [&]() { *abort_flag = 1u; };
   // Enter the window that step n begins, if it begins one.
-  auto window = [&](int64_t n) {
-    if (n % (kInfo / 2) != 0) return true;
-    const int64_t w = n / (kInfo / 2);
+  auto window = [&](int n) {
+    if (n & (kInfo / 2 - 1)) return true;
+    const int w = n / (kInfo / 2);
     return mbar_wait(&i_full[w & 1], (uint32_t)(w >> 1) & 1u, DERR_TIMEOUT_FULL);
   };
   // Leave the window that step n ends.
-  auto leave = [&](int64_t n) {
-    if ((n + 1) % (kInfo / 2) == 0 && lane == 0) mbar_arrive(&i_empty[(n / (kInfo / 2)) & 1]);
+  auto leave = [&](int n) {
+    if (((n + 1) & (kInfo / 2 - 1)) == 0 && lane == 0) mbar_arrive(&i_empty[(n / (kInfo / 2)) & 1]);
   };
 
   if (warp == 0) {
     if (run) {
       // the whole warp walks: every kInfo pages it looks up the next window
-      const int64_t total = share.end - share.begin;
+      const int total = (int)(share.end - share.begin);
       Share ahead = share;  // the walk of the page list
       Seg as;
       bool more = ahead.next(as);
       int as_step = more ? as.s0 : 0;
-      int64_t n = 0;  // steps loaded
+      int n = 0;  // steps loaded
       bool ok = true;
       while (n < total && ok) {
-        const int64_t w = n / (kInfo / 2);
+        const int w = n / (kInfo / 2);
         // the window's pages: lane i has pages 2 i, 2 i + 1 = step n + i
         ok = warp_all(!*abort_flag && mbar_wait(&i_empty[w & 1], ((uint32_t)(w >> 1) & 1u) ^ 1u, DERR_TIMEOUT_EMPTY));
         if (!ok) break;
@@ -332,16 +388,16 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
             mine[h].ks = s.x;
             mine[h].vs = s.y;
           }
-          info[(2 * (n + lane) + h) % (2 * kInfo)] = mine[h];
+          info[(2 * (n + lane) + h) & (2 * kInfo - 1)] = mine[h];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&i_full[w & 1]);
-        const int64_t stop = min(total, n + kInfo / 2);
+        const int stop = min(total, n + kInfo / 2);
         if (lane == 0) {
           for (; n < stop; ++n) {
             const PageInfo p0 = info_of(n, 0), p1 = info_of(n, 1);
             const uint32_t bytes = ((p0.page >= 0) + (p1.page >= 0)) * kPage * D;
-            const int ks = (int)(n % KST), rs = (int)(n % RST);
+            const int ks = n % KST, rs = n % RST;
             if (*abort_flag || !mbar_wait(&k_empty[ks], ((uint32_t)(n / KST) & 1u) ^ 1u, DERR_TIMEOUT_EMPTY)) break;
             mbar_arrive_expect_tx(&k_full[ks], bytes);
             uint8_t* dk = sk + ks * L::K;
@@ -367,55 +423,63 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
       }
       // nothing may land after the CTA is gone
       if (lane == 0) {
-        for (int64_t i = n > KST ? n - KST : 0; i < n; ++i)
+        for (int i = max(0, n - KST); i < n; ++i)
           mbar_wait(&k_full[i % KST], (uint32_t)(i / KST) & 1u, DERR_TIMEOUT_DRAIN);
-        for (int64_t i = n > RST ? n - RST : 0; i < n; ++i)
+        for (int i = max(0, n - RST); i < n; ++i)
           mbar_wait(&r_full[i % RST], (uint32_t)(i / RST) & 1u, DERR_TIMEOUT_DRAIN);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && run) {
+    // The whole warp walks, so that what the products take is in uniform
+    // registers; one lane issues.
+    if (run) {
       bool ok = true;
-      int64_t n0 = 0;             // steps of the segments before
+      int n0 = 0;                 // steps of the segments before
       uint32_t qn[2] = {0, 0};    // segments of each slot
       uint32_t pn[2] = {0, 0};    // P handed over by each slot (steps)
       auto wait = [&](uint64_t* b, uint32_t parity, uint32_t why) {
-        if (ok && (*abort_flag || !mbar_wait(b, parity, why))) ok = false;
+        if (ok) ok = warp_all(!*abort_flag && mbar_wait(b, parity, why));
         return ok;
       };
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
       // S of step j for slot s; the first to use the step waits for its keys, the last frees them
       auto issue_s = [&](int j, int s, bool first, bool last) {
-        const int64_t n = n0 + j;
-        const int st = (int)(n % KST);
+        const int n = n0 + j, st = n % KST;
         if (first && !wait(&k_full[st], (uint32_t)(n / KST) & 1u, DERR_TIMEOUT_FULL)) return;
         tc_fence_after();
-        const uint32_t q = smem_u32(sq + s * 2 * L::QP), k = smem_u32(sk + st * L::K);
+        const uint64_t q = desc_bytes<D>(base + s * 2 * L::QP), k = desc_bytes<D>(base + L::OFF_K + st * L::K);
+        const uint32_t d = tm + TM_S + s * kStepTokens;
+        if (elect_one()) {
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+          for (int part = 0; part < 2; ++part)
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i)
-            tc_mma_f8(tmem + TM_S + s * kStepTokens, desc_bytes<D>(q + part * L::QP + 32 * i),
-                      desc_bytes<D>(k + 32 * i), idS, (part | i) ? 1u : 0u);
-        tc_commit(&s_full[s]);
-        if (last) tc_commit(&k_empty[st]);
+            for (int i = 0; i < D / 32; ++i)
+              tc_mma_f8(d, q + ((part * L::QP + 32 * i) >> 4), k + ((32 * i) >> 4), idS, (part | i) ? 1u : 0u);
+          tc_commit(&s_full[s]);
+          if (last) tc_commit(&k_empty[st]);
+        }
+        __syncwarp();
       };
       auto issue_pv = [&](int j, int s, bool first, bool last, bool begins) {
-        const int64_t n = n0 + j;
-        const int st = (int)(n % VST);
+        const int n = n0 + j, st = n % VST;
+        const uint64_t v = smem_desc_sw128(base + L::OFF_V + st * L::V, 16, 1024);
+        const uint32_t d = tm + TM_O + s * D, p = tm + TM_S + s * kStepTokens;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (!wait(&p_full[2 * s + h], pn[s] & 1u, DERR_TIMEOUT_BFULL)) return;
           if (h == 0 && first && !wait(&v_full[st], (uint32_t)(n / VST) & 1u, DERR_TIMEOUT_FULL)) return;
           tc_fence_after();
-          const uint32_t v = smem_u32(sv + st * L::V + h * (D * 128));
+          if (elect_one()) {
 #pragma unroll
-          for (int i = 0; i < kPage / 16; ++i)
-            tc_mma_f16_ta(tmem + TM_O + s * D, tmem + TM_S + s * kStepTokens + h * 32 + i * 8,
-                          smem_desc_sw128(v + 32 * i, 16, 1024), idO, (begins && h == 0 && i == 0) ? 0u : 1u);
-          tc_commit(&o_done[2 * s + h]);
+            for (int i = 0; i < kPage / 16; ++i)
+              tc_mma_f16_ta(d, p + h * 32 + i * 8, v + ((h * (D * 128) + 32 * i) >> 4), idO,
+                            (begins && h == 0 && i == 0) ? 0u : 1u);
+            tc_commit(&o_done[2 * s + h]);
+            if (h == 1 && last) tc_commit(&v_empty[st]);
+          }
+          __syncwarp();
         }
         ++pn[s];
-        if (last) tc_commit(&v_empty[st]);
       };
       while (ok && share.next(sg)) {
         const int J = sg.s1 - sg.s0;
@@ -441,19 +505,20 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
         n0 += J;
       }
       if (!ok) give_up();
-      tc_commit(drain);
+      if (elect_one()) tc_commit(drain);
+      __syncwarp();
       mbar_wait(drain, 0u, DERR_TIMEOUT_DRAIN);
     }
   } else if (warp < 4) {
     // ---- values: codes [D][64 tokens] of each page -> fp16 operand rows of 64 tokens
     if (run) {
       const int w = warp - 2;
-      int64_t n = 0;
+      int n = 0;
       bool ok = true;
       while (ok && share.next(sg)) {
         const int kv_end = sg.past + sg.n;
         for (int j = sg.s0; j < sg.s1 && ok; ++j, ++n) {
-          const int rs = (int)(n % RST), st = (int)(n % VST);
+          const int rs = n % RST, st = n % VST;
           ok = warp_all(!*abort_flag && window(n) &&
                         mbar_wait(&v_empty[st], ((uint32_t)(n / VST) & 1u) ^ 1u, DERR_TIMEOUT_EMPTY) &&
                         mbar_wait(&r_full[rs], (uint32_t)(n / RST) & 1u, DERR_TIMEOUT_FULL));
@@ -464,29 +529,35 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
             const int left = kv_end - (2 * j + h) * kPage;  // tokens of the page that are the sequence's
             const uint8_t* src = sr + rs * L::K + h * (kPage * D);
             uint8_t* dst = sv + st * L::V + h * (D * 128);
+            const int r0 = w * (D / 2) + (lane >> 2), u = lane & 3;
+            uint4 x[D / 16];
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+              x[i] = have ? *reinterpret_cast<const uint4*>(src + (r0 + 8 * i) * kPage + 16 * u) : make_uint4(0, 0, 0, 0);
+            if (left < kPage) {  // places behind the last token hold anything, NaN too
+              uint32_t keep[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int m = left - 16 * u - 4 * e;
+                keep[e] = m >= 4 ? 0xffffffffu : m <= 0 ? 0u : (1u << (8 * m)) - 1u;
+              }
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                x[i].x &= keep[0];
+                x[i].y &= keep[1];
+                x[i].z &= keep[2];
+                x[i].w &= keep[3];
+              }
+            }
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
-              const int r = w * (D / 2) + 8 * i + (lane >> 2), u = lane & 3;
-              uint32_t x[4] = {0, 0, 0, 0};
-              if (have) {
-                const uint4 v = *reinterpret_cast<const uint4*>(src + r * kPage + 16 * u);
-                x[0] = v.x;
-                x[1] = v.y;
-                x[2] = v.z;
-                x[3] = v.w;
-                if (left < kPage) {  // places behind the last token hold anything, NaN too
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    const int m = left - 16 * u - 4 * e;
-                    x[e] &= m >= 4 ? 0xffffffffu : m <= 0 ? 0u : (1u << (8 * m)) - 1u;
-                  }
-                }
-              }
               uint32_t y[8];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) decode4(x[e], y[2 * e], y[2 * e + 1]);
-              sts128(dst + swizzled<128>(r, 2 * u), y[0], y[1], y[2], y[3]);
-              sts128(dst + swizzled<128>(r, 2 * u + 1), y[4], y[5], y[6], y[7]);
+              decode4(x[i].x, y[0], y[1]);
+              decode4(x[i].y, y[2], y[3]);
+              decode4(x[i].z, y[4], y[5]);
+              decode4(x[i].w, y[6], y[7]);
+              sts128(dst + swizzled<128>(r0 + 8 * i, 2 * u), y[0], y[1], y[2], y[3]);
+              sts128(dst + swizzled<128>(r0 + 8 * i, 2 * u + 1), y[4], y[5], y[6], y[7]);
             }
           }
           fence_proxy_async_smem();
@@ -504,9 +575,9 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
     // ---- rows: thread <-> row r of slot s
     const int s = (warp - 4) >> 2, q4 = warp & 3, r = q4 * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
-    const uint32_t t_s = trow + TM_S + s * kStepTokens;
+    const uint32_t t_s = trow + TM_S + s * kStepTokens, t_o = trow + TM_O + s * D;
     uint8_t* q_hi = sq + s * 2 * L::QP;
-    int64_t n0 = 0;
+    int n0 = 0;
     uint32_t sn = 0;         // steps of this slot
     uint32_t dn = 0;         // dual segments with both slots in use
     bool ok = true;
@@ -514,7 +585,73 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
       ok = warp_all(!*abort_flag && mbar_wait(b, parity, why));
       return ok;
     };
-    while (ok && share.next(sg)) {
+    // The warp's 32 rows of Q in two e4m3 parts, a row at a time over the lanes
+    // (its tensor products of the segment before are through: they gave the last
+    // S).  Returns this thread's row's factor of S.
+    auto stage = [&](const Seg& g) {
+      if (g.dual && s >= g.s1 - g.s0) return 0.0f;  // the slot has no step
+      constexpr int E = D / 32, B = 16;             // elements a lane; rows in flight
+      const int first = (g.dual ? 0 : s * kSlotRows) + q4 * 32;
+      float qs = 0.0f;
+#pragma unroll 1
+      for (int b = 0; b < 32; b += B) {
+        uint32_t x[B][E / 2];
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+          const int local = first + b + i, R = g.r0 + local, tok = R / a.G;
+#pragma unroll
+          for (int k = 0; k < E / 2; ++k) x[i][k] = 0u;
+          if (local < g.rows) {
+            const uint16_t* src =
+                a.q + (int64_t)(g.row0 + tok) * a.sq + (g.head * a.G + R - tok * a.G) * D + lane * E;
+            if (E == 4) {
+              const uint2 w = *reinterpret_cast<const uint2*>(src);
+              x[i][0] = w.x;
+              x[i][E / 2 - 1] = w.y;
+            } else {
+              x[i][0] = *reinterpret_cast<const uint32_t*>(src);
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int k = 0; k < E / 2; ++k) top = __vmaxu2(top, x[i][k] & 0x7fff7fffu);
+          top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+          // the largest at (224, 448]; a row that is not finite gives NaN
+          const int e = max((int)(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u), -126);
+          const float qk = __uint_as_float((uint32_t)(127 - e) << 23);
+          if (lane == b + i)
+            qs = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : a.sl2 * __uint_as_float((uint32_t)(e + 127) << 23);
+          uint32_t hi = 0, lo = 0;
+#pragma unroll
+          for (int k = 0; k < E / 2; ++k) {
+            const float f0 = bf16_lo(x[i][k]) * qk, f1 = bf16_hi(x[i][k]) * qk;
+            float g0, g1;
+            const uint32_t ph = e4m3x2(f0, f1);
+            e4m3x2_values(ph, g0, g1);
+            hi |= ph << (16 * k);
+            lo |= e4m3x2(f0 - g0, f1 - g1) << (16 * k);
+          }
+          const uint32_t at = swizzled<D>(q4 * 32 + b + i, lane * E / 16) + (uint32_t)(lane * E % 16);
+          if (E == 4) {
+            *reinterpret_cast<uint32_t*>(q_hi + at) = hi;
+            *reinterpret_cast<uint32_t*>(q_hi + L::QP + at) = lo;
+          } else {
+            *reinterpret_cast<uint16_t*>(q_hi + at) = (uint16_t)hi;
+            *reinterpret_cast<uint16_t*>(q_hi + L::QP + at) = (uint16_t)lo;
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[s]);
+      return qs;
+    };
+    bool have = share.next(sg);
+    float qs = have ? stage(sg) : 0.0f;
+    while (have) {
       const int J = sg.s1 - sg.s0;
       const int local = sg.dual ? r : s * kSlotRows + r;  // row of the tile
       const bool valid = local < sg.rows;
@@ -522,54 +659,10 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
       const int h = sg.head * a.G + R - tok * a.G;
       const int lim = valid ? sg.past + tok + 1 : 0;  // tokens that the row sees
       const bool active = !sg.dual || s < J;
-      float m = -INFINITY, l = 0.0f, vref = 0.0f, qs = 0.0f;
-      if (active) {
-        // the row of Q in two e4m3 parts
-        const uint16_t* src = a.q + (int64_t)(sg.row0 + tok) * a.sq + h * D;
-        uint32_t top = 0;
-        uint4 x[D / 8];
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          x[i] = valid ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
-          top = __vmaxu2(top, __vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu));
-          top = __vmaxu2(top, __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
-        }
-        top = max(top & 0xffffu, top >> 16);
-        // the largest at (224, 448]; a row that is not finite gives NaN
-        const int e = (int)(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u);
-        const float qk = __uint_as_float((uint32_t)(127 - max(e, -126)) << 23);
-        qs = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : a.sl2 / qk;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t w[4] = {x[2 * i + j].x, x[2 * i + j].y, x[2 * i + j].z, x[2 * i + j].w};
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint32_t ph[2], pl[2];
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const float f0 = bf16_lo(w[2 * k + y]) * qk, f1 = bf16_hi(w[2 * k + y]) * qk;
-                float g0, g1;
-                ph[y] = e4m3x2(f0, f1);
-                e4m3x2_values(ph[y], g0, g1);
-                pl[y] = e4m3x2(f0 - g0, f1 - g1);
-              }
-              hi[2 * j + k] = ph[0] | ph[1] << 16;
-              lo[2 * j + k] = pl[0] | pl[1] << 16;
-            }
-          }
-          sts128(q_hi + swizzled<D>(r, i), hi[0], hi[1], hi[2], hi[3]);
-          sts128(q_hi + L::QP + swizzled<D>(r, i), lo[0], lo[1], lo[2], lo[3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[s]);
-      }
-      int done = 0;  // halves handed over in this segment
-      for (int j = 0; j < J && ok; ++j) {
-        const int64_t n = n0 + j;
+      float m = -INFINITY, l = 0.0f, vref = 0.0f;
+      bool begun = false;  // something is in O
+      for (int j = 0; j < J; ++j) {
+        const int n = n0 + j;
         if (!(ok = warp_all(!*abort_flag && window(n)))) break;
         if (sg.dual && (j & 1) != s) {
           leave(n);
@@ -578,7 +671,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
         if (!wait(&s_full[s], sn & 1u, DERR_TIMEOUT_ACC)) break;
         tc_fence_after();
 #pragma unroll 1
-        for (int half = 0; half < 2 && ok; ++half) {
+        for (int half = 0; half < 2; ++half) {
           const PageInfo pi = info_of(n, half);
           uint32_t p[32];
           if (pi.page < 0) {
@@ -600,71 +693,67 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
             float cf = qs * pi.ks;
             cf = cf < 1e-37f ? 1e-37f : cf;  // not below fp32's range: -inf * 0 is NaN
             const int vis = lim - (2 * (sg.s0 + j) + half) * kPage;
-            const bool masked = __any_sync(0xffffffffu, vis < kPage);
-            if (masked) {
-#pragma unroll
-              for (int i = 0; i < 64; ++i)
-                if (i >= vis) v[i] = -INFINITY;
+            // The ordinary page: all rows see all of it, m stands and vr is a power of two, 2^e, which goes
+            // into the exponent.  The sum bounds the largest: at 2^kLag or less, m may stay.
+            const int e = (int)(__float_as_uint(pi.vs) >> 23) - (int)(__float_as_uint(vref) >> 23) + kChMargin;
+            const bool plain = ((__float_as_uint(pi.vs) | __float_as_uint(vref)) & 0x7fffffu) == 0u && e >= -20 &&
+                               e <= kChMargin && vis >= kPage && m > -INFINITY;
+            bool grown = false, rest = true;
+            if (warp_all(plain)) {
+              const float sum = weigh_plain(v, cf, m - (float)e, p) * __uint_as_float((uint32_t)(127 - e) << 23);
+              grown = !(sum <= (float)(1 << kLag));
+              rest = !warp_all(!grown);
+              if (!rest) l += sum;
             }
-            float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < 64; i += 4)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) t[k] = fmaxf(t[k], v[i + k]);
-            const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * cf;
-            const bool up = top > m + kLag || pi.vs > vref;
-            if (__any_sync(0xffffffffu, up)) {
-              const float nm = top > m + kLag ? top : m;
-              const float nv = fmaxf(vref, pi.vs);  // a NaN scale is no reference
-              float f = nm == m ? 1.0f : ex2(m - nm);
-              l *= f;
-              f *= vref == nv ? 1.0f : vref / nv;
-              m = nm;
-              vref = nv;
-              if (done > 0) {
-                // O of the halves before
-                if (!wait(&o_done[2 * s + (half ^ 1)], (sn + half - 1) & 1u, DERR_TIMEOUT_ACC)) break;
-                tc_fence_after();
-#pragma unroll 1
-                for (int cc = 0; cc < D; cc += 32) {
-                  uint32_t o[32];
-                  tmem_ld_32x32b_x32(trow + TM_O + s * D + cc, o);
-                  tmem_ld_wait();
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                  tmem_st_32x32b_x32(trow + TM_O + s * D + cc, o);
-                }
-                tmem_st_wait();
-              }
-            }
-            const float ref = m == -INFINITY ? 0.0f : m;
-            const float vr = (pi.vs == 0.0f ? 0.0f : pi.vs / vref) * (float)(1 << kChMargin);
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-              float y0 = ex2(fmaf(v[i], cf, -ref)), y1 = ex2(fmaf(v[i + 1], cf, -ref));
-              if (masked) {  // a row gets none of the scales of a page that it does not see, NaN included
-                if (i >= vis) y0 = 0.0f;
-                if (i + 1 >= vis) y1 = 0.0f;
-              }
-              sum[i & 2] += y0;
-              sum[(i & 2) + 1] += y1;
-              y0 *= vr;
-              y1 *= vr;
+            if (rest) {
+              const bool masked = __any_sync(0xffffffffu, vis < kPage);
               if (masked) {
-                if (i >= vis) y0 = 0.0f;
-                if (i + 1 >= vis) y1 = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 64; ++i)
+                  if (i >= vis) v[i] = -INFINITY;
               }
-              p[i / 2] = pack_f16x2(y0, y1);
+              float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int i = 0; i < 64; i += 4)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) t[k] = fmaxf(t[k], v[i + k]);
+              const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * cf;
+              const bool up = top > m + (grown ? 0.0f : (float)kLag);
+              if (__any_sync(0xffffffffu, up || pi.vs > vref)) {
+                const float nm = up ? top : m;
+                const float nv = fmaxf(vref, pi.vs);  // a NaN scale is no reference
+                float f = nm == m ? 1.0f : ex2(m - nm);
+                l *= f;
+                f *= vref == nv ? 1.0f : vref / nv;
+                m = nm;
+                vref = nv;
+                if (begun) {
+                  // O of the halves before
+                  if (!wait(&o_done[2 * s + (half ^ 1)], (sn + half - 1) & 1u, DERR_TIMEOUT_ACC)) break;
+                  tc_fence_after();
+#pragma unroll 1
+                  for (int cc = 0; cc < D; cc += 16) {
+                    uint32_t o[16];
+                    tmem_ld_32x32b_x16(t_o + cc, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                    tmem_st_32x32b_x16(t_o + cc, o);
+                  }
+                  tmem_st_wait();
+                }
+              }
+              const float ref = m == -INFINITY ? 0.0f : m;
+              const float vr = (pi.vs == 0.0f ? 0.0f : pi.vs / vref) * (float)(1 << kChMargin);
+              l += weigh(v, cf, ref, vr, vis, p);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           }
           tmem_st_32x32b_x32(t_s + half * 32, p);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full[2 * s + half]);
-          ++done;
+          begun = true;
         }
         if (!ok) break;
         ++sn;
@@ -672,7 +761,10 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
       }
       if (!ok) break;
       n0 += J;
-      // ---- the segment's end
+      // ---- the segment's end; the next one's rows go first, and its first products run beside this
+      Seg nx;
+      have = share.next(nx);
+      const float qn = have ? stage(nx) : 0.0f;
       const bool joined = sg.dual && J > 1;
       if (active && !wait(&o_done[2 * s + 1], (sn - 1) & 1u, DERR_TIMEOUT_ACC)) break;
       tc_fence_after();
@@ -685,73 +777,78 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
           if (lane == 0) mbar_arrive(ml_full);
           // slot 0 has read O of slot 1 before this slot goes on
           if (!wait(o1_free, dn & 1u, DERR_TIMEOUT_ACC)) break;
-          ++dn;
         } else {
           if (!wait(ml_full, dn & 1u, DERR_TIMEOUT_ACC)) break;
           tc_fence_after();
-          ++dn;
           const float4 y = ml[r];
           m1 = y.x;
           l1 = y.y;
           v1 = y.z;
         }
+        ++dn;
       }
-      if (sg.dual && s == 1) continue;
-      const float mm = fmaxf(m, m1), ref = mm == -INFINITY ? 0.0f : mm;
-      const float e0 = m == -INFINITY ? 0.0f : ex2(m - ref), e1 = m1 == -INFINITY ? 0.0f : ex2(m1 - ref);
-      const float sum = l * e0 + l1 * e1;
-      const bool none = sum == 0.0f;
-      const float inv = none ? 0.0f : (1.0f / (1 << kChMargin)) / sum;
-      const float f0 = e0 * vref * inv, f1 = e1 * v1 * inv;
-      const float lse2 = none ? -INFINITY : mm + log2f(sum);
-      uint16_t* dst = a.o + (int64_t)(sg.row0 + tok) * a.so + h * D;
-      const int64_t part = (int64_t)sg.slot * kChunkRows + local;
-      const bool v8 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0u && (a.so & 15) == 0;
+      if (!(sg.dual && s == 1)) {
+        const float mm = fmaxf(m, m1), ref = mm == -INFINITY ? 0.0f : mm;
+        const float e0 = m == -INFINITY ? 0.0f : ex2(m - ref), e1 = m1 == -INFINITY ? 0.0f : ex2(m1 - ref);
+        const float sum = l * e0 + l1 * e1;
+        const bool none = sum == 0.0f;
+        const float inv = none ? 0.0f : (1.0f / (1 << kChMargin)) / sum;
+        const float f0 = e0 * vref * inv, f1 = e1 * v1 * inv;
+        const float lse2 = none ? -INFINITY : mm + log2f(sum);
+        uint16_t* dst = a.o + (int64_t)(sg.row0 + tok) * a.so + h * D;
+        const int64_t part = (int64_t)sg.slot * kChunkRows + local;
+        const bool v8 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0u && (a.so & 15) == 0;
 #pragma unroll 1
-      for (int cc = 0; cc < D; cc += 32) {
-        uint32_t o0[32], o1[32];
-        tmem_ld_32x32b_x32(trow + TM_O + cc + s * D, o0);
-        if (joined) tmem_ld_32x32b_x32(trow + TM_O + D + cc, o1);
-        tmem_ld_wait();
-        if (valid) {
-          float y[32];
+        for (int cc = 0; cc < D; cc += 32) {
+          uint32_t o0[32], o1[32];
+          tmem_ld_32x32b_x32(t_o + cc, o0);
+          if (joined) tmem_ld_32x32b_x32(trow + TM_O + D + cc, o1);
+          tmem_ld_wait();
+          if (valid) {
+            float y[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            y[i] = none ? 0.0f : __uint_as_float(o0[i]) * f0;
-            if (joined && !none) y[i] += __uint_as_float(o1[i]) * f1;
-          }
-          if (sg.slot >= 0) {
-            float4* d4 = reinterpret_cast<float4*>(c.part_o + part * D + cc);
+            for (int i = 0; i < 32; ++i) {
+              y[i] = none ? 0.0f : __uint_as_float(o0[i]) * f0;
+              if (joined && !none) y[i] += __uint_as_float(o1[i]) * f1;
+            }
+            if (sg.slot >= 0) {
+              float* d = c.part_o + part * D + cc;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d4[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-          } else {
-            uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
-            if (v8) {
-              st_global_v8(dst + cc, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
-              st_global_v8(dst + cc + 16, w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]);
+              for (int i = 0; i < 32; i += 8)
+                st_global_v8(d + i, __float_as_uint(y[i]), __float_as_uint(y[i + 1]), __float_as_uint(y[i + 2]),
+                             __float_as_uint(y[i + 3]), __float_as_uint(y[i + 4]), __float_as_uint(y[i + 5]),
+                             __float_as_uint(y[i + 6]), __float_as_uint(y[i + 7]));
             } else {
+              uint32_t w[16];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint4*>(dst + cc + 8 * i) =
-                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+              for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
+              if (v8) {
+                st_global_v8(dst + cc, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+                st_global_v8(dst + cc + 16, w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  *reinterpret_cast<uint4*>(dst + cc + 8 * i) =
+                      make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+              }
             }
           }
+          __syncwarp();
         }
-        __syncwarp();
+        if (valid) {
+          if (sg.slot >= 0)
+            c.part_l[part] = lse2;
+          else if (a.lse)
+            a.lse[(int64_t)h * a.T + sg.row0 + tok] = lse2 * kLn2;
+        }
+        tc_fence_before();
+        if (joined) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o1_free);
+        }
       }
-      if (valid) {
-        if (sg.slot >= 0)
-          c.part_l[part] = lse2;
-        else if (a.lse)
-          a.lse[(int64_t)h * a.T + sg.row0 + tok] = lse2 * kLn2;
-      }
-      tc_fence_before();
-      if (joined) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(o1_free);
-      }
+      sg = nx;
+      qs = qn;
     }
     if (!ok) give_up();
   }
