@@ -62,7 +62,7 @@ template <int D>
 struct ChSmem {
   static constexpr int KST = 3;  // steps of keys in flight
   static constexpr int RST = 2;  // of value codes
-  static constexpr int VST = 2;  // decoded
+  static constexpr int VST = 2;  // decoded (two: the products' warp counts on it)
   static constexpr uint32_t QP = kSlotRows * D;          // one part of a slot's rows
   static constexpr uint32_t K = kStepTokens * D;
   static constexpr uint32_t V = kStepTokens * D * 2;
@@ -168,6 +168,11 @@ WS_DEVINL void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
       "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+WS_DEVINL void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 WS_DEVINL void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* bar, int32_t x, int32_t y, int32_t z) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
@@ -193,6 +198,24 @@ WS_DEVINL bool elect_one() {
   uint32_t p;
   asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
   return p != 0u;
+}
+// A wait of so many polls at most: a poll, a vote and a branch where the barrier
+// is through (mbar_wait's clock reading and the abort flag at every wait cost
+// more than the products they wait for).  A role that gave up is seen after a
+// thousand polls.  The answer is the warp's.
+constexpr uint32_t kPolls = 1u << 23;
+WS_DEVINL bool poll(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort_flag) {
+  uint32_t it = 0;
+  while (!__any_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+    if ((++it & 1023u) == 0u && __any_sync(0xffffffffu, it >= kPolls || *abort_flag != 0u)) return false;
+  return true;
+}
+// The same for one thread.
+WS_DEVINL bool poll_one(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort_flag) {
+  uint32_t it = 0;
+  while (!mbar_try_wait(bar, parity))
+    if ((++it & 1023u) == 0u && (it >= kPolls || *abort_flag != 0u)) return false;
+  return true;
 }
 WS_DEVINL bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
 
@@ -231,21 +254,6 @@ WS_DEVINL float weigh_plain(const float (&v)[64], float cf, float shift, uint32_
   unpair(add2(sum[0], sum[1]), a, b);
   return a + b;
 }
-// The same of the first `vis` tokens, y = 2^(v cf - ref): their sum, and y vr as fp16 pairs.  A row gets none
-// of the scales of a page that it does not see, NaN included.
-WS_DEVINL float weigh(const float (&v)[64], float cf, float ref, float vr, int vis, uint32_t (&p)[32]) {
-  float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const float y0 = 2 * i < vis ? ex2(fmaf(v[2 * i], cf, -ref)) : 0.0f;
-    const float y1 = 2 * i + 1 < vis ? ex2(fmaf(v[2 * i + 1], cf, -ref)) : 0.0f;
-    sum[0] += y0;
-    sum[1] += y1;
-    p[i] = pack_f16x2(2 * i < vis ? y0 * vr : 0.0f, 2 * i + 1 < vis ? y1 * vr : 0.0f);
-  }
-  return sum[0] + sum[1];
-}
-
 template <int D>
 __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constant__ ChunkArgs c) {
   using L = ChSmem<D>;
@@ -325,18 +333,21 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
   const bool run = *skip_flag == 0u;
   Share share(c, (int)blockIdx.x);
   const KvAttnArgs& a = c.a;
-  Seg sg;
+  Seg sg = {};
   // Steps are numbered through the share; step n's pages are 2 n and 2 n + 1 of
   // the share's list of pages, in windows of kInfo.
   auto info_of = [&](int n, int half) -> const PageInfo& {
     return info[(2 * n + half) & (2 * kInfo - 1)];
   };
-  auto give_up = [&]() { *abort_flag = 1u; };
+  auto give_up = [&](uint32_t why) {
+    if (*abort_flag == 0u) atomicOr(&g_dev_error, why);
+    *abort_flag = 1u;
+  };
   // Enter the window that step n begins, if it begins one.
   auto window = [&](int n) {
     if (n & (kInfo / 2 - 1)) return true;
     const int w = n / (kInfo / 2);
-    return mbar_wait(&i_full[w & 1], (uint32_t)(w >> 1) & 1u, DERR_TIMEOUT_FULL);
+    return poll(&i_full[w & 1], (uint32_t)(w >> 1) & 1u, abort_flag);
   };
   // Leave the window that step n ends.
   auto leave = [&](int n) {
@@ -356,7 +367,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
       while (n < total && ok) {
         const int w = n / (kInfo / 2);
         // the window's pages: lane i has pages 2 i, 2 i + 1 = step n + i
-        ok = warp_all(!*abort_flag && mbar_wait(&i_empty[w & 1], ((uint32_t)(w >> 1) & 1u) ^ 1u, DERR_TIMEOUT_EMPTY));
+        ok = poll(&i_empty[w & 1], ((uint32_t)(w >> 1) & 1u) ^ 1u, abort_flag);
         if (!ok) break;
         PageInfo mine[2];
         int head = 0;
@@ -398,12 +409,12 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
             const PageInfo p0 = info_of(n, 0), p1 = info_of(n, 1);
             const uint32_t bytes = ((p0.page >= 0) + (p1.page >= 0)) * kPage * D;
             const int ks = n % KST, rs = n % RST;
-            if (*abort_flag || !mbar_wait(&k_empty[ks], ((uint32_t)(n / KST) & 1u) ^ 1u, DERR_TIMEOUT_EMPTY)) break;
+            if (!poll_one(&k_empty[ks], ((uint32_t)(n / KST) & 1u) ^ 1u, abort_flag)) break;
             mbar_arrive_expect_tx(&k_full[ks], bytes);
             uint8_t* dk = sk + ks * L::K;
             if (p0.page >= 0) tma_load_3d(dk, &c.tk, &k_full[ks], 0, 0, p0.page);
             if (p1.page >= 0) tma_load_3d(dk + kPage * D, &c.tk, &k_full[ks], 0, 0, p1.page);
-            if (*abort_flag || !mbar_wait(&r_empty[rs], ((uint32_t)(n / RST) & 1u) ^ 1u, DERR_TIMEOUT_EMPTY)) {
+            if (!poll_one(&r_empty[rs], ((uint32_t)(n / RST) & 1u) ^ 1u, abort_flag)) {
               mbar_wait(&k_full[ks], (uint32_t)(n / KST) & 1u, DERR_TIMEOUT_DRAIN);
               break;
             }
@@ -414,7 +425,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
               bulk_load(dr + kPage * D, a.v + (int64_t)p1.page * (kPage * D), kPage * D, &r_full[rs]);
           }
           if (n < stop) {
-            give_up();
+            give_up(DERR_TIMEOUT_EMPTY);
             ok = false;
           }
         }
@@ -434,77 +445,85 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
     // registers; one lane issues.
     if (run) {
       bool ok = true;
-      int n0 = 0;                 // steps of the segments before
-      uint32_t qn[2] = {0, 0};    // segments of each slot
-      uint32_t pn[2] = {0, 0};    // P handed over by each slot (steps)
-      auto wait = [&](uint64_t* b, uint32_t parity, uint32_t why) {
-        if (ok) ok = warp_all(!*abort_flag && mbar_wait(b, parity, why));
+      uint32_t qn = 0, pn = 0;              // parities of each slot's segments and steps, a bit each
+      int kst = 0, vst = 0;                 // stages in use, and their parities
+      uint32_t kph = 0, vph = 0;
+      auto wait = [&](uint64_t* b, uint32_t parity) {
+        ok = poll(b, parity & 1u, abort_flag);
         return ok;
       };
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
-      // S of step j for slot s; the first to use the step waits for its keys, the last frees them
-      auto issue_s = [&](int j, int s, bool first, bool last) {
-        const int n = n0 + j, st = n % KST;
-        if (first && !wait(&k_full[st], (uint32_t)(n / KST) & 1u, DERR_TIMEOUT_FULL)) return;
-        tc_fence_after();
-        const uint64_t q = desc_bytes<D>(base + s * 2 * L::QP), k = desc_bytes<D>(base + L::OFF_K + st * L::K);
-        const uint32_t d = tm + TM_S + s * kStepTokens;
-        if (elect_one()) {
-#pragma unroll
-          for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-              tc_mma_f8(d, q + ((part * L::QP + 32 * i) >> 4), k + ((32 * i) >> 4), idS, (part | i) ? 1u : 0u);
-          tc_commit(&s_full[s]);
-          if (last) tc_commit(&k_empty[st]);
-        }
-        __syncwarp();
-      };
-      auto issue_pv = [&](int j, int s, bool first, bool last, bool begins) {
-        const int n = n0 + j, st = n % VST;
-        const uint64_t v = smem_desc_sw128(base + L::OFF_V + st * L::V, 16, 1024);
-        const uint32_t d = tm + TM_O + s * D, p = tm + TM_S + s * kStepTokens;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!wait(&p_full[2 * s + h], pn[s] & 1u, DERR_TIMEOUT_BFULL)) return;
-          if (h == 0 && first && !wait(&v_full[st], (uint32_t)(n / VST) & 1u, DERR_TIMEOUT_FULL)) return;
-          tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int i = 0; i < kPage / 16; ++i)
-              tc_mma_f16_ta(d, p + h * 32 + i * 8, v + ((h * (D * 128) + 32 * i) >> 4), idO,
-                            (begins && h == 0 && i == 0) ? 0u : 1u);
-            tc_commit(&o_done[2 * s + h]);
-            if (h == 1 && last) tc_commit(&v_empty[st]);
-          }
-          __syncwarp();
-        }
-        ++pn[s];
-      };
+      // descriptors: the low word moves, the high word stays
+      const uint64_t dk0 = desc_bytes<D>(0u), dv0 = smem_desc_sw128(0u, 16, 1024);
       while (ok && share.next(sg)) {
-        const int J = sg.s1 - sg.s0;
-        for (int s = 0; s < 2 && ok; ++s) {
-          if (sg.dual && s >= J) continue;
-          if (!wait(&q_full[s], qn[s] & 1u, DERR_TIMEOUT_FULL)) break;
-          ++qn[s];
-        }
-        if (sg.dual) {
-          for (int j = 0; j < min(2, J) && ok; ++j) issue_s(j, j, true, true);
-          for (int j = 0; j < J && ok; ++j) {
-            issue_pv(j, j & 1, true, true, j < 2);
-            if (ok && j + 2 < J) issue_s(j + 2, j & 1, true, true);
-          }
-        } else {
-          for (int s = 0; s < 2 && ok; ++s) issue_s(0, s, s == 0, s == 1);
-          for (int j = 0; j < J && ok; ++j)
-            for (int s = 0; s < 2 && ok; ++s) {
-              issue_pv(j, s, s == 0, s == 1, j == 0);
-              if (ok && j + 1 < J) issue_s(j + 1, s, s == 0, s == 1);
+        // Event e is step j of slot e & 1: both slots' of one step come together, or (dual) the steps in turn.
+        // P V of event e, then S of event e + 2, the same slot's next.
+        const int J = sg.s1 - sg.s0, E = sg.dual ? J : 2 * J;
+#pragma unroll 1
+        for (int e0 = -2; e0 < E && ok; e0 += 2) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const int e = e0 + s;
+            const bool begins = sg.dual || s == 0, ends = sg.dual || s == 1;  // the first, the last to use a step
+            const bool pv = e >= 0 && e < E, next = e + 2 < E;
+            // what is long there, before the slot's P
+            if (pv && begins && !wait(&v_full[vst], vph)) break;
+            if (next && begins && !wait(&k_full[kst], kph)) break;
+            if (next && e < 0) {  // the slot's first of the segment
+              if (!wait(&q_full[s], qn >> s)) break;
+              qn ^= 1u << s;
             }
+            if (pv) {
+              const uint64_t v = dv0 + ((base + L::OFF_V + vst * L::V) >> 4);
+              const uint32_t d = tm + TM_O + s * D, p = tm + TM_S + s * kStepTokens;
+              if (!wait(&p_full[2 * s], pn >> s)) break;
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < kPage / 16; ++i)
+                  tc_mma_f16_ta(d, p + i * 8, v + ((32 * i) >> 4), idO, (e < 2 && i == 0) ? 0u : 1u);
+                tc_commit(&o_done[2 * s]);
+              }
+              __syncwarp();
+              if (!wait(&p_full[2 * s + 1], pn >> s)) break;
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < kPage / 16; ++i)
+                  tc_mma_f16_ta(d, p + 32 + i * 8, v + ((D * 128 + 32 * i) >> 4), idO, 1u);
+                tc_commit(&o_done[2 * s + 1]);
+                if (ends) tc_commit(&v_empty[vst]);
+              }
+              __syncwarp();
+              pn ^= 1u << s;
+              if (ends) {
+                vst ^= 1;
+                vph ^= vst == 0;
+              }
+            }
+            if (next) {
+              tc_fence_after();
+              const uint64_t q = dk0 + ((base + s * 2 * L::QP) >> 4), k = dk0 + ((base + L::OFF_K + kst * L::K) >> 4);
+              const uint32_t d = tm + TM_S + s * kStepTokens;
+              if (elect_one()) {
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                  for (int i = 0; i < D / 32; ++i)
+                    tc_mma_f8(d, q + ((part * L::QP + 32 * i) >> 4), k + ((32 * i) >> 4), idS, (part | i) ? 1u : 0u);
+                tc_commit(&s_full[s]);
+                if (ends) tc_commit(&k_empty[kst]);
+              }
+              __syncwarp();
+              if (ends) {
+                kst = kst == KST - 1 ? 0 : kst + 1;
+                kph ^= kst == 0;
+              }
+            }
+          }
         }
-        n0 += J;
       }
-      if (!ok) give_up();
+      if (!ok) give_up(DERR_TIMEOUT_BFULL);
       if (elect_one()) tc_commit(drain);
       __syncwarp();
       mbar_wait(drain, 0u, DERR_TIMEOUT_DRAIN);
@@ -519,11 +538,10 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
         const int kv_end = sg.past + sg.n;
         for (int j = sg.s0; j < sg.s1 && ok; ++j, ++n) {
           const int rs = n % RST, st = n % VST;
-          ok = warp_all(!*abort_flag && window(n) &&
-                        mbar_wait(&v_empty[st], ((uint32_t)(n / VST) & 1u) ^ 1u, DERR_TIMEOUT_EMPTY) &&
-                        mbar_wait(&r_full[rs], (uint32_t)(n / RST) & 1u, DERR_TIMEOUT_FULL));
+          ok = window(n) && poll(&v_empty[st], ((uint32_t)(n / VST) & 1u) ^ 1u, abort_flag) &&
+               poll(&r_full[rs], (uint32_t)(n / RST) & 1u, abort_flag);
           if (!ok) break;
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             const bool have = info_of(n, h).page >= 0;
             const int left = kv_end - (2 * j + h) * kPage;  // tokens of the page that are the sequence's
@@ -569,7 +587,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
           leave(n);
         }
       }
-      if (!ok) give_up();
+      if (!ok) give_up(DERR_TIMEOUT_BEMPTY);
     }
   } else if (run) {
     // ---- rows: thread <-> row r of slot s
@@ -581,8 +599,8 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
     uint32_t sn = 0;         // steps of this slot
     uint32_t dn = 0;         // dual segments with both slots in use
     bool ok = true;
-    auto wait = [&](uint64_t* b, uint32_t parity, uint32_t why) {
-      ok = warp_all(!*abort_flag && mbar_wait(b, parity, why));
+    auto wait = [&](uint64_t* b, uint32_t parity) {
+      ok = poll(b, parity & 1u, abort_flag);
       return ok;
     };
     // The warp's 32 rows of Q in two e4m3 parts, a row at a time over the lanes
@@ -590,7 +608,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
     // S).  Returns this thread's row's factor of S.
     auto stage = [&](const Seg& g) {
       if (g.dual && s >= g.s1 - g.s0) return 0.0f;  // the slot has no step
-      constexpr int E = D / 32, B = 16;             // elements a lane; rows in flight
+      constexpr int E = D / 32, B = 8;              // elements a lane; rows in flight
       const int first = (g.dual ? 0 : s * kSlotRows) + q4 * 32;
       float qs = 0.0f;
 #pragma unroll 1
@@ -649,40 +667,134 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
       if (lane == 0) mbar_arrive(&q_full[s]);
       return qs;
     };
-    bool have = share.next(sg);
-    float qs = have ? stage(sg) : 0.0f;
-    while (have) {
+    bool have = false;  // a segment whose result is in O
+    float qs = 0.0f, m = 0.0f, l = 0.0f, vref = 0.0f;
+    for (;;) {
+      // the next segment's rows go first: its first products run beside the epilogue of the one before
+      Seg nx;
+      const bool more = share.next(nx);
+      const float qn = more ? stage(nx) : 0.0f;
       const int J = sg.s1 - sg.s0;
       const int local = sg.dual ? r : s * kSlotRows + r;  // row of the tile
-      const bool valid = local < sg.rows;
-      const int R = sg.r0 + local, tok = valid ? R / a.G : 0;
-      const int h = sg.head * a.G + R - tok * a.G;
-      const int lim = valid ? sg.past + tok + 1 : 0;  // tokens that the row sees
-      const bool active = !sg.dual || s < J;
-      float m = -INFINITY, l = 0.0f, vref = 0.0f;
+      if (have) {
+        const bool active = !sg.dual || s < J, joined = sg.dual && J > 1;
+        if (active && !wait(&o_done[2 * s + 1], sn - 1)) break;
+        tc_fence_after();
+        float m1 = -INFINITY, l1 = 0.0f, v1 = 0.0f;
+        if (joined) {
+          if (s == 1) {
+            ml[r] = make_float4(m, l, vref, 0.0f);
+            tc_fence_before();
+          }
+          __syncwarp();
+          if (s == 1 && lane == 0) mbar_arrive(ml_full);
+          // slot 0 takes both; slot 1 goes on when O of it has been read
+          if (!wait(s == 1 ? o1_free : ml_full, dn)) break;
+          ++dn;
+          tc_fence_after();
+          if (s == 0) {
+            const float4 y = ml[r];
+            m1 = y.x;
+            l1 = y.y;
+            v1 = y.z;
+          }
+        }
+        if (!(sg.dual && s == 1)) {
+          const bool valid = local < sg.rows;
+          const int R = sg.r0 + local, tok = valid ? R / a.G : 0, h = sg.head * a.G + R - tok * a.G;
+          const float mm = fmaxf(m, m1), ref = mm == -INFINITY ? 0.0f : mm;
+          const float e0 = m == -INFINITY ? 0.0f : ex2(m - ref), e1 = m1 == -INFINITY ? 0.0f : ex2(m1 - ref);
+          const float sum = l * e0 + l1 * e1;
+          const bool none = sum == 0.0f;
+          const float inv = none ? 0.0f : (1.0f / (1 << kChMargin)) / sum;
+          const float f0 = e0 * vref * inv, f1 = e1 * v1 * inv;
+          const float lse2 = none ? -INFINITY : mm + log2f(sum);
+          uint16_t* dst = a.o + (int64_t)(sg.row0 + tok) * a.so + h * D;
+          const int64_t part = (int64_t)sg.slot * kChunkRows + local;
+          const bool v8 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0u && (a.so & 15) == 0;
+#pragma unroll 1
+          for (int cc = 0; cc < D; cc += 16) {
+            uint32_t o0[16], o1[16];
+            tmem_ld_32x32b_x16(t_o + cc, o0);
+            if (joined) tmem_ld_32x32b_x16(trow + TM_O + D + cc, o1);
+            tmem_ld_wait();
+            if (valid) {
+              float y[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                y[i] = none ? 0.0f : __uint_as_float(o0[i]) * f0;
+                if (joined && !none) y[i] += __uint_as_float(o1[i]) * f1;
+              }
+              if (sg.slot >= 0) {
+                float* d = c.part_o + part * D + cc;
+#pragma unroll
+                for (int i = 0; i < 16; i += 8)
+                  st_global_v8(d + i, __float_as_uint(y[i]), __float_as_uint(y[i + 1]), __float_as_uint(y[i + 2]),
+                               __float_as_uint(y[i + 3]), __float_as_uint(y[i + 4]), __float_as_uint(y[i + 5]),
+                               __float_as_uint(y[i + 6]), __float_as_uint(y[i + 7]));
+              } else {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
+                if (v8) {
+                  st_global_v8(dst + cc, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+                } else {
+                  *reinterpret_cast<uint4*>(dst + cc) = make_uint4(w[0], w[1], w[2], w[3]);
+                  *reinterpret_cast<uint4*>(dst + cc + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+              }
+            }
+            __syncwarp();
+          }
+          if (valid) {
+            if (sg.slot >= 0)
+              c.part_l[part] = lse2;
+            else if (a.lse)
+              a.lse[(int64_t)h * a.T + sg.row0 + tok] = lse2 * kLn2;
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (joined && lane == 0) mbar_arrive(o1_free);
+        }
+      }
+      if (!more) break;
+      sg = nx;
+      qs = qn;
+      have = true;
+      m = -INFINITY;
+      l = vref = 0.0f;
+      const int J1 = sg.s1 - sg.s0, mine = sg.dual ? r : s * kSlotRows + r;
+      const int lim = mine < sg.rows ? sg.past + (sg.r0 + mine) / a.G + 1 : 0;  // tokens that the row sees
       bool begun = false;  // something is in O
-      for (int j = 0; j < J; ++j) {
+      for (int j = 0; j < J1; ++j) {
         const int n = n0 + j;
-        if (!(ok = warp_all(!*abort_flag && window(n)))) break;
+        if (!(ok = window(n))) break;
         if (sg.dual && (j & 1) != s) {
           leave(n);
           continue;
         }
-        if (!wait(&s_full[s], sn & 1u, DERR_TIMEOUT_ACC)) break;
+        if (!wait(&s_full[s], sn)) break;
         tc_fence_after();
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           const PageInfo pi = info_of(n, half);
-          uint32_t p[32];
-          if (pi.page < 0) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) p[i] = 0u;
-          } else {
+          const uint32_t t_p = t_s + half * 32, t_v = t_s + half * kPage;
+          float cf = qs * pi.ks;
+          cf = cf < 1e-37f ? 1e-37f : cf;  // not below fp32's range: -inf * 0 is NaN
+          const int vis = pi.page >= 0 ? lim - (2 * (sg.s0 + j) + half) * kPage : 0;  // of the page, seen
+          // The ordinary page: all rows see all of it, m stands and the scale of its P is a power of two, 2^e, which
+          // goes into the exponent.  The sum bounds the largest: at 2^kLag or less, m may stay.
+          const int e = (int)(__float_as_uint(pi.vs) >> 23) - (int)(__float_as_uint(vref) >> 23) + kChMargin;
+          const bool plain = ((__float_as_uint(pi.vs) | __float_as_uint(vref)) & 0x7fffffu) == 0u && e >= -20 &&
+                             e <= kChMargin && vis >= kPage && m > -INFINITY;
+          bool grown = false, rest = true;
+          if (warp_all(plain)) {
+            uint32_t p[32];
             float v[64];
             {
               uint32_t x0[32], x1[32];
-              tmem_ld_32x32b_x32(t_s + half * kPage, x0);
-              tmem_ld_32x32b_x32(t_s + half * kPage + 32, x1);
+              tmem_ld_32x32b_x32(t_v, x0);
+              tmem_ld_32x32b_x32(t_v + 32, x1);
               tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
@@ -690,65 +802,69 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
                 v[32 + i] = __uint_as_float(x1[i]);
               }
             }
-            float cf = qs * pi.ks;
-            cf = cf < 1e-37f ? 1e-37f : cf;  // not below fp32's range: -inf * 0 is NaN
-            const int vis = lim - (2 * (sg.s0 + j) + half) * kPage;
-            // The ordinary page: all rows see all of it, m stands and vr is a power of two, 2^e, which goes
-            // into the exponent.  The sum bounds the largest: at 2^kLag or less, m may stay.
-            const int e = (int)(__float_as_uint(pi.vs) >> 23) - (int)(__float_as_uint(vref) >> 23) + kChMargin;
-            const bool plain = ((__float_as_uint(pi.vs) | __float_as_uint(vref)) & 0x7fffffu) == 0u && e >= -20 &&
-                               e <= kChMargin && vis >= kPage && m > -INFINITY;
-            bool grown = false, rest = true;
-            if (warp_all(plain)) {
-              const float sum = weigh_plain(v, cf, m - (float)e, p) * __uint_as_float((uint32_t)(127 - e) << 23);
-              grown = !(sum <= (float)(1 << kLag));
-              rest = !warp_all(!grown);
-              if (!rest) l += sum;
-            }
-            if (rest) {
-              const bool masked = __any_sync(0xffffffffu, vis < kPage);
-              if (masked) {
-#pragma unroll
-                for (int i = 0; i < 64; ++i)
-                  if (i >= vis) v[i] = -INFINITY;
-              }
-              float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-              for (int i = 0; i < 64; i += 4)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) t[k] = fmaxf(t[k], v[i + k]);
-              const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * cf;
-              const bool up = top > m + (grown ? 0.0f : (float)kLag);
-              if (__any_sync(0xffffffffu, up || pi.vs > vref)) {
-                const float nm = up ? top : m;
-                const float nv = fmaxf(vref, pi.vs);  // a NaN scale is no reference
-                float f = nm == m ? 1.0f : ex2(m - nm);
-                l *= f;
-                f *= vref == nv ? 1.0f : vref / nv;
-                m = nm;
-                vref = nv;
-                if (begun) {
-                  // O of the halves before
-                  if (!wait(&o_done[2 * s + (half ^ 1)], (sn + half - 1) & 1u, DERR_TIMEOUT_ACC)) break;
-                  tc_fence_after();
-#pragma unroll 1
-                  for (int cc = 0; cc < D; cc += 16) {
-                    uint32_t o[16];
-                    tmem_ld_32x32b_x16(t_o + cc, o);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                    tmem_st_32x32b_x16(t_o + cc, o);
-                  }
-                  tmem_st_wait();
-                }
-              }
-              const float ref = m == -INFINITY ? 0.0f : m;
-              const float vr = (pi.vs == 0.0f ? 0.0f : pi.vs / vref) * (float)(1 << kChMargin);
-              l += weigh(v, cf, ref, vr, vis, p);
+            const float sum = weigh_plain(v, cf, m - (float)e, p) * __uint_as_float((uint32_t)(127 - e) << 23);
+            grown = !(sum <= (float)(1 << kLag));
+            rest = !warp_all(!grown);
+            if (!rest) {
+              l += sum;
+              tmem_st_32x32b_x32(t_p, p);
             }
           }
-          tmem_st_32x32b_x32(t_s + half * 32, p);
+          if (rest) {
+            // Any other page, 16 columns at a time: the maximum, then P, whose columns follow behind those of S.
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int cc = 0; cc < kPage; cc += 16) {
+              uint32_t x[16];
+              tmem_ld_32x32b_x16(t_v + cc, x);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) top = cc + i < vis ? fmaxf(top, __uint_as_float(x[i])) : top;
+            }
+            top *= cf;
+            const bool up = top > m + (grown ? 0.0f : (float)kLag);
+            if (__any_sync(0xffffffffu, up || pi.vs > vref)) {
+              const float nm = up ? top : m;
+              const float nv = fmaxf(vref, pi.vs);  // a NaN scale is no reference
+              float f = nm == m ? 1.0f : ex2(m - nm);
+              l *= f;
+              f *= vref == nv ? 1.0f : vref / nv;
+              m = nm;
+              vref = nv;
+              if (begun) {
+                // O of the halves before
+                if (!wait(&o_done[2 * s + (half ^ 1)], sn + half - 1)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int cc = 0; cc < D; cc += 16) {
+                  uint32_t o[16];
+                  tmem_ld_32x32b_x16(t_o + cc, o);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                  tmem_st_32x32b_x16(t_o + cc, o);
+                }
+              }
+            }
+            const float ref = m == -INFINITY ? 0.0f : m;
+            const float vr = (pi.vs == 0.0f ? 0.0f : pi.vs / vref) * (float)(1 << kChMargin);
+#pragma unroll 1
+            for (int cc = 0; cc < kPage; cc += 16) {
+              uint32_t x[16], p[8];
+              tmem_ld_32x32b_x16(t_v + cc, x);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                // a row gets none of the scales of a page that it does not see, NaN included
+                const bool in0 = cc + 2 * i < vis, in1 = cc + 2 * i + 1 < vis;
+                const float y0 = in0 ? ex2(fmaf(__uint_as_float(x[2 * i]), cf, -ref)) : 0.0f;
+                const float y1 = in1 ? ex2(fmaf(__uint_as_float(x[2 * i + 1]), cf, -ref)) : 0.0f;
+                l += y0 + y1;
+                p[i] = pack_f16x2(in0 ? y0 * vr : 0.0f, in1 ? y1 * vr : 0.0f);
+              }
+              tmem_st_32x32b_x8(t_p + cc / 2, p);
+            }
+          }
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -760,97 +876,9 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
         leave(n);
       }
       if (!ok) break;
-      n0 += J;
-      // ---- the segment's end; the next one's rows go first, and its first products run beside this
-      Seg nx;
-      have = share.next(nx);
-      const float qn = have ? stage(nx) : 0.0f;
-      const bool joined = sg.dual && J > 1;
-      if (active && !wait(&o_done[2 * s + 1], (sn - 1) & 1u, DERR_TIMEOUT_ACC)) break;
-      tc_fence_after();
-      float m1 = -INFINITY, l1 = 0.0f, v1 = 0.0f;
-      if (joined) {
-        if (s == 1) {
-          ml[r] = make_float4(m, l, vref, 0.0f);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(ml_full);
-          // slot 0 has read O of slot 1 before this slot goes on
-          if (!wait(o1_free, dn & 1u, DERR_TIMEOUT_ACC)) break;
-        } else {
-          if (!wait(ml_full, dn & 1u, DERR_TIMEOUT_ACC)) break;
-          tc_fence_after();
-          const float4 y = ml[r];
-          m1 = y.x;
-          l1 = y.y;
-          v1 = y.z;
-        }
-        ++dn;
-      }
-      if (!(sg.dual && s == 1)) {
-        const float mm = fmaxf(m, m1), ref = mm == -INFINITY ? 0.0f : mm;
-        const float e0 = m == -INFINITY ? 0.0f : ex2(m - ref), e1 = m1 == -INFINITY ? 0.0f : ex2(m1 - ref);
-        const float sum = l * e0 + l1 * e1;
-        const bool none = sum == 0.0f;
-        const float inv = none ? 0.0f : (1.0f / (1 << kChMargin)) / sum;
-        const float f0 = e0 * vref * inv, f1 = e1 * v1 * inv;
-        const float lse2 = none ? -INFINITY : mm + log2f(sum);
-        uint16_t* dst = a.o + (int64_t)(sg.row0 + tok) * a.so + h * D;
-        const int64_t part = (int64_t)sg.slot * kChunkRows + local;
-        const bool v8 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0u && (a.so & 15) == 0;
-#pragma unroll 1
-        for (int cc = 0; cc < D; cc += 32) {
-          uint32_t o0[32], o1[32];
-          tmem_ld_32x32b_x32(t_o + cc, o0);
-          if (joined) tmem_ld_32x32b_x32(trow + TM_O + D + cc, o1);
-          tmem_ld_wait();
-          if (valid) {
-            float y[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              y[i] = none ? 0.0f : __uint_as_float(o0[i]) * f0;
-              if (joined && !none) y[i] += __uint_as_float(o1[i]) * f1;
-            }
-            if (sg.slot >= 0) {
-              float* d = c.part_o + part * D + cc;
-#pragma unroll
-              for (int i = 0; i < 32; i += 8)
-                st_global_v8(d + i, __float_as_uint(y[i]), __float_as_uint(y[i + 1]), __float_as_uint(y[i + 2]),
-                             __float_as_uint(y[i + 3]), __float_as_uint(y[i + 4]), __float_as_uint(y[i + 5]),
-                             __float_as_uint(y[i + 6]), __float_as_uint(y[i + 7]));
-            } else {
-              uint32_t w[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
-              if (v8) {
-                st_global_v8(dst + cc, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
-                st_global_v8(dst + cc + 16, w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  *reinterpret_cast<uint4*>(dst + cc + 8 * i) =
-                      make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-              }
-            }
-          }
-          __syncwarp();
-        }
-        if (valid) {
-          if (sg.slot >= 0)
-            c.part_l[part] = lse2;
-          else if (a.lse)
-            a.lse[(int64_t)h * a.T + sg.row0 + tok] = lse2 * kLn2;
-        }
-        tc_fence_before();
-        if (joined) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(o1_free);
-        }
-      }
-      sg = nx;
-      qs = qn;
+      n0 += J1;
     }
-    if (!ok) give_up();
+    if (!ok) give_up(DERR_TIMEOUT_ACC);
   }
   tc_fence_before();
   __syncthreads();
