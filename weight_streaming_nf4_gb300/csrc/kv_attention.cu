@@ -64,9 +64,10 @@ WS_DEVINL float q_scale(float top) {
 template <int D>
 struct DecodeSmem {
   static constexpr uint32_t PAGE = kPage * D;      // bytes of a page's keys, or values
-  static constexpr uint32_t WARP = 2 * PAGE;       // both
-  static constexpr uint32_t OFF_BAR = kDecodeWarps * WARP;
-  static constexpr uint32_t BYTES = OFF_BAR + kDecodeWarps * 16 + 128;
+  static constexpr int RING = 3;                   // a warp's copies: keys, values, keys, ... in turn
+  static constexpr uint32_t OFF_BAR = kDecodeWarps * RING * PAGE;
+  static constexpr uint32_t BYTES = OFF_BAR + kDecodeWarps * RING * 8 + 128;
+  static constexpr int CTAS = decode_warps(D) / kDecodeWarps;  // an SM
 };
 
 // A page of a tile on a warp's way: what it takes to load and to use it.
@@ -78,7 +79,7 @@ struct Step {
 };
 
 template <int D, int NQ>
-__global__ void __launch_bounds__(kDecodeWarps * 32, 3) k_kv_decode(const __grid_constant__ KvAttnArgs a) {
+__global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_decode(const __grid_constant__ KvAttnArgs a) {
   using L = DecodeSmem<D>;
   constexpr int KS = D / 16;   // contraction steps of S
   constexpr int HT = D / 16;   // 16-element tiles of O
@@ -86,12 +87,10 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 3) k_kv_decode(const __grid
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   const int warp = (int)warp_id(), lane = (int)lane_id(), g = lane >> 2, t = lane & 3;
-  uint8_t* sk = smem + warp * L::WARP;
-  uint8_t* sv = sk + L::PAGE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR) + 2 * warp;
+  uint8_t* ring = smem + warp * (L::RING * L::PAGE);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR) + L::RING * warp;
   if (lane == 0) {
-    mbar_init(&bars[0], 1);
-    mbar_init(&bars[1], 1);
+    for (int i = 0; i < L::RING; ++i) mbar_init(&bars[i], 1);
     fence_barrier_init();
   }
   __syncwarp();
@@ -108,8 +107,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 3) k_kv_decode(const __grid
   if (u >= U) return;
   const int begin = (int)unit_start(u, W, U), end = (int)unit_start(u + 1, W, U);
 
-  // the steps: pages begin .. end - 1 of the tiles' pages behind one another
+  // The steps: pages begin .. end - 1 of the tiles' pages behind one another.
   auto fill = [&](Step& s) {
+    s.ks = s.vs = 0.0f;
     s.page = a.table[(int64_t)s.seq * a.max_pages + s.p];
     if (s.page < 0 || s.page >= a.n_pages) {
       s.page = -1;
@@ -126,19 +126,56 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 3) k_kv_decode(const __grid
     s.p = max(begin, tl.z) - tl.z;
     s.pend = min(end, tiles[tile + 1].z) - tl.z;
   };
-  auto load = [&](const Step& s, bool values) {
-    if (s.page < 0 || lane) return;
-    const int64_t at = ((int64_t)s.page * a.nkv + head) * L::PAGE;
-    mbar_arrive_expect_tx(&bars[values], L::PAGE);
-    bulk_load(values ? sv : sk, (values ? a.v : a.k) + at, L::PAGE, &bars[values]);
+  auto follow = [&](Step& s) {  // the step behind s, none: pend 0
+    if (s.p + 1 < s.pend) {
+      ++s.p;
+    } else if (tiles[s.tile + 1].z < end) {
+      enter(s, s.tile + 1);
+    } else {
+      s.pend = 0;
+      s.page = -1;
+      return;
+    }
+    fill(s);
   };
-  Step nxt;
-  enter(nxt, reinterpret_cast<const int*>(a.plan + a.L.unit)[u]);
-  fill(nxt);
+  // Copies go round the ring; a page that is none completes its turn at once.
+  int in = 0, out = 0;            // ring places of the next copy, and of the next to be used
+  uint32_t out_ph = 0;
+  auto load = [&](const Step& s, bool values) {
+    if (s.pend == 0) return;
+    if (lane == 0) {
+      if (s.page < 0) {
+        mbar_arrive(&bars[in]);
+      } else {
+        const int64_t at = ((int64_t)s.page * a.nkv + head) * L::PAGE;
+        mbar_arrive_expect_tx(&bars[in], L::PAGE);
+        bulk_load(ring + in * L::PAGE, (values ? a.v : a.k) + at, L::PAGE, &bars[in]);
+      }
+    }
+    in = in == L::RING - 1 ? 0 : in + 1;
+  };
+  // The next copy has come.  Where it does not, the others in flight are waited for.
+  auto take = [&]() {
+    if (__all_sync(0xffffffffu, mbar_wait(&bars[out], out_ph, DERR_TIMEOUT_FULL))) return true;
+    for (int i = 1; i < L::RING; ++i) {
+      const int b = (out + i) % L::RING;
+      mbar_wait(&bars[b], out + i >= L::RING ? out_ph ^ 1u : out_ph, DERR_TIMEOUT_DRAIN);
+    }
+    return false;
+  };
+  auto next_place = [&]() {
+    out = out == L::RING - 1 ? 0 : out + 1;
+    out_ph ^= out == 0;
+  };
+  Step cur, nxt, nx2;
+  enter(cur, reinterpret_cast<const int*>(a.plan + a.L.unit)[u]);
+  fill(cur);
+  nxt = cur;
+  follow(nxt);
+  load(cur, false);
+  load(cur, true);
   load(nxt, false);
-  load(nxt, true);
-  bool more = true, fresh = true;
-  uint32_t phase = 0;
+  bool fresh = true;
 
   uint32_t bq[NQ][KS][2];          // Q^T operands
   float o[NQ][HT][4];              // O^T: elements 16 ht + g (+ 8), rows 8 nq + 2t (+ 1)
@@ -148,17 +185,10 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 3) k_kv_decode(const __grid
   int rows = 0, kv_end = 0, first_lim = 0;
   int4 tl = make_int4(0, 0, 0, 0), sq = tl;
 
-  while (more) {
-    const Step cur = nxt;
+  for (; cur.pend != 0; cur = nxt, nxt = nx2) {
     const bool last = cur.p + 1 == cur.pend;
-    if (!last)
-      ++nxt.p;
-    else
-      more = tiles[cur.tile + 1].z < end;
-    if (more) {
-      if (last) enter(nxt, cur.tile + 1);
-      fill(nxt);
-    }
+    nx2 = nxt;
+    if (nxt.pend != 0) follow(nx2);
     if (fresh) {
       tl = tiles[cur.tile];
       sq = seqs[cur.seq];
@@ -211,11 +241,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 3) k_kv_decode(const __grid
       }
     }
 
+    if (!take()) return;
     if (cur.page >= 0) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&bars[0], phase, DERR_TIMEOUT_FULL))) {
-        mbar_wait(&bars[1], phase, DERR_TIMEOUT_DRAIN);
-        return;
-      }
+      const uint8_t* sk = ring + out * L::PAGE;
       // S^T.  Row r of block b (8 rows) is token 16 (r / 2) + 2 b + r % 2.
       float s[NQ][4][4];
 #pragma unroll
@@ -243,7 +271,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 3) k_kv_decode(const __grid
         }
       }
       __syncwarp();
-      if (more) load(nxt, false);
+      next_place();
+      load(nxt, true);
 
       // softmax: columns (rows of q) 2t, 2t + 1; tokens 16 (g / 2) + 4 mt + g % 2 (+ 2)
       const int tok0 = cur.p * kPage + 16 * (g >> 1) + (g & 1);
@@ -263,24 +292,25 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 3) k_kv_decode(const __grid
       uint32_t bp[NQ][4][2];
 #pragma unroll
       for (int nq = 0; nq < NQ; ++nq) {
-        float nm[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float c = qs[nq][e] * cur.ks;
-          float top = -INFINITY;
+        float nm[2], cf[2];
+        if (tail) {
 #pragma unroll
           for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float& x = s[nq][mt][2 * h + e];
-              x *= c;
-              if (tail && tok0 + 4 * mt + 2 * h >= lim[nq][e]) x = -INFINITY;
-              top = fmaxf(top, x);
-            }
+            for (int i = 0; i < 4; ++i)
+              if (tok0 + 4 * mt + 2 * (i >> 1) >= lim[nq][i & 1]) s[nq][mt][i] = -INFINITY;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float c = qs[nq][e] * cur.ks;
+          cf[e] = c < 1e-37f ? 1e-37f : c;  // not below fp32's range: -inf * 0 is NaN
+          float top = -INFINITY;
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) top = fmaxf(top, fmaxf(s[nq][mt][e], s[nq][mt][2 + e]));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          nm[e] = fmaxf(m[nq][e], top);
+          nm[e] = fmaxf(m[nq][e], top * cf[e]);
         }
         const bool moved = nm[0] != m[nq][0] || nm[1] != m[nq][1];
         if (__any_sync(0xffffffffu, moved)) {
@@ -304,27 +334,38 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 3) k_kv_decode(const __grid
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float& x = s[nq][mt][2 * h + e];
-              x = ex2(x - ref);
-              l[nq][e] += x;
+              x = ex2(fmaf(x, cf[e], -ref));
             }
+        }
+        if (tail) {  // a row gets none of the scales of a page that it does not see, NaN included
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (tok0 + 4 * mt + 2 * (i >> 1) >= lim[nq][i & 1]) s[nq][mt][i] = 0.0f;
         }
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float x0 = s[nq][mt][2 * h] * vr, x1 = s[nq][mt][2 * h + 1] * vr;
-            if (tail) {  // a row that does not see a token gets none of its page's scale, NaN included
-              if (tok0 + 4 * mt + 2 * h >= lim[nq][0]) x0 = 0.0f;
-              if (tok0 + 4 * mt + 2 * h >= lim[nq][1]) x1 = 0.0f;
-            }
-            bp[nq][mt][h] = transpose8x8(pack_f16x2(x0, x1));
+          for (int i = 0; i < 4; ++i) {
+            l[nq][i & 1] += s[nq][mt][i];
+            s[nq][mt][i] *= vr;
           }
+        if (tail) {
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (tok0 + 4 * mt + 2 * (i >> 1) >= lim[nq][i & 1]) s[nq][mt][i] = 0.0f;
+        }
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) bp[nq][mt][h] = transpose8x8(pack_f16x2(s[nq][mt][2 * h], s[nq][mt][2 * h + 1]));
       }
 
-      if (!__all_sync(0xffffffffu, mbar_wait(&bars[1], phase, DERR_TIMEOUT_FULL))) {
-        if (more && nxt.page >= 0) mbar_wait(&bars[0], phase ^ 1u, DERR_TIMEOUT_DRAIN);
-        return;
-      }
+      if (!take()) return;
+      const uint8_t* sv = ring + out * L::PAGE;
       // places behind the last token hold anything: P is zero there, and a code could be NaN
       const int left = kv_end - cur.p * kPage - 16 * t;
 #pragma unroll
@@ -351,11 +392,14 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 3) k_kv_decode(const __grid
         }
       }
       __syncwarp();
-      if (more) load(nxt, true);
-      phase ^= 1u;
-    } else if (more) {
-      load(nxt, false);
+      next_place();
+      load(nx2, false);
+    } else {
+      next_place();
       load(nxt, true);
+      if (!take()) return;
+      next_place();
+      load(nx2, false);
     }
 
     fresh = last;
@@ -398,8 +442,10 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 3) k_kv_decode(const __grid
 }
 
 // Cut tiles: row r's pieces o_i with log2-sums l_i are sum 2^(l_i) o_i / sum 2^(l_i).
-// One CTA a row; its warps take every eighth piece, joined in their order.
-constexpr int kJoinWarps = 8;
+// One CTA a row; its warps take every sixteenth piece, eight in flight, joined in
+// their order (two contexts of 130000 tokens leave 450 pieces a row: eight warps
+// with four in flight took 30 us).
+constexpr int kJoinWarps = 16;
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const __grid_constant__ KvAttnArgs a) {
   constexpr int E = D / 32;  // elements a lane
@@ -416,23 +462,46 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const __grid_consta
   const int warp = (int)warp_id(), lane = (int)lane_id();
   const int64_t stride = (int64_t)a.nkv * kTileRows;
   const int64_t base = (int64_t)sp.y * stride + (int64_t)head * kTileRows + r;
+  // a lane's share of the pieces' log2-sums, then the warp's largest; NaN is none
   float m = -INFINITY;
-  for (int i = warp; i < sp.z; i += kJoinWarps) {
-    const float x = a.part_l[base + i * stride];
-    m = x != x ? x : fmaxf(m, x);
-    if (x != x) break;
-  }
+  for (int i = warp + kJoinWarps * lane; i < sp.z; i += kJoinWarps * 32) m = fmaxf(m, a.part_l[base + i * stride]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float acc[E], l = 0.0f;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.0f;
   const float ref = m == -INFINITY ? 0.0f : m;
-#pragma unroll 4
-  for (int i = warp; i < sp.z; i += kJoinWarps) {
-    const float wt = ex2(a.part_l[base + i * stride] - ref);
-    const float* src = a.part_o + (base + i * stride) * D + lane * E;
-    l += wt;
+  for (int i0 = warp; i0 < sp.z; i0 += 8 * kJoinWarps) {
+    float w[8], x[8][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += wt * src[e];
+    for (int k = 0; k < 8; ++k) {
+      const int i = i0 + k * kJoinWarps;
+      w[k] = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[k][e] = 0.0f;
+      if (i < sp.z) {
+        w[k] = a.part_l[base + i * stride];
+        const float* src = a.part_o + (base + i * stride) * D + lane * E;
+        if (E == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(src);
+          x[k][0] = f.x;
+          x[k][1] = f.y;
+          x[k][E - 2] = f.z;
+          x[k][E - 1] = f.w;
+        } else {
+          const float2 f = *reinterpret_cast<const float2*>(src);
+          x[k][0] = f.x;
+          x[k][1] = f.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float wt = ex2(w[k] - ref);
+      l += wt;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += wt * x[k][e];
+    }
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
@@ -475,8 +544,7 @@ KvWork kv_work(const KvShape& s, const KvLayout& L) {
 template <int D, int NQ>
 cudaError_t launch_decode(const KvAttnArgs& a, int64_t units, cudaStream_t st) {
   constexpr uint32_t bytes = DecodeSmem<D>::BYTES;
-  const cudaError_t e =
-      cudaFuncSetAttribute(k_kv_decode<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  const cudaError_t e = allow_smem<k_kv_decode<D, NQ>>((int)bytes);
   if (e != cudaSuccess) return e;
   note_launch();
   const int64_t warps = units * a.nkv;

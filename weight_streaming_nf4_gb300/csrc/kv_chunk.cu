@@ -930,8 +930,7 @@ __global__ void __launch_bounds__(kChJoinRows * 32) k_kv_chunk_join(const __grid
 
 template <int D>
 cudaError_t launch_chunk(const ChunkArgs& c, cudaStream_t st) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(k_kv_chunk<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ChSmem<D>::BYTES);
+  const cudaError_t e = allow_smem<k_kv_chunk<D>>((int)ChSmem<D>::BYTES);
   if (e != cudaSuccess) return e;
   note_launch();
   const cudaError_t f = launch_pdl(k_kv_chunk<D>, dim3((unsigned)c.a.L.c_max_units), dim3(kChThreads),

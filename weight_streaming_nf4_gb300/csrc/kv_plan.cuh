@@ -2,6 +2,7 @@
 // k_kv_plan writes on the device and the append and attention kernels read.
 #pragma once
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -10,7 +11,9 @@ namespace ws {
 
 constexpr int kPage = WS_KV_PAGE;
 constexpr int kTileRows = 16;    // rows of a tile of the decode kernel, which has the sequences of up to so many
-constexpr int kWarpsPerSm = 12;  // of the decode kernel, resident
+// Resident warps of the decode kernel an SM: eight with 24 KB of pages on their
+// way each (D = 128), twelve with 12 KB (D = 64).
+constexpr int decode_warps(int hd) { return hd == 128 ? 8 : 12; }
 constexpr int kChunkRows = 256;  // rows of a tile of the chunk kernel, which has the others
 constexpr int kChunkMinSteps = 4;  // steps (two pages) of a share of the chunk kernel's work, at least
 
@@ -65,7 +68,7 @@ inline KvLayout kv_layout(const KvShape& s) {
   L.max_append = std::min<int64_t>(std::min<int64_t>(s.T, live * (((int64_t)s.max_new + 62) / kPage + 1)),
                                    s.T / kPage + 2 * live);
   L.max_tiles = G <= kTileRows ? live : 0;
-  L.max_units = std::max<int64_t>(1, (int64_t)device_sm_count() * kWarpsPerSm / s.nkv);
+  L.max_units = std::max<int64_t>(1, (int64_t)device_sm_count() * decode_warps(s.hd) / s.nkv);
   L.c_max_tiles = kv_chunk_tiles(s);
   L.c_max_units = device_sm_count();
   size_t o = sizeof(KvHeader);
@@ -111,6 +114,20 @@ struct KvAttnArgs {
   int nkv, G, max_pages;
   float sl2;            // softmax scale times log2(e)
 };
+
+// Lets a kernel have `bytes` of dynamic shared memory, once a device.
+template <auto KERNEL>
+inline cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // 2^x with the hardware approximation (relative error about 2^-22).
 WS_DEVINL float ex2(float x) {

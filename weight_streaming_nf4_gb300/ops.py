@@ -875,6 +875,7 @@ class Rope:
         self.turns = torch.tensor([x - (1 << 64) if x >> 63 else x for x in t], dtype=torch.int64, device=device)
         self.rot, self.interleaved, self.factor = 2 * n, bool(interleaved), float(factor)
         self.c = RopeC(self.turns.data_ptr(), self.rot, int(self.interleaved), self.factor, 0)
+        self.ref = C.byref(self.c)
 
 
 def rope(rot: int, base: float = 10000.0, interleaved=False, scaling="none", inv_freq=None, factor=None,
@@ -891,29 +892,48 @@ def rope(rot: int, base: float = 10000.0, interleaved=False, scaling="none", inv
     return Rope(inv_freq, interleaved, out if factor is None else factor, device)
 
 
-def _rows_ok(t, M, heads, hd, name):
-    """bf16 rows [M, heads*hd] whose rows are contiguous, at any stride (a multiple of 8)."""
-    _need(t.dtype == torch.bfloat16 and t.dim() == 2 and t.shape[0] == M and t.shape[1] == heads * hd
-          and t.stride(1) == 1 and (M == 1 or t.stride(0) >= heads * hd), f"{name}: bf16 [M, heads*head_dim], rows contiguous")
-    if t.get_device() != _device():
-        raise ValueError(f"{name} on {t.device}; the call runs on the current device (cuda:{_device()})")
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
-def _row_stride(t):
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _rows(t, M, width, dev, name):
+    """Row stride of bf16 rows [M, width] on device `dev`: rows contiguous, at any stride (a multiple of 8)."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not _BF16 or len(shape) != 2 or shape[0] != M or shape[1] != width or stride[1] != 1 or t.get_device() != dev:
+        _need(t.dtype is _BF16 and tuple(shape) == (M, width), f"{name}: bf16 [{M}, {width}]")
+        _need(stride[1] == 1, f"{name}: the elements of a row lie side by side")
+        raise ValueError(f"{name} on {t.device}; the call runs on the current device (cuda:{dev})")
+    return stride[0] if M > 1 else width
 
 
-def _rope_checks(q, k, head_dim, rope, positions, q_gain, k_gain):
-    _need(q.dim() == 2 and k.dim() == 2 and q.shape[0] == k.shape[0], "q and k: [M, heads*head_dim]")
-    M, nh, nkv = q.shape[0], q.shape[1] // head_dim, k.shape[1] // head_dim
-    _rows_ok(q, M, nh, head_dim, "q")
-    _rows_ok(k, M, nkv, head_dim, "k")
-    _need(rope is None or (positions is not None and positions.dtype == torch.int32 and tuple(positions.shape) == (M,)),
-          "positions: int32 [M]")
-    for g in (q_gain, k_gain):
-        _need(g is None or (g.dtype == torch.float32 and tuple(g.shape) == (head_dim,)), "gains: fp32 [head_dim]")
-    _here(positions if rope is not None else None, q_gain, k_gain, None if rope is None else rope.turns)
-    return M, nh, nkv
+def _vector(t, dtype, shape, dev, name):
+    """Address of a contiguous tensor of that type and shape on device `dev`, or None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _need(t.dtype is dtype and t.shape == shape, f"{name}: {dtype} {list(shape)}")
+        _here(t)
+    return t.data_ptr()
+
+
+def _current(stream, dev):
+    """cudaStream_t of a stream, or of the current one of device `dev`."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _rope_args(q, k, head_dim, rope, positions, q_gain, k_gain, dev):
+    """(M, query and kv heads, row strides of q and k, rope's, the positions' and the gains' addresses)."""
+    _need(q.dim() == 2 and k.dim() == 2, "q and k: [M, heads*head_dim]")
+    M, wq = q.shape
+    wk = k.shape[1]
+    _need(wq % head_dim == 0 and wk % head_dim == 0, "q and k: [M, heads*head_dim]")
+    sq, sk = _rows(q, M, wq, dev, "q"), _rows(k, M, wk, dev, "k")
+    ref = pos = None
+    if rope is not None:
+        _need(positions is not None, "positions: int32 [M]")
+        _need(rope.turns.get_device() == dev, "the rotary positions' frequencies lie on q's device")
+        ref, pos = rope.ref, _vector(positions, _I32, (M,), dev, "positions")
+    return (M, wq // head_dim, wk // head_dim, sq, sk, ref, pos, _vector(q_gain, _F32, (head_dim,), dev, "q_gain"),
+            _vector(k_gain, _F32, (head_dim,), dev, "k_gain"))
 
 
 def qk_norm_rope_fwd(q, k, head_dim: int, rope: Rope = None, positions=None, q_gain=None, k_gain=None,
@@ -921,15 +941,16 @@ def qk_norm_rope_fwd(q, k, head_dim: int, rope: Rope = None, positions=None, q_g
     """ws_qk_norm_rope_fwd: q [M, n_heads*head_dim] and k [M, n_kv_heads*head_dim] bf16 (rows may lie at a
     stride), each head normed where its gain (fp32 [head_dim]) is given, then rotated by the positions
     (int32 [M]) where `rope` is.  Returns (q_out, k_out); they may be q and k themselves."""
-    M, nh, nkv = _rope_checks(q, k, head_dim, rope, positions, q_gain, k_gain)
-    q_out = _empty((M, nh * head_dim), torch.bfloat16, q.device, stream) if q_out is None else q_out
-    k_out = _empty((M, nkv * head_dim), torch.bfloat16, q.device, stream) if k_out is None else k_out
-    _rows_ok(q_out, M, nh, head_dim, "q_out")
-    _rows_ok(k_out, M, nkv, head_dim, "k_out")
+    dev = _device()
+    M, nh, nkv, sq, sk, ref, pos, gq, gk = _rope_args(q, k, head_dim, rope, positions, q_gain, k_gain, dev)
+    if q_out is None:
+        q_out = _empty((M, nh * head_dim), _BF16, q.device, stream)
+    if k_out is None:
+        k_out = _empty((M, nkv * head_dim), _BF16, q.device, stream)
+    soq, sok = _rows(q_out, M, nh * head_dim, dev, "q_out"), _rows(k_out, M, nkv * head_dim, dev, "k_out")
     _check("ws_qk_norm_rope_fwd",
-           _lib.ws_qk_norm_rope_fwd(None if rope is None else C.byref(rope.c), _addr(positions), M, nh, nkv, head_dim,
-                                    eps, _addr(q_gain), _addr(k_gain), _addr(q), _row_stride(q), _addr(k), _row_stride(k),
-                                    _addr(q_out), _row_stride(q_out), _addr(k_out), _row_stride(k_out), _raw(stream)))
+           _lib.ws_qk_norm_rope_fwd(ref, pos, M, nh, nkv, head_dim, eps, gq, gk, q.data_ptr(), sq, k.data_ptr(), sk,
+                                    q_out.data_ptr(), soq, k_out.data_ptr(), sok, _current(stream, dev)))
     return q_out, k_out
 
 
@@ -946,33 +967,38 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, head_dim: int, rope: Rope = None, pos
     """ws_qk_norm_rope_bwd: (dq, dk, dq_gain, dk_gain) from the forward's inputs and the upstream gradients.
     want_gains: make gradients of the gains that are given (they come back None otherwise);
     grad_accumulate: add them into the given dq_gain and dk_gain."""
-    M, nh, nkv = _rope_checks(q, k, head_dim, rope, positions, q_gain, k_gain)
-    dq = _empty((M, nh * head_dim), torch.bfloat16, q.device, stream) if dq is None else dq
-    dk = _empty((M, nkv * head_dim), torch.bfloat16, q.device, stream) if dk is None else dk
-    for t, h, name in ((dq_out, nh, "dq_out"), (dk_out, nkv, "dk_out"), (dq, nh, "dq"), (dk, nkv, "dk")):
-        _rows_ok(t, M, h, head_dim, name)
+    dev = _device()
+    M, nh, nkv, sq, sk, ref, pos, gq, gk = _rope_args(q, k, head_dim, rope, positions, q_gain, k_gain, dev)
+    wq, wk = nh * head_dim, nkv * head_dim
+    if dq is None:
+        dq = _empty((M, wq), _BF16, q.device, stream)
+    if dk is None:
+        dk = _empty((M, wk), _BF16, q.device, stream)
     _need(not grad_accumulate or (want_gains and (q_gain is None or dq_gain is not None) and (k_gain is None or dk_gain is not None)),
           "grad_accumulate needs the gradients to add into")
     if not want_gains:
         dq_gain = dk_gain = None
     else:
+        _need((dq_gain is None or q_gain is not None) and (dk_gain is None or k_gain is not None),
+              "gradients of gains that are not given")
         if q_gain is not None and dq_gain is None:
-            dq_gain = _empty((head_dim,), torch.float32, q.device, stream)
+            dq_gain = _empty((head_dim,), _F32, q.device, stream)
         if k_gain is not None and dk_gain is None:
-            dk_gain = _empty((head_dim,), torch.float32, q.device, stream)
-    for g, of in ((dq_gain, q_gain), (dk_gain, k_gain)):
-        _need(g is None or (of is not None and g.dtype == torch.float32 and tuple(g.shape) == (head_dim,)),
-              "dq_gain, dk_gain: fp32 [head_dim], for gains that are given")
-    if workspace is None and (dq_gain is not None or dk_gain is not None):
-        workspace = _empty((qk_norm_rope_workspace_size(M, nh, nkv, head_dim),), torch.uint8, q.device, stream)
-    _here(dq_gain, dk_gain, workspace)
+            dk_gain = _empty((head_dim,), _F32, q.device, stream)
+    ws, nbytes = None, 0
+    if dq_gain is not None or dk_gain is not None:
+        if workspace is None:
+            workspace = _empty((qk_norm_rope_workspace_size(M, nh, nkv, head_dim),), torch.uint8, q.device, stream)
+        _here(workspace)
+        ws, nbytes = workspace.data_ptr(), workspace.nbytes
     _check("ws_qk_norm_rope_bwd",
-           _lib.ws_qk_norm_rope_bwd(None if rope is None else C.byref(rope.c), _addr(positions), M, nh, nkv, head_dim,
-                                    eps, _addr(q_gain), _addr(k_gain), _addr(q), _row_stride(q), _addr(k), _row_stride(k),
-                                    _addr(dq_out), _row_stride(dq_out), _addr(dk_out), _row_stride(dk_out),
-                                    _addr(dq), _row_stride(dq), _addr(dk), _row_stride(dk), _addr(dq_gain), _addr(dk_gain),
-                                    WS_ACC_GRADS if grad_accumulate else 0, _addr(workspace),
-                                    0 if workspace is None else workspace.nbytes, _raw(stream)))
+           _lib.ws_qk_norm_rope_bwd(ref, pos, M, nh, nkv, head_dim, eps, gq, gk, q.data_ptr(), sq, k.data_ptr(), sk,
+                                    dq_out.data_ptr(), _rows(dq_out, M, wq, dev, "dq_out"),
+                                    dk_out.data_ptr(), _rows(dk_out, M, wk, dev, "dk_out"),
+                                    dq.data_ptr(), _rows(dq, M, wq, dev, "dq"), dk.data_ptr(), _rows(dk, M, wk, dev, "dk"),
+                                    _vector(dq_gain, _F32, (head_dim,), dev, "dq_gain"),
+                                    _vector(dk_gain, _F32, (head_dim,), dev, "dk_gain"),
+                                    WS_ACC_GRADS if grad_accumulate else 0, ws, nbytes, _current(stream, dev)))
     return dq, dk, dq_gain, dk_gain
 
 
@@ -994,6 +1020,7 @@ class KVCache:
         self.k, self.v, self.scale = k.detach(), v.detach(), scale.detach()
         self.n_pages, self.n_kv_heads, _, self.head_dim = k.shape
         self.c = KVCacheC(k.data_ptr(), v.data_ptr(), scale.data_ptr(), self.n_pages, self.n_kv_heads, self.head_dim)
+        self.ref, self.device = C.byref(self.c), k.get_device()
 
 
 def kv_cache(n_pages: int, n_kv_heads: int, head_dim: int, device="cuda") -> KVCache:
@@ -1016,6 +1043,7 @@ class KVPlan:
         _check("ws_kv_plan_size", _lib.ws_kv_plan_size(C.byref(self.c), C.byref(n)))
         self.data = _empty((int(n.value),), torch.uint8, table.device, stream)
         self.c.data = self.data.data_ptr()
+        self.ref, self.device = C.byref(self.c), table.get_device()
 
 
 def kv_plan(past, row_start, page_table, T: int, max_new: int, n_heads: int, n_kv_heads: int, head_dim: int,
@@ -1036,19 +1064,21 @@ def kv_plan(past, row_start, page_table, T: int, max_new: int, n_heads: int, n_k
     return plan
 
 
-def _kv_checks(cache, plan):
-    _need((cache.n_kv_heads, cache.head_dim) == (plan.n_kv_heads, plan.head_dim), "the plan was made for another cache")
-    d = _device()
-    _need(cache.k.get_device() == d and plan.data.get_device() == d, "the cache and the plan lie on the current device")
+def _kv_device(cache, plan):
+    """The current device, where the cache and the plan have to be."""
+    dev = _device()
+    if cache.device != dev or plan.device != dev or cache.head_dim != plan.head_dim or cache.n_kv_heads != plan.n_kv_heads:
+        _need((cache.n_kv_heads, cache.head_dim) == (plan.n_kv_heads, plan.head_dim), "the plan was made for another cache")
+        raise ValueError(f"the cache and the plan lie on the current device (cuda:{dev})")
+    return dev
 
 
 def kv_append(cache: KVCache, plan: KVPlan, k, v, stream=None):
     """ws_kv_append: the step's rows k and v [T, n_kv_heads*head_dim] bf16 (rows may lie at a stride) into the cache."""
-    _kv_checks(cache, plan)
-    _rows_ok(k, plan.T, plan.n_kv_heads, plan.head_dim, "k")
-    _rows_ok(v, plan.T, plan.n_kv_heads, plan.head_dim, "v")
-    _check("ws_kv_append", _lib.ws_kv_append(C.byref(cache.c), C.byref(plan.c), _addr(k), _row_stride(k), _addr(v),
-                                             _row_stride(v), _raw(stream)))
+    dev = _kv_device(cache, plan)
+    w = plan.n_kv_heads * plan.head_dim
+    sk, sv = _rows(k, plan.T, w, dev, "k"), _rows(v, plan.T, w, dev, "v")
+    _check("ws_kv_append", _lib.ws_kv_append(cache.ref, plan.ref, k.data_ptr(), sk, v.data_ptr(), sv, _current(stream, dev)))
 
 
 def attention_kv_workspace_size(plan: KVPlan) -> int:
@@ -1062,22 +1092,20 @@ def attention_kv(q, cache: KVCache, plan: KVPlan, scale: float = None, o=None, l
     """ws_attention_kv: the step's rows q [T, n_heads*head_dim] bf16 over the cache (the step's own keys and values
     appended before).  scale: 1/sqrt(head_dim) unless given.  Returns (o bf16 [T, n_heads*head_dim], lse fp32
     [n_heads, T] or None)."""
-    _kv_checks(cache, plan)
+    dev = _kv_device(cache, plan)
     T, nh, hd = plan.T, plan.n_heads, plan.head_dim
-    _rows_ok(q, T, nh, hd, "q")
+    sq = _rows(q, T, nh * hd, dev, "q")
     if o is None:
-        o = _empty((T, nh * hd), torch.bfloat16, q.device, stream)
-    _rows_ok(o, T, nh, hd, "o")
+        o = _empty((T, nh * hd), _BF16, q.device, stream)
     if lse is None and want_lse:
-        lse = _empty((nh, T), torch.float32, q.device, stream)
-    _need(lse is None or (lse.dtype == torch.float32 and tuple(lse.shape) == (nh, T)), "lse: fp32 [n_heads, T]")
+        lse = _empty((nh, T), _F32, q.device, stream)
     if workspace is None:
         workspace = _empty((attention_kv_workspace_size(plan),), torch.uint8, q.device, stream)
-    _here(lse, workspace)
+    _here(workspace)
     _check("ws_attention_kv",
-           _lib.ws_attention_kv(C.byref(cache.c), C.byref(plan.c), _addr(q), _row_stride(q),
-                                hd ** -0.5 if scale is None else scale, _addr(o), _row_stride(o), _addr(lse),
-                                _addr(workspace), workspace.nbytes, _raw(stream)))
+           _lib.ws_attention_kv(cache.ref, plan.ref, q.data_ptr(), sq, hd ** -0.5 if scale is None else scale, o.data_ptr(),
+                                _rows(o, T, nh * hd, dev, "o"), _vector(lse, _F32, (nh, T), dev, "lse"),
+                                workspace.data_ptr(), workspace.nbytes, _current(stream, dev)))
     return o, lse
 
 
