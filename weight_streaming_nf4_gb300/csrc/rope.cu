@@ -29,7 +29,12 @@ namespace ws {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kBatch = 4;        // heads a group has in flight at a time
+// Heads a group has in flight at a time.  16384 tokens of 40 + 8 heads: 92 us with
+// two, 77 with four, 72 with eight; backward (two inputs a head, and registers for
+// the gains' gradients), 8192 tokens of 28 + 4: 52 with one, 39.5 with two, 54 with
+// three.
+constexpr int kFwdBatch = 8;
+constexpr int kBwdBatch = 2;
 constexpr int kGainRows = 32;    // rows that k_rope_gain adds side by side
 
 struct RopeArgs {
@@ -141,10 +146,10 @@ WS_DEVINL void fwd_heads(const RopeArgs& a, const Token<D, IL>& tok, const uint1
   if (gain) load_gain(gain, tok.c0, tok.c1, w);
   // a warp's groups have different tokens and parts but take the same steps:
   // one whose heads are through goes along with zeros
-  for (int j0 = 0; j0 < heads; j0 += kBatch * a.parts) {
-    uint4 raw[kBatch][2];
+  for (int j0 = 0; j0 < heads; j0 += kFwdBatch * a.parts) {
+    uint4 raw[kFwdBatch][2];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < kFwdBatch; ++i) {
       const int h = j0 + i * a.parts + first;
       if (h < heads)
         load16(x + h * D, tok.c0, tok.c1, raw[i]);
@@ -152,7 +157,7 @@ WS_DEVINL void fwd_heads(const RopeArgs& a, const Token<D, IL>& tok, const uint1
         raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < kFwdBatch; ++i) {
       if (j0 + i * a.parts >= heads) break;
       const int h = j0 + i * a.parts + first;
       Vec16 v = unpack16(raw[i]);
@@ -190,7 +195,7 @@ template <int D, bool IL, bool GAINS>
 WS_DEVINL void bwd_heads(const RopeArgs& a, const Token<D, IL>& tok, const uint16_t* x,
                          const uint16_t* u, uint16_t* o, const float* gain, int first, int heads,
                          bool live, float (&dg)[16]) {
-  constexpr int B = kBatch / 2;  // two inputs a head
+  constexpr int B = kBwdBatch;
   float w[16];
   if (gain) load_gain(gain, tok.c0, tok.c1, w);
   for (int j0 = 0; j0 < heads; j0 += B * a.parts) {
@@ -306,8 +311,10 @@ ws_status rope_shape(int64_t M, int32_t nh, int32_t nkv, int32_t hd) {
   return hd == 64 || hd == 128 ? WS_OK : WS_ERR_SHAPE;
 }
 
-// Threads that the device holds at once, about: enough groups to fill it.
-int64_t full_groups(int hd) { return (int64_t)device_sm_count() * 1536 / (hd / 16); }
+// Groups of about the threads that the device holds at once (768 an SM at the
+// kernels' registers; with twice as many the backward of 512 tokens took 23 us
+// for 17, that of 8192 tokens 45 for 39).
+int64_t full_groups(int hd) { return (int64_t)device_sm_count() * 768 / (hd / 16); }
 
 // Groups a token's heads are dealt to: as few as fill the device (each then
 // makes the sines and cosines for more heads).
