@@ -603,69 +603,50 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
       ok = poll(b, parity & 1u, abort_flag);
       return ok;
     };
-    // The warp's 32 rows of Q in two e4m3 parts, a row at a time over the lanes
-    // (its tensor products of the segment before are through: they gave the last
-    // S).  Returns this thread's row's factor of S.
+    // This thread's row of Q in two e4m3 parts (the products of the segment
+    // before are through: they gave the last S).  Returns its factor of S.  Two
+    // passes over the row, its maximum and its codes, in a rolled loop: code that
+    // runs once a segment comes from far away, eight instructions in some 300 clocks.
     auto stage = [&](const Seg& g) {
       if (g.dual && s >= g.s1 - g.s0) return 0.0f;  // the slot has no step
-      constexpr int E = D / 32, B = 8;              // elements a lane; rows in flight
-      const int first = (g.dual ? 0 : s * kSlotRows) + q4 * 32;
-      float qs = 0.0f;
+      const int local = g.dual ? r : s * kSlotRows + r, R = g.r0 + local, tok = R / a.G;
+      const bool valid = local < g.rows;
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(g.row0 + (valid ? tok : 0)) * a.sq +
+                                                        (g.head * a.G + (valid ? R - tok * a.G : 0)) * D);
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 x = valid ? src[i] : make_uint4(0, 0, 0, 0);
+        top = __vmaxu2(top, __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu));
+        top = __vmaxu2(top, __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+      }
+      top = max(top & 0xffffu, top >> 16);
+      // the largest at (224, 448]; a row that is not finite gives NaN
+      const int e = max((int)(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u), -126);
+      const float qk = __uint_as_float((uint32_t)(127 - e) << 23);
+      uint4 n0 = valid ? src[0] : make_uint4(0, 0, 0, 0);
 #pragma unroll 1
-      for (int b = 0; b < 32; b += B) {
-        uint32_t x[B][E / 2];
+      for (int i = 0; i < D / 8; ++i) {
+        const uint32_t w[4] = {n0.x, n0.y, n0.z, n0.w};
+        if (i + 1 < D / 8 && valid) n0 = src[i + 1];
+        uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
-        for (int i = 0; i < B; ++i) {
-          const int local = first + b + i, R = g.r0 + local, tok = R / a.G;
-#pragma unroll
-          for (int k = 0; k < E / 2; ++k) x[i][k] = 0u;
-          if (local < g.rows) {
-            const uint16_t* src =
-                a.q + (int64_t)(g.row0 + tok) * a.sq + (g.head * a.G + R - tok * a.G) * D + lane * E;
-            if (E == 4) {
-              const uint2 w = *reinterpret_cast<const uint2*>(src);
-              x[i][0] = w.x;
-              x[i][E / 2 - 1] = w.y;
-            } else {
-              x[i][0] = *reinterpret_cast<const uint32_t*>(src);
-            }
-          }
+        for (int k = 0; k < 4; ++k) {
+          const float f0 = bf16_lo(w[k]) * qk, f1 = bf16_hi(w[k]) * qk;
+          float g0, g1;
+          const uint32_t ph = e4m3x2(f0, f1);
+          e4m3x2_values(ph, g0, g1);
+          hi[k >> 1] |= ph << (16 * (k & 1));
+          lo[k >> 1] |= e4m3x2(f0 - g0, f1 - g1) << (16 * (k & 1));
         }
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
-          uint32_t top = 0;
-#pragma unroll
-          for (int k = 0; k < E / 2; ++k) top = __vmaxu2(top, x[i][k] & 0x7fff7fffu);
-          top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-          // the largest at (224, 448]; a row that is not finite gives NaN
-          const int e = max((int)(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u), -126);
-          const float qk = __uint_as_float((uint32_t)(127 - e) << 23);
-          if (lane == b + i)
-            qs = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : a.sl2 * __uint_as_float((uint32_t)(e + 127) << 23);
-          uint32_t hi = 0, lo = 0;
-#pragma unroll
-          for (int k = 0; k < E / 2; ++k) {
-            const float f0 = bf16_lo(x[i][k]) * qk, f1 = bf16_hi(x[i][k]) * qk;
-            float g0, g1;
-            const uint32_t ph = e4m3x2(f0, f1);
-            e4m3x2_values(ph, g0, g1);
-            hi |= ph << (16 * k);
-            lo |= e4m3x2(f0 - g0, f1 - g1) << (16 * k);
-          }
-          const uint32_t at = swizzled<D>(q4 * 32 + b + i, lane * E / 16) + (uint32_t)(lane * E % 16);
-          if (E == 4) {
-            *reinterpret_cast<uint32_t*>(q_hi + at) = hi;
-            *reinterpret_cast<uint32_t*>(q_hi + L::QP + at) = lo;
-          } else {
-            *reinterpret_cast<uint16_t*>(q_hi + at) = (uint16_t)hi;
-            *reinterpret_cast<uint16_t*>(q_hi + L::QP + at) = (uint16_t)lo;
-          }
-        }
+        const uint32_t at = swizzled<D>(r, i >> 1) + 8 * (i & 1);
+        *reinterpret_cast<uint2*>(q_hi + at) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(q_hi + L::QP + at) = make_uint2(lo[0], lo[1]);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[s]);
-      return qs;
+      return top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : a.sl2 * __uint_as_float((uint32_t)(e + 127) << 23);
     };
     bool have = false;  // a segment whose result is in O
     float qs = 0.0f, m = 0.0f, l = 0.0f, vref = 0.0f;
