@@ -192,9 +192,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
     if (fresh) {
       tl = tiles[cur.tile];
       sq = seqs[cur.seq];
-      rows = min(kTileRows, sq.z * a.G - tl.y);
+      rows = sq.z * a.G;
       kv_end = sq.x + sq.z;
-      first_lim = sq.x + tl.y / a.G + 1;
+      first_lim = sq.x + 1;
       vref = 0.0f;
 #pragma unroll
       for (int nq = 0; nq < NQ; ++nq) {
@@ -204,8 +204,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
 #pragma unroll
         for (int i = 0; i < 2 * KW; ++i) x[i] = make_uint4(0, 0, 0, 0);
         if (r < rows) {
-          const int R = tl.y + r, i = R / a.G;
-          const uint16_t* src = a.q + (int64_t)(sq.y + i) * a.sq + (head * a.G + R - i * a.G) * D + t * (D / 4);
+          const int i = r / a.G;
+          const uint16_t* src = a.q + (int64_t)(sq.y + i) * a.sq + (head * a.G + r - i * a.G) * D + t * (D / 4);
 #pragma unroll
           for (int j = 0; j < 2 * KW; ++j) x[j] = *reinterpret_cast<const uint4*>(src + 8 * j);
         }
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
         for (int e = 0; e < 2; ++e) {
           const int c = 2 * t + e;  // the row of this thread's columns of S^T
           qs[nq][e] = a.sl2 / __shfl_sync(0xffffffffu, qk, 4 * c);
-          lim[nq][e] = 8 * nq + c < rows ? sq.x + (tl.y + 8 * nq + c) / a.G + 1 : 0;
+          lim[nq][e] = 8 * nq + c < rows ? sq.x + (8 * nq + c) / a.G + 1 : 0;
           m[nq][e] = -INFINITY;
           l[nq][e] = 0.0f;
         }
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
         const int r = 8 * nq + 2 * t + e;
         if (r >= rows) continue;
         if (tl.w < 0) {
-          const int R = tl.y + r, i = R / a.G, h = head * a.G + R - i * a.G;
+          const int i = r / a.G, h = head * a.G + r - i * a.G;
           uint16_t* dst = a.o + (int64_t)(sq.y + i) * a.so + h * D;
 #pragma unroll
           for (int ht = 0; ht < HT; ++ht) {
@@ -442,91 +442,103 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
 }
 
 // Cut tiles: row r's pieces o_i with log2-sums l_i are sum 2^(l_i) o_i / sum 2^(l_i).
-// One CTA a row; its warps take every sixteenth piece, eight in flight, joined in
-// their order (two contexts of 130000 tokens leave 450 pieces a row: eight warps
-// with four in flight took 30 us).
-constexpr int kJoinWarps = 16;
+// Few pieces (decode batches): a warp a row, all rows in one CTA.  Many (two
+// contexts of 130000 tokens leave 300 a row): a CTA a row, its warps taking every
+// sixteenth piece.  Eight pieces are in flight a warp, and sums have a fixed
+// order.  What it takes to know where to look is one trip to memory.
+constexpr int kJoinWarps = 16, kJoinFlight = 8, kJoinFew = 16;
+static_assert(kJoinWarps == kTileRows, "a warp a row");
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const __grid_constant__ KvAttnArgs a) {
   constexpr int E = D / 32;  // elements a lane
   __shared__ float so[kJoinWarps][D], sl[kJoinWarps], sm[kJoinWarps];
   pdl_wait();
   pdl_launch_dependents();
-  const KvHeader* hdr = reinterpret_cast<const KvHeader*>(a.plan);
-  if ((int)blockIdx.x >= hdr->n_split) return;
-  const int4 sp = reinterpret_cast<const int4*>(a.plan + a.L.split)[blockIdx.x];
-  const int4 tl = reinterpret_cast<const int4*>(a.plan + a.L.tile)[sp.x];
-  const int4 sq = reinterpret_cast<const int4*>(a.plan + a.L.seq)[tl.x];
-  const int head = (int)blockIdx.y, r = (int)blockIdx.z, R = tl.y + r;
-  if (R >= sq.z * a.G) return;
+  const int n_split = reinterpret_cast<const KvHeader*>(a.plan)->n_split;
+  const int4* entry = reinterpret_cast<const int4*>(a.plan + a.L.split) + 2 * blockIdx.x;
+  const int4 sp = entry[0], sq = entry[1];
   const int warp = (int)warp_id(), lane = (int)lane_id();
+  const bool few = sp.y <= kJoinFew;
+  const int head = (int)blockIdx.y, r = few ? warp : (int)blockIdx.z, rows = sq.z * a.G;
+  if ((int)blockIdx.x >= n_split || (few ? blockIdx.z != 0 : r >= rows)) return;
+  const int first = few ? 0 : warp, step = few ? 1 : kJoinWarps;
   const int64_t stride = (int64_t)a.nkv * kTileRows;
-  const int64_t base = (int64_t)sp.y * stride + (int64_t)head * kTileRows + r;
-  // a lane's share of the pieces' log2-sums, then the warp's largest; NaN is none
-  float m = -INFINITY;
-  for (int i = warp + kJoinWarps * lane; i < sp.z; i += kJoinWarps * 32) m = fmaxf(m, a.part_l[base + i * stride]);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float acc[E], l = 0.0f;
+  const int64_t base = (int64_t)sp.x * stride + (int64_t)head * kTileRows + r;
+  float m = -INFINITY, l = 0.0f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-  const float ref = m == -INFINITY ? 0.0f : m;
-  for (int i0 = warp; i0 < sp.z; i0 += 8 * kJoinWarps) {
-    float w[8], x[8][E];
+  if (r < rows) {
+    for (int i0 = first; i0 < sp.y; i0 += kJoinFlight * step) {
+      float w[kJoinFlight], x[kJoinFlight][E];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int i = i0 + k * kJoinWarps;
-      w[k] = -INFINITY;
+      for (int k = 0; k < kJoinFlight; ++k) {
+        const int i = i0 + k * step;
+        w[k] = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[k][e] = 0.0f;
-      if (i < sp.z) {
-        w[k] = a.part_l[base + i * stride];
-        const float* src = a.part_o + (base + i * stride) * D + lane * E;
-        if (E == 4) {
-          const float4 f = *reinterpret_cast<const float4*>(src);
-          x[k][0] = f.x;
-          x[k][1] = f.y;
-          x[k][E - 2] = f.z;
-          x[k][E - 1] = f.w;
-        } else {
-          const float2 f = *reinterpret_cast<const float2*>(src);
-          x[k][0] = f.x;
-          x[k][1] = f.y;
+        for (int e = 0; e < E; ++e) x[k][e] = 0.0f;
+        if (i < sp.y) {
+          w[k] = a.part_l[base + i * stride];
+          const float* src = a.part_o + (base + i * stride) * D + lane * E;
+          if (E == 4) {
+            const float4 f = *reinterpret_cast<const float4*>(src);
+            x[k][0] = f.x;
+            x[k][1] = f.y;
+            x[k][E - 2] = f.z;
+            x[k][E - 1] = f.w;
+          } else {
+            const float2 f = *reinterpret_cast<const float2*>(src);
+            x[k][0] = f.x;
+            x[k][1] = f.y;
+          }
         }
       }
+      float nm = m;
+#pragma unroll
+      for (int k = 0; k < kJoinFlight; ++k) nm = fmaxf(nm, w[k]);
+      const float ref = nm == -INFINITY ? 0.0f : nm, c = m == -INFINITY ? 0.0f : ex2(m - ref);
+      m = nm;
+      l *= c;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= c;
+#pragma unroll
+      for (int k = 0; k < kJoinFlight; ++k) {
+        const float wt = ex2(w[k] - ref);
+        l += wt;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += wt * x[k][e];
+      }
     }
+  }
+  if (!few) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float wt = ex2(w[k] - ref);
-      l += wt;
+    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
+    if (lane == 0) {
+      sl[warp] = l;
+      sm[warp] = m;
+    }
+    __syncthreads();
+    if (warp) return;
+    m = -INFINITY;
+    for (int i = 0; i < kJoinWarps; ++i) m = fmaxf(m, sm[i]);
+    const float ref = m == -INFINITY ? 0.0f : m;
+    l = 0.0f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += wt * x[k][e];
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    for (int i = 0; i < kJoinWarps; ++i) {
+      const float c = sm[i] == -INFINITY ? 0.0f : ex2(sm[i] - ref);
+      l += sl[i] * c;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += so[i][lane * E + e] * c;
     }
   }
+  if (r >= rows) return;
+  const bool none = l == 0.0f;
+  const int i = r / a.G, h = head * a.G + r - i * a.G;
+  uint16_t* dst = a.o + (int64_t)(sq.y + i) * a.so + h * D + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
-  if (lane == 0) {
-    sl[warp] = l;
-    sm[warp] = m;
-  }
-  __syncthreads();
-  if ((int)threadIdx.x >= D) return;
-  float top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, sm[i]);
-  const float rt = top == -INFINITY ? 0.0f : top;
-  float sum = 0.0f, y = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kJoinWarps; ++i) {
-    const float c = sm[i] == -INFINITY ? 0.0f : ex2(sm[i] - rt);
-    sum += sl[i] * c;
-    y += so[i][threadIdx.x] * c;
-  }
-  const bool none = sum == 0.0f;
-  const int i = R / a.G, h = head * a.G + R - i * a.G;
-  a.o[(int64_t)(sq.y + i) * a.so + h * D + threadIdx.x] = f32_to_bf16_bits(none ? 0.0f : y / sum);
-  if (a.lse && threadIdx.x == 0)
-    a.lse[(int64_t)h * a.T + sq.y + i] = none ? -INFINITY : (top + log2f(sum)) * kLn2;
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(dst + e) = none ? 0u : pack_bf16x2(__fdiv_rn(acc[e], l), __fdiv_rn(acc[e + 1], l));
+  if (a.lse && lane == 0) a.lse[(int64_t)h * a.T + sq.y + i] = none ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 struct KvWork {

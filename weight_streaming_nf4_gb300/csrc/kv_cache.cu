@@ -157,7 +157,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const KvPlanArgs a) {
     if (u1 > u0) {
       tile[i].w = j;
       // slot = unit + index among the cut tiles: no two pieces share one
-      split[j] = make_int4(i, u0 + j, u1 - u0 + 1, 0);
+      split[2 * j] = make_int4(u0 + j, u1 - u0 + 1, 0, 0);
+      split[2 * j + 1] = seq[tile[i].x];
     }
     n_split += total;
   }
@@ -205,7 +206,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const KvPlanArgs a) {
       if (u <= Uc) c_unit[u] = make_int4(t, h, cuts ? (first ? j : j - 1) : -1, 0);
       if (first) {
         const int64_t end = (int64_t)h * Wc + c_tile[t + 1].z;
-        c_split[j] = make_int4(t, u - 1 + j, unit_of(end - 1, all, Uc) - (u - 1) + 1, h);
+        c_split[2 * j] = make_int4(u - 1 + j, unit_of(end - 1, all, Uc) - (u - 1) + 1, c_tile[t].y, h);
+        c_split[2 * j + 1] = seq[c_tile[t].x];
       }
       n_cut += total;
     }

@@ -867,46 +867,73 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
   if (warp == 1) tmem_dealloc(tmem, TM_COLS);
 }
 
-// Cut (head, tile) pairs: a row's pieces joined in the order of the shares, one
-// warp a row.
-constexpr int kChJoinRows = 8;
+// Cut (head, tile) pairs: a row's pieces joined in the order of the shares, four
+// rows a warp at a time.
+constexpr int kChJoinWarps = 8, kChJoinRows = 4;
 template <int D>
-__global__ void __launch_bounds__(kChJoinRows * 32) k_kv_chunk_join(const __grid_constant__ ChunkArgs c) {
+__global__ void __launch_bounds__(kChJoinWarps * 32) k_kv_chunk_join(const __grid_constant__ ChunkArgs c) {
   constexpr int E = D / 32;
   pdl_wait();
   pdl_launch_dependents();
   const KvAttnArgs& a = c.a;
-  const KvHeader* hdr = reinterpret_cast<const KvHeader*>(a.plan);
-  if ((int)blockIdx.x >= hdr->c_split) return;
-  const int4 sp = reinterpret_cast<const int4*>(a.plan + a.L.c_split)[blockIdx.x];
-  const int4 tl = reinterpret_cast<const int4*>(a.plan + a.L.c_tile)[sp.x];
-  const int4 sq = reinterpret_cast<const int4*>(a.plan + a.L.seq)[tl.x];
-  const int lane = (int)lane_id(), local = (int)blockIdx.y * kChJoinRows + (int)warp_id(), R = tl.y + local;
-  if (R >= sq.z * a.G) return;
-  const int64_t base = (int64_t)sp.y * kChunkRows + local;
-  float m = -INFINITY;
-  for (int i = 0; i < sp.z; ++i) m = fmaxf(m, c.part_l[base + (int64_t)i * kChunkRows]);
-  const float ref = m == -INFINITY ? 0.0f : m;
-  float acc[E], sum = 0.0f;
+  const int n_split = reinterpret_cast<const KvHeader*>(a.plan)->c_split;
+  const int4* entry = reinterpret_cast<const int4*>(a.plan + a.L.c_split) + 2 * blockIdx.x;
+  const int4 sp = entry[0], sq = entry[1];
+  const int lane = (int)lane_id(), rows = min(kChunkRows, sq.z * a.G - sp.z);
+  const int first = ((int)blockIdx.y * kChJoinWarps + (int)warp_id()) * kChJoinRows;
+  if ((int)blockIdx.x >= n_split || first >= rows) return;
+  const int64_t base = (int64_t)sp.x * kChunkRows;
+  float m[kChJoinRows], sum[kChJoinRows], acc[kChJoinRows][E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i < sp.z; ++i) {
-    const int64_t at = base + (int64_t)i * kChunkRows;
-    const float w = ex2(c.part_l[at] - ref);
-    const float* src = c.part_o + at * D + lane * E;
-    sum += w;
+  for (int r = 0; r < kChJoinRows; ++r) {
+    m[r] = -INFINITY;
+    sum[r] = 0.0f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += w * src[e];
+    for (int e = 0; e < E; ++e) acc[r][e] = 0.0f;
   }
-  const bool none = sum == 0.0f;
-  const int tok = R / a.G, h = sp.w * a.G + R - tok * a.G;
-  uint16_t* dst = a.o + (int64_t)(sq.y + tok) * a.so + h * D + lane * E;
+#pragma unroll 2
+  for (int i = 0; i < sp.y; ++i) {
+    float w[kChJoinRows], x[kChJoinRows][E];
 #pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<uint32_t*>(dst + e) =
-        none ? 0u : pack_bf16x2(__fdiv_rn(acc[e], sum), __fdiv_rn(acc[e + 1], sum));
-  if (a.lse && lane == 0) a.lse[(int64_t)h * a.T + sq.y + tok] = none ? -INFINITY : (m + log2f(sum)) * kLn2;
+    for (int r = 0; r < kChJoinRows; ++r) {
+      const int64_t at = base + (int64_t)i * kChunkRows + min(first + r, rows - 1);
+      w[r] = c.part_l[at];
+      const float* src = c.part_o + at * D + lane * E;
+      if (E == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(src);
+        x[r][0] = f.x;
+        x[r][1] = f.y;
+        x[r][E - 2] = f.z;
+        x[r][E - 1] = f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(src);
+        x[r][0] = f.x;
+        x[r][1] = f.y;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kChJoinRows; ++r) {
+      const float nm = fmaxf(m[r], w[r]), ref = nm == -INFINITY ? 0.0f : nm;
+      const float old = m[r] == -INFINITY ? 0.0f : ex2(m[r] - ref), now = ex2(w[r] - ref);
+      m[r] = nm;
+      sum[r] = sum[r] * old + now;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[r][e] = acc[r][e] * old + now * x[r][e];
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kChJoinRows; ++r) {
+    if (first + r >= rows) break;
+    const bool none = sum[r] == 0.0f;
+    const int R = sp.z + first + r, tok = R / a.G, h = sp.w * a.G + R - tok * a.G;
+    uint16_t* dst = a.o + (int64_t)(sq.y + tok) * a.so + h * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+      *reinterpret_cast<uint32_t*>(dst + e) =
+          none ? 0u : pack_bf16x2(__fdiv_rn(acc[r][e], sum[r]), __fdiv_rn(acc[r][e + 1], sum[r]));
+    if (a.lse && lane == 0)
+      a.lse[(int64_t)h * a.T + sq.y + tok] = none ? -INFINITY : (m[r] + log2f(sum[r])) * kLn2;
+  }
 }
 
 template <int D>
@@ -918,8 +945,8 @@ cudaError_t launch_chunk(const ChunkArgs& c, cudaStream_t st) {
                                    ChSmem<D>::BYTES, st, c);
   if (f != cudaSuccess) return f;
   note_launch();
-  return launch_pdl(k_kv_chunk_join<D>, dim3((unsigned)c.a.L.c_max_units, kChunkRows / kChJoinRows),
-                    dim3(kChJoinRows * 32), 0, st, c);
+  return launch_pdl(k_kv_chunk_join<D>, dim3((unsigned)c.a.L.c_max_units, kChunkRows / (kChJoinWarps * kChJoinRows)),
+                    dim3(kChJoinWarps * 32), 0, st, c);
 }
 
 // Partial results lie in slots unit + index of the cut pair: below 2 units.

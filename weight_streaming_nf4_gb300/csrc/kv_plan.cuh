@@ -35,11 +35,11 @@ struct KvHeader {
 // int4 arrays:
 //   seq     {tokens before the call, first row of q, new tokens, 0}
 //   append  {first row, page (-1: none), first place in it, rows}
-//   tile    {sequence, first row, pages of the tiles before it, index among the cut ones or -1},
-//           one more at the end with the pages of all
-//   split   {tile, first slot, pieces, 0}
+//   tile    {sequence, 0, pages of the tiles before it, index among the cut ones or -1}, a sequence
+//           each, one more at the end with the pages of all
+//   split   two each: {first slot, pieces, first row, 0}, the sequence's entry
 //   c_tile  {sequence, first row, steps of the tiles before it, 0}, one more at the end
-//   c_split {tile, first slot, pieces, head}
+//   c_split two each: {first slot, pieces, first row, head}, the sequence's entry
 // and
 //   pre     prefix sums over the sequences {pages to append to, tiles, chunk tiles, 0}
 //   unit    first tile of each unit (int)
@@ -81,10 +81,10 @@ inline KvLayout kv_layout(const KvShape& s) {
   L.pre = take((int64_t)s.n_seq * 16);
   L.append = take(L.max_append * 16);
   L.tile = take((L.max_tiles + 1) * 16);
-  L.split = take(L.max_units * 16);
+  L.split = take(L.max_units * 32);
   L.unit = take(L.max_units * 4);
   L.c_tile = take((L.c_max_tiles + 1) * 16);
-  L.c_split = take(L.c_max_units * 16);
+  L.c_split = take(L.c_max_units * 32);
   L.c_unit = take((L.c_max_units + 1) * 16);
   L.bytes = o;
   return L;
