@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
   int lim[NQ][2];                  // tokens each row sees
   float vref = 0.0f;
   int rows = 0, kv_end = 0, first_lim = 0;
+  bool wide = false;               // more than eight rows: the second half of the operands is in use
   int4 tl = make_int4(0, 0, 0, 0), sq = tl;
 
   for (; cur.pend != 0; cur = nxt, nxt = nx2) {
@@ -193,6 +194,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
       tl = tiles[cur.tile];
       sq = seqs[cur.seq];
       rows = sq.z * a.G;
+      wide = rows > 8;
       kv_end = sq.x + sq.z;
       first_lim = sq.x + 1;
       vref = 0.0f;
@@ -267,7 +269,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
           decode4(i == 0 ? w0.x : i == 1 ? w0.y : i == 2 ? w0.z : w0.w, a0, a2);
           decode4(i == 0 ? w1.x : i == 1 ? w1.y : i == 2 ? w1.z : w1.w, a1, a3);
 #pragma unroll
-          for (int nq = 0; nq < NQ; ++nq) mma_f16(s[nq][mt], a0, a1, a2, a3, bq[nq][ks][0], bq[nq][ks][1]);
+          for (int nq = 0; nq < NQ; ++nq)
+            if (nq == 0 || wide) mma_f16(s[nq][mt], a0, a1, a2, a3, bq[nq][ks][0], bq[nq][ks][1]);
         }
       }
       __syncwarp();
@@ -292,6 +295,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
       uint32_t bp[NQ][4][2];
 #pragma unroll
       for (int nq = 0; nq < NQ; ++nq) {
+        if (nq > 0 && !wide) break;
         float nm[2], cf[2];
         if (tail) {
 #pragma unroll
@@ -388,7 +392,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
           decode4(x0[i], a0, a2);
           decode4(x1[i], a1, a3);
 #pragma unroll
-          for (int nq = 0; nq < NQ; ++nq) mma_f16(o[nq][ht], a0, a1, a2, a3, bp[nq][i][0], bp[nq][i][1]);
+          for (int nq = 0; nq < NQ; ++nq)
+            if (nq == 0 || wide) mma_f16(o[nq][ht], a0, a1, a2, a3, bp[nq][i][0], bp[nq][i][1]);
         }
       }
       __syncwarp();
