@@ -745,7 +745,8 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
       m = -INFINITY;
       l = vref = 0.0f;
       const int J1 = sg.s1 - sg.s0, mine = sg.dual ? r : s * kSlotRows + r;
-      const int lim = mine < sg.rows ? sg.past + (sg.r0 + mine) / a.G + 1 : 0;  // tokens that the row sees
+      // tokens that the row sees; a row that is none (zero queries, nothing is stored) goes along with the last
+      const int lim = mine < sg.rows ? sg.past + (sg.r0 + mine) / a.G + 1 : sg.past + sg.n;
       bool begun = false;  // something is in O
       for (int j = 0; j < J1; ++j) {
         const int n = n0 + j;
