@@ -477,3 +477,65 @@ def test_offsets_past_32_bits(ops):
         ops.kv_append(c, plan, k, v)
         outs.append(ops.attention_kv(q, c, plan)[0])
     assert torch.equal(*outs)
+
+
+WIDE = [(1, 1024, 128, [70], [1]), (1, 1024, 64, [5, 0], [2, 1]), (256, 1, 64, [3, 64], [1, 2]), (256, 4, 64, [90], [20]),
+        (2, 17, 128, [200, 64], [1, 1]), (4, 8, 128, [640, 127, 0], [2, 3, 2])]
+
+
+@pytest.mark.parametrize("case", WIDE, ids=[str(i) for i in range(len(WIDE))])
+def test_many_heads_and_rows_about_a_tile_s(ops, case):
+    test_attention(ops, case)
+
+
+def test_as_many_sequences_as_a_plan_takes(ops):
+    nkv, G, hd, n = 1, 2, 64, 4096
+    past = [(0, 1, 63, 64, 130)[i * 7 % 5] for i in range(n)]
+    new = [0 if i % 11 == 3 else 1 for i in range(n)]
+    table, pages = pages_for(past, new)
+    cache = empty_cache(ops, pages, nkv, hd)
+    for t in (cache.k, cache.v):  # what the cache holds before: any finite codes
+        t.view(torch.uint8).copy_(torch.randint(0, 0x7f, t.shape, dtype=torch.uint8, generator=torch.Generator().manual_seed(1)))
+    cache.scale.fill_(2.0 ** -7)
+    model = Model(cache)
+    T = sum(new)
+    k, v, q = rows(1, T, nkv, hd), rows(2, T, nkv, hd), rows(3, T, nkv * G, hd)
+    plan = ops.kv_plan(ints(past), ints(starts(new)), ints(table), T, 1, G * nkv, nkv, hd)
+    ops.kv_append(cache, plan, k, v)
+    model.append(past, new, table, k, v)
+    model.check(cache)
+    check_attention(ops, cache, model, plan, past, new, table, q)
+
+
+def test_two_calls_at_once_and_two_graphs_in_turn(ops):
+    """One plan and one cache, read by calls on two streams with a workspace each, and by two captured calls that share
+    one and are replayed in turn: the bits of single calls."""
+    nkv, G, hd, past, new = 4, 5, 128, [9000, 300, 77], [1, 90, 2]
+    table, n = pages_for(past, new)
+    cache = empty_cache(ops, n, nkv, hd)
+    model = Model(cache)
+    step(ops, cache, model, [0] * 3, past, table, G=G)
+    plan = step(ops, cache, model, past, new, table, G=G, seed=9)
+    qs = [rows(i, plan.T, nkv * G, hd) for i in (4, 5)]
+    want = [check_attention(ops, cache, model, plan, past, new, table, q)[0] for q in qs]
+    size = ops.attention_kv_workspace_size(plan)
+    spaces = [torch.empty(size, dtype=torch.uint8, device=DEV) for _ in qs]
+    outs = [torch.zeros_like(w) for w in want]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for q, ws, o, s in zip(qs, spaces, outs, streams):
+            ops.attention_kv(q, cache, plan, o=o, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    assert ops.device_error() == 0 and all(torch.equal(a, b) for a, b in zip(outs, want))
+    graphs = []
+    for q, o in zip(qs, outs):
+        o.zero_()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            ops.attention_kv(q, cache, plan, o=o, workspace=spaces[0])
+    for _ in range(4):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert ops.device_error() == 0 and all(torch.equal(a, b) for a, b in zip(outs, want))
