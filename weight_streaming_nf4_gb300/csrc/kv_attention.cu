@@ -546,15 +546,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const __grid_consta
   if (a.lse && lane == 0) a.lse[(int64_t)h * a.T + sq.y + i] = none ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
+// Where the partial results lie in the workspace: the decode kernel's sums behind
+// its rows, the chunk kernel's behind both.
 struct KvWork {
-  size_t part_l, bytes;
+  size_t part_l, chunk, bytes;
 };
 KvWork kv_work(const KvShape& s, const KvLayout& L) {
   // a cut tile's pieces lie in slots unit + index of the tile: below 2 max_units
-  const size_t rows = (size_t)(2 * L.max_units) * s.nkv * kTileRows;
+  const size_t rows = L.max_tiles > 0 ? (size_t)(2 * L.max_units) * s.nkv * kTileRows : 0;
   KvWork w;
   w.part_l = rows * s.hd * 4;
-  w.bytes = (w.part_l + rows * 4 + 15) / 16 * 16;
+  w.chunk = w.part_l + rows * 4;  // a multiple of 64
+  w.bytes = w.chunk + kv_chunk_bytes(s) + 16;  // the chunk kernel stores 32 bytes at a time, the caller's is at 16
   return w;
 }
 
@@ -581,7 +584,7 @@ ws_status ws_attention_kv_workspace_size(const ws_kv_plan* plan, size_t* bytes) 
   const ws_status st = kv_shape(plan, &s);
   if (st != WS_OK) return st;
   if (!bytes) return WS_ERR_INVALID;
-  *bytes = kv_work(s, kv_layout(s)).bytes + kv_chunk_bytes(s);
+  *bytes = kv_work(s, kv_layout(s)).bytes;
   return WS_OK;
 }
 
@@ -600,7 +603,7 @@ ws_status ws_attention_kv(const ws_kv_cache* cache, const ws_kv_plan* plan, cons
   KvAttnArgs a;
   a.L = kv_layout(s);
   const KvWork w = kv_work(s, a.L);
-  if (ws_bytes < w.bytes + kv_chunk_bytes(s)) return WS_ERR_OOM;
+  if (ws_bytes < w.bytes) return WS_ERR_OOM;
   a.k = cache->k;
   a.v = cache->v;
   a.scale = cache->scale;
@@ -609,8 +612,9 @@ ws_status ws_attention_kv(const ws_kv_cache* cache, const ws_kv_plan* plan, cons
   a.q = q;
   a.o = o;
   a.lse = lse;
-  a.part_o = static_cast<float*>(workspace);
-  a.part_l = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.part_l);
+  uint8_t* work = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 31) & ~uintptr_t(31));
+  a.part_o = reinterpret_cast<float*>(work);
+  a.part_l = reinterpret_cast<float*>(work + w.part_l);
   a.n_pages = cache->n_pages;
   a.sq = q_stride;
   a.so = o_stride;
@@ -621,7 +625,7 @@ ws_status ws_attention_kv(const ws_kv_cache* cache, const ws_kv_plan* plan, cons
   a.sl2 = scale * kLog2e;
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = cudaSuccess;
-  if (a.L.c_max_tiles > 0) e = run_kv_chunk(a, s, static_cast<uint8_t*>(workspace) + w.bytes, st);
+  if (a.L.c_max_tiles > 0) e = run_kv_chunk(a, s, work + w.chunk, st);
   if (e != cudaSuccess) return WS_ERR_CUDA;
   if (a.L.max_tiles > 0) {
     const bool few = std::min<int64_t>((int64_t)s.max_new * a.G, kTileRows) <= 8;  // rows of a tile
