@@ -449,12 +449,15 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
 // Cut tiles: row r's pieces o_i with log2-sums l_i are sum 2^(l_i) o_i / sum 2^(l_i).
 // Few pieces (decode batches): a warp a row, all rows in one CTA.  Many (two
 // contexts of 130000 tokens leave 300 a row): a CTA a row, its warps taking every
-// sixteenth piece.  Eight pieces are in flight a warp, and sums have a fixed
-// order.  What it takes to know where to look is one trip to memory.
-constexpr int kJoinWarps = 16, kJoinFlight = 8, kJoinFew = 16;
+// sixteenth piece.  Sums have a fixed order.  Bound by latency: what it takes to
+// know where to look is one trip to memory, and CTAs that find nothing there leave
+// the sooner the more fit on an SM.  Four pieces in flight a warp and two CTAs an
+// SM: 48 contexts of 16000 tokens, 40 + 8 heads, take 162 us in all, two contexts
+// of 130000 54; eight and one CTA 166 and 53.
+constexpr int kJoinWarps = 16, kJoinFlight = 4, kJoinFew = 16;
 static_assert(kJoinWarps == kTileRows, "a warp a row");
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const __grid_constant__ KvAttnArgs a) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 2) k_kv_join(const __grid_constant__ KvAttnArgs a) {
   constexpr int E = D / 32;  // elements a lane
   __shared__ float so[kJoinWarps][D], sl[kJoinWarps], sm[kJoinWarps];
   pdl_wait();
