@@ -237,22 +237,17 @@ WS_DEVINL f32x2 add2(f32x2 a, f32x2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// A row's 64 scores of a page as 2^(v cf - shift), fp16 pairs; returns their sum.
-WS_DEVINL float weigh_plain(const float (&v)[64], float cf, float shift, uint32_t (&p)[32]) {
-  const f32x2 c2 = pair(cf, cf), r2 = pair(-shift, -shift);
-  f32x2 sum[2] = {0ull, 0ull};  // two zeros each
+// 32 of a row's scores as 2^(x cf - shift), fp16 pairs; their sums are added to sum.
+WS_DEVINL void weigh_plain(const uint32_t (&x)[32], f32x2 c2, f32x2 r2, f32x2 (&sum)[2], uint32_t* p) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
+  for (int i = 0; i < 16; ++i) {
     float y0, y1;
-    unpair(fma2(pair(v[2 * i], v[2 * i + 1]), c2, r2), y0, y1);
+    unpair(fma2(pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2, r2), y0, y1);
     y0 = ex2(y0);
     y1 = ex2(y1);
     sum[i & 1] = add2(sum[i & 1], pair(y0, y1));
     p[i] = pack_f16x2(y0, y1);
   }
-  float a, b;
-  unpair(add2(sum[0], sum[1]), a, b);
-  return a + b;
 }
 template <int D>
 __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constant__ ChunkArgs c) {
@@ -369,26 +364,27 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
         // the window's pages: lane i has pages 2 i, 2 i + 1 = step n + i
         ok = poll(&i_empty[w & 1], ((uint32_t)(w >> 1) & 1u) ^ 1u, abort_flag);
         if (!ok) break;
-        PageInfo mine[2];
-        int head = 0;
-        for (int i = 0; i < kInfo / 2; ++i) {
-          if (more && as_step == as.s1) {
+        // lane i has step n + i; a segment or two make up a window, and each page costs one trip for all lanes
+        int seq = 0, head = 0, p = 0, pend = 0;  // pages from pend on are seen by no row of the tile
+        for (int filled = 0; filled < kInfo / 2 && more;) {
+          const int cnt = min(kInfo / 2 - filled, as.s1 - as_step);
+          if (lane >= filled && lane < filled + cnt) {
+            seq = as.seq;
+            head = as.head;
+            p = 2 * (as_step + lane - filled);
+            pend = (as.past + (as.r0 + as.rows - 1) / a.G) / kPage + 1;
+          }
+          filled += cnt;
+          as_step += cnt;
+          if (as_step == as.s1) {
             more = ahead.next(as);
             as_step = as.s0;
           }
-          if (i == lane) {
-            head = as.head;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int p = 2 * as_step + h;
-              mine[h].page = more && p < a.max_pages ? a.table[(int64_t)as.seq * a.max_pages + p] : -1;
-              // pages that no row of the tile sees are not there
-              const int last = (min(as.n * a.G, as.r0 + kChunkRows) - 1) / a.G;
-              if (!more || p * kPage > as.past + last) mine[h].page = -1;
-            }
-          }
-          if (more) ++as_step;
         }
+        PageInfo mine[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          mine[h].page = p + h < pend ? a.table[(int64_t)seq * a.max_pages + p + h] : -1;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           mine[h].ks = mine[h].vs = 0.0f;
@@ -772,19 +768,19 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
           bool grown = false, rest = true;
           if (warp_all(plain)) {
             uint32_t p[32];
-            float v[64];
-            {
-              uint32_t x0[32], x1[32];
-              tmem_ld_32x32b_x32(t_v, x0);
-              tmem_ld_32x32b_x32(t_v + 32, x1);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                v[i] = __uint_as_float(x0[i]);
-                v[32 + i] = __uint_as_float(x1[i]);
-              }
-            }
-            const float sum = weigh_plain(v, cf, m - (float)e, p) * __uint_as_float((uint32_t)(127 - e) << 23);
+            uint32_t x0[32], x1[32];
+            const float shift = m - (float)e;
+            const f32x2 c2 = pair(cf, cf), r2 = pair(-shift, -shift);
+            f32x2 two[2] = {0ull, 0ull};  // two zeros each
+            tmem_ld_32x32b_x32(t_v, x0);
+            tmem_ld_wait();
+            tmem_ld_32x32b_x32(t_v + 32, x1);
+            weigh_plain(x0, c2, r2, two, p);
+            tmem_ld_wait();
+            weigh_plain(x1, c2, r2, two, p + 16);
+            float sum, other;
+            unpair(add2(two[0], two[1]), sum, other);
+            sum = (sum + other) * __uint_as_float((uint32_t)(127 - e) << 23);
             grown = !(sum <= (float)(1 << kLag));
             rest = !warp_all(!grown);
             if (!rest) {
