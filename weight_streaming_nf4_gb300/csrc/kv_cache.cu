@@ -168,45 +168,51 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const KvPlanArgs a) {
       unit[u] = last_at_most(n_tiles, (int)unit_start(u, W, U), [&](int j) { return tile[j].z; });
 
   // ---- chunk: 256-row tiles, shares of all heads' steps
-  int Wc = 0;
+  // A tile's cost is kChunkTileCost and its steps, or half of those where both slots share them (tiles of up to
+  // half the rows).  A share that would begin in the first part begins with the tile.
+  auto halved = [&](int rows) { return rows <= kChunkRows / 2; };
+  int Wc = 0, cost = 0;
   for (int base = 0; base < c_tiles; base += kPlanThreads) {
     const int i = base + tid;
-    int steps = 0, s = 0, r0 = 0;
+    int steps = 0, s = 0, r0 = 0, mine = 0;
     if (i < c_tiles) {
       s = last_at_most(n, i, [&](int j) { return pre[j].z; });
       r0 = (i - pre[s].z) * kChunkRows;
-      const int last = min(seq[s].z * G, r0 + kChunkRows) - 1;
-      steps = (seq[s].x + last / G) / (2 * kPage) + 1;
+      const int rows = min(seq[s].z * G - r0, kChunkRows);
+      steps = (seq[s].x + (r0 + rows - 1) / G) / (2 * kPage) + 1;
+      mine = kChunkTileCost + (halved(rows) ? (steps + 1) / 2 : steps);
     }
-    int total;
-    const int at = block_scan(steps, &total);
-    if (i < c_tiles) c_tile[i] = make_int4(s, r0, Wc + at, 0);
+    int total, all;
+    const int at = block_scan(steps, &total), before = block_scan(mine, &all);
+    if (i < c_tiles) c_tile[i] = make_int4(s, r0, Wc + at, cost + before);
     Wc += total;
+    cost += all;
   }
-  if (tid == 0) c_tile[c_tiles] = make_int4(0, 0, Wc, 0);
+  if (tid == 0) c_tile[c_tiles] = make_int4(0, 0, Wc, cost);
   __syncthreads();
   int Uc = 0, n_cut = 0;
   if (c_tiles > 0) {
-    const int64_t all = (int64_t)Wc * a.s.nkv;
+    const int64_t all = (int64_t)cost * a.s.nkv;
     Uc = (int)max((int64_t)1, min(a.L.c_max_units, all / kChunkMinSteps));
     // a unit's start cuts a (head, tile) pair, or lies between two; units that start in one pair come together
     for (int base = 0; base <= Uc; base += kPlanThreads) {
       const int u = base + tid;
-      int t = 0, h = a.s.nkv;
-      bool cuts = false, first = false;
+      int t = 0, h = a.s.nkv, step = 0;
+      bool first = false;
       if (u < Uc) {
         const int64_t x = unit_start(u, all, Uc);
-        h = (int)(x / Wc);
-        const int y = (int)(x % Wc);
-        t = last_at_most(c_tiles, y, [&](int j) { return c_tile[j].z; });
-        cuts = y != c_tile[t].z;
-        first = cuts && unit_of((int64_t)h * Wc + c_tile[t].z, all, Uc) == u - 1;
+        h = (int)(x / cost);
+        const int y = (int)(x % cost);
+        t = last_at_most(c_tiles, y, [&](int j) { return c_tile[j].w; });
+        step = max(y - c_tile[t].w - kChunkTileCost, 0);
+        if (halved(seq[c_tile[t].x].z * G - c_tile[t].y)) step *= 2;
+        first = step > 0 && unit_start(u - 1, all, Uc) <= (int64_t)h * cost + c_tile[t].w + kChunkTileCost;
       }
       int total;
       const int j = n_cut + block_scan(first, &total);
-      if (u <= Uc) c_unit[u] = make_int4(t, h, cuts ? (first ? j : j - 1) : -1, 0);
+      if (u <= Uc) c_unit[u] = make_int4(t, h, step > 0 ? (first ? j : j - 1) : -1, step);
       if (first) {
-        const int64_t end = (int64_t)h * Wc + c_tile[t + 1].z;
+        const int64_t end = (int64_t)h * cost + c_tile[t + 1].w;
         c_split[2 * j] = make_int4(u - 1 + j, unit_of(end - 1, all, Uc) - (u - 1) + 1, c_tile[t].y, h);
         c_split[2 * j + 1] = seq[c_tile[t].x];
       }
@@ -404,9 +410,9 @@ ws_status kv_shape(const ws_kv_plan* p, KvShape* s) {
     return WS_ERR_SHAPE;
   if (p->head_dim != 64 && p->head_dim != 128) return WS_ERR_SHAPE;
   *s = KvShape{p->T, p->n_seq, p->max_pages, p->max_new, p->n_heads, p->n_kv_heads, p->head_dim};
-  // the chunk kernel counts the steps of one head, and those of a share of all heads, in 32 bits
-  const int64_t steps = kv_chunk_tiles(*s) * (s->max_pages / 2 + 1);
-  if (steps > 0x7fffffff || steps * s->nkv > (int64_t)1 << 36) return WS_ERR_SHAPE;
+  // the chunk kernel's shares count one head's cost in 32 bits, all heads' in 64
+  const int64_t cost = kv_chunk_tiles(*s) * (s->max_pages / 2 + 1 + kChunkTileCost);
+  if (cost > 0x7fffffff || cost * s->nkv > (int64_t)1 << 36) return WS_ERR_SHAPE;
   return WS_OK;
 }
 ws_status kv_check(const ws_kv_cache* c, const ws_kv_plan* p, KvShape* s) {

@@ -107,11 +107,11 @@ struct Share {
     const int U = h->c_units;
     begin = end = at = 0;
     if (u >= U) return;
-    begin = unit_start(u, (int64_t)W * nkv, U);
-    end = unit_start(u + 1, (int64_t)W * nkv, U);
-    at = begin;
-    tile = units[u].x;
-    head = units[u].y;
+    const int4 b = units[u], e = units[u + 1];
+    tile = b.x;
+    head = b.y;
+    begin = at = (int64_t)head * W + tiles[tile].z + b.w;
+    end = (int64_t)e.y * W + tiles[e.x].z + e.w;
   }
   WS_DEVINL bool next(Seg& s) {
     if (at >= end) return false;

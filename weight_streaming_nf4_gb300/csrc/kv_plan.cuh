@@ -15,7 +15,11 @@ constexpr int kTileRows = 16;    // rows of a tile of the decode kernel, which h
 // way each (D = 128), twelve with 12 KB (D = 64).
 constexpr int decode_warps(int hd) { return hd == 128 ? 8 : 12; }
 constexpr int kChunkRows = 256;  // rows of a tile of the chunk kernel, which has the others
-constexpr int kChunkMinSteps = 4;  // steps (two pages) of a share of the chunk kernel's work, at least
+constexpr int kChunkMinSteps = 8;  // steps (two pages) of a share of the chunk kernel's work, at least
+// What beginning a tile costs, in steps: a share's length counts it, so that shares with many short tiles end with
+// the others.
+constexpr int kChunkTileCost = 4;
+static_assert(kChunkMinSteps > kChunkTileCost, "every share has a step");
 
 // Rows are a sequence's (new token, query head of one kv head) pairs, token by
 // token.  The decode kernel's plan is per kv head, the same for all; the chunk
@@ -28,7 +32,7 @@ struct KvHeader {
   int n_split;   // tiles cut by a unit's end
   int c_tiles;   // chunk: tiles
   int c_steps;   // sum of their steps
-  int c_units;   // equal shares of n_kv_heads times those steps, one CTA each
+  int c_units;   // shares of n_kv_heads times those, equal in cost, one CTA each
   int c_split;   // (head, tile) pairs cut by a unit's end
   int pad[7];
 };
@@ -38,13 +42,13 @@ struct KvHeader {
 //   tile    {sequence, 0, pages of the tiles before it, index among the cut ones or -1}, a sequence
 //           each, one more at the end with the pages of all
 //   split   two each: {first slot, pieces, first row, 0}, the sequence's entry
-//   c_tile  {sequence, first row, steps of the tiles before it, 0}, one more at the end
+//   c_tile  {sequence, first row, steps of the tiles before it, their cost}, one more at the end
 //   c_split two each: {first slot, pieces, first row, head}, the sequence's entry
 // and
 //   pre     prefix sums over the sequences {pages to append to, tiles, chunk tiles, 0}
 //   unit    first tile of each unit (int)
-//   c_unit  {first tile, first head, index among the cut pairs of the one that its start cuts or -1, 0},
-//           one more at the end
+//   c_unit  {first tile, first head, index among the cut pairs of the one that its start cuts or -1, first
+//           step of the tile}, one more at the end
 struct KvLayout {
   size_t seq, pre, append, tile, split, unit, c_tile, c_split, c_unit, bytes;  // byte offsets
   int64_t max_append, max_tiles, max_units, c_max_tiles, c_max_units;
