@@ -620,14 +620,25 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
       // the largest at (224, 448]; a row that is not finite gives NaN
       const int e = max((int)(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u), -126);
       const float qk = __uint_as_float((uint32_t)(127 - e) << 23);
-      uint4 n0 = valid ? src[0] : make_uint4(0, 0, 0, 0);
+      uint4 n0 = {}, n1 = {}, n2 = {}, n3 = {};
+      if (valid) {
+        n0 = src[0];
+        n1 = src[1];
+        n2 = src[2];
+        n3 = src[3];
+      }
 #pragma unroll 1
-      for (int i = 0; i < D / 8; ++i) {
-        const uint32_t w[4] = {n0.x, n0.y, n0.z, n0.w};
-        if (i + 1 < D / 8 && valid) n0 = src[i + 1];
-        uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+      for (int i = 0; i < D / 16; ++i) {
+        const uint32_t w[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
+        n0 = n2;
+        n1 = n3;
+        if (i + 2 < D / 16 && valid) {
+          n2 = src[2 * i + 4];
+          n3 = src[2 * i + 5];
+        }
+        uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 8; ++k) {
           const float f0 = bf16_lo(w[k]) * qk, f1 = bf16_hi(w[k]) * qk;
           float g0, g1;
           const uint32_t ph = e4m3x2(f0, f1);
@@ -635,9 +646,9 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
           hi[k >> 1] |= ph << (16 * (k & 1));
           lo[k >> 1] |= e4m3x2(f0 - g0, f1 - g1) << (16 * (k & 1));
         }
-        const uint32_t at = swizzled<D>(r, i >> 1) + 8 * (i & 1);
-        *reinterpret_cast<uint2*>(q_hi + at) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(q_hi + L::QP + at) = make_uint2(lo[0], lo[1]);
+        const uint32_t at = swizzled<D>(r, i);
+        *reinterpret_cast<uint4*>(q_hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(q_hi + L::QP + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
       fence_proxy_async_smem();
       __syncwarp();
