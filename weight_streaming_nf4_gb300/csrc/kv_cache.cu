@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const KvPlanArgs a) {
   // ---- chunk: 256-row tiles, shares of all heads' steps
   // A tile's cost is kChunkTileCost and its steps, or half of those where both slots share them (tiles of up to
   // half the rows).  A share that would begin in the first part begins with the tile.
-  auto halved = [&](int rows) { return rows <= kChunkRows / 2; };
+  auto halved = [](int rows) { return rows <= kChunkRows / 2; };
+  auto opening = [](bool half) { return half ? kChunkHalfTileCost : kChunkTileCost; };
   int Wc = 0, cost = 0;
   for (int base = 0; base < c_tiles; base += kPlanThreads) {
     const int i = base + tid;
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const KvPlanArgs a) {
       r0 = (i - pre[s].z) * kChunkRows;
       const int rows = min(seq[s].z * G - r0, kChunkRows);
       steps = (seq[s].x + (r0 + rows - 1) / G) / (2 * kPage) + 1;
-      mine = kChunkTileCost + (halved(rows) ? (steps + 1) / 2 : steps);
+      mine = opening(halved(rows)) + (halved(rows) ? (steps + 1) / 2 : steps);
     }
     int total, all;
     const int at = block_scan(steps, &total), before = block_scan(mine, &all);
@@ -204,9 +205,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const KvPlanArgs a) {
         h = (int)(x / cost);
         const int y = (int)(x % cost);
         t = last_at_most(c_tiles, y, [&](int j) { return c_tile[j].w; });
-        step = max(y - c_tile[t].w - kChunkTileCost, 0);
-        if (halved(seq[c_tile[t].x].z * G - c_tile[t].y)) step *= 2;
-        first = step > 0 && unit_start(u - 1, all, Uc) <= (int64_t)h * cost + c_tile[t].w + kChunkTileCost;
+        const bool half = halved(seq[c_tile[t].x].z * G - c_tile[t].y);
+        const int open = c_tile[t].w + opening(half);
+        step = max(y - open, 0) << half;
+        first = step > 0 && unit_start(u - 1, all, Uc) <= (int64_t)h * cost + open;
       }
       int total;
       const int j = n_cut + block_scan(first, &total);

@@ -15,10 +15,10 @@ constexpr int kTileRows = 16;    // rows of a tile of the decode kernel, which h
 // way each (D = 128), twelve with 12 KB (D = 64).
 constexpr int decode_warps(int hd) { return hd == 128 ? 8 : 12; }
 constexpr int kChunkRows = 256;  // rows of a tile of the chunk kernel, which has the others
-constexpr int kChunkMinSteps = 8;  // steps (two pages) of a share of the chunk kernel's work, at least
+constexpr int kChunkMinSteps = 12;  // steps (two pages) of a share of the chunk kernel's work, at least
 // What beginning a tile costs, in steps: a share's length counts it, so that shares with many short tiles end with
 // the others.
-constexpr int kChunkTileCost = 4;
+constexpr int kChunkTileCost = 10, kChunkHalfTileCost = 4;
 static_assert(kChunkMinSteps > kChunkTileCost, "every share has a step");
 
 // Rows are a sequence's (new token, query head of one kv head) pairs, token by
