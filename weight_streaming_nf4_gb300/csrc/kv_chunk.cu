@@ -610,32 +610,27 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
       const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(g.row0 + (valid ? tok : 0)) * a.sq +
                                                         (g.head * a.G + (valid ? R - tok * a.G : 0)) * D);
       uint32_t top = 0;
+#pragma unroll 1
+      for (int i0 = 0; i0 < D / 8; i0 += 8) {
+        uint4 x[8];
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const uint4 x = valid ? src[i] : make_uint4(0, 0, 0, 0);
-        top = __vmaxu2(top, __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu));
-        top = __vmaxu2(top, __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+        for (int k = 0; k < 8; ++k) x[k] = valid ? src[i0 + k] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          top = __vmaxu2(top, __vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu));
+          top = __vmaxu2(top, __vmaxu2(x[k].z & 0x7fff7fffu, x[k].w & 0x7fff7fffu));
+          *reinterpret_cast<uint4*>(q_hi + (k & 1) * L::QP + swizzled<D>(r, (i0 + k) >> 1)) = x[k];
+        }
       }
       top = max(top & 0xffffu, top >> 16);
       // the largest at (224, 448]; a row that is not finite gives NaN
       const int e = max((int)(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u), -126);
       const float qk = __uint_as_float((uint32_t)(127 - e) << 23);
-      uint4 n0 = {}, n1 = {}, n2 = {}, n3 = {};
-      if (valid) {
-        n0 = src[0];
-        n1 = src[1];
-        n2 = src[2];
-        n3 = src[3];
-      }
 #pragma unroll 1
       for (int i = 0; i < D / 16; ++i) {
+        const uint32_t at = swizzled<D>(r, i);
+        const uint4 n0 = *reinterpret_cast<const uint4*>(q_hi + at), n1 = *reinterpret_cast<const uint4*>(q_hi + L::QP + at);
         const uint32_t w[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
-        n0 = n2;
-        n1 = n3;
-        if (i + 2 < D / 16 && valid) {
-          n2 = src[2 * i + 4];
-          n3 = src[2 * i + 5];
-        }
         uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -646,7 +641,6 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
           hi[k >> 1] |= ph << (16 * (k & 1));
           lo[k >> 1] |= e4m3x2(f0 - g0, f1 - g1) << (16 * (k & 1));
         }
-        const uint32_t at = swizzled<D>(r, i);
         *reinterpret_cast<uint4*>(q_hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(q_hi + L::QP + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
