@@ -494,13 +494,15 @@ ws_status ws_qk_norm_rope_bwd(const ws_rope* rope, const int32_t* positions, int
  *   scale  fp32  [n_pages, n_kv_heads, 2]                      (keys', values')
  * The value that a code stands for is code * scale.  head_dim 64 or 128; device
  * memory, 16-byte aligned, the caller's; what is in it before the first append
- * does not matter. */
+ * does not matter.  A cache that a caller fills by other means than ws_kv_append
+ * has powers of two from 2^-126 on, or NaN, as scales, no code that is NaN in a
+ * sequence's places, and zeros for codes under a scale that is NaN. */
 enum { WS_KV_PAGE = 64, WS_KV_MAX_SEQS = 4096 };
 typedef struct {
   uint8_t* k;
   uint8_t* v;
   float* scale;
-  int64_t n_pages;              /* 1 .. 2^31 - 1 */
+  int64_t n_pages;              /* n_pages * n_kv_heads: 1 .. 2^31 - 1 */
   int32_t n_kv_heads, head_dim;
 } ws_kv_cache;
 /* A step's plan, made on the device once a step and shared by all layers (their
@@ -514,7 +516,8 @@ typedef struct {
  * outside the given memory is touched: past is taken as at least 0, a sequence's
  * rows beyond max_new, beyond T or beyond its table are left out (their output
  * rows stay as they were), and a page below 0 or from n_pages on holds nothing
- * (append drops its rows, attention passes over them). */
+ * (append drops its rows, attention passes over them).  A plan that is made again
+ * in the same memory waits, in its stream, for the calls that read it. */
 typedef struct {
   void* data;                   /* device, ws_kv_plan_size bytes */
   const int32_t* page_table;
@@ -522,8 +525,10 @@ typedef struct {
   int32_t n_seq;                /* 1 .. WS_KV_MAX_SEQS */
   int32_t max_pages;            /* row length of page_table; n_seq * max_pages <= 2^28 */
   int32_t max_new;              /* the most rows that a sequence may bring: 1 .. T */
-  int32_t n_heads, n_kv_heads, head_dim;  /* n_heads a multiple of n_kv_heads */
+  int32_t n_heads, n_kv_heads, head_dim;  /* n_heads <= 1024, a multiple of n_kv_heads <= 256 */
 } ws_kv_plan;
+/* Where max_new G > 16, G = n_heads / n_kv_heads: (T G / 256 + min(n_seq, T)) (max_pages / 2 + 11) stays
+ * below 2^31, and n_kv_heads times it below 2^36; WS_ERR_SHAPE far beyond. */
 ws_status ws_kv_plan_size(const ws_kv_plan* plan, size_t* bytes);
 ws_status ws_kv_plan_init(const ws_kv_plan* plan, const int32_t* past, const int32_t* row_start,
                           ws_stream_t stream);
@@ -532,10 +537,11 @@ ws_status ws_kv_plan_init(const ws_kv_plan* plan, const int32_t* past, const int
  * two 2^e, e >= -126, with max|x| <= 448 2^e over its tokens; a page that goes on
  * keeps a scale no smaller than it has, and where it grows the older codes are
  * rounded again (which changes only those that become subnormal).  A value that is
- * not finite makes its page's scale for that head NaN, and with it what reads the
- * page, until the page is begun anew.  Rounding is to nearest, ties to even.  A page
- * that receives rows belongs to one sequence (full pages may be shared); places
- * behind the appended rows stay as they were. */
+ * not finite makes its page's scale for that head NaN (the codes that it would have
+ * are zero), and with it what reads the page, until the page is begun anew.
+ * Rounding is to nearest, ties to even.  A page that receives rows stands in one
+ * place of one sequence's table (full pages may be shared); places behind the
+ * appended rows stay as they were.  Tokens are taken back by a smaller past[s]. */
 ws_status ws_kv_append(const ws_kv_cache* cache, const ws_kv_plan* plan, const uint16_t* k,
                        int64_t k_stride, const uint16_t* v, int64_t v_stride, ws_stream_t stream);
 /* Attention of the step's rows q [T, n_heads*head_dim] bf16 over the cache, which
@@ -546,8 +552,11 @@ ws_status ws_kv_append(const ws_kv_cache* cache, const ws_kv_plan* plan, const u
  * with k_j, v_j the values that the codes stand for.  scale > 0 (1/sqrt(head_dim) as
  * a rule).  A row that sees no page gets zeros and -infinity.  Sums and softmax are
  * fp32; probabilities enter the second product in fp16, relative to the largest.
- * No atomics: a given plan always gives the same bits.  Calls that may run at the
- * same time need a workspace each; a plan is only read. */
+ * Queries are held in fp16 (sequences of up to 16 rows, n_heads / n_kv_heads of a
+ * token) or as two e4m3 numbers: off by at most 2^-17.8 of their row's largest
+ * element.  o overlaps nothing else.  No atomics: a given plan always gives the same
+ * bits.  Calls that may run at the same time need a workspace each (16-byte
+ * aligned); a plan is only read. */
 ws_status ws_attention_kv_workspace_size(const ws_kv_plan* plan, size_t* bytes);
 ws_status ws_attention_kv(const ws_kv_cache* cache, const ws_kv_plan* plan, const uint16_t* q,
                           int64_t q_stride, float scale, uint16_t* o, int64_t o_stride, float* lse,

@@ -6,7 +6,9 @@
 // group) pairs, R = i G + h % G, so a group's heads share what is read.
 //
 // Decoding rows (k_kv_decode; sequences of more than kTileRows rows go to
-// kv_chunk.cu).  Bound by memory: each code is read once.  One
+// kv_chunk.cu: a second tile of 16 would read the codes again.  24 sequences of
+// 16000 tokens and 40 + 8 heads take 104 us with 15 rows each here, 134 with 20
+// there).  Bound by memory: each code is read once.  One
 // warp has a contiguous share of the pages of all 16-row tiles (equal shares,
 // so ragged batches fill the device), copies a page's keys and values (8 KB
 // each at D = 128) into shared memory while the ones before are used, and joins
@@ -21,6 +23,11 @@
 // Queries enter as fp16 times a power of two of their row, values' scales go
 // into P relative to the largest scale so far, keys' scales into the exponent.
 // Tiles cut by a share's end are joined by k_kv_join, in a fixed order.
+// Where no tile of the plan can have more than eight rows, NQ = 1 leaves the
+// second half of the operands out (188 registers for 244).
+// 48 sequences of 16000 tokens, 40 + 8 heads of 128: 162 us with the join, 6.1
+// TB/s.  Two of 130000, 28 + 4 heads, two new tokens each: 53 us, 4.1 TB/s, as a
+// share is 13 pages: start, ramp and partial results are a third.
 #define WS_KV_TU 1
 #include <math.h>
 
@@ -39,7 +46,6 @@ namespace {
 
 constexpr int kDecodeWarps = 4;
 constexpr int kPMargin = 14;  // P in [0, 1] times 2^14 in fp16, so that pages with small scales keep bits
-
 
 WS_DEVINL void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                        uint32_t b1) {

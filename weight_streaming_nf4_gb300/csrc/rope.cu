@@ -17,7 +17,8 @@
 // D/16 threads has one token and walks over some of its heads, so the sines
 // and cosines (eight pairs a thread, in registers) serve all of them; a thread
 // has both elements of each of its pairs, two 16-byte pieces a head, and the
-// only exchange is the head's sum.
+// only exchange is the head's sum.  16384 rows of 40 + 8 heads of 128 take 71 us
+// (5.7 TB/s), 8192 rows of 28 + 4 backward 38 us (5.3 TB/s).
 #include <math.h>
 
 #include <algorithm>
