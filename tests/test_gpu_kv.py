@@ -482,7 +482,8 @@ def test_offsets_past_32_bits(ops):
 
 
 WIDE = [(1, 1024, 128, [70], [1]), (1, 1024, 64, [5, 0], [2, 1]), (256, 1, 64, [3, 64], [1, 2]), (256, 4, 64, [90], [20]),
-        (2, 17, 128, [200, 64], [1, 1]), (4, 8, 128, [640, 127, 0], [2, 3, 2])]
+        (2, 17, 128, [200, 64], [1, 1]), (4, 8, 128, [640, 127, 0], [2, 3, 2]), (8, 1, 64, [0] * 20, [17] * 20),
+        (2, 3, 128, [37 * i % 150 for i in range(60)], [(5, 6, 43, 44, 90)[i % 5] for i in range(60)]), (2, 5, 128, [0], [1639])]
 
 
 @pytest.mark.parametrize("case", WIDE, ids=[str(i) for i in range(len(WIDE))])
