@@ -36,6 +36,7 @@ constexpr int kRopeThreads = 256;
 // three.
 constexpr int kFwdBatch = 8;
 constexpr int kBwdBatch = 2;
+constexpr int kGainRow = kRopeThreads + 8;  // floats of a row of the threads' sums, padded
 constexpr int kGainRows = 32;    // rows that k_rope_gain adds side by side
 
 struct RopeArgs {
@@ -195,8 +196,11 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_fwd(const RopeArgs a) {
 template <int D, bool IL, bool GAINS>
 WS_DEVINL void bwd_heads(const RopeArgs& a, const Token<D, IL>& tok, const uint16_t* x,
                          const uint16_t* u, uint16_t* o, const float* gain, int first, int heads,
-                         bool live, float (&dg)[16]) {
+                         bool live, float* sums) {
   constexpr int B = kBwdBatch;
+  float dg[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) dg[j] = 0.0f;
   float w[16];
   if (gain) load_gain(gain, tok.c0, tok.c1, w);
   for (int j0 = 0; j0 < heads; j0 += B * a.parts) {
@@ -236,49 +240,48 @@ WS_DEVINL void bwd_heads(const RopeArgs& a, const Token<D, IL>& tok, const uint1
       if (live && h < heads) store16(o + h * D, tok.c0, tok.c1, d);
     }
   }
+  if (GAINS) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) sums[j * kGainRow] += dg[j];
+  }
 }
 
-// The CTAs take the (token, part) units in turn; each sums its share of the
-// gains' gradients in registers, then over its groups in their order.
+// The CTAs take the (token, part) units in turn.  A thread's share of the gains'
+// gradients grows in its own place in shared memory, a unit's heads at a time; then
+// the CTA's groups are summed in their order.  16384 tokens of 40 + 8 heads: 132 us
+// (4.6 TB/s); with the sums of all units in registers, which leave one CTA an SM,
+// 172.
 template <int D, bool IL, bool GAINS>
-__global__ void __launch_bounds__(kRopeThreads) k_rope_bwd(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 2) k_rope_bwd(const RopeArgs a) {
   constexpr int T = D / 16, G = kRopeThreads / T;
-  __shared__ float sum[GAINS ? G : 1][D + 4];
+  __shared__ float sum[GAINS ? 32 : 1][kGainRow];  // [q, k][element of the thread][thread]
   pdl_wait();
   pdl_launch_dependents();
-  const int t = (int)threadIdx.x % T, g = (int)threadIdx.x / T;
+  const int tid = (int)threadIdx.x, t = tid % T, g = tid / T;
   const int64_t units = a.M * a.parts;
-  float dgq[16], dgk[16];
-#pragma unroll
-  for (int j = 0; j < 16; ++j) dgq[j] = dgk[j] = 0.0f;
-  int c0 = 0, c1 = 0;
+  if (GAINS)
+    for (int j = 0; j < 32; ++j) sum[j][tid] = 0.0f;
   for (int64_t u0 = (int64_t)blockIdx.x * G; u0 < units; u0 += (int64_t)gridDim.x * G) {
     const int64_t unit = u0 + g;
     const bool live = unit < units;
     const int64_t m = live ? unit / a.parts : 0;
     const int part = live ? (int)(unit % a.parts) : 0;
     const Token<D, IL> tok(a, t, m);
-    c0 = tok.c0;
-    c1 = tok.c1;
     bwd_heads<D, IL, GAINS>(a, tok, a.q + m * a.sq, a.uq + m * a.suq, a.oq + m * a.soq, a.gq, part,
-                            a.nh, live, dgq);
+                            a.nh, live, &sum[0][tid]);
     const int first = (part - a.nh % a.parts + a.parts) % a.parts;
     bwd_heads<D, IL, GAINS>(a, tok, a.k + m * a.sk, a.uk + m * a.suk, a.ok + m * a.sok, a.gk, first,
-                            a.nkv, live, dgk);
+                            a.nkv, live, &sum[GAINS ? 16 : 0][tid]);
   }
   if (GAINS) {
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        sum[g][(j < 8 ? c0 : c1) * 8 + (j & 7)] = which ? dgk[j] : dgq[j];
-      __syncthreads();
-      for (int d = (int)threadIdx.x; d < D; d += kRopeThreads) {
-        float s = 0.0f;
-        for (int i = 0; i < G; ++i) s += sum[i][d];
-        a.partial[((int64_t)blockIdx.x * 2 + which) * D + d] = s;
-      }
+    __syncthreads();
+    const int rt = a.turns ? a.rot / 16 : 0;
+    for (int i = tid; i < 2 * D; i += kRopeThreads) {
+      const int row = i / T, c = i % T, j = row & 15;  // element j of the groups' threads c
+      float s = 0.0f;
+      for (int k = 0; k < G; ++k) s += sum[row][k * T + c];
+      const int piece = j < 8 ? (c < rt ? c : 2 * c) : (c < rt ? c + rt : 2 * c + 1);
+      a.partial[((int64_t)blockIdx.x * 2 + (row >> 4)) * D + piece * 8 + (j & 7)] = s;
     }
   }
 }
@@ -312,15 +315,18 @@ ws_status rope_shape(int64_t M, int32_t nh, int32_t nkv, int32_t hd) {
   return hd == 64 || hd == 128 ? WS_OK : WS_ERR_SHAPE;
 }
 
-// Groups of about the threads that the device holds at once (768 an SM at the
-// kernels' registers; with twice as many the backward of 512 tokens took 23 us
-// for 17, that of 8192 tokens 45 for 39).
-int64_t full_groups(int hd) { return (int64_t)device_sm_count() * 768 / (hd / 16); }
+// Threads of an SM whose groups a call is dealt to: about as many as it holds at
+// the kernels' registers (with twice as many the backward of 512 tokens took 23 us
+// for 17, that of 8192 tokens 45 for 39); for the backward with gradients of gains
+// the two CTAs that run at once (2048 tokens of 40 + 8 heads: 22 us, with 768 and
+// four CTAs 28.5, with 256 and two 28).
+constexpr int kFullThreads = 768, kGainThreads = 512;
+int64_t full_groups(int hd, int threads) { return (int64_t)device_sm_count() * threads / (hd / 16); }
 
 // Groups a token's heads are dealt to: as few as fill the device (each then
 // makes the sines and cosines for more heads).
-int rope_parts(int64_t M, int heads, int hd) {
-  const int64_t want = full_groups(hd) / M;
+int rope_parts(int64_t M, int heads, int hd, int threads = kFullThreads) {
+  const int64_t want = full_groups(hd, threads) / M;
   return (int)std::max<int64_t>(1, std::min<int64_t>(want, heads));
 }
 int64_t rope_ctas(int64_t M, int parts, int hd) {
@@ -329,7 +335,7 @@ int64_t rope_ctas(int64_t M, int parts, int hd) {
 }
 // CTAs of the backward where they sum gradients: no more than run at once.
 int64_t rope_gain_ctas(int64_t M, int parts, int hd) {
-  return std::min<int64_t>(rope_ctas(M, parts, hd), (int64_t)device_sm_count() * 4);
+  return std::min<int64_t>(rope_ctas(M, parts, hd), (int64_t)device_sm_count() * kGainThreads / kRopeThreads);
 }
 
 ws_status check_io(const void* p, int64_t stride, int32_t heads, int32_t hd) {
@@ -428,7 +434,8 @@ ws_status ws_qk_norm_rope_workspace_size(int64_t M, int32_t n_heads, int32_t n_k
   if (!bytes) return WS_ERR_INVALID;
   const ws_status s = rope_shape(M, n_heads, n_kv_heads, head_dim);
   if (s != WS_OK) return s;
-  *bytes = (size_t)rope_gain_ctas(M, rope_parts(M, n_heads + n_kv_heads, head_dim), head_dim) * 2 * head_dim * 4;
+  const int parts = rope_parts(M, n_heads + n_kv_heads, head_dim, kGainThreads);
+  *bytes = (size_t)rope_gain_ctas(M, parts, head_dim) * 2 * head_dim * 4;
   return WS_OK;
 }
 
@@ -458,6 +465,7 @@ ws_status ws_qk_norm_rope_bwd(const ws_rope* rope, const int32_t* positions, int
   if ((dq_gain && !al4r(dq_gain)) || (dk_gain && !al4r(dk_gain))) return WS_ERR_ALIGN;
   const bool gains = dq_gain || dk_gain;
   RopeArgs a = rope_args(rope, positions, M, n_heads, n_kv_heads, head_dim, eps, q_gain, k_gain);
+  if (gains) a.parts = rope_parts(M, n_heads + n_kv_heads, head_dim, kGainThreads);
   const int64_t ctas = gains ? rope_gain_ctas(M, a.parts, head_dim) : rope_ctas(M, a.parts, head_dim);
   if (gains) {
     if (!workspace) return WS_ERR_INVALID;
