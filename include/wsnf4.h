@@ -551,7 +551,8 @@ ws_status ws_kv_append(const ws_kv_cache* cache, const ws_kv_plan* plan, const u
  *   lse = ln sum_j exp(scale q_i . k_j)                [n_heads, T] fp32, or NULL
  * with k_j, v_j the values that the codes stand for.  scale > 0 (1/sqrt(head_dim) as
  * a rule).  A row that sees no page gets zeros and -infinity.  Sums and softmax are
- * fp32; probabilities enter the second product in fp16, relative to the largest.
+ * fp32; probabilities, relative to the largest, enter the second product as two
+ * fp16 numbers (2^-22 of themselves).
  * Queries are held in fp16 (sequences of up to 16 rows, n_heads / n_kv_heads of a
  * token) or as two e4m3 numbers: off by at most 2^-17.8 of their row's largest
  * element.  o overlaps nothing else.  No atomics: a given plan always gives the same

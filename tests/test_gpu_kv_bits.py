@@ -1,0 +1,86 @@
+"""The precision of attention over the 8-bit cache, held to what the header states: results whose large terms cancel, so
+that the rounding to bf16 does not hide what is lost before it.
+
+Tolerance.  An element is rounded to bf16 once, 2^-8 of it.  Before that, with N tokens seen and p_j their probabilities:
+- a probability enters the second product as two fp16 numbers, hi and the rest: off by at most 2^-11 2^-11 = 2^-22 of itself,
+  and by 2^-31 of the row's largest p_j S_j (S_j the scale of its page's values) however small it is: the rest's steps end at
+  2^-24, half of one is 2^-25, and the largest enters as 2^6 or more.  Codes are 448 at most, so N times 448 2^-31 max_j p_j S_j;
+- 2^x and the rounding of x, |x| <= 16: 2^-22 + 2^-24 16 < 2^-19; the sums of p_j and of p_j v_j, N roundings of 2^-24 each;
+- a score, delta = scale (2^-18 max_j sum_i |q_i k_ij| + 2^-21 max|q| max_j sum_{i small} |k_ij|): fp32 sums of hd products in two
+  parts, and queries that are exact down to 2^-14 of their row's largest element and off by 2^-21.8 of it below (small)."""
+import math
+
+import pytest
+import torch
+
+from test_gpu_kv import DEV, PAGE, Model, empty_cache, ints
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ops():
+    from weight_streaming_nf4_gb300 import ops as o
+    return o
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def bf16(x):
+    return x.bfloat16().to(DEV)
+
+
+def check(ops, k, v, q, past, G, scale=None, pages=None):
+    """One sequence: k, v [past + n, nkv, hd] appended, its last n rows' q [n, nkv*G, hd] against 64 bits of the cached values."""
+    total, nkv, hd = k.shape
+    n, scale = total - past, hd ** -0.5 if scale is None else scale
+    pages = list(range(-(-total // PAGE)))[::-1] if pages is None else pages
+    cache = empty_cache(ops, len(pages), nkv, hd)
+    model = Model(cache)
+    flat = [t.reshape(total, nkv * hd) for t in (k, v)]
+    for a, b in ((0, past), (past, total)):
+        if b > a:
+            plan = ops.kv_plan(ints([a]), ints([0, b - a]), ints([pages]), b - a, b - a, nkv * G, nkv, hd)
+            ops.kv_append(cache, plan, flat[0][a:b], flat[1][a:b])
+            model.append([a], [b - a], [pages], flat[0][a:b], flat[1][a:b])
+    model.check(cache)
+    o, lse = ops.attention_kv(q.reshape(n, -1), cache, plan, scale=scale, want_lse=True)
+    torch.cuda.synchronize()
+    assert ops.device_error() == 0
+    at = torch.tensor(pages, device=DEV)
+    kk, vv = ((t[at] * model.s[at, :, c, None, None]).transpose(0, 1).reshape(nkv, -1, hd)[:, :total] for c, t in ((0, model.k), (1, model.v)))
+    S = model.s[at, :, 1].t().repeat_interleave(PAGE, 1)[:, :total]
+    x = q.double().view(n, nkv, G, hd).permute(1, 2, 0, 3)
+    seen = torch.arange(total, device=DEV) <= past + torch.arange(n, device=DEV)[:, None]
+    s = (torch.einsum("hgnd,hjd->hgnj", x, kk) * scale).masked_fill(~seen, -math.inf)
+    ref = torch.logsumexp(s, -1)
+    p = s.softmax(-1)
+    want, size = torch.einsum("hgnj,hjd->hgnd", p, vv), torch.einsum("hgnj,hjd->hgnd", p, vv.abs())
+    top = x.abs().amax(-1, keepdim=True)
+    small = (x.abs() < 2.0 ** -14 * top).double()
+    delta = scale * (2.0 ** -18 * torch.einsum("hgnd,hjd->hgnj", x.abs(), kk.abs()).amax(-1)
+                     + 2.0 ** -21 * top[..., 0] * torch.einsum("hgnd,hjd->hgnj", small, kk.abs()).amax(-1))
+    floor = 2.0 ** -31 * 448 * total * (p * S[:, None, None]).amax(-1)
+    rel = 2.0 ** -22 + 2.0 ** -19 + 2 * total * 2.0 ** -24
+    tol = 2.0 ** -8 * want.abs() + (rel + 2 * delta)[..., None] * size + floor[..., None]
+    got = o.double().view(n, nkv, G, hd).permute(1, 2, 0, 3)
+    worst = ((got - want).abs() / tol).max().item()
+    assert worst <= 1, worst
+    assert ((lse.double().view(nkv, G, n) - ref).abs() <= delta + 2.0 ** -19 + total * 2.0 ** -24 + 2.0 ** -22 * ref.abs()).all()
+    return o
+
+
+FORMS = [  # kv heads, query heads of each, head size, tokens before, new rows: up to 8, up to 16, up to 128 rows a tile, more
+    (4, 2, 64, 30, 1), (4, 5, 128, 40, 1), (4, 8, 64, 20, 2), (2, 16, 128, 40, 1), (4, 4, 64, 3, 20), (2, 5, 128, 20, 25),
+    (2, 8, 64, 0, 40), (2, 8, 128, 8, 40), (4, 2, 64, 150, 1), (2, 8, 128, 100, 40)]
+
+
+@pytest.mark.parametrize("form", FORMS, ids=[str(i) for i in range(len(FORMS))])
+def test_probabilities_are_not_rounded_to_a_half(ops, form):
+    """Values of both signs cancel; scores differ little, so no token decides alone."""
+    nkv, G, hd, past, n = form
+    g = gen(sum(form))
+    k, q = bf16(torch.randn(past + n, nkv, hd, generator=g) * 0.2), bf16(torch.randn(n, nkv * G, hd, generator=g) * 0.5)
+    check(ops, k, bf16(torch.randn(past + n, nkv, hd, generator=g)), q, past, G)

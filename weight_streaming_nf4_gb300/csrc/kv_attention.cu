@@ -22,6 +22,9 @@
 // which row of S^T is chosen so that P arrives where V^T wants it.
 // Queries enter as fp16 times a power of two of their row, values' scales go
 // into P relative to the largest scale so far, keys' scales into the exponent.
+// P enters as two fp16 numbers, what one leaves being the other: 2^-22 of itself
+// for the 2^-11 of one, which is what results of terms that cancel are off by.
+// The second product's operations double; the pages' way stays what bounds it.
 // Tiles cut by a share's end are joined by k_kv_join, in a fixed order.
 // Where no tile of the plan can have more than eight rows, NQ = 1 leaves the
 // second half of the operands out (188 registers for 244).
@@ -45,7 +48,7 @@ cudaError_t kv_read_and_clear_dev_error(uint32_t* flags) {
 namespace {
 
 constexpr int kDecodeWarps = 4;
-constexpr int kPMargin = 14;  // P in [0, 1] times 2^14 in fp16, so that pages with small scales keep bits
+constexpr int kPMargin = 14;  // P in [0, 1] times 2^14, so that pages with small scales keep bits in fp16
 
 WS_DEVINL void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                        uint32_t b1) {
@@ -298,7 +301,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
       }
       float vr = cur.vs == 0.0f ? 0.0f : cur.vs / vref;  // NaN for a page that holds one
       vr *= (float)(1 << kPMargin);
-      uint32_t bp[NQ][4][2];
+      uint32_t bp[NQ][4][2], br[NQ][4][2];  // P as fp16 and the rest
 #pragma unroll
       for (int nq = 0; nq < NQ; ++nq) {
         if (nq > 0 && !wide) break;
@@ -371,7 +374,12 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) bp[nq][mt][h] = transpose8x8(pack_f16x2(s[nq][mt][2 * h], s[nq][mt][2 * h + 1]));
+          for (int h = 0; h < 2; ++h) {
+            uint32_t hi, rest;
+            split_f16x2(s[nq][mt][2 * h], s[nq][mt][2 * h + 1], hi, rest);
+            bp[nq][mt][h] = transpose8x8(hi);
+            br[nq][mt][h] = transpose8x8(rest);
+          }
       }
 
       if (!take()) return;
@@ -399,7 +407,10 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
           decode4(x1[i], a1, a3);
 #pragma unroll
           for (int nq = 0; nq < NQ; ++nq)
-            if (nq == 0 || wide) mma_f16(o[nq][ht], a0, a1, a2, a3, bp[nq][i][0], bp[nq][i][1]);
+            if (nq == 0 || wide) {
+              mma_f16(o[nq][ht], a0, a1, a2, a3, bp[nq][i][0], bp[nq][i][1]);
+              mma_f16(o[nq][ht], a0, a1, a2, a3, br[nq][i][0], br[nq][i][1]);
+            }
         }
       }
       __syncwarp();

@@ -9,9 +9,10 @@
 //                all eight bits of bf16, down to 2^-10 of the row's largest
 //                element, and an absolute error of 2^-17.8 of it below; two
 //                products at twice fp16's rate cost what one fp16 product does
-//   P = 2^(S c - m), fp16, over the same columns of tensor memory
-//   O += P V     kind::f16, A from tensor memory, V decoded to fp16 (exact) by two
-//                warps, once for both slots
+//   P = 2^(S c - m) as fp16 and, for every 16 tokens behind it, what fp16 leaves of it
+//                (2^-22 of P for 2^-11), in the same columns of tensor memory
+//   O += P V     kind::f16, two products, A from tensor memory, V decoded to fp16
+//                (exact) by two warps, once for both slots
 // A row is a thread's, so its maximum and sum need no exchange.  m moves only
 // when a row's maximum has grown by 2^8 or more (P stays below 2^15 in fp16):
 // then the softmax warps wait for the products before and rescale O in tensor
@@ -57,7 +58,7 @@ constexpr int kSlotRows = 128;
 constexpr int kStepTokens = 2 * kPage;
 constexpr int kInfo = 64;      // pages of a window of the pages' list
 constexpr int kLag = 8;        // powers of two by which a row's maximum may outgrow m
-constexpr int kChMargin = 7;   // P 2^7: below 2^15 in fp16
+constexpr int kChMargin = 7;   // P 2^7: up to 2^15 in fp16
 
 struct ChunkArgs {
   KvAttnArgs a;
@@ -176,11 +177,6 @@ WS_DEVINL void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
       "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-WS_DEVINL void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
 WS_DEVINL void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* bar, int32_t x, int32_t y, int32_t z) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
@@ -245,8 +241,9 @@ WS_DEVINL f32x2 add2(f32x2 a, f32x2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// 32 of a row's scores as 2^(x cf - shift), fp16 pairs; their sums are added to sum.
-WS_DEVINL void weigh_plain(const uint32_t (&x)[32], f32x2 c2, f32x2 r2, f32x2 (&sum)[2], uint32_t* p) {
+// 32 of a row's scores as 2^(x cf - shift), as they lie in tensor memory: for every 16 tokens eight columns of fp16
+// pairs and eight of what those leave.  Their sums are added to sum.
+WS_DEVINL void weigh_plain(const uint32_t (&x)[32], f32x2 c2, f32x2 r2, f32x2 (&sum)[2], uint32_t (&p)[32]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     float y0, y1;
@@ -254,7 +251,8 @@ WS_DEVINL void weigh_plain(const uint32_t (&x)[32], f32x2 c2, f32x2 r2, f32x2 (&
     y0 = ex2(y0);
     y1 = ex2(y1);
     sum[i & 1] = add2(sum[i & 1], pair(y0, y1));
-    p[i] = pack_f16x2(y0, y1);
+    const int at = (i & 8) * 2 + (i & 7);
+    split_f16x2(y0, y1, p[at], p[at + 8]);
   }
 }
 template <int D>
@@ -484,8 +482,8 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
               tc_fence_after();
               if (elect_one()) {
 #pragma unroll
-                for (int i = 0; i < kPage / 16; ++i)
-                  tc_mma_f16_ta(d, p + i * 8, v + ((32 * i) >> 4), idO, (e < 2 && i == 0) ? 0u : 1u);
+                for (int i = 0; i < kPage / 8; ++i)  // 16 tokens' P, then what fp16 leaves of it
+                  tc_mma_f16_ta(d, p + i * 8, v + ((32 * (i >> 1)) >> 4), idO, (e < 2 && i == 0) ? 0u : 1u);
                 tc_commit(&o_done[2 * s]);
               }
               __syncwarp();
@@ -493,8 +491,8 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
               tc_fence_after();
               if (elect_one()) {
 #pragma unroll
-                for (int i = 0; i < kPage / 16; ++i)
-                  tc_mma_f16_ta(d, p + 32 + i * 8, v + ((D * 128 + 32 * i) >> 4), idO, 1u);
+                for (int i = 0; i < kPage / 8; ++i)
+                  tc_mma_f16_ta(d, p + kPage + i * 8, v + ((D * 128 + 32 * (i >> 1)) >> 4), idO, 1u);
                 tc_commit(&o_done[2 * s + 1]);
                 if (ends) tc_commit(&v_empty[vst]);
               }
@@ -769,7 +767,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           const PageInfo pi = info_of(n, half);
-          const uint32_t t_p = t_s + half * 32, t_v = t_s + half * kPage;
+          const uint32_t t_v = t_s + half * kPage;  // the page's scores, and in their place P
           float cf = qs * pi.ks;
           cf = cf < 1e-37f ? 1e-37f : cf;  // not below fp32's range: -inf * 0 is NaN
           const int vis = pi.page >= 0 ? lim - (2 * (sg.s0 + j) + half) * kPage : 0;  // of the page, seen
@@ -780,7 +778,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
                              e <= kChMargin && vis >= kPage && m > -INFINITY;
           bool grown = false, rest = true;
           if (warp_all(plain)) {
-            uint32_t p[32];
+            uint32_t p0[32], p1[32];
             uint32_t x0[32], x1[32];
             const float shift = m - (float)e;
             const f32x2 c2 = pair(cf, cf), r2 = pair(-shift, -shift);
@@ -788,9 +786,9 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
             tmem_ld_32x32b_x32(t_v, x0);
             tmem_ld_wait();
             tmem_ld_32x32b_x32(t_v + 32, x1);
-            weigh_plain(x0, c2, r2, two, p);
+            weigh_plain(x0, c2, r2, two, p0);
             tmem_ld_wait();
-            weigh_plain(x1, c2, r2, two, p + 16);
+            weigh_plain(x1, c2, r2, two, p1);
             float sum, other;
             unpair(add2(two[0], two[1]), sum, other);
             sum = (sum + other) * __uint_as_float((uint32_t)(127 - e) << 23);
@@ -798,11 +796,12 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
             rest = !warp_all(!grown);
             if (!rest) {
               l += sum;
-              tmem_st_32x32b_x32(t_p, p);
+              tmem_st_32x32b_x32(t_v, p0);
+              tmem_st_32x32b_x32(t_v + 32, p1);
             }
           }
           if (rest) {
-            // Any other page, 16 columns at a time: the maximum, then P, whose columns follow behind those of S.
+            // Any other page, 16 columns at a time: the maximum, then P in the place of S.
             float top = -INFINITY;
 #pragma unroll 1
             for (int cc = 0; cc < kPage; cc += 16) {
@@ -841,7 +840,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
             const float vr = (pi.vs == 0.0f ? 0.0f : pi.vs / vref) * (float)(1 << kChMargin);
 #pragma unroll 1
             for (int cc = 0; cc < kPage; cc += 16) {
-              uint32_t x[16], p[8];
+              uint32_t x[16], p[16];
               tmem_ld_32x32b_x16(t_v + cc, x);
               tmem_ld_wait();
 #pragma unroll
@@ -851,9 +850,9 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
                 const float y0 = in0 ? ex2(fmaf(__uint_as_float(x[2 * i]), cf, -ref)) : 0.0f;
                 const float y1 = in1 ? ex2(fmaf(__uint_as_float(x[2 * i + 1]), cf, -ref)) : 0.0f;
                 l += y0 + y1;
-                p[i] = pack_f16x2(in0 ? y0 * vr : 0.0f, in1 ? y1 * vr : 0.0f);
+                split_f16x2(in0 ? y0 * vr : 0.0f, in1 ? y1 * vr : 0.0f, p[i], p[i + 8]);
               }
-              tmem_st_32x32b_x8(t_p + cc / 2, p);
+              tmem_st_32x32b_x16(t_v + cc, p);
             }
           }
           tmem_st_wait();

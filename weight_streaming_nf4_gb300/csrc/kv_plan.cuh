@@ -146,6 +146,15 @@ WS_DEVINL uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// Two probabilities as fp16 and what that leaves, also fp16: 2^-22 of themselves, or 2^-25 where that is more.
+WS_DEVINL void split_f16x2(float a, float b, uint32_t& hi, uint32_t& rest) {
+  hi = pack_f16x2(a, b);
+  float x, y;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}"
+      : "=f"(x), "=f"(y)
+      : "r"(hi));
+  rest = pack_f16x2(a - x, b - y);
+}
 // Codes 0, 1 (lo) and 2, 3 (hi) of a word, exact in fp16.
 WS_DEVINL void decode4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
