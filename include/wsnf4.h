@@ -551,8 +551,10 @@ ws_status ws_kv_append(const ws_kv_cache* cache, const ws_kv_plan* plan, const u
  *   lse = ln sum_j exp(scale q_i . k_j)                [n_heads, T] fp32, or NULL
  * with k_j, v_j the values that the codes stand for.  scale > 0 (1/sqrt(head_dim) as
  * a rule).  A row that sees no page gets zeros and -infinity.  Sums and softmax are
- * fp32; probabilities, relative to the largest, enter the second product as two
- * fp16 numbers (2^-22 of themselves).
+ * fp32; a probability times the scale of its page's values enters the second
+ * product, relative to the row's largest such product, as two fp16 numbers: off by
+ * 2^-22 of itself, or by 2^-31 of that largest where this is more.  A page whose
+ * probabilities are all below 2^-100 of the row's largest counts as none.
  * Queries are held in fp16 (sequences of up to 16 rows, n_heads / n_kv_heads of a
  * token) or as two e4m3 numbers: off by at most 2^-17.8 of their row's largest
  * element.  o overlaps nothing else.  No atomics: a given plan always gives the same

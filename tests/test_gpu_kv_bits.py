@@ -84,3 +84,32 @@ def test_probabilities_are_not_rounded_to_a_half(ops, form):
     g = gen(sum(form))
     k, q = bf16(torch.randn(past + n, nkv, hd, generator=g) * 0.2), bf16(torch.randn(n, nkv * G, hd, generator=g) * 0.5)
     check(ops, k, bf16(torch.randn(past + n, nkv, hd, generator=g)), q, past, G)
+
+
+WEIGHTS = [  # for each page of the cache: its values' size 2^e, its scores' distance from the others' in powers of two
+    [(30, -90), (0, 0), (0, 0)], [(0, 0), (30, -90), (0, 0)], [(0, 0), (0, 0), (30, -90)], [(60, -90), (0, 0), (-3, 0)],
+    [(100, -250), (0, 0), (0, 0)], [(0, 0), (100, -250), (0, 0)], [(30, -30), (0, 0), (0, 0)], [(0, 0), (0, 0), (30, -30)],
+    [(-45, 45), (45, -45), (0, 0)], [(45, -45), (0, 0), (-45, 45)], [(0, 0), (-40, 12), (-20, 12)], [(-20, -12), (-40, -25), (20, -80)],
+    [(8, -8), (12, -12), (4, -4)], [(3, 0), (-4, 7), (12, -9)]]
+
+
+# With few pages each is a share of its own for up to 16 rows, so their forms have 256 kv heads (whose pages share four
+# to a head) and the pattern four times.
+@pytest.mark.parametrize("form", [(256, 2, 64, 1, 4), (256, 4, 64, 4, 4), (130, 1, 128, 2, 4), (2, 2, 64, 1, 1), (2, 4, 64, 20, 1), (1, 8, 128, 40, 1)],
+                         ids=["8rows", "16rows", "2rows", "whole", "slot", "tile"])
+@pytest.mark.parametrize("pages", WEIGHTS, ids=[str(i) for i in range(len(WEIGHTS))])
+def test_a_page_counts_by_its_weight_times_its_scale(ops, form, pages):
+    """Pages of large values that hardly count, and of small ones that decide: in any order, each keeps its bits."""
+    nkv, G, hd, n, times = form
+    pages = pages * times
+    past = PAGE * len(pages)
+    g = gen(n + hd)
+    k, v = torch.randn(past + n, nkv, hd, generator=g) * 0.2, torch.randn(past + n, nkv, hd, generator=g)
+    k[..., 0] = 0
+    for i, (e, d) in enumerate(pages):
+        at = slice(PAGE * i, PAGE * (i + 1))
+        v[at] *= 2.0 ** e
+        k[at, :, 0] = d * math.log(2)
+    q = torch.randn(n, nkv * G, hd, generator=g) * 0.3
+    q[..., 0] = hd ** 0.5
+    check(ops, bf16(k), bf16(v), bf16(q), past, G)

@@ -21,7 +21,7 @@
 // exchange but a transposition of P in registers (movmatrix).  Which token is
 // which row of S^T is chosen so that P arrives where V^T wants it.
 // Queries enter as fp16 times a power of two of their row, values' scales go
-// into P relative to the largest scale so far, keys' scales into the exponent.
+// into P (page_ref in kv_plan.cuh), keys' scales into the exponent.
 // P enters as two fp16 numbers, what one leaves being the other: 2^-22 of itself
 // for the 2^-11 of one, which is what results of terms that cancel are off by.
 // The second product's operations double; the pages' way stays what bounds it.
@@ -48,7 +48,7 @@ cudaError_t kv_read_and_clear_dev_error(uint32_t* flags) {
 namespace {
 
 constexpr int kDecodeWarps = 4;
-constexpr int kPMargin = 14;  // P in [0, 1] times 2^14, so that pages with small scales keep bits in fp16
+constexpr int kPMargin = 14;  // P in [0, 1] times 2^14, so that small ones keep bits in fp16
 
 WS_DEVINL void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                        uint32_t b1) {
@@ -188,9 +188,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
 
   uint32_t bq[NQ][KS][2];          // Q^T operands
   float o[NQ][HT][4];              // O^T: elements 16 ht + g (+ 8), rows 8 nq + 2t (+ 1)
-  float m[NQ][2], l[NQ][2], qs[NQ][2];
+  float m[NQ][2], l[NQ][2], ref[NQ][2], qs[NQ][2];
   int lim[NQ][2];                  // tokens each row sees
-  float vref = 0.0f;
   int rows = 0, kv_end = 0, first_lim = 0;
   bool wide = false;               // more than eight rows: the second half of the operands is in use
   int4 tl = make_int4(0, 0, 0, 0), sq = tl;
@@ -206,7 +205,6 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
       wide = rows > 8;
       kv_end = sq.x + sq.z;
       first_lim = sq.x + 1;
-      vref = 0.0f;
 #pragma unroll
       for (int nq = 0; nq < NQ; ++nq) {
         // row 8 nq + g: elements D/4 t .. of it
@@ -242,7 +240,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
           const int c = 2 * t + e;  // the row of this thread's columns of S^T
           qs[nq][e] = a.sl2 / __shfl_sync(0xffffffffu, qk, 4 * c);
           lim[nq][e] = 8 * nq + c < rows ? sq.x + (8 * nq + c) / a.G + 1 : 0;
-          m[nq][e] = -INFINITY;
+          m[nq][e] = ref[nq][e] = -INFINITY;
           l[nq][e] = 0.0f;
         }
 #pragma unroll
@@ -289,23 +287,13 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
       // softmax: columns (rows of q) 2t, 2t + 1; tokens 16 (g / 2) + 4 mt + g % 2 (+ 2)
       const int tok0 = cur.p * kPage + 16 * (g >> 1) + (g & 1);
       const bool tail = (cur.p + 1) * kPage > first_lim;
-      if (cur.vs > vref) {  // a larger scale than any before
-        const float c = vref / cur.vs;
-#pragma unroll
-        for (int nq = 0; nq < NQ; ++nq)
-#pragma unroll
-          for (int ht = 0; ht < HT; ++ht)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[nq][ht][e] *= c;
-        vref = cur.vs;
-      }
-      float vr = cur.vs == 0.0f ? 0.0f : cur.vs / vref;  // NaN for a page that holds one
-      vr *= (float)(1 << kPMargin);
+      float vf;  // NaN for a page that holds one
+      const float ve = scale_parts(cur.vs, vf);
       uint32_t bp[NQ][4][2], br[NQ][4][2];  // P as fp16 and the rest
 #pragma unroll
       for (int nq = 0; nq < NQ; ++nq) {
         if (nq > 0 && !wide) break;
-        float nm[2], cf[2];
+        float nm[2], nr[2], cf[2], vr[2];
         if (tail) {
 #pragma unroll
           for (int mt = 0; mt < 4; ++mt)
@@ -323,16 +311,22 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          nm[e] = fmaxf(m[nq][e], top * cf[e]);
+          top *= cf[e];
+          nm[e] = fmaxf(m[nq][e], top);
+          // (infinities of one sign give NaN, which the maximum passes over)
+          nr[e] = fmaxf(floorf(ref[nq][e] + (m[nq][e] - nm[e])), page_ref(top - nm[e], ve));
+          vr[e] = page_factor(ve, nr[e], (float)kPMargin) * vf;
         }
-        const bool moved = nm[0] != m[nq][0] || nm[1] != m[nq][1];
+        const bool moved = nm[0] != m[nq][0] || nm[1] != m[nq][1] || nr[0] != ref[nq][0] || nr[1] != ref[nq][1];
         if (__any_sync(0xffffffffu, moved)) {
           float c[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            c[e] = nm[e] == -INFINITY ? 1.0f : ex2(m[nq][e] - nm[e]);
+            const float d = m[nq][e] - nm[e], dr = ref[nq][e] - nr[e];
+            l[nq][e] *= nm[e] == -INFINITY ? 1.0f : ex2(d);
+            c[e] = nm[e] == -INFINITY ? 1.0f : ex2(d + dr);
             m[nq][e] = nm[e];
-            l[nq][e] *= c[e];
+            ref[nq][e] = nr[e];
           }
 #pragma unroll
           for (int ht = 0; ht < HT; ++ht)
@@ -341,13 +335,13 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float ref = nm[e] == -INFINITY ? 0.0f : nm[e];
+          const float base = nm[e] == -INFINITY ? 0.0f : nm[e];
 #pragma unroll
           for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float& x = s[nq][mt][2 * h + e];
-              x = ex2(fmaf(x, cf[e], -ref));
+              x = ex2(fmaf(x, cf[e], -base));
             }
         }
         if (tail) {  // a row gets none of the scales of a page that it does not see, NaN included
@@ -362,7 +356,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             l[nq][i & 1] += s[nq][mt][i];
-            s[nq][mt][i] *= vr;
+            s[nq][mt][i] *= vr[i & 1];
           }
         if (tail) {
 #pragma unroll
@@ -436,7 +430,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
         sum += __shfl_xor_sync(0xffffffffu, sum, 8);
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         const bool none = sum == 0.0f;
-        const float f = none ? 0.0f : vref * (1.0f / (1 << kPMargin)) / sum;
+        const float f = (1.0f / (1 << kPMargin)) / sum, g2 = pow2(ref[nq][e]);
         const float lse2 = none ? -INFINITY : m[nq][e] + log2f(sum);
         const int r = 8 * nq + 2 * t + e;
         if (r >= rows) continue;
@@ -445,8 +439,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
           uint16_t* dst = a.o + (int64_t)(sq.y + i) * a.so + h * D;
 #pragma unroll
           for (int ht = 0; ht < HT; ++ht) {
-            dst[16 * ht + g] = f32_to_bf16_bits(none ? 0.0f : o[nq][ht][e] * f);
-            dst[16 * ht + g + 8] = f32_to_bf16_bits(none ? 0.0f : o[nq][ht][2 + e] * f);
+            dst[16 * ht + g] = f32_to_bf16_bits(none ? 0.0f : o[nq][ht][e] * f * g2);
+            dst[16 * ht + g + 8] = f32_to_bf16_bits(none ? 0.0f : o[nq][ht][2 + e] * f * g2);
           }
           if (a.lse && g == 0) a.lse[(int64_t)h * a.T + sq.y + i] = lse2 * kLn2;
         } else {
@@ -454,8 +448,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
           float* dst = a.part_o + at * D;
 #pragma unroll
           for (int ht = 0; ht < HT; ++ht) {
-            dst[16 * ht + g] = none ? 0.0f : o[nq][ht][e] * f;
-            dst[16 * ht + g + 8] = none ? 0.0f : o[nq][ht][2 + e] * f;
+            dst[16 * ht + g] = none ? 0.0f : o[nq][ht][e] * f * g2;
+            dst[16 * ht + g + 8] = none ? 0.0f : o[nq][ht][2 + e] * f * g2;
           }
           if (g == 0) a.part_l[at] = lse2;
         }

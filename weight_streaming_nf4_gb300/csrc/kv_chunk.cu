@@ -16,7 +16,8 @@
 // A row is a thread's, so its maximum and sum need no exchange.  m moves only
 // when a row's maximum has grown by 2^8 or more (P stays below 2^15 in fp16):
 // then the softmax warps wait for the products before and rescale O in tensor
-// memory.  Keys' scales go into c, values' into P relative to the largest so far.
+// memory.  Keys' scales go into c, values' into P (page_ref in kv_plan.cuh, as lazy
+// as m).
 // A tile of up to 128 rows has both slots on the same rows, on steps of their
 // own (even, odd), joined at the end: without that the products would wait for
 // the softmax at every step.
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
   uint8_t* sr = smem + L::OFF_R;
   uint8_t* sv = smem + L::OFF_V;
   PageInfo* info = reinterpret_cast<PageInfo*>(smem + L::OFF_INFO);  // [2][kInfo]
-  float4* ml = reinterpret_cast<float4*>(smem + L::OFF_ML);          // slot 1's m, l, vref of each row
+  float4* ml = reinterpret_cast<float4*>(smem + L::OFF_ML);          // slot 1's m, l, oref of each row
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* k_full = bars;
   uint64_t* k_empty = k_full + KST;
@@ -656,7 +657,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
       return top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : a.sl2 * __uint_as_float((uint32_t)(e + 127) << 23);
     };
     bool have = false;  // a segment whose result is in O
-    float qs = 0.0f, m = 0.0f, l = 0.0f, vref = 0.0f;
+    float qs = 0.0f, m = 0.0f, l = 0.0f, oref = 0.0f;  // oref: of O, see page_ref
     for (;;) {
       // the next segment's rows go first: its first products run beside the epilogue of the one before
       Seg nx;
@@ -668,10 +669,10 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
         const bool active = !sg.dual || s < J, joined = sg.dual && J > 1;
         if (active && !wait(&o_done[2 * s + 1], sn - 1)) break;
         tc_fence_after();
-        float m1 = -INFINITY, l1 = 0.0f, v1 = 0.0f;
+        float m1 = -INFINITY, l1 = 0.0f, r1 = 0.0f;
         if (joined) {
           if (s == 1) {
-            ml[r] = make_float4(m, l, vref, 0.0f);
+            ml[r] = make_float4(m, l, oref, 0.0f);
             tc_fence_before();
           }
           __syncwarp();
@@ -684,7 +685,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
             const float4 y = ml[r];
             m1 = y.x;
             l1 = y.y;
-            v1 = y.z;
+            r1 = y.z;
           }
         }
         if (!(sg.dual && s == 1)) {
@@ -695,7 +696,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
           const float sum = l * e0 + l1 * e1;
           const bool none = sum == 0.0f;
           const float inv = none ? 0.0f : (1.0f / (1 << kChMargin)) / sum;
-          const float f0 = e0 * vref * inv, f1 = e1 * v1 * inv;
+          const float f0 = e0 * inv, f1 = e1 * inv, g0 = pow2(oref), g1 = pow2(r1);
           const float lse2 = none ? -INFINITY : mm + log2f(sum);
           uint16_t* dst = a.o + (int64_t)(sg.row0 + tok) * a.so + h * D;
           const int64_t part = (int64_t)sg.slot * kChunkRows + local;
@@ -710,8 +711,8 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
               float y[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                y[i] = none ? 0.0f : __uint_as_float(o0[i]) * f0;
-                if (joined && !none) y[i] += __uint_as_float(o1[i]) * f1;
+                y[i] = none ? 0.0f : __uint_as_float(o0[i]) * f0 * g0;
+                if (joined && !none) y[i] += __uint_as_float(o1[i]) * f1 * g1;
               }
               if (sg.slot >= 0) {
                 float* d = c.part_o + part * D + cc;
@@ -749,8 +750,8 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
       sg = nx;
       qs = qn;
       have = true;
-      m = -INFINITY;
-      l = vref = 0.0f;
+      m = oref = -INFINITY;
+      l = 0.0f;
       const int J1 = sg.s1 - sg.s0, mine = sg.dual ? r : s * kSlotRows + r;
       // tokens that the row sees; a row that is none (zero queries, nothing is stored) goes along with the last
       const int lim = mine < sg.rows ? sg.past + (sg.r0 + mine) / a.G + 1 : sg.past + sg.n;
@@ -771,16 +772,16 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
           float cf = qs * pi.ks;
           cf = cf < 1e-37f ? 1e-37f : cf;  // not below fp32's range: -inf * 0 is NaN
           const int vis = pi.page >= 0 ? lim - (2 * (sg.s0 + j) + half) * kPage : 0;  // of the page, seen
-          // The ordinary page: all rows see all of it, m stands and the scale of its P is a power of two, 2^e, which
-          // goes into the exponent.  The sum bounds the largest: at 2^kLag or less, m may stay.
-          const int e = (int)(__float_as_uint(pi.vs) >> 23) - (int)(__float_as_uint(vref) >> 23) + kChMargin;
-          const bool plain = ((__float_as_uint(pi.vs) | __float_as_uint(vref)) & 0x7fffffu) == 0u && e >= -20 &&
-                             e <= kChMargin && vis >= kPage && m > -INFINITY;
+          // The ordinary page: all rows see all of it, m and O's reference stand and the scale of its P is a power of
+          // two, 2^e, which goes into the exponent.  The sum bounds the largest: at 2^kLag or less, both may stay.
+          float vf;
+          const float ve = scale_parts(pi.vs, vf), e = ve - oref + (float)kChMargin;
+          const bool plain = vf == 1.0f && e >= -20.0f && e <= (float)(kChMargin + kLag) && vis >= kPage && m > -INFINITY;
           bool grown = false, rest = true;
           if (warp_all(plain)) {
             uint32_t p0[32], p1[32];
             uint32_t x0[32], x1[32];
-            const float shift = m - (float)e;
+            const float shift = m - e;
             const f32x2 c2 = pair(cf, cf), r2 = pair(-shift, -shift);
             f32x2 two[2] = {0ull, 0ull};  // two zeros each
             tmem_ld_32x32b_x32(t_v, x0);
@@ -791,8 +792,10 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
             weigh_plain(x1, c2, r2, two, p1);
             float sum, other;
             unpair(add2(two[0], two[1]), sum, other);
-            sum = (sum + other) * __uint_as_float((uint32_t)(127 - e) << 23);
-            grown = !(sum <= (float)(1 << kLag));
+            sum += other;
+            grown = !(sum <= (float)(1 << (kLag + kChMargin)));
+            sum *= pow2(-e);
+            grown |= !(sum <= (float)(1 << kLag));
             rest = !warp_all(!grown);
             if (!rest) {
               l += sum;
@@ -812,15 +815,16 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
               for (int i = 0; i < 16; ++i) top = cc + i < vis ? fmaxf(top, __uint_as_float(x[i])) : top;
             }
             top *= cf;
-            const bool up = top > m + (grown ? 0.0f : (float)kLag);
-            if (__any_sync(0xffffffffu, up || pi.vs > vref)) {
-              const float nm = up ? top : m;
-              const float nv = fmaxf(vref, pi.vs);  // a NaN scale is no reference
-              float f = nm == m ? 1.0f : ex2(m - nm);
-              l *= f;
-              f *= vref == nv ? 1.0f : vref / nv;
+            const float lag = grown ? 0.0f : (float)kLag;
+            const bool up = top > m + lag;
+            const float nm = up ? top : m, need = page_ref(top - nm, ve);
+            // (infinities of one sign give NaN, which the maximum passes over)
+            const float nr = up || need > oref + lag ? fmaxf(floorf(oref + (m - nm)), need) : oref;
+            if (__any_sync(0xffffffffu, up || nr != oref)) {
+              const float f = up || nr != oref ? ex2((m - nm) + (oref - nr)) : 1.0f;
+              if (up) l *= ex2(m - nm);
               m = nm;
-              vref = nv;
+              oref = nr;
               if (begun) {
                 // O of the halves before
                 if (!wait(&o_done[2 * s + (half ^ 1)], sn + half - 1)) break;
@@ -837,7 +841,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
               }
             }
             const float ref = m == -INFINITY ? 0.0f : m;
-            const float vr = (pi.vs == 0.0f ? 0.0f : pi.vs / vref) * (float)(1 << kChMargin);
+            const float vr = page_factor(ve, oref, (float)kChMargin) * vf;
 #pragma unroll 1
             for (int cc = 0; cc < kPage; cc += 16) {
               uint32_t x[16], p[16];

@@ -146,6 +146,26 @@ WS_DEVINL uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// O's reference.  A row's sum of exponentials goes by m, its scores' maximum; what it gathers from the values by
+// 2^(m + ref), ref a whole number: a page whose values' scale is 2^e enters with 2^(x - m) 2^(e - ref), so what counts
+// for fp16's range is the weight times the scale.  (By the largest scale alone, a page of no weight would push the
+// others out of fp16.)  `at` is the largest score of a page less m: the least reference that holds the page.  Pages whose
+// scores all lie 100 or more below m do not count.
+WS_DEVINL float page_ref(float at, float e) { return at > -100.0f ? ceilf(at + e) : -INFINITY; }
+// The factor of 2^(x - m) for a page of exponent e, 2^margin included.
+WS_DEVINL float page_factor(float e, float ref, float margin) { return e - ref > 110.0f ? 0.0f : ex2(e - ref + margin); }
+// A values' scale as f 2^e: f = 1 for the powers of two that append makes, NaN for NaN; other numbers (f in (1/2, 1))
+// serve too.
+WS_DEVINL float scale_parts(float s, float& f) {
+  const uint32_t b = __float_as_uint(s), rest = b & 0x007fffffu;
+  const bool normal = b - 0x00800000u < 0x7f000000u;
+  f = !normal ? s * 0x1p126f : rest ? __uint_as_float(rest | 0x3f000000u) : 1.0f;
+  return normal ? (float)((int)(b >> 23) - 127 + (rest != 0)) : -126.0f;
+}
+// 2^e for a whole number, brought into [-126, 127].
+WS_DEVINL float pow2(float e) {
+  return __uint_as_float((uint32_t)((int)fminf(fmaxf(e, -126.0f), 127.0f) + 127) << 23);
+}
 // Two probabilities as fp16 and what that leaves, also fp16: 2^-22 of themselves, or 2^-25 where that is more.
 WS_DEVINL void split_f16x2(float a, float b, uint32_t& hi, uint32_t& rest) {
   hi = pack_f16x2(a, b);
