@@ -556,8 +556,8 @@ ws_status ws_kv_append(const ws_kv_cache* cache, const ws_kv_plan* plan, const u
  * 2^-22 of itself, or by 2^-31 of that largest where this is more.  A page whose
  * probabilities are all below 2^-100 of the row's largest counts as none.
  * Queries are held in fp16 (sequences of up to 16 rows, n_heads / n_kv_heads of a
- * token) or as two e4m3 numbers: off by at most 2^-17.8 of their row's largest
- * element.  o overlaps nothing else.  No atomics: a given plan always gives the same
+ * token) or as the sum of an e4m3 and an e5m2 number: exact down to 2^-14 of their
+ * row's largest element, off by at most 2^-21.8 of it below.  o overlaps nothing else.  No atomics: a given plan always gives the same
  * bits.  Calls that may run at the same time need a workspace each (16-byte
  * aligned); a plan is only read. */
 ws_status ws_attention_kv_workspace_size(const ws_kv_plan* plan, size_t* bytes);

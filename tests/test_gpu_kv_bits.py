@@ -113,3 +113,19 @@ def test_a_page_counts_by_its_weight_times_its_scale(ops, form, pages):
     q = torch.randn(n, nkv * G, hd, generator=g) * 0.3
     q[..., 0] = hd ** 0.5
     check(ops, bf16(k), bf16(v), bf16(q), past, G)
+
+
+@pytest.mark.parametrize("form", FORMS, ids=[str(i) for i in range(len(FORMS))])
+@pytest.mark.parametrize("large", [2.0 ** 6, 448 * 2.0 ** -5, 2.0 ** 20])
+def test_small_elements_of_a_query_beside_a_large_one(ops, form, large):
+    """One channel of the queries is 2^11 to 2^13 times the others, and the keys hold nothing there: what counts are the
+    others' bits.  They are exact down to 2^-14 of the largest."""
+    nkv, G, hd, past, n = form
+    g = gen(sum(form) + 1)
+    k = torch.randn(past + n, nkv, hd, generator=g) * 2
+    k[..., 5] = 0
+    size = torch.rand(n, nkv * G, hd, generator=g) * 3 + 1  # 1 to 4, 2^-13 to 2^-11 of the largest
+    q = size * torch.sign(torch.randn(n, nkv * G, hd, generator=g)) * 2.0 ** -13 * large
+    q[..., 5] = large
+    scale = 2.0 ** 11 / large * hd ** -0.5
+    check(ops, bf16(k), bf16(torch.randn(past + n, nkv, hd, generator=g)), bf16(q), past, G, scale=scale)

@@ -5,9 +5,10 @@
 // A tile is 256 rows (new token, head of the group) of one kv head, two slots of
 // 128; a step is two pages.  For each step and slot
 //   S = Q K^T    kind::f8f6f4: the key codes as TMA brings them, nothing decoded.
-//                A row of Q enters as a power of two times hi + lo, two e4m3 numbers:
-//                all eight bits of bf16, down to 2^-10 of the row's largest
-//                element, and an absolute error of 2^-17.8 of it below; two
+//                A row of Q enters as a power of two times hi + lo, hi in e4m3 and
+//                lo in e5m2 (hi leaves at most eight of bf16's last places, either
+//                way, so three bits hold them, at e5m2's range): exact down to 2^-14
+//                of the row's largest element, off by 2^-21.8 of it below; two
 //                products at twice fp16's rate cost what one fp16 product does
 //   P = 2^(S c - m) as fp16 and, for every 16 tokens behind it, what fp16 leaves of it
 //                (2^-22 of P for 2^-11), in the same columns of tensor memory
@@ -262,6 +263,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
   constexpr int KST = L::KST, RST = L::RST, VST = L::VST;
   constexpr uint32_t TM_S = 0, TM_O = 2 * kStepTokens, TM_COLS = 512;
   constexpr uint32_t idS = (1u << 4) | ((kStepTokens >> 3) << 17) | ((kSlotRows >> 4) << 24);  // e4m3, e4m3, fp32
+  constexpr uint32_t idLo = idS | (1u << 7);                                                   // e5m2, e4m3, fp32
   constexpr uint32_t idO = (1u << 4) | ((D >> 3) << 17) | ((kSlotRows >> 4) << 24);            // fp16, fp16, fp32
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -513,7 +515,8 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                   for (int i = 0; i < D / 32; ++i)
-                    tc_mma_f8(d, q + ((part * L::QP + 32 * i) >> 4), k + ((32 * i) >> 4), idS, (part | i) ? 1u : 0u);
+                    tc_mma_f8(d, q + ((part * L::QP + 32 * i) >> 4), k + ((32 * i) >> 4), part ? idLo : idS,
+                              (part | i) ? 1u : 0u);
                 tc_commit(&s_full[s]);
                 if (ends) tc_commit(&k_empty[kst]);
               }
@@ -606,7 +609,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
       ok = poll(b, parity & 1u, abort_flag);
       return ok;
     };
-    // This thread's row of Q in two e4m3 parts (the products of the segment
+    // This thread's row of Q in its two parts (the products of the segment
     // before are through: they gave the last S).  Returns its factor of S.  Two
     // passes over the row, its maximum and its codes, in a rolled loop: code that
     // runs once a segment comes from far away, eight instructions in some 300 clocks.
@@ -646,7 +649,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
           const uint32_t ph = e4m3x2(f0, f1);
           e4m3x2_values(ph, g0, g1);
           hi[k >> 1] |= ph << (16 * (k & 1));
-          lo[k >> 1] |= e4m3x2(f0 - g0, f1 - g1) << (16 * (k & 1));
+          lo[k >> 1] |= e5m2x2(f0 - g0, f1 - g1) << (16 * (k & 1));
         }
         *reinterpret_cast<uint4*>(q_hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(q_hi + L::QP + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);

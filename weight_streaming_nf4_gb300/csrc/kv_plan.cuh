@@ -188,6 +188,12 @@ WS_DEVINL uint32_t e4m3x2(float a, float b) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(b), "f"(a));
   return h;
 }
+// The same for e5m2.
+WS_DEVINL uint32_t e5m2x2(float a, float b) {
+  uint16_t h;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(h) : "f"(b), "f"(a));
+  return h;
+}
 // The values of two codes (low byte first).
 WS_DEVINL void e4m3x2_values(uint32_t w, float& lo, float& hi) {
   asm("{\n .reg .b32 x;\n .reg .b16 l, h;\n cvt.rn.f16x2.e4m3x2 x, %2;\n mov.b32 {l, h}, x;\n"
