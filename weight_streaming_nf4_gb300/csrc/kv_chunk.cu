@@ -38,7 +38,8 @@
 // order of the shares.
 //
 // Warps: 0 loads, 1 issues the products, 2 and 3 decode values, 4-7 and 8-11 are the
-// slots' rows (three warps on each quarter of an SM: 168 registers a thread).  Every wait is bounded (see common.cuh).
+// slots' rows (three warps on each quarter of an SM: 168 registers a thread).  Every wait is bounded, by
+// kWaitLimitNs of common.cuh.
 #define WS_KV_TU 1
 #include <math.h>
 
@@ -205,22 +206,31 @@ WS_DEVINL bool elect_one() {
   asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
   return p != 0u;
 }
-// A wait of so many polls at most: a poll, a vote and a branch where the barrier
-// is through (mbar_wait's clock reading and the abort flag at every wait cost
-// more than the products they wait for).  A role that gave up is seen after a
-// thousand polls.  The answer is the warp's.
-constexpr uint32_t kPolls = 1u << 23;
+// A wait: a poll, a vote and a branch where the barrier is through (mbar_wait's
+// clock reading and the abort flag at every wait cost more than the products they
+// wait for).  Every lane sees the phase complete for itself, since a vote orders
+// no memory.  After 256 polls, and every 256 from then on, the clock and the other
+// roles are looked at: kWaitLimitNs later, or where a role gave up, so does this one.
+// The answer is the warp's.
+struct WaitLimit {
+  uint64_t t0 = 0;
+  WS_DEVINL bool over(const volatile uint32_t* abort_flag) {
+    const uint64_t now = globaltimer();
+    if (t0 == 0) t0 = now;
+    return *abort_flag != 0u || now - t0 > kWaitLimitNs;
+  }
+};
 WS_DEVINL bool poll(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort_flag) {
-  uint32_t it = 0;
-  while (!__any_sync(0xffffffffu, mbar_try_wait(bar, parity)))
-    if ((++it & 1023u) == 0u && __any_sync(0xffffffffu, it >= kPolls || *abort_flag != 0u)) return false;
+  WaitLimit limit;
+  for (uint32_t it = 1; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++it)
+    if ((it & 255u) == 0u && __any_sync(0xffffffffu, limit.over(abort_flag))) return false;
   return true;
 }
 // The same for one thread.
 WS_DEVINL bool poll_one(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort_flag) {
-  uint32_t it = 0;
-  while (!mbar_try_wait(bar, parity))
-    if ((++it & 1023u) == 0u && (it >= kPolls || *abort_flag != 0u)) return false;
+  WaitLimit limit;
+  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it)
+    if ((it & 255u) == 0u && limit.over(abort_flag)) return false;
   return true;
 }
 WS_DEVINL bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
