@@ -537,11 +537,16 @@ ws_status ws_kv_plan_init(const ws_kv_plan* plan, const int32_t* past, const int
  * two 2^e, e >= -126, with max|x| <= 448 2^e over its tokens; a page that goes on
  * keeps a scale no smaller than it has, and where it grows the older codes are
  * rounded again (which changes only those that become subnormal).  A value that is
- * not finite makes its page's scale for that head NaN (the codes that it would have
- * are zero), and with it what reads the page, until the page is begun anew.
- * Rounding is to nearest, ties to even.  A page that receives rows stands in one
- * place of one sequence's table (full pages may be shared); places behind the
- * appended rows stay as they were.  Tokens are taken back by a smaller past[s]. */
+ * not finite makes its page's scale for that head NaN (the codes that the call's rows
+ * would have there are zero), and with it what reads the page.  Rounding is to
+ * nearest, ties to even.  A page that receives rows stands in one place of one
+ * sequence's table (full pages may be shared); places behind the appended rows stay
+ * as they were.
+ * Tokens are taken back by a smaller past[s].  What they did to the scale of the last
+ * page that is kept stays: where it had grown, older values stay rounded to its codes
+ * (off by up to 2^-10 of the scale).  A page that turned NaN gets its earlier scale
+ * again when it goes on from the place where the call's rows began, or from one before;
+ * from one between the call's rows it stays NaN, until it is begun anew. */
 ws_status ws_kv_append(const ws_kv_cache* cache, const ws_kv_plan* plan, const uint16_t* k,
                        int64_t k_stride, const uint16_t* v, int64_t v_stride, ws_stream_t stream);
 /* Attention of the step's rows q [T, n_heads*head_dim] bf16 over the cache, which

@@ -264,6 +264,20 @@ WS_DEVINL float scale_for(uint32_t top) {
   const int e = (int)(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u);
   return __uint_as_float((uint32_t)(max(e, -126) + 127) << 23);
 }
+// A page that goes on from place `lo` and turns NaN keeps in the NaN what it was: the exponent of its scale, and lo, from
+// which on its codes are zero.  Going on from there or before, those that were not finite having been taken back, gives
+// the scale again.  Bits 14 to 21 tell such a NaN from others.
+constexpr uint32_t kNan = 0x7fc00000u, kNanMark = kNan | 0xa5u << 14;
+WS_DEVINL float nan_of(float scale, int lo) {
+  const uint32_t b = __float_as_uint(scale);
+  if (isnan(scale)) return scale;
+  return __uint_as_float(lo > 0 && (b & 0x807fffffu) == 0u ? kNanMark | (b >> 23) << 6 | (uint32_t)lo : kNan);
+}
+// The scale of a page that goes on from place lo.
+WS_DEVINL float scale_at(float scale, int lo) {
+  const uint32_t b = __float_as_uint(scale);
+  return (b & ~0x3fffu) == kNanMark && lo <= (int)(b & 63u) ? __uint_as_float((b >> 6 & 0xffu) << 23) : scale;
+}
 WS_DEVINL uint32_t max_abs(const uint4& w, uint32_t m) {
   m = __vmaxu2(m, w.x & 0x7fff7fffu);
   m = __vmaxu2(m, w.y & 0x7fff7fffu);
@@ -298,7 +312,8 @@ __global__ void __launch_bounds__(D) k_kv_append(const AppendArgs a) {
   uint8_t* pk = a.k + at * (kPage * D);
   uint8_t* pv = a.v + at * (kPage * D);
   float2* ps = reinterpret_cast<float2*>(a.scale) + at;
-  const float2 old = lo > 0 ? *ps : make_float2(0.0f, 0.0f);
+  float2 old = lo > 0 ? *ps : make_float2(0.0f, 0.0f);
+  old = make_float2(scale_at(old.x, lo), scale_at(old.y, lo));
 
   uint4 xk[8], xv[8];
   uint32_t mk = 0, mv = 0;
@@ -331,8 +346,14 @@ __global__ void __launch_bounds__(D) k_kv_append(const AppendArgs a) {
   }
   // a page that goes on keeps a scale no smaller than it had, NaN included
   float ks = scale_for(mk), vs = scale_for(mv);
-  if (lo > 0 && !(old.x <= ks) && !isnan(ks)) ks = old.x;
-  if (lo > 0 && !(old.y <= vs) && !isnan(vs)) vs = old.y;
+  if (isnan(ks))
+    ks = nan_of(old.x, lo);
+  else if (lo > 0 && !(old.x <= ks))
+    ks = old.x;
+  if (isnan(vs))
+    vs = nan_of(old.y, lo);
+  else if (lo > 0 && !(old.y <= vs))
+    vs = old.y;
   const bool grow_k = lo > 0 && ks > old.x, grow_v = lo > 0 && vs > old.y;
   // codes under a NaN scale are zero: a code that is NaN would reach rows that do not see it, as 0 * NaN
   const bool bad_k = isnan(ks), bad_v = isnan(vs);
