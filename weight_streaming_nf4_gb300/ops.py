@@ -832,16 +832,21 @@ def attention_bwd(q, k, v, o32, lse, dO, n_seq: int, head_dim: int, dq=None, dk=
 
 
 # ------------------------------------------------------------------------------ norm and rotary positions
-def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = None,
                      original: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
-                     attention_factor: float = None):
+                     attention_factor: float = None, scale: float = None):
     """Rotary frequencies (radians a position, a list of rot/2) and the factor of cosine and sine.
-    scaling, for contexts `factor` times as long as the `original` positions of training:
-    "none"; "linear": positions divided by the factor (Chen et al., 2023); "ntk": the base raised so
-    that the slowest pair turns a factor slower and the fastest as before; "yarn" (Peng et al., 2023):
+    scaling, for contexts `scale` times (`factor` is the same) as long as the `original` positions of
+    training: "none"; "linear": positions divided by it (Chen et al., 2023); "ntk": the base raised so
+    that the slowest pair turns so much slower and the fastest as before; "yarn" (Peng et al., 2023):
     pairs that turn more than beta_fast times within `original` positions stay, those below beta_slow
-    turns are slowed by the factor, a linear ramp between, and cosine and sine times attention_factor
-    (0.1 ln(factor) + 1 unless given)."""
+    turns are slowed by it, a linear ramp between, and cosine and sine times attention_factor
+    (0.1 ln(scale) + 1 unless given; 1 for the others)."""
+    _need(factor is None or scale is None, "scale and factor are the same")
+    factor = scale if factor is None else factor
+    _need(factor is not None or scaling == "none", "scaling needs scale, how many times as long the context is")
+    factor = 1.0 if factor is None else factor
+    _need(scaling != "none" or factor == 1.0, "scale without a scaling (linear, ntk or yarn)")
     _need(rot >= 16 and rot % 16 == 0, "rot: a multiple of 16")
     _need(math.isfinite(base) and base > 1.0 and math.isfinite(factor) and factor >= 1.0, "base > 1, factor >= 1")
     _need(scaling in ("none", "linear", "ntk", "yarn"), "scaling: none, linear, ntk or yarn")
@@ -879,17 +884,19 @@ class Rope:
 
 
 def rope(rot: int, base: float = 10000.0, interleaved=False, scaling="none", inv_freq=None, factor=None,
-         device="cuda", **kw) -> Rope:
-    """Rotary positions of the first `rot` elements of a head: rope_frequencies' (base, scaling, and in
-    kw scale, original, ...), or the caller's own inv_freq (rot/2) with the factor of cosine and sine."""
-    out = 1.0
+         device="cuda", attention_factor=None, **kw) -> Rope:
+    """Rotary positions of the first `rot` elements of a head: rope_frequencies' (base, scaling, attention_factor,
+    and in kw scale, original, beta_fast, beta_slow), or the caller's own inv_freq (rot/2), its scaling done, with
+    the factor of cosine and sine as attention_factor or factor."""
     if inv_freq is None:
-        kw["factor"] = kw.pop("scale", 1.0)
-        inv_freq, out = rope_frequencies(rot, base, scaling, **kw)
+        _need(factor is None, "the stretch is scale, the factor of cosine and sine attention_factor")
+        inv_freq, factor = rope_frequencies(rot, base, scaling, attention_factor=attention_factor, **kw)
     else:
         _need(not kw and scaling == "none", "inv_freq comes with its scaling done")
+        _need(factor is None or attention_factor is None, "factor and attention_factor are the same")
+        factor = attention_factor if factor is None else factor
     _need(len(inv_freq) == rot // 2 and rot % 2 == 0, "inv_freq: rot/2 of them")
-    return Rope(inv_freq, interleaved, out if factor is None else factor, device)
+    return Rope(inv_freq, interleaved, 1.0 if factor is None else factor, device)
 
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
