@@ -517,7 +517,9 @@ typedef struct {
  * rows beyond max_new, beyond T or beyond its table are left out (their output
  * rows stay as they were), and a page below 0 or from n_pages on holds nothing
  * (append drops its rows, attention passes over them).  A plan that is made again
- * in the same memory waits, in its stream, for the calls that read it. */
+ * in the same memory waits, in its stream, for the calls that read it.  Calls that find
+ * no plan of their struct's sizes in `data` (none was made there yet, or one for others)
+ * do nothing but set WS_DERR_BAD_CONFIG. */
 typedef struct {
   void* data;                   /* device, ws_kv_plan_size bytes */
   const int32_t* page_table;

@@ -34,7 +34,7 @@ static_assert((DERR_TIMEOUT_FULL | DERR_TIMEOUT_EMPTY | DERR_TIMEOUT_BFULL | DER
 
 #if defined(WS_GEMM_TU) || defined(WS_ATTN_TU) || defined(WS_FEW_TU) || defined(WS_KV_TU)
 // Device error word of a translation unit with spin-waits (the GEMM unit, the
-// attention unit, the few-row unit and the two cache-attention units each own
+// attention unit, the few-row unit and the three cache units each own
 // one); ws_device_error reads and clears them all.
 static __device__ uint32_t g_dev_error = 0;
 #define WS_HAS_WAITS 1

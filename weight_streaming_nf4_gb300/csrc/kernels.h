@@ -270,6 +270,7 @@ ws_status kv_check(const ws_kv_cache* c, const ws_kv_plan* p, KvShape* s);
 struct KvAttnArgs;
 size_t kv_chunk_bytes(const KvShape& s);  // of its partial results
 cudaError_t run_kv_chunk(const KvAttnArgs& a, const KvShape& s, void* partial, cudaStream_t st);
+cudaError_t kv_cache_read_and_clear_dev_error(uint32_t* flags);
 cudaError_t kv_read_and_clear_dev_error(uint32_t* flags);
 cudaError_t kv_chunk_read_and_clear_dev_error(uint32_t* flags);
 

@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
   __syncwarp();
   pdl_wait();
   pdl_launch_dependents();
-  if (*(volatile uint32_t*)&g_dev_error != 0u) return;
+  if (*(volatile uint32_t*)&g_dev_error != 0u || !plan_filled_or_say(a.plan, a.L.sig)) return;
 
   const KvHeader* hdr = reinterpret_cast<const KvHeader*>(a.plan);
   const int4* tiles = reinterpret_cast<const int4*>(a.plan + a.L.tile);
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) k_kv_join(const __grid_con
   const int warp = (int)warp_id(), lane = (int)lane_id();
   const bool few = sp.y <= kJoinFew;
   const int head = (int)blockIdx.y, r = few ? warp : (int)blockIdx.z, rows = sq.z * a.G;
-  if ((int)blockIdx.x >= n_split || (few ? blockIdx.z != 0 : r >= rows)) return;
+  if (!plan_filled(a.plan, a.L.sig) || (int)blockIdx.x >= n_split || (few ? blockIdx.z != 0 : r >= rows)) return;
   const int first = few ? 0 : warp, step = few ? 1 : kJoinWarps;
   const int64_t stride = (int64_t)a.nkv * kTileRows;
   const int64_t base = (int64_t)sp.x * stride + (int64_t)head * kTileRows + r;

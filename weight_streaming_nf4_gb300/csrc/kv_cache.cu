@@ -9,11 +9,20 @@
 // scale gains nothing over a power of two, and with powers of two the codes of
 // a page whose scale grows keep their values exactly but for those that become
 // subnormal: appending token by token is as good as all at once.
+#define WS_KV_TU 1
 #include <math.h>
 
 #include "kv_plan.cuh"
 
 namespace ws {
+
+cudaError_t kv_cache_read_and_clear_dev_error(uint32_t* flags) {
+  cudaError_t e = cudaMemcpyFromSymbol(flags, g_dev_error, sizeof(uint32_t));
+  if (e != cudaSuccess) return e;
+  const uint32_t zero = 0;
+  return cudaMemcpyToSymbol(g_dev_error, &zero, sizeof(uint32_t));
+}
+
 namespace {
 
 constexpr int kPlanThreads = 1024;
@@ -231,6 +240,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const KvPlanArgs a) {
     hdr->c_steps = Wc;
     hdr->c_units = Uc;
     hdr->c_split = n_cut;
+    hdr->sig[0] = a.L.sig[0];
+    hdr->sig[1] = a.L.sig[1];
   }
 }
 
@@ -240,6 +251,7 @@ struct AppendArgs {
   float* scale;
   const uint8_t* plan;
   size_t off_append;
+  uint32_t sig[2];
   const uint16_t *xk, *xv;
   int64_t sk, sv, n_pages;
   int nkv;
@@ -302,6 +314,7 @@ __global__ void __launch_bounds__(D) k_kv_append(const AppendArgs a) {
   __shared__ uint32_t top[2][D / 32];
   pdl_wait();
   pdl_launch_dependents();
+  if (!plan_filled_or_say(a.plan, a.sig)) return;
   const int item = (int)blockIdx.x / a.nkv, head = (int)blockIdx.x % a.nkv;
   if (item >= reinterpret_cast<const KvHeader*>(a.plan)->n_append) return;
   const int4 it = reinterpret_cast<const int4*>(a.plan + a.off_append)[item];
@@ -497,6 +510,8 @@ ws_status ws_kv_append(const ws_kv_cache* cache, const ws_kv_plan* plan, const u
   a.scale = cache->scale;
   a.plan = static_cast<const uint8_t*>(plan->data);
   a.off_append = L.append;
+  a.sig[0] = L.sig[0];
+  a.sig[1] = L.sig[1];
   a.xk = k;
   a.xv = v;
   a.sk = k_stride;

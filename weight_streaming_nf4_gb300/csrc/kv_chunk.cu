@@ -107,7 +107,7 @@ struct Share {
   const int4 *tiles, *seqs, *units;
   int64_t begin, end, at;
   int W, u, tile, head, nkv, G;
-  WS_DEVINL Share(const ChunkArgs& c, int unit) {
+  WS_DEVINL Share(const ChunkArgs& c, int unit, bool run) {
     const KvHeader* h = reinterpret_cast<const KvHeader*>(c.a.plan);
     tiles = reinterpret_cast<const int4*>(c.a.plan + c.a.L.c_tile);
     seqs = reinterpret_cast<const int4*>(c.a.plan + c.a.L.seq);
@@ -118,7 +118,7 @@ struct Share {
     W = h->c_steps;
     const int U = h->c_units;
     begin = end = at = 0;
-    if (u >= U) return;
+    if (!run || u >= U) return;
     const int4 b = units[u], e = units[u + 1];
     tile = b.x;
     head = b.y;
@@ -344,8 +344,8 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
   pdl_launch_dependents();
-  const bool run = *skip_flag == 0u;
-  Share share(c, (int)blockIdx.x);
+  const bool run = *skip_flag == 0u && plan_filled_or_say(c.a.plan, c.a.L.sig);
+  Share share(c, (int)blockIdx.x, run);
   const KvAttnArgs& a = c.a;
   Seg sg = {};
   // Steps are numbered through the share; step n's pages are 2 n and 2 n + 1 of
@@ -908,7 +908,7 @@ __global__ void __launch_bounds__(kChJoinWarps * 32) k_kv_chunk_join(const __gri
   const int4 sp = entry[0], sq = entry[1];
   const int lane = (int)lane_id(), rows = min(kChunkRows, sq.z * a.G - sp.z);
   const int first = ((int)blockIdx.y * kChJoinWarps + (int)warp_id()) * kChJoinRows;
-  if ((int)blockIdx.x >= n_split || first >= rows) return;
+  if (!plan_filled(a.plan, a.L.sig) || (int)blockIdx.x >= n_split || first >= rows) return;
   const int64_t base = (int64_t)sp.x * kChunkRows;
   float m[kChJoinRows], sum[kChJoinRows], acc[kChJoinRows][E];
 #pragma unroll

@@ -36,7 +36,8 @@ struct KvHeader {
   int c_steps;   // sum of their steps
   int c_units;   // shares of n_kv_heads times those, equal in cost, one CTA each
   int c_split;   // (head, tile) pairs cut by a unit's end
-  int pad[7];
+  uint32_t sig[2];  // of the sizes that it was made for
+  int pad[5];
 };
 // int4 arrays:
 //   seq     {tokens before the call, first row of q, new tokens, 0}
@@ -54,6 +55,7 @@ struct KvHeader {
 struct KvLayout {
   size_t seq, pre, append, tile, split, unit, c_tile, c_split, c_unit, bytes;  // byte offsets
   int64_t max_append, max_tiles, max_units, c_max_tiles, c_max_units;
+  uint32_t sig[2];
 };
 
 struct KvShape {
@@ -93,8 +95,30 @@ inline KvLayout kv_layout(const KvShape& s) {
   L.c_split = take(L.c_max_units * 32);
   L.c_unit = take((L.c_max_units + 1) * 16);
   L.bytes = o;
+  uint64_t h = 0x9e3779b97f4a7c15ull;  // the sizes, mixed: no zeros, no other plan's
+  for (const int64_t x : {s.T, (int64_t)s.n_seq, (int64_t)s.max_pages, (int64_t)s.max_new, (int64_t)s.nh, (int64_t)s.nkv,
+                          (int64_t)s.hd, (int64_t)device_sm_count()}) {
+    h = (h ^ (uint64_t)x) * 0xbf58476d1ce4e5b9ull;
+    h ^= h >> 31;
+  }
+  L.sig[0] = (uint32_t)h | 1u;
+  L.sig[1] = (uint32_t)(h >> 32);
   return L;
 }
+// True where the memory holds a plan of these sizes.  What reads a plan asks first: memory that was never filled, or for
+// other sizes, would lead it anywhere.
+WS_DEVINL bool plan_filled(const uint8_t* plan, const uint32_t (&sig)[2]) {
+  const KvHeader* h = reinterpret_cast<const KvHeader*>(plan);
+  return h->sig[0] == sig[0] && h->sig[1] == sig[1];
+}
+#ifdef WS_HAS_WAITS
+// The same for a kernel; one that has to leave says so in the device error word.
+WS_DEVINL bool plan_filled_or_say(const uint8_t* plan, const uint32_t (&sig)[2]) {
+  const bool ok = plan_filled(plan, sig);
+  if (!ok && threadIdx.x == 0) atomicOr(&g_dev_error, DERR_BAD_CONFIG);
+  return ok;
+}
+#endif
 
 // Unit u has places [unit_start(u), unit_start(u + 1)) of W; unit_of is its inverse.
 __host__ __device__ inline int64_t unit_start(int u, int64_t W, int U) { return u * W / U; }

@@ -81,6 +81,10 @@ cudaError_t read_and_clear_dev_error(uint32_t* flags) {
   e = kv_read_and_clear_dev_error(&kv);
   *flags |= kv;
   if (e != cudaSuccess) return e;
+  uint32_t cache = 0;
+  e = kv_cache_read_and_clear_dev_error(&cache);
+  *flags |= cache;
+  if (e != cudaSuccess) return e;
   uint32_t chunk = 0;
   e = kv_chunk_read_and_clear_dev_error(&chunk);
   *flags |= chunk;
