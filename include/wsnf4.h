@@ -529,7 +529,7 @@ typedef struct {
   int32_t max_new;              /* the most rows that a sequence may bring: 1 .. T */
   int32_t n_heads, n_kv_heads, head_dim;  /* n_heads <= 1024, a multiple of n_kv_heads <= 256 */
 } ws_kv_plan;
-/* Where max_new G > 16, G = n_heads / n_kv_heads: (T G / 256 + min(n_seq, T)) (max_pages / 2 + 7) stays
+/* Where max_new G > 16, G = n_heads / n_kv_heads: (T G / 256 + min(n_seq, T)) (max_pages / 2 + 6) stays
  * below 2^31, and n_kv_heads times it below 2^36; WS_ERR_SHAPE far beyond. */
 ws_status ws_kv_plan_size(const ws_kv_plan* plan, size_t* bytes);
 ws_status ws_kv_plan_init(const ws_kv_plan* plan, const int32_t* past, const int32_t* row_start,

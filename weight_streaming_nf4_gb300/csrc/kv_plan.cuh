@@ -18,11 +18,12 @@ constexpr int kChunkRows = 256;  // rows of a tile of the chunk kernel, which ha
 constexpr int kChunkMinSteps = 12;  // steps (two pages) of a share of the chunk kernel's work, at least
 // What beginning a tile costs, in steps: a share's length counts it, so that shares with many beginnings end with the
 // others.  Tiles of up to half the rows, whose two slots share their steps, have an entry of their own, and their
-// steps count half.  In us: two prompts (1800 + 1519 rows of 40 + 8 heads behind 6000 and 3392 tokens), a step with three
-// prompts of 485 to 700 rows among 30 single ones (28 + 4 heads), 24 sequences of 4 and of 20 rows (40 + 8 heads; 240k
-// and 60k tokens in all), and with 14 + 2 heads of 64 the prompts and the mixed step again: 10 and 4 410, 171, 158, 71,
-// 135, 85; 8 and 3 407, 171, 156, 69, 134, 81; 6 and 3 402, 171, 156, 69, 136, 79; 4 and 2 400, 173, 159, 74, 133, 79.
-constexpr int kChunkTileCost = 6, kChunkHalfTileCost = 3;
+// steps count half.  In us, four draws of inputs in turn: two prompts (1800 + 1519 rows of 40 + 8 heads behind 6000 and
+// 3392 tokens), a step with three prompts of 485 to 700 rows among 30 single ones (28 + 4 heads), 24 sequences of 4 and
+// of 20 rows (40 + 8 heads; 240k and 60k tokens in all), and with 14 + 2 heads of 64 the prompts and the mixed step again:
+// 10 and 4 421, 165, 156, 72, 137, 89; 8 and 3 418, 164, 156, 70, 136, 85; 5 and 3 413, 164, 156, 70, 136, 83; 4 and 2
+// 414, 165, 159, 75, 135, 83.
+constexpr int kChunkTileCost = 5, kChunkHalfTileCost = 3;
 static_assert(kChunkMinSteps > kChunkTileCost, "every share has a step");
 
 // Rows are a sequence's (new token, query head of one kv head) pairs, token by
