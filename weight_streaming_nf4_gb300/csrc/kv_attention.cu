@@ -7,12 +7,12 @@
 //
 // Decoding rows (k_kv_decode; sequences of more than kTileRows rows go to
 // kv_chunk.cu: a second tile of 16 would read the codes again.  24 sequences of
-// 16000 tokens and 40 + 8 heads take 104 us with 15 rows each here, 134 with 20
-// there).  Bound by memory: each code is read once.  One
+// 2400 to 16000 tokens, 240k in all, 40 + 8 heads: 116 us with 15 rows each here,
+// 157 with 20 there).  Bound by memory: each code is read once.  One
 // warp has a contiguous share of the pages of all 16-row tiles (equal shares,
 // so ragged batches fill the device), copies a page's keys and values (8 KB
 // each at D = 128) into shared memory while the ones before are used, and joins
-// its pages with a running maximum and sum.  Both products are the small-tile
+// its pages with a running maximum and sum (Milakov and Gimelshein, 2018).  Both products are the small-tile
 // tensor operation m16n8k16 in fp16, which holds e4m3 codes exactly:
 //   S^T = K Q^T  (16 tokens x 8 rows),   O^T += V^T P^T  (16 elements x 8 rows).
 // The contraction may run in any order, so a thread takes 32 (D = 64: 16)
@@ -27,10 +27,12 @@
 // The second product's operations double; the pages' way stays what bounds it.
 // Tiles cut by a share's end are joined by k_kv_join, in a fixed order.
 // Where no tile of the plan can have more than eight rows, NQ = 1 leaves the
-// second half of the operands out (188 registers for 244).
-// 48 sequences of 16000 tokens, 40 + 8 heads of 128: 162 us with the join, 6.1
-// TB/s.  Two of 130000, 28 + 4 heads, two new tokens each: 53 us, 4.1 TB/s, as a
-// share is 13 pages: start, ramp and partial results are a third.
+// second half of the operands out (188 registers for 252).
+// 48 sequences of 2400 to 16000 tokens, 479k in all, 40 + 8 heads of 128: 158 us
+// with the join, 6.2 TB/s (0.92 of the copy rate).  Two of 130000 and 85000, 28 + 4
+// heads, two new tokens each: 60 us, 3.6 TB/s: a share is 11 pages, so start, ramp
+// and partial results are a quarter, and 14 rows of P in two parts take four tensor
+// operations where up to eight rows in one part take one (53 us with one part).
 #define WS_KV_TU 1
 #include <math.h>
 
@@ -458,13 +460,13 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
 }
 
 // Cut tiles: row r's pieces o_i with log2-sums l_i are sum 2^(l_i) o_i / sum 2^(l_i).
-// Few pieces (decode batches): a warp a row, all rows in one CTA.  Many (two
-// contexts of 130000 tokens leave 300 a row): a CTA a row, its warps taking every
+// Few pieces (decode batches): a warp a row, all rows in one CTA.  Many (contexts of
+// 130000 and 85000 tokens leave 185 and 121 a row): a CTA a row, its warps taking every
 // sixteenth piece.  Sums have a fixed order.  Bound by latency: what it takes to
 // know where to look is one trip to memory, and CTAs that find nothing there leave
 // the sooner the more fit on an SM.  Four pieces in flight a warp and two CTAs an
-// SM: 48 contexts of 16000 tokens, 40 + 8 heads, take 162 us in all, two contexts
-// of 130000 54; eight and one CTA 166 and 53.
+// SM: the 48 sequences above take 158 us in all, the two 60.5; eight and one CTA 162
+// and 59.5.
 constexpr int kJoinWarps = 16, kJoinFlight = 4, kJoinFew = 16;
 static_assert(kJoinWarps == kTileRows, "a warp a row");
 template <int D>

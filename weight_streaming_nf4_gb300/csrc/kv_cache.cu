@@ -78,8 +78,8 @@ WS_DEVINL int last_at_most(int n, int x, F at) {
 // One CTA.  Everything read from the caller's arrays is brought into range
 // here, and the other kernels go by the plan alone: tokens beyond the table or
 // beyond max_new, rows beyond T and pages that are none cannot be reached.
-// Bound by latency (prefix sums and searches, one after another): 8 us for 1 to
-// 48 sequences, 11 for 33 with chunks among them, once a step for all layers.
+// Bound by latency (prefix sums and searches, one after another): 8 to 11 us for 1
+// to 48 sequences, 11 to 12 for 33 with chunks among them, once a step for all layers.
 __global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const KvPlanArgs a) {
   pdl_wait();
   pdl_launch_dependents();
@@ -305,8 +305,8 @@ WS_DEVINL float elem(const uint4& w, int i) {  // element i of eight
 // of the page's tokens 8t .. 8t + 7: rows come in 16-byte pieces, key codes
 // leave in 8-byte pieces of whole rows, value codes are turned round through
 // shared memory.  Bound by memory for prompts (3 bytes an element: eight prompts,
-// 22600 rows of 8 heads of 128, in 26 us, 5.3 TB/s), by the latency of two
-// dependent loads and the launch for single tokens (48 rows: 5 us).
+// 22600 rows of 8 heads of 128, in 27 us, 5.2 TB/s), by the latency of three
+// dependent loads and the launch for single tokens (48 rows: 6 us in a stream).
 template <int D>
 __global__ void __launch_bounds__(D) k_kv_append(const AppendArgs a) {
   constexpr int C = D / 8;  // pieces of a row; D = C * 8 threads

@@ -15,7 +15,9 @@
 //   O += P V     kind::f16, two products, A from tensor memory, V decoded to fp16
 //                (exact) by two warps, once for both slots
 // A row is a thread's, so its maximum and sum need no exchange.  m moves only
-// when a row's maximum has grown by 2^8 or more (P stays below 2^15 in fp16):
+// when a row's maximum has grown by 2^8 or more, as far as fp16 holds P (that the
+// maximum may lag, and that two tiles of queries take turns on the tensor cores,
+// are known from published attention algorithms; Shah et al., 2024, for the latter):
 // then the softmax warps wait for the products before and rescale O in tensor
 // memory.  Keys' scales go into c, values' into P (page_ref in kv_plan.cuh, as lazy
 // as m).
@@ -23,16 +25,20 @@
 // own (even, odd), joined at the end: without that the products would wait for
 // the softmax at every step.
 //
-// Two prompts, 2900 rows of 40 + 8 heads behind some 6000 tokens, take 316 us
-// (1.2 PFLOP/s; the tensor pipe is busy half of the time).  A step takes some
-// 3300 clocks where its products are 2048.  Neither fewer products (an eighth of
-// them: 0.88 of the time), nor a softmax without exponentials (0.99), nor values
-// that are not decoded (1.0) shortens it much: it is the chain of a slot's step,
-// S to softmax to P V to the next S, over barriers, with the two slots' chains
-// beside each other; a third does not fit in tensor memory at D = 128.  Halves of
-// S as products of their own (N = 64) took 1.15 of the time, two warps that issue
-// or a turn taken by the slots were no faster.  The rest is what a tile's
-// beginning costs (queries staged, O written: some eight steps).
+// Two prompts, 1800 + 1519 rows of 40 + 8 heads behind 6000 and 3392 tokens, take
+// 413 us (0.93 PFLOP/s of the definition's products, three of which are made for
+// two; the tensor pipe is busy 0.66 of the time).  A step takes some 4200 clocks
+// where its products are 3072: it is the chain of a slot's step, S to softmax to
+// P V to the next S, over barriers, with the two slots' chains beside each other; a
+// third does not fit in tensor memory at D = 128.  P's second part takes a quarter
+// (without its products 0.88 of the time, without making it 0.96).  With P in one
+// part, 3300 clocks for 2048, neither fewer products (an eighth of them: 0.88),
+// nor a softmax without exponentials (0.99), nor values that are not decoded (1.0)
+// shortened it much; halves of S as products of their own (N = 64) took 1.15, two
+// warps that issue or a turn taken by the slots were no faster.  The rest is what a
+// tile's beginning costs (queries staged, O written: some five steps).  With 14 + 2
+// heads of 64 the two prompts take 136 us, 0.49 PFLOP/s: half the products on the
+// same chain, the tensor pipe busy 0.36 of the time.
 // Shares of equal cost, over all heads, one CTA an SM: a share that begins or
 // ends inside a tile leaves a partial result, joined by k_kv_chunk_join in the
 // order of the shares.
@@ -896,8 +902,8 @@ __global__ void __launch_bounds__(kChThreads, 1) k_kv_chunk(const __grid_constan
 }
 
 // Cut (head, tile) pairs: a row's pieces joined in the order of the shares, two
-// rows a warp at a time, two pieces each in flight (two prompts, 2900 rows: 316 us
-// in all, with four rows a warp 318, with eight 321).
+// rows a warp at a time, two pieces each in flight (the two prompts above: 413 us in
+// all, with four rows a warp as long, with eight 425).
 constexpr int kChJoinWarps = 8, kChJoinRows = 2;
 template <int D>
 __global__ void __launch_bounds__(kChJoinWarps * 32) k_kv_chunk_join(const __grid_constant__ ChunkArgs c) {
