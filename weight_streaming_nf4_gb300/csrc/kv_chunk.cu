@@ -28,7 +28,7 @@
 // Two prompts, 1800 + 1519 rows of 40 + 8 heads behind 6000 and 3392 tokens, take
 // 413 us (0.93 PFLOP/s of the definition's products, three of which are made for
 // two; the tensor pipe is busy 0.66 of the time).  A step takes some 4200 clocks
-// where its products are 3072: it is the chain of a slot's step, S to softmax to
+// where its products are 3.1 thousand: it is the chain of a slot's step, S to softmax to
 // P V to the next S, over barriers, with the two slots' chains beside each other; a
 // third does not fit in tensor memory at D = 128.  P's second part takes a quarter
 // (without its products 0.88 of the time, without making it 0.96).  With P in one
