@@ -561,7 +561,7 @@ ws_status ws_kv_append(const ws_kv_cache* cache, const ws_kv_plan* plan, const u
  * fp32; a probability times the scale of its page's values enters the second
  * product, relative to the row's largest such product, as two fp16 numbers: off by
  * 2^-22 of itself, or by 2^-31 of that largest where this is more.  A page whose
- * probabilities are all below 2^-100 of the row's largest counts as none.
+ * probabilities are all below 2^-100 of the row's largest may count as none.
  * Queries are held in fp16 (sequences of up to 16 rows, n_heads / n_kv_heads of a
  * token) or as the sum of an e4m3 and an e5m2 number: exact down to 2^-14 of their
  * row's largest element, off by at most 2^-21.8 of it below.  o overlaps nothing else.  No atomics: a given plan always gives the same
