@@ -564,9 +564,11 @@ ws_status ws_kv_append(const ws_kv_cache* cache, const ws_kv_plan* plan, const u
  * probabilities are all below 2^-100 of the row's largest may count as none.
  * Queries are held in fp16 (sequences of up to 16 rows, n_heads / n_kv_heads of a
  * token) or as the sum of an e4m3 and an e5m2 number: exact down to 2^-14 of their
- * row's largest element, off by at most 2^-21.8 of it below.  o overlaps nothing else.  No atomics: a given plan always gives the same
- * bits.  Calls that may run at the same time need a workspace each (16-byte
- * aligned); a plan is only read. */
+ * row's largest element, off by at most 2^-21.8 of it below.  Sums of sequences of
+ * more rows are the tensor cores' own: every addition of 16 products cuts off up to
+ * 2^-23 of the sum (some 2^-16 of a result over 10000 tokens).  o overlaps nothing
+ * else.  No atomics: a given plan always gives the same bits.  Calls that may run at
+ * the same time need a workspace each (16-byte aligned); a plan is only read. */
 ws_status ws_attention_kv_workspace_size(const ws_kv_plan* plan, size_t* bytes);
 ws_status ws_attention_kv(const ws_kv_cache* cache, const ws_kv_plan* plan, const uint16_t* q,
                           int64_t q_stride, float scale, uint16_t* o, int64_t o_stride, float* lse,

@@ -129,3 +129,45 @@ def test_small_elements_of_a_query_beside_a_large_one(ops, form, large):
     q[..., 5] = large
     scale = 2.0 ** 11 / large * hd ** -0.5
     check(ops, bf16(k), bf16(torch.randn(past + n, nkv, hd, generator=g)), bf16(q), past, G, scale=scale)
+
+
+@pytest.mark.parametrize("hd,G,n", [(64, 2, 1), (64, 8, 2), (128, 2, 1), (128, 4, 4)], ids=["64-8rows", "64-16rows", "128-8rows", "128-16rows"])
+def test_long_sums_of_single_tokens_are_rounded_not_cut_off(ops, hd, G, n):
+    """Shares of 128 pages whose first half has positive values and whose second half negative ones: a sum rises, and falls
+    to nearly nothing, so the result shows what its additions lose.  The tensor cores' additions cut off: in a page eight,
+    each by up to 2^-23 of the page's sum, 2^-20 of the sizes in all; pages are added in fp32, rounded to nearest, 128
+    roundings of up to 2^-24 of half the sizes and of either sign, 2^-22 in the mean.  2^-19 of the sizes (root mean
+    square), and the rounding to bf16; additions that cut off all the way lose 1024 times up to 2^-24 of a quarter in the
+    mean, 2^-16."""
+    nkv, share = 8, 128
+    units = torch.cuda.get_device_properties(0).multi_processor_count * (8 if hd == 128 else 12) // nkv
+    pages = units * share
+    g = torch.Generator(DEV).manual_seed(hd + n)
+    cache = ops.kv_cache(pages, nkv, hd)
+    cache.k.view(torch.uint8).copy_(torch.randint(0, 0x38, cache.k.shape, dtype=torch.uint8, generator=g, device=DEV))  # 0 to 1
+    cache.v.view(torch.uint8).copy_(torch.randint(0x30, 0x40, cache.v.shape, dtype=torch.uint8, generator=g, device=DEV))  # 1/2 to 2
+    sign = (torch.arange(pages, device=DEV) % share >= share // 2).to(torch.uint8) << 7
+    cache.v.view(torch.uint8).bitwise_or_(sign[:, None, None, None])
+    cache.scale.fill_(1.0)
+    total = pages * PAGE
+    q = (torch.randn(n, nkv * G, hd, generator=g, device=DEV) * 0.5).bfloat16()
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
+    plan = ops.kv_plan(ints([total - n]), ints([0, n]), table, n, n, nkv * G, nkv, hd)
+    o, lse = ops.attention_kv(q.view(n, -1), cache, plan, want_lse=True)
+    torch.cuda.synchronize()
+    assert ops.device_error() == 0
+    err = own = size = 0.0
+    for h in (0, nkv - 1):
+        k, v = cache.k[:, h].double().view(total, hd), cache.v[:, h].double().transpose(1, 2).reshape(total, hd)
+        x = q.view(n, nkv, G, hd)[:, h].double().reshape(n * G, hd)
+        s = x @ k.t() * hd ** -0.5
+        s.view(n, G, total)[:, :, total - n:].masked_fill_(torch.ones(n, n, dtype=torch.bool, device=DEV).triu(1)[:, None], -math.inf)
+        ref = torch.logsumexp(s, 1)
+        p = s.softmax(1)
+        want = p @ v
+        got = o.view(n, nkv, G, hd)[:, h].double().reshape(n * G, hd)
+        err, own, size = err + (got - want).square().sum().item(), own + want.square().sum().item(), size + (p @ v.abs()).square().sum().item()
+        got = lse.view(nkv, G, n)[h].t().reshape(-1).double()
+        assert ((got - ref).abs() <= 2.0 ** -19 + 2.0 ** -22 * ref.abs()).all()
+    assert own < 2.0 ** -12 * size  # it does cancel
+    assert err ** 0.5 <= 2.0 ** -9 * own ** 0.5 + 2.0 ** -19 * size ** 0.5, (err / size) ** 0.5

@@ -7,7 +7,7 @@
 //
 // Decoding rows (k_kv_decode; sequences of more than kTileRows rows go to
 // kv_chunk.cu: a second tile of 16 would read the codes again.  24 sequences of
-// 2400 to 16000 tokens, 240k in all, 40 + 8 heads: 116 us with 15 rows each here,
+// 2400 to 16000 tokens, 240k in all, 40 + 8 heads: 123 us with 15 rows each here,
 // 157 with 20 there).  Bound by memory: each code is read once.  One
 // warp has a contiguous share of the pages of all 16-row tiles (equal shares,
 // so ragged batches fill the device), copies a page's keys and values (8 KB
@@ -25,14 +25,20 @@
 // P enters as two fp16 numbers, what one leaves being the other: 2^-22 of itself
 // for the 2^-11 of one, which is what results of terms that cancel are off by.
 // The second product's operations double; the pages' way stays what bounds it.
+// A page's products are summed by themselves and then added to O: the tensor
+// cores' additions cut off instead of rounding, up to 2^-23 of the sum each time,
+// and over a share of 128 pages would lose 2^-16 of its sizes, always the same way.
+// (Free for up to eight rows; for sixteen, whose registers are all in use, 4 us of
+// the 64 below.)
 // Tiles cut by a share's end are joined by k_kv_join, in a fixed order.
 // Where no tile of the plan can have more than eight rows, NQ = 1 leaves the
-// second half of the operands out (188 registers for 252).
+// second half of the operands out (188 registers for 255).
 // 48 sequences of 2400 to 16000 tokens, 479k in all, 40 + 8 heads of 128: 158 us
 // with the join, 6.2 TB/s (0.92 of the copy rate).  Two of 130000 and 85000, 28 + 4
-// heads, two new tokens each: 60 us, 3.6 TB/s: a share is 11 pages, so start, ramp
+// heads, two new tokens each: 64 us, 3.4 TB/s: a share is 11 pages, so start, ramp
 // and partial results are a quarter, and 14 rows of P in two parts take four tensor
-// operations where up to eight rows in one part take one (53 us with one part).
+// operations where up to eight rows in one part take one (53 us with one part, summed
+// in the tensor cores).
 #define WS_KV_TU 1
 #include <math.h>
 
@@ -189,7 +195,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
   bool fresh = true;
 
   uint32_t bq[NQ][KS][2];          // Q^T operands
-  float o[NQ][HT][4];              // O^T: elements 16 ht + g (+ 8), rows 8 nq + 2t (+ 1)
+  float o[NQ][HT][4];              // O^T, sums over the pages so far: elements 16 ht + g (+ 8), rows 8 nq + 2t (+ 1)
   float m[NQ][2], l[NQ][2], ref[NQ][2], qs[NQ][2];
   int lim[NQ][2];                  // tokens each row sees
   int rows = 0, kv_end = 0, first_lim = 0;
@@ -396,6 +402,11 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
             x1[i] &= keep;
           }
         }
+        float add[NQ][4];
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) add[nq][e] = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t a0, a1, a2, a3;
@@ -404,10 +415,14 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
 #pragma unroll
           for (int nq = 0; nq < NQ; ++nq)
             if (nq == 0 || wide) {
-              mma_f16(o[nq][ht], a0, a1, a2, a3, bp[nq][i][0], bp[nq][i][1]);
-              mma_f16(o[nq][ht], a0, a1, a2, a3, br[nq][i][0], br[nq][i][1]);
+              mma_f16(add[nq], a0, a1, a2, a3, bp[nq][i][0], bp[nq][i][1]);
+              mma_f16(add[nq], a0, a1, a2, a3, br[nq][i][0], br[nq][i][1]);
             }
         }
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nq][ht][e] += add[nq][e];
       }
       __syncwarp();
       next_place();
@@ -465,8 +480,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeSmem<D>::CTAS) k_kv_d
 // sixteenth piece.  Sums have a fixed order.  Bound by latency: what it takes to
 // know where to look is one trip to memory, and CTAs that find nothing there leave
 // the sooner the more fit on an SM.  Four pieces in flight a warp and two CTAs an
-// SM: the 48 sequences above take 158 us in all, the two 60.5; eight and one CTA 162
-// and 59.5.
+// SM: the 48 sequences above take 158 us in all, the two 64; eight and one CTA 162
+// and 63.
 constexpr int kJoinWarps = 16, kJoinFlight = 4, kJoinFew = 16;
 static_assert(kJoinWarps == kTileRows, "a warp a row");
 template <int D>
